@@ -18,7 +18,9 @@ LIB_PATH = os.path.join(_PKG, "libbeam.so")
 
 BEAM_KV_BF16, BEAM_KV_FP8_E4M3 = 0, 1
 BEAM_ATTN_SWA_ROPE, BEAM_ATTN_NOPE_SSMAX = 0, 1
+BEAM_PAGED_BF16, BEAM_PAGED_FP8, BEAM_PAGED_NVFP4 = 0, 1, 2
 DEV_BAD_POSITION, DEV_BAD_SEQ, DEV_BAD_EXPERT, DEV_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+DEV_BAD_PAGE = 0x10
 
 
 class BeamError(RuntimeError):
@@ -41,6 +43,15 @@ class LayerCfgC(ctypes.Structure):
                 ("topk_groups", ctypes.c_int32), ("topk", ctypes.c_int32),
                 ("d_ff_expert", ctypes.c_int32), ("d_ff_dense", ctypes.c_int32),
                 ("route_scale", ctypes.c_float)]
+
+
+class PagedKVC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("row_scale", ctypes.c_void_p),
+                ("block_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("dtype", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_kv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+                ("table_stride", ctypes.c_int32), ("window", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -66,8 +77,14 @@ _SIGS = {
     "beam_route_noalloc": [_P, _P, _P, _P, _I, _P, _P, _P],
     "beam_lm_head": [_P, _P, _I, _I, _I, _F, _P, _P],
     "beam_selftest_wait_timeout": [_P],
+    "beam_paged_kv_write": [_P, _P, _I, _P, _P, _I, _P, _P],
+    "beam_paged_kv_read": [_P, _P, _P, _P, _I, _I, _P, _P],
+    "beam_paged_attn": [_P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _Z, _P],
+    "beam_paged_workspace_bytes": [_P, _I, _I],
+    "beam_paged_kv_bytes": [_I, _I, _I, _I, _I],
 }
 _RES = {"beam_workspace_bytes": _Z, "beam_kv_cache_bytes": _Z,
+        "beam_paged_workspace_bytes": _Z, "beam_paged_kv_bytes": _Z,
         "beam_status_string": ctypes.c_char_p, "beam_launch_count": ctypes.c_uint64,
         "beam_last_cuda_error": ctypes.c_char_p}
 
@@ -161,6 +178,82 @@ class KVCache:
                         self.v_scale, self.k.shape[0], self.k.shape[2], self.window)
 
 
+def _want(name, t, dtype, shape=None):
+    """Refuses a tensor that the library would read as something else: another type, another
+    device than the current one, a shape or strides that are not the documented ones."""
+    if t.dtype != dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise BeamError(f"{name}: a contiguous {dtype} tensor"
+                        f"{'' if shape is None else ' of shape ' + str(tuple(shape))} is wanted, "
+                        f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+    if t.get_device() != torch.cuda.current_device():
+        raise BeamError(f"{name}: on {t.device}, but the current device is "
+                        f"cuda:{torch.cuda.current_device()}")
+
+
+class PagedKVCache:
+    """One layer's pages (beam_paged_kv in include/beam.h).
+
+    k, v        [num_pages][n_kv][page_size][D] bf16, or uint8 codes: [...][D] e4m3 (FP8), or
+                [...][D/2] e2m1 pairs (NVFP4, recognised by its block_scale)
+    page_table  [num_seqs][pages per sequence] int32
+    row_scale   [num_pages][n_kv][2][page_size] uint8; None for bf16
+    block_scale [num_pages][n_kv][2][page_size][D/16] uint8; NVFP4 only
+    window      0 for full attention, else the sliding window
+    The tensors are checked once, here, and must not be replaced afterwards (their contents may
+    change, the page table's among them)."""
+
+    def __init__(self, k, v, page_table, row_scale=None, block_scale=None, window=0):
+        if k.dim() != 4 or page_table.dim() != 2:
+            raise BeamError("PagedKVCache: k and v are [num_pages][n_kv][page_size][...], "
+                            "page_table [num_seqs][pages]")
+        pages, n_kv, size, width = k.shape
+        code = torch.bfloat16 if row_scale is None else torch.uint8
+        _want("k", k, code)
+        _want("v", v, code, k.shape)
+        _want("page_table", page_table, torch.int32)
+        self.dtype = BEAM_PAGED_BF16
+        if row_scale is not None:
+            _want("row_scale", row_scale, torch.uint8, (pages, n_kv, 2, size))
+            self.dtype = BEAM_PAGED_FP8
+        if block_scale is not None:
+            if row_scale is None:
+                raise BeamError("PagedKVCache: block_scale without row_scale")
+            width *= 2
+            _want("block_scale", block_scale, torch.uint8, (pages, n_kv, 2, size, width // 16))
+            self.dtype = BEAM_PAGED_NVFP4
+        self.k, self.v, self.page_table = k, v, page_table
+        self.row_scale, self.block_scale, self.window = row_scale, block_scale, int(window)
+        self.n_kv, self.page_size, self.head_dim = n_kv, size, width
+        self.device = k.get_device()
+        self._c = PagedKVC(k.data_ptr(), v.data_ptr(),
+                           0 if row_scale is None else row_scale.data_ptr(),
+                           0 if block_scale is None else block_scale.data_ptr(),
+                           page_table.data_ptr(), self.dtype, pages, size, n_kv, width,
+                           page_table.shape[0], page_table.shape[1], self.window)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, num_pages, page_size, n_kv, head_dim, page_table, dtype=BEAM_PAGED_BF16,
+              window=0):
+        """Pages of zeros on the page table's device."""
+        dev = page_table.device
+        width = {BEAM_PAGED_BF16: head_dim, BEAM_PAGED_FP8: head_dim,
+                 BEAM_PAGED_NVFP4: head_dim // 2}[dtype]
+        kind = torch.bfloat16 if dtype == BEAM_PAGED_BF16 else torch.uint8
+        dims = (num_pages, n_kv, page_size, width)
+        row = block = None
+        if dtype != BEAM_PAGED_BF16:
+            row = torch.zeros((num_pages, n_kv, 2, page_size), dtype=torch.uint8, device=dev)
+        if dtype == BEAM_PAGED_NVFP4:
+            block = torch.zeros((num_pages, n_kv, 2, page_size, head_dim // 16),
+                                dtype=torch.uint8, device=dev)
+        return cls(torch.zeros(dims, dtype=kind, device=dev),
+                   torch.zeros(dims, dtype=kind, device=dev), page_table, row, block, window)
+
+    def c(self):
+        return self._ref
+
+
 class Workspace:
     """Device scratch for the library calls, grown on demand (256-byte aligned)."""
 
@@ -224,6 +317,76 @@ def beam_moe(cfg: LayerCfg, u, topk_idx, topk_w, w_gate_up, w_down, out, ws: tor
     _check(lib().beam_moe(ctypes.byref(c), _ptr(u), _ptr(topk_idx), _ptr(topk_w),
                           _ptr(w_gate_up), _ptr(w_down), u.shape[0], _ptr(out), _ptr(ws),
                           ws.numel(), _stream(stream)), "beam_moe")
+
+
+def paged_workspace_bytes(cfg: LayerCfg, T: int, max_pos: int) -> int:
+    c = cfg.c()
+    return lib().beam_paged_workspace_bytes(ctypes.byref(c), T, max_pos)
+
+
+def paged_kv_bytes(num_pages, n_kv, page_size, head_dim, dtype=BEAM_PAGED_BF16) -> int:
+    return lib().beam_paged_kv_bytes(num_pages, n_kv, page_size, head_dim, dtype)
+
+
+def beam_paged_kv_write(k, v, seq_id, pos, cache: PagedKVCache, stream=None):
+    """k, v [T][n_kv][D] bf16 (rows of a token contiguous, any stride between tokens that is a
+    multiple of 8) into the cache's pages."""
+    T = k.shape[0]
+    for name, x in (("k", k), ("v", v)):
+        if (x.dtype != torch.bfloat16 or x.shape != (T, cache.n_kv, cache.head_dim) or
+                (T and (x.stride(2) != 1 or (cache.n_kv > 1 and x.stride(1) != cache.head_dim))) or
+                x.get_device() != cache.device):
+            raise BeamError(f"beam_paged_kv_write: {name} must be bf16 [T][{cache.n_kv}]"
+                            f"[{cache.head_dim}] with contiguous rows on the cache's device")
+    if T > 1 and k.stride(0) != v.stride(0):
+        raise BeamError("beam_paged_kv_write: k and v have different strides between tokens")
+    _want("seq_id", seq_id, torch.int32, (T,))
+    _want("pos", pos, torch.int32, (T,))
+    _check(lib().beam_paged_kv_write(_ptr(k), _ptr(v),
+                                     k.stride(0) if T > 1 else cache.n_kv * cache.head_dim,
+                                     _ptr(seq_id), _ptr(pos), T, cache.c(), _stream(stream)),
+           "beam_paged_kv_write")
+
+
+def beam_paged_kv_read(cache: PagedKVCache, seq_id, first, last, max_len, dst: KVCache,
+                       stream=None):
+    """Positions first[i]..last[i] of sequence seq_id[i] into row i of the contiguous BF16 cache
+    dst, slot (p-1) % capacity."""
+    N = seq_id.shape[0]
+    _want("seq_id", seq_id, torch.int32, (N,))
+    _want("first", first, torch.int32, (N,))
+    _want("last", last, torch.int32, (N,))
+    if dst.fp8:
+        raise BeamError("beam_paged_kv_read: the destination cache is BF16")
+    dims = (dst.k.shape[0], cache.n_kv, dst.k.shape[2], cache.head_dim)
+    _want("dst.k", dst.k, torch.bfloat16, dims)
+    _want("dst.v", dst.v, torch.bfloat16, dims)
+    kc = dst.c()
+    _check(lib().beam_paged_kv_read(cache.c(), _ptr(seq_id), _ptr(first), _ptr(last), N,
+                                    int(max_len), ctypes.byref(kc), _stream(stream)),
+           "beam_paged_kv_read")
+
+
+def beam_paged_attn(cfg: LayerCfg, q, g, gate_bias, cache: PagedKVCache, seq_id, pos, max_pos,
+                    w_o, out, ws: torch.Tensor, stream=None):
+    """Decode attention over the pages; g, gate_bias None: no gate; w_o None: out is [T][n_q*D]."""
+    T, bf = q.shape[0], torch.bfloat16
+    _want("q", q, bf, (T, cfg.n_q, cfg.head_dim))
+    if (g is None) != (gate_bias is None):
+        raise BeamError("beam_paged_attn: g and gate_bias go together")
+    if g is not None:
+        _want("g", g, bf, (T, cfg.n_q * cfg.head_dim))
+        _want("gate_bias", gate_bias, bf, (cfg.n_q,))
+    if w_o is not None:
+        _want("w_o", w_o, bf, (cfg.hidden, cfg.n_q * cfg.head_dim))
+    _want("out", out, bf, (T, cfg.n_q * cfg.head_dim if w_o is None else cfg.hidden))
+    _want("seq_id", seq_id, torch.int32, (T,))
+    _want("pos", pos, torch.int32, (T,))
+    c = cfg.c()
+    _check(lib().beam_paged_attn(ctypes.byref(c), _ptr(q), _ptr(g), _ptr(gate_bias), cache.c(),
+                                 _ptr(seq_id), _ptr(pos), T, int(max_pos), _ptr(w_o), _ptr(out),
+                                 _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "beam_paged_attn")
 
 
 class NvFp4ExpertsC(ctypes.Structure):

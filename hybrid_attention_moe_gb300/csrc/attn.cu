@@ -26,6 +26,7 @@
 #include "gemm_tc.cuh"
 #include "gemv.cuh"
 #include "mma.cuh"
+#include "paged.cuh"
 
 namespace beam {
 namespace {
@@ -799,6 +800,13 @@ cudaError_t launch_prefill(const uint16_t* q, const uint16_t* g, const uint16_t*
 
 }  // namespace
 
+cudaError_t o_proj(const uint16_t* og, int T, int HD, const uint16_t* w_o, int H, uint16_t* out,
+                   cudaStream_t st) {
+  return T >= kGemmMinT && tc::gemm_supported(og, HD, w_o, HD, HD)
+             ? tc::gemm_bf16(og, T, HD, HD, w_o, H, HD, out, H, true, st)
+             : launch_gemv<kOutBF16>(w_o, H, HD, og, T, nullptr, out, H, st);
+}
+
 size_t attn_ws_bytes(const beam_layer_cfg* c, int T, int max_pos, int window) {
   size_t b = align_up(size_t(T) * c->n_q * c->head_dim * 2, 256);
   {   // the split-K decode form may be chosen for any T (decode_form)
@@ -910,10 +918,7 @@ extern "C" beam_status beam_attn(const beam_layer_cfg* cfg, const beam_bf16* q,
               : launch_prefill<64, false>(q, g, gate_bias, seq_id, pos, T, cfg->n_q, cfg->n_kv, *cache, sl2, og, st);
     if (e != cudaSuccess) return cuda_status(e);
   }
-  const cudaError_t ge =
-      T >= kGemmMinT && tc::gemm_supported(og, HD, w_o, HD, HD)
-          ? tc::gemm_bf16(og, T, HD, HD, w_o, H, HD, out, H, true, st)
-          : launch_gemv<kOutBF16>(w_o, H, HD, og, T, nullptr, out, H, st);
+  const cudaError_t ge = o_proj(og, T, HD, w_o, H, out, st);
   if (ge != cudaSuccess) return cuda_status(ge);
   return BEAM_OK;
 }

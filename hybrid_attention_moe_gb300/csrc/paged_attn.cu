@@ -1,0 +1,1010 @@
+// Decode attention over the paged cache: one new token per row, the row's keys split over the
+// SMs and joined.
+//
+//   o[h] = sum_i e^(x_i - m) v_i / sum_i e^(x_i - m),  x_i = q[h].k_i / sqrt(D),  m = max x_i
+//
+// over the row's keys i, computed in one pass with the running (m, sum, O) of a softmax, which
+// partial results of disjoint key ranges join by. Bounded by the bytes of the keys and values.
+//
+// Split. A (row, KV head) pair's keys are cut into blocks of BK; the blocks of all pairs, laid
+// end to end, are cut into one equal range per CTA (one CTA per SM). The ranges are computed on
+// the device from the rows' own lengths, so a batch of very unequal sequences still gives every
+// SM the same bytes. A pair that one CTA holds whole is finished there; the partials of a split
+// pair go to the workspace and a second small kernel joins them. Pairs of at most kWholeBlocks
+// blocks are never split (a CTA takes the pairs that begin in its range) and need no join.
+//
+// Per CTA a producer warp reads the page table (one lane per page of the block, a block ahead)
+// and issues a TMA load per page for K and V into a ring of stages, with the rows' scales and,
+// for a pair's first block, its q rows beside them. The consumer warps each take 16 keys of a
+// block. The tiles are transposed, so that the query heads of a KV group are the 8-wide N side
+// of mma.sync m16n8k16 (two N tiles for 9 to 16 heads):
+//   S^T[16 keys x 8 heads] = K[16 x D] . Q^T,   O^T[D x 8 heads] += V^T[D x 16 keys] . P^T
+// P is split into a high and a low half, so it carries twice the operand type's bits.
+//
+// FP8 and NVFP4 codes become f16 in registers, exactly (e2m1 times its e4m3 block scale has 6
+// significant bits), and the products run in f16 with FP32 accumulation. The d axis is permuted
+// the same way in q and K, and undone on the output for V, so that a thread's codes are
+// contiguous bytes. The rows' powers of two never enter an f16 value: K's multiplies the FP32
+// logits; V's goes into P relative to the largest one that the warp has seen (E), as
+// p * 2^(e - E + 7), so that P's largest values lie near the top of f16 and rows of smaller
+// values keep their bits. q is scaled by a power of two per head in the same manner.
+//
+// Every wait is bounded: on expiry the CTA records BEAM_DEV_TIMEOUT, stops issuing, lets its
+// issued copies land and finishes without valid results.
+#include <cuda.h>
+#include <math.h>
+
+#include "mma.cuh"
+#include "paged.cuh"
+#include "tcgen05.cuh"
+
+namespace beam {
+namespace paged {
+namespace {
+
+using namespace beam::tc;
+
+constexpr float kNegInf = -INFINITY;
+constexpr float kRescale = 8.f;     // log2 units by which the running max may lag
+constexpr int kMaxGrid = 152;       // CTAs, and so parts of one pair, at most
+constexpr int kMaxT = 1024;         // rows of one launch
+constexpr int kWholeBlocks = 4;
+constexpr int kBias = 7;            // P <= 2^kRescale, times 2^7: below 65504
+
+template <int FMT, int D_, int NT_>
+struct Cfg {
+  static constexpr int D = D_, NT = NT_, HEADS = 8 * NT;
+  static constexpr int ROWB = row_bytes(FMT, D);
+  static constexpr int PLANES = ROWB > 128 ? 2 : 1;   // 128-byte columns of a row
+  // consumer warps, 16 keys each: a block holds 32 KB of K and V where that fits
+  static constexpr int NCW = FMT == kFmtBF16 ? (D == 128 ? 4 : 8)
+                             : FMT == kFmtNVFP4 && D == 128 && NT == 1 ? 16 : 8;
+  static constexpr int THREADS = (NCW + 1) * 32;
+  static constexpr int BK = 16 * NCW;
+  static constexpr int KB = BK * ROWB;
+  static constexpr int BSB = FMT == kFmtNVFP4 ? 2 * BK * (D / 16) : 0;
+  static constexpr int RSB = FMT != kFmtBF16 ? 2 * BK : 0;
+  static constexpr int QB = HEADS * D * 2;
+  static constexpr int OBS = 2 * KB, ORS = OBS + BSB, OQ = ORS + RSB;   // offsets in a stage
+  static constexpr int STAGE = (OQ + QB + 1023) / 1024 * 1024;
+  static constexpr int NST = FMT == kFmtNVFP4 && NCW == 16 ? 3 : 4;
+  static constexpr int OLD = D + 4;   // row stride of the combine buffer (floats)
+  static constexpr int OW = NST * STAGE;                         // [NCW][HEADS][OLD]
+  static constexpr int MLW = OW + NCW * HEADS * OLD * 4;         // [NCW][HEADS][2]
+  static constexpr int FW = MLW + NCW * HEADS * 2 * 4;           // [NCW][HEADS]
+  static constexpr int LH = FW + NCW * HEADS * 4;                // [HEADS] sums, maxima
+  static constexpr int CUM = LH + 2 * HEADS * 4;                 // [kMaxT + 1] block prefix
+  static constexpr int MISC = (CUM + (kMaxT + 1) * 4 + 15) / 16 * 16;   // -, abort, issued, -; masks
+  static constexpr int BAR = MISC + 16 + 16;
+  static constexpr int BYTES = BAR + 2 * NST * 8 + 1024;         // + alignment slack
+  static_assert(BYTES <= 227 * 1024, "stage ring exceeds shared memory");
+  static_assert(NST <= 4, "one mask word per stage");
+};
+
+struct Params {
+  const uint16_t* q;
+  const uint16_t* g;
+  const uint16_t* gate_bias;
+  const int32_t* seq_id;
+  const int32_t* pos;
+  uint16_t* og;
+  float* part_acc;   // [grid][2][HEADS][D]: a CTA's partials of its first and its last pair
+  float* part_ml;    // [grid][2][HEADS][2]
+  int4* join;        // [grid]: (row, KV head, parts, slot of the first part); parts 0: nothing
+  beam_paged_kv c;
+  int T, n_q, n_kv, G, max_pos, shift, whole;
+  float sl2;
+};
+
+// Row t's keys are positions [lo, p], in blocks blk0 .. blk0 + nb - 1 (block b: BK * b + 1 ..).
+struct Row {
+  int p, s, lo, blk0, nb;
+  unsigned bad;
+};
+template <int BK>
+__device__ __forceinline__ Row row_of(const Params& P, int t) {
+  Row r;
+  r.p = P.pos[t];
+  r.s = P.seq_id[t];
+  r.bad = 0;
+  if (r.p < 0 || r.p > P.max_pos || (r.p > 0 && ((r.p - 1) >> P.shift) >= P.c.table_stride))
+    r.bad = BEAM_DEV_BAD_POSITION;
+  else if (r.p > 0 && (r.s < 0 || r.s >= P.c.num_seqs))
+    r.bad = BEAM_DEV_BAD_SEQ;
+  r.lo = P.c.window > 0 ? max(1, r.p - P.c.window + 1) : 1;
+  r.blk0 = (r.lo - 1) / BK;
+  r.nb = r.bad || r.p == 0 ? 0 : (r.p - 1) / BK - r.blk0 + 1;
+  return r;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movtrans(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+template <int W>
+__device__ __forceinline__ void lds(uint32_t a, uint32_t* v) {
+  if constexpr (W == 4)
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a));
+  else if constexpr (W == 2)
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(a));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(a));
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int NTHREADS>
+__device__ __forceinline__ void consumer_bar() {
+  asm volatile("bar.sync 1, %0;" ::"n"(NTHREADS) : "memory");
+}
+// Untiled bulk copy (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst), "l"(src), "r"(bytes), "r"(mbar)
+      : "memory");
+}
+// Byte o of a region of 128-byte rows under the 128-byte TMA swizzle.
+__device__ __forceinline__ uint32_t sw(uint32_t o) { return o ^ (((o >> 7) & 7u) << 4); }
+
+template <int N>
+__device__ constexpr int log2_of() {
+  return N <= 1 ? 0 : 1 + log2_of<(N > 1 ? N / 2 : 1)>();
+}
+
+// The four outputs from column d of query head h of a pair's KV group.
+__device__ __forceinline__ void finish(const Params& P, int t, int hk, int h, int d, int D,
+                                       float4 O, float L) {
+  const int hq = hk * P.G + h;
+  const size_t oi = (size_t(t) * P.n_q + hq) * D + d;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  float o[4] = {O.x * inv, O.y * inv, O.z * inv, O.w * inv};
+  if (P.g != nullptr) {
+    const float gb = bf2f(P.gate_bias[hq]);
+    const uint2 gv = *reinterpret_cast<const uint2*>(P.g + oi);
+    o[0] *= sigmoidf_(bf_lo(gv.x) + gb);
+    o[1] *= sigmoidf_(bf_hi(gv.x) + gb);
+    o[2] *= sigmoidf_(bf_lo(gv.y) + gb);
+    o[3] *= sigmoidf_(bf_hi(gv.y) + gb);
+  }
+  *reinterpret_cast<uint2*>(P.og + oi) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+}
+
+// The state of one warp over its keys of a pair.
+template <class C>
+struct WarpState {
+  float m[C::NT][2], l[C::NT][2];
+  float acc[C::NT][C::D / 16][4];
+  int E;   // quantised caches: the largest scale byte of a value row so far
+};
+
+// One warp's 16 keys of a staged block. kb: the stage; kbase: position of the warp's first key;
+// the row's keys are positions [lo, p]. qs: FP32 factor of the logits per accumulator column.
+template <int FMT, class C>
+__device__ __forceinline__ void warp_block(uint32_t kb, int w, const uint32_t (&qb)[C::NT][C::D / 16][2],
+                                           const float (&qs)[C::NT][2], int pse_shift, int kbase,
+                                           int lo, int p, WarpState<C>& S) {
+  constexpr int D = C::D, NT = C::NT, KK = D / 16;
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const uint32_t vb = kb + C::KB;
+  float sa[NT][4], sb[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sa[n][e] = sb[n][e] = 0.f;
+  // Offset of a key's scale in the staged [page][K | V][key of the page] order.
+  auto srow = [&](int key, int kv) {
+    return ((((key >> pse_shift) << 1) + kv) << pse_shift) + (key & ((1 << pse_shift) - 1));
+  };
+  // ---- S^T = K . Q^T
+  if constexpr (FMT == kFmtBF16) {
+    const int rk = 16 * w + ((lane >> 3) & 1) * 8 + (lane & 7), ck = (lane >> 4) & 1;
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      uint32_t a[4];
+      const uint32_t off = (kk >> 2) * (C::KB / C::PLANES) + rk * 128 + (((2 * (kk & 3) + ck) ^ (lane & 7)) << 4);
+      ldsm_x4(kb + off, a[0], a[1], a[2], a[3]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_bf16((kk & 1) ? sb[n] : sa[n], a, qb[n][kk][0], qb[n][kk][1]);
+    }
+  } else {
+    // a thread's codes of keys g and g + 8: the d range [c D/4, (c + 1) D/4), four of a k step
+    constexpr int KW = C::ROWB / 16;   // words of a key in one thread
+    uint32_t w0[KW], w1[KW];
+    const uint32_t o0 = (16 * w + g) * C::ROWB + c * (C::ROWB / 4), o1 = o0 + 8 * C::ROWB;
+    if constexpr (KW == 8) {
+      lds<4>(kb + sw(o0), w0);
+      lds<4>(kb + sw(o0 + 16), w0 + 4);
+      lds<4>(kb + sw(o1), w1);
+      lds<4>(kb + sw(o1 + 16), w1 + 4);
+    } else {
+      lds<KW>(kb + sw(o0), w0);
+      lds<KW>(kb + sw(o1), w1);
+    }
+    if constexpr (FMT == kFmtFP8) {
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        uint32_t a[4];
+        e4m3x4_f16(w0[kk], a[0], a[2]);
+        e4m3x4_f16(w1[kk], a[1], a[3]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_f16((kk & 1) ? sb[n] : sa[n], a, qb[n][kk][0], qb[n][kk][1]);
+      }
+    } else {
+      // block scales of the thread's d range: two blocks (D 128) or one (D 64)
+      const uint32_t s0 = kb + C::OBS + srow(16 * w + g, 0) * (D / 16);
+      const uint32_t s1 = kb + C::OBS + srow(16 * w + g + 8, 0) * (D / 16);
+      uint32_t f0, f1;
+      if constexpr (D == 128) {
+        f0 = e4m3x2_f16x2(lds_u16(s0 + 2 * c));
+        f1 = e4m3x2_f16x2(lds_u16(s1 + 2 * c));
+      } else {
+        f0 = e4m3x2_f16x2(lds_u8(s0 + c) * 0x101u);
+        f1 = e4m3x2_f16x2(lds_u8(s1 + c) * 0x101u);
+      }
+#pragma unroll
+      for (int j = 0; j < KW; ++j) {   // a word: the codes of two k steps
+        uint32_t h0[4], h1[4];
+        e2m1x8_f16(w0[j], h0);
+        e2m1x8_f16(w1[j], h1);
+        const uint32_t sel = D == 64 ? 0x3210u : (j < KW / 2 ? 0x1010u : 0x3232u);
+        const uint32_t b0 = prmt(f0, f0, sel), b1 = prmt(f1, f1, sel);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t a[4] = {mul_f16x2(h0[2 * e], b0), mul_f16x2(h1[2 * e], b1),
+                                 mul_f16x2(h0[2 * e + 1], b0), mul_f16x2(h1[2 * e + 1], b1)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            mma_f16(e ? sb[n] : sa[n], a, qb[n][2 * j + e][0], qb[n][2 * j + e][1]);
+        }
+      }
+    }
+  }
+  // ---- logits, running max. S^T fragment: [0] (key g, head 2c), [1] (g, 2c+1), [2], [3] key g + 8
+  const int kp0 = kbase + g;
+  const bool v0 = kp0 >= lo && kp0 <= p, v1 = kp0 + 8 >= lo && kp0 + 8 <= p;
+  float ks0 = 1.f, ks1 = 1.f;
+  int e0 = 0, e1 = 0;   // scale bytes of the value rows
+  if constexpr (FMT != kFmtBF16) {
+    const uint32_t rs = kb + C::ORS;
+    ks0 = pow2_of(lds_u8(rs + srow(16 * w + g, 0)));
+    ks1 = pow2_of(lds_u8(rs + srow(16 * w + g + 8, 0)));
+    e0 = int(lds_u8(rs + srow(16 * w + g, 1)));
+    e1 = int(lds_u8(rs + srow(16 * w + g + 8, 1)));
+    const int top = __reduce_max_sync(0xffffffffu, max(v0 && e0 != 255 ? e0 : 0, v1 && e1 != 255 ? e1 : 0));
+    if (top > S.E) {   // the accumulators hold values relative to 2^E
+      const float f = ex2(float(S.E - top));
+      S.E = top;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int mt = 0; mt < KK; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S.acc[n][mt][e] *= f;
+    }
+  }
+  uint32_t bh[NT][2], bl[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float x[4];
+    x[0] = v0 ? (sa[n][0] + sb[n][0]) * (qs[n][0] * ks0) : kNegInf;
+    x[1] = v0 ? (sa[n][1] + sb[n][1]) * (qs[n][1] * ks0) : kNegInf;
+    x[2] = v1 ? (sa[n][2] + sb[n][2]) * (qs[n][0] * ks1) : kNegInf;
+    x[3] = v1 ? (sa[n][3] + sb[n][3]) * (qs[n][1] * ks1) : kNegInf;
+    float mh[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      mh[0] = fmaxf(mh[0], __shfl_xor_sync(0xffffffffu, mh[0], o));
+      mh[1] = fmaxf(mh[1], __shfl_xor_sync(0xffffffffu, mh[1], o));
+    }
+    float(&m)[2] = S.m[n];
+    float(&l)[2] = S.l[n];
+    if (__any_sync(0xffffffffu, mh[0] > m[0] + kRescale || mh[1] > m[1] + kRescale)) {
+      float cr[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float mn = fmaxf(m[h], mh[h]);
+        cr[h] = m[h] == kNegInf ? 0.f : ex2(m[h] - mn);
+        m[h] = mn;
+        l[h] *= cr[h];
+      }
+#pragma unroll
+      for (int mt = 0; mt < KK; ++mt) {
+        S.acc[n][mt][0] *= cr[0];
+        S.acc[n][mt][1] *= cr[1];
+        S.acc[n][mt][2] *= cr[0];
+        S.acc[n][mt][3] *= cr[1];
+      }
+    }
+    const float ms0 = m[0] == kNegInf ? 0.f : m[0], ms1 = m[1] == kNegInf ? 0.f : m[1];
+    float p0 = ex2(x[0] - ms0), p1 = ex2(x[1] - ms1);
+    float p2 = ex2(x[2] - ms0), p3 = ex2(x[3] - ms1);
+    l[0] += p0 + p2;
+    l[1] += p1 + p3;
+    // P (key rows, head columns) as hi + lo, then transposed into the B fragments of P^T:
+    // b0 = (keys 2c, 2c+1; head g), b1 = (keys 2c+8, 2c+9; head g)
+    uint32_t h01, h23, l01, l23;
+    if constexpr (FMT == kFmtBF16) {
+      h01 = pack_bf16x2(p0, p1);
+      h23 = pack_bf16x2(p2, p3);
+      l01 = pack_bf16x2(p0 - bf_lo(h01), p1 - bf_hi(h01));
+      l23 = pack_bf16x2(p2 - bf_lo(h23), p3 - bf_hi(h23));
+    } else {
+      // 2^(e - E + kBias); NaN for a row that holds no numbers; a key that is not the row's
+      // weighs exactly nothing whatever its scale byte says
+      auto rel = [&](int e) {
+        const int b = e - S.E + 127 + kBias;
+        return e == 255 ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float(b > 0 ? unsigned(b) << 23 : 0u);
+      };
+      const float vs0 = v0 ? rel(e0) : 0.f, vs1 = v1 ? rel(e1) : 0.f;
+      p0 *= vs0;
+      p1 *= vs0;
+      p2 *= vs1;
+      p3 *= vs1;
+      float f0, f1, f2, f3;
+      h01 = pack_f16x2(p0, p1);
+      h23 = pack_f16x2(p2, p3);
+      unpack_f16(h01, f0, f1);
+      unpack_f16(h23, f2, f3);
+      l01 = pack_f16x2(p0 - f0, p1 - f1);
+      l23 = pack_f16x2(p2 - f2, p3 - f3);
+    }
+    bh[n][0] = movtrans(h01);
+    bh[n][1] = movtrans(h23);
+    bl[n][0] = movtrans(l01);
+    bl[n][1] = movtrans(l23);
+  }
+  // ---- O^T += V^T . P^T. Keys outside [lo, p] (whose slots may hold anything, NaN included)
+  // have their values replaced by zeros, so that P = 0 there contributes exactly nothing.
+  const bool full = kbase >= lo && kbase + 15 <= p;
+  uint32_t m01 = 0xFFFFFFFFu, m89 = 0xFFFFFFFFu;
+  if (!full) {
+    auto ok = [&](int k) { return kbase + k >= lo && kbase + k <= p; };
+    m01 = (ok(2 * c) ? 0x0000FFFFu : 0u) | (ok(2 * c + 1) ? 0xFFFF0000u : 0u);
+    m89 = (ok(2 * c + 8) ? 0x0000FFFFu : 0u) | (ok(2 * c + 9) ? 0xFFFF0000u : 0u);
+  }
+  auto pv = [&](int mt, uint32_t (&a)[4]) {
+    if (!full) {
+      a[0] &= m01;
+      a[1] &= m01;
+      a[2] &= m89;
+      a[3] &= m89;
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if constexpr (FMT == kFmtBF16) {
+        mma_bf16(S.acc[n][mt], a, bh[n][0], bh[n][1]);
+        mma_bf16(S.acc[n][mt], a, bl[n][0], bl[n][1]);
+      } else {
+        mma_f16(S.acc[n][mt], a, bh[n][0], bh[n][1]);
+        mma_f16(S.acc[n][mt], a, bl[n][0], bl[n][1]);
+      }
+    }
+  };
+  if constexpr (FMT == kFmtBF16) {
+    const int rv = 16 * w + ((lane >> 4) & 1) * 8 + (lane & 7), cv = (lane >> 3) & 1;
+#pragma unroll
+    for (int mt = 0; mt < KK; ++mt) {
+      uint32_t a[4];
+      ldsm_x4_t(vb + (mt >> 2) * (C::KB / C::PLANES) + rv * 128 + (((2 * (mt & 3) + cv) ^ (lane & 7)) << 4),
+                a[0], a[1], a[2], a[3]);
+      pv(mt, a);
+    }
+  } else {
+    // keys {2c, 2c+1, 2c+8, 2c+9}, d range [g D/8, (g + 1) D/8): logical row g of m tile mt is
+    // d = g D/8 + 2 mt, row g + 8 the next one
+    constexpr int VW = C::ROWB / 32;
+    uint32_t r[4][VW];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      lds<VW>(vb + sw((16 * w + 2 * c + (k & 1) + 8 * (k >> 1)) * C::ROWB + g * (C::ROWB / 8)), r[k]);
+    if constexpr (FMT == kFmtFP8) {
+#pragma unroll
+      for (int mt = 0; mt < KK; ++mt) {
+        const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;
+        uint32_t a[4];
+        e4m3x4_f16(prmt(r[0][mt >> 1], r[1][mt >> 1], sel), a[0], a[1]);
+        e4m3x4_f16(prmt(r[2][mt >> 1], r[3][mt >> 1], sel), a[2], a[3]);
+        pv(mt, a);
+      }
+    } else {
+      // the thread's d range lies in one block of 16: one scale per key
+      uint32_t s[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        s[k] = lds_u8(kb + C::OBS + srow(16 * w + 2 * c + (k & 1) + 8 * (k >> 1), 1) * (D / 16) +
+                      (D == 128 ? g : g >> 1));
+      const uint32_t f01 = e4m3x2_f16x2(s[0] | (s[1] << 8)), f89 = e4m3x2_f16x2(s[2] | (s[3] << 8));
+      constexpr uint32_t kLow = 0x0F0F0F0Fu;
+#pragma unroll
+      for (int j = 0; j < VW; ++j) {
+        // bytes of (key 2c, key 2c+1) code pairs: even elements of four m tiles, then odd ones
+        uint32_t ae[4], ao[4], be[4], bo[4];
+        e2m1x8_f16((r[0][j] & kLow) | ((r[1][j] & kLow) << 4), ae);
+        e2m1x8_f16(((r[0][j] >> 4) & kLow) | (r[1][j] & ~kLow), ao);
+        e2m1x8_f16((r[2][j] & kLow) | ((r[3][j] & kLow) << 4), be);
+        e2m1x8_f16(((r[2][j] >> 4) & kLow) | (r[3][j] & ~kLow), bo);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t a[4] = {mul_f16x2(ae[i], f01), mul_f16x2(ao[i], f01), mul_f16x2(be[i], f89),
+                           mul_f16x2(bo[i], f89)};
+          pv(4 * j + i, a);
+        }
+      }
+    }
+  }
+}
+
+template <int FMT, int D, int NT>
+__global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kernel(
+    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+    const Params P) {
+  using C = Cfg<FMT, D, NT>;
+  constexpr int NCT = C::NCW * 32, BK = C::BK;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(sm);
+  const uint32_t bar_full = sbase + C::BAR, bar_empty = bar_full + 8 * C::NST;
+  volatile int* misc = reinterpret_cast<volatile int*>(sm + C::MISC);   // -, abort, issued, -
+  volatile unsigned* masks = reinterpret_cast<volatile unsigned*>(sm + C::MISC + 16);
+  int* cum = reinterpret_cast<int*>(sm + C::CUM);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::NST; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, C::NCW);
+    }
+    misc[1] = 0;
+    misc[2] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
+  // ---- plan: cum[t] = blocks of one KV head in rows 0 .. t - 1
+  const int T = P.T;
+  for (int t = threadIdx.x; t < T; t += C::THREADS) {
+    const Row r = row_of<BK>(P, t);
+    cum[t + 1] = r.nb;
+    if (r.bad && blockIdx.x == 0) flag(r.bad);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int per = (T + 31) / 32, a = min(T, lane * per), b = min(T, a + per);
+    int sum = 0;
+    for (int t = a; t < b; ++t) sum += cum[t + 1];
+    int run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += u;
+    }
+    run -= sum;
+    for (int t = a; t < b; ++t) {
+      run += cum[t + 1];
+      cum[t + 1] = run;
+    }
+    if (lane == 0) cum[0] = 0;
+  }
+  __syncthreads();
+  const int total = cum[T] * P.n_kv;
+  const int R = max(1, (total + int(gridDim.x) - 1) / int(gridDim.x));
+  int f_lo = int(min(int64_t(total), int64_t(blockIdx.x) * R)), f_hi = min(total, f_lo + R);
+  // row of flat block f: the last t with cum[t] * n_kv <= f
+  auto row_at = [&](int f) {
+    int a = 0, b = T;   // cum[a] * n_kv <= f < cum[b] * n_kv
+    while (b - a > 1) {
+      const int mid = (a + b) >> 1;
+      if (cum[mid] * P.n_kv <= f) a = mid;
+      else b = mid;
+    }
+    return a;
+  };
+  if (P.whole) {   // move both ends up to the next pair's first block
+    auto up = [&](int f) {
+      if (f >= total) return total;
+      const int t = row_at(f), nb = cum[t + 1] - cum[t], r = (f - cum[t] * P.n_kv) % nb;
+      return r ? f + nb - r : f;
+    };
+    f_lo = up(f_lo);
+    f_hi = up(f_hi);
+  }
+  const int t_lo = f_lo < f_hi ? row_at(f_lo) : 0;
+
+  if (warp == C::NCW) {
+    // ---------------- producer
+    const int pse = min(P.c.page_size, BK);               // keys of a page in a block
+    const int npg = BK / pse;
+    struct At {
+      int t, hk, j, nb, blk0, lo, p, s;
+    };
+    auto load_row = [&](At& a) {
+      const Row r = row_of<BK>(P, a.t);
+      a.nb = r.nb;
+      a.blk0 = r.blk0;
+      a.lo = r.lo;
+      a.p = r.p;
+      a.s = r.s;
+    };
+    auto advance = [&](At& a) {
+      if (++a.j < a.nb) return;
+      a.j = 0;
+      if (++a.hk < P.n_kv) return;
+      a.hk = 0;
+      do ++a.t;
+      while (a.t < T && cum[a.t + 1] == cum[a.t]);
+      if (a.t < T) load_row(a);
+    };
+    // lane i's page of the block: its number, or -2 where the block has no key in it
+    auto fetch = [&](const At& a) -> int {
+      if (lane >= npg) return -2;
+      const int k0 = (a.blk0 + a.j) * BK + lane * pse;   // keys k0 + 1 .. k0 + pse
+      if (k0 + pse < a.lo || k0 + 1 > a.p) return -2;
+      return P.c.page_table[size_t(a.s) * P.c.table_stride + (k0 >> P.shift)];
+    };
+    At at{t_lo, 0, 0, 1, 0, 1, 0, 0};
+    int id = -2;
+    if (f_lo < f_hi) {
+      load_row(at);
+      const int r = f_lo - cum[at.t] * P.n_kv;
+      at.hk = r / at.nb;
+      at.j = r - at.hk * at.nb;
+      id = fetch(at);
+    }
+    int i = 0;
+    for (int f = f_lo; f < f_hi; ++f, ++i) {
+      const At a = at;
+      const int page = id;
+      advance(at);
+      if (f + 1 < f_hi) id = fetch(at);   // the next block's pages, while this one waits
+      const int st = i % C::NST;
+      bool go = misc[1] == 0;
+      if (go && i >= C::NST) go = mbar_wait(bar_empty + 8 * st, ((i / C::NST) - 1) & 1);
+      if (!__all_sync(0xffffffffu, go)) {
+        if (lane == 0) misc[1] = 1;
+        break;
+      }
+      const bool ok = page >= 0 && page < P.c.num_pages;
+      if (page != -2 && !ok) flag(BEAM_DEV_BAD_PAGE);
+      const unsigned okm = __ballot_sync(0xffffffffu, ok);
+      const unsigned slices = __ballot_sync(0xffffffffu, lane < C::NCW && ((okm >> (lane * 16 / pse)) & 1u));
+      const uint32_t base = sbase + st * C::STAGE, fb = bar_full + 8 * st;
+      const bool with_q = f == f_lo || a.j == 0;
+      if (lane == 0) {
+        masks[st] = slices;
+        const uint32_t per = uint32_t(2 * pse * (C::ROWB + (FMT != kFmtBF16 ? 1 : 0) + (FMT == kFmtNVFP4 ? D / 16 : 0)));
+        mbar_expect_tx(fb, __popc(okm) * per + (with_q ? P.G * D * 2 : 0));
+      }
+      __syncwarp();
+      if (ok) {
+        const int z = page * P.n_kv + a.hk;
+        const int off = ((a.blk0 + a.j) * BK + lane * pse) & (P.c.page_size - 1);   // first key in the page
+        const uint32_t dk = base + lane * pse * (C::ROWB / C::PLANES), dv = dk + C::KB;
+        const int y = C::PLANES == 2 ? off : off * C::ROWB / 128;
+        tma_load_3d(dk, &tk, 0, y, z, fb);
+        if constexpr (C::PLANES == 2) tma_load_3d(dk + C::KB / 2, &tk, 128, y, z, fb);
+        tma_load_3d(dv, &tv, 0, y, z, fb);
+        if constexpr (C::PLANES == 2) tma_load_3d(dv + C::KB / 2, &tv, 128, y, z, fb);
+        if constexpr (FMT != kFmtBF16) {
+          const size_t row = size_t(z) * 2 * P.c.page_size + off;
+          const uint32_t dr = base + C::ORS + lane * 2 * pse;
+          if (npg > 1 || pse == P.c.page_size) {
+            bulk_load(dr, P.c.row_scale + row, 2 * pse, fb);
+          } else {   // part of a page: K's and V's scales apart
+            bulk_load(dr, P.c.row_scale + row, pse, fb);
+            bulk_load(dr + pse, P.c.row_scale + row + P.c.page_size, pse, fb);
+          }
+          if constexpr (FMT == kFmtNVFP4) {
+            const uint32_t db = base + C::OBS + lane * 2 * pse * (D / 16);
+            if (npg > 1 || pse == P.c.page_size) {
+              bulk_load(db, P.c.block_scale + row * (D / 16), 2 * pse * (D / 16), fb);
+            } else {
+              bulk_load(db, P.c.block_scale + row * (D / 16), pse * (D / 16), fb);
+              bulk_load(db + pse * (D / 16), P.c.block_scale + (row + P.c.page_size) * (D / 16),
+                        pse * (D / 16), fb);
+            }
+          }
+        }
+      }
+      if (with_q && lane == 31)
+        bulk_load(base + C::OQ, P.q + (size_t(a.t) * P.n_q + a.hk * P.G) * D, P.G * D * 2, fb);
+      __syncwarp();
+    }
+    if (lane == 0) misc[2] = i;
+  } else {
+    // ---------------- consumers
+    const int w = warp, g = lane >> 2, c = lane & 3, ct = threadIdx.x;
+    const int pse_shift = min(P.shift, log2_of<BK>());
+    float* Ow = reinterpret_cast<float*>(sm + C::OW);
+    float* MLw = reinterpret_cast<float*>(sm + C::MLW);
+    float* FWs = reinterpret_cast<float*>(sm + C::FW);
+    float* LHs = reinterpret_cast<float*>(sm + C::LH);   // [0, HEADS) sums, then maxima
+    const int G = P.G;
+    int i = 0, t = t_lo, f = f_lo;
+    int4 join = make_int4(0, 0, 0, 0);
+    int hk = 0, j0 = 0;
+    if (f_lo < f_hi) {
+      const int nb = cum[t + 1] - cum[t], r = f_lo - cum[t] * P.n_kv;
+      hk = r / nb;
+      j0 = r - hk * nb;
+    }
+    while (f < f_hi) {
+      const Row row = row_of<BK>(P, t);
+      const int f_pair = cum[t] * P.n_kv + hk * row.nb;   // the pair's first block
+      const int j1 = min(row.nb, f_hi - f_pair);
+      uint32_t qb[NT][D / 16][2];
+      float qs[NT][2];
+      WarpState<C> S;
+      S.E = 0;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        S.m[n][0] = S.m[n][1] = kNegInf;
+        S.l[n][0] = S.l[n][1] = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) S.acc[n][mt][0] = S.acc[n][mt][1] = S.acc[n][mt][2] = S.acc[n][mt][3] = 0.f;
+      }
+      for (int j = j0; j < j1; ++j, ++i) {
+        const int st = i % C::NST;
+        const uint32_t kb = sbase + st * C::STAGE;
+        bool ok = misc[1] == 0;
+        if (ok) ok = mbar_wait(bar_full + 8 * st, (i / C::NST) & 1);
+        if (__all_sync(0xffffffffu, ok)) {
+          if (j == j0) {
+            // q fragments (B operand, column = head g of the tile)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const int h = 8 * n + g;
+              const bool rok = h < G;
+              const uint32_t qa = kb + C::OQ + (rok ? h : 0) * D * 2;
+              if constexpr (FMT == kFmtBF16) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  lds<1>(qa + (8 * kk + c) * 4, &qb[n][kk][0]);
+                  lds<1>(qa + (8 * kk + c + 4) * 4, &qb[n][kk][1]);
+                  if (!rok) qb[n][kk][0] = qb[n][kk][1] = 0u;
+                }
+                qs[n][0] = qs[n][1] = P.sl2;
+              } else {
+                unsigned mx = 0;   // the head's largest magnitude, as a bf16 pattern
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  lds<2>(qa + (D / 8) * c * 4 + kk * 8, qb[n][kk]);
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    if (!rok) qb[n][kk][e] = 0u;
+                    mx = max(mx, max(qb[n][kk][e] & 0x7FFFu, (qb[n][kk][e] >> 16) & 0x7FFFu));
+                  }
+                }
+                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                // q * 2^(me - 127): the largest magnitude lies in [2^14, 2^15)
+                const int me = min(254, 268 - int(mx >> 7));
+                const float up = __uint_as_float(unsigned(me) << 23);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    qb[n][kk][e] = pack_f16x2(bf_lo(qb[n][kk][e]) * up, bf_hi(qb[n][kk][e]) * up);
+                const float back = P.sl2 * pow2_of(unsigned(254 - me));
+                qs[n][0] = __shfl_sync(0xffffffffu, back, 8 * c);
+                qs[n][1] = __shfl_sync(0xffffffffu, back, 8 * c + 4);
+              }
+            }
+          }
+          const int kbase = BK * (row.blk0 + j) + 16 * w + 1;
+          if (((masks[st] >> w) & 1u) && kbase <= row.p && kbase + 15 >= row.lo)
+            warp_block<FMT, C>(kb, w, qb, qs, pse_shift, kbase, row.lo, row.p, S);
+        } else if (lane == 0) {
+          misc[1] = 1;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_empty + 8 * st);
+      }
+      // ---- combine the consumer warps' partials of the pair
+      const float unit = FMT == kFmtBF16 ? 1.f : ldexpf(1.f, S.E - 127 - kBias);
+      consumer_bar<NCT>();   // the previous pair's readers of the combine area are done
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          S.l[n][0] += __shfl_xor_sync(0xffffffffu, S.l[n][0], o);
+          S.l[n][1] += __shfl_xor_sync(0xffffffffu, S.l[n][1], o);
+        }
+        const int h0 = w * C::HEADS + 8 * n + 2 * c;
+        float* ow = Ow + h0 * C::OLD;
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) {
+          const int da = FMT == kFmtBF16 ? 16 * mt + g : (D / 8) * g + 2 * mt;
+          const int db = FMT == kFmtBF16 ? da + 8 : da + 1;
+          ow[da] = S.acc[n][mt][0] * unit;
+          ow[C::OLD + da] = S.acc[n][mt][1] * unit;
+          ow[db] = S.acc[n][mt][2] * unit;
+          ow[C::OLD + db] = S.acc[n][mt][3] * unit;
+        }
+        if (g == 0) {
+          MLw[h0 * 2] = S.m[n][0];
+          MLw[h0 * 2 + 1] = S.l[n][0];
+          MLw[h0 * 2 + 2] = S.m[n][1];
+          MLw[h0 * 2 + 3] = S.l[n][1];
+        }
+      }
+      consumer_bar<NCT>();
+      if (ct < G) {
+        const int h = ct;
+        float M = kNegInf;
+#pragma unroll
+        for (int ww = 0; ww < C::NCW; ++ww) M = fmaxf(M, MLw[(ww * C::HEADS + h) * 2]);
+        float L = 0.f;
+#pragma unroll
+        for (int ww = 0; ww < C::NCW; ++ww) {
+          const float fw = M == kNegInf ? 0.f : ex2(MLw[(ww * C::HEADS + h) * 2] - M);
+          FWs[ww * C::HEADS + h] = fw;
+          L += fw * MLw[(ww * C::HEADS + h) * 2 + 1];
+        }
+        LHs[h] = L;
+        LHs[C::HEADS + h] = M;
+      }
+      consumer_bar<NCT>();
+      const bool split = j0 > 0 || j1 < row.nb;
+      const int slot = f == f_lo ? 0 : 1;   // the CTA's first pair, or its last
+      const size_t pb = (size_t(2 * blockIdx.x) + slot) * C::HEADS;
+      for (int idx = ct; idx < G * (D / 4); idx += NCT) {
+        const int h = idx / (D / 4), d = 4 * (idx - h * (D / 4));
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int ww = 0; ww < C::NCW; ++ww) {
+          const float fw = FWs[ww * C::HEADS + h];
+          const float4 v = *reinterpret_cast<const float4*>(Ow + (ww * C::HEADS + h) * C::OLD + d);
+          O.x += fw * v.x;
+          O.y += fw * v.y;
+          O.z += fw * v.z;
+          O.w += fw * v.w;
+        }
+        if (split) {
+          *reinterpret_cast<float4*>(P.part_acc + (pb + h) * D + d) = O;
+        } else {
+          finish(P, t, hk, h, d, D, O, LHs[h]);
+        }
+      }
+      if (split && ct < G) {
+        P.part_ml[(pb + ct) * 2] = LHs[C::HEADS + ct];
+        P.part_ml[(pb + ct) * 2 + 1] = LHs[ct];
+      }
+      if (j0 == 0 && j1 < row.nb)   // the pair begins here and runs on
+        join = make_int4(t, hk, (f_pair + row.nb - 1) / R - int(blockIdx.x) + 1, slot);
+      // ---- next pair
+      f = f_pair + j1;
+      j0 = 0;
+      if (++hk == P.n_kv) {
+        hk = 0;
+        do ++t;
+        while (t < T && cum[t + 1] == cum[t]);
+      }
+    }
+    if (ct == 0) P.join[blockIdx.x] = join;
+    // ---- rows that attend to nothing
+    for (int r = blockIdx.x; r < T; r += gridDim.x)
+      if (cum[r + 1] == cum[r])
+        for (int x = ct; x < P.n_q * (D / 8); x += NCT)
+          reinterpret_cast<uint4*>(P.og + size_t(r) * P.n_q * D)[x] = make_uint4(0, 0, 0, 0);
+  }
+  __syncthreads();
+  pdl_trigger();   // not earlier: the join and what follows would run beside the key stream
+  if (warp == C::NCW && lane == 0) {
+    // normally a no-op: every issued block was consumed; after an expired wait, let the
+    // copies still in flight land before the CTA's shared memory is released
+    const int n = misc[2];
+    for (int k = n > C::NST ? n - C::NST : 0; k < n; ++k)
+      mbar_wait(bar_full + 8 * (k % C::NST), (k / C::NST) & 1);
+    if (misc[1]) flag(BEAM_DEV_TIMEOUT);
+  }
+}
+
+// Join of the pair that begins in CTA blockIdx.x's range and runs on past it, one query head
+// (blockIdx.y) per CTA, one thread per output element.
+template <int D, int HEADS>
+__global__ void __launch_bounds__(D) paged_join_kernel(const Params P) {
+  pdl_trigger();
+  __shared__ float wsh[kMaxGrid], lsh[kMaxGrid];
+  pdl_wait();
+  const int4 jn = P.join[blockIdx.x];
+  const int n = jn.z, h = blockIdx.y;
+  if (n == 0) return;
+  // the first part's slot is jn.w; in the CTAs after it the pair is the first
+  auto slot = [&](int s) { return (size_t(2 * (blockIdx.x + s)) + (s == 0 ? jn.w : 0)) * HEADS + h; };
+  for (int s = threadIdx.x; s < n; s += D) {
+    const float2 v = __ldcg(reinterpret_cast<const float2*>(P.part_ml + slot(s) * 2));
+    wsh[s] = v.x;
+    lsh[s] = v.y;
+  }
+  __syncthreads();
+  float M = kNegInf;
+  for (int s = 0; s < n; ++s) M = fmaxf(M, wsh[s]);
+  float L = 0.f, O = 0.f;
+  int s = 0;
+  for (; s + 8 <= n; s += 8) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = __ldcg(P.part_acc + slot(s + u) * D + threadIdx.x);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float fw = M == kNegInf ? 0.f : ex2(wsh[s + u] - M);
+      O += fw * v[u];
+      L += fw * lsh[s + u];
+    }
+  }
+  for (; s < n; ++s) {
+    const float fw = M == kNegInf ? 0.f : ex2(wsh[s] - M);
+    O += fw * __ldcg(P.part_acc + slot(s) * D + threadIdx.x);
+    L += fw * lsh[s];
+  }
+  const int hq = jn.y * P.G + h;
+  const size_t oi = (size_t(jn.x) * P.n_q + hq) * D + threadIdx.x;
+  float o = L == 0.f ? 0.f : O / L;
+  if (P.g != nullptr) o *= sigmoidf_(bf2f(P.g[oi]) + bf2f(P.gate_bias[hq]));
+  P.og[oi] = f2bf(o);
+}
+
+int block_keys(int fmt, int D, int nt) {
+  if (fmt == kFmtBF16) return D == 128 ? Cfg<kFmtBF16, 128, 1>::BK : Cfg<kFmtBF16, 64, 1>::BK;
+  if (fmt == kFmtFP8) return Cfg<kFmtFP8, 128, 1>::BK;
+  return D == 128 && nt == 1 ? Cfg<kFmtNVFP4, 128, 1>::BK : Cfg<kFmtNVFP4, 128, 2>::BK;
+}
+
+int max_grid() {
+  const int sms = num_sms_cached();
+  return sms < kMaxGrid ? sms : kMaxGrid;
+}
+
+template <int FMT, int D, int NT>
+cudaError_t launch(const Params& p, int grid, bool join, cudaStream_t st) {
+  using C = Cfg<FMT, D, NT>;
+  const beam_paged_kv& c = p.c;
+  CUtensorMap mk, mv;
+  const int rows = C::PLANES == 2 ? c.page_size : c.page_size * C::ROWB / 128;
+  const int pse = c.page_size < C::BK ? c.page_size : C::BK;
+  const uint64_t inner = C::PLANES == 2 ? 256 : 128;
+  const uint64_t dims[3] = {inner, uint64_t(rows), uint64_t(c.num_pages) * c.n_kv};
+  const uint64_t str[2] = {inner, uint64_t(c.page_size) * C::ROWB};
+  const uint32_t box[3] = {128, uint32_t(C::PLANES == 2 ? pse : pse * C::ROWB / 128), 1};
+  if (!encode_tiled(&mk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.k, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tiled(&mv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.v, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  auto kern = paged_decode_kernel<FMT, D, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::BYTES, st, mk, mv, p);
+  if (e != cudaSuccess || !join) return e;
+  return launch_pdl(paged_join_kernel<D, C::HEADS>, dim3(grid, p.G), dim3(D), 0, st, p);
+}
+
+template <int FMT>
+cudaError_t launch_fmt(const Params& p, int grid, bool join, cudaStream_t st) {
+  const bool one = p.G <= 8;
+  if (p.c.head_dim == 128)
+    return one ? launch<FMT, 128, 1>(p, grid, join, st) : launch<FMT, 128, 2>(p, grid, join, st);
+  return one ? launch<FMT, 64, 1>(p, grid, join, st) : launch<FMT, 64, 2>(p, grid, join, st);
+}
+
+}  // namespace
+}  // namespace paged
+}  // namespace beam
+
+extern "C" size_t beam_paged_workspace_bytes(const beam_layer_cfg* cfg, int T, int max_pos) {
+  using namespace beam;
+  using namespace beam::paged;
+  (void)max_pos;
+  if (cfg == nullptr || T <= 0 || cfg->n_q <= 0 || cfg->head_dim <= 0) return 256;
+  const size_t parts = size_t(kMaxGrid) * 2 * 16;
+  return align_up(parts * cfg->head_dim * 4, 256) + align_up(parts * 2 * 4, 256) +
+         align_up(kMaxGrid * sizeof(int4), 256) +
+         align_up(size_t(T) * cfg->n_q * cfg->head_dim * 2, 256);
+}
+
+extern "C" beam_status beam_paged_attn(const beam_layer_cfg* cfg, const beam_bf16* q,
+                                       const beam_bf16* g, const beam_bf16* gate_bias,
+                                       const beam_paged_kv* cache, const int32_t* seq_id,
+                                       const int32_t* pos, int T, int max_pos,
+                                       const beam_bf16* w_o, beam_bf16* out, void* ws,
+                                       size_t ws_bytes, beam_stream_t stream) {
+  using namespace beam;
+  using namespace beam::paged;
+  beam_status stt = check_cfg_attn(cfg);
+  if (stt != BEAM_OK) return stt;
+  if ((stt = check(cache)) != BEAM_OK) return stt;
+  if (cache->n_kv != cfg->n_kv || cache->head_dim != cfg->head_dim || T < 0 || max_pos < 0)
+    return BEAM_ERR_INVALID_ARG;
+  if (T == 0) return BEAM_OK;
+  if (!q || !seq_id || !pos || !out || !ws || (g == nullptr) != (gate_bias == nullptr))
+    return BEAM_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16_or_null(g) || !aligned16_or_null(w_o) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return BEAM_ERR_INVALID_ARG;
+  if (!tc::tensor_map_encoder_ready()) return BEAM_ERR_UNSUPPORTED;
+  const int D = cfg->head_dim, HD = cfg->n_q * D, G = cfg->n_q / cfg->n_kv, nt = G > 8 ? 2 : 1;
+  const int BK = block_keys(cache->dtype, D, nt);
+  const int64_t table = int64_t(cache->table_stride) * cache->page_size;
+  const int64_t reach = max_pos < table ? max_pos : table;
+  int64_t keys = reach;
+  if (cache->window > 0 && cache->window < keys) keys = cache->window;
+  // most blocks of a pair: a window may begin anywhere in its first block
+  const int64_t nb = (keys + BK - 1) / BK + (keys < reach ? 1 : 0);
+  const int slice = T < kMaxT ? T : kMaxT;
+  if (nb * slice * cfg->n_kv > INT32_MAX) return BEAM_ERR_UNSUPPORTED;   // flat block numbers
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  Carver cv{static_cast<char*>(ws), ws_bytes};
+  const size_t parts = size_t(kMaxGrid) * 2 * 8 * nt;
+  Params p{};
+  p.part_acc = cv.take<float>(parts * D);
+  p.part_ml = cv.take<float>(parts * 2);
+  p.join = cv.take<int4>(kMaxGrid);
+  uint16_t* og = w_o ? cv.take<uint16_t>(size_t(T) * HD) : out;
+  if (!cv.ok) return BEAM_ERR_INVALID_ARG;
+  p.gate_bias = gate_bias;
+  p.c = *cache;
+  p.n_q = cfg->n_q;
+  p.n_kv = cfg->n_kv;
+  p.G = G;
+  p.max_pos = max_pos;
+  p.shift = log2i(cache->page_size);
+  p.whole = nb <= kWholeBlocks;
+  p.sl2 = float(1.4426950408889634 / sqrt(double(D)));
+  for (int t0 = 0; t0 < T; t0 += kMaxT) {   // slices in stream order share the workspace
+    p.T = T - t0 < kMaxT ? T - t0 : kMaxT;
+    p.q = q + size_t(t0) * HD;
+    p.g = g ? g + size_t(t0) * HD : nullptr;
+    p.og = og + size_t(t0) * HD;
+    p.seq_id = seq_id + t0;
+    p.pos = pos + t0;
+    int64_t grid = nb * p.T * cfg->n_kv;
+    if (p.whole) grid = int64_t(p.T) * cfg->n_kv;
+    if (grid > max_grid()) grid = max_grid();
+    if (grid < 1) grid = 1;
+    cudaError_t e;
+    if (cache->dtype == kFmtBF16) e = launch_fmt<kFmtBF16>(p, int(grid), !p.whole, st);
+    else if (cache->dtype == kFmtFP8) e = launch_fmt<kFmtFP8>(p, int(grid), !p.whole, st);
+    else e = launch_fmt<kFmtNVFP4>(p, int(grid), !p.whole, st);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  if (w_o != nullptr) {
+    const cudaError_t ge = o_proj(og, T, HD, w_o, cfg->hidden, out, st);
+    if (ge != cudaSuccess) return cuda_status(ge);
+  }
+  return BEAM_OK;
+}

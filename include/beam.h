@@ -58,6 +58,7 @@ typedef enum {
 #define BEAM_DEV_BAD_SEQ 0x2u       /* seq_id outside [0, num_seqs) */
 #define BEAM_DEV_BAD_EXPERT 0x4u    /* expert index outside [0, n_experts) */
 #define BEAM_DEV_TIMEOUT 0x8u       /* a bounded on-device wait expired (result invalid) */
+#define BEAM_DEV_BAD_PAGE 0x10u     /* page table entry outside [0, num_pages) where a key is due */
 
 typedef enum { BEAM_KV_BF16 = 0, BEAM_KV_FP8_E4M3 = 1 } beam_kv_dtype;
 
@@ -295,6 +296,109 @@ size_t beam_workspace_bytes(const beam_layer_cfg* cfg, int T, int max_pos);
 
 /* Bytes of one layer's K+V cache: 2 * num_seqs * n_kv * capacity * head_dim * elem size. */
 size_t beam_kv_cache_bytes(int num_seqs, int n_kv, int capacity, int head_dim, int dtype);
+
+/* ---- paged key-value cache ---------------------------------------------------------------
+ * A pool of pages of page_size tokens shared by all sequences, and a page table that names
+ * each sequence's pages in order: position p (1-based) of sequence s lies in page
+ * page_table[s][(p-1) / page_size] at offset (p-1) % page_size. Rows are quantised as they are
+ * written, each with its own scale, so an 8- or 4-bit cache needs no calibrated constants
+ * (beam_kv_cache's FP8 form has one scale per layer, fixed before anything is written).
+ * (The Beam page serves through a paged engine and prints no layout: the layout is this
+ * library's own; NVFP4 is the element format of beam_nvfp4_experts.)
+ *
+ * A row is the head_dim elements of one token's K or V in one KV head. Its scale is a power of
+ * two, 2^(b - 127), stored as the byte b:
+ *   BF16   the bf16 values; no scales.
+ *   FP8    e4m3 codes, one byte each. value = code * 2^(b-127), b the least byte >= 0 with
+ *          max|x| <= 448 * 2^(b-127); code = e4m3(x * 2^(127-b)).
+ *   NVFP4  e2m1 codes, two per byte (even element in the low nibble), and an e4m3 scale s for
+ *          each 16 consecutive elements. value = code * s * 2^(b-127), b the least byte >= 0
+ *          with max|x| <= 2688 * 2^(b-127); s = e4m3(max16|x| * 2^(127-b) / 6);
+ *          code = e2m1(x * 2^(127-b) / s), saturating at 6, and 0 where s is 0.
+ * All roundings are to nearest, ties to even, so the codes are the same on every run and every
+ * device. A row that holds an infinity or a NaN is stored as b = 255 with all codes and block
+ * scales 0, and reads back as NaN. Every stored value is exact in bf16 down to bf16's own
+ * smallest magnitudes. */
+typedef enum { BEAM_PAGED_BF16 = 0, BEAM_PAGED_FP8 = 1, BEAM_PAGED_NVFP4 = 2 } beam_paged_dtype;
+
+/* All arrays are device arrays, 16-byte aligned (page_table: 4-byte).
+ *  k, v         [num_pages][n_kv][page_size][2 * D | D | D / 2 bytes] (BF16 | FP8 | NVFP4)
+ *  row_scale    [num_pages][n_kv][2][page_size] bytes b, K's then V's; NULL for BF16
+ *  block_scale  [num_pages][n_kv][2][page_size][D / 16] e4m3; NVFP4 only, else NULL
+ *  page_table   [num_seqs][table_stride] int32 page numbers. Entries of pages that a call need
+ *               not touch (past a sequence's end, before its window) may hold anything.
+ *  page_size    16, 32, 64, 128 or 256, and a page of one head at least 1024 bytes of K (NVFP4
+ *               with head_dim 64: page_size >= 32); otherwise BEAM_ERR_UNSUPPORTED.
+ *  head_dim     64 or 128.
+ *  window       0 for full attention, else the sliding window W (keys p-W+1 .. p); only
+ *               beam_paged_attn reads it. A sequence may drop the pages before its window. */
+typedef struct {
+  void* k;
+  void* v;
+  uint8_t* row_scale;
+  uint8_t* block_scale;
+  const int32_t* page_table;
+  int32_t dtype; /* beam_paged_dtype */
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t n_kv;
+  int32_t head_dim;
+  int32_t num_seqs;
+  int32_t table_stride;
+  int32_t window;
+} beam_paged_kv;
+
+/* Writes the K and V rows of T tokens into the pages, quantising them to the cache's format.
+ *  k, v      (device) bf16: token t's n_kv * head_dim elements start at t * token_stride
+ *            (elements, a multiple of 8 and at least n_kv * head_dim, so rows of a packed
+ *            projection can be written as they lie); 16-byte aligned.
+ *  seq_id, pos (device) [T] int32. pos 0: a padding row, nothing is written. Out of range
+ *            (pos < 0 or past the page table, seq_id, page): the token is skipped, a bit is set.
+ * No two tokens of a call may name the same slot: what that slot then holds is undefined (no
+ * other slot is touched). Pages' other rows keep their contents. No workspace. */
+beam_status beam_paged_kv_write(const beam_bf16* k, const beam_bf16* v, int token_stride,
+                                const int32_t* seq_id, const int32_t* pos, int T,
+                                const beam_paged_kv* cache, beam_stream_t stream);
+
+/* Reads positions first[i] .. last[i] of sequence seq_id[i], i < N, back into a contiguous BF16
+ * cache, the form that beam_attn's prefill takes: row i of dst, slot (p-1) % dst->capacity.
+ *  seq_id, first, last (device) [N] int32; last < first reads nothing. A range that starts
+ *           before 1, ends past the page table, or is longer than max_len or dst->capacity is
+ *           skipped and BEAM_DEV_BAD_POSITION set; positions in a bad page are skipped and
+ *           BEAM_DEV_BAD_PAGE set. Slots that are not read into keep their contents.
+ *  max_len  host-side upper bound of last - first + 1 (sizes the grid).
+ *  dst      BF16, the cache's n_kv and head_dim, num_seqs >= N. A row of b = 255 gives NaN.
+ * The same sequence may be read into several rows. No workspace. */
+beam_status beam_paged_kv_read(const beam_paged_kv* cache, const int32_t* seq_id,
+                               const int32_t* first, const int32_t* last, int N, int max_len,
+                               const beam_kv_cache* dst, beam_stream_t stream);
+
+/* GQA attention of one new token per row over the pages, optional sigmoid output gate and
+ * o_proj: beam_attn for the paged cache, for decode batches (several rows may name the same
+ * sequence; each reads its own keys). Query head i reads KV head i / (n_q/n_kv), n_q/n_kv <= 16.
+ * Row t at position p = pos[t] attends to keys max(1, p-W+1) .. p (W = cache->window) or
+ * 1 .. p, which must have been written:
+ *   o = softmax(q.k / sqrt(D)) v in FP32;  og = bf16(o * sigmoid(g + gate_bias[head])),
+ * or og = bf16(o) where g is NULL (one rounding; beam_attn also rounds o before the gate).
+ *  q, g      (device) as in beam_attn; g and gate_bias may both be NULL (no gate).
+ *  pos       0: a padding row that attends to nothing; its output row is zero. A row whose
+ *            position or sequence is out of range (pos < 0, > max_pos or past the page table)
+ *            sets a bit and is zero too. Keys in a bad page are left out and a bit is set.
+ *  max_pos   host-side upper bound of pos[].
+ *  w_o       (device) [H][n_q*D] bf16: out = og W_o^T, [T][H]; NULL: out = og, [T][n_q*D].
+ *  ws        beam_paged_workspace_bytes(cfg, T, max_pos) bytes. */
+beam_status beam_paged_attn(const beam_layer_cfg* cfg, const beam_bf16* q, const beam_bf16* g,
+                            const beam_bf16* gate_bias, const beam_paged_kv* cache,
+                            const int32_t* seq_id, const int32_t* pos, int T, int max_pos,
+                            const beam_bf16* w_o, beam_bf16* out, void* ws, size_t ws_bytes,
+                            beam_stream_t stream);
+
+/* Workspace bytes of beam_paged_attn: at most 4 MiB, and T * n_q * head_dim * 2 more for the
+ * input of o_proj. */
+size_t beam_paged_workspace_bytes(const beam_layer_cfg* cfg, int T, int max_pos);
+
+/* Bytes of a paged cache of num_pages pages, scales included (the page table is not). */
+size_t beam_paged_kv_bytes(int num_pages, int n_kv, int page_size, int head_dim, int dtype);
 
 /* Reads and clears the current device's status word (BEAM_DEV_* bits); synchronises
  * `stream` first. */
