@@ -158,6 +158,17 @@ class LayerCfg:
                          self.n_experts, self.n_groups, self.topk_groups, self.topk,
                          self.d_ff_expert, self.d_ff_dense, self.route_scale)
 
+    def __setattr__(self, name, value):
+        self.__dict__.pop("_kept", None)
+        self.__dict__[name] = value
+
+    def _ref(self):
+        """Reference to a C struct of the present values, built again after a change."""
+        kept = self.__dict__.get("_kept")
+        if kept is None:
+            kept = self.__dict__["_kept"] = self.c()
+        return ctypes.byref(kept)
+
 
 @dataclasses.dataclass
 class KVCache:
@@ -178,16 +189,31 @@ class KVCache:
                         self.v_scale, self.k.shape[0], self.k.shape[2], self.window)
 
 
-def _want(name, t, dtype, shape=None):
-    """Refuses a tensor that the library would read as something else: another type, another
-    device than the current one, a shape or strides that are not the documented ones."""
-    if t.dtype != dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
-        raise BeamError(f"{name}: a contiguous {dtype} tensor"
-                        f"{'' if shape is None else ' of shape ' + str(tuple(shape))} is wanted, "
-                        f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
-    if t.get_device() != torch.cuda.current_device():
-        raise BeamError(f"{name}: on {t.device}, but the current device is "
+def _refuse(name, t, dtype, shape, device):
+    want = f"a contiguous {dtype} tensor" + ("" if shape is None else f" of shape {tuple(shape)}")
+    raise BeamError(f"{name}: {want} on cuda:{device} is wanted, got {t.dtype} {tuple(t.shape)} "
+                    f"with strides {t.stride()} on {t.device}")
+
+
+def _want(device, name, t, dtype, shape=None):
+    """Refuses a tensor that the library would read as something else: another type or device,
+    a shape or strides that are not the documented ones."""
+    if (t.dtype != dtype or not t.is_contiguous() or (shape is not None and t.shape != shape) or
+            t.get_device() != device):
+        _refuse(name, t, dtype, shape, device)
+
+
+def _on_device(cache):
+    """The cache's device, which has to be the current one: the library launches there."""
+    if cache.device != torch.cuda.current_device():
+        raise BeamError(f"the cache is on cuda:{cache.device}, but the current device is "
                         f"cuda:{torch.cuda.current_device()}")
+    return cache.device
+
+
+def _raw_stream(stream, device):
+    """The handle of `stream`, or of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 class PagedKVCache:
@@ -208,23 +234,26 @@ class PagedKVCache:
                             "page_table [num_seqs][pages]")
         pages, n_kv, size, width = k.shape
         code = torch.bfloat16 if row_scale is None else torch.uint8
-        _want("k", k, code)
-        _want("v", v, code, k.shape)
-        _want("page_table", page_table, torch.int32)
+        dev = k.get_device()
+        _want(dev, "k", k, code)
+        _want(dev, "v", v, code, k.shape)
+        _want(dev, "page_table", page_table, torch.int32)
         self.dtype = BEAM_PAGED_BF16
         if row_scale is not None:
-            _want("row_scale", row_scale, torch.uint8, (pages, n_kv, 2, size))
+            _want(dev, "row_scale", row_scale, torch.uint8, (pages, n_kv, 2, size))
             self.dtype = BEAM_PAGED_FP8
         if block_scale is not None:
             if row_scale is None:
                 raise BeamError("PagedKVCache: block_scale without row_scale")
             width *= 2
-            _want("block_scale", block_scale, torch.uint8, (pages, n_kv, 2, size, width // 16))
+            _want(dev, "block_scale", block_scale, torch.uint8, (pages, n_kv, 2, size, width // 16))
             self.dtype = BEAM_PAGED_NVFP4
+        if dev < 0:
+            raise BeamError("PagedKVCache: the tensors must be on a CUDA device")
         self.k, self.v, self.page_table = k, v, page_table
         self.row_scale, self.block_scale, self.window = row_scale, block_scale, int(window)
         self.n_kv, self.page_size, self.head_dim = n_kv, size, width
-        self.device = k.get_device()
+        self.device = dev
         self._c = PagedKVC(k.data_ptr(), v.data_ptr(),
                            0 if row_scale is None else row_scale.data_ptr(),
                            0 if block_scale is None else block_scale.data_ptr(),
@@ -249,9 +278,6 @@ class PagedKVCache:
                                 dtype=torch.uint8, device=dev)
         return cls(torch.zeros(dims, dtype=kind, device=dev),
                    torch.zeros(dims, dtype=kind, device=dev), page_table, row, block, window)
-
-    def c(self):
-        return self._ref
 
 
 class Workspace:
@@ -331,62 +357,78 @@ def paged_kv_bytes(num_pages, n_kv, page_size, head_dim, dtype=BEAM_PAGED_BF16) 
 def beam_paged_kv_write(k, v, seq_id, pos, cache: PagedKVCache, stream=None):
     """k, v [T][n_kv][D] bf16 (rows of a token contiguous, any stride between tokens that is a
     multiple of 8) into the cache's pages."""
-    T = k.shape[0]
+    dev = _on_device(cache)
+    n_kv, D = cache.n_kv, cache.head_dim
+    T, step = k.shape[0], n_kv * D
     for name, x in (("k", k), ("v", v)):
-        if (x.dtype != torch.bfloat16 or x.shape != (T, cache.n_kv, cache.head_dim) or
-                (T and (x.stride(2) != 1 or (cache.n_kv > 1 and x.stride(1) != cache.head_dim))) or
-                x.get_device() != cache.device):
-            raise BeamError(f"beam_paged_kv_write: {name} must be bf16 [T][{cache.n_kv}]"
-                            f"[{cache.head_dim}] with contiguous rows on the cache's device")
-    if T > 1 and k.stride(0) != v.stride(0):
-        raise BeamError("beam_paged_kv_write: k and v have different strides between tokens")
-    _want("seq_id", seq_id, torch.int32, (T,))
-    _want("pos", pos, torch.int32, (T,))
-    _check(lib().beam_paged_kv_write(_ptr(k), _ptr(v),
-                                     k.stride(0) if T > 1 else cache.n_kv * cache.head_dim,
-                                     _ptr(seq_id), _ptr(pos), T, cache.c(), _stream(stream)),
-           "beam_paged_kv_write")
+        if x.dtype != torch.bfloat16 or x.shape != (T, n_kv, D) or x.get_device() != dev:
+            _refuse(name, x, torch.bfloat16, (T, n_kv, D), dev)
+        if T and not x.is_contiguous():
+            s0, s1, s2 = x.stride()
+            if s2 != 1 or (n_kv > 1 and s1 != D):
+                raise BeamError(f"beam_paged_kv_write: the rows of a token of {name} must be "
+                                f"contiguous, got strides {x.stride()}")
+    if T > 1:
+        step = k.stride(0)
+        if v.stride(0) != step:
+            raise BeamError("beam_paged_kv_write: k and v have different strides between tokens")
+    _want(dev, "seq_id", seq_id, torch.int32, (T,))
+    _want(dev, "pos", pos, torch.int32, (T,))
+    st = lib().beam_paged_kv_write(k.data_ptr(), v.data_ptr(), step, seq_id.data_ptr(),
+                                   pos.data_ptr(), T, cache._ref, _raw_stream(stream, dev))
+    if st:
+        _check(st, "beam_paged_kv_write")
 
 
 def beam_paged_kv_read(cache: PagedKVCache, seq_id, first, last, max_len, dst: KVCache,
                        stream=None):
     """Positions first[i]..last[i] of sequence seq_id[i] into row i of the contiguous BF16 cache
     dst, slot (p-1) % capacity."""
+    dev = _on_device(cache)
     N = seq_id.shape[0]
-    _want("seq_id", seq_id, torch.int32, (N,))
-    _want("first", first, torch.int32, (N,))
-    _want("last", last, torch.int32, (N,))
-    if dst.fp8:
-        raise BeamError("beam_paged_kv_read: the destination cache is BF16")
-    dims = (dst.k.shape[0], cache.n_kv, dst.k.shape[2], cache.head_dim)
-    _want("dst.k", dst.k, torch.bfloat16, dims)
-    _want("dst.v", dst.v, torch.bfloat16, dims)
+    _want(dev, "seq_id", seq_id, torch.int32, (N,))
+    _want(dev, "first", first, torch.int32, (N,))
+    _want(dev, "last", last, torch.int32, (N,))
+    rows, _, cap, _ = dst.k.shape
+    dims = (rows, cache.n_kv, cap, cache.head_dim)
+    _want(dev, "dst.k", dst.k, torch.bfloat16, dims)
+    _want(dev, "dst.v", dst.v, torch.bfloat16, dims)
     kc = dst.c()
-    _check(lib().beam_paged_kv_read(cache.c(), _ptr(seq_id), _ptr(first), _ptr(last), N,
-                                    int(max_len), ctypes.byref(kc), _stream(stream)),
-           "beam_paged_kv_read")
+    st = lib().beam_paged_kv_read(cache._ref, seq_id.data_ptr(), first.data_ptr(),
+                                  last.data_ptr(), N, int(max_len), ctypes.byref(kc),
+                                  _raw_stream(stream, dev))
+    if st:
+        _check(st, "beam_paged_kv_read")
 
 
 def beam_paged_attn(cfg: LayerCfg, q, g, gate_bias, cache: PagedKVCache, seq_id, pos, max_pos,
                     w_o, out, ws: torch.Tensor, stream=None):
     """Decode attention over the pages; g, gate_bias None: no gate; w_o None: out is [T][n_q*D]."""
-    T, bf = q.shape[0], torch.bfloat16
-    _want("q", q, bf, (T, cfg.n_q, cfg.head_dim))
+    dev, bf = _on_device(cache), torch.bfloat16
+    T, n_q, D = q.shape[0], cfg.n_q, cfg.head_dim
+    _want(dev, "q", q, bf, (T, n_q, D))
+    pg = pb = pw = None
     if (g is None) != (gate_bias is None):
         raise BeamError("beam_paged_attn: g and gate_bias go together")
     if g is not None:
-        _want("g", g, bf, (T, cfg.n_q * cfg.head_dim))
-        _want("gate_bias", gate_bias, bf, (cfg.n_q,))
+        _want(dev, "g", g, bf, (T, n_q * D))
+        _want(dev, "gate_bias", gate_bias, bf, (n_q,))
+        pg, pb = g.data_ptr(), gate_bias.data_ptr()
+    width = n_q * D
     if w_o is not None:
-        _want("w_o", w_o, bf, (cfg.hidden, cfg.n_q * cfg.head_dim))
-    _want("out", out, bf, (T, cfg.n_q * cfg.head_dim if w_o is None else cfg.hidden))
-    _want("seq_id", seq_id, torch.int32, (T,))
-    _want("pos", pos, torch.int32, (T,))
-    c = cfg.c()
-    _check(lib().beam_paged_attn(ctypes.byref(c), _ptr(q), _ptr(g), _ptr(gate_bias), cache.c(),
-                                 _ptr(seq_id), _ptr(pos), T, int(max_pos), _ptr(w_o), _ptr(out),
-                                 _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
-           "beam_paged_attn")
+        width = cfg.hidden
+        _want(dev, "w_o", w_o, bf, (width, n_q * D))
+        pw = w_o.data_ptr()
+    _want(dev, "out", out, bf, (T, width))
+    _want(dev, "seq_id", seq_id, torch.int32, (T,))
+    _want(dev, "pos", pos, torch.int32, (T,))
+    _want(dev, "ws", ws, torch.uint8)
+    st = lib().beam_paged_attn(cfg._ref(), q.data_ptr(), pg, pb, cache._ref,
+                               seq_id.data_ptr(), pos.data_ptr(), T, int(max_pos), pw,
+                               out.data_ptr(), ws.data_ptr(), ws.numel(),
+                               _raw_stream(stream, dev))
+    if st:
+        _check(st, "beam_paged_attn")
 
 
 class NvFp4ExpertsC(ctypes.Structure):

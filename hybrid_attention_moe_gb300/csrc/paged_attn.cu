@@ -45,6 +45,7 @@ namespace {
 using namespace beam::tc;
 
 constexpr float kNegInf = -INFINITY;
+constexpr float kLowest = -3e38f;   // a running max that has seen nothing: finite, so differences are
 constexpr float kRescale = 8.f;     // log2 units by which the running max may lag
 constexpr int kMaxGrid = 152;       // CTAs, and so parts of one pair, at most
 constexpr int kMaxT = 1024;         // rows of one launch
@@ -56,27 +57,30 @@ struct Cfg {
   static constexpr int D = D_, NT = NT_, HEADS = 8 * NT;
   static constexpr int ROWB = row_bytes(FMT, D);
   static constexpr int PLANES = ROWB > 128 ? 2 : 1;   // 128-byte columns of a row
-  // consumer warps, 16 keys each: a block holds 32 KB of K and V where that fits
-  static constexpr int NCW = FMT == kFmtBF16 ? (D == 128 ? 4 : 8)
-                             : FMT == kFmtNVFP4 && D == 128 && NT == 1 ? 16 : 8;
+  // consumer warps, and 16-key slices that each takes of a block: a block holds 32 KB of K and V
+  // where that fits
+  static constexpr int NCW = FMT == kFmtBF16 && D == 128 ? 4 : 8;
+  static constexpr int SPW = FMT == kFmtNVFP4 && D == 128 && NT == 1 ? 2 : 1;
   static constexpr int THREADS = (NCW + 1) * 32;
-  static constexpr int BK = 16 * NCW;
+  static constexpr int SLICES = NCW * SPW, BK = 16 * SLICES;
   static constexpr int KB = BK * ROWB;
   static constexpr int BSB = FMT == kFmtNVFP4 ? 2 * BK * (D / 16) : 0;
   static constexpr int RSB = FMT != kFmtBF16 ? 2 * BK : 0;
   static constexpr int QB = HEADS * D * 2;
   static constexpr int OBS = 2 * KB, ORS = OBS + BSB, OQ = ORS + RSB;   // offsets in a stage
   static constexpr int STAGE = (OQ + QB + 1023) / 1024 * 1024;
-  static constexpr int NST = FMT == kFmtNVFP4 && NCW == 16 ? 3 : 4;
   static constexpr int OLD = D + 4;   // row stride of the combine buffer (floats)
-  static constexpr int OW = NST * STAGE;                         // [NCW][HEADS][OLD]
-  static constexpr int MLW = OW + NCW * HEADS * OLD * 4;         // [NCW][HEADS][2]
-  static constexpr int FW = MLW + NCW * HEADS * 2 * 4;           // [NCW][HEADS]
-  static constexpr int LH = FW + NCW * HEADS * 4;                // [HEADS] sums, maxima
-  static constexpr int CUM = LH + 2 * HEADS * 4;                 // [kMaxT + 1] block prefix
-  static constexpr int MISC = (CUM + (kMaxT + 1) * 4 + 15) / 16 * 16;   // -, abort, issued, -; masks
+  static constexpr int OWB = NCW * HEADS * OLD * 4, MLB = NCW * HEADS * 2 * 4;
+  static constexpr int NOW = NT == 1 ? 2 : 1;             // combine buffers
+  static constexpr int NST = 4 * STAGE + NOW * (OWB + MLB) <= 216 * 1024 ? 4 : 3;
+  static constexpr int OW = NST * STAGE;                  // [NOW][NCW][HEADS][OLD]: O partials
+  static constexpr int MLW = OW + NOW * OWB;              // [NOW][NCW][HEADS][2]: (m, l)
+  static constexpr int CUM = MLW + NOW * MLB;             // [kMaxT + 1] block prefix
+  static constexpr int POS = CUM + (kMaxT + 1) * 4;       // [kMaxT] positions
+  static constexpr int MISC = (POS + kMaxT * 4 + 15) / 16 * 16;   // -, abort, issued, -; masks
   static constexpr int BAR = MISC + 16 + 16;
-  static constexpr int BYTES = BAR + 2 * NST * 8 + 1024;         // + alignment slack
+  static constexpr int BYTES = BAR + 2 * NST * 8 + 1024;  // + alignment slack
+  static constexpr int ITEMS = (HEADS * (D / 4) + NCW * 32 - 1) / (NCW * 32);   // finished outputs
   static_assert(BYTES <= 227 * 1024, "stage ring exceeds shared memory");
   static_assert(NST <= 4, "one mask word per stage");
 };
@@ -184,166 +188,208 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // Byte o of a region of 128-byte rows under the 128-byte TMA swizzle.
 __device__ __forceinline__ uint32_t sw(uint32_t o) { return o ^ (((o >> 7) & 7u) << 4); }
 
-template <int N>
-__device__ constexpr int log2_of() {
-  return N <= 1 ? 0 : 1 + log2_of<(N > 1 ? N / 2 : 1)>();
-}
-
-// The four outputs from column d of query head h of a pair's KV group.
-__device__ __forceinline__ void finish(const Params& P, int t, int hk, int h, int d, int D,
-                                       float4 O, float L) {
-  const int hq = hk * P.G + h;
-  const size_t oi = (size_t(t) * P.n_q + hq) * D + d;
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  float o[4] = {O.x * inv, O.y * inv, O.z * inv, O.w * inv};
-  if (P.g != nullptr) {
-    const float gb = bf2f(P.gate_bias[hq]);
-    const uint2 gv = *reinterpret_cast<const uint2*>(P.g + oi);
-    o[0] *= sigmoidf_(bf_lo(gv.x) + gb);
-    o[1] *= sigmoidf_(bf_hi(gv.x) + gb);
-    o[2] *= sigmoidf_(bf_lo(gv.y) + gb);
-    o[3] *= sigmoidf_(bf_hi(gv.y) + gb);
-  }
-  *reinterpret_cast<uint2*>(P.og + oi) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
-}
-
 // The state of one warp over its keys of a pair.
 template <class C>
 struct WarpState {
-  float m[C::NT][2], l[C::NT][2];
+  float m[C::NT][2], l[C::NT][2];   // running max (lags by up to kRescale) and sum, heads 2c, 2c+1
   float acc[C::NT][C::D / 16][4];
   int E;   // quantised caches: the largest scale byte of a value row so far
 };
 
-// One warp's 16 keys of a staged block. kb: the stage; kbase: position of the warp's first key;
-// the row's keys are positions [lo, p]. qs: FP32 factor of the logits per accumulator column.
+// Offsets in a stage that a lane uses for every block.
 template <int FMT, class C>
-__device__ __forceinline__ void warp_block(uint32_t kb, int w, const uint32_t (&qb)[C::NT][C::D / 16][2],
-                                           const float (&qs)[C::NT][2], int pse_shift, int kbase,
-                                           int lo, int p, WarpState<C>& S) {
-  constexpr int D = C::D, NT = C::NT, KK = D / 16;
+struct Lane {
+  uint32_t k[2], v[4];   // codes of its keys: K rows g, g + 8; V rows 2c, 2c + 1, 2c + 8, 2c + 9
+  int rs, pse;           // scale index of the slice's first key, and from K's scales to V's
+};
+template <int FMT, class C>
+__device__ __forceinline__ Lane<FMT, C> lane_of(int slice, int pse) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const uint32_t vb = kb + C::KB;
-  float sa[NT][4], sb[NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sa[n][e] = sb[n][e] = 0.f;
-  // Offset of a key's scale in the staged [page][K | V][key of the page] order.
-  auto srow = [&](int key, int kv) {
-    return ((((key >> pse_shift) << 1) + kv) << pse_shift) + (key & ((1 << pse_shift) - 1));
-  };
-  // ---- S^T = K . Q^T
+  Lane<FMT, C> r;
   if constexpr (FMT == kFmtBF16) {
-    const int rk = 16 * w + ((lane >> 3) & 1) * 8 + (lane & 7), ck = (lane >> 4) & 1;
-#pragma unroll
-    for (int kk = 0; kk < KK; ++kk) {
-      uint32_t a[4];
-      const uint32_t off = (kk >> 2) * (C::KB / C::PLANES) + rk * 128 + (((2 * (kk & 3) + ck) ^ (lane & 7)) << 4);
-      ldsm_x4(kb + off, a[0], a[1], a[2], a[3]);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) mma_bf16((kk & 1) ? sb[n] : sa[n], a, qb[n][kk][0], qb[n][kk][1]);
-    }
+    // ldmatrix rows; the k step (or m tile) e XORs e << 5 into the chunk, 128-byte swizzle
+    const int rk = 16 * slice + ((lane >> 3) & 1) * 8 + (lane & 7), ck = (lane >> 4) & 1;
+    const int rv = 16 * slice + ((lane >> 4) & 1) * 8 + (lane & 7), cv = (lane >> 3) & 1;
+    r.k[0] = uint32_t(rk * 128 + ((ck ^ (lane & 7)) << 4));
+    r.v[0] = uint32_t(rv * 128 + ((cv ^ (lane & 7)) << 4)) + C::KB;
   } else {
-    // a thread's codes of keys g and g + 8: the d range [c D/4, (c + 1) D/4), four of a k step
-    constexpr int KW = C::ROWB / 16;   // words of a key in one thread
-    uint32_t w0[KW], w1[KW];
-    const uint32_t o0 = (16 * w + g) * C::ROWB + c * (C::ROWB / 4), o1 = o0 + 8 * C::ROWB;
-    if constexpr (KW == 8) {
-      lds<4>(kb + sw(o0), w0);
-      lds<4>(kb + sw(o0 + 16), w0 + 4);
-      lds<4>(kb + sw(o1), w1);
-      lds<4>(kb + sw(o1 + 16), w1 + 4);
-    } else {
-      lds<KW>(kb + sw(o0), w0);
-      lds<KW>(kb + sw(o1), w1);
-    }
-    if constexpr (FMT == kFmtFP8) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      r.k[e] = sw((16 * slice + g + 8 * e) * C::ROWB + c * (C::ROWB / 4));
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      r.v[e] = C::KB + sw((16 * slice + 2 * c + (e & 1) + 8 * (e >> 1)) * C::ROWB + g * (C::ROWB / 8));
+  }
+  // scales lie as [page][K | V][key of the page]; a slice lies in one page
+  const int key = 16 * slice;
+  r.rs = (key / pse) * 2 * pse + (key & (pse - 1));
+  r.pse = pse;
+  return r;
+}
+
+// One warp's slices (SPW of 16 keys) of a staged block. kb: the stage; kbase[i]: position of
+// slice i's first key; live: bit i, slice i has keys; the row's keys are positions [lo, p].
+// qs: FP32 factor of the logits per accumulator column.
+template <int FMT, class C>
+__device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)[C::SPW],
+                                           const uint32_t (&qb)[C::NT][C::D / 16][2],
+                                           const float (&qs)[C::NT][2], const int (&kbase)[C::SPW],
+                                           unsigned live, int lo, int p, WarpState<C>& S) {
+  constexpr int D = C::D, NT = C::NT, KK = D / 16, SPW = C::SPW;
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  float sx[SPW][NT][4];
+  bool full[SPW];
+#pragma unroll
+  for (int i = 0; i < SPW; ++i)
+    full[i] = ((live >> i) & 1u) && kbase[i] >= lo && kbase[i] + 15 <= p;
+  auto valid = [&](int i, int key) {
+    return ((live >> i) & 1u) && kbase[i] + key >= lo && kbase[i] + key <= p;
+  };
+  // ---- S^T = K . Q^T, two accumulation chains per tile
+#pragma unroll
+  for (int i = 0; i < SPW; ++i) {
+    float sb[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sx[i][n][e] = sb[n][e] = 0.f;
+    if constexpr (FMT == kFmtBF16) {
 #pragma unroll
       for (int kk = 0; kk < KK; ++kk) {
         uint32_t a[4];
-        e4m3x4_f16(w0[kk], a[0], a[2]);
-        e4m3x4_f16(w1[kk], a[1], a[3]);
+        ldsm_x4(kb + (kk >> 2) * (C::KB / C::PLANES) + (ln[i].k[0] ^ uint32_t((kk & 3) << 5)), a[0], a[1], a[2], a[3]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma_f16((kk & 1) ? sb[n] : sa[n], a, qb[n][kk][0], qb[n][kk][1]);
+        for (int n = 0; n < NT; ++n) mma_bf16((kk & 1) ? sb[n] : sx[i][n], a, qb[n][kk][0], qb[n][kk][1]);
       }
     } else {
-      // block scales of the thread's d range: two blocks (D 128) or one (D 64)
-      const uint32_t s0 = kb + C::OBS + srow(16 * w + g, 0) * (D / 16);
-      const uint32_t s1 = kb + C::OBS + srow(16 * w + g + 8, 0) * (D / 16);
-      uint32_t f0, f1;
-      if constexpr (D == 128) {
-        f0 = e4m3x2_f16x2(lds_u16(s0 + 2 * c));
-        f1 = e4m3x2_f16x2(lds_u16(s1 + 2 * c));
+      // a thread's codes of keys g and g + 8: the d range [c D/4, (c + 1) D/4), four of a k step
+      constexpr int KW = C::ROWB / 16;   // words of a key in one thread
+      uint32_t w0[KW], w1[KW];
+      if constexpr (KW == 8) {
+        lds<4>(kb + ln[i].k[0], w0);
+        lds<4>(kb + (ln[i].k[0] ^ 16u), w0 + 4);
+        lds<4>(kb + ln[i].k[1], w1);
+        lds<4>(kb + (ln[i].k[1] ^ 16u), w1 + 4);
       } else {
-        f0 = e4m3x2_f16x2(lds_u8(s0 + c) * 0x101u);
-        f1 = e4m3x2_f16x2(lds_u8(s1 + c) * 0x101u);
+        lds<KW>(kb + ln[i].k[0], w0);
+        lds<KW>(kb + ln[i].k[1], w1);
       }
+      if constexpr (FMT == kFmtFP8) {
 #pragma unroll
-      for (int j = 0; j < KW; ++j) {   // a word: the codes of two k steps
-        uint32_t h0[4], h1[4];
-        e2m1x8_f16(w0[j], h0);
-        e2m1x8_f16(w1[j], h1);
-        const uint32_t sel = D == 64 ? 0x3210u : (j < KW / 2 ? 0x1010u : 0x3232u);
-        const uint32_t b0 = prmt(f0, f0, sel), b1 = prmt(f1, f1, sel);
+        for (int kk = 0; kk < KK; ++kk) {
+          uint32_t a[4];
+          e4m3x4_f16(w0[kk], a[0], a[2]);
+          e4m3x4_f16(w1[kk], a[1], a[3]);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t a[4] = {mul_f16x2(h0[2 * e], b0), mul_f16x2(h1[2 * e], b1),
-                                 mul_f16x2(h0[2 * e + 1], b0), mul_f16x2(h1[2 * e + 1], b1)};
+          for (int n = 0; n < NT; ++n) mma_f16((kk & 1) ? sb[n] : sx[i][n], a, qb[n][kk][0], qb[n][kk][1]);
+        }
+      } else {
+        // block scales of the thread's d range: two blocks (D 128) or one (D 64)
+        const uint32_t s0 = kb + C::OBS + (ln[i].rs + g) * (D / 16);
+        uint32_t f0, f1;
+        if constexpr (D == 128) {
+          f0 = e4m3x2_f16x2(lds_u16(s0 + 2 * c));
+          f1 = e4m3x2_f16x2(lds_u16(s0 + 8 * (D / 16) + 2 * c));
+        } else {
+          f0 = e4m3x2_f16x2(lds_u8(s0 + c) * 0x101u);
+          f1 = e4m3x2_f16x2(lds_u8(s0 + 8 * (D / 16) + c) * 0x101u);
+        }
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma_f16(e ? sb[n] : sa[n], a, qb[n][2 * j + e][0], qb[n][2 * j + e][1]);
+        for (int j = 0; j < KW; ++j) {   // a word: the codes of two k steps
+          uint32_t h0[4], h1[4];
+          e2m1x8_f16(w0[j], h0);
+          e2m1x8_f16(w1[j], h1);
+          const uint32_t sel = D == 64 ? 0x3210u : (j < KW / 2 ? 0x1010u : 0x3232u);
+          const uint32_t b0 = prmt(f0, f0, sel), b1 = prmt(f1, f1, sel);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t a[4] = {mul_f16x2(h0[2 * e], b0), mul_f16x2(h1[2 * e], b1),
+                                   mul_f16x2(h0[2 * e + 1], b0), mul_f16x2(h1[2 * e + 1], b1)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma_f16(e ? sb[n] : sx[i][n], a, qb[n][2 * j + e][0], qb[n][2 * j + e][1]);
+          }
         }
       }
     }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sx[i][n][e] += sb[n][e];
   }
-  // ---- logits, running max. S^T fragment: [0] (key g, head 2c), [1] (g, 2c+1), [2], [3] key g + 8
-  const int kp0 = kbase + g;
-  const bool v0 = kp0 >= lo && kp0 <= p, v1 = kp0 + 8 >= lo && kp0 + 8 <= p;
-  float ks0 = 1.f, ks1 = 1.f;
-  int e0 = 0, e1 = 0;   // scale bytes of the value rows
-  if constexpr (FMT != kFmtBF16) {
-    const uint32_t rs = kb + C::ORS;
-    ks0 = pow2_of(lds_u8(rs + srow(16 * w + g, 0)));
-    ks1 = pow2_of(lds_u8(rs + srow(16 * w + g + 8, 0)));
-    e0 = int(lds_u8(rs + srow(16 * w + g, 1)));
-    e1 = int(lds_u8(rs + srow(16 * w + g + 8, 1)));
-    const int top = __reduce_max_sync(0xffffffffu, max(v0 && e0 != 255 ? e0 : 0, v1 && e1 != 255 ? e1 : 0));
-    if (top > S.E) {   // the accumulators hold values relative to 2^E
-      const float f = ex2(float(S.E - top));
+  // ---- logits relative to the running max, in log2 units. S^T fragment: [0] (key g, head 2c),
+  // [1] (g, 2c+1), [2], [3] key g + 8. Whether any exceeds it by kRescale is one vote; the
+  // max itself is taken across the warp only then.
+  int ev[SPW][2];        // scale bytes of the value rows (quantised caches)
+  float y[SPW][NT][4];
+  bool over = false;
+#pragma unroll
+  for (int i = 0; i < SPW; ++i) {
+    float ks[2] = {1.f, 1.f};
+    if constexpr (FMT != kFmtBF16) {
+      const uint32_t rs = kb + C::ORS + ln[i].rs + g;
+      ks[0] = pow2_of(lds_u8(rs));
+      ks[1] = pow2_of(lds_u8(rs + 8));
+      ev[i][0] = int(lds_u8(rs + ln[i].pse));
+      ev[i][1] = int(lds_u8(rs + ln[i].pse + 8));
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float f = FMT == kFmtBF16 ? qs[n][e & 1] : qs[n][e & 1] * ks[e >> 1];
+        sx[i][n][e] *= f;
+      }
+    if (!full[i]) {   // keys that are not the row's weigh nothing, whatever their slots hold
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (valid(i, g + 8 * h)) continue;
+        ev[i][h] = 0;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) sx[i][n][2 * h] = sx[i][n][2 * h + 1] = kNegInf;
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[i][n][e] = sx[i][n][e] - S.m[n][e & 1];
+        over |= y[i][n][e] > kRescale;
+      }
+    if constexpr (FMT != kFmtBF16)
+      over |= (ev[i][0] != 255 && ev[i][0] > S.E) || (ev[i][1] != 255 && ev[i][1] > S.E);
+  }
+  if (__any_sync(0xffffffffu, over)) {
+    float unit = 1.f;   // the accumulators hold values relative to 2^E
+    if constexpr (FMT != kFmtBF16) {
+      int top = S.E;
+#pragma unroll
+      for (int i = 0; i < SPW; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) top = ev[i][h] != 255 ? max(top, ev[i][h]) : top;
+      top = __reduce_max_sync(0xffffffffu, top);
+      unit = ex2(float(S.E - top));
       S.E = top;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int mt = 0; mt < KK; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) S.acc[n][mt][e] *= f;
     }
-  }
-  uint32_t bh[NT][2], bl[NT][2];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    float x[4];
-    x[0] = v0 ? (sa[n][0] + sb[n][0]) * (qs[n][0] * ks0) : kNegInf;
-    x[1] = v0 ? (sa[n][1] + sb[n][1]) * (qs[n][1] * ks0) : kNegInf;
-    x[2] = v1 ? (sa[n][2] + sb[n][2]) * (qs[n][0] * ks1) : kNegInf;
-    x[3] = v1 ? (sa[n][3] + sb[n][3]) * (qs[n][1] * ks1) : kNegInf;
-    float mh[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      mh[0] = fmaxf(mh[0], __shfl_xor_sync(0xffffffffu, mh[0], o));
-      mh[1] = fmaxf(mh[1], __shfl_xor_sync(0xffffffffu, mh[1], o));
-    }
-    float(&m)[2] = S.m[n];
-    float(&l)[2] = S.l[n];
-    if (__any_sync(0xffffffffu, mh[0] > m[0] + kRescale || mh[1] > m[1] + kRescale)) {
+    for (int n = 0; n < NT; ++n) {
       float cr[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float mn = fmaxf(m[h], mh[h]);
-        cr[h] = m[h] == kNegInf ? 0.f : ex2(m[h] - mn);
-        m[h] = mn;
-        l[h] *= cr[h];
+        float mn = S.m[n][h];
+#pragma unroll
+        for (int i = 0; i < SPW; ++i) mn = fmaxf(mn, fmaxf(sx[i][n][h], sx[i][n][2 + h]));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        cr[h] = ex2(S.m[n][h] - mn);
+        S.m[n][h] = mn;
+        S.l[n][h] *= cr[h];
+#pragma unroll
+        for (int i = 0; i < SPW; ++i) {
+          y[i][n][h] = sx[i][n][h] - mn;
+          y[i][n][2 + h] = sx[i][n][2 + h] - mn;
+        }
+        cr[h] *= unit;
       }
 #pragma unroll
       for (int mt = 0; mt < KK; ++mt) {
@@ -353,119 +399,113 @@ __device__ __forceinline__ void warp_block(uint32_t kb, int w, const uint32_t (&
         S.acc[n][mt][3] *= cr[1];
       }
     }
-    const float ms0 = m[0] == kNegInf ? 0.f : m[0], ms1 = m[1] == kNegInf ? 0.f : m[1];
-    float p0 = ex2(x[0] - ms0), p1 = ex2(x[1] - ms1);
-    float p2 = ex2(x[2] - ms0), p3 = ex2(x[3] - ms1);
-    l[0] += p0 + p2;
-    l[1] += p1 + p3;
-    // P (key rows, head columns) as hi + lo, then transposed into the B fragments of P^T:
-    // b0 = (keys 2c, 2c+1; head g), b1 = (keys 2c+8, 2c+9; head g)
-    uint32_t h01, h23, l01, l23;
-    if constexpr (FMT == kFmtBF16) {
-      h01 = pack_bf16x2(p0, p1);
-      h23 = pack_bf16x2(p2, p3);
-      l01 = pack_bf16x2(p0 - bf_lo(h01), p1 - bf_hi(h01));
-      l23 = pack_bf16x2(p2 - bf_lo(h23), p3 - bf_hi(h23));
-    } else {
-      // 2^(e - E + kBias); NaN for a row that holds no numbers; a key that is not the row's
-      // weighs exactly nothing whatever its scale byte says
-      auto rel = [&](int e) {
-        const int b = e - S.E + 127 + kBias;
-        return e == 255 ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float(b > 0 ? unsigned(b) << 23 : 0u);
-      };
-      const float vs0 = v0 ? rel(e0) : 0.f, vs1 = v1 ? rel(e1) : 0.f;
-      p0 *= vs0;
-      p1 *= vs0;
-      p2 *= vs1;
-      p3 *= vs1;
-      float f0, f1, f2, f3;
-      h01 = pack_f16x2(p0, p1);
-      h23 = pack_f16x2(p2, p3);
-      unpack_f16(h01, f0, f1);
-      unpack_f16(h23, f2, f3);
-      l01 = pack_f16x2(p0 - f0, p1 - f1);
-      l23 = pack_f16x2(p2 - f2, p3 - f3);
-    }
-    bh[n][0] = movtrans(h01);
-    bh[n][1] = movtrans(h23);
-    bl[n][0] = movtrans(l01);
-    bl[n][1] = movtrans(l23);
   }
-  // ---- O^T += V^T . P^T. Keys outside [lo, p] (whose slots may hold anything, NaN included)
-  // have their values replaced by zeros, so that P = 0 there contributes exactly nothing.
-  const bool full = kbase >= lo && kbase + 15 <= p;
-  uint32_t m01 = 0xFFFFFFFFu, m89 = 0xFFFFFFFFu;
-  if (!full) {
-    auto ok = [&](int k) { return kbase + k >= lo && kbase + k <= p; };
-    m01 = (ok(2 * c) ? 0x0000FFFFu : 0u) | (ok(2 * c + 1) ? 0xFFFF0000u : 0u);
-    m89 = (ok(2 * c + 8) ? 0x0000FFFFu : 0u) | (ok(2 * c + 9) ? 0xFFFF0000u : 0u);
-  }
-  auto pv = [&](int mt, uint32_t (&a)[4]) {
-    if (!full) {
-      a[0] &= m01;
-      a[1] &= m01;
-      a[2] &= m89;
-      a[3] &= m89;
+  // ---- P, then its transpose as the B fragments of P^T: b[0] = (keys 2c, 2c+1; head g),
+  // b[1] = (keys 2c+8, 2c+9; head g). BF16: P in a high and a low half.
+  constexpr int PH = FMT == kFmtBF16 ? 2 : 1;
+  uint32_t pb[SPW][NT][PH][2];
+#pragma unroll
+  for (int i = 0; i < SPW; ++i) {
+    float vs[2];
+    if constexpr (FMT != kFmtBF16) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {   // 2^(e - E + kBias); NaN for a row that holds no numbers
+        const int b = ev[i][h] - S.E + 127 + kBias;
+        vs[h] = __uint_as_float(ev[i][h] == 255 ? 0x7FFFFFFFu : (b > 0 ? unsigned(b) << 23 : 0u));
+      }
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      float w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = ex2(y[i][n][e]);
+      S.l[n][0] += w[0] + w[2];
+      S.l[n][1] += w[1] + w[3];
       if constexpr (FMT == kFmtBF16) {
-        mma_bf16(S.acc[n][mt], a, bh[n][0], bh[n][1]);
-        mma_bf16(S.acc[n][mt], a, bl[n][0], bl[n][1]);
+        const uint32_t h01 = pack_bf16x2(w[0], w[1]), h23 = pack_bf16x2(w[2], w[3]);
+        pb[i][n][0][0] = movtrans(h01);
+        pb[i][n][0][1] = movtrans(h23);
+        pb[i][n][PH - 1][0] = movtrans(pack_bf16x2(w[0] - bf_lo(h01), w[1] - bf_hi(h01)));
+        pb[i][n][PH - 1][1] = movtrans(pack_bf16x2(w[2] - bf_lo(h23), w[3] - bf_hi(h23)));
       } else {
-        mma_f16(S.acc[n][mt], a, bh[n][0], bh[n][1]);
-        mma_f16(S.acc[n][mt], a, bl[n][0], bl[n][1]);
+        pb[i][n][0][0] = movtrans(pack_f16x2(w[0] * vs[0], w[1] * vs[0]));
+        pb[i][n][0][1] = movtrans(pack_f16x2(w[2] * vs[1], w[3] * vs[1]));
       }
     }
-  };
-  if constexpr (FMT == kFmtBF16) {
-    const int rv = 16 * w + ((lane >> 4) & 1) * 8 + (lane & 7), cv = (lane >> 3) & 1;
+  }
+  // ---- O^T += V^T . P^T. Keys that are not the row's have their values replaced by zeros, so
+  // that P = 0 there contributes exactly nothing (their slots may hold anything, NaN included).
 #pragma unroll
-    for (int mt = 0; mt < KK; ++mt) {
-      uint32_t a[4];
-      ldsm_x4_t(vb + (mt >> 2) * (C::KB / C::PLANES) + rv * 128 + (((2 * (mt & 3) + cv) ^ (lane & 7)) << 4),
-                a[0], a[1], a[2], a[3]);
-      pv(mt, a);
-    }
-  } else {
-    // keys {2c, 2c+1, 2c+8, 2c+9}, d range [g D/8, (g + 1) D/8): logical row g of m tile mt is
-    // d = g D/8 + 2 mt, row g + 8 the next one
-    constexpr int VW = C::ROWB / 32;
-    uint32_t r[4][VW];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      lds<VW>(vb + sw((16 * w + 2 * c + (k & 1) + 8 * (k >> 1)) * C::ROWB + g * (C::ROWB / 8)), r[k]);
-    if constexpr (FMT == kFmtFP8) {
+  for (int i = 0; i < SPW; ++i) {
+    if constexpr (FMT == kFmtBF16) {
+      uint32_t m01 = 0xFFFFFFFFu, m89 = 0xFFFFFFFFu;
+      if (!full[i]) {
+        m01 = (valid(i, 2 * c) ? 0x0000FFFFu : 0u) | (valid(i, 2 * c + 1) ? 0xFFFF0000u : 0u);
+        m89 = (valid(i, 2 * c + 8) ? 0x0000FFFFu : 0u) | (valid(i, 2 * c + 9) ? 0xFFFF0000u : 0u);
+      }
 #pragma unroll
       for (int mt = 0; mt < KK; ++mt) {
-        const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;
         uint32_t a[4];
-        e4m3x4_f16(prmt(r[0][mt >> 1], r[1][mt >> 1], sel), a[0], a[1]);
-        e4m3x4_f16(prmt(r[2][mt >> 1], r[3][mt >> 1], sel), a[2], a[3]);
-        pv(mt, a);
+        ldsm_x4_t(kb + (mt >> 2) * (C::KB / C::PLANES) + (ln[i].v[0] ^ uint32_t((mt & 3) << 5)), a[0], a[1], a[2], a[3]);
+        a[0] &= m01;
+        a[1] &= m01;
+        a[2] &= m89;
+        a[3] &= m89;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma_bf16(S.acc[n][mt], a, pb[i][n][0][0], pb[i][n][0][1]);
+          mma_bf16(S.acc[n][mt], a, pb[i][n][PH - 1][0], pb[i][n][PH - 1][1]);
+        }
       }
     } else {
-      // the thread's d range lies in one block of 16: one scale per key
-      uint32_t s[4];
+      // keys {2c, 2c+1, 2c+8, 2c+9}, d range [g D/8, (g + 1) D/8): logical row g of m tile mt is
+      // d = g D/8 + 2 mt, row g + 8 the next one
+      constexpr int VW = C::ROWB / 32;
+      uint32_t r[4][VW], bs[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        s[k] = lds_u8(kb + C::OBS + srow(16 * w + 2 * c + (k & 1) + 8 * (k >> 1), 1) * (D / 16) +
-                      (D == 128 ? g : g >> 1));
-      const uint32_t f01 = e4m3x2_f16x2(s[0] | (s[1] << 8)), f89 = e4m3x2_f16x2(s[2] | (s[3] << 8));
-      constexpr uint32_t kLow = 0x0F0F0F0Fu;
+      for (int k = 0; k < 4; ++k) lds<VW>(kb + ln[i].v[k], r[k]);
+      if constexpr (FMT == kFmtNVFP4) {   // the d range lies in one block of 16: one scale per key
+        const uint32_t sa = kb + C::OBS + (ln[i].rs + ln[i].pse + 2 * c) * (D / 16) + (D == 128 ? g : g >> 1);
 #pragma unroll
-      for (int j = 0; j < VW; ++j) {
-        // bytes of (key 2c, key 2c+1) code pairs: even elements of four m tiles, then odd ones
-        uint32_t ae[4], ao[4], be[4], bo[4];
-        e2m1x8_f16((r[0][j] & kLow) | ((r[1][j] & kLow) << 4), ae);
-        e2m1x8_f16(((r[0][j] >> 4) & kLow) | (r[1][j] & ~kLow), ao);
-        e2m1x8_f16((r[2][j] & kLow) | ((r[3][j] & kLow) << 4), be);
-        e2m1x8_f16(((r[2][j] >> 4) & kLow) | (r[3][j] & ~kLow), bo);
+        for (int k = 0; k < 4; ++k) bs[k] = lds_u8(sa + ((k & 1) + 8 * (k >> 1)) * (D / 16));
+      }
+      if (!full[i]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t a[4] = {mul_f16x2(ae[i], f01), mul_f16x2(ao[i], f01), mul_f16x2(be[i], f89),
-                           mul_f16x2(bo[i], f89)};
-          pv(4 * j + i, a);
+        for (int k = 0; k < 4; ++k) {
+          if (valid(i, 2 * c + (k & 1) + 8 * (k >> 1))) continue;
+          bs[k] = 0;
+#pragma unroll
+          for (int j = 0; j < VW; ++j) r[k][j] = 0;
+        }
+      }
+      if constexpr (FMT == kFmtFP8) {
+#pragma unroll
+        for (int mt = 0; mt < KK; ++mt) {
+          const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;
+          uint32_t a[4];
+          e4m3x4_f16(prmt(r[0][mt >> 1], r[1][mt >> 1], sel), a[0], a[1]);
+          e4m3x4_f16(prmt(r[2][mt >> 1], r[3][mt >> 1], sel), a[2], a[3]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16(S.acc[n][mt], a, pb[i][n][0][0], pb[i][n][0][1]);
+        }
+      } else {
+        const uint32_t f01 = e4m3x2_f16x2(bs[0] | (bs[1] << 8)), f89 = e4m3x2_f16x2(bs[2] | (bs[3] << 8));
+        constexpr uint32_t kLow = 0x0F0F0F0Fu;
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+          // bytes of (key 2c, key 2c+1) code pairs: even elements of four m tiles, then odd ones
+          uint32_t ae[4], ao[4], be[4], bo[4];
+          e2m1x8_f16((r[0][j] & kLow) | ((r[1][j] << 4) & ~kLow), ae);
+          e2m1x8_f16(((r[0][j] >> 4) & kLow) | (r[1][j] & ~kLow), ao);
+          e2m1x8_f16((r[2][j] & kLow) | ((r[3][j] << 4) & ~kLow), be);
+          e2m1x8_f16(((r[2][j] >> 4) & kLow) | (r[3][j] & ~kLow), bo);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t a[4] = {mul_f16x2(ae[q], f01), mul_f16x2(ao[q], f01), mul_f16x2(be[q], f89),
+                                   mul_f16x2(bo[q], f89)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(S.acc[n][4 * j + q], a, pb[i][n][0][0], pb[i][n][0][1]);
+          }
         }
       }
     }
@@ -486,6 +526,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
   volatile int* misc = reinterpret_cast<volatile int*>(sm + C::MISC);   // -, abort, issued, -
   volatile unsigned* masks = reinterpret_cast<volatile unsigned*>(sm + C::MISC + 16);
   int* cum = reinterpret_cast<int*>(sm + C::CUM);
+  int* rpos = reinterpret_cast<int*>(sm + C::POS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NST; ++s) {
@@ -502,6 +543,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
   for (int t = threadIdx.x; t < T; t += C::THREADS) {
     const Row r = row_of<BK>(P, t);
     cum[t + 1] = r.nb;
+    rpos[t] = r.p;
     if (r.bad && blockIdx.x == 0) flag(r.bad);
   }
   __syncthreads();
@@ -603,7 +645,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
       const bool ok = page >= 0 && page < P.c.num_pages;
       if (page != -2 && !ok) flag(BEAM_DEV_BAD_PAGE);
       const unsigned okm = __ballot_sync(0xffffffffu, ok);
-      const unsigned slices = __ballot_sync(0xffffffffu, lane < C::NCW && ((okm >> (lane * 16 / pse)) & 1u));
+      const unsigned slices = __ballot_sync(0xffffffffu, lane < C::SLICES && ((okm >> (lane * 16 / pse)) & 1u));
       const uint32_t base = sbase + st * C::STAGE, fb = bar_full + 8 * st;
       const bool with_q = f == f_lo || a.j == 0;
       if (lane == 0) {
@@ -650,13 +692,11 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
   } else {
     // ---------------- consumers
     const int w = warp, g = lane >> 2, c = lane & 3, ct = threadIdx.x;
-    const int pse_shift = min(P.shift, log2_of<BK>());
-    float* Ow = reinterpret_cast<float*>(sm + C::OW);
-    float* MLw = reinterpret_cast<float*>(sm + C::MLW);
-    float* FWs = reinterpret_cast<float*>(sm + C::FW);
-    float* LHs = reinterpret_cast<float*>(sm + C::LH);   // [0, HEADS) sums, then maxima
+    Lane<FMT, C> ln[C::SPW];
+#pragma unroll
+    for (int e = 0; e < C::SPW; ++e) ln[e] = lane_of<FMT, C>(w + e * C::NCW, min(P.c.page_size, BK));
     const int G = P.G;
-    int i = 0, t = t_lo, f = f_lo;
+    int i = 0, t = t_lo, f = f_lo, buf = 0;
     int4 join = make_int4(0, 0, 0, 0);
     int hk = 0, j0 = 0;
     if (f_lo < f_hi) {
@@ -665,16 +705,32 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
       j0 = r - hk * nb;
     }
     while (f < f_hi) {
-      const Row row = row_of<BK>(P, t);
-      const int f_pair = cum[t] * P.n_kv + hk * row.nb;   // the pair's first block
-      const int j1 = min(row.nb, f_hi - f_pair);
+      const int p = rpos[t], lo = P.c.window > 0 ? max(1, p - P.c.window + 1) : 1;
+      const int blk0 = (lo - 1) / BK, nb = cum[t + 1] - cum[t];
+      const int f_pair = cum[t] * P.n_kv + hk * nb;   // the pair's first block
+      const int j1 = min(nb, f_hi - f_pair);
+      const bool split = j0 > 0 || j1 < nb;
+      // the gate of the outputs that this thread finishes: fetched now, used after the keys
+      uint2 gv[C::ITEMS];
+      float gb[C::ITEMS];
+      const size_t o_pair = (size_t(t) * P.n_q + hk * G) * D;
+      if (P.g != nullptr && !split) {
+#pragma unroll
+        for (int it = 0; it < C::ITEMS; ++it) {
+          const int idx = ct + it * NCT;
+          if (idx < G * (D / 4)) {
+            gv[it] = *reinterpret_cast<const uint2*>(P.g + o_pair + 4 * idx);
+            gb[it] = bf2f(P.gate_bias[hk * G + idx / (D / 4)]);
+          }
+        }
+      }
       uint32_t qb[NT][D / 16][2];
       float qs[NT][2];
       WarpState<C> S;
       S.E = 0;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        S.m[n][0] = S.m[n][1] = kNegInf;
+        S.m[n][0] = S.m[n][1] = kLowest;
         S.l[n][0] = S.l[n][1] = 0.f;
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt) S.acc[n][mt][0] = S.acc[n][mt][1] = S.acc[n][mt][2] = S.acc[n][mt][3] = 0.f;
@@ -727,18 +783,30 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
               }
             }
           }
-          const int kbase = BK * (row.blk0 + j) + 16 * w + 1;
-          if (((masks[st] >> w) & 1u) && kbase <= row.p && kbase + 15 >= row.lo)
-            warp_block<FMT, C>(kb, w, qb, qs, pse_shift, kbase, row.lo, row.p, S);
+          const unsigned mask = masks[st];
+          int kbase[C::SPW];
+          unsigned live = 0;
+#pragma unroll
+          for (int e = 0; e < C::SPW; ++e) {
+            const int sl = w + e * C::NCW;
+            kbase[e] = BK * (blk0 + j) + 16 * sl + 1;
+            if (((mask >> sl) & 1u) && kbase[e] <= p && kbase[e] + 15 >= lo) live |= 1u << e;
+          }
+          if (live) warp_block<FMT, C>(kb, ln, qb, qs, kbase, live, lo, p, S);
         } else if (lane == 0) {
           misc[1] = 1;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_empty + 8 * st);
       }
-      // ---- combine the consumer warps' partials of the pair
+      // ---- combine the consumer warps' partials of the pair. Two buffers in turn: who writes
+      // one has passed the barrier of the pair between, which its last readers came to later
+      // (one buffer, where two do not fit, needs a barrier of its own).
+      if constexpr (C::NOW == 1) consumer_bar<NCT>();
+      float* Ow = reinterpret_cast<float*>(sm + C::OW + buf * C::OWB);
+      float2* MLw = reinterpret_cast<float2*>(sm + C::MLW + buf * C::MLB);
+      buf = C::NOW - 1 - buf;
       const float unit = FMT == kFmtBF16 ? 1.f : ldexpf(1.f, S.E - 127 - kBias);
-      consumer_bar<NCT>();   // the previous pair's readers of the combine area are done
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -758,39 +826,31 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
           ow[C::OLD + db] = S.acc[n][mt][3] * unit;
         }
         if (g == 0) {
-          MLw[h0 * 2] = S.m[n][0];
-          MLw[h0 * 2 + 1] = S.l[n][0];
-          MLw[h0 * 2 + 2] = S.m[n][1];
-          MLw[h0 * 2 + 3] = S.l[n][1];
+          MLw[h0] = make_float2(S.m[n][0], S.l[n][0]);
+          MLw[h0 + 1] = make_float2(S.m[n][1], S.l[n][1]);
         }
       }
       consumer_bar<NCT>();
-      if (ct < G) {
-        const int h = ct;
-        float M = kNegInf;
-#pragma unroll
-        for (int ww = 0; ww < C::NCW; ++ww) M = fmaxf(M, MLw[(ww * C::HEADS + h) * 2]);
-        float L = 0.f;
-#pragma unroll
-        for (int ww = 0; ww < C::NCW; ++ww) {
-          const float fw = M == kNegInf ? 0.f : ex2(MLw[(ww * C::HEADS + h) * 2] - M);
-          FWs[ww * C::HEADS + h] = fw;
-          L += fw * MLw[(ww * C::HEADS + h) * 2 + 1];
-        }
-        LHs[h] = L;
-        LHs[C::HEADS + h] = M;
-      }
-      consumer_bar<NCT>();
-      const bool split = j0 > 0 || j1 < row.nb;
       const int slot = f == f_lo ? 0 : 1;   // the CTA's first pair, or its last
       const size_t pb = (size_t(2 * blockIdx.x) + slot) * C::HEADS;
-      for (int idx = ct; idx < G * (D / 4); idx += NCT) {
+#pragma unroll
+      for (int it = 0; it < C::ITEMS; ++it) {
+        const int idx = ct + it * NCT;
+        if (idx >= G * (D / 4)) break;
         const int h = idx / (D / 4), d = 4 * (idx - h * (D / 4));
+        float M = kLowest, L = 0.f;
+        float2 ml[C::NCW];
+#pragma unroll
+        for (int ww = 0; ww < C::NCW; ++ww) {
+          ml[ww] = MLw[ww * C::HEADS + h];
+          M = fmaxf(M, ml[ww].x);
+        }
         float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int ww = 0; ww < C::NCW; ++ww) {
-          const float fw = FWs[ww * C::HEADS + h];
+          const float fw = ex2(ml[ww].x - M);
           const float4 v = *reinterpret_cast<const float4*>(Ow + (ww * C::HEADS + h) * C::OLD + d);
+          L += fw * ml[ww].y;
           O.x += fw * v.x;
           O.y += fw * v.y;
           O.z += fw * v.z;
@@ -798,16 +858,21 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
         }
         if (split) {
           *reinterpret_cast<float4*>(P.part_acc + (pb + h) * D + d) = O;
-        } else {
-          finish(P, t, hk, h, d, D, O, LHs[h]);
+          if (d == 0) *reinterpret_cast<float2*>(P.part_ml + (pb + h) * 2) = make_float2(M, L);
+          continue;
         }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        float o[4] = {O.x * inv, O.y * inv, O.z * inv, O.w * inv};
+        if (P.g != nullptr) {
+          o[0] *= sigmoidf_(bf_lo(gv[it].x) + gb[it]);
+          o[1] *= sigmoidf_(bf_hi(gv[it].x) + gb[it]);
+          o[2] *= sigmoidf_(bf_lo(gv[it].y) + gb[it]);
+          o[3] *= sigmoidf_(bf_hi(gv[it].y) + gb[it]);
+        }
+        *reinterpret_cast<uint2*>(P.og + o_pair + 4 * idx) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
       }
-      if (split && ct < G) {
-        P.part_ml[(pb + ct) * 2] = LHs[C::HEADS + ct];
-        P.part_ml[(pb + ct) * 2 + 1] = LHs[ct];
-      }
-      if (j0 == 0 && j1 < row.nb)   // the pair begins here and runs on
-        join = make_int4(t, hk, (f_pair + row.nb - 1) / R - int(blockIdx.x) + 1, slot);
+      if (j0 == 0 && j1 < nb)   // the pair begins here and runs on
+        join = make_int4(t, hk, (f_pair + nb - 1) / R - int(blockIdx.x) + 1, slot);
       // ---- next pair
       f = f_pair + j1;
       j0 = 0;
@@ -854,7 +919,7 @@ __global__ void __launch_bounds__(D) paged_join_kernel(const Params P) {
     lsh[s] = v.y;
   }
   __syncthreads();
-  float M = kNegInf;
+  float M = kLowest;
   for (int s = 0; s < n; ++s) M = fmaxf(M, wsh[s]);
   float L = 0.f, O = 0.f;
   int s = 0;
@@ -864,13 +929,13 @@ __global__ void __launch_bounds__(D) paged_join_kernel(const Params P) {
     for (int u = 0; u < 8; ++u) v[u] = __ldcg(P.part_acc + slot(s + u) * D + threadIdx.x);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const float fw = M == kNegInf ? 0.f : ex2(wsh[s + u] - M);
+      const float fw = ex2(wsh[s + u] - M);
       O += fw * v[u];
       L += fw * lsh[s + u];
     }
   }
   for (; s < n; ++s) {
-    const float fw = M == kNegInf ? 0.f : ex2(wsh[s] - M);
+    const float fw = ex2(wsh[s] - M);
     O += fw * __ldcg(P.part_acc + slot(s) * D + threadIdx.x);
     L += fw * lsh[s];
   }
@@ -881,10 +946,14 @@ __global__ void __launch_bounds__(D) paged_join_kernel(const Params P) {
   P.og[oi] = f2bf(o);
 }
 
+template <int FMT>
+int block_keys_of(int D, int nt) {
+  if (D == 128) return nt == 1 ? Cfg<FMT, 128, 1>::BK : Cfg<FMT, 128, 2>::BK;
+  return nt == 1 ? Cfg<FMT, 64, 1>::BK : Cfg<FMT, 64, 2>::BK;
+}
 int block_keys(int fmt, int D, int nt) {
-  if (fmt == kFmtBF16) return D == 128 ? Cfg<kFmtBF16, 128, 1>::BK : Cfg<kFmtBF16, 64, 1>::BK;
-  if (fmt == kFmtFP8) return Cfg<kFmtFP8, 128, 1>::BK;
-  return D == 128 && nt == 1 ? Cfg<kFmtNVFP4, 128, 1>::BK : Cfg<kFmtNVFP4, 128, 2>::BK;
+  return fmt == kFmtBF16 ? block_keys_of<kFmtBF16>(D, nt)
+         : fmt == kFmtFP8 ? block_keys_of<kFmtFP8>(D, nt) : block_keys_of<kFmtNVFP4>(D, nt);
 }
 
 int max_grid() {

@@ -4,14 +4,16 @@ sizes, layouts and values where they can go wrong.
 Writing and reading are exact by definition: codes, scales and values must be equal.
 
 Attention: |out - ref| <= 2^-8 |ref| (half a bf16 step, the one rounding of the result) plus an
-absolute term from the FP32 work before it, per element
-    W (2 d + 2^-15) + n 2^-32 V / 1
+absolute term from the work before it, per element
+    W (2 d + r) + n 2^-32 V
 with W = sum p|v| (64 bits). d bounds the logit error: D products summed in FP32, each sum off by
-at most 2^-23 of the sum of magnitudes: d = D 2^-23 max_i sum|q k_i| / sqrt(D). 2^-15 covers P's
-two bf16 halves (2^-17), exp2 (2^-21) and the FP32 sums. The last term is the f16 floor of the
-quantised caches: a P value below f16's smallest step 2^-24 at the bias 2^7 is off by half of
-it, 2^-32, times the largest stored magnitude V of the row's keys. The gate's sigmoid is within
-2^-20 and scales what it gates.
+at most 2^-23 of the sum of magnitudes: d = D 2^-23 max_i sum|q k_i| / sqrt(D). r bounds the
+relative error of a weight p itself, which enters the sum as (p + dp) v with |dp| <= r p, so the
+sum moves by at most r W: 2^-15 over a BF16 cache (P in two bf16 halves, 2^-17, exp2, 2^-21, and
+the FP32 sums); over a quantised cache P is rounded to f16 once, half a step, 2^-11, and the rest
+is 2^-15 as before. The last term is the f16 floor there: a P value below f16's smallest step
+2^-24 at the bias 2^7 is off by half of it, 2^-32, times the largest stored magnitude V of the
+row's n keys. The gate's sigmoid is within 2^-20 and scales what it gates.
 """
 import numpy as np
 import pytest
@@ -119,7 +121,8 @@ def tolerance(cfg, hc, q, seq, pos, ref, mag):
             d = D * 2.0 ** -23 * np.max(np.abs(K[h // grp]) @ np.abs(q[t, h])) / np.sqrt(D)
             sl = slice(h * D, (h + 1) * D)
             floor = 0.0 if hc.fmt == "bf16" else V.shape[1] * 2.0 ** -32 * np.max(np.abs(V[h // grp]))
-            tol[t, sl] += mag[t, sl] * (2 * d + 2.0 ** -15) + floor
+            r = 2.0 ** -15 + (0.0 if hc.fmt == "bf16" else 2.0 ** -11)
+            tol[t, sl] += mag[t, sl] * (2 * d + r) + floor
     return tol
 
 
