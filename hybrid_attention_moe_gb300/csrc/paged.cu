@@ -2,6 +2,7 @@
 // BF16 cache. The formats are those of include/beam.h (beam_paged_kv).
 //
 // Both kernels move bytes once: bounded by HBM for long calls and by the launch for short ones.
+#include "mma.cuh"
 #include "paged.cuh"
 
 namespace beam {
@@ -15,8 +16,8 @@ struct WriteParams {
   const int32_t* pos;
   beam_paged_kv c;
   int64_t token_stride;
-  int rows;   // T * n_kv * 2
-  int shift;  // log2(page_size)
+  int T, parts;   // parts: warps of one token
+  int shift;      // log2(page_size)
 };
 
 // Where a token's rows go: the page, or -1 (padding, or out of range: the bit to set in bad).
@@ -40,94 +41,129 @@ __device__ __forceinline__ int page_of(const beam_paged_kv& c, int s, int p, int
   return pg;
 }
 
-// D / 8 lanes hold one row, eight elements each, so a warp takes 2 (D 128) or 4 (D 64) rows, in
-// the order (token, head, K | V). The row's largest magnitude is an integer maximum of the
-// bf16 patterns without their signs (they order like the values, and infinities and NaNs come
-// out on top); the row's power of two follows from that pattern's exponent and fraction alone,
-// so nothing is rounded before the codes are.
+// x to 14 significant bits (to nearest, ties away from zero).
+__device__ __forceinline__ float round14(float x) {
+  return __uint_as_float((__float_as_uint(x) + 0x200u) & 0xFFFFFC00u);
+}
+
+// The multiple of 2^-12 nearest to x * r (|x * r| < 2^10), with x's sign.
+__device__ __forceinline__ float quotient(float x, float r) {
+  constexpr float kMagic = 0x1.8p11f;   // the step of FP32 in [2^11, 2^12) is 2^-12
+  const float q = fmaf(x, r, kMagic) - kMagic;
+  return __uint_as_float((__float_as_uint(q) & 0x7FFFFFFFu) | (__float_as_uint(x) & 0x80000000u));
+}
+
+// A warp takes up to kHeads KV heads of one token, K and V, and issues all its loads before the
+// page is looked up. A lane holds 16 elements of a row (an NVFP4 block; a BF16 row, which is only
+// moved, is taken 8 a lane). The row's largest magnitude is an integer maximum of the bf16
+// patterns without their signs (they order like the values, and infinities and NaNs come out on
+// top); the row's power of two follows from that pattern's exponent and fraction alone, so
+// nothing is rounded before the codes are.
+//
+// Quotients by s are taken with a reciprocal and rounded to multiples of 2^-12. A quotient that is
+// a midpoint of two codes (0.25 at least, 3 bits) comes back exactly; any other one is further
+// from every midpoint (2^-8 of it, 2^-10 at least: the dividend has 8 bits, s 4 and the midpoint 3)
+// than the errors reach (2^-20 and 2^-13), so the code is that of the exact quotient. The sixth
+// of the block's largest value is rounded to 14 bits in the same manner: a midpoint of e4m3 has 5
+// bits, and any other sixth is 2^-8 of it away (the dividend has 8 bits, 6 midpoints 7).
+constexpr int kHeads = 4;
 template <int FMT, int D>
-__global__ void __launch_bounds__(256) paged_write_kernel(const WriteParams P) {
+__global__ void __launch_bounds__(256, 5) paged_write_kernel(const WriteParams P) {
   pdl_trigger();
   pdl_wait();
-  constexpr int LPR = D / 8;
-  const int lane = threadIdx.x & 31, sub = lane % LPR;
+  constexpr int EPL = FMT == kFmtBF16 ? 8 : 16, NV = EPL / 8;
+  constexpr int LPR = D / EPL, HPI = 16 / LPR;          // lanes of a row, heads of a step
+  constexpr int U = kHeads > HPI ? kHeads / HPI : 1;
+  const int lane = threadIdx.x & 31, sub = lane % LPR, kv = (lane / LPR) & 1;
   const int warp = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int row = warp * (32 / LPR) + lane / LPR;
-  const bool live = row < P.rows;
-  const int r = live ? row : P.rows - 1;   // idle lanes repeat the last row and store nothing
-  const int kv = r & 1, th = r >> 1;
-  const int t = th / P.c.n_kv, hk = th - t * P.c.n_kv;
-  const uint4 x = *reinterpret_cast<const uint4*>((kv ? P.v : P.k) + t * P.token_stride +
-                                                  hk * D + sub * 8);
+  const int t = warp / P.parts, h0 = (warp - t * P.parts) * kHeads + lane / (2 * LPR);
+  if (t >= P.T) return;
+  const int n_kv = P.c.n_kv;
+  const uint16_t* src = (kv ? P.v : P.k) + t * P.token_stride + sub * EPL;
+  uint4 x[U][NV];
+#pragma unroll
+  for (int u = 0; u < U; ++u)   // heads past the last repeat it and store nothing
+#pragma unroll
+    for (int a = 0; a < NV; ++a)
+      x[u][a] = reinterpret_cast<const uint4*>(src + min(h0 + u * HPI, n_kv - 1) * D)[a];
   const int p = P.pos[t];
   unsigned bad;
   const int pg = page_of(P.c, P.seq_id[t], p, P.shift, bad);
-  if (bad && live && hk == 0 && kv == 0 && sub == 0) flag(bad);
-  const bool store = live && pg >= 0;
+  if (bad && h0 == 0 && lane == 0) flag(bad);
+  if (pg < 0) return;   // the whole warp: one token
   const int off = (p - 1) & (P.c.page_size - 1);
-  const size_t head = size_t(store ? pg : 0) * P.c.n_kv + hk;
-  const size_t at = head * P.c.page_size + (store ? off : 0);          // row of k or v
-  const size_t sat = (head * 2 + kv) * P.c.page_size + (store ? off : 0);   // row of the scales
-  uint8_t* dst = static_cast<uint8_t*>(kv ? P.c.v : P.c.k) + at * row_bytes(FMT, D);
-  if constexpr (FMT == kFmtBF16) {
-    if (store) *reinterpret_cast<uint4*>(dst + sub * 16) = x;
-  } else {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    unsigned mx = 0;   // the lane's largest magnitude, as a bf16 pattern
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      mx = max(mx, w[i] & 0x7FFFu);
-      mx = max(mx, (w[i] >> 16) & 0x7FFFu);
-    }
-    unsigned rm = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));   // of the block of 16
-    const unsigned bm = rm;
-#pragma unroll
-    for (int o = 2; o < LPR; o <<= 1) rm = max(rm, __shfl_xor_sync(0xffffffffu, rm, o));
-    const bool finite = rm < 0x7F80u;
-    // most = 448 = 1.75 * 2^8 (fraction 96 / 128), or 2688 = 1.3125 * 2^11 (fraction 40 / 128)
-    constexpr int kExp = FMT == kFmtFP8 ? 8 : 11, kFrac = FMT == kFmtFP8 ? 96 : 40;
-    const int b = max(0, int(rm >> 7) - kExp + (int(rm & 127u) > kFrac ? 1 : 0));
-    const float inv = __uint_as_float(unsigned(254 - b) << 23);   // 2^(127 - b)
-    float y[8];
-    unpack8(x, y);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = finite ? y[i] * inv : 0.f;
-    if constexpr (FMT == kFmtFP8) {
-      uint32_t c2[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        c2[i] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * i], y[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-      if (store)
-        *reinterpret_cast<uint2*>(dst + sub * 8) = make_uint2(c2[0] | (c2[1] << 16), c2[2] | (c2[3] << 16));
+  for (int u = 0; u < U; ++u) {
+    const int hk = h0 + u * HPI;
+    const bool store = hk < n_kv;
+    const size_t head = size_t(pg) * n_kv + (store ? hk : 0);
+    const size_t sat = (head * 2 + kv) * P.c.page_size + off;   // row of the scales
+    uint8_t* dst = static_cast<uint8_t*>(kv ? P.c.v : P.c.k) + (head * P.c.page_size + off) * row_bytes(FMT, D);
+    if constexpr (FMT == kFmtBF16) {
+      if (store) *reinterpret_cast<uint4*>(dst + sub * 16) = x[u][0];
     } else {
-      const float bmax = finite ? __uint_as_float(bm << 16) * inv : 0.f;
-      const unsigned s = __nv_cvt_float_to_fp8(__fdiv_rn(bmax, 6.f), __NV_SATFINITE, __NV_E4M3);
-      float sf, unused;
-      unpack_f16(e4m3x2_f16x2(s), sf, unused);
-      const float rs = s ? __fdiv_rn(1.f, sf) : 0.f;
-      uint32_t codes = 0;
+      // largest magnitudes of even and odd elements, as two bf16 patterns
+      constexpr unsigned kAbs = 0x7FFF7FFFu;
+      unsigned mx = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // y / s from the reciprocal, then to 14 significant bits. A quotient that is a midpoint
-        // of two codes has 3 bits and comes back exactly; any other one is further from every
-        // midpoint (2^-8 of it: y has 8 bits, s 4, the midpoint 3) than the two errors
-        // (2^-22 and 2^-14) reach, so the code is that of the exact quotient.
-        float q[2];
+      for (int a = 0; a < NV; ++a)
+        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x[u][a].x & kAbs, x[u][a].y & kAbs),
+                                   __vmaxu2(x[u][a].z & kAbs, x[u][a].w & kAbs)));
+      const unsigned bm = max(mx & 0xFFFFu, mx >> 16);   // of the block of 16
+      unsigned rm = bm;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          q[e] = __uint_as_float((__float_as_uint(y[2 * i + e] * rs) + 0x200u) & 0xFFFFFC00u);
-        uint32_t c;
-        asm("{.reg .b8 z; cvt.rn.satfinite.e2m1x2.f32 z, %2, %1; cvt.u32.u8 %0, z;}"
-            : "=r"(c)
-            : "f"(q[0]), "f"(q[1]));
-        codes |= (c & 0xFFu) << (8 * i);
+      for (int o = 1; o < LPR; o <<= 1) rm = max(rm, __shfl_xor_sync(0xffffffffu, rm, o));
+      const bool finite = rm < 0x7F80u;
+      // most = 448 = 1.75 * 2^8 (fraction 96 / 128), or 2688 = 1.3125 * 2^11 (fraction 40 / 128)
+      constexpr int kExp = FMT == kFmtFP8 ? 8 : 11, kFrac = FMT == kFmtFP8 ? 96 : 40;
+      const int b = max(0, int(rm >> 7) - kExp + (int(rm & 127u) > kFrac ? 1 : 0));
+      float inv = __uint_as_float(unsigned(254 - b) << 23);   // 2^(127 - b)
+      float y[EPL];
+#pragma unroll
+      for (int a = 0; a < NV; ++a) unpack8(x[u][a], y + 8 * a);
+      if constexpr (FMT == kFmtFP8) {
+        uint32_t w[EPL / 4];
+#pragma unroll
+        for (int i = 0; i < EPL / 4; ++i) {
+          const float* z = y + 4 * i;
+          w[i] = uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(z[0] * inv, z[1] * inv), __NV_SATFINITE, __NV_E4M3)) |
+                 uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(z[2] * inv, z[3] * inv), __NV_SATFINITE, __NV_E4M3)) << 16;
+          if (!finite) w[i] = 0u;
+        }
+        if (store) *reinterpret_cast<uint4*>(dst + sub * EPL) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        const float q6 = round14(__uint_as_float(bm << 16) * inv * (1.f / 6.f));
+        const unsigned s = finite ? __nv_cvt_float_to_fp8(q6, __NV_SATFINITE, __NV_E4M3) : 0u;
+        float sf, rs, unused;
+        unpack_f16(e4m3x2_f16x2(s), sf, unused);
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(sf));
+        if (b < 16) {   // 2^(127 - b) / s may pass FP32's range: part of it goes to the elements
+          inv *= 0x1p-32f;
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) y[i] *= 0x1p32f;
+        }
+        rs *= inv;
+        uint32_t w[EPL / 8];
+#pragma unroll
+        for (int i = 0; i < EPL / 8; ++i) {
+          float q[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) q[e] = quotient(y[8 * i + e], rs);
+          asm("{.reg .b8 a, b, c, d;"
+              " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1; cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;"
+              " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5; cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;"
+              " mov.b32 %0, {a, b, c, d};}"
+              : "=r"(w[i])
+              : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+          if (s == 0) w[i] = 0u;   // the block is zeros, or the row holds no numbers
+        }
+        if (store) {
+          *reinterpret_cast<uint2*>(dst + sub * (EPL / 2)) = make_uint2(w[0], w[1]);
+          P.c.block_scale[sat * (D / 16) + sub] = uint8_t(s);
+        }
       }
-      if (store) {
-        *reinterpret_cast<uint32_t*>(dst + sub * 4) = s ? codes : 0u;
-        if ((sub & 1) == 0) P.c.block_scale[sat * (D / 16) + (sub >> 1)] = uint8_t(s);
-      }
+      if (store && sub == 0) P.c.row_scale[sat] = finite ? uint8_t(b) : uint8_t(255);
     }
-    if (store && sub == 0) P.c.row_scale[sat] = finite ? uint8_t(b) : uint8_t(255);
   }
 }
 
@@ -141,15 +177,17 @@ struct ReadParams {
   int cap, max_len, shift;
 };
 
-// A CTA takes kReadKeys consecutive positions of one (row, KV head), K and V. A thread holds
-// eight elements of a key: 16, 8 or 4 bytes of codes in, 16 bytes out.
-constexpr int kReadKeys = 64;
+// A CTA takes read_keys consecutive positions of one (row, KV head), K and V, in passes. A thread
+// holds two chunks of eight elements of a key, half a row apart (so that a warp's stores are
+// whole sectors): 2 x 16, 8 or 4 bytes of codes in, 2 x 16 bytes out.
+constexpr int read_passes(int fmt) { return fmt == kFmtNVFP4 ? 4 : 2; }
+constexpr int read_keys(int fmt, int D) { return read_passes(fmt) * (256 / (D / 16)); }
 
 template <int FMT, int D>
 __global__ void __launch_bounds__(256) paged_read_kernel(const ReadParams P) {
   pdl_trigger();
   pdl_wait();
-  constexpr int TPR = D / 8, KPP = 256 / TPR, NP = kReadKeys / KPP;   // keys per pass, passes
+  constexpr int TPR = D / 16, KPP = 256 / TPR, NP = read_passes(FMT), KEYS = read_keys(FMT, D);
   const int i = blockIdx.z, hk = blockIdx.y;
   const int first = P.first[i], last = P.last[i], s = P.seq_id[i];
   if (last < first) return;
@@ -163,67 +201,112 @@ __global__ void __launch_bounds__(256) paged_read_kernel(const ReadParams P) {
     if (blockIdx.x == 0 && hk == 0 && threadIdx.x == 0) flag(bad);
     return;
   }
-  if (int(blockIdx.x) * kReadKeys > last - first) return;
-  const int p0 = first + int(blockIdx.x) * kReadKeys;
+  if (int(blockIdx.x) * KEYS > last - first) return;
+  const int p0 = first + int(blockIdx.x) * KEYS;
   const int sub = threadIdx.x % TPR, key = threadIdx.x / TPR;
   const int32_t* table = P.c.page_table + size_t(s) * P.c.table_stride;
+  // all pages, then all codes and scales, then the stores: each step's loads are in flight at once
+  size_t at[NP];   // the key's row of codes; scale rows follow from it
+  bool ok[NP];
 #pragma unroll
   for (int j = 0; j < NP; ++j) {
     const int p = p0 + j * KPP + key;
-    if (p > last) break;
-    const int pg = table[(p - 1) >> P.shift];
+    ok[j] = p <= last;
+    const int pg = ok[j] ? table[(p - 1) >> P.shift] : 0;
     if (pg < 0 || pg >= P.c.num_pages) {
       if (hk == 0 && sub == 0) flag(BEAM_DEV_BAD_PAGE);
-      continue;
+      ok[j] = false;
     }
-    const size_t head = size_t(pg) * P.c.n_kv + hk;
-    const int off = (p - 1) & (P.c.page_size - 1);
-    const size_t to = ((size_t(i) * P.c.n_kv + hk) * P.cap + (p - 1) % P.cap) * D + sub * 8;
+    at[j] = (size_t(ok[j] ? pg : 0) * P.c.n_kv + hk) * P.c.page_size + ((p - 1) & (P.c.page_size - 1));
+  }
+  constexpr int CW = FMT == kFmtBF16 ? 4 : (FMT == kFmtFP8 ? 2 : 1);   // words of eight codes
+  constexpr int ROWB = row_bytes(FMT, D);
+  uint32_t w[NP][2][2][CW], rs[NP][2], bs[NP][2][2];
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    if (!ok[j]) continue;
+    // [page][head][key] -> [page][head][K | V][key]
+    const size_t sat = 2 * at[j] - (at[j] & size_t(P.c.page_size - 1));
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      const uint8_t* src = static_cast<const uint8_t*>(kv ? P.c.v : P.c.k) +
-                           (head * P.c.page_size + off) * row_bytes(FMT, D);
-      uint4 o;
-      if constexpr (FMT == kFmtBF16) {
-        o = *reinterpret_cast<const uint4*>(src + sub * 16);
-      } else {
-        const size_t sat = (head * 2 + kv) * P.c.page_size + off;
-        float f = pow2_of(P.c.row_scale[sat]);
-        uint32_t h[4];
-        if constexpr (FMT == kFmtFP8) {
-          const uint2 c = *reinterpret_cast<const uint2*>(src + sub * 8);
-          e4m3x4_f16(c.x, h[0], h[1]);
-          e4m3x4_f16(c.y, h[2], h[3]);
-        } else {
-          e2m1x8_f16(*reinterpret_cast<const uint32_t*>(src + sub * 4), h);
-        }
-        float bs = 1.f, unused;
-        if constexpr (FMT == kFmtNVFP4)
-          unpack_f16(e4m3x2_f16x2(P.c.block_scale[sat * (D / 16) + (sub >> 1)]), bs, unused);
-        uint32_t r[4];
+      const uint8_t* src = static_cast<const uint8_t*>(kv ? P.c.v : P.c.k) + at[j] * ROWB + sub * CW * 4;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float a, b;
-          unpack_f16(h[e], a, b);
-          // code * s is exact, so the only rounding is that to bf16
-          r[e] = pack_bf2(a * bs * f, b * bs * f);
+      for (int h = 0; h < 2; ++h, src += ROWB / 2) {
+        if constexpr (CW == 4) {
+          const uint4 x = *reinterpret_cast<const uint4*>(src);
+          w[j][kv][h][0] = x.x; w[j][kv][h][1] = x.y; w[j][kv][h][2] = x.z; w[j][kv][h][3] = x.w;
+        } else if constexpr (CW == 2) {
+          const uint2 x = *reinterpret_cast<const uint2*>(src);
+          w[j][kv][h][0] = x.x; w[j][kv][h][1] = x.y;
+        } else {
+          w[j][kv][h][0] = *reinterpret_cast<const uint32_t*>(src);
         }
-        o = make_uint4(r[0], r[1], r[2], r[3]);
       }
-      *reinterpret_cast<uint4*>((kv ? P.v : P.k) + to) = o;
+      if constexpr (FMT != kFmtBF16) {
+        const size_t r = sat + (kv ? P.c.page_size : 0);
+        rs[j][kv] = P.c.row_scale[r];
+        if constexpr (FMT == kFmtNVFP4) {
+          const uint8_t* b = P.c.block_scale + r * (D / 16) + (sub >> 1);
+          bs[j][kv][0] = b[0];
+          bs[j][kv][1] = b[D / 32];
+        }
+      }
+    }
+  }
+  const int slot0 = (p0 - 1) % P.cap;
+  const size_t row = (size_t(i) * P.c.n_kv + hk) * P.cap;
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    if (!ok[j]) continue;
+    int slot = slot0 + j * KPP + key;   // the range is no longer than the ring: one lap at most
+    if (slot >= P.cap) slot -= P.cap;
+    const size_t to = (row + slot) * D + sub * 8;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      uint16_t* dst = (kv ? P.v : P.k) + to;
+      const float f = FMT == kFmtBF16 ? 1.f : pow2_of(rs[j][kv]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h, dst += D / 2) {
+        uint32_t r[4];
+        if constexpr (FMT == kFmtBF16) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) r[e] = w[j][kv][h][e];
+        } else {
+          uint32_t c[4];
+          float unit = f;
+          if constexpr (FMT == kFmtFP8) {
+            e4m3x4_f16(w[j][kv][h][0], c[0], c[1]);
+            e4m3x4_f16(w[j][kv][h][CW - 1], c[2], c[3]);
+          } else {
+            float sf, unused;
+            unpack_f16(e4m3x2_f16x2(bs[j][kv][h]), sf, unused);
+            e2m1x8_f16(w[j][kv][h][0], c);
+            unit = sf * f;
+          }
+          // code * unit has 6 bits: exact down to FP32's smallest 2^-149, which no stored value
+          // passes (2^-10 * 2^-127), so the only rounding is that to bf16
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float a, b;
+            unpack_f16(c[e], a, b);
+            r[e] = pack_bf16x2(a * unit, b * unit);
+          }
+        }
+        *reinterpret_cast<uint4*>(dst) = make_uint4(r[0], r[1], r[2], r[3]);
+      }
     }
   }
 }
 
 template <int FMT, int D>
 cudaError_t launch_write(const WriteParams& p, cudaStream_t st) {
-  const int per = 8 * (32 / (D / 8));
-  return launch_pdl(paged_write_kernel<FMT, D>, dim3((p.rows + per - 1) / per), dim3(256), 0, st, p);
+  const int warps = p.T * p.parts;
+  return launch_pdl(paged_write_kernel<FMT, D>, dim3((warps + 7) / 8), dim3(256), 0, st, p);
 }
 template <int FMT, int D>
 cudaError_t launch_read(const ReadParams& p, int N, cudaStream_t st) {
   return launch_pdl(paged_read_kernel<FMT, D>,
-                    dim3((p.max_len + kReadKeys - 1) / kReadKeys, p.c.n_kv, N), dim3(256), 0, st, p);
+                    dim3((p.max_len + read_keys(FMT, D) - 1) / read_keys(FMT, D), p.c.n_kv, N), dim3(256), 0, st, p);
 }
 
 }  // namespace
@@ -253,8 +336,8 @@ extern "C" beam_status beam_paged_kv_write(const beam_bf16* k, const beam_bf16* 
       (token_stride & 7) || token_stride < cache->n_kv * cache->head_dim)
     return BEAM_ERR_INVALID_ARG;
   if (int64_t(T) * cache->n_kv * 2 > INT32_MAX - 64) return BEAM_ERR_UNSUPPORTED;
-  const WriteParams p{k, v, seq_id, pos, *cache, token_stride, T * cache->n_kv * 2,
-                      log2i(cache->page_size)};
+  const WriteParams p{k, v, seq_id, pos, *cache, token_stride, T,
+                      (cache->n_kv + kHeads - 1) / kHeads, log2i(cache->page_size)};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool wide = cache->head_dim == 128;
   cudaError_t e;
