@@ -47,7 +47,8 @@ using namespace beam::tc;
 constexpr float kNegInf = -INFINITY;
 constexpr float kLowest = -3e38f;   // a running max that has seen nothing: finite, so differences are
 constexpr float kRescale = 8.f;     // log2 units by which the running max may lag
-constexpr int kMaxGrid = 152;       // CTAs, and so parts of one pair, at most
+constexpr int kMaxGrid = 152;       // CTAs at most
+constexpr int kMaxParts = 2 * kMaxGrid;   // ranges, and so parts of one pair
 constexpr int kMaxT = 1024;         // rows of one launch
 constexpr int kWholeBlocks = 4;
 constexpr int kBias = 7;            // P <= 2^kRescale, times 2^7: below 65504
@@ -57,12 +58,17 @@ struct Cfg {
   static constexpr int D = D_, NT = NT_, HEADS = 8 * NT;
   static constexpr int ROWB = row_bytes(FMT, D);
   static constexpr int PLANES = ROWB > 128 ? 2 : 1;   // 128-byte columns of a row
-  // consumer warps, and 16-key slices that each takes of a block: a block holds 32 KB of K and V
-  // where that fits
-  static constexpr int NCW = FMT == kFmtBF16 && D == 128 ? 4 : 8;
-  static constexpr int SPW = FMT == kFmtNVFP4 && D == 128 && NT == 1 ? 2 : 1;
-  static constexpr int THREADS = (NCW + 1) * 32;
-  static constexpr int SLICES = NCW * SPW, BK = 16 * SLICES;
+  // A group is WPG consumer warps, SPW slices of 16 keys of a block each, with its own range of
+  // blocks and ring of stages: what one group spends on waits and on a pair's end, the other's
+  // arithmetic covers
+  static constexpr int GROUPS = NT == 1 ? 2 : 1;
+  static constexpr int WPG = NT == 1 || (FMT == kFmtBF16 && D == 128) ? 4 : 8;
+  static constexpr int SPW = NT == 1 && !(FMT == kFmtBF16 && D == 128) ? 2 : 1;
+  static constexpr int NCW = WPG * GROUPS, NCT = WPG * 32;   // consumer warps, threads of a group
+  // four producer warps: K and V of each group, or of the even and odd blocks of the one group
+  static constexpr int STEP = GROUPS == 2 ? 1 : 2;
+  static constexpr int THREADS = (NCW + 4) * 32;
+  static constexpr int SLICES = WPG * SPW, BK = 16 * SLICES;
   static constexpr int KB = BK * ROWB;
   static constexpr int BSB = FMT == kFmtNVFP4 ? 2 * BK * (D / 16) : 0;
   static constexpr int RSB = FMT != kFmtBF16 ? 2 * BK : 0;
@@ -70,19 +76,20 @@ struct Cfg {
   static constexpr int OBS = 2 * KB, ORS = OBS + BSB, OQ = ORS + RSB;   // offsets in a stage
   static constexpr int STAGE = (OQ + QB + 1023) / 1024 * 1024;
   static constexpr int OLD = D + 4;   // row stride of the combine buffer (floats)
-  static constexpr int OWB = NCW * HEADS * OLD * 4, MLB = NCW * HEADS * 2 * 4;
-  static constexpr int NOW = NT == 1 ? 2 : 1;             // combine buffers
-  static constexpr int NST = 4 * STAGE + NOW * (OWB + MLB) <= 216 * 1024 ? 4 : 3;
-  static constexpr int OW = NST * STAGE;                  // [NOW][NCW][HEADS][OLD]: O partials
-  static constexpr int MLW = OW + NOW * OWB;              // [NOW][NCW][HEADS][2]: (m, l)
-  static constexpr int CUM = MLW + NOW * MLB;             // [kMaxT + 1] block prefix
+  static constexpr int OWB = WPG * HEADS * OLD * 4, MLB = WPG * HEADS * 2 * 4;   // of one group
+  static constexpr int NOW = 4 * STAGE + 2 * GROUPS * (OWB + MLB) <= 216 * 1024 ? 2 : 1;   // buffers
+  static constexpr int FIT = (216 * 1024 - NOW * GROUPS * (OWB + MLB)) / STAGE;
+  static constexpr int NSTG = FIT / GROUPS > 4 ? 4 : FIT / GROUPS, NST = NSTG * GROUPS;   // stages of a group
+  static constexpr int OW = NST * STAGE;                  // [GROUPS][NOW][WPG][HEADS][OLD]: O partials
+  static constexpr int MLW = OW + GROUPS * NOW * OWB;     // [GROUPS][NOW][WPG][HEADS][2]: (m, l)
+  static constexpr int CUM = MLW + GROUPS * NOW * MLB;    // [kMaxT + 1] block prefix
   static constexpr int POS = CUM + (kMaxT + 1) * 4;       // [kMaxT] positions
-  static constexpr int MISC = (POS + kMaxT * 4 + 15) / 16 * 16;   // -, abort, issued, -; masks
-  static constexpr int BAR = MISC + 16 + 16;
+  static constexpr int MISC = (POS + kMaxT * 4 + 15) / 16 * 16;   // -, abort, -, -; masks
+  static constexpr int BAR = MISC + 16 + 8 * 4;
   static constexpr int BYTES = BAR + 2 * NST * 8 + 1024;  // + alignment slack
-  static constexpr int ITEMS = (HEADS * (D / 4) + NCW * 32 - 1) / (NCW * 32);   // finished outputs
+  static constexpr int ITEMS = (HEADS * (D / 4) + NCT - 1) / NCT;   // 4 outputs that a thread finishes
   static_assert(BYTES <= 227 * 1024, "stage ring exceeds shared memory");
-  static_assert(NST <= 4, "one mask word per stage");
+  static_assert(NSTG >= 2 && NST <= 8, "one mask word per stage");
 };
 
 struct Params {
@@ -92,11 +99,11 @@ struct Params {
   const int32_t* seq_id;
   const int32_t* pos;
   uint16_t* og;
-  float* part_acc;   // [grid][2][HEADS][D]: a CTA's partials of its first and its last pair
-  float* part_ml;    // [grid][2][HEADS][2]
-  int4* join;        // [grid]: (row, KV head, parts, slot of the first part); parts 0: nothing
+  float* part_acc;   // [ranges][2][HEADS][D]: a range's partials of its first and its last pair
+  float* part_ml;    // [ranges][2][HEADS][2]
+  int4* join;        // [ranges]: (row, KV head, parts, slot of the first part); parts 0: nothing
   beam_paged_kv c;
-  int T, n_q, n_kv, G, max_pos, shift, whole;
+  int T, n_q, n_kv, G, max_pos, shift, whole, ranges;
   float sl2;
 };
 
@@ -164,8 +171,8 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 template <int NTHREADS>
-__device__ __forceinline__ void consumer_bar() {
-  asm volatile("bar.sync 1, %0;" ::"n"(NTHREADS) : "memory");
+__device__ __forceinline__ void consumer_bar(int group) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(NTHREADS) : "memory");
 }
 // Untiled bulk copy (16-byte aligned, a multiple of 16 bytes).
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -217,39 +224,36 @@ __device__ __forceinline__ Lane<FMT, C> lane_of(int slice, int pse) {
   return r;
 }
 
-// One warp's slices (SPW of 16 keys) of a staged block. kb: the stage; kbase[i]: position of
-// slice i's first key; live: bit i, slice i has keys; the row's keys are positions [lo, p].
-// qs: FP32 factor of the logits per accumulator column.
+// One warp's slices (SPW of 16 keys, WPG slices apart) of a staged block. kb: the stage; kbase:
+// position of the first slice's first key; live: bit i, slice i has keys; the row's keys are
+// positions [lo, p]. qs: FP32 factor of the logits per accumulator column.
 template <int FMT, class C>
 __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)[C::SPW],
                                            const uint32_t (&qb)[C::NT][C::D / 16][2],
-                                           const float (&qs)[C::NT][2], const int (&kbase)[C::SPW],
-                                           unsigned live, int lo, int p, WarpState<C>& S) {
-  constexpr int D = C::D, NT = C::NT, KK = D / 16, SPW = C::SPW;
+                                           const float (&qs)[C::NT][2], int kbase, unsigned live,
+                                           int lo, int p, WarpState<C>& S) {
+  constexpr int D = C::D, NT = C::NT, KK = D / 16, SPW = C::SPW, GAP = 16 * C::WPG;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  float sx[SPW][NT][4];
-  bool full[SPW];
-#pragma unroll
-  for (int i = 0; i < SPW; ++i)
-    full[i] = ((live >> i) & 1u) && kbase[i] >= lo && kbase[i] + 15 <= p;
+  const bool full = live == (1u << SPW) - 1 && kbase >= lo && kbase + (SPW - 1) * GAP + 15 <= p;
   auto valid = [&](int i, int key) {
-    return ((live >> i) & 1u) && kbase[i] + key >= lo && kbase[i] + key <= p;
+    const int pos = kbase + i * GAP + key;
+    return ((live >> i) & 1u) && pos >= lo && pos <= p;
   };
-  // ---- S^T = K . Q^T, two accumulation chains per tile
+  float sx[SPW][NT][4];
+  // ---- S^T = K . Q^T. Fragment: [0] (key g, head 2c), [1] (g, 2c+1), [2], [3] key g + 8
 #pragma unroll
   for (int i = 0; i < SPW; ++i) {
-    float sb[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sx[i][n][e] = sb[n][e] = 0.f;
+      for (int e = 0; e < 4; ++e) sx[i][n][e] = 0.f;
     if constexpr (FMT == kFmtBF16) {
 #pragma unroll
       for (int kk = 0; kk < KK; ++kk) {
         uint32_t a[4];
         ldsm_x4(kb + (kk >> 2) * (C::KB / C::PLANES) + (ln[i].k[0] ^ uint32_t((kk & 3) << 5)), a[0], a[1], a[2], a[3]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma_bf16((kk & 1) ? sb[n] : sx[i][n], a, qb[n][kk][0], qb[n][kk][1]);
+        for (int n = 0; n < NT; ++n) mma_bf16(sx[i][n], a, qb[n][kk][0], qb[n][kk][1]);
       }
     } else {
       // a thread's codes of keys g and g + 8: the d range [c D/4, (c + 1) D/4), four of a k step
@@ -271,7 +275,7 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
           e4m3x4_f16(w0[kk], a[0], a[2]);
           e4m3x4_f16(w1[kk], a[1], a[3]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16((kk & 1) ? sb[n] : sx[i][n], a, qb[n][kk][0], qb[n][kk][1]);
+          for (int n = 0; n < NT; ++n) mma_f16(sx[i][n], a, qb[n][kk][0], qb[n][kk][1]);
         }
       } else {
         // block scales of the thread's d range: two blocks (D 128) or one (D 64)
@@ -284,79 +288,88 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
           f0 = e4m3x2_f16x2(lds_u8(s0 + c) * 0x101u);
           f1 = e4m3x2_f16x2(lds_u8(s0 + 8 * (D / 16) + c) * 0x101u);
         }
+        uint32_t b0 = 0, b1 = 0;
 #pragma unroll
         for (int j = 0; j < KW; ++j) {   // a word: the codes of two k steps
           uint32_t h0[4], h1[4];
           e2m1x8_f16(w0[j], h0);
           e2m1x8_f16(w1[j], h1);
-          const uint32_t sel = D == 64 ? 0x3210u : (j < KW / 2 ? 0x1010u : 0x3232u);
-          const uint32_t b0 = prmt(f0, f0, sel), b1 = prmt(f1, f1, sel);
+          if (j % (KW / (D / 64)) == 0) {   // the next block's scale, in both halves
+            const uint32_t sel = j == 0 ? 0x1010u : 0x3232u;
+            b0 = prmt(f0, f0, sel);
+            b1 = prmt(f1, f1, sel);
+          }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const uint32_t a[4] = {mul_f16x2(h0[2 * e], b0), mul_f16x2(h1[2 * e], b1),
                                    mul_f16x2(h0[2 * e + 1], b0), mul_f16x2(h1[2 * e + 1], b1)};
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-              mma_f16(e ? sb[n] : sx[i][n], a, qb[n][2 * j + e][0], qb[n][2 * j + e][1]);
+            for (int n = 0; n < NT; ++n) mma_f16(sx[i][n], a, qb[n][2 * j + e][0], qb[n][2 * j + e][1]);
           }
         }
       }
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sx[i][n][e] += sb[n][e];
   }
-  // ---- logits relative to the running max, in log2 units. S^T fragment: [0] (key g, head 2c),
-  // [1] (g, 2c+1), [2], [3] key g + 8. Whether any exceeds it by kRescale is one vote; the
-  // max itself is taken across the warp only then.
+  // ---- y = logit - running max, in log2 units. Whether any exceeds it by kRescale (or a value
+  // row's scale the largest so far) is one vote; the max itself is taken across the warp only then.
   int ev[SPW][2];        // scale bytes of the value rows (quantised caches)
+  float fk[SPW][2];      // scales of the key rows
   float y[SPW][NT][4];
-  bool over = false;
+  float most = kNegInf;
+  int top = 0;
 #pragma unroll
   for (int i = 0; i < SPW; ++i) {
-    float ks[2] = {1.f, 1.f};
     if constexpr (FMT != kFmtBF16) {
       const uint32_t rs = kb + C::ORS + ln[i].rs + g;
-      ks[0] = pow2_of(lds_u8(rs));
-      ks[1] = pow2_of(lds_u8(rs + 8));
+      const uint32_t k2 = lds_u8(rs) | (lds_u8(rs + 8) << 8);
       ev[i][0] = int(lds_u8(rs + ln[i].pse));
       ev[i][1] = int(lds_u8(rs + ln[i].pse + 8));
+      uint32_t f2;   // 2^(b - 127) of both rows as bf16 (NaN for 255)
+      asm("{.reg .b16 b; cvt.u16.u32 b, %1; cvt.rn.bf16x2.ue8m0x2 %0, b;}" : "=r"(f2) : "r"(k2));
+      fk[i][0] = bf_lo(f2);
+      fk[i][1] = bf_hi(f2);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float f = FMT == kFmtBF16 ? qs[n][e & 1] : qs[n][e & 1] * ks[e >> 1];
-        sx[i][n][e] *= f;
-      }
-    if (!full[i]) {   // keys that are not the row's weigh nothing, whatever their slots hold
+      for (int e = 0; e < 4; ++e)
+        y[i][n][e] = fmaf(sx[i][n][e], FMT == kFmtBF16 ? qs[n][e & 1] : qs[n][e & 1] * fk[i][e >> 1], -S.m[n][e & 1]);
+  }
+  if (!full) {   // keys that are not the row's weigh nothing, whatever their slots hold
+#pragma unroll
+    for (int i = 0; i < SPW; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (valid(i, g + 8 * h)) continue;
         ev[i][h] = 0;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) sx[i][n][2 * h] = sx[i][n][2 * h + 1] = kNegInf;
+        for (int n = 0; n < NT; ++n) y[i][n][2 * h] = y[i][n][2 * h + 1] = kNegInf;
       }
-    }
+  }
+#pragma unroll
+  for (int i = 0; i < SPW; ++i) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y[i][n][e] = sx[i][n][e] - S.m[n][e & 1];
-        over |= y[i][n][e] > kRescale;
-      }
-    if constexpr (FMT != kFmtBF16)
-      over |= (ev[i][0] != 255 && ev[i][0] > S.E) || (ev[i][1] != 255 && ev[i][1] > S.E);
+      most = fmaxf(most, fmaxf(fmaxf(y[i][n][0], y[i][n][1]), fmaxf(y[i][n][2], y[i][n][3])));
+    if constexpr (FMT != kFmtBF16) top = max(top, max(ev[i][0], ev[i][1]));
   }
+  bool over = most > kRescale;
+  if constexpr (FMT != kFmtBF16) over |= top > S.E;
   if (__any_sync(0xffffffffu, over)) {
     float unit = 1.f;   // the accumulators hold values relative to 2^E
     if constexpr (FMT != kFmtBF16) {
-      int top = S.E;
+      top = S.E;
 #pragma unroll
       for (int i = 0; i < SPW; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) top = ev[i][h] != 255 ? max(top, ev[i][h]) : top;
+        for (int h = 0; h < 2; ++h) {
+          if (ev[i][h] != 255) {
+            top = max(top, ev[i][h]);
+          } else {   // a row that holds no numbers: neither does what reads it
+#pragma unroll
+            for (int n = 0; n < NT; ++n) y[i][n][2 * h] = y[i][n][2 * h + 1] = __uint_as_float(0x7FFFFFFFu);
+          }
+        }
       top = __reduce_max_sync(0xffffffffu, top);
       unit = ex2(float(S.E - top));
       S.E = top;
@@ -366,18 +379,33 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
       float cr[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float mn = S.m[n][h];
+        float up = 0.f;   // how far the max rises; from the lowest value it starts at, y is the logit
+        float old = S.m[n][h];
+        if (old == kLowest) {   // nothing seen so far: the logits themselves
+          up = kLowest;
+          old = 0.f;
 #pragma unroll
-        for (int i = 0; i < SPW; ++i) mn = fmaxf(mn, fmaxf(sx[i][n][h], sx[i][n][2 + h]));
+          for (int i = 0; i < SPW; ++i)
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        cr[h] = ex2(S.m[n][h] - mn);
-        S.m[n][h] = mn;
+            for (int r = 0; r < 2; ++r) {
+              float& v = y[i][n][2 * r + h];
+              if (v != kNegInf && v == v)
+                v = sx[i][n][2 * r + h] * (FMT == kFmtBF16 ? qs[n][h] : qs[n][h] * fk[i][r]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < SPW; ++i) up = fmaxf(up, fmaxf(y[i][n][h], y[i][n][2 + h]));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
+        const float now = old + up;
+        up = now - old;   // as rounded: what follows is relative to the new max
+        cr[h] = S.m[n][h] == kLowest ? 0.f : ex2(-up);
+        S.m[n][h] = now;
         S.l[n][h] *= cr[h];
 #pragma unroll
         for (int i = 0; i < SPW; ++i) {
-          y[i][n][h] = sx[i][n][h] - mn;
-          y[i][n][2 + h] = sx[i][n][2 + h] - mn;
+          y[i][n][h] -= up;
+          y[i][n][2 + h] -= up;
         }
         cr[h] *= unit;
       }
@@ -396,13 +424,11 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
   uint32_t pb[SPW][NT][PH][2];
 #pragma unroll
   for (int i = 0; i < SPW; ++i) {
-    float vs[2];
+    float vs[2] = {1.f, 1.f};
     if constexpr (FMT != kFmtBF16) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {   // 2^(e - E + kBias); NaN for a row that holds no numbers
-        const int b = ev[i][h] - S.E + 127 + kBias;
-        vs[h] = __uint_as_float(ev[i][h] == 255 ? 0x7FFFFFFFu : (b > 0 ? unsigned(b) << 23 : 0u));
-      }
+      for (int h = 0; h < 2; ++h)   // 2^(e - E + kBias), 0 below FP32's normal range
+        vs[h] = __uint_as_float(unsigned(max(ev[i][h] - S.E + 127 + kBias, 0)) << 23);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -429,7 +455,7 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
   for (int i = 0; i < SPW; ++i) {
     if constexpr (FMT == kFmtBF16) {
       uint32_t m01 = 0xFFFFFFFFu, m89 = 0xFFFFFFFFu;
-      if (!full[i]) {
+      if (!full) {
         m01 = (valid(i, 2 * c) ? 0x0000FFFFu : 0u) | (valid(i, 2 * c + 1) ? 0xFFFF0000u : 0u);
         m89 = (valid(i, 2 * c + 8) ? 0x0000FFFFu : 0u) | (valid(i, 2 * c + 9) ? 0xFFFF0000u : 0u);
       }
@@ -451,7 +477,7 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
       // keys {2c, 2c+1, 2c+8, 2c+9}, d range [g D/8, (g + 1) D/8): logical row g of m tile mt is
       // d = g D/8 + 2 mt, row g + 8 the next one
       constexpr int VW = C::ROWB / 32;
-      uint32_t r[4][VW], bs[4];
+      uint32_t r[4][VW], bs[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < 4; ++k) lds<VW>(kb + ln[i].v[k], r[k]);
       if constexpr (FMT == kFmtNVFP4) {   // the d range lies in one block of 16: one scale per key
@@ -459,7 +485,7 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
 #pragma unroll
         for (int k = 0; k < 4; ++k) bs[k] = lds_u8(sa + ((k & 1) + 8 * (k >> 1)) * (D / 16));
       }
-      if (!full[i]) {
+      if (!full) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (valid(i, 2 * c + (k & 1) + 8 * (k >> 1))) continue;
@@ -507,24 +533,23 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
     const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
     const Params P) {
   using C = Cfg<FMT, D, NT>;
-  constexpr int NCT = C::NCW * 32, BK = C::BK;
+  constexpr int NCT = C::NCT, BK = C::BK;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(sm);
   const uint32_t bar_full = sbase + C::BAR, bar_empty = bar_full + 8 * C::NST;
-  volatile int* misc = reinterpret_cast<volatile int*>(sm + C::MISC);   // -, abort, issued, -
+  volatile int* misc = reinterpret_cast<volatile int*>(sm + C::MISC);   // -, abort, -, -
   volatile unsigned* masks = reinterpret_cast<volatile unsigned*>(sm + C::MISC + 16);
   int* cum = reinterpret_cast<int*>(sm + C::CUM);
   int* rpos = reinterpret_cast<int*>(sm + C::POS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NST; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
-      mbar_init(bar_empty + 8 * s, C::NCW);
+      mbar_init(bar_full + 8 * s, 2);   // the producers of K and of V
+      mbar_init(bar_empty + 8 * s, C::WPG);
     }
     misc[1] = 0;
-    misc[2] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait();
@@ -556,8 +581,11 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
   }
   __syncthreads();
   const int total = cum[T] * P.n_kv;
-  const int R = max(1, (total + int(gridDim.x) - 1) / int(gridDim.x));
-  int f_lo = int(min(int64_t(total), int64_t(blockIdx.x) * R)), f_hi = min(total, f_lo + R);
+  // the warp's group and its range of the flat blocks
+  const int grp = warp < C::NCW ? warp / C::WPG : (warp - C::NCW) % C::GROUPS;
+  const int range = grp * int(gridDim.x) + int(blockIdx.x);
+  const int R = max(1, (total + P.ranges - 1) / P.ranges);
+  int f_lo = int(min(int64_t(total), int64_t(range) * R)), f_hi = min(total, f_lo + R);
   // row of flat block f: the last t with cum[t] * n_kv <= f
   auto row_at = [&](int f) {
     int a = 0, b = T;   // cum[a] * n_kv <= f < cum[b] * n_kv
@@ -579,10 +607,11 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
   }
   const int t_lo = f_lo < f_hi ? row_at(f_lo) : 0;
 
-  if (warp == C::NCW) {
-    // ---------------- producer
-    const int pse = min(P.c.page_size, BK);               // keys of a page in a block
-    const int npg = BK / pse;
+  if (warp >= C::NCW) {
+    // ---------------- producers
+    const int par = C::GROUPS == 1 ? (warp - C::NCW) & 1 : 0;   // first of the warp's blocks
+    const bool vals = warp - C::NCW >= 2;
+    const int pse = min(P.c.page_size, BK), npg = BK / pse;   // keys of a page in a block, pages
     struct At {
       int t, hk, j, nb, blk0, lo, p, s;
     };
@@ -594,14 +623,23 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
       a.p = r.p;
       a.s = r.s;
     };
-    auto advance = [&](At& a) {
-      if (++a.j < a.nb) return;
-      a.j = 0;
-      if (++a.hk < P.n_kv) return;
-      a.hk = 0;
-      do ++a.t;
-      while (a.t < T && cum[a.t + 1] == cum[a.t]);
-      if (a.t < T) load_row(a);
+    auto advance = [&](At& a, int by) {   // stays on the last pair at the end
+      a.j += by;
+      while (a.j >= a.nb) {
+        int hk = a.hk + 1, t = a.t;
+        if (hk == P.n_kv) {
+          hk = 0;
+          do ++t;
+          while (t < T && cum[t + 1] == cum[t]);
+          if (t == T) return;
+        }
+        a.j -= a.nb;
+        a.hk = hk;
+        if (t != a.t) {
+          a.t = t;
+          load_row(a);
+        }
+      }
     };
     // lane i's page of the block: its number, or -2 where the block has no key in it
     auto fetch = [&](const At& a) -> int {
@@ -612,22 +650,25 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
     };
     At at{t_lo, 0, 0, 1, 0, 1, 0, 0};
     int id = -2;
-    if (f_lo < f_hi) {
+    if (f_lo + par < f_hi) {
       load_row(at);
       const int r = f_lo - cum[at.t] * P.n_kv;
       at.hk = r / at.nb;
       at.j = r - at.hk * at.nb;
+      advance(at, par);
       id = fetch(at);
     }
-    int i = 0;
-    for (int f = f_lo; f < f_hi; ++f, ++i) {
+    int i = par;
+    for (int f = f_lo + par; f < f_hi; f += C::STEP, i += C::STEP) {
       const At a = at;
       const int page = id;
-      advance(at);
-      if (f + 1 < f_hi) id = fetch(at);   // the next block's pages, while this one waits
-      const int st = i % C::NST;
+      if (f + C::STEP < f_hi) {
+        advance(at, C::STEP);
+        id = fetch(at);   // the pages of the next block, while this one waits
+      }
+      const int st = grp * C::NSTG + i % C::NSTG;
       bool go = misc[1] == 0;
-      if (go && i >= C::NST) go = mbar_wait(bar_empty + 8 * st, ((i / C::NST) - 1) & 1);
+      if (go && i >= C::NSTG) go = mbar_wait(bar_empty + 8 * st, ((i / C::NSTG) - 1) & 1);
       if (!__all_sync(0xffffffffu, go)) {
         if (lane == 0) misc[1] = 1;
         break;
@@ -635,56 +676,62 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
       const bool ok = page >= 0 && page < P.c.num_pages;
       if (page != -2 && !ok) flag(BEAM_DEV_BAD_PAGE);
       const unsigned okm = __ballot_sync(0xffffffffu, ok);
-      const unsigned slices = __ballot_sync(0xffffffffu, lane < C::SLICES && ((okm >> (lane * 16 / pse)) & 1u));
       const uint32_t base = sbase + st * C::STAGE, fb = bar_full + 8 * st;
-      const bool with_q = f == f_lo || a.j == 0;
-      if (lane == 0) {
-        masks[st] = slices;
-        const uint32_t per = uint32_t(2 * pse * (C::ROWB + (FMT != kFmtBF16 ? 1 : 0) + (FMT == kFmtNVFP4 ? D / 16 : 0)));
-        mbar_expect_tx(fb, __popc(okm) * per + (with_q ? P.G * D * 2 : 0));
-      }
-      __syncwarp();
-      if (ok) {
-        const int z = page * P.n_kv + a.hk;
-        const int off = ((a.blk0 + a.j) * BK + lane * pse) & (P.c.page_size - 1);   // first key in the page
-        const uint32_t dk = base + lane * pse * (C::ROWB / C::PLANES), dv = dk + C::KB;
-        const int y = C::PLANES == 2 ? off : off * C::ROWB / 128;
-        tma_load_3d(dk, &tk, 0, y, z, fb);
-        if constexpr (C::PLANES == 2) tma_load_3d(dk + C::KB / 2, &tk, 128, y, z, fb);
-        tma_load_3d(dv, &tv, 0, y, z, fb);
-        if constexpr (C::PLANES == 2) tma_load_3d(dv + C::KB / 2, &tv, 128, y, z, fb);
-        if constexpr (FMT != kFmtBF16) {
-          const size_t row = size_t(z) * 2 * P.c.page_size + off;
-          const uint32_t dr = base + C::ORS + lane * 2 * pse;
-          if (npg > 1 || pse == P.c.page_size) {
-            bulk_load(dr, P.c.row_scale + row, 2 * pse, fb);
-          } else {   // part of a page: K's and V's scales apart
-            bulk_load(dr, P.c.row_scale + row, pse, fb);
-            bulk_load(dr + pse, P.c.row_scale + row + P.c.page_size, pse, fb);
+      const int z = page * P.n_kv + a.hk;
+      const int off = ((a.blk0 + a.j) * BK + lane * pse) & (P.c.page_size - 1);   // first key in the page
+      const int y = C::PLANES == 2 ? off : off * C::ROWB / 128;
+      const bool part = pse < P.c.page_size;   // part of a page: K's and V's scales lie apart
+      if (!vals) {
+        const bool with_q = f == f_lo || a.j == 0;   // a pair's first block here
+        const unsigned slices = __ballot_sync(0xffffffffu, lane < C::SLICES && ((okm >> (lane * 16 / pse)) & 1u));
+        if (lane == 0) {
+          masks[st] = slices;
+          mbar_expect_tx(fb, __popc(okm) * pse * (C::ROWB + (FMT != kFmtBF16 ? 2 : 0)) + (with_q ? P.G * D * 2 : 0));
+        }
+        __syncwarp();
+        if (ok) {
+          const uint32_t dk = base + lane * pse * (C::ROWB / C::PLANES);
+          tma_load_3d(dk, &tk, 0, y, z, fb);
+          if constexpr (C::PLANES == 2) tma_load_3d(dk + C::KB / 2, &tk, 128, y, z, fb);
+          if constexpr (FMT != kFmtBF16) {
+            const uint8_t* src = P.c.row_scale + size_t(z) * 2 * P.c.page_size + off;
+            const uint32_t dr = base + C::ORS + lane * 2 * pse;
+            bulk_load(dr, src, part ? pse : 2 * pse, fb);
+            if (part) bulk_load(dr + pse, src + P.c.page_size, pse, fb);
           }
+        }
+        if (with_q && lane == 31)
+          bulk_load(base + C::OQ, P.q + (size_t(a.t) * P.n_q + a.hk * P.G) * D, P.G * D * 2, fb);
+      } else {
+        if (lane == 0)
+          mbar_expect_tx(fb, __popc(okm) * pse * (C::ROWB + (FMT == kFmtNVFP4 ? 2 * (D / 16) : 0)));
+        __syncwarp();
+        if (ok) {
+          const uint32_t dv = base + C::KB + lane * pse * (C::ROWB / C::PLANES);
+          tma_load_3d(dv, &tv, 0, y, z, fb);
+          if constexpr (C::PLANES == 2) tma_load_3d(dv + C::KB / 2, &tv, 128, y, z, fb);
           if constexpr (FMT == kFmtNVFP4) {
+            const uint8_t* src = P.c.block_scale + (size_t(z) * 2 * P.c.page_size + off) * (D / 16);
             const uint32_t db = base + C::OBS + lane * 2 * pse * (D / 16);
-            if (npg > 1 || pse == P.c.page_size) {
-              bulk_load(db, P.c.block_scale + row * (D / 16), 2 * pse * (D / 16), fb);
-            } else {
-              bulk_load(db, P.c.block_scale + row * (D / 16), pse * (D / 16), fb);
-              bulk_load(db + pse * (D / 16), P.c.block_scale + (row + P.c.page_size) * (D / 16),
-                        pse * (D / 16), fb);
-            }
+            bulk_load(db, src, (part ? 1 : 2) * pse * (D / 16), fb);
+            if (part) bulk_load(db + pse * (D / 16), src + P.c.page_size * (D / 16), pse * (D / 16), fb);
           }
         }
       }
-      if (with_q && lane == 31)
-        bulk_load(base + C::OQ, P.q + (size_t(a.t) * P.n_q + a.hk * P.G) * D, P.G * D * 2, fb);
       __syncwarp();
     }
-    if (lane == 0) misc[2] = i;
+    // normally done at once, with the last blocks: after an expired wait elsewhere, let the copies
+    // in flight land before the CTA's shared memory is released
+    if (lane == 0)
+      for (int k = i - C::STEP; k >= 0 && k >= i - C::NSTG; k -= C::STEP)
+        mbar_wait(bar_full + 8 * (grp * C::NSTG + k % C::NSTG), (k / C::NSTG) & 1);
   } else {
     // ---------------- consumers
-    const int w = warp, g = lane >> 2, c = lane & 3, ct = threadIdx.x;
+    const int w = warp % C::WPG, g = lane >> 2, c = lane & 3, ct = threadIdx.x % NCT;
     Lane<FMT, C> ln[C::SPW];
 #pragma unroll
-    for (int e = 0; e < C::SPW; ++e) ln[e] = lane_of<FMT, C>(w + e * C::NCW, min(P.c.page_size, BK));
+    for (int e = 0; e < C::SPW; ++e) ln[e] = lane_of<FMT, C>(w + e * C::WPG, min(P.c.page_size, BK));
+    bool dead = false;   // a wait has expired: the rest of the range passes without results
     const int G = P.G;
     int i = 0, t = t_lo, f = f_lo, buf = 0;
     int4 join = make_int4(0, 0, 0, 0);
@@ -726,11 +773,10 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
         for (int mt = 0; mt < D / 16; ++mt) S.acc[n][mt][0] = S.acc[n][mt][1] = S.acc[n][mt][2] = S.acc[n][mt][3] = 0.f;
       }
       for (int j = j0; j < j1; ++j, ++i) {
-        const int st = i % C::NST;
+        const int st = grp * C::NSTG + i % C::NSTG;
         const uint32_t kb = sbase + st * C::STAGE;
-        bool ok = misc[1] == 0;
-        if (ok) ok = mbar_wait(bar_full + 8 * st, (i / C::NST) & 1);
-        if (__all_sync(0xffffffffu, ok)) {
+        if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(bar_full + 8 * st, (i / C::NSTG) & 1));
+        if (!dead) {
           if (j == j0) {
             // q fragments (B operand, column = head g of the tile)
 #pragma unroll
@@ -773,14 +819,12 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
               }
             }
           }
-          const unsigned mask = masks[st];
-          int kbase[C::SPW];
+          const int kbase = BK * (blk0 + j) + 16 * w + 1;
           unsigned live = 0;
 #pragma unroll
           for (int e = 0; e < C::SPW; ++e) {
-            const int sl = w + e * C::NCW;
-            kbase[e] = BK * (blk0 + j) + 16 * sl + 1;
-            if (((mask >> sl) & 1u) && kbase[e] <= p && kbase[e] + 15 >= lo) live |= 1u << e;
+            const int k0 = kbase + 16 * C::WPG * e;
+            if (((masks[st] >> (w + e * C::WPG)) & 1u) && k0 <= p && k0 + 15 >= lo) live |= 1u << e;
           }
           if (live) warp_block<FMT, C>(kb, ln, qb, qs, kbase, live, lo, p, S);
         } else if (lane == 0) {
@@ -792,9 +836,9 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
       // ---- combine the consumer warps' partials of the pair. Two buffers in turn: who writes
       // one has passed the barrier of the pair between, which its last readers came to later
       // (one buffer, where two do not fit, needs a barrier of its own).
-      if constexpr (C::NOW == 1) consumer_bar<NCT>();
-      float* Ow = reinterpret_cast<float*>(sm + C::OW + buf * C::OWB);
-      float2* MLw = reinterpret_cast<float2*>(sm + C::MLW + buf * C::MLB);
+      if constexpr (C::NOW == 1) consumer_bar<NCT>(grp);
+      float* Ow = reinterpret_cast<float*>(sm + C::OW + (grp * C::NOW + buf) * C::OWB);
+      float2* MLw = reinterpret_cast<float2*>(sm + C::MLW + (grp * C::NOW + buf) * C::MLB);
       buf = C::NOW - 1 - buf;
       const float unit = FMT == kFmtBF16 ? 1.f : ldexpf(1.f, S.E - 127 - kBias);
 #pragma unroll
@@ -820,27 +864,24 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
           MLw[h0 + 1] = make_float2(S.m[n][1], S.l[n][1]);
         }
       }
-      consumer_bar<NCT>();
-      const int slot = f == f_lo ? 0 : 1;   // the CTA's first pair, or its last
-      const size_t pb = (size_t(2 * blockIdx.x) + slot) * C::HEADS;
+      consumer_bar<NCT>(grp);
+      const int slot = f == f_lo ? 0 : 1;   // the range's first pair, or its last
+      const size_t pb = (size_t(2 * range) + slot) * C::HEADS;
 #pragma unroll
       for (int it = 0; it < C::ITEMS; ++it) {
         const int idx = ct + it * NCT;
         if (idx >= G * (D / 4)) break;
         const int h = idx / (D / 4), d = 4 * (idx - h * (D / 4));
         float M = kLowest, L = 0.f;
-        float2 ml[C::NCW];
-#pragma unroll
-        for (int ww = 0; ww < C::NCW; ++ww) {
-          ml[ww] = MLw[ww * C::HEADS + h];
-          M = fmaxf(M, ml[ww].x);
-        }
         float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int ww = 0; ww < C::NCW; ++ww) {
-          const float fw = ex2(ml[ww].x - M);
+        for (int ww = 0; ww < C::WPG; ++ww) M = fmaxf(M, MLw[ww * C::HEADS + h].x);
+#pragma unroll
+        for (int ww = 0; ww < C::WPG; ++ww) {
+          const float2 ml = MLw[ww * C::HEADS + h];
+          const float fw = ex2(ml.x - M);
+          L += fw * ml.y;
           const float4 v = *reinterpret_cast<const float4*>(Ow + (ww * C::HEADS + h) * C::OLD + d);
-          L += fw * ml[ww].y;
           O.x += fw * v.x;
           O.y += fw * v.y;
           O.z += fw * v.z;
@@ -862,7 +903,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
         *reinterpret_cast<uint2*>(P.og + o_pair + 4 * idx) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
       }
       if (j0 == 0 && j1 < nb)   // the pair begins here and runs on
-        join = make_int4(t, hk, (f_pair + nb - 1) / R - int(blockIdx.x) + 1, slot);
+        join = make_int4(t, hk, (f_pair + nb - 1) / R - range + 1, slot);
       // ---- next pair
       f = f_pair + j1;
       j0 = 0;
@@ -872,36 +913,29 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
         while (t < T && cum[t + 1] == cum[t]);
       }
     }
-    if (ct == 0) P.join[blockIdx.x] = join;
+    if (ct == 0 && range < P.ranges) P.join[range] = join;
     // ---- rows that attend to nothing
     for (int r = blockIdx.x; r < T; r += gridDim.x)
       if (cum[r + 1] == cum[r])
-        for (int x = ct; x < P.n_q * (D / 8); x += NCT)
+        for (int x = threadIdx.x; x < P.n_q * (D / 8); x += C::GROUPS * NCT)
           reinterpret_cast<uint4*>(P.og + size_t(r) * P.n_q * D)[x] = make_uint4(0, 0, 0, 0);
   }
   __syncthreads();
   pdl_trigger();   // not earlier: the join and what follows would run beside the key stream
-  if (warp == C::NCW && lane == 0) {
-    // normally a no-op: every issued block was consumed; after an expired wait, let the
-    // copies still in flight land before the CTA's shared memory is released
-    const int n = misc[2];
-    for (int k = n > C::NST ? n - C::NST : 0; k < n; ++k)
-      mbar_wait(bar_full + 8 * (k % C::NST), (k / C::NST) & 1);
-    if (misc[1]) flag(BEAM_DEV_TIMEOUT);
-  }
+  if (threadIdx.x == 0 && misc[1]) flag(BEAM_DEV_TIMEOUT);
 }
 
-// Join of the pair that begins in CTA blockIdx.x's range and runs on past it, one query head
+// Join of the pair that begins in range blockIdx.x and runs on past it, one query head
 // (blockIdx.y) per CTA, one thread per output element.
 template <int D, int HEADS>
 __global__ void __launch_bounds__(D) paged_join_kernel(const Params P) {
   pdl_trigger();
-  __shared__ float wsh[kMaxGrid], lsh[kMaxGrid];
+  __shared__ float wsh[kMaxParts], lsh[kMaxParts];
   pdl_wait();
   const int4 jn = P.join[blockIdx.x];
   const int n = jn.z, h = blockIdx.y;
   if (n == 0) return;
-  // the first part's slot is jn.w; in the CTAs after it the pair is the first
+  // the first part's slot is jn.w; in the ranges after it the pair is the first
   auto slot = [&](int s) { return (size_t(2 * (blockIdx.x + s)) + (s == 0 ? jn.w : 0)) * HEADS + h; };
   for (int s = threadIdx.x; s < n; s += D) {
     const float2 v = __ldcg(reinterpret_cast<const float2*>(P.part_ml + slot(s) * 2));
@@ -951,9 +985,15 @@ int max_grid() {
   return sms < kMaxGrid ? sms : kMaxGrid;
 }
 
+// pairs: (row, KV head) pairs; blocks: an upper bound of their blocks
 template <int FMT, int D, int NT>
-cudaError_t launch(const Params& p, int grid, bool join, cudaStream_t st) {
+cudaError_t launch(Params p, int64_t pairs, int64_t blocks, cudaStream_t st) {
   using C = Cfg<FMT, D, NT>;
+  // a range is not smaller than a block, nor, where pairs are not split, than a pair
+  const int64_t units = p.whole ? pairs : blocks;
+  const int sms = max_grid();
+  p.ranges = int(units < C::GROUPS * sms ? units : C::GROUPS * sms);
+  const int grid = p.ranges < sms ? p.ranges : sms;
   const beam_paged_kv& c = p.c;
   CUtensorMap mk, mv;
   const int rows = C::PLANES == 2 ? c.page_size : c.page_size * C::ROWB / 128;
@@ -969,16 +1009,16 @@ cudaError_t launch(const Params& p, int grid, bool join, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::BYTES, st, mk, mv, p);
-  if (e != cudaSuccess || !join) return e;
-  return launch_pdl(paged_join_kernel<D, C::HEADS>, dim3(grid, p.G), dim3(D), 0, st, p);
+  if (e != cudaSuccess || p.whole) return e;
+  return launch_pdl(paged_join_kernel<D, C::HEADS>, dim3(p.ranges, p.G), dim3(D), 0, st, p);
 }
 
 template <int FMT>
-cudaError_t launch_fmt(const Params& p, int grid, bool join, cudaStream_t st) {
+cudaError_t launch_fmt(const Params& p, int64_t pairs, int64_t blocks, cudaStream_t st) {
   const bool one = p.G <= 8;
   if (p.c.head_dim == 128)
-    return one ? launch<FMT, 128, 1>(p, grid, join, st) : launch<FMT, 128, 2>(p, grid, join, st);
-  return one ? launch<FMT, 64, 1>(p, grid, join, st) : launch<FMT, 64, 2>(p, grid, join, st);
+    return one ? launch<FMT, 128, 1>(p, pairs, blocks, st) : launch<FMT, 128, 2>(p, pairs, blocks, st);
+  return one ? launch<FMT, 64, 1>(p, pairs, blocks, st) : launch<FMT, 64, 2>(p, pairs, blocks, st);
 }
 
 }  // namespace
@@ -990,9 +1030,9 @@ extern "C" size_t beam_paged_workspace_bytes(const beam_layer_cfg* cfg, int T, i
   using namespace beam::paged;
   (void)max_pos;
   if (cfg == nullptr || T <= 0 || cfg->n_q <= 0 || cfg->head_dim <= 0) return 256;
-  const size_t parts = size_t(kMaxGrid) * 2 * 16;
+  const size_t parts = size_t(kMaxParts) * 2 * 8;   // or half the ranges, of 16 heads
   return align_up(parts * cfg->head_dim * 4, 256) + align_up(parts * 2 * 4, 256) +
-         align_up(kMaxGrid * sizeof(int4), 256) +
+         align_up(kMaxParts * sizeof(int4), 256) +
          align_up(size_t(T) * cfg->n_q * cfg->head_dim * 2, 256);
 }
 
@@ -1028,11 +1068,11 @@ extern "C" beam_status beam_paged_attn(const beam_layer_cfg* cfg, const beam_bf1
   if (nb * slice * cfg->n_kv > INT32_MAX) return BEAM_ERR_UNSUPPORTED;   // flat block numbers
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   Carver cv{static_cast<char*>(ws), ws_bytes};
-  const size_t parts = size_t(kMaxGrid) * 2 * 8 * nt;
+  const size_t parts = size_t(kMaxParts) * 2 * 8;
   Params p{};
   p.part_acc = cv.take<float>(parts * D);
   p.part_ml = cv.take<float>(parts * 2);
-  p.join = cv.take<int4>(kMaxGrid);
+  p.join = cv.take<int4>(kMaxParts);
   uint16_t* og = w_o ? cv.take<uint16_t>(size_t(T) * HD) : out;
   if (!cv.ok) return BEAM_ERR_INVALID_ARG;
   p.gate_bias = gate_bias;
@@ -1051,14 +1091,11 @@ extern "C" beam_status beam_paged_attn(const beam_layer_cfg* cfg, const beam_bf1
     p.og = og + size_t(t0) * HD;
     p.seq_id = seq_id + t0;
     p.pos = pos + t0;
-    int64_t grid = nb * p.T * cfg->n_kv;
-    if (p.whole) grid = int64_t(p.T) * cfg->n_kv;
-    if (grid > max_grid()) grid = max_grid();
-    if (grid < 1) grid = 1;
+    const int64_t pairs = int64_t(p.T) * cfg->n_kv, blocks = nb * pairs;
     cudaError_t e;
-    if (cache->dtype == kFmtBF16) e = launch_fmt<kFmtBF16>(p, int(grid), !p.whole, st);
-    else if (cache->dtype == kFmtFP8) e = launch_fmt<kFmtFP8>(p, int(grid), !p.whole, st);
-    else e = launch_fmt<kFmtNVFP4>(p, int(grid), !p.whole, st);
+    if (cache->dtype == kFmtBF16) e = launch_fmt<kFmtBF16>(p, pairs, blocks, st);
+    else if (cache->dtype == kFmtFP8) e = launch_fmt<kFmtFP8>(p, pairs, blocks, st);
+    else e = launch_fmt<kFmtNVFP4>(p, pairs, blocks, st);
     if (e != cudaSuccess) return cuda_status(e);
   }
   if (w_o != nullptr) {

@@ -381,7 +381,8 @@ def test_attention_leaves_bad_pages_out(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
-@pytest.mark.parametrize("qe,ke,ve", [(0, 0, 60), (0, 0, -90), (60, -60, 0), (-40, 40, 3), (-100, 0, 0)])
+@pytest.mark.parametrize("qe,ke,ve", [(0, 0, 60), (0, 0, -90), (60, -60, 0), (-40, 40, 3), (-100, 0, 0),
+                                       (119, -122, 0)])
 def test_attention_magnitudes(fmt, qe, ke, ve):
     """Queries, keys and values far from 1: the powers of two carry them."""
     cfg = cfg_for(4, 2, 128)
