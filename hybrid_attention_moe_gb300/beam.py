@@ -166,8 +166,8 @@ class LayerCfg:
         """Reference to a C struct of the present values, built again after a change."""
         kept = self.__dict__.get("_kept")
         if kept is None:
-            kept = self.__dict__["_kept"] = self.c()
-        return ctypes.byref(kept)
+            kept = self.__dict__["_kept"] = ctypes.byref(self.c())
+        return kept
 
 
 @dataclasses.dataclass
@@ -189,26 +189,20 @@ class KVCache:
                         self.v_scale, self.k.shape[0], self.k.shape[2], self.window)
 
 
-def _refuse(name, t, dtype, shape, device):
-    want = f"a contiguous {dtype} tensor" + ("" if shape is None else f" of shape {tuple(shape)}")
-    raise BeamError(f"{name}: {want} on cuda:{device} is wanted, got {t.dtype} {tuple(t.shape)} "
-                    f"with strides {t.stride()} on {t.device}")
-
-
-def _want(device, name, t, dtype, shape=None):
+def _want(device, name, t, dtype, n):
     """Refuses a tensor that the library would read as something else: another type or device,
-    a shape or strides that are not the documented ones."""
-    if (t.dtype != dtype or not t.is_contiguous() or (shape is not None and t.shape != shape) or
-            t.get_device() != device):
-        _refuse(name, t, dtype, shape, device)
+    gaps between its elements, or not the n elements of the documented shape."""
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != device:
+        raise BeamError(f"{name}: {n} contiguous {dtype} elements on cuda:{device} are wanted, got "
+                        f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
 def _on_device(cache):
     """The cache's device, which has to be the current one: the library launches there."""
-    if cache.device != torch.cuda.current_device():
-        raise BeamError(f"the cache is on cuda:{cache.device}, but the current device is "
-                        f"cuda:{torch.cuda.current_device()}")
-    return cache.device
+    dev = torch._C._cuda_getDevice()
+    if cache.device != dev:
+        raise BeamError(f"the cache is on cuda:{cache.device}, but the current device is cuda:{dev}")
+    return dev
 
 
 def _raw_stream(stream, device):
@@ -235,18 +229,19 @@ class PagedKVCache:
         pages, n_kv, size, width = k.shape
         code = torch.bfloat16 if row_scale is None else torch.uint8
         dev = k.get_device()
-        _want(dev, "k", k, code)
-        _want(dev, "v", v, code, k.shape)
-        _want(dev, "page_table", page_table, torch.int32)
+        _want(dev, "k", k, code, k.numel())
+        _want(dev, "v", v, code, k.numel())
+        _want(dev, "page_table", page_table, torch.int32, page_table.numel())
         self.dtype = BEAM_PAGED_BF16
         if row_scale is not None:
-            _want(dev, "row_scale", row_scale, torch.uint8, (pages, n_kv, 2, size))
+            _want(dev, "row_scale", row_scale, torch.uint8, pages * n_kv * 2 * size)
             self.dtype = BEAM_PAGED_FP8
         if block_scale is not None:
             if row_scale is None:
                 raise BeamError("PagedKVCache: block_scale without row_scale")
             width *= 2
-            _want(dev, "block_scale", block_scale, torch.uint8, (pages, n_kv, 2, size, width // 16))
+            _want(dev, "block_scale", block_scale, torch.uint8,
+                  pages * n_kv * 2 * size * width // 16)
             self.dtype = BEAM_PAGED_NVFP4
         if dev < 0:
             raise BeamError("PagedKVCache: the tensors must be on a CUDA device")
@@ -362,7 +357,8 @@ def beam_paged_kv_write(k, v, seq_id, pos, cache: PagedKVCache, stream=None):
     T, step = k.shape[0], n_kv * D
     for name, x in (("k", k), ("v", v)):
         if x.dtype != torch.bfloat16 or x.shape != (T, n_kv, D) or x.get_device() != dev:
-            _refuse(name, x, torch.bfloat16, (T, n_kv, D), dev)
+            raise BeamError(f"beam_paged_kv_write: {name} must be bfloat16 ({T}, {n_kv}, {D}) on "
+                            f"cuda:{dev}, got {x.dtype} {tuple(x.shape)} on {x.device}")
         if T and not x.is_contiguous():
             s0, s1, s2 = x.stride()
             if s2 != 1 or (n_kv > 1 and s1 != D):
@@ -372,8 +368,8 @@ def beam_paged_kv_write(k, v, seq_id, pos, cache: PagedKVCache, stream=None):
         step = k.stride(0)
         if v.stride(0) != step:
             raise BeamError("beam_paged_kv_write: k and v have different strides between tokens")
-    _want(dev, "seq_id", seq_id, torch.int32, (T,))
-    _want(dev, "pos", pos, torch.int32, (T,))
+    _want(dev, "seq_id", seq_id, torch.int32, T)
+    _want(dev, "pos", pos, torch.int32, T)
     st = lib().beam_paged_kv_write(k.data_ptr(), v.data_ptr(), step, seq_id.data_ptr(),
                                    pos.data_ptr(), T, cache._ref, _raw_stream(stream, dev))
     if st:
@@ -386,13 +382,12 @@ def beam_paged_kv_read(cache: PagedKVCache, seq_id, first, last, max_len, dst: K
     dst, slot (p-1) % capacity."""
     dev = _on_device(cache)
     N = seq_id.shape[0]
-    _want(dev, "seq_id", seq_id, torch.int32, (N,))
-    _want(dev, "first", first, torch.int32, (N,))
-    _want(dev, "last", last, torch.int32, (N,))
+    _want(dev, "seq_id", seq_id, torch.int32, N)
+    _want(dev, "first", first, torch.int32, N)
+    _want(dev, "last", last, torch.int32, N)
     rows, _, cap, _ = dst.k.shape
-    dims = (rows, cache.n_kv, cap, cache.head_dim)
-    _want(dev, "dst.k", dst.k, torch.bfloat16, dims)
-    _want(dev, "dst.v", dst.v, torch.bfloat16, dims)
+    _want(dev, "dst.k", dst.k, torch.bfloat16, rows * cache.n_kv * cap * cache.head_dim)
+    _want(dev, "dst.v", dst.v, torch.bfloat16, rows * cache.n_kv * cap * cache.head_dim)
     kc = dst.c()
     st = lib().beam_paged_kv_read(cache._ref, seq_id.data_ptr(), first.data_ptr(),
                                   last.data_ptr(), N, int(max_len), ctypes.byref(kc),
@@ -404,29 +399,35 @@ def beam_paged_kv_read(cache: PagedKVCache, seq_id, first, last, max_len, dst: K
 def beam_paged_attn(cfg: LayerCfg, q, g, gate_bias, cache: PagedKVCache, seq_id, pos, max_pos,
                     w_o, out, ws: torch.Tensor, stream=None):
     """Decode attention over the pages; g, gate_bias None: no gate; w_o None: out is [T][n_q*D]."""
-    dev, bf = _on_device(cache), torch.bfloat16
-    T, n_q, D = q.shape[0], cfg.n_q, cfg.head_dim
-    _want(dev, "q", q, bf, (T, n_q, D))
-    pg = pb = pw = None
+    dev, bf, i32 = _on_device(cache), torch.bfloat16, torch.int32
+    T, n_q = q.size(0), cfg.n_q
+    row = n_q * cfg.head_dim
+    n, width = T * row, row if w_o is None else cfg.hidden
     if (g is None) != (gate_bias is None):
         raise BeamError("beam_paged_attn: g and gate_bias go together")
+    # one test of everything; what is wrong is looked for where it fails
+    if not (q.dtype is bf and q.numel() == n and q.is_contiguous() and q.get_device() == dev and
+            out.dtype is bf and out.numel() == T * width and out.is_contiguous() and
+            out.get_device() == dev and seq_id.dtype is i32 and seq_id.numel() == T and
+            seq_id.is_contiguous() and seq_id.get_device() == dev and pos.dtype is i32 and
+            pos.numel() == T and pos.is_contiguous() and pos.get_device() == dev and
+            ws.is_contiguous() and ws.get_device() == dev):
+        _want(dev, "q", q, bf, n)
+        _want(dev, "out", out, bf, T * width)
+        _want(dev, "seq_id", seq_id, i32, T)
+        _want(dev, "pos", pos, i32, T)
+        _want(dev, "ws", ws, ws.dtype, ws.numel())
+    pg = pb = pw = None
     if g is not None:
-        _want(dev, "g", g, bf, (T, n_q * D))
-        _want(dev, "gate_bias", gate_bias, bf, (n_q,))
+        _want(dev, "g", g, bf, n)
+        _want(dev, "gate_bias", gate_bias, bf, n_q)
         pg, pb = g.data_ptr(), gate_bias.data_ptr()
-    width = n_q * D
     if w_o is not None:
-        width = cfg.hidden
-        _want(dev, "w_o", w_o, bf, (width, n_q * D))
+        _want(dev, "w_o", w_o, bf, width * row)
         pw = w_o.data_ptr()
-    _want(dev, "out", out, bf, (T, width))
-    _want(dev, "seq_id", seq_id, torch.int32, (T,))
-    _want(dev, "pos", pos, torch.int32, (T,))
-    _want(dev, "ws", ws, torch.uint8)
-    st = lib().beam_paged_attn(cfg._ref(), q.data_ptr(), pg, pb, cache._ref,
-                               seq_id.data_ptr(), pos.data_ptr(), T, int(max_pos), pw,
-                               out.data_ptr(), ws.data_ptr(), ws.numel(),
-                               _raw_stream(stream, dev))
+    st = lib().beam_paged_attn(cfg._ref(), q.data_ptr(), pg, pb, cache._ref, seq_id.data_ptr(),
+                               pos.data_ptr(), T, int(max_pos), pw, out.data_ptr(), ws.data_ptr(),
+                               ws.nbytes, _raw_stream(stream, dev))
     if st:
         _check(st, "beam_paged_attn")
 

@@ -48,7 +48,7 @@ constexpr float kNegInf = -INFINITY;
 constexpr float kLowest = -3e38f;   // a running max that has seen nothing: finite, so differences are
 constexpr float kRescale = 8.f;     // log2 units by which the running max may lag
 constexpr int kMaxGrid = 152;       // CTAs at most
-constexpr int kMaxParts = 2 * kMaxGrid;   // ranges, and so parts of one pair
+constexpr int kMaxParts = 3 * kMaxGrid;   // ranges, and so parts of one pair, at most
 constexpr int kMaxT = 1024;         // rows of one launch
 constexpr int kWholeBlocks = 4;
 constexpr int kBias = 7;            // P <= 2^kRescale, times 2^7: below 65504
@@ -61,12 +61,12 @@ struct Cfg {
   // A group is WPG consumer warps, SPW slices of 16 keys of a block each, with its own range of
   // blocks and ring of stages: what one group spends on waits and on a pair's end, the other's
   // arithmetic covers
-  static constexpr int GROUPS = NT == 1 ? 2 : 1;
-  static constexpr int WPG = NT == 1 || (FMT == kFmtBF16 && D == 128) ? 4 : 8;
-  static constexpr int SPW = NT == 1 && !(FMT == kFmtBF16 && D == 128) ? 2 : 1;
+  static constexpr bool HEAVY = FMT == kFmtBF16 ? D == 128 : NT == 2 && D == 128;   // one slice fills it
+  static constexpr int GROUPS = FMT == kFmtNVFP4 && D == 128 && NT == 1 ? 3 : 2;
+  static constexpr int WPG = 4, SPW = HEAVY ? 1 : 2;
   static constexpr int NCW = WPG * GROUPS, NCT = WPG * 32;   // consumer warps, threads of a group
-  // four producer warps: K and V of each group, or of the even and odd blocks of the one group
-  static constexpr int STEP = GROUPS == 2 ? 1 : 2;
+  // four producer warps: K and V of each of two groups, or both for each of three (one warp idle)
+  static constexpr bool BOTH = GROUPS == 3;
   static constexpr int THREADS = (NCW + 4) * 32;
   static constexpr int SLICES = WPG * SPW, BK = 16 * SLICES;
   static constexpr int KB = BK * ROWB;
@@ -77,7 +77,7 @@ struct Cfg {
   static constexpr int STAGE = (OQ + QB + 1023) / 1024 * 1024;
   static constexpr int OLD = D + 4;   // row stride of the combine buffer (floats)
   static constexpr int OWB = WPG * HEADS * OLD * 4, MLB = WPG * HEADS * 2 * 4;   // of one group
-  static constexpr int NOW = 4 * STAGE + 2 * GROUPS * (OWB + MLB) <= 216 * 1024 ? 2 : 1;   // buffers
+  static constexpr int NOW = GROUPS < 3 && 4 * STAGE + 2 * GROUPS * (OWB + MLB) <= 216 * 1024 ? 2 : 1;
   static constexpr int FIT = (216 * 1024 - NOW * GROUPS * (OWB + MLB)) / STAGE;
   static constexpr int NSTG = FIT / GROUPS > 4 ? 4 : FIT / GROUPS, NST = NSTG * GROUPS;   // stages of a group
   static constexpr int OW = NST * STAGE;                  // [GROUPS][NOW][WPG][HEADS][OLD]: O partials
@@ -85,11 +85,11 @@ struct Cfg {
   static constexpr int CUM = MLW + GROUPS * NOW * MLB;    // [kMaxT + 1] block prefix
   static constexpr int POS = CUM + (kMaxT + 1) * 4;       // [kMaxT] positions
   static constexpr int MISC = (POS + kMaxT * 4 + 15) / 16 * 16;   // -, abort, -, -; masks
-  static constexpr int BAR = MISC + 16 + 8 * 4;
+  static constexpr int BAR = MISC + 16 + 12 * 4;
   static constexpr int BYTES = BAR + 2 * NST * 8 + 1024;  // + alignment slack
   static constexpr int ITEMS = (HEADS * (D / 4) + NCT - 1) / NCT;   // 4 outputs that a thread finishes
   static_assert(BYTES <= 227 * 1024, "stage ring exceeds shared memory");
-  static_assert(NSTG >= 2 && NST <= 8, "one mask word per stage");
+  static_assert(NSTG >= 2 && NST <= 12, "one mask word per stage");
 };
 
 struct Params {
@@ -184,6 +184,15 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 // Byte o of a region of 128-byte rows under the 128-byte TMA swizzle.
 __device__ __forceinline__ uint32_t sw(uint32_t o) { return o ^ (((o >> 7) & 7u) << 4); }
+
+// Place of element d in a row of the combine buffer. Over a quantised cache lane g writes
+// neighbours of the range [g D/8, (g + 1) D/8): exchanging groups of four spreads the eight lanes
+// over all banks.
+template <int FMT, int D>
+__device__ __forceinline__ int spread(int d) {
+  if (FMT == kFmtBF16) return d;
+  return D == 128 ? d ^ (((d >> 4) & 7) << 2) : d ^ (((d >> 5) & 1) << 2);
+}
 
 // The state of one warp over its keys of a pair.
 template <class C>
@@ -546,40 +555,58 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NST; ++s) {
-      mbar_init(bar_full + 8 * s, 2);   // the producers of K and of V
+      mbar_init(bar_full + 8 * s, C::BOTH ? 1 : 2);   // the producers of K and of V
       mbar_init(bar_empty + 8 * s, C::WPG);
     }
     misc[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  __syncthreads();
   pdl_wait();
   // ---- plan: cum[t] = blocks of one KV head in rows 0 .. t - 1
   const int T = P.T;
-  for (int t = threadIdx.x; t < T; t += C::THREADS) {
-    const Row r = row_of<BK>(P, t);
-    cum[t + 1] = r.nb;
-    rpos[t] = r.p;
-    if (r.bad && blockIdx.x == 0) flag(r.bad);
-  }
-  __syncthreads();
-  if (warp == 0) {
-    const int per = (T + 31) / 32, a = min(T, lane * per), b = min(T, a + per);
-    int sum = 0;
-    for (int t = a; t < b; ++t) sum += cum[t + 1];
-    int run = sum;
+  if (T <= 32) {   // every warp works it out, and writes the same
+    const Row r = row_of<BK>(P, min(lane, T - 1));
+    if (r.bad && lane < T && blockIdx.x == 0 && warp == 0) flag(r.bad);
+    int run = lane < T ? r.nb : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, run, o);
       if (lane >= o) run += u;
     }
-    run -= sum;
-    for (int t = a; t < b; ++t) {
-      run += cum[t + 1];
-      cum[t + 1] = run;
+    if (lane < T) {
+      cum[lane + 1] = run;
+      rpos[lane] = r.p;
     }
     if (lane == 0) cum[0] = 0;
+    __syncwarp();
+  } else {
+    for (int t = threadIdx.x; t < T; t += C::THREADS) {
+      const Row r = row_of<BK>(P, t);
+      cum[t + 1] = r.nb;
+      rpos[t] = r.p;
+      if (r.bad && blockIdx.x == 0) flag(r.bad);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const int per = (T + 31) / 32, a = min(T, lane * per), b = min(T, a + per);
+      int sum = 0;
+      for (int t = a; t < b; ++t) sum += cum[t + 1];
+      int run = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += u;
+      }
+      run -= sum;
+      for (int t = a; t < b; ++t) {
+        run += cum[t + 1];
+        cum[t + 1] = run;
+      }
+      if (lane == 0) cum[0] = 0;
+    }
+    __syncthreads();
   }
-  __syncthreads();
   const int total = cum[T] * P.n_kv;
   // the warp's group and its range of the flat blocks
   const int grp = warp < C::NCW ? warp / C::WPG : (warp - C::NCW) % C::GROUPS;
@@ -609,8 +636,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
 
   if (warp >= C::NCW) {
     // ---------------- producers
-    const int par = C::GROUPS == 1 ? (warp - C::NCW) & 1 : 0;   // first of the warp's blocks
-    const bool vals = warp - C::NCW >= 2;
+    const bool keys = C::BOTH || warp - C::NCW < 2, vals = C::BOTH || warp - C::NCW >= 2;
+    if (C::BOTH && warp - C::NCW == 3) f_hi = f_lo;
     const int pse = min(P.c.page_size, BK), npg = BK / pse;   // keys of a page in a block, pages
     struct At {
       int t, hk, j, nb, blk0, lo, p, s;
@@ -623,23 +650,14 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
       a.p = r.p;
       a.s = r.s;
     };
-    auto advance = [&](At& a, int by) {   // stays on the last pair at the end
-      a.j += by;
-      while (a.j >= a.nb) {
-        int hk = a.hk + 1, t = a.t;
-        if (hk == P.n_kv) {
-          hk = 0;
-          do ++t;
-          while (t < T && cum[t + 1] == cum[t]);
-          if (t == T) return;
-        }
-        a.j -= a.nb;
-        a.hk = hk;
-        if (t != a.t) {
-          a.t = t;
-          load_row(a);
-        }
-      }
+    auto advance = [&](At& a) {   // there is a next block
+      if (++a.j < a.nb) return;
+      a.j = 0;
+      if (++a.hk < P.n_kv) return;
+      a.hk = 0;
+      do ++a.t;
+      while (cum[a.t + 1] == cum[a.t]);
+      load_row(a);
     };
     // lane i's page of the block: its number, or -2 where the block has no key in it
     auto fetch = [&](const At& a) -> int {
@@ -650,20 +668,19 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
     };
     At at{t_lo, 0, 0, 1, 0, 1, 0, 0};
     int id = -2;
-    if (f_lo + par < f_hi) {
+    if (f_lo < f_hi) {
       load_row(at);
       const int r = f_lo - cum[at.t] * P.n_kv;
       at.hk = r / at.nb;
       at.j = r - at.hk * at.nb;
-      advance(at, par);
       id = fetch(at);
     }
-    int i = par;
-    for (int f = f_lo + par; f < f_hi; f += C::STEP, i += C::STEP) {
+    int i = 0;
+    for (int f = f_lo; f < f_hi; ++f, ++i) {
       const At a = at;
       const int page = id;
-      if (f + C::STEP < f_hi) {
-        advance(at, C::STEP);
+      if (f + 1 < f_hi) {
+        advance(at);
         id = fetch(at);   // the pages of the next block, while this one waits
       }
       const int st = grp * C::NSTG + i % C::NSTG;
@@ -681,12 +698,13 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
       const int off = ((a.blk0 + a.j) * BK + lane * pse) & (P.c.page_size - 1);   // first key in the page
       const int y = C::PLANES == 2 ? off : off * C::ROWB / 128;
       const bool part = pse < P.c.page_size;   // part of a page: K's and V's scales lie apart
-      if (!vals) {
+      if (keys) {
         const bool with_q = f == f_lo || a.j == 0;   // a pair's first block here
         const unsigned slices = __ballot_sync(0xffffffffu, lane < C::SLICES && ((okm >> (lane * 16 / pse)) & 1u));
         if (lane == 0) {
           masks[st] = slices;
-          mbar_expect_tx(fb, __popc(okm) * pse * (C::ROWB + (FMT != kFmtBF16 ? 2 : 0)) + (with_q ? P.G * D * 2 : 0));
+          const int row = C::BOTH ? 2 * C::ROWB + 2 + 2 * (D / 16) : C::ROWB + (FMT != kFmtBF16 ? 2 : 0);
+          mbar_expect_tx(fb, __popc(okm) * pse * row + (with_q ? P.G * D * 2 : 0));
         }
         __syncwarp();
         if (ok) {
@@ -702,8 +720,9 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
         }
         if (with_q && lane == 31)
           bulk_load(base + C::OQ, P.q + (size_t(a.t) * P.n_q + a.hk * P.G) * D, P.G * D * 2, fb);
-      } else {
-        if (lane == 0)
+      }
+      if (vals) {
+        if (lane == 0 && !C::BOTH)
           mbar_expect_tx(fb, __popc(okm) * pse * (C::ROWB + (FMT == kFmtNVFP4 ? 2 * (D / 16) : 0)));
         __syncwarp();
         if (ok) {
@@ -723,7 +742,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
     // normally done at once, with the last blocks: after an expired wait elsewhere, let the copies
     // in flight land before the CTA's shared memory is released
     if (lane == 0)
-      for (int k = i - C::STEP; k >= 0 && k >= i - C::NSTG; k -= C::STEP)
+      for (int k = i - 1; k >= 0 && k >= i - C::NSTG; --k)
         mbar_wait(bar_full + 8 * (grp * C::NSTG + k % C::NSTG), (k / C::NSTG) & 1);
   } else {
     // ---------------- consumers
@@ -840,7 +859,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
       float* Ow = reinterpret_cast<float*>(sm + C::OW + (grp * C::NOW + buf) * C::OWB);
       float2* MLw = reinterpret_cast<float2*>(sm + C::MLW + (grp * C::NOW + buf) * C::MLB);
       buf = C::NOW - 1 - buf;
-      const float unit = FMT == kFmtBF16 ? 1.f : ldexpf(1.f, S.E - 127 - kBias);
+      // 2^(E - 127 - kBias)
+      const float unit = __uint_as_float(S.E > kBias ? unsigned(S.E - kBias) << 23 : 0x00800000u >> (kBias + 1 - S.E));
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -852,12 +872,17 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
         float* ow = Ow + h0 * C::OLD;
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt) {
-          const int da = FMT == kFmtBF16 ? 16 * mt + g : (D / 8) * g + 2 * mt;
-          const int db = FMT == kFmtBF16 ? da + 8 : da + 1;
-          ow[da] = S.acc[n][mt][0] * unit;
-          ow[C::OLD + da] = S.acc[n][mt][1] * unit;
-          ow[db] = S.acc[n][mt][2] * unit;
-          ow[C::OLD + db] = S.acc[n][mt][3] * unit;
+          const float(&a)[4] = S.acc[n][mt];
+          if constexpr (FMT == kFmtBF16) {   // rows g, g + 8 of m tile mt
+            ow[16 * mt + g] = a[0];
+            ow[C::OLD + 16 * mt + g] = a[1];
+            ow[16 * mt + g + 8] = a[2];
+            ow[C::OLD + 16 * mt + g + 8] = a[3];
+          } else {   // neighbours
+            const int d = spread<FMT, D>(D / 8 * g + 2 * mt);
+            *reinterpret_cast<float2*>(ow + d) = make_float2(a[0] * unit, a[2] * unit);
+            *reinterpret_cast<float2*>(ow + C::OLD + d) = make_float2(a[1] * unit, a[3] * unit);
+          }
         }
         if (g == 0) {
           MLw[h0] = make_float2(S.m[n][0], S.l[n][0]);
@@ -881,7 +906,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
           const float2 ml = MLw[ww * C::HEADS + h];
           const float fw = ex2(ml.x - M);
           L += fw * ml.y;
-          const float4 v = *reinterpret_cast<const float4*>(Ow + (ww * C::HEADS + h) * C::OLD + d);
+          const float4 v = *reinterpret_cast<const float4*>(Ow + (ww * C::HEADS + h) * C::OLD + spread<FMT, D>(d));
           O.x += fw * v.x;
           O.y += fw * v.y;
           O.z += fw * v.z;
@@ -926,47 +951,60 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
 }
 
 // Join of the pair that begins in range blockIdx.x and runs on past it, one query head
-// (blockIdx.y) per CTA, one thread per output element.
-template <int D, int HEADS>
-__global__ void __launch_bounds__(D) paged_join_kernel(const Params P) {
+// (blockIdx.y) per CTA: WAYS threads per output element share the parts.
+template <int D, int HEADS, int WAYS>
+__global__ void __launch_bounds__(D * WAYS) paged_join_kernel(const Params P) {
   pdl_trigger();
-  __shared__ float wsh[kMaxParts], lsh[kMaxParts];
+  __shared__ float wsh[kMaxParts], lsh[kMaxParts], acc[WAYS][D], sum[WAYS];
   pdl_wait();
   const int4 jn = P.join[blockIdx.x];
-  const int n = jn.z, h = blockIdx.y;
+  const int n = jn.z, h = blockIdx.y, d = threadIdx.x % D, way = threadIdx.x / D;
   if (n == 0) return;
   // the first part's slot is jn.w; in the ranges after it the pair is the first
   auto slot = [&](int s) { return (size_t(2 * (blockIdx.x + s)) + (s == 0 ? jn.w : 0)) * HEADS + h; };
-  for (int s = threadIdx.x; s < n; s += D) {
+  for (int s = threadIdx.x; s < n; s += D * WAYS) {
     const float2 v = __ldcg(reinterpret_cast<const float2*>(P.part_ml + slot(s) * 2));
     wsh[s] = v.x;
     lsh[s] = v.y;
   }
+  // the parts' values do not wait for their weights
+  constexpr int U = 8;
+  float v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    v[u] = way + u * WAYS < n ? __ldcg(P.part_acc + slot(way + u * WAYS) * D + d) : 0.f;
+  const int hq = jn.y * P.G + h;
+  const size_t oi = (size_t(jn.x) * P.n_q + hq) * D + d;
+  float gate = 0.f;
+  if (way == 0 && P.g != nullptr) gate = bf2f(P.g[oi]) + bf2f(P.gate_bias[hq]);
   __syncthreads();
   float M = kLowest;
   for (int s = 0; s < n; ++s) M = fmaxf(M, wsh[s]);
   float L = 0.f, O = 0.f;
-  int s = 0;
-  for (; s + 8 <= n; s += 8) {
-    float v[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = __ldcg(P.part_acc + slot(s + u) * D + threadIdx.x);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const float fw = ex2(wsh[s + u] - M);
-      O += fw * v[u];
-      L += fw * lsh[s + u];
-    }
-  }
-  for (; s < n; ++s) {
+  for (int u = 0; u < U; ++u) {
+    const int s = way + u * WAYS;
+    if (s >= n) break;
     const float fw = ex2(wsh[s] - M);
-    O += fw * __ldcg(P.part_acc + slot(s) * D + threadIdx.x);
+    O += fw * v[u];
     L += fw * lsh[s];
   }
-  const int hq = jn.y * P.G + h;
-  const size_t oi = (size_t(jn.x) * P.n_q + hq) * D + threadIdx.x;
+  for (int s = way + U * WAYS; s < n; s += WAYS) {
+    const float fw = ex2(wsh[s] - M);
+    O += fw * __ldcg(P.part_acc + slot(s) * D + d);
+    L += fw * lsh[s];
+  }
+  acc[way][d] = O;
+  if (d == 0) sum[way] = L;
+  __syncthreads();
+  if (way != 0) return;
+#pragma unroll
+  for (int u = 1; u < WAYS; ++u) {
+    O += acc[u][d];
+    L += sum[u];
+  }
   float o = L == 0.f ? 0.f : O / L;
-  if (P.g != nullptr) o *= sigmoidf_(bf2f(P.g[oi]) + bf2f(P.gate_bias[hq]));
+  if (P.g != nullptr) o *= sigmoidf_(gate);
   P.og[oi] = f2bf(o);
 }
 
@@ -979,6 +1017,9 @@ int block_keys(int fmt, int D, int nt) {
   return fmt == kFmtBF16 ? block_keys_of<kFmtBF16>(D, nt)
          : fmt == kFmtFP8 ? block_keys_of<kFmtFP8>(D, nt) : block_keys_of<kFmtNVFP4>(D, nt);
 }
+
+// Rows of partial results: two pairs a range, 8 nt heads each (three ranges a CTA with nt = 1 only).
+size_t part_rows(int nt) { return size_t(nt == 1 ? 3 : 2) * kMaxGrid * 2 * 8 * nt; }
 
 int max_grid() {
   const int sms = num_sms_cached();
@@ -1010,7 +1051,10 @@ cudaError_t launch(Params p, int64_t pairs, int64_t blocks, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::BYTES, st, mk, mv, p);
   if (e != cudaSuccess || p.whole) return e;
-  return launch_pdl(paged_join_kernel<D, C::HEADS>, dim3(p.ranges, p.G), dim3(D), 0, st, p);
+  // many parts to a pair: more threads fetch them at once (one pair's 38 parts: 4.4 -> 3 us)
+  if (p.ranges >= 4 * pairs)
+    return launch_pdl(paged_join_kernel<D, C::HEADS, 4>, dim3(p.ranges, p.G), dim3(4 * D), 0, st, p);
+  return launch_pdl(paged_join_kernel<D, C::HEADS, 1>, dim3(p.ranges, p.G), dim3(D), 0, st, p);
 }
 
 template <int FMT>
@@ -1030,7 +1074,7 @@ extern "C" size_t beam_paged_workspace_bytes(const beam_layer_cfg* cfg, int T, i
   using namespace beam::paged;
   (void)max_pos;
   if (cfg == nullptr || T <= 0 || cfg->n_q <= 0 || cfg->head_dim <= 0) return 256;
-  const size_t parts = size_t(kMaxParts) * 2 * 8;   // or half the ranges, of 16 heads
+  const size_t parts = part_rows(1) > part_rows(2) ? part_rows(1) : part_rows(2);
   return align_up(parts * cfg->head_dim * 4, 256) + align_up(parts * 2 * 4, 256) +
          align_up(kMaxParts * sizeof(int4), 256) +
          align_up(size_t(T) * cfg->n_q * cfg->head_dim * 2, 256);
@@ -1068,7 +1112,7 @@ extern "C" beam_status beam_paged_attn(const beam_layer_cfg* cfg, const beam_bf1
   if (nb * slice * cfg->n_kv > INT32_MAX) return BEAM_ERR_UNSUPPORTED;   // flat block numbers
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   Carver cv{static_cast<char*>(ws), ws_bytes};
-  const size_t parts = size_t(kMaxParts) * 2 * 8;
+  const size_t parts = part_rows(nt);
   Params p{};
   p.part_acc = cv.take<float>(parts * D);
   p.part_ml = cv.take<float>(parts * 2);

@@ -393,7 +393,7 @@ beam_status beam_paged_attn(const beam_layer_cfg* cfg, const beam_bf16* q, const
                             const beam_bf16* w_o, beam_bf16* out, void* ws, size_t ws_bytes,
                             beam_stream_t stream);
 
-/* Workspace bytes of beam_paged_attn: at most 4 MiB, and T * n_q * head_dim * 2 more for the
+/* Workspace bytes of beam_paged_attn: at most 8 MiB, and T * n_q * head_dim * 2 more for the
  * input of o_proj. */
 size_t beam_paged_workspace_bytes(const beam_layer_cfg* cfg, int T, int max_pos);
 

@@ -178,8 +178,8 @@ def test_attn_argument_checks(lib):  # noqa: F811
     # 1024 rows over 8 heads of 2^30 keys: flat block numbers would pass 32 bits
     big = handle(table_stride=1 << 26, page_size=16)
     assert attn(h=big, T=1024, max_pos=1 << 30) == 2
-    assert B.paged_workspace_bytes(cfg, 1, 100) <= (4 << 20) + 48 * 128 * 2
-    assert B.paged_workspace_bytes(cfg, 300, 100) <= (4 << 20) + 300 * 48 * 128 * 2
+    assert B.paged_workspace_bytes(cfg, 1, 100) <= (8 << 20) + 48 * 128 * 2
+    assert B.paged_workspace_bytes(cfg, 300, 100) <= (8 << 20) + 300 * 48 * 128 * 2
 
 
 def test_paged_bytes(lib):  # noqa: F811
