@@ -50,7 +50,7 @@ constexpr float kRescale = 8.f;     // log2 units by which the running max may l
 constexpr int kMaxGrid = 152;       // CTAs at most
 constexpr int kMaxParts = 3 * kMaxGrid;   // ranges, and so parts of one pair, at most
 constexpr int kMaxT = 1024;         // rows of one launch
-constexpr int kWholeBlocks = 4;
+constexpr int kWholeBlocks = 8;
 constexpr int kBias = 7;            // P <= 2^kRescale, times 2^7: below 65504
 
 template <int FMT, int D_, int NT_>
@@ -85,7 +85,8 @@ struct Cfg {
   static constexpr int CUM = MLW + GROUPS * NOW * MLB;    // [kMaxT + 1] block prefix
   static constexpr int POS = CUM + (kMaxT + 1) * 4;       // [kMaxT] positions
   static constexpr int MISC = (POS + kMaxT * 4 + 15) / 16 * 16;   // -, abort, -, -; masks
-  static constexpr int BAR = MISC + 16 + 12 * 4;
+  static constexpr int JOIN = MISC + 16 + 12 * 4;         // [GROUPS] pairs that begin in a group's range
+  static constexpr int BAR = JOIN + 3 * 16;
   static constexpr int BYTES = BAR + 2 * NST * 8 + 1024;  // + alignment slack
   static constexpr int ITEMS = (HEADS * (D / 4) + NCT - 1) / NCT;   // 4 outputs that a thread finishes
   static_assert(BYTES <= 227 * 1024, "stage ring exceeds shared memory");
@@ -170,6 +171,17 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Loads that stay where they are written, ahead of their use.
+__device__ __forceinline__ uint2 ld_ahead(const uint16_t* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint16_t ld_ahead16(const uint16_t* p) {
+  uint16_t v;
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
 template <int NTHREADS>
 __device__ __forceinline__ void consumer_bar(int group) {
   asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(NTHREADS) : "memory");
@@ -192,6 +204,20 @@ template <int FMT, int D>
 __device__ __forceinline__ int spread(int d) {
   if (FMT == kFmtBF16) return d;
   return D == 128 ? d ^ (((d >> 4) & 7) << 2) : d ^ (((d >> 5) & 1) << 2);
+}
+
+// Four neighbouring outputs: normalised, gated, rounded once.
+__device__ __forceinline__ void finish4(bool gated, float4 O, float L, uint2 g, float bias,
+                                        uint16_t* out) {
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  float o[4] = {O.x * inv, O.y * inv, O.z * inv, O.w * inv};
+  if (gated) {
+    o[0] *= sigmoidf_(bf_lo(g.x) + bias);
+    o[1] *= sigmoidf_(bf_hi(g.x) + bias);
+    o[2] *= sigmoidf_(bf_lo(g.y) + bias);
+    o[3] *= sigmoidf_(bf_hi(g.y) + bias);
+  }
+  *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
 }
 
 // The state of one warp over its keys of a pair.
@@ -537,6 +563,13 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
   }
 }
 
+// Row of the partial results of part s of a joined pair and its query head h: the first part's slot
+// is jn.w, and in the ranges after it the pair is the first.
+template <int HEADS>
+__device__ __forceinline__ size_t part_row(const int4& jn, int range, int s, int h) {
+  return (size_t(2 * (range + s)) + (s == 0 ? jn.w : 0)) * HEADS + h;
+}
+
 template <int FMT, int D, int NT>
 __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kernel(
     const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -550,6 +583,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
   const uint32_t bar_full = sbase + C::BAR, bar_empty = bar_full + 8 * C::NST;
   volatile int* misc = reinterpret_cast<volatile int*>(sm + C::MISC);   // -, abort, -, -
   volatile unsigned* masks = reinterpret_cast<volatile unsigned*>(sm + C::MISC + 16);
+  int4* joins = reinterpret_cast<int4*>(sm + C::JOIN);
   int* cum = reinterpret_cast<int*>(sm + C::CUM);
   int* rpos = reinterpret_cast<int*>(sm + C::POS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -608,11 +642,6 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
     __syncthreads();
   }
   const int total = cum[T] * P.n_kv;
-  // the warp's group and its range of the flat blocks
-  const int grp = warp < C::NCW ? warp / C::WPG : (warp - C::NCW) % C::GROUPS;
-  const int range = grp * int(gridDim.x) + int(blockIdx.x);
-  const int R = max(1, (total + P.ranges - 1) / P.ranges);
-  int f_lo = int(min(int64_t(total), int64_t(range) * R)), f_hi = min(total, f_lo + R);
   // row of flat block f: the last t with cum[t] * n_kv <= f
   auto row_at = [&](int f) {
     int a = 0, b = T;   // cum[a] * n_kv <= f < cum[b] * n_kv
@@ -623,14 +652,27 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
     }
     return a;
   };
-  if (P.whole) {   // move both ends up to the next pair's first block
-    auto up = [&](int f) {
-      if (f >= total) return total;
-      const int t = row_at(f), nb = cum[t + 1] - cum[t], r = (f - cum[t] * P.n_kv) % nb;
+  // the warp's group and its range of the flat blocks
+  const int grp = warp < C::NCW ? warp / C::WPG : (warp - C::NCW) % C::GROUPS;
+  const int range = P.whole ? int(blockIdx.x) * C::GROUPS + grp : grp * int(gridDim.x) + int(blockIdx.x);
+  int f0 = 0, R, f_lo, f_hi;   // ranges of R blocks from f0
+  if (P.whole) {
+    // the CTA's equal share, both ends moved up to the next pair's first block, is cut for the groups
+    const int share = max(1, (total + int(gridDim.x) - 1) / int(gridDim.x));
+    auto up = [&](int64_t x) {
+      if (x >= total) return total;
+      const int f = int(x), t = row_at(f), nb = cum[t + 1] - cum[t], r = (f - cum[t] * P.n_kv) % nb;
       return r ? f + nb - r : f;
     };
-    f_lo = up(f_lo);
-    f_hi = up(f_hi);
+    f0 = up(int64_t(blockIdx.x) * share);
+    const int end = up(int64_t(blockIdx.x + 1) * share);
+    R = max(1, (end - f0 + C::GROUPS - 1) / C::GROUPS);
+    f_lo = min(end, f0 + grp * R);
+    f_hi = min(end, f_lo + R);
+  } else {
+    R = max(1, (total + P.ranges - 1) / P.ranges);
+    f_lo = int(min(int64_t(total), int64_t(range) * R));
+    f_hi = min(total, f_lo + R);
   }
   const int t_lo = f_lo < f_hi ? row_at(f_lo) : 0;
 
@@ -775,8 +817,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
         for (int it = 0; it < C::ITEMS; ++it) {
           const int idx = ct + it * NCT;
           if (idx < G * (D / 4)) {
-            gv[it] = *reinterpret_cast<const uint2*>(P.g + o_pair + 4 * idx);
-            gb[it] = bf2f(P.gate_bias[hk * G + idx / (D / 4)]);
+            gv[it] = ld_ahead(P.g + o_pair + 4 * idx);
+            gb[it] = bf2f(ld_ahead16(P.gate_bias + hk * G + idx / (D / 4)));
           }
         }
       }
@@ -917,18 +959,10 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
           if (d == 0) *reinterpret_cast<float2*>(P.part_ml + (pb + h) * 2) = make_float2(M, L);
           continue;
         }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        float o[4] = {O.x * inv, O.y * inv, O.z * inv, O.w * inv};
-        if (P.g != nullptr) {
-          o[0] *= sigmoidf_(bf_lo(gv[it].x) + gb[it]);
-          o[1] *= sigmoidf_(bf_hi(gv[it].x) + gb[it]);
-          o[2] *= sigmoidf_(bf_lo(gv[it].y) + gb[it]);
-          o[3] *= sigmoidf_(bf_hi(gv[it].y) + gb[it]);
-        }
-        *reinterpret_cast<uint2*>(P.og + o_pair + 4 * idx) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+        finish4(P.g != nullptr, O, L, gv[it], gb[it], P.og + o_pair + 4 * idx);
       }
       if (j0 == 0 && j1 < nb)   // the pair begins here and runs on
-        join = make_int4(t, hk, (f_pair + nb - 1) / R - range + 1, slot);
+        join = make_int4(t, hk, (f_pair + nb - 1 - f0) / R - (f_lo - f0) / R + 1, slot);
       // ---- next pair
       f = f_pair + j1;
       j0 = 0;
@@ -938,7 +972,10 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
         while (t < T && cum[t + 1] == cum[t]);
       }
     }
-    if (ct == 0 && range < P.ranges) P.join[range] = join;
+    if (ct == 0) {
+      if (P.whole) joins[grp] = join;
+      else if (range < P.ranges) P.join[range] = join;
+    }
     // ---- rows that attend to nothing
     for (int r = blockIdx.x; r < T; r += gridDim.x)
       if (cum[r + 1] == cum[r])
@@ -947,6 +984,47 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
   }
   __syncthreads();
   pdl_trigger();   // not earlier: the join and what follows would run beside the key stream
+  if (P.whole) {
+    // pairs that the CTA's groups share, joined here: at most GROUPS parts each
+    for (int x = threadIdx.x; x < C::GROUPS * P.G * (D / 4); x += C::THREADS) {
+      const int gr = x / (P.G * (D / 4)), y = x - gr * P.G * (D / 4), h = y / (D / 4), d = 4 * (y - h * (D / 4));
+      const int4 jn = joins[gr];
+      if (jn.z == 0) continue;
+      const int first = int(blockIdx.x) * C::GROUPS + gr;
+      float2 ml[C::GROUPS];
+      float4 v[C::GROUPS];
+      float M = kLowest, L = 0.f;
+#pragma unroll
+      for (int s = 0; s < C::GROUPS; ++s) {
+        ml[s] = make_float2(kLowest, 0.f);
+        v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s >= jn.z) continue;
+        const size_t r = part_row<C::HEADS>(jn, first, s, h);
+        ml[s] = __ldcg(reinterpret_cast<const float2*>(P.part_ml + 2 * r));
+        v[s] = __ldcg(reinterpret_cast<const float4*>(P.part_acc + r * D + d));
+        M = fmaxf(M, ml[s].x);
+      }
+      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int s = 0; s < C::GROUPS; ++s) {
+        const float fw = ex2(ml[s].x - M);
+        L += fw * ml[s].y;
+        O.x += fw * v[s].x;
+        O.y += fw * v[s].y;
+        O.z += fw * v[s].z;
+        O.w += fw * v[s].w;
+      }
+      const int hq = jn.y * P.G + h;
+      const size_t oi = (size_t(jn.x) * P.n_q + hq) * D + d;
+      uint2 gv = make_uint2(0, 0);
+      float gb = 0.f;
+      if (P.g != nullptr) {
+        gv = *reinterpret_cast<const uint2*>(P.g + oi);
+        gb = bf2f(P.gate_bias[hq]);
+      }
+      finish4(P.g != nullptr, O, L, gv, gb, P.og + oi);
+    }
+  }
   if (threadIdx.x == 0 && misc[1]) flag(BEAM_DEV_TIMEOUT);
 }
 
@@ -960,8 +1038,7 @@ __global__ void __launch_bounds__(D * WAYS) paged_join_kernel(const Params P) {
   const int4 jn = P.join[blockIdx.x];
   const int n = jn.z, h = blockIdx.y, d = threadIdx.x % D, way = threadIdx.x / D;
   if (n == 0) return;
-  // the first part's slot is jn.w; in the ranges after it the pair is the first
-  auto slot = [&](int s) { return (size_t(2 * (blockIdx.x + s)) + (s == 0 ? jn.w : 0)) * HEADS + h; };
+  auto slot = [&](int s) { return part_row<HEADS>(jn, blockIdx.x, s, h); };
   for (int s = threadIdx.x; s < n; s += D * WAYS) {
     const float2 v = __ldcg(reinterpret_cast<const float2*>(P.part_ml + slot(s) * 2));
     wsh[s] = v.x;
@@ -1030,11 +1107,11 @@ int max_grid() {
 template <int FMT, int D, int NT>
 cudaError_t launch(Params p, int64_t pairs, int64_t blocks, cudaStream_t st) {
   using C = Cfg<FMT, D, NT>;
-  // a range is not smaller than a block, nor, where pairs are not split, than a pair
-  const int64_t units = p.whole ? pairs : blocks;
-  const int sms = max_grid();
-  p.ranges = int(units < C::GROUPS * sms ? units : C::GROUPS * sms);
-  const int grid = p.ranges < sms ? p.ranges : sms;
+  // no range smaller than a block, no CTA with less than a pair where CTAs do not share pairs
+  const int sms = max_grid(), most = C::GROUPS * sms;
+  p.ranges = int(blocks < most ? blocks : most);
+  const int units = p.whole ? int(pairs < sms ? pairs : sms) : p.ranges;
+  const int grid = units < sms ? units : sms;
   const beam_paged_kv& c = p.c;
   CUtensorMap mk, mv;
   const int rows = C::PLANES == 2 ? c.page_size : c.page_size * C::ROWB / 128;
