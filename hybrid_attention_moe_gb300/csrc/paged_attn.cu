@@ -1028,61 +1028,90 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
   if (threadIdx.x == 0 && misc[1]) flag(BEAM_DEV_TIMEOUT);
 }
 
-// Join of the pair that begins in range blockIdx.x and runs on past it, one query head
-// (blockIdx.y) per CTA: WAYS threads per output element share the parts.
+// Join of the pair that begins in range blockIdx.x and runs on past it: four neighbouring outputs
+// a thread, WAYS threads to share their parts; the parts' weights are found as they come.
+constexpr int kJoinThreads = 256;
 template <int D, int HEADS, int WAYS>
-__global__ void __launch_bounds__(D * WAYS) paged_join_kernel(const Params P) {
+__global__ void __launch_bounds__(kJoinThreads * WAYS) paged_join_kernel(const Params P) {
   pdl_trigger();
-  __shared__ float wsh[kMaxParts], lsh[kMaxParts], acc[WAYS][D], sum[WAYS];
+  __shared__ float4 acc[WAYS][kJoinThreads];
+  __shared__ float2 part[WAYS][kJoinThreads];
   pdl_wait();
   const int4 jn = P.join[blockIdx.x];
-  const int n = jn.z, h = blockIdx.y, d = threadIdx.x % D, way = threadIdx.x / D;
+  const int n = jn.z, lane = threadIdx.x % kJoinThreads, way = threadIdx.x / kJoinThreads;
   if (n == 0) return;
-  auto slot = [&](int s) { return part_row<HEADS>(jn, blockIdx.x, s, h); };
-  for (int s = threadIdx.x; s < n; s += D * WAYS) {
-    const float2 v = __ldcg(reinterpret_cast<const float2*>(P.part_ml + slot(s) * 2));
-    wsh[s] = v.x;
-    lsh[s] = v.y;
-  }
-  // the parts' values do not wait for their weights
-  constexpr int U = 8;
-  float v[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    v[u] = way + u * WAYS < n ? __ldcg(P.part_acc + slot(way + u * WAYS) * D + d) : 0.f;
-  const int hq = jn.y * P.G + h;
-  const size_t oi = (size_t(jn.x) * P.n_q + hq) * D + d;
-  float gate = 0.f;
-  if (way == 0 && P.g != nullptr) gate = bf2f(P.g[oi]) + bf2f(P.gate_bias[hq]);
-  __syncthreads();
-  float M = kLowest;
-  for (int s = 0; s < n; ++s) M = fmaxf(M, wsh[s]);
-  float L = 0.f, O = 0.f;
+  for (int x0 = 0; x0 < HEADS * (D / 4); x0 += kJoinThreads) {
+    const int x = x0 + lane, h = x / (D / 4), d = 4 * (x - h * (D / 4));
+    const bool live = h < P.G;
+    const int hq = jn.y * P.G + h;
+    const size_t oi = (size_t(jn.x) * P.n_q + hq) * D + d;
+    uint2 gv = make_uint2(0, 0);
+    float gb = 0.f, M = kLowest, L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live && way == 0 && P.g != nullptr) {
+      gv = ld_ahead(P.g + oi);
+      gb = bf2f(ld_ahead16(P.gate_bias + hq));
+    }
+    constexpr int U = WAYS == 1 ? 8 : 5;   // parts in flight
+    for (int s0 = way; s0 < n && live; s0 += U * WAYS) {
+      float2 ml[U];
+      float4 v[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int s = way + u * WAYS;
-    if (s >= n) break;
-    const float fw = ex2(wsh[s] - M);
-    O += fw * v[u];
-    L += fw * lsh[s];
-  }
-  for (int s = way + U * WAYS; s < n; s += WAYS) {
-    const float fw = ex2(wsh[s] - M);
-    O += fw * __ldcg(P.part_acc + slot(s) * D + d);
-    L += fw * lsh[s];
-  }
-  acc[way][d] = O;
-  if (d == 0) sum[way] = L;
-  __syncthreads();
-  if (way != 0) return;
+      for (int u = 0; u < U; ++u) {
+        const int s = s0 + u * WAYS;
+        ml[u] = make_float2(kLowest, 0.f);
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s >= n) continue;
+        const size_t r = part_row<HEADS>(jn, blockIdx.x, s, h);
+        ml[u] = __ldcg(reinterpret_cast<const float2*>(P.part_ml + 2 * r));
+        v[u] = __ldcg(reinterpret_cast<const float4*>(P.part_acc + r * D + d));
+      }
+      float top = M;
 #pragma unroll
-  for (int u = 1; u < WAYS; ++u) {
-    O += acc[u][d];
-    L += sum[u];
+      for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
+      const float f = ex2(M - top);
+      M = top;
+      L *= f;
+      O.x *= f;
+      O.y *= f;
+      O.z *= f;
+      O.w *= f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float fw = ex2(ml[u].x - M);
+        L += fw * ml[u].y;
+        O.x += fw * v[u].x;
+        O.y += fw * v[u].y;
+        O.z += fw * v[u].z;
+        O.w += fw * v[u].w;
+      }
+    }
+    if (WAYS > 1) {
+      acc[way][lane] = O;
+      part[way][lane] = make_float2(M, L);
+      __syncthreads();
+      if (way == 0) {
+        float top = M;
+#pragma unroll
+        for (int u = 1; u < WAYS; ++u) top = fmaxf(top, part[u][lane].x);
+        L = 0.f;
+        O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < WAYS; ++u) {
+          const float fw = ex2(part[u][lane].x - top);
+          const float4 v = acc[u][lane];
+          L += fw * part[u][lane].y;
+          O.x += fw * v.x;
+          O.y += fw * v.y;
+          O.z += fw * v.z;
+          O.w += fw * v.w;
+        }
+      }
+      __syncthreads();
+    }
+    if (live && way == 0) finish4(P.g != nullptr, O, L, gv, gb, P.og + oi);
   }
-  float o = L == 0.f ? 0.f : O / L;
-  if (P.g != nullptr) o *= sigmoidf_(gate);
-  P.og[oi] = f2bf(o);
 }
 
 template <int FMT>
@@ -1128,10 +1157,10 @@ cudaError_t launch(Params p, int64_t pairs, int64_t blocks, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::BYTES, st, mk, mv, p);
   if (e != cudaSuccess || p.whole) return e;
-  // many parts to a pair: more threads fetch them at once (one pair's 38 parts: 4.4 -> 3 us)
-  if (p.ranges >= 4 * pairs)
-    return launch_pdl(paged_join_kernel<D, C::HEADS, 4>, dim3(p.ranges, p.G), dim3(4 * D), 0, st, p);
-  return launch_pdl(paged_join_kernel<D, C::HEADS, 1>, dim3(p.ranges, p.G), dim3(D), 0, st, p);
+  // many parts to a pair: more threads fetch them at once
+  if (p.ranges >= 8 * pairs)
+    return launch_pdl(paged_join_kernel<D, C::HEADS, 4>, dim3(p.ranges), dim3(4 * kJoinThreads), 0, st, p);
+  return launch_pdl(paged_join_kernel<D, C::HEADS, 1>, dim3(p.ranges), dim3(kJoinThreads), 0, st, p);
 }
 
 template <int FMT>
