@@ -8,6 +8,8 @@ being term 1 ("MoE and residual stream" section); layers 0-2 use the dense SwiGL
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import beam as B
@@ -27,8 +29,16 @@ class BeamStack:
              an MoE layer may hold "nvfp4" (synth.expert_weights_nvfp4) or "fp8"
              (synth.expert_weights_fp8) instead of w_gate_up/w_down, and then runs
              beam_moe_nvfp4 or beam_moe_fp8).
-    caches : list of B.KVCache, one per layer (window = W on sliding-window layers, 0 on NoPE).
+    caches : list of B.KVCache, one per layer (window = W on sliding-window layers, 0 on NoPE),
+             or of B.PagedKVCache. A paged layer projects into a staging row per token, writes
+             it into the pages (beam_paged_kv_write), and attends with beam_paged_attn up to
+             PAGED_MAX_Q tokens per sequence; with more it reads the sequences' context back
+             into a contiguous BF16 cache (beam_paged_kv_read) that beam_attn's prefill takes.
     """
+
+    # A call's tokens of one sequence each read their keys in beam_paged_attn; the way through a
+    # contiguous copy writes and reads them in BF16 once more, whatever the tokens' number.
+    PAGED_MAX_Q = 4
 
     def __init__(self, shape, weights, caches, first_layer=0, n_layers=None, device="cuda"):
         """weights[i] / caches[i] belong to global layer first_layer + i of an n_layers-deep
@@ -48,6 +58,69 @@ class BeamStack:
         self.ws = B.Workspace(device)
         self.device = device
         self._bufs = {}
+        self._stage = {}
+        self._copies = {}
+        self.paged = any(isinstance(c, B.PagedKVCache) for c in caches)
+
+    def stage(self, T):
+        """A row per token for the projection's K and V: a ring of one slot per "sequence"."""
+        s = self._stage.get(T)
+        if s is None:
+            dims = (T, self.shape.n_kv, 1, self.shape.head_dim)
+            k, v = (torch.empty(dims, dtype=torch.bfloat16, device=self.device) for _ in "kv")
+            rows = torch.arange(T, dtype=torch.int32, device=self.device)
+            s = (B.KVCache(k, v, window=1), rows, k.view(T, *dims[1::2]), v.view(T, *dims[1::2]))
+            self._stage = {T: s}
+        return s
+
+    def context(self, kc, seq_id, pos, max_pos, max_q):
+        """What a paged layer's prefill reads: (contiguous cache, its sequences, first, last,
+        longest), one row per sequence of the page table. Sequences without tokens in the call
+        read nothing. Layers of one window share the cache."""
+        n, W = kc.page_table.shape[0], kc.window
+        longest = max_pos if W == 0 else min(max_pos, W - 1 + max_q)
+        # a ring's capacity is a multiple of the attention's key tiles
+        cap = longest if W == 0 else (W - 1 + max_q + 127) // 128 * 128
+        copy = self._copies.get((n, W))
+        if copy is None or copy.k.shape[2] != cap:
+            self._copies.pop((n, W), None)
+            dims = (n, self.shape.n_kv, cap, self.shape.head_dim)
+            k, v = (torch.empty(dims, dtype=torch.bfloat16, device=self.device) for _ in "kv")
+            copy = self._copies[(n, W)] = B.KVCache(k, v, window=W)
+        known = (seq_id >= 0) & (seq_id < n)      # the others are flagged by the library
+        s = torch.where(known, seq_id, 0).long()
+        last = torch.zeros(n, dtype=torch.int32, device=pos.device)
+        last.scatter_reduce_(0, s, torch.where(known, pos, 0), "amax")
+        first = torch.full_like(last, 2 ** 31 - 1)
+        first.scatter_reduce_(0, s, torch.where(known, pos, 2 ** 31 - 1), "amin")
+        first = (first - W + 1).clamp_min(1) if W else torch.ones_like(last)
+        first = torch.where(last > 0, first, 1)
+        return copy, torch.arange(n, dtype=torch.int32, device=pos.device), first, last, longest
+
+    def attention(self, i, b, seq_id, pos, max_pos, ws, stream, max_q_per_seq):
+        """Projection, cache write and attention of the i-th layer held, from b["u"] to b["a"]."""
+        W, cfg, kc = self.W[i], self.cfgs[i], self.caches[i]
+        if not isinstance(kc, B.PagedKVCache):
+            B.beam_qkv_gate(cfg, b["u"], W["w_qkvg"], W["q_norm"], W["k_norm"], seq_id, pos, b["q"],
+                            b["g"], kc, ws, stream)
+            B.beam_attn(cfg, b["q"], b["g"], W["gate_bias"], kc, seq_id, pos, max_pos, W["w_o"],
+                        b["a"], ws, stream, max_q_per_seq)
+            return
+        T = seq_id.shape[0]
+        max_q = T if max_q_per_seq is None else max_q_per_seq
+        stage, rows, k, v = self.stage(T)
+        B.beam_qkv_gate(cfg, b["u"], W["w_qkvg"], W["q_norm"], W["k_norm"], rows, pos, b["q"],
+                        b["g"], stage, ws, stream)
+        B.beam_paged_kv_write(k, v, seq_id, pos, kc, stream)
+        if max_q <= self.PAGED_MAX_Q:
+            B.beam_paged_attn(cfg, b["q"], b["g"], W["gate_bias"], kc, seq_id, pos, max_pos,
+                              W["w_o"], b["a"], ws, stream)
+            return
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            copy, every, first, last, longest = self.context(kc, seq_id, pos, max_pos, max_q)
+        B.beam_paged_kv_read(kc, every, first, last, longest, copy, stream)
+        B.beam_attn(cfg, b["q"], b["g"], W["gate_bias"], copy, seq_id, pos, max_pos, W["w_o"],
+                    b["a"], ws, stream, max_q_per_seq)
 
     def buffers(self, T):
         b = self._bufs.get(T)
@@ -73,14 +146,11 @@ class BeamStack:
         (h, u of the next layer). With a trace list, appends the layer's intermediate tensors:
         u_attn, q, g, attn, h_mid (h after the attention residual), mlp_in, mlp, route
         (logits, idx, w) on MoE layers, and the output h."""
-        W, cfg, kc = self.W[i], self.cfgs[i], self.caches[i]
+        W, cfg = self.W[i], self.cfgs[i]
         l = self.ids[i]
         if trace is not None:
             trace.append({"u_attn": b["u"].clone()})
-        B.beam_qkv_gate(cfg, b["u"], W["w_qkvg"], W["q_norm"], W["k_norm"], seq_id, pos, b["q"],
-                        b["g"], kc, ws, stream)
-        B.beam_attn(cfg, b["q"], b["g"], W["gate_bias"], kc, seq_id, pos, max_pos, W["w_o"],
-                    b["a"], ws, stream, max_q_per_seq)
+        self.attention(i, b, seq_id, pos, max_pos, ws, stream, max_q_per_seq)
         B.beam_boundary_norm(b["a"], b["h"], b["u"], W["attn_post"], W["mlp_pre"], 2 * l + 2,
                              cfg.eps, stream)
         if trace is not None:
@@ -115,7 +185,10 @@ class BeamStack:
         None = T). Returns h after the last residual addition (an internal buffer)."""
         T = e.shape[0]
         b = self.buffers(T)
-        ws = self.ws.get(B.workspace_bytes(self.cfgs[0], T, max_pos))
+        need = B.workspace_bytes(self.cfgs[0], T, max_pos)
+        if self.paged:
+            need = max(need, B.paged_workspace_bytes(self.cfgs[0], T, max_pos))
+        ws = self.ws.get(need)
         b["h"].copy_(e)
         B.beam_boundary_norm(None, b["h"], b["u"], None, self.W[0]["attn_pre"], 1,
                              self.cfgs[0].eps, stream)

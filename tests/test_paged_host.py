@@ -205,3 +205,60 @@ def test_binding_refuses_wrong_tensors():
                 lambda: B.PagedKVCache(k, k, table, block_scale=torch.zeros((3, 2, 2, 16, 4), dtype=torch.uint8))):
         with pytest.raises((B.BeamError, RuntimeError)):
             bad()
+
+
+def test_stack_takes_paged_layers(monkeypatch):
+    """BeamStack over paged caches (recorded calls, no kernel): up to PAGED_MAX_Q tokens per
+    sequence write and attend in the pages; more read the context back for beam_attn, with the
+    range of each sequence that has tokens in the call."""
+    from hybrid_attention_moe_gb300 import beam as B
+    from hybrid_attention_moe_gb300 import stack as S
+    shape = synth.TINY
+    W = [synth.layer_weights(shape, layer, 0) for layer in range(2)]
+
+    def paged(window):
+        c = object.__new__(B.PagedKVCache)
+        c.page_table, c.window = torch.zeros((4, 5), dtype=torch.int32), window
+        return c
+
+    caches = [paged(shape.window), B.KVCache(torch.zeros(1), torch.zeros(1), 0)]
+    st = S.BeamStack(shape, W, caches, device="cpu")
+    seen = []
+    for name in ("beam_qkv_gate", "beam_attn", "beam_boundary_norm", "beam_dense_mlp", "beam_route",
+                 "beam_moe", "beam_paged_kv_write", "beam_paged_kv_read", "beam_paged_attn"):
+        monkeypatch.setattr(B, name, lambda *a, _n=name, **k: seen.append((_n, a)))
+    monkeypatch.setattr(B, "workspace_bytes", lambda *a: 100)
+    monkeypatch.setattr(B, "paged_workspace_bytes", lambda *a: 5000)
+
+    def forward(seq, pos, max_q):
+        seen.clear()
+        e = torch.zeros((len(seq), shape.hidden), dtype=torch.bfloat16)
+        st.forward(e, torch.tensor(seq, dtype=torch.int32), torch.tensor(pos, dtype=torch.int32),
+                   max(pos), max_q_per_seq=max_q)
+        names = [n for n, _ in seen if n not in ("beam_boundary_norm", "beam_dense_mlp",
+                                                 "beam_route", "beam_moe")]
+        return names, dict(reversed(seen))     # the first call of each name
+
+    names, args = forward([2, 0], [30, 7], 1)
+    assert names == ["beam_qkv_gate", "beam_paged_kv_write", "beam_paged_attn", "beam_qkv_gate", "beam_attn"]
+    stage = args["beam_qkv_gate"][9]
+    assert stage.window == 1 and stage.k.shape == (2, shape.n_kv, 1, shape.head_dim)
+    assert args["beam_qkv_gate"][5].tolist() == [0, 1]          # a staging row per token
+    k, v, seq, pos, cache = args["beam_paged_kv_write"][:5]
+    assert k.shape == (2, shape.n_kv, shape.head_dim) and k.data_ptr() == stage.k.data_ptr()
+    assert seq.tolist() == [2, 0] and cache is caches[0]
+    assert args["beam_paged_attn"][10].numel() >= 5000
+
+    n = 9
+    names, args = forward([2] * n + [0] * 6, list(range(30, 30 + n)) + list(range(1, 7)), n)
+    assert names == ["beam_qkv_gate", "beam_paged_kv_write", "beam_paged_kv_read", "beam_attn",
+                     "beam_qkv_gate", "beam_attn"]
+    cache, every, first, last, longest, copy = args["beam_paged_kv_read"][:6]
+    w = shape.window
+    assert every.tolist() == [0, 1, 2, 3] and last.tolist() == [6, 0, 38, 0]
+    assert first.tolist() == [1, 1, 30 - w + 1, 1] and longest == w - 1 + n
+    assert copy.window == w and copy.k.shape[2] >= longest and copy.k.shape[2] % 128 == 0
+    assert args["beam_attn"][4] is copy
+    # sequence ids that name nothing do not reach the ranges
+    names, args = forward([-1, 99] + [1] * 5, [50, 60, 3, 4, 5, 6, 7], 5)
+    assert args["beam_paged_kv_read"][3].tolist() == [0, 7, 0, 0]
