@@ -46,13 +46,6 @@ __device__ __forceinline__ float round14(float x) {
   return __uint_as_float((__float_as_uint(x) + 0x200u) & 0xFFFFFC00u);
 }
 
-// The multiple of 2^-12 nearest to x * r (|x * r| < 2^10), with x's sign.
-__device__ __forceinline__ float quotient(float x, float r) {
-  constexpr float kMagic = 0x1.8p11f;   // the step of FP32 in [2^11, 2^12) is 2^-12
-  const float q = fmaf(x, r, kMagic) - kMagic;
-  return __uint_as_float((__float_as_uint(q) & 0x7FFFFFFFu) | (__float_as_uint(x) & 0x80000000u));
-}
-
 // A warp takes up to kHeads KV heads of one token, K and V, and issues all its loads before the
 // page is looked up. A lane holds 16 elements of a row (an NVFP4 block; a BF16 row, which is only
 // moved, is taken 8 a lane). The row's largest magnitude is an integer maximum of the bf16
@@ -60,15 +53,15 @@ __device__ __forceinline__ float quotient(float x, float r) {
 // top); the row's power of two follows from that pattern's exponent and fraction alone, so
 // nothing is rounded before the codes are.
 //
-// Quotients by s are taken with a reciprocal and rounded to multiples of 2^-12. A quotient that is
-// a midpoint of two codes (0.25 at least, 3 bits) comes back exactly; any other one is further
-// from every midpoint (2^-8 of it, 2^-10 at least: the dividend has 8 bits, s 4 and the midpoint 3)
-// than the errors reach (2^-20 and 2^-13), so the code is that of the exact quotient. The sixth
-// of the block's largest value is rounded to 14 bits in the same manner: a midpoint of e4m3 has 5
-// bits, and any other sixth is 2^-8 of it away (the dividend has 8 bits, 6 midpoints 7).
-constexpr int kHeads = 4;
+// Quotients by s are taken with a reciprocal and rounded to f16. A quotient that is a midpoint of
+// two codes (3 bits) comes back exactly; any other one is 2^-8 of the midpoint or more away from it
+// (the dividend has 8 bits, s 4), which the reciprocal's error (2^-21) and half a step of f16
+// (2^-11) do not reach, so the code is that of the exact quotient. The sixth of the block's largest
+// value is rounded to 14 bits in the same manner: a midpoint of e4m3 has 5 bits, and any other
+// sixth is 2^-8 of it away (the dividend has 8 bits, 6 midpoints 7).
+constexpr int kHeads = 8;
 template <int FMT, int D>
-__global__ void __launch_bounds__(256, 5) paged_write_kernel(const WriteParams P) {
+__global__ void __launch_bounds__(256, 4) paged_write_kernel(const WriteParams P) {
   pdl_trigger();
   pdl_wait();
   constexpr int EPL = FMT == kFmtBF16 ? 8 : 16, NV = EPL / 8;
@@ -146,15 +139,15 @@ __global__ void __launch_bounds__(256, 5) paged_write_kernel(const WriteParams P
         uint32_t w[EPL / 8];
 #pragma unroll
         for (int i = 0; i < EPL / 8; ++i) {
-          float q[8];
+          uint32_t q[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) q[e] = quotient(y[8 * i + e], rs);
+          for (int e = 0; e < 4; ++e) q[e] = pack_f16x2(y[8 * i + 2 * e] * rs, y[8 * i + 2 * e + 1] * rs);
           asm("{.reg .b8 a, b, c, d;"
-              " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1; cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;"
-              " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5; cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;"
+              " cvt.rn.satfinite.e2m1x2.f16x2 a, %1; cvt.rn.satfinite.e2m1x2.f16x2 b, %2;"
+              " cvt.rn.satfinite.e2m1x2.f16x2 c, %3; cvt.rn.satfinite.e2m1x2.f16x2 d, %4;"
               " mov.b32 %0, {a, b, c, d};}"
               : "=r"(w[i])
-              : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+              : "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3]));
           if (s == 0) w[i] = 0u;   // the block is zeros, or the row holds no numbers
         }
         if (store) {
