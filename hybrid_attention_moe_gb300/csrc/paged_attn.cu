@@ -65,8 +65,9 @@ struct Cfg {
   static constexpr int GROUPS = FMT == kFmtNVFP4 && D == 128 && NT == 1 ? 3 : 2;
   static constexpr int WPG = 4, SPW = HEAVY ? 1 : 2;
   static constexpr int NCW = WPG * GROUPS, NCT = WPG * 32;   // consumer warps, threads of a group
-  // four producer warps: K and V of each of two groups, or both for each of three (one warp idle)
-  static constexpr bool BOTH = GROUPS == 3;
+  // four more warps: a producer for each group, and with two groups a finisher for each, which
+  // joins the consumer warps' partials of a pair while they take the next one
+  static constexpr bool FIN = GROUPS == 2;
   static constexpr int THREADS = (NCW + 4) * 32;
   static constexpr int SLICES = WPG * SPW, BK = 16 * SLICES;
   static constexpr int KB = BK * ROWB;
@@ -184,7 +185,16 @@ __device__ __forceinline__ uint16_t ld_ahead16(const uint16_t* p) {
 }
 template <int NTHREADS>
 __device__ __forceinline__ void consumer_bar(int group) {
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(NTHREADS) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group * 5), "n"(NTHREADS) : "memory");
+}
+// Hand-over of combine buffer `buf` between a group's consumers and its finisher: full (which = 0)
+// or empty (1). WAIT: the side that waits; the other only arrives.
+template <int NTHREADS, bool WAIT>
+__device__ __forceinline__ void pair_bar(int group, int which, int buf) {
+  const int id = 2 + group * 5 + which * 2 + buf;
+  __syncwarp();
+  if (WAIT) asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(NTHREADS) : "memory");
+  else asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(NTHREADS) : "memory");
 }
 // Untiled bulk copy (16-byte aligned, a multiple of 16 bytes).
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -563,6 +573,39 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
   }
 }
 
+// The consumer warps' partials of a pair (combine buffer b of the CTA), joined: the four outputs
+// from element idx of the pair's [G][D / 4]. A pair that other ranges share goes to the workspace
+// (rows pb ..), another is finished.
+template <int FMT, class C>
+__device__ __forceinline__ void join_warps(const Params& P, uint8_t* sm, int b, int idx, bool split,
+                                           size_t pb, size_t o_pair, uint2 gv, float gb) {
+  constexpr int D = C::D;
+  const float* Ow = reinterpret_cast<const float*>(sm + C::OW + b * C::OWB);
+  const float2* MLw = reinterpret_cast<const float2*>(sm + C::MLW + b * C::MLB);
+  const int h = idx / (D / 4), d = 4 * (idx - h * (D / 4));
+  float M = kLowest, L = 0.f;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int ww = 0; ww < C::WPG; ++ww) M = fmaxf(M, MLw[ww * C::HEADS + h].x);
+#pragma unroll
+  for (int ww = 0; ww < C::WPG; ++ww) {
+    const float2 ml = MLw[ww * C::HEADS + h];
+    const float fw = ex2(ml.x - M);
+    L += fw * ml.y;
+    const float4 v = *reinterpret_cast<const float4*>(Ow + (ww * C::HEADS + h) * C::OLD + spread<FMT, D>(d));
+    O.x += fw * v.x;
+    O.y += fw * v.y;
+    O.z += fw * v.z;
+    O.w += fw * v.w;
+  }
+  if (split) {
+    *reinterpret_cast<float4*>(P.part_acc + (pb + h) * D + d) = O;
+    if (d == 0) *reinterpret_cast<float2*>(P.part_ml + (pb + h) * 2) = make_float2(M, L);
+  } else {
+    finish4(P.g != nullptr, O, L, gv, gb, P.og + o_pair + 4 * idx);
+  }
+}
+
 // Row of the partial results of part s of a joined pair and its query head h: the first part's slot
 // is jn.w, and in the ranges after it the pair is the first.
 template <int HEADS>
@@ -589,7 +632,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NST; ++s) {
-      mbar_init(bar_full + 8 * s, C::BOTH ? 1 : 2);   // the producers of K and of V
+      mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, C::WPG);
     }
     misc[1] = 0;
@@ -675,11 +718,39 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
     f_hi = min(total, f_lo + R);
   }
   const int t_lo = f_lo < f_hi ? row_at(f_lo) : 0;
+  // the range's pairs in order: flat block f is block j0 of the pair whose blocks begin at f_pair;
+  // the range holds its blocks j0 .. j1 - 1 of nb
+  struct PairAt {
+    int f, t, hk, nb, f_pair, j0, j1;
+  };
+  auto pair_at = [&](int f) {
+    PairAt a{f, t_lo, 0, 1, f, 0, 0};
+    if (f >= f_hi) return a;   // an empty range: no blocks from f on
+    a.nb = cum[t_lo + 1] - cum[t_lo];
+    const int r = f - cum[t_lo] * P.n_kv;
+    a.hk = r / a.nb;
+    a.j0 = r - a.hk * a.nb;
+    a.f_pair = f - a.j0;
+    a.j1 = min(a.nb, f_hi - a.f_pair);
+    return a;
+  };
+  auto next_pair = [&](PairAt a) {
+    a.f = a.f_pair + a.j1;
+    if (a.f >= f_hi) return a;
+    if (++a.hk == P.n_kv) {
+      a.hk = 0;
+      do ++a.t;
+      while (cum[a.t + 1] == cum[a.t]);
+      a.nb = cum[a.t + 1] - cum[a.t];
+    }
+    a.f_pair = a.f;
+    a.j0 = 0;
+    a.j1 = min(a.nb, f_hi - a.f);
+    return a;
+  };
 
-  if (warp >= C::NCW) {
+  if (warp >= C::NCW && warp < C::NCW + C::GROUPS) {
     // ---------------- producers
-    const bool keys = C::BOTH || warp - C::NCW < 2, vals = C::BOTH || warp - C::NCW >= 2;
-    if (C::BOTH && warp - C::NCW == 3) f_hi = f_lo;
     const int pse = min(P.c.page_size, BK), npg = BK / pse;   // keys of a page in a block, pages
     struct At {
       int t, hk, j, nb, blk0, lo, p, s;
@@ -740,45 +811,35 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
       const int off = ((a.blk0 + a.j) * BK + lane * pse) & (P.c.page_size - 1);   // first key in the page
       const int y = C::PLANES == 2 ? off : off * C::ROWB / 128;
       const bool part = pse < P.c.page_size;   // part of a page: K's and V's scales lie apart
-      if (keys) {
-        const bool with_q = f == f_lo || a.j == 0;   // a pair's first block here
-        const unsigned slices = __ballot_sync(0xffffffffu, lane < C::SLICES && ((okm >> (lane * 16 / pse)) & 1u));
-        if (lane == 0) {
-          masks[st] = slices;
-          const int row = C::BOTH ? 2 * C::ROWB + 2 + 2 * (D / 16) : C::ROWB + (FMT != kFmtBF16 ? 2 : 0);
-          mbar_expect_tx(fb, __popc(okm) * pse * row + (with_q ? P.G * D * 2 : 0));
-        }
-        __syncwarp();
-        if (ok) {
-          const uint32_t dk = base + lane * pse * (C::ROWB / C::PLANES);
-          tma_load_3d(dk, &tk, 0, y, z, fb);
-          if constexpr (C::PLANES == 2) tma_load_3d(dk + C::KB / 2, &tk, 128, y, z, fb);
-          if constexpr (FMT != kFmtBF16) {
-            const uint8_t* src = P.c.row_scale + size_t(z) * 2 * P.c.page_size + off;
-            const uint32_t dr = base + C::ORS + lane * 2 * pse;
-            bulk_load(dr, src, part ? pse : 2 * pse, fb);
-            if (part) bulk_load(dr + pse, src + P.c.page_size, pse, fb);
-          }
-        }
-        if (with_q && lane == 31)
-          bulk_load(base + C::OQ, P.q + (size_t(a.t) * P.n_q + a.hk * P.G) * D, P.G * D * 2, fb);
+      const bool with_q = f == f_lo || a.j == 0;   // a pair's first block here
+      const unsigned slices = __ballot_sync(0xffffffffu, lane < C::SLICES && ((okm >> (lane * 16 / pse)) & 1u));
+      if (lane == 0) {
+        masks[st] = slices;
+        constexpr int row = C::ROWB + (FMT != kFmtBF16 ? 1 : 0) + (FMT == kFmtNVFP4 ? D / 16 : 0);
+        mbar_expect_tx(fb, __popc(okm) * pse * 2 * row + (with_q ? P.G * D * 2 : 0));
       }
-      if (vals) {
-        if (lane == 0 && !C::BOTH)
-          mbar_expect_tx(fb, __popc(okm) * pse * (C::ROWB + (FMT == kFmtNVFP4 ? 2 * (D / 16) : 0)));
-        __syncwarp();
-        if (ok) {
-          const uint32_t dv = base + C::KB + lane * pse * (C::ROWB / C::PLANES);
-          tma_load_3d(dv, &tv, 0, y, z, fb);
-          if constexpr (C::PLANES == 2) tma_load_3d(dv + C::KB / 2, &tv, 128, y, z, fb);
+      __syncwarp();
+      if (ok) {
+        const uint32_t dk = base + lane * pse * (C::ROWB / C::PLANES), dv = dk + C::KB;
+        tma_load_3d(dk, &tk, 0, y, z, fb);
+        if constexpr (C::PLANES == 2) tma_load_3d(dk + C::KB / 2, &tk, 128, y, z, fb);
+        tma_load_3d(dv, &tv, 0, y, z, fb);
+        if constexpr (C::PLANES == 2) tma_load_3d(dv + C::KB / 2, &tv, 128, y, z, fb);
+        if constexpr (FMT != kFmtBF16) {
+          const size_t sr = size_t(z) * 2 * P.c.page_size + off;
+          const uint32_t dr = base + C::ORS + lane * 2 * pse;
+          bulk_load(dr, P.c.row_scale + sr, part ? pse : 2 * pse, fb);
+          if (part) bulk_load(dr + pse, P.c.row_scale + sr + P.c.page_size, pse, fb);
           if constexpr (FMT == kFmtNVFP4) {
-            const uint8_t* src = P.c.block_scale + (size_t(z) * 2 * P.c.page_size + off) * (D / 16);
+            const uint8_t* src = P.c.block_scale + sr * (D / 16);
             const uint32_t db = base + C::OBS + lane * 2 * pse * (D / 16);
             bulk_load(db, src, (part ? 1 : 2) * pse * (D / 16), fb);
             if (part) bulk_load(db + pse * (D / 16), src + P.c.page_size * (D / 16), pse * (D / 16), fb);
           }
         }
       }
+      if (with_q && lane == 31)
+        bulk_load(base + C::OQ, P.q + (size_t(a.t) * P.n_q + a.hk * P.G) * D, P.G * D * 2, fb);
       __syncwarp();
     }
     // normally done at once, with the last blocks: after an expired wait elsewhere, let the copies
@@ -786,6 +847,38 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
     if (lane == 0)
       for (int k = i - 1; k >= 0 && k >= i - C::NSTG; --k)
         mbar_wait(bar_full + 8 * (grp * C::NSTG + k % C::NSTG), (k / C::NSTG) & 1);
+  } else if (warp >= C::NCW) {
+    if constexpr (C::FIN) {
+      // ---------------- finishers: all pairs but the range's last, which nothing follows
+      int buf = 0;
+      for (PairAt a = pair_at(f_lo); a.f_pair + a.j1 < f_hi; a = next_pair(a)) {
+        const bool split = a.j0 > 0 || a.j1 < a.nb;
+        const size_t o_pair = (size_t(a.t) * P.n_q + a.hk * P.G) * D;
+        const size_t pb = size_t(2 * range) * C::HEADS;   // split: the range's first pair
+        constexpr int N = 8;   // outputs whose gates a lane fetches ahead
+#pragma unroll 1
+        for (int x0 = 0; x0 < C::HEADS * (D / 4); x0 += 32 * N) {
+          uint2 gv[N];
+          float gb[N];
+#pragma unroll
+          for (int u = 0; u < N; ++u) {
+            const int idx = x0 + 32 * u + lane;
+            if (P.g != nullptr && !split && idx < P.G * (D / 4)) {
+              gv[u] = ld_ahead(P.g + o_pair + 4 * idx);
+              gb[u] = bf2f(ld_ahead16(P.gate_bias + a.hk * P.G + idx / (D / 4)));
+            }
+          }
+          if (x0 == 0) pair_bar<NCT + 32, true>(grp, 0, buf);
+#pragma unroll
+          for (int u = 0; u < N; ++u) {
+            const int idx = x0 + 32 * u + lane;
+            if (idx < P.G * (D / 4)) join_warps<FMT, C>(P, sm, grp * C::NOW + buf, idx, split, pb, o_pair, gv[u], gb[u]);
+          }
+        }
+        pair_bar<NCT + 32, false>(grp, 1, buf);
+        buf = C::NOW - 1 - buf;
+      }
+    }
   } else {
     // ---------------- consumers
     const int w = warp % C::WPG, g = lane >> 2, c = lane & 3, ct = threadIdx.x % NCT;
@@ -794,34 +887,29 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
     for (int e = 0; e < C::SPW; ++e) ln[e] = lane_of<FMT, C>(w + e * C::WPG, min(P.c.page_size, BK));
     bool dead = false;   // a wait has expired: the rest of the range passes without results
     const int G = P.G;
-    int i = 0, t = t_lo, f = f_lo, buf = 0;
+    int i = 0, buf = 0, pairs = 0;
     int4 join = make_int4(0, 0, 0, 0);
-    int hk = 0, j0 = 0;
-    if (f_lo < f_hi) {
-      const int nb = cum[t + 1] - cum[t], r = f_lo - cum[t] * P.n_kv;
-      hk = r / nb;
-      j0 = r - hk * nb;
-    }
-    while (f < f_hi) {
-      const int p = rpos[t], lo = P.c.window > 0 ? max(1, p - P.c.window + 1) : 1;
-      const int blk0 = (lo - 1) / BK, nb = cum[t + 1] - cum[t];
-      const int f_pair = cum[t] * P.n_kv + hk * nb;   // the pair's first block
-      const int j1 = min(nb, f_hi - f_pair);
-      const bool split = j0 > 0 || j1 < nb;
-      // the gate of the outputs that this thread finishes: fetched now, used after the keys
+    for (PairAt at = pair_at(f_lo); at.f < f_hi; at = next_pair(at)) {
+      const int p = rpos[at.t], lo = P.c.window > 0 ? max(1, p - P.c.window + 1) : 1;
+      const int blk0 = (lo - 1) / BK, j0 = at.j0, j1 = at.j1;
+      const bool split = j0 > 0 || j1 < at.nb;
+      // the gate of the outputs that this thread finishes: fetched ahead
       uint2 gv[C::ITEMS];
       float gb[C::ITEMS];
-      const size_t o_pair = (size_t(t) * P.n_q + hk * G) * D;
-      if (P.g != nullptr && !split) {
+      const size_t o_pair = (size_t(at.t) * P.n_q + at.hk * G) * D;
+      auto fetch_gate = [&] {
+        if (P.g == nullptr || split) return;
 #pragma unroll
         for (int it = 0; it < C::ITEMS; ++it) {
           const int idx = ct + it * NCT;
           if (idx < G * (D / 4)) {
             gv[it] = ld_ahead(P.g + o_pair + 4 * idx);
-            gb[it] = bf2f(ld_ahead16(P.gate_bias + hk * G + idx / (D / 4)));
+            gb[it] = bf2f(ld_ahead16(P.gate_bias + at.hk * G + idx / (D / 4)));
           }
         }
-      }
+      };
+      const bool mine = !C::FIN || at.f_pair + j1 >= f_hi;   // no finisher, or the range's last pair
+      if (!C::FIN) fetch_gate();
       uint32_t qb[NT][D / 16][2];
       float qs[NT][2];
       WarpState<C> S;
@@ -894,13 +982,15 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_empty + 8 * st);
       }
-      // ---- combine the consumer warps' partials of the pair. Two buffers in turn: who writes
-      // one has passed the barrier of the pair between, which its last readers came to later
-      // (one buffer, where two do not fit, needs a barrier of its own).
-      if constexpr (C::NOW == 1) consumer_bar<NCT>(grp);
+      // ---- the warp's partial of the pair, into a buffer that its last reader has left
+      if (C::FIN && mine) fetch_gate();
+      if constexpr (C::FIN) {
+        if (pairs >= C::NOW) pair_bar<NCT + 32, true>(grp, 1, buf);
+      } else if constexpr (C::NOW == 1) {
+        consumer_bar<NCT>(grp);
+      }
       float* Ow = reinterpret_cast<float*>(sm + C::OW + (grp * C::NOW + buf) * C::OWB);
       float2* MLw = reinterpret_cast<float2*>(sm + C::MLW + (grp * C::NOW + buf) * C::MLB);
-      buf = C::NOW - 1 - buf;
       // 2^(E - 127 - kBias)
       const float unit = __uint_as_float(S.E > kBias ? unsigned(S.E - kBias) << 23 : 0x00800000u >> (kBias + 1 - S.E));
 #pragma unroll
@@ -931,47 +1021,27 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
           MLw[h0 + 1] = make_float2(S.m[n][1], S.l[n][1]);
         }
       }
-      consumer_bar<NCT>(grp);
-      const int slot = f == f_lo ? 0 : 1;   // the range's first pair, or its last
-      const size_t pb = (size_t(2 * range) + slot) * C::HEADS;
+      if (!mine) {
+        pair_bar<NCT + 32, false>(grp, 0, buf);
+      } else {
+        // without a finisher two buffers in turn: who writes one has passed the barrier of the pair
+        // between, which its last readers came to later
+        consumer_bar<NCT>(grp);
+        const int slot = at.f == f_lo ? 0 : 1;   // the range's first pair, or its last
+        const size_t pb = (size_t(2 * range) + slot) * C::HEADS;
 #pragma unroll
-      for (int it = 0; it < C::ITEMS; ++it) {
-        const int idx = ct + it * NCT;
-        if (idx >= G * (D / 4)) break;
-        const int h = idx / (D / 4), d = 4 * (idx - h * (D / 4));
-        float M = kLowest, L = 0.f;
-        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int ww = 0; ww < C::WPG; ++ww) M = fmaxf(M, MLw[ww * C::HEADS + h].x);
-#pragma unroll
-        for (int ww = 0; ww < C::WPG; ++ww) {
-          const float2 ml = MLw[ww * C::HEADS + h];
-          const float fw = ex2(ml.x - M);
-          L += fw * ml.y;
-          const float4 v = *reinterpret_cast<const float4*>(Ow + (ww * C::HEADS + h) * C::OLD + spread<FMT, D>(d));
-          O.x += fw * v.x;
-          O.y += fw * v.y;
-          O.z += fw * v.z;
-          O.w += fw * v.w;
+        for (int it = 0; it < C::ITEMS; ++it) {
+          const int idx = ct + it * NCT;
+          if (idx < G * (D / 4)) join_warps<FMT, C>(P, sm, grp * C::NOW + buf, idx, split, pb, o_pair, gv[it], gb[it]);
         }
-        if (split) {
-          *reinterpret_cast<float4*>(P.part_acc + (pb + h) * D + d) = O;
-          if (d == 0) *reinterpret_cast<float2*>(P.part_ml + (pb + h) * 2) = make_float2(M, L);
-          continue;
-        }
-        finish4(P.g != nullptr, O, L, gv[it], gb[it], P.og + o_pair + 4 * idx);
+        if (j0 == 0 && j1 < at.nb)   // the pair begins here and runs on
+          join = make_int4(at.t, at.hk, (at.f_pair + at.nb - 1 - f0) / R - (f_lo - f0) / R + 1, slot);
       }
-      if (j0 == 0 && j1 < nb)   // the pair begins here and runs on
-        join = make_int4(t, hk, (f_pair + nb - 1 - f0) / R - (f_lo - f0) / R + 1, slot);
-      // ---- next pair
-      f = f_pair + j1;
-      j0 = 0;
-      if (++hk == P.n_kv) {
-        hk = 0;
-        do ++t;
-        while (t < T && cum[t + 1] == cum[t]);
-      }
+      buf = C::NOW - 1 - buf;
+      ++pairs;
     }
+    // every release of a buffer is waited for: that of the last pair but one is left
+    if (C::FIN && C::NOW == 2 && pairs >= 2) pair_bar<NCT + 32, true>(grp, 1, buf);
     if (ct == 0) {
       if (P.whole) joins[grp] = join;
       else if (range < P.ranges) P.join[range] = join;
