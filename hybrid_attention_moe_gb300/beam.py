@@ -352,24 +352,29 @@ def paged_kv_bytes(num_pages, n_kv, page_size, head_dim, dtype=BEAM_PAGED_BF16) 
 def beam_paged_kv_write(k, v, seq_id, pos, cache: PagedKVCache, stream=None):
     """k, v [T][n_kv][D] bf16 (rows of a token contiguous, any stride between tokens that is a
     multiple of 8) into the cache's pages."""
-    dev = _on_device(cache)
+    dev, bf, i32 = _on_device(cache), torch.bfloat16, torch.int32
     n_kv, D = cache.n_kv, cache.head_dim
-    T, step = k.shape[0], n_kv * D
-    for name, x in (("k", k), ("v", v)):
-        if x.dtype != torch.bfloat16 or x.shape != (T, n_kv, D) or x.get_device() != dev:
-            raise BeamError(f"beam_paged_kv_write: {name} must be bfloat16 ({T}, {n_kv}, {D}) on "
-                            f"cuda:{dev}, got {x.dtype} {tuple(x.shape)} on {x.device}")
-        if T and not x.is_contiguous():
-            s0, s1, s2 = x.stride()
-            if s2 != 1 or (n_kv > 1 and s1 != D):
+    T, step = k.size(0), n_kv * D
+    n = T * step
+    # one test of everything for rows that lie side by side; others, and what is wrong, below
+    if not (k.dtype is bf and k.numel() == n and k.is_contiguous() and k.get_device() == dev and
+            v.dtype is bf and v.numel() == n and v.is_contiguous() and v.get_device() == dev and
+            seq_id.dtype is i32 and seq_id.numel() == T and seq_id.is_contiguous() and
+            seq_id.get_device() == dev and pos.dtype is i32 and pos.numel() == T and
+            pos.is_contiguous() and pos.get_device() == dev):
+        for name, x in (("k", k), ("v", v)):
+            if x.dtype != bf or x.shape != (T, n_kv, D) or x.get_device() != dev:
+                raise BeamError(f"beam_paged_kv_write: {name} must be bfloat16 ({T}, {n_kv}, {D}) "
+                                f"on cuda:{dev}, got {x.dtype} {tuple(x.shape)} on {x.device}")
+            if T and (x.stride(2) != 1 or (n_kv > 1 and x.stride(1) != D)):
                 raise BeamError(f"beam_paged_kv_write: the rows of a token of {name} must be "
                                 f"contiguous, got strides {x.stride()}")
-    if T > 1:
-        step = k.stride(0)
-        if v.stride(0) != step:
-            raise BeamError("beam_paged_kv_write: k and v have different strides between tokens")
-    _want(dev, "seq_id", seq_id, torch.int32, T)
-    _want(dev, "pos", pos, torch.int32, T)
+        if T > 1:
+            step = k.stride(0)
+            if v.stride(0) != step:
+                raise BeamError("beam_paged_kv_write: k and v have different strides between tokens")
+        _want(dev, "seq_id", seq_id, i32, T)
+        _want(dev, "pos", pos, i32, T)
     st = lib().beam_paged_kv_write(k.data_ptr(), v.data_ptr(), step, seq_id.data_ptr(),
                                    pos.data_ptr(), T, cache._ref, _raw_stream(stream, dev))
     if st:
@@ -380,15 +385,23 @@ def beam_paged_kv_read(cache: PagedKVCache, seq_id, first, last, max_len, dst: K
                        stream=None):
     """Positions first[i]..last[i] of sequence seq_id[i] into row i of the contiguous BF16 cache
     dst, slot (p-1) % capacity."""
-    dev = _on_device(cache)
-    N = seq_id.shape[0]
-    _want(dev, "seq_id", seq_id, torch.int32, N)
-    _want(dev, "first", first, torch.int32, N)
-    _want(dev, "last", last, torch.int32, N)
-    rows, _, cap, _ = dst.k.shape
-    _want(dev, "dst.k", dst.k, torch.bfloat16, rows * cache.n_kv * cap * cache.head_dim)
-    _want(dev, "dst.v", dst.v, torch.bfloat16, rows * cache.n_kv * cap * cache.head_dim)
-    kc = dst.c()
+    dev, i32, k, v = _on_device(cache), torch.int32, dst.k, dst.v
+    N = seq_id.numel()
+    rows, _, cap, _ = k.shape
+    n = rows * cache.n_kv * cap * cache.head_dim
+    if not (seq_id.dtype is i32 and seq_id.is_contiguous() and seq_id.get_device() == dev and
+            first.dtype is i32 and first.numel() == N and first.is_contiguous() and
+            first.get_device() == dev and last.dtype is i32 and last.numel() == N and
+            last.is_contiguous() and last.get_device() == dev and k.dtype is torch.bfloat16 and
+            k.numel() == n and k.is_contiguous() and k.get_device() == dev and
+            v.dtype is torch.bfloat16 and v.shape == k.shape and v.is_contiguous() and
+            v.get_device() == dev):
+        for name, x in (("seq_id", seq_id), ("first", first), ("last", last)):
+            _want(dev, name, x, i32, N)
+        for name, x in (("dst.k", k), ("dst.v", v)):
+            _want(dev, name, x, torch.bfloat16, n)
+        raise BeamError(f"beam_paged_kv_read: dst.k {tuple(k.shape)} and dst.v {tuple(v.shape)} differ")
+    kc = KVCacheC(k.data_ptr(), v.data_ptr(), BEAM_KV_BF16, 1.0, 1.0, rows, cap, dst.window)
     st = lib().beam_paged_kv_read(cache._ref, seq_id.data_ptr(), first.data_ptr(),
                                   last.data_ptr(), N, int(max_len), ctypes.byref(kc),
                                   _raw_stream(stream, dev))

@@ -433,6 +433,25 @@ def test_attention_nan_rows_reach_their_readers_only(fmt):
     assert np.all(np.isfinite(o[2:]))
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+def test_attention_over_shared_pages(fmt):
+    """Two sequences with a common prefix share its pages, a third repeats one page; a call with
+    one row of each, and one whose every row is padding under a bound of 0."""
+    cfg = cfg_for(6, 2, 64)
+    c, *_ = make_cache(fmt, 2, 64, 32, [200, 150, 96], 231)
+    c.page_table[1, :3] = c.page_table[0, :3]
+    c.page_table[2, :3] = c.page_table[0, 1]
+    q = randn(232, 3, 6, 64)
+    seq, pos = ints([0, 1, 2]), ints([200, 150, 96])
+    out = attend(cfg, c, q, seq, pos, 200)
+    assert status() == 0
+    check_attn(cfg, c, q, seq, pos, out)
+    out = attend(cfg, c, q, seq, ints([0, 0, 0]), 0)
+    assert status() == 0 and not out.any()
+    out = attend(cfg, c, q, seq, pos, 0)
+    assert status() == B.DEV_BAD_POSITION and not out.any()
+
+
 def test_attention_many_rows():
     """More rows than one launch takes (1024): the slices share the workspace in order."""
     cfg = cfg_for(2, 1, 64)
