@@ -1,7 +1,11 @@
 // Paged key-value cache: rows quantised as they are written, and read back into a contiguous
 // BF16 cache. The formats are those of include/beam.h (beam_paged_kv).
 //
-// Both kernels move bytes once: bounded by HBM for long calls and by the launch for short ones.
+// Both kernels move bytes once and do little with them. Reading back is bounded by HBM (192,000
+// tokens of 8 heads from FP8: 176.5 us, 99% of the copy rate). Writing 16,384 tokens of 8 heads:
+// BF16 21.4 us, FP8 16.1, NVFP4 15.3 with the input in L2 and 21.8 from HBM (59% of the copy rate),
+// where the quantisation's ~180 warp instructions for 512 elements keep the issue slots 55% busy.
+// A decode step's rows (32 tokens) take 2.5 us, most of it the launch and three dependent loads.
 #include "mma.cuh"
 #include "paged.cuh"
 

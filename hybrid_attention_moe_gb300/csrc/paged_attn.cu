@@ -4,32 +4,52 @@
 //   o[h] = sum_i e^(x_i - m) v_i / sum_i e^(x_i - m),  x_i = q[h].k_i / sqrt(D),  m = max x_i
 //
 // over the row's keys i, computed in one pass with the running (m, sum, O) of a softmax, which
-// partial results of disjoint key ranges join by. Bounded by the bytes of the keys and values.
+// partial results of disjoint key ranges join by.
+//
+// What bounds it (device time in a graph; HBM 6784.5 GB/s as a copy): the bytes of the keys and
+// values over long contexts: 128 sequences of 17 to 16,385 tokens in FP8 323 us, 99% of the copy
+// rate; one of 100,001 in BF16 66.7 us, 91%, the rest being the start (1.6 us of plan, 0.9 us of page
+// lookups) and the join (3 us). Over an NVFP4 cache the arithmetic: 4 sequences of 60,000 to
+// 100,001 tokens 82.4 us, 67%: about 345 warp instructions for 16 keys of one KV head, 128 of them
+// the conversions and the scaling of the codes, which keep the issue slots 64% and the integer
+// pipe 59% busy.
 //
 // Split. A (row, KV head) pair's keys are cut into blocks of BK; the blocks of all pairs, laid
-// end to end, are cut into one equal range per CTA (one CTA per SM). The ranges are computed on
-// the device from the rows' own lengths, so a batch of very unequal sequences still gives every
-// SM the same bytes. A pair that one CTA holds whole is finished there; the partials of a split
-// 
+// end to end, are cut into equal ranges, two or three per CTA (one CTA per SM). The ranges are
+// computed on the device from the rows' own lengths, so a batch of very unequal sequences still
+// gives every SM the same bytes. A pair that one range holds whole is finished there; the partials
+// of a split pair go to the workspace and a second small kernel joins them. Where pairs are short
+// (the rule and its measurements stand at the launch) a CTA takes whole pairs, its groups share
+// them, and it joins them itself.
 //
-// Per CTA a producer warp reads the page table (one lane per page of the block, a block ahead)
-// and issues a TMA load per page for K and V into a ring of stages, with the rows' scales and,
-// for a pair's first block, its q rows beside them. The consumer warps each take 16 keys of a
-// block. The tiles are transposed, so that the query heads of a KV group are the 8-wide N side
-// of mma.sync m16n8k16 (two N tiles for 9 to 16 heads):
+// A CTA has two or three groups, each with its own range and ring of stages:
+//  - a producer warp reads the page table (one lane per page of a block, a block ahead) and issues
+//    a TMA load per page for K and V, bulk copies of the rows' scales and, with a pair's first
+//    block, of its q rows;
+//  - four consumer warps take one or two slices of 16 keys of every block. More warps with fewer
+//    registers were slower (16 of 96 registers: FP8 370 us against 333, with spills);
+//  - with two groups a finisher warp joins the consumers' partials of a pair while they go on
+//    (330 -> 323 us; windows of 512 keys 37.3 -> 35.2). NVFP4 at head dim 128, bound by arithmetic,
+//    has a third group instead (88.5 -> 82.4 us).
+//
+// Tiles are transposed, so that the query heads of a KV group are the 8-wide N side of mma.sync
+// m16n8k16 (two N tiles for 9 to 16 heads):
 //   S^T[16 keys x 8 heads] = K[16 x D] . Q^T,   O^T[D x 8 heads] += V^T[D x 16 keys] . P^T
-// P is split into a high and a low half, so it carries twice the operand type's bits.
+// The running max lags by up to 2^8: a vote decides whether it moves at all, so the common block
+// has no shuffle (439 -> 393 us with the two points below).
 //
-// FP8 and NVFP4 codes become f16 in registers, exactly (e2m1 times its e4m3 block scale has 6
-// significant bits), and the products run in f16 with FP32 accumulation. The d axis is permuted
-// the same way in q and K, and undone on the output for V, so that a thread's codes are
-// contiguous bytes. The rows' powers of two never enter an f16 value: K's multiplies the FP32
-// logits; V's goes into P relative to the largest one that the warp has seen (E), as
-// p * 2^(e - E + 7), so that P's largest values lie near the top of f16 and rows of smaller
-// values keep their bits. q is scaled by a power of two per head in the same manner.
+// Roundings. Logits, sums and O are FP32. Over a BF16 cache P is split into a high and a low bf16
+// half (16 bits). Over FP8 and NVFP4 the codes become f16 in registers, exactly (e2m1 times its
+// e4m3 block scale has 6 significant bits), and P is rounded once to f16: its half step, 2^-11 of a
+// weight, is far below the cache's own (2^-4 and 2^-2), and the low half cost a third of the
+// arithmetic. The rows' powers of two never enter an f16 value: K's multiplies the FP32 logits;
+// V's goes into P relative to the largest one that the warp has seen (E), as p * 2^(e - E + 7), so
+// that P's largest values lie near the top of f16 and rows of smaller values keep their bits. q is
+// scaled by a power of two per head in the same manner. The d axis is permuted the same way in q
+// and K, and undone on the output for V, so that a thread's codes are contiguous bytes.
 //
-// Every wait is bounded: on expiry the CTA records BEAM_DEV_TIMEOUT, stops issuing, lets its
-// issued copies land and finishes without valid results.
+// Every mbarrier wait is bounded: on expiry the CTA records BEAM_DEV_TIMEOUT, stops issuing, lets
+// its issued copies land and finishes without valid results.
 #include <cuda.h>
 #include <math.h>
 

@@ -15,7 +15,9 @@ moe_prefill (grouped tensor-core GEMMs, 2048 tokens over 32 experts), attn_nope_
 (tensor-core attention: one sequence, 2048 new tokens after --ctx cached keys, NoPE, BF16 KV),
 attn_swa_prefill (the same over a 512-key sliding window, 8 sequences), attn_nope_verify
 (--tokens new tokens of one sequence after --ctx cached keys, NoPE, BF16 KV, bound = tokens:
-the grouped decode form of a verification batch).
+the grouped decode form of a verification batch), paged_decode, paged_write, paged_read (the
+paged cache in the format --kv: attention of one new token for each of --tokens sequences of
+--ctx tokens; writing --ctx tokens of one; reading all back).
 """
 from __future__ import annotations
 
@@ -42,6 +44,7 @@ def main():
     ap.add_argument("--warmup", type=int, default=2)
     ap.add_argument("--ctx", type=int, default=16384)
     ap.add_argument("--tokens", type=int, default=1)
+    ap.add_argument("--kv", choices=("bf16", "fp8", "nvfp4"), default="fp8")
     args = ap.parse_args()
     _build.build()
     dev = "cuda"
@@ -156,6 +159,35 @@ def main():
         ws = torch.empty(B.workspace_bytes(cf, T, ctx + T), dtype=torch.uint8, device=dev)
         fn = lambda: B.beam_attn(cf, q, gg, W["gate_bias"], kc, seq, pos, ctx + T, W["w_o"], out,  # noqa: E731
                                  ws, max_q_per_seq=T)
+    elif c in ("paged_decode", "paged_write", "paged_read"):
+        S, ctx, page = args.tokens, args.ctx, 64
+        cf = B.LayerCfg.from_shape(shape, B.BEAM_ATTN_NOPE_SSMAX)
+        per = -(-ctx // page)
+        table = torch.randperm(S * per, generator=torch.Generator().manual_seed(0))
+        kind = {"bf16": B.BEAM_PAGED_BF16, "fp8": B.BEAM_PAGED_FP8, "nvfp4": B.BEAM_PAGED_NVFP4}
+        cache = B.PagedKVCache.empty(S * per, page, shape.n_kv, shape.head_dim,
+                                     table.view(S, per).to(torch.int32).to(dev), kind[args.kv])
+        k, v = (synth.normal((ctx, shape.n_kv, shape.head_dim), 1.0, 0.0, 0, (x,), dev) for x in "kv")
+        seqs = torch.arange(S, dtype=torch.int32, device=dev)
+        pos = torch.arange(1, ctx + 1, dtype=torch.int32, device=dev)
+        for i in range(S):
+            B.beam_paged_kv_write(k, v, torch.full_like(pos, i), pos, cache)
+        if c == "paged_write":
+            row = torch.zeros_like(pos)
+            fn = lambda: B.beam_paged_kv_write(k, v, row, pos, cache)  # noqa: E731
+        elif c == "paged_read":
+            dims = (S, shape.n_kv, ctx, shape.head_dim)
+            dst = B.KVCache(*(torch.empty(dims, dtype=torch.bfloat16, device=dev) for _ in "kv"))
+            first, last = torch.ones_like(seqs), torch.full_like(seqs, ctx)
+            fn = lambda: B.beam_paged_kv_read(cache, seqs, first, last, ctx, dst)  # noqa: E731
+        else:
+            q = synth.normal((S, shape.n_q, shape.head_dim), 1.0, 0.0, 0, ("q",), dev)
+            gg = synth.activations(S, shape.q_rows, 0, "g", dev)
+            gb = synth.normal((shape.n_q,), 1.0, 0.0, 0, ("gate_bias",), dev)
+            last = torch.full_like(seqs, ctx)
+            out = torch.empty((S, shape.q_rows), dtype=torch.bfloat16, device=dev)
+            ws = torch.empty(B.paged_workspace_bytes(cf, S, ctx), dtype=torch.uint8, device=dev)
+            fn = lambda: B.beam_paged_attn(cf, q, gg, gb, cache, seqs, last, ctx, None, out, ws)  # noqa: E731
     elif c == "route_decode":
         R = synth.router_weights(shape, 3, 0, device=dev)
         u = synth.activations(1, H, 0, "u", dev)
