@@ -53,6 +53,8 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "mma.cuh"
 #include "paged.cuh"
 #include "tcgen05.cuh"
@@ -1220,6 +1222,21 @@ int max_grid() {
   return sms < kMaxGrid ? sms : kMaxGrid;
 }
 
+// The paged_decode_kernel's shared memory, asked for once per device (0.2 us of the ~3.5 of a call).
+// The attribute does not change again, so two threads that ask at once do no harm.
+template <int FMT, int D, int NT>
+cudaError_t allow_smem() {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(paged_decode_kernel<FMT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Cfg<FMT, D, NT>::BYTES);
+  if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
 // pairs: (row, KV head) pairs; blocks: an upper bound of their blocks
 template <int FMT, int D, int NT>
 cudaError_t launch(Params p, int64_t pairs, int64_t blocks, cudaStream_t st) {
@@ -1241,7 +1258,7 @@ cudaError_t launch(Params p, int64_t pairs, int64_t blocks, cudaStream_t st) {
       !encode_tiled(&mv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.v, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   auto kern = paged_decode_kernel<FMT, D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+  cudaError_t e = allow_smem<FMT, D, NT>();
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::BYTES, st, mk, mv, p);
   if (e != cudaSuccess || p.whole) return e;
@@ -1329,11 +1346,13 @@ extern "C" beam_status beam_paged_attn(const beam_layer_cfg* cfg, const beam_bf1
     p.seq_id = seq_id + t0;
     p.pos = pos + t0;
     const int64_t pairs = int64_t(p.T) * cfg->n_kv, blocks = nb * pairs;
-    // Pairs stay in one CTA where its groups can share them out evenly without the join's launch:
-    // where they have a block or two, or at most eight with enough pairs for every SM. Measured,
-    // whole against split: BF16, 16 sequences of 256 keys 8.3 against 9.1 us, 64 of 500 22.2 against
-    // 24.2; but 4 of 500 12.1 against 8.4, FP8, 16 of 1000 13.9 against 11.5.
-    p.whole = nb <= 2 || (nb <= 8 && 5 * pairs >= nb * max_grid());
+    // Pairs stay in one CTA, whose groups share them out, where they have at most four blocks, or
+    // eight with enough pairs for every SM: it saves the join's launch, 1.7 us of the host's time.
+    // Device time measured, whole against split: BF16, 16 sequences of 256 keys (4 blocks) 8.3
+    // against 9.1 us, 64 of 500 (8) 22.2 against 24.2, 1 of 200 (4) 6.7 against 6.4, 4 of 256 7.8 against
+    // 6.7 (a call from the host: 7.8 against 9.4); but 4 of 500 12.1 against 8.4, FP8, 16 of 1000 (8)
+    // 13.9 against 11.5.
+    p.whole = nb <= 4 || (nb <= 8 && 5 * pairs >= nb * max_grid());
     cudaError_t e;
     if (cache->dtype == kFmtBF16) e = launch_fmt<kFmtBF16>(p, pairs, blocks, st);
     else if (cache->dtype == kFmtFP8) e = launch_fmt<kFmtFP8>(p, pairs, blocks, st);
