@@ -3,9 +3,9 @@
 //
 // Both kernels move bytes once and do little with them. Reading back is bounded by HBM (192,000
 // tokens of 8 heads from FP8: 176.5 us, 99% of the copy rate). Writing 16,384 tokens of 8 heads:
-// BF16 21.4 us, FP8 16.1, NVFP4 15.3 with the input in L2 and 21.8 from HBM (59% of the copy rate),
+// BF16 20.3 us, FP8 15.9, NVFP4 15.0 with the input in L2 and 21.8 from HBM (59% of the copy rate),
 // where the quantisation's ~180 warp instructions for 512 elements keep the issue slots 55% busy.
-// A decode step's rows (32 tokens) take 2.5 us, most of it the launch and three dependent loads.
+// A decode step's rows (32 tokens) take 2.3 us, most of it the launch and three dependent loads.
 #include "mma.cuh"
 #include "paged.cuh"
 
@@ -65,7 +65,7 @@ __device__ __forceinline__ float round14(float x) {
 // sixth is 2^-8 of it away (the dividend has 8 bits, 6 midpoints 7).
 constexpr int kHeads = 8;
 template <int FMT, int D>
-__global__ void __launch_bounds__(256, 4) paged_write_kernel(const WriteParams P) {
+__global__ void __launch_bounds__(128, 8) paged_write_kernel(const WriteParams P) {
   pdl_trigger();
   pdl_wait();
   constexpr int EPL = FMT == kFmtBF16 ? 8 : 16, NV = EPL / 8;
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(256) paged_read_kernel(const ReadParams P) {
 template <int FMT, int D>
 cudaError_t launch_write(const WriteParams& p, cudaStream_t st) {
   const int warps = p.T * p.parts;
-  return launch_pdl(paged_write_kernel<FMT, D>, dim3((warps + 7) / 8), dim3(256), 0, st, p);
+  return launch_pdl(paged_write_kernel<FMT, D>, dim3((warps + 3) / 4), dim3(128), 0, st, p);
 }
 template <int FMT, int D>
 cudaError_t launch_read(const ReadParams& p, int N, cudaStream_t st) {
