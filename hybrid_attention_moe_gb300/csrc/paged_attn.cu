@@ -29,8 +29,9 @@
 //  - four consumer warps take one or two slices of 16 keys of every block. More warps with fewer
 //    registers were slower (16 of 96 registers: FP8 370 us against 333, with spills);
 //  - with two groups a finisher warp joins the consumers' partials of a pair while they go on
-//    (330 -> 323 us; windows of 512 keys 37.3 -> 35.2). NVFP4 at head dim 128, bound by arithmetic,
-//    has a third group instead (88.5 -> 82.4 us).
+//    (330 -> 323 us; windows of 512 keys 37.3 -> 35.2). NVFP4 with up to eight heads, bound by
+//    arithmetic, has a third group instead (88.5 -> 82.4 us; head dim 64, 39 sequences of 20,236
+//    tokens, 160 -> 136).
 //
 // Tiles are transposed, so that the query heads of a KV group are the 8-wide N side of mma.sync
 // m16n8k16 (two N tiles for 9 to 16 heads):
@@ -69,7 +70,8 @@ constexpr float kNegInf = -INFINITY;
 constexpr float kLowest = -3e38f;   // a running max that has seen nothing: finite, so differences are
 constexpr float kRescale = 8.f;     // log2 units by which the running max may lag
 constexpr int kMaxGrid = 152;       // CTAs at most
-constexpr int kMaxParts = 3 * kMaxGrid;   // ranges, and so parts of one pair, at most
+constexpr int kMaxGroups = 3;      // groups of a CTA at most
+constexpr int kMaxParts = kMaxGroups * kMaxGrid;   // ranges, and so parts of one pair, at most
 constexpr int kMaxT = 1024;         // rows of one launch
 constexpr int kBias = 7;            // P <= 2^kRescale, times 2^7: below 65504
 
@@ -82,7 +84,7 @@ struct Cfg {
   // blocks and ring of stages: what one group spends on waits and on a pair's end, the other's
   // arithmetic covers
   static constexpr bool HEAVY = FMT == kFmtBF16 ? D == 128 : NT == 2 && D == 128;   // one slice fills it
-  static constexpr int GROUPS = FMT == kFmtNVFP4 && D == 128 && NT == 1 ? 3 : 2;
+  static constexpr int GROUPS = FMT == kFmtNVFP4 && NT == 1 ? 3 : 2;
   static constexpr int WPG = 4, SPW = HEAVY ? 1 : 2;
   static constexpr int NCW = WPG * GROUPS, NCT = WPG * 32;   // consumer warps, threads of a group
   // four more warps: a producer for each group, and with two groups a finisher for each, which
@@ -110,6 +112,7 @@ struct Cfg {
   static constexpr int BAR = JOIN + 3 * 16;
   static constexpr int BYTES = BAR + 2 * NST * 8 + 1024;  // + alignment slack
   static constexpr int ITEMS = (HEADS * (D / 4) + NCT - 1) / NCT;   // 4 outputs that a thread finishes
+  static_assert(GROUPS <= kMaxGroups, "the workspace is sized for kMaxGroups ranges a CTA");
   static_assert(BYTES <= 227 * 1024, "stage ring exceeds shared memory");
   static_assert(NSTG >= 2 && NST <= 12, "one mask word per stage");
 };
@@ -1214,8 +1217,8 @@ int block_keys(int fmt, int D, int nt) {
          : fmt == kFmtFP8 ? block_keys_of<kFmtFP8>(D, nt) : block_keys_of<kFmtNVFP4>(D, nt);
 }
 
-// Rows of partial results: two pairs a range, 8 nt heads each (three ranges a CTA with nt = 1 only).
-size_t part_rows(int nt) { return size_t(nt == 1 ? 3 : 2) * kMaxGrid * 2 * 8 * nt; }
+// Rows of partial results: two pairs a range, 8 nt heads each.
+size_t part_rows(int nt) { return size_t(kMaxParts) * 2 * 8 * nt; }
 
 int max_grid() {
   const int sms = num_sms_cached();
@@ -1285,7 +1288,7 @@ extern "C" size_t beam_paged_workspace_bytes(const beam_layer_cfg* cfg, int T, i
   using namespace beam::paged;
   (void)max_pos;
   if (cfg == nullptr || T <= 0 || cfg->n_q <= 0 || cfg->head_dim <= 0) return 256;
-  const size_t parts = part_rows(1) > part_rows(2) ? part_rows(1) : part_rows(2);
+  const size_t parts = part_rows(2);
   return align_up(parts * cfg->head_dim * 4, 256) + align_up(parts * 2 * 4, 256) +
          align_up(kMaxParts * sizeof(int4), 256) +
          align_up(size_t(T) * cfg->n_q * cfg->head_dim * 2, 256);
