@@ -29,7 +29,9 @@
 //  - four consumer warps take one or two slices of 16 keys of every block. More warps with fewer
 //    registers were slower (16 of 96 registers: FP8 370 us against 333, with spills);
 //  - with two groups a finisher warp joins the consumers' partials of a pair while they go on
-//    (330 -> 323 us; windows of 512 keys 37.3 -> 35.2). NVFP4 with up to eight heads, bound by
+//    (330 -> 323 us; windows of 512 keys 37.3 -> 35.2). It takes four or eight heads at a time, without
+//    a branch or a division between them: 106 sequences of 3 tokens, 8 KV heads of 16 heads each,
+//    27.6 -> 17.1 us, of 5 each 12.4 -> 11.0. NVFP4 with up to eight heads, bound by
 //    arithmetic, has a third group instead (88.5 -> 82.4 us; head dim 64, 39 sequences of 20,236
 //    tokens, 160 -> 136).
 //
@@ -239,18 +241,31 @@ __device__ __forceinline__ int spread(int d) {
   return D == 128 ? d ^ (((d >> 4) & 7) << 2) : d ^ (((d >> 5) & 1) << 2);
 }
 
+// Reciprocals to one unit in FP32's last place, 2^-16 of the rounding to BF16 that follows; a
+// division's slow path would end the overlap of a thread's outputs.
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Factor of a row's outputs whose weights sum to L (0 or at least a half).
+__device__ __forceinline__ float inverse(float L) { return L == 0.f ? 0.f : rcp(L); }
+__device__ __forceinline__ void gate4(float4& o, uint2 g, float bias) {
+  o.x *= rcp(1.f + __expf(-(bf_lo(g.x) + bias)));
+  o.y *= rcp(1.f + __expf(-(bf_hi(g.x) + bias)));
+  o.z *= rcp(1.f + __expf(-(bf_lo(g.y) + bias)));
+  o.w *= rcp(1.f + __expf(-(bf_hi(g.y) + bias)));
+}
+__device__ __forceinline__ uint2 pack4(float4 o) {
+  return make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+}
 // Four neighbouring outputs: normalised, gated, rounded once.
 __device__ __forceinline__ void finish4(bool gated, float4 O, float L, uint2 g, float bias,
                                         uint16_t* out) {
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  float o[4] = {O.x * inv, O.y * inv, O.z * inv, O.w * inv};
-  if (gated) {
-    o[0] *= sigmoidf_(bf_lo(g.x) + bias);
-    o[1] *= sigmoidf_(bf_hi(g.x) + bias);
-    o[2] *= sigmoidf_(bf_lo(g.y) + bias);
-    o[3] *= sigmoidf_(bf_hi(g.y) + bias);
-  }
-  *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+  const float inv = inverse(L);
+  float4 o = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
+  if (gated) gate4(o, g, bias);
+  *reinterpret_cast<uint2*>(out) = pack4(o);
 }
 
 // The state of one warp over its keys of a pair.
@@ -878,24 +893,75 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
         const bool split = a.j0 > 0 || a.j1 < a.nb;
         const size_t o_pair = (size_t(a.t) * P.n_q + a.hk * P.G) * D;
         const size_t pb = size_t(2 * range) * C::HEADS;   // split: the range's first pair
-        constexpr int N = 8;   // outputs whose gates a lane fetches ahead
-#pragma unroll 1
-        for (int x0 = 0; x0 < C::HEADS * (D / 4); x0 += 32 * N) {
-          uint2 gv[N];
-          float gb[N];
+        // A step finishes PER heads, four outputs a lane; lane h holds head h's weights. U steps at a
+        // time without a branch between them, so that one's latencies cover another's.
+        constexpr int PER = 128 / D, N = C::HEADS / PER, U = 4;
+        const int hl = lane % C::HEADS, sub = lane / (D / 4), d = 4 * (lane % (D / 4));
+        const bool gated = P.g != nullptr && !split;
+        uint2 gv[N];   // the gates, ahead of the wait
+        float bias = 0.f;
 #pragma unroll
-          for (int u = 0; u < N; ++u) {
-            const int idx = x0 + 32 * u + lane;
-            if (P.g != nullptr && !split && idx < P.G * (D / 4)) {
-              gv[u] = ld_ahead(P.g + o_pair + 4 * idx);
-              gb[u] = bf2f(ld_ahead16(P.gate_bias + a.hk * P.G + idx / (D / 4)));
+        for (int u = 0; u < N; ++u) gv[u] = make_uint2(0u, 0u);
+        if (gated) {
+          if (hl < P.G) bias = bf2f(ld_ahead16(P.gate_bias + a.hk * P.G + hl));
+#pragma unroll
+          for (int u = 0; u < N; ++u)
+            if (u * PER + sub < P.G) gv[u] = ld_ahead(P.g + o_pair + (u * PER + sub) * D + d);
+        }
+        pair_bar<NCT + 32, true>(grp, 0, buf);
+        const float* Ow = reinterpret_cast<const float*>(sm + C::OW + (grp * C::NOW + buf) * C::OWB);
+        const float2* MLw = reinterpret_cast<const float2*>(sm + C::MLW + (grp * C::NOW + buf) * C::MLB);
+        float M = kLowest, L = 0.f, fw[C::WPG];
+#pragma unroll
+        for (int ww = 0; ww < C::WPG; ++ww) M = fmaxf(M, MLw[ww * C::HEADS + hl].x);
+#pragma unroll
+        for (int ww = 0; ww < C::WPG; ++ww) {
+          const float2 ml = MLw[ww * C::HEADS + hl];
+          fw[ww] = ex2(ml.x - M);
+          L += fw[ww] * ml.y;
+        }
+        const float inv = inverse(L);
+        if (split && lane < P.G) *reinterpret_cast<float2*>(P.part_ml + (pb + lane) * 2) = make_float2(M, L);
+#pragma unroll
+        for (int u0 = 0; u0 < N; u0 += U) {
+          if (u0 * PER >= P.G) break;
+          float4 O[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int h = (u0 + u) * PER + sub;
+            O[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int ww = 0; ww < C::WPG; ++ww) {
+              const float f = __shfl_sync(0xffffffffu, fw[ww], h);
+              const float4 v = *reinterpret_cast<const float4*>(Ow + (ww * C::HEADS + h) * C::OLD + spread<FMT, D>(d));
+              O[u].x += f * v.x;
+              O[u].y += f * v.y;
+              O[u].z += f * v.z;
+              O[u].w += f * v.w;
             }
           }
-          if (x0 == 0) pair_bar<NCT + 32, true>(grp, 0, buf);
+          if (split) {
 #pragma unroll
-          for (int u = 0; u < N; ++u) {
-            const int idx = x0 + 32 * u + lane;
-            if (idx < P.G * (D / 4)) join_warps<FMT, C>(P, sm, grp * C::NOW + buf, idx, split, pb, o_pair, gv[u], gb[u]);
+            for (int u = 0; u < U; ++u) {
+              const int h = (u0 + u) * PER + sub;
+              if (h < P.G) *reinterpret_cast<float4*>(P.part_acc + (pb + h) * D + d) = O[u];
+            }
+            continue;
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const float f = __shfl_sync(0xffffffffu, inv, (u0 + u) * PER + sub);
+            O[u] = make_float4(O[u].x * f, O[u].y * f, O[u].z * f, O[u].w * f);
+          }
+          if (gated) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              gate4(O[u], gv[u0 + u], __shfl_sync(0xffffffffu, bias, (u0 + u) * PER + sub));
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int h = (u0 + u) * PER + sub;
+            if (h < P.G) *reinterpret_cast<uint2*>(P.og + o_pair + h * D + d) = pack4(O[u]);
           }
         }
         pair_bar<NCT + 32, false>(grp, 1, buf);
