@@ -10,7 +10,7 @@
 // values over long contexts: 128 sequences of 17 to 16,385 tokens in FP8 323 us, 99% of the copy
 // rate; one of 100,001 in BF16 66.7 us, 91%, the rest being the start (1.6 us of plan, 0.9 us of page
 // lookups) and the join (3 us). Over an NVFP4 cache the arithmetic: 4 sequences of 60,000 to
-// 100,001 tokens 82.4 us, 67%: about 345 warp instructions for 16 keys of one KV head, 128 of them
+// 100,001 tokens 80.4 us, 69%: about 345 warp instructions for 16 keys of one KV head, 128 of them
 // the conversions and the scaling of the codes, which keep the issue slots 64% and the integer
 // pipe 59% busy.
 //
@@ -31,9 +31,9 @@
 //  - with two groups a finisher warp joins the consumers' partials of a pair while they go on
 //    (330 -> 323 us; windows of 512 keys 37.3 -> 35.2). It takes four or eight heads at a time, without
 //    a branch or a division between them: 106 sequences of 3 tokens, 8 KV heads of 16 heads each,
-//    27.6 -> 17.1 us, of 5 each 12.4 -> 11.0. NVFP4 with up to eight heads, bound by
-//    arithmetic, has a third group instead (88.5 -> 82.4 us; head dim 64, 39 sequences of 20,236
-//    tokens, 160 -> 136).
+//    27.6 -> 17.1 us, of 5 each 12.4 -> 11.0. NVFP4, bound by arithmetic, has
+//    a third group instead (4 sequences of 60,000 to 100,001 tokens 88.5 -> 82.4 us; head dim 64, 39
+//    of 20,236, 160 -> 136), but for 9 to 16 heads at head dim 64 (199 -> 207).
 //
 // Tiles are transposed, so that the query heads of a KV group are the 8-wide N side of mma.sync
 // m16n8k16 (two N tiles for 9 to 16 heads):
@@ -86,7 +86,11 @@ struct Cfg {
   // blocks and ring of stages: what one group spends on waits and on a pair's end, the other's
   // arithmetic covers
   static constexpr bool HEAVY = FMT == kFmtBF16 ? D == 128 : NT == 2 && D == 128;   // one slice fills it
-  static constexpr int GROUPS = FMT == kFmtNVFP4 && NT == 1 ? 3 : 2;
+  static constexpr int GROUPS = FMT == kFmtNVFP4 && (D == 128 || NT == 1) ? 3 : 2;
+  // q fragments in shared memory, where the registers that would hold them (16 or 32) are short:
+  // 39 sequences of 20,236 tokens, 8 KV heads of 16 heads: FP8 313 -> 276 us, NVFP4 346 (with two
+  // groups) -> 292; of 8 heads, NVFP4 184 -> 180
+  static constexpr bool QSM = FMT != kFmtBF16 && D == 128;
   static constexpr int WPG = 4, SPW = HEAVY ? 1 : 2;
   static constexpr int NCW = WPG * GROUPS, NCT = WPG * 32;   // consumer warps, threads of a group
   // four more warps: a producer for each group, and with two groups a finisher for each, which
@@ -102,12 +106,15 @@ struct Cfg {
   static constexpr int STAGE = (OQ + QB + 1023) / 1024 * 1024;
   static constexpr int OLD = D + 4;   // row stride of the combine buffer (floats)
   static constexpr int OWB = WPG * HEADS * OLD * 4, MLB = WPG * HEADS * 2 * 4;   // of one group
+  // with a finisher no barrier lies between a pair's last read of them and the next pair's write
+  static constexpr int QBUFS = FIN ? 2 : 1, QFB = QSM ? GROUPS * QBUFS * QB : 0;
   static constexpr int NOW = GROUPS < 3 && 4 * STAGE + 2 * GROUPS * (OWB + MLB) <= 216 * 1024 ? 2 : 1;
-  static constexpr int FIT = (216 * 1024 - NOW * GROUPS * (OWB + MLB)) / STAGE;
+  static constexpr int FIT = (216 * 1024 - NOW * GROUPS * (OWB + MLB) - QFB) / STAGE;
   static constexpr int NSTG = FIT / GROUPS > 4 ? 4 : FIT / GROUPS, NST = NSTG * GROUPS;   // stages of a group
   static constexpr int OW = NST * STAGE;                  // [GROUPS][NOW][WPG][HEADS][OLD]: O partials
   static constexpr int MLW = OW + GROUPS * NOW * OWB;     // [GROUPS][NOW][WPG][HEADS][2]: (m, l)
-  static constexpr int CUM = MLW + GROUPS * NOW * MLB;    // [kMaxT + 1] block prefix
+  static constexpr int QF = MLW + GROUPS * NOW * MLB;     // [GROUPS][QBUFS][NT][D / 16][32 lanes] 8 bytes
+  static constexpr int CUM = QF + QFB;    // [kMaxT + 1] block prefix
   static constexpr int POS = CUM + (kMaxT + 1) * 4;       // [kMaxT] positions
   static constexpr int MISC = (POS + kMaxT * 4 + 15) / 16 * 16;   // -, abort, -, -; masks
   static constexpr int JOIN = MISC + 16 + 12 * 4;         // [GROUPS] pairs that begin in a group's range
@@ -309,10 +316,10 @@ __device__ __forceinline__ Lane<FMT, C> lane_of(int slice, int pse) {
 
 // One warp's slices (SPW of 16 keys, WPG slices apart) of a staged block. kb: the stage; kbase:
 // position of the first slice's first key; live: bit i, slice i has keys; the row's keys are
-// positions [lo, p]. qs: FP32 factor of the logits per accumulator column.
+// positions [lo, p]. q: fragments qb, or (QSM) at qf. qs: FP32 factor of the logits per accumulator column.
 template <int FMT, class C>
 __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)[C::SPW],
-                                           const uint32_t (&qb)[C::NT][C::D / 16][2],
+                                           const uint32_t (&qb)[C::NT][C::D / 16][2], uint32_t qf,
                                            const float (&qs)[C::NT][2], int kbase, unsigned live,
                                            int lo, int p, WarpState<C>& S) {
   constexpr int D = C::D, NT = C::NT, KK = D / 16, SPW = C::SPW, GAP = 16 * C::WPG;
@@ -341,6 +348,15 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
     } else {
       // a thread's codes of keys g and g + 8: the d range [c D/4, (c + 1) D/4), four of a k step
       constexpr int KW = C::ROWB / 16;   // words of a key in one thread
+      auto mma_q = [&](int n, int kk, const uint32_t (&a)[4]) {
+        if constexpr (C::QSM) {
+          uint32_t b[2];
+          lds<2>(qf + (n * KK + kk) * 256, b);
+          mma_f16(sx[i][n], a, b[0], b[1]);
+        } else {
+          mma_f16(sx[i][n], a, qb[n][kk][0], qb[n][kk][1]);
+        }
+      };
       uint32_t w0[KW], w1[KW];
       if constexpr (KW == 8) {
         lds<4>(kb + ln[i].k[0], w0);
@@ -358,7 +374,7 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
           e4m3x4_f16(w0[kk], a[0], a[2]);
           e4m3x4_f16(w1[kk], a[1], a[3]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(sx[i][n], a, qb[n][kk][0], qb[n][kk][1]);
+          for (int n = 0; n < NT; ++n) mma_q(n, kk, a);
         }
       } else {
         // block scales of the thread's d range: two blocks (D 128) or one (D 64)
@@ -387,7 +403,7 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
             const uint32_t a[4] = {mul_f16x2(h0[2 * e], b0), mul_f16x2(h1[2 * e], b1),
                                    mul_f16x2(h0[2 * e + 1], b0), mul_f16x2(h1[2 * e + 1], b1)};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(sx[i][n], a, qb[n][2 * j + e][0], qb[n][2 * j + e][1]);
+            for (int n = 0; n < NT; ++n) mma_q(n, 2 * j + e, a);
           }
         }
       }
@@ -974,6 +990,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
     Lane<FMT, C> ln[C::SPW];
 #pragma unroll
     for (int e = 0; e < C::SPW; ++e) ln[e] = lane_of<FMT, C>(w + e * C::WPG, min(P.c.page_size, BK));
+    const uint32_t qf = sbase + C::QF + grp * C::QBUFS * C::QB + lane * 8;
     bool dead = false;   // a wait has expired: the rest of the range passes without results
     const int G = P.G;
     int i = 0, buf = 0, pairs = 0;
@@ -998,7 +1015,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
         }
       };
       const bool mine = !C::FIN || at.f_pair + j1 >= f_hi;   // no finisher, or the range's last pair
-      if (!C::FIN) fetch_gate();
+      if (!C::FIN && !C::QSM) fetch_gate();
+      const int q_buf = C::QBUFS == 2 ? pairs & 1 : 0;
       uint32_t qb[NT][D / 16][2];
       float qs[NT][2];
       WarpState<C> S;
@@ -1051,11 +1069,19 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
 #pragma unroll
                   for (int e = 0; e < 2; ++e)
                     qb[n][kk][e] = pack_f16x2(bf_lo(qb[n][kk][e]) * up, bf_hi(qb[n][kk][e]) * up);
+                if constexpr (C::QSM) {   // each warp writes a part of what all hold
+                  uint8_t* dst = sm + C::QF + (grp * C::QBUFS + q_buf) * C::QB + n * D * 16 + lane * 8;
+#pragma unroll
+                  for (int kk = 0; kk < D / 16; ++kk)
+                    if (kk % C::WPG == w)
+                      *reinterpret_cast<uint2*>(dst + kk * 256) = make_uint2(qb[n][kk][0], qb[n][kk][1]);
+                }
                 const float back = P.sl2 * pow2_of(unsigned(254 - me));
                 qs[n][0] = __shfl_sync(0xffffffffu, back, 8 * c);
                 qs[n][1] = __shfl_sync(0xffffffffu, back, 8 * c + 4);
               }
             }
+            if constexpr (C::QSM) consumer_bar<NCT>(grp);   // once a pair and warp, live or dead
           }
           const int kbase = BK * (blk0 + j) + 16 * w + 1;
           unsigned live = 0;
@@ -1064,15 +1090,18 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
             const int k0 = kbase + 16 * C::WPG * e;
             if (((masks[st] >> (w + e * C::WPG)) & 1u) && k0 <= p && k0 + 15 >= lo) live |= 1u << e;
           }
-          if (live) warp_block<FMT, C>(kb, ln, qb, qs, kbase, live, lo, p, S);
-        } else if (lane == 0) {
-          misc[1] = 1;
+          if (live) warp_block<FMT, C>(kb, ln, qb, qf + q_buf * C::QB, qs, kbase, live, lo, p, S);
+        } else {
+          if constexpr (C::QSM) {
+            if (j == j0) consumer_bar<NCT>(grp);
+          }
+          if (lane == 0) misc[1] = 1;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_empty + 8 * st);
       }
       // ---- the warp's partial of the pair, into a buffer that its last reader has left
-      if (C::FIN && mine) fetch_gate();
+      if (mine && (C::FIN || C::QSM)) fetch_gate();
       if constexpr (C::FIN) {
         if (pairs >= C::NOW) pair_bar<NCT + 32, true>(grp, 1, buf);
       } else if constexpr (C::NOW == 1) {
