@@ -87,7 +87,8 @@ class BeamStack:
             dims = (n, self.shape.n_kv, cap, self.shape.head_dim)
             k, v = (torch.empty(dims, dtype=torch.bfloat16, device=self.device) for _ in "kv")
             copy = self._copies[(n, W)] = B.KVCache(k, v, window=W)
-        known = (seq_id >= 0) & (seq_id < n)      # the others are flagged by the library
+        # other tokens are flagged by the library, and reach into no sequence's range
+        known = (seq_id >= 0) & (seq_id < n) & (pos >= 1) & (pos <= max_pos)
         s = torch.where(known, seq_id, 0).long()
         last = torch.zeros(n, dtype=torch.int32, device=pos.device)
         last.scatter_reduce_(0, s, torch.where(known, pos, 0), "amax")

@@ -164,3 +164,19 @@ def test_captured_decode_step_equals_the_eager_one():
     assert status() == 0
     for x, y in zip(*runs):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("bad", [(0, 0), (1, -3), (-1, 5), (SEQS, 5)])
+def test_a_bad_token_of_a_chunk_leaves_the_others_as_they_are(bad):
+    """(sequence, position) of a token that the library flags, last of a chunk: the other tokens'
+    results are those beside a good one of a third sequence."""
+    W = weights()
+    runs = []
+    for last in ((2, 18), bad):
+        st = BeamStack(TINY, W, paged_caches("fp8"))
+        prefill(st)
+        seq, pos = [1] * 30 + [0] * 30 + [last[0]], list(range(34, 64)) + list(range(50, 80)) + [last[1]]
+        e, s, p = tokens(seq, pos, 7)
+        runs.append(st.forward(e, s, p, max(pos), max_q_per_seq=30)[:60].clone())
+        assert bool(status()) == (last is bad)
+    assert torch.equal(*runs)

@@ -262,3 +262,23 @@ def test_stack_takes_paged_layers(monkeypatch):
     # sequence ids that name nothing do not reach the ranges
     names, args = forward([-1, 99] + [1] * 5, [50, 60, 3, 4, 5, 6, 7], 5)
     assert args["beam_paged_kv_read"][3].tolist() == [0, 7, 0, 0]
+
+
+@pytest.mark.parametrize("bad", [(0, 0), (2, 0), (2, -7), (0, 39), (0, 10 ** 6), (-1, 3), (4, 3)])
+@pytest.mark.parametrize("windowed", [False, True])
+def test_context_of_a_chunk_with_a_bad_token(bad, windowed):
+    """The ranges that a paged prefill reads back do not depend on tokens that the library flags."""
+    from hybrid_attention_moe_gb300 import beam as B
+    from hybrid_attention_moe_gb300 import stack as S
+    st = object.__new__(S.BeamStack)
+    st.shape, st.device, st._copies = synth.TINY, "cpu", {}
+    kc = object.__new__(B.PagedKVCache)
+    kc.page_table, kc.window = torch.zeros((4, 5), dtype=torch.int32), synth.TINY.window if windowed else 0
+    seq, pos, n, most = [2] * 9 + [0] * 6, list(range(30, 39)) + list(range(1, 7)), 9, 38
+
+    def ranges(seq, pos):
+        s, p = (torch.tensor(x, dtype=torch.int32) for x in (seq, pos))
+        _, every, first, last, longest = st.context(kc, s, p, most, n)
+        return every.tolist(), first.tolist(), last.tolist(), longest
+
+    assert ranges(seq + [bad[0]], pos + [bad[1]]) == ranges(seq, pos)
