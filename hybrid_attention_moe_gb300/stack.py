@@ -109,7 +109,9 @@ class BeamStack:
             return
         T = seq_id.shape[0]
         max_q = T if max_q_per_seq is None else max_q_per_seq
-        stage, rows, k, v = self.stage(T)
+        # buffers that a later call may drop belong to the stream that uses them
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            stage, rows, k, v = self.stage(T)
         B.beam_qkv_gate(cfg, b["u"], W["w_qkvg"], W["q_norm"], W["k_norm"], rows, pos, b["q"],
                         b["g"], stage, ws, stream)
         B.beam_paged_kv_write(k, v, seq_id, pos, kc, stream)

@@ -180,3 +180,18 @@ def test_a_bad_token_of_a_chunk_leaves_the_others_as_they_are(bad):
         runs.append(st.forward(e, s, p, max(pos), max_q_per_seq=30)[:60].clone())
         assert bool(status()) == (last is bad)
     assert torch.equal(*runs)
+
+
+def test_paged_buffers_belong_to_the_stream_of_the_call():
+    st = BeamStack(TINY, weights(), paged_caches("fp8"))
+    side, seen = torch.cuda.Stream(), []
+    for name in ("stage", "context"):
+        def wrapped(*a, _f=getattr(st, name)):
+            seen.append(torch.cuda.current_stream())
+            return _f(*a)
+        setattr(st, name, wrapped)
+    e, s, p = tokens([0] * 9, list(range(1, 10)), 3)
+    torch.cuda.synchronize()
+    st.forward(e, s, p, 9, stream=side, max_q_per_seq=9)
+    torch.cuda.synchronize()
+    assert len(seen) == 2 * TINY.n_layers and all(x == side for x in seen)
