@@ -660,3 +660,21 @@ def test_bindings_refuse_wrong_tensors():
     with pytest.raises(B.BeamError):
         B.beam_paged_kv_read(c, seq, ints([1]), pos, 20, B.KVCache(dst.k.view(torch.uint8), dst.v.view(torch.uint8)))
     assert status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("G", [5, 16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_over_every_range(fmt, G, D):
+    """More blocks than there are ranges on any GB300, so that every range writes partials: within
+    a workspace of exactly the size asked for."""
+    cfg, lens = cfg_for(8 * G, 8, D), [4000, 2500, 1900]
+    c, *_ = make_cache(fmt, 8, D, 32, lens, 31)
+    q, seq, pos = randn(33, 3, 8 * G, D), ints([2, 0, 1]), ints([1900, 4000, 2500])
+    need = B.paged_workspace_bytes(cfg, 3, 4000)
+    buf = torch.full((need + 65536,), 0x5A, dtype=torch.uint8, device=DEV)
+    out = torch.full((3, 8 * G * D), 7.0, dtype=torch.bfloat16, device=DEV)
+    B.beam_paged_attn(cfg, q, None, None, c, seq, pos, 4000, None, out, buf[:need])
+    assert status() == 0
+    check_attn(cfg, c, q, seq, pos, out)
+    assert bool((buf[need:] == 0x5A).all())
