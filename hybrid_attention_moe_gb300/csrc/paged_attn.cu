@@ -1049,32 +1049,32 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
                 }
                 qs[n][0] = qs[n][1] = P.sl2;
               } else {
-                unsigned mx = 0;   // the head's largest magnitude, as a bf16 pattern
+                unsigned mx = 0;   // the head's largest magnitude, as a bf16 pattern (at first two)
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                   lds<2>(qa + (D / 8) * c * 4 + kk * 8, qb[n][kk]);
 #pragma unroll
                   for (int e = 0; e < 2; ++e) {
                     if (!rok) qb[n][kk][e] = 0u;
-                    mx = max(mx, max(qb[n][kk][e] & 0x7FFFu, (qb[n][kk][e] >> 16) & 0x7FFFu));
+                    mx = __vmaxu2(mx, qb[n][kk][e] & 0x7FFF7FFFu);
                   }
                 }
+                mx = max(mx & 0xFFFFu, mx >> 16);
                 mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 // q * 2^(me - 127): the largest magnitude lies in [2^14, 2^15)
                 const int me = min(254, 268 - int(mx >> 7));
                 const float up = __uint_as_float(unsigned(me) << 23);
+                // QSM: each warp writes its part of what all read
+                uint8_t* dst = sm + C::QF + (grp * C::QBUFS + q_buf) * C::QB + n * D * 16 + lane * 8;
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  if (C::QSM && kk % C::WPG != w) continue;
 #pragma unroll
                   for (int e = 0; e < 2; ++e)
                     qb[n][kk][e] = pack_f16x2(bf_lo(qb[n][kk][e]) * up, bf_hi(qb[n][kk][e]) * up);
-                if constexpr (C::QSM) {   // each warp writes a part of what all hold
-                  uint8_t* dst = sm + C::QF + (grp * C::QBUFS + q_buf) * C::QB + n * D * 16 + lane * 8;
-#pragma unroll
-                  for (int kk = 0; kk < D / 16; ++kk)
-                    if (kk % C::WPG == w)
-                      *reinterpret_cast<uint2*>(dst + kk * 256) = make_uint2(qb[n][kk][0], qb[n][kk][1]);
+                  if constexpr (C::QSM)
+                    *reinterpret_cast<uint2*>(dst + kk * 256) = make_uint2(qb[n][kk][0], qb[n][kk][1]);
                 }
                 const float back = P.sl2 * pow2_of(unsigned(254 - me));
                 qs[n][0] = __shfl_sync(0xffffffffu, back, 8 * c);
