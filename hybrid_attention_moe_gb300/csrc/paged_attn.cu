@@ -87,10 +87,10 @@ struct Cfg {
   // arithmetic covers
   static constexpr bool HEAVY = FMT == kFmtBF16 ? D == 128 : NT == 2 && D == 128;   // one slice fills it
   static constexpr int GROUPS = FMT == kFmtNVFP4 && (D == 128 || NT == 1) ? 3 : 2;
-  // q fragments in shared memory, where the registers that would hold them (16 or 32) are short:
-  // 39 sequences of 20,236 tokens, 8 KV heads of 16 heads: FP8 313 -> 276 us, NVFP4 346 (with two
-  // groups) -> 292; of 8 heads, NVFP4 184 -> 180
-  static constexpr bool QSM = FMT != kFmtBF16 && D == 128;
+  // over quantised caches q's fragments lie in shared memory, not in 8 to 32 registers: 39 sequences
+  // of 20,236 tokens, 8 KV heads of 16 heads: FP8 313 -> 276 us, NVFP4 346 (with two groups) -> 292;
+  // of 8 heads, NVFP4 184 -> 180, 64-wide 136 -> 132
+  static constexpr bool QSM = FMT != kFmtBF16;
   static constexpr int WPG = 4, SPW = HEAVY ? 1 : 2;
   static constexpr int NCW = WPG * GROUPS, NCT = WPG * 32;   // consumer warps, threads of a group
   // four more warps: a producer for each group, and with two groups a finisher for each, which
@@ -316,7 +316,7 @@ __device__ __forceinline__ Lane<FMT, C> lane_of(int slice, int pse) {
 
 // One warp's slices (SPW of 16 keys, WPG slices apart) of a staged block. kb: the stage; kbase:
 // position of the first slice's first key; live: bit i, slice i has keys; the row's keys are
-// positions [lo, p]. q: fragments qb, or (QSM) at qf. qs: FP32 factor of the logits per accumulator column.
+// positions [lo, p]. q: fragments qb (BF16) or at qf. qs: FP32 factor of the logits per accumulator column.
 template <int FMT, class C>
 __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)[C::SPW],
                                            const uint32_t (&qb)[C::NT][C::D / 16][2], uint32_t qf,
@@ -349,13 +349,9 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
       // a thread's codes of keys g and g + 8: the d range [c D/4, (c + 1) D/4), four of a k step
       constexpr int KW = C::ROWB / 16;   // words of a key in one thread
       auto mma_q = [&](int n, int kk, const uint32_t (&a)[4]) {
-        if constexpr (C::QSM) {
-          uint32_t b[2];
-          lds<2>(qf + (n * KK + kk) * 256, b);
-          mma_f16(sx[i][n], a, b[0], b[1]);
-        } else {
-          mma_f16(sx[i][n], a, qb[n][kk][0], qb[n][kk][1]);
-        }
+        uint32_t b[2];
+        lds<2>(qf + (n * KK + kk) * 256, b);
+        mma_f16(sx[i][n], a, b[0], b[1]);
       };
       uint32_t w0[KW], w1[KW];
       if constexpr (KW == 8) {
@@ -1015,7 +1011,6 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
         }
       };
       const bool mine = !C::FIN || at.f_pair + j1 >= f_hi;   // no finisher, or the range's last pair
-      if (!C::FIN && !C::QSM) fetch_gate();
       const int q_buf = C::QBUFS == 2 ? pairs & 1 : 0;
       uint32_t qb[NT][D / 16][2];
       float qs[NT][2];
@@ -1065,16 +1060,15 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
                 // q * 2^(me - 127): the largest magnitude lies in [2^14, 2^15)
                 const int me = min(254, 268 - int(mx >> 7));
                 const float up = __uint_as_float(unsigned(me) << 23);
-                // QSM: each warp writes its part of what all read
+                // each warp writes its part of what all read
                 uint8_t* dst = sm + C::QF + (grp * C::QBUFS + q_buf) * C::QB + n * D * 16 + lane * 8;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                  if (C::QSM && kk % C::WPG != w) continue;
+                  if (kk % C::WPG != w) continue;
 #pragma unroll
                   for (int e = 0; e < 2; ++e)
                     qb[n][kk][e] = pack_f16x2(bf_lo(qb[n][kk][e]) * up, bf_hi(qb[n][kk][e]) * up);
-                  if constexpr (C::QSM)
-                    *reinterpret_cast<uint2*>(dst + kk * 256) = make_uint2(qb[n][kk][0], qb[n][kk][1]);
+                  *reinterpret_cast<uint2*>(dst + kk * 256) = make_uint2(qb[n][kk][0], qb[n][kk][1]);
                 }
                 const float back = P.sl2 * pow2_of(unsigned(254 - me));
                 qs[n][0] = __shfl_sync(0xffffffffu, back, 8 * c);
@@ -1101,7 +1095,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
         if (lane == 0) mbar_arrive(bar_empty + 8 * st);
       }
       // ---- the warp's partial of the pair, into a buffer that its last reader has left
-      if (mine && (C::FIN || C::QSM)) fetch_gate();
+      if (mine) fetch_gate();
       if constexpr (C::FIN) {
         if (pairs >= C::NOW) pair_bar<NCT + 32, true>(grp, 1, buf);
       } else if constexpr (C::NOW == 1) {
