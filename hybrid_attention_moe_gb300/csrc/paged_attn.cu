@@ -45,10 +45,12 @@
 // half (16 bits). Over FP8 and NVFP4 the codes become f16 in registers, exactly (e2m1 times its
 // e4m3 block scale has 6 significant bits), and P is rounded once to f16: its half step, 2^-11 of a
 // weight, is far below the cache's own (2^-4 and 2^-2), and the low half cost a third of the
-// arithmetic. The rows' powers of two never enter an f16 value: K's multiplies the FP32 logits;
-// V's goes into P relative to the largest one that the warp has seen (E), as p * 2^(e - E + 7), so
-// that P's largest values lie near the top of f16 and rows of smaller values keep their bits. q is
-// scaled by a power of two per head in the same manner. The d axis is permuted the same way in q
+// arithmetic. The rows' powers of two never enter an f16 value: K's multiplies the FP32 logits x;
+// V's (2^e) goes into P = 2^(x + e - Z + 7), where Z is a second running max, that of x + e. So P's
+// largest values lie near the top of f16 whatever the scales are, a row of large values that
+// weighs nothing takes no bits from the others, and what P loses below f16's smallest step is at
+// most 2^-32 of the largest weighted scale for each key. q is scaled by a power of two per head in
+// the same manner. The d axis is permuted the same way in q
 // and K, and undone on the output for V, so that a thread's codes are contiguous bytes.
 //
 // Every mbarrier wait is bounded: on expiry the CTA records BEAM_DEV_TIMEOUT, stops issuing, lets
@@ -92,6 +94,8 @@ struct Cfg {
   // of 8 heads, NVFP4 184 -> 180, 64-wide 136 -> 132
   static constexpr bool QSM = FMT != kFmtBF16;
   static constexpr int WPG = 4, SPW = HEAVY ? 1 : 2;
+  // log2 units by which a reference may lag: P <= 2^(kRescale + kBias) in f16, below 65504
+  static constexpr float LAG = FMT == kFmtBF16 ? kRescale : kRescale + kBias;
   static constexpr int NCW = WPG * GROUPS, NCT = WPG * 32;   // consumer warps, threads of a group
   // four more warps: a producer for each group, and with two groups a finisher for each, which
   // joins the consumer warps' partials of a pair while they take the next one
@@ -279,8 +283,10 @@ __device__ __forceinline__ void finish4(bool gated, float4 O, float L, uint2 g, 
 template <class C>
 struct WarpState {
   float m[C::NT][2], l[C::NT][2];   // running max (lags by up to kRescale) and sum, heads 2c, 2c+1
+  // quantised caches: acc holds sums of 2^x v relative to 2^z, z = the running max (lagging in the
+  // same manner) of x + e, e the value rows' exponents, less kBias
+  float z[C::NT][2];
   float acc[C::NT][C::D / 16][4];
-  int E;   // quantised caches: the largest scale byte of a value row so far
 };
 
 // Offsets in a stage that a lane uses for every block.
@@ -405,12 +411,12 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
       }
     }
   }
-  // ---- y = logit - running max, in log2 units. Whether any exceeds it by kRescale (or a value
-  // row's scale the largest so far) is one vote; the max itself is taken across the warp only then.
+  // ---- y = x - m: log2 of a key's weight, x its logit in log2 units. Over a quantised cache also
+  // z = x + e - Z: log2 of its weight times its value row's scale 2^e. Whether any exceeds its
+  // reference is one vote; the references themselves are taken across the warp only then.
   int ev[SPW][2];        // scale bytes of the value rows (quantised caches)
   float fk[SPW][2];      // scales of the key rows
-  float y[SPW][NT][4];
-  float most = kNegInf;
+  float y[SPW][NT][4], z[SPW][NT][4];
   int top = 0;
 #pragma unroll
   for (int i = 0; i < SPW; ++i) {
@@ -424,11 +430,6 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
       fk[i][0] = bf_lo(f2);
       fk[i][1] = bf_hi(f2);
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        y[i][n][e] = fmaf(sx[i][n][e], FMT == kFmtBF16 ? qs[n][e & 1] : qs[n][e & 1] * fk[i][e >> 1], -S.m[n][e & 1]);
   }
   if (!full) {   // keys that are not the row's weigh nothing, whatever their slots hold
 #pragma unroll
@@ -437,72 +438,81 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
       for (int h = 0; h < 2; ++h) {
         if (valid(i, g + 8 * h)) continue;
         ev[i][h] = 0;
+        fk[i][h] = 1.f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) y[i][n][2 * h] = y[i][n][2 * h + 1] = kNegInf;
+        for (int n = 0; n < NT; ++n) sx[i][n][2 * h] = sx[i][n][2 * h + 1] = kNegInf;
       }
   }
+  auto factor = [&](int i, int n, int e) {   // of a product, to x
+    return FMT == kFmtBF16 ? qs[n][e & 1] : qs[n][e & 1] * fk[i][e >> 1];
+  };
+  auto weigh = [&] {
+#pragma unroll
+    for (int i = 0; i < SPW; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float f = factor(i, n, e);
+          y[i][n][e] = fmaf(sx[i][n][e], f, -S.m[n][e & 1]);
+          if constexpr (FMT != kFmtBF16)
+            z[i][n][e] = fmaf(sx[i][n][e], f, float(ev[i][e >> 1] - 127) - S.z[n][e & 1]);
+        }
+  };
+  weigh();
+  float most = kNegInf;
 #pragma unroll
   for (int i = 0; i < SPW; ++i) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-      most = fmaxf(most, fmaxf(fmaxf(y[i][n][0], y[i][n][1]), fmaxf(y[i][n][2], y[i][n][3])));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        most = fmaxf(most, y[i][n][e]);
+        if constexpr (FMT != kFmtBF16) most = fmaxf(most, z[i][n][e]);
+      }
     if constexpr (FMT != kFmtBF16) top = max(top, max(ev[i][0], ev[i][1]));
   }
-  bool over = most > kRescale;
-  if constexpr (FMT != kFmtBF16) over |= top > S.E;
+  bool over = most > C::LAG;
+  if constexpr (FMT != kFmtBF16) over |= top == 255;
   if (__any_sync(0xffffffffu, over)) {
-    float unit = 1.f;   // the accumulators hold values relative to 2^E
     if constexpr (FMT != kFmtBF16) {
-      top = S.E;
 #pragma unroll
       for (int i = 0; i < SPW; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (ev[i][h] != 255) {
-            top = max(top, ev[i][h]);
-          } else {   // a row that holds no numbers: neither does what reads it
+          if (ev[i][h] != 255) continue;   // else a row that holds no numbers: neither does what reads it
 #pragma unroll
-            for (int n = 0; n < NT; ++n) y[i][n][2 * h] = y[i][n][2 * h + 1] = __uint_as_float(0x7FFFFFFFu);
-          }
+          for (int n = 0; n < NT; ++n) sx[i][n][2 * h] = sx[i][n][2 * h + 1] = __uint_as_float(0x7FFFFFFFu);
         }
-      top = __reduce_max_sync(0xffffffffu, top);
-      unit = ex2(float(S.E - top));
-      S.E = top;
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float cr[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float up = 0.f;   // how far the max rises; from the lowest value it starts at, y is the logit
-        float old = S.m[n][h];
-        if (old == kLowest) {   // nothing seen so far: the logits themselves
-          up = kLowest;
-          old = 0.f;
+        float m = S.m[n][h], zz = FMT == kFmtBF16 ? 0.f : S.z[n][h] + kBias;
 #pragma unroll
-          for (int i = 0; i < SPW; ++i)
+        for (int i = 0; i < SPW; ++i)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              float& v = y[i][n][2 * r + h];
-              if (v != kNegInf && v == v)
-                v = sx[i][n][2 * r + h] * (FMT == kFmtBF16 ? qs[n][h] : qs[n][h] * fk[i][r]);
-            }
+          for (int r = 0; r < 2; ++r) {
+            const float x = sx[i][n][2 * r + h] * factor(i, n, 2 * r + h);
+            m = fmaxf(m, x);
+            if constexpr (FMT != kFmtBF16) zz = fmaxf(zz, x + float(ev[i][r] - 127));
+          }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          if constexpr (FMT != kFmtBF16) zz = fmaxf(zz, __shfl_xor_sync(0xffffffffu, zz, o));
         }
-#pragma unroll
-        for (int i = 0; i < SPW; ++i) up = fmaxf(up, fmaxf(y[i][n][h], y[i][n][2 + h]));
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
-        const float now = old + up;
-        up = now - old;   // as rounded: what follows is relative to the new max
-        cr[h] = S.m[n][h] == kLowest ? 0.f : ex2(-up);
-        S.m[n][h] = now;
-        S.l[n][h] *= cr[h];
-#pragma unroll
-        for (int i = 0; i < SPW; ++i) {
-          y[i][n][h] -= up;
-          y[i][n][2 + h] -= up;
+        const float cm = ex2(S.m[n][h] - m);   // 0 at the first numbers seen
+        S.m[n][h] = m;
+        S.l[n][h] *= cm;
+        cr[h] = cm;
+        if constexpr (FMT != kFmtBF16) {
+          zz -= kBias;
+          cr[h] = ex2(S.z[n][h] - zz);
+          S.z[n][h] = zz;
         }
-        cr[h] *= unit;
       }
 #pragma unroll
       for (int mt = 0; mt < KK; ++mt) {
@@ -512,6 +522,7 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
         S.acc[n][mt][3] *= cr[1];
       }
     }
+    weigh();
   }
   // ---- P, then its transpose as the B fragments of P^T: b[0] = (keys 2c, 2c+1; head g),
   // b[1] = (keys 2c+8, 2c+9; head g). BF16: P in a high and a low half.
@@ -519,12 +530,6 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
   uint32_t pb[SPW][NT][PH][2];
 #pragma unroll
   for (int i = 0; i < SPW; ++i) {
-    float vs[2] = {1.f, 1.f};
-    if constexpr (FMT != kFmtBF16) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)   // 2^(e - E + kBias), 0 below FP32's normal range
-        vs[h] = __uint_as_float(unsigned(max(ev[i][h] - S.E + 127 + kBias, 0)) << 23);
-    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float w[4];
@@ -539,8 +544,8 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
         pb[i][n][PH - 1][0] = movtrans(pack_bf16x2(w[0] - bf_lo(h01), w[1] - bf_hi(h01)));
         pb[i][n][PH - 1][1] = movtrans(pack_bf16x2(w[2] - bf_lo(h23), w[3] - bf_hi(h23)));
       } else {
-        pb[i][n][0][0] = movtrans(pack_f16x2(w[0] * vs[0], w[1] * vs[0]));
-        pb[i][n][0][1] = movtrans(pack_f16x2(w[2] * vs[1], w[3] * vs[1]));
+        pb[i][n][0][0] = movtrans(pack_f16x2(ex2(z[i][n][0]), ex2(z[i][n][1])));
+        pb[i][n][0][1] = movtrans(pack_f16x2(ex2(z[i][n][2]), ex2(z[i][n][3])));
       }
     }
   }
@@ -1015,10 +1020,9 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
       uint32_t qb[NT][D / 16][2];
       float qs[NT][2];
       WarpState<C> S;
-      S.E = 0;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        S.m[n][0] = S.m[n][1] = kLowest;
+        S.m[n][0] = S.m[n][1] = S.z[n][0] = S.z[n][1] = kLowest;
         S.l[n][0] = S.l[n][1] = 0.f;
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt) S.acc[n][mt][0] = S.acc[n][mt][1] = S.acc[n][mt][2] = S.acc[n][mt][3] = 0.f;
@@ -1103,8 +1107,6 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
       }
       float* Ow = reinterpret_cast<float*>(sm + C::OW + (grp * C::NOW + buf) * C::OWB);
       float2* MLw = reinterpret_cast<float2*>(sm + C::MLW + (grp * C::NOW + buf) * C::MLB);
-      // 2^(E - 127 - kBias)
-      const float unit = __uint_as_float(S.E > kBias ? unsigned(S.E - kBias) << 23 : 0x00800000u >> (kBias + 1 - S.E));
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -1114,6 +1116,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
         }
         const int h0 = w * C::HEADS + 8 * n + 2 * c;
         float* ow = Ow + h0 * C::OLD;
+        // acc relative to 2^m, as l is: 2^(z - m) in two steps, which alone may leave FP32's range
+        const float u0 = ex2(0.5f * (S.z[n][0] - S.m[n][0])), u1 = ex2(0.5f * (S.z[n][1] - S.m[n][1]));
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt) {
           const float(&a)[4] = S.acc[n][mt];
@@ -1124,8 +1128,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::THREADS, 1) paged_decode_kern
             ow[C::OLD + 16 * mt + g + 8] = a[3];
           } else {   // neighbours
             const int d = spread<FMT, D>(D / 8 * g + 2 * mt);
-            *reinterpret_cast<float2*>(ow + d) = make_float2(a[0] * unit, a[2] * unit);
-            *reinterpret_cast<float2*>(ow + C::OLD + d) = make_float2(a[1] * unit, a[3] * unit);
+            *reinterpret_cast<float2*>(ow + d) = make_float2(a[0] * u0 * u0, a[2] * u0 * u0);
+            *reinterpret_cast<float2*>(ow + C::OLD + d) = make_float2(a[1] * u1 * u1, a[3] * u1 * u1);
           }
         }
         if (g == 0) {
