@@ -222,6 +222,13 @@ class PagedKVCache:
     The tensors are checked once, here, and must not be replaced afterwards (their contents may
     change, the page table's among them)."""
 
+    page_size = 256   # the largest; a cache holds its own
+
+    @property
+    def positions(self):
+        """Positions that a sequence's row of the page table reaches."""
+        return self.page_table.shape[1] * self.page_size
+
     def __init__(self, k, v, page_table, row_scale=None, block_scale=None, window=0):
         if k.dim() != 4 or page_table.dim() != 2:
             raise BeamError("PagedKVCache: k and v are [num_pages][n_kv][page_size][...], "

@@ -78,6 +78,7 @@ class BeamStack:
         longest), one row per sequence of the page table. Sequences without tokens in the call
         read nothing. Layers of one window share the cache."""
         n, W = kc.page_table.shape[0], kc.window
+        max_pos = min(max_pos, kc.positions)
         longest = max_pos if W == 0 else min(max_pos, W - 1 + max_q)
         # a ring's capacity is a multiple of the attention's key tiles
         cap = longest if W == 0 else (W - 1 + max_q + 127) // 128 * 128
@@ -120,6 +121,10 @@ class BeamStack:
                               W["w_o"], b["a"], ws, stream)
             return
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            # a token past the table was flagged by the write; beam_attn shares key tiles between a
+            # sequence's tokens, and must not take it for the sequence's end
+            max_pos = min(max_pos, kc.positions)
+            pos = pos.masked_fill(pos > max_pos, 0)
             copy, every, first, last, longest = self.context(kc, seq_id, pos, max_pos, max_q)
         B.beam_paged_kv_read(kc, every, first, last, longest, copy, stream)
         B.beam_attn(cfg, b["q"], b["g"], W["gate_bias"], copy, seq_id, pos, max_pos, W["w_o"],
