@@ -222,7 +222,7 @@ class PagedKVCache:
     The tensors are checked once, here, and must not be replaced afterwards (their contents may
     change, the page table's among them)."""
 
-    page_size = 256   # the largest; a cache holds its own
+    page_size, num_pages = 256, 2 ** 31 - 1   # the largest; a cache holds its own
 
     @property
     def positions(self):
@@ -254,7 +254,7 @@ class PagedKVCache:
             raise BeamError("PagedKVCache: the tensors must be on a CUDA device")
         self.k, self.v, self.page_table = k, v, page_table
         self.row_scale, self.block_scale, self.window = row_scale, block_scale, int(window)
-        self.n_kv, self.page_size, self.head_dim = n_kv, size, width
+        self.num_pages, self.n_kv, self.page_size, self.head_dim = pages, n_kv, size, width
         self.device = dev
         self._c = PagedKVC(k.data_ptr(), v.data_ptr(),
                            0 if row_scale is None else row_scale.data_ptr(),

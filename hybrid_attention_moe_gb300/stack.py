@@ -34,6 +34,8 @@ class BeamStack:
              it into the pages (beam_paged_kv_write), and attends with beam_paged_attn up to
              PAGED_MAX_Q tokens per sequence; with more it reads the sequences' context back
              into a contiguous BF16 cache (beam_paged_kv_read) that beam_attn's prefill takes.
+             There a token with a key in a bad page attends to nothing (beam_paged_attn leaves
+             that key out); both set BEAM_DEV_BAD_PAGE.
     """
 
     # A call's tokens of one sequence each read their keys in beam_paged_attn; the way through a
@@ -99,6 +101,19 @@ class BeamStack:
         first = torch.where(last > 0, first, 1)
         return copy, torch.arange(n, dtype=torch.int32, device=pos.device), first, last, longest
 
+    def readable(self, kc, seq_id, pos, first, last, longest):
+        """pos, with 0 (attends to nothing) for tokens some of whose keys beam_paged_kv_read does
+        not bring: one lies in a page that is none, or the sequence's tokens lie further apart
+        than the copy reaches. Either is flagged by the read; the copy holds something else there."""
+        table, size = kc.page_table, kc.page_size
+        s = seq_id.clamp(0, table.shape[0] - 1).long()
+        none = ((table < 0) | (table >= kc.num_pages)).cumsum(1)       # up to each page
+        lo = (pos - kc.window).clamp_min(0) if kc.window else torch.zeros_like(pos)
+        a, b = lo // size, (pos - 1).clamp_min(0) // size              # pages of a token's keys
+        before = torch.where(a > 0, none[s, (a - 1).clamp_min(0).long()], 0)
+        whole = (none[s, b.long()] == before) & ((last - first)[s] < longest)
+        return torch.where(whole, pos, 0)
+
     def attention(self, i, b, seq_id, pos, max_pos, ws, stream, max_q_per_seq):
         """Projection, cache write and attention of the i-th layer held, from b["u"] to b["a"]."""
         W, cfg, kc = self.W[i], self.cfgs[i], self.caches[i]
@@ -126,6 +141,7 @@ class BeamStack:
             max_pos = min(max_pos, kc.positions)
             pos = pos.masked_fill(pos > max_pos, 0)
             copy, every, first, last, longest = self.context(kc, seq_id, pos, max_pos, max_q)
+            pos = self.readable(kc, seq_id, pos, first, last, longest)
         B.beam_paged_kv_read(kc, every, first, last, longest, copy, stream)
         B.beam_attn(cfg, b["q"], b["g"], W["gate_bias"], copy, seq_id, pos, max_pos, W["w_o"],
                     b["a"], ws, stream, max_q_per_seq)

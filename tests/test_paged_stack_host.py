@@ -36,3 +36,24 @@ def test_context_leaves_tokens_past_the_page_table_out(window, bad):
         return every.tolist(), first.tolist(), last.tolist(), longest
 
     assert ranges(seq + [2], pos + [bad]) == ranges(seq, pos)
+
+
+@pytest.mark.parametrize("window", [0, 20])
+def test_tokens_with_keys_that_are_not_read_attend_to_nothing(window):
+    """readable() against the definition: every key of the token in a page of the pool, and the
+    sequence's range within the copy."""
+    st, kc = stack(), paged(rows=3, pages=6, page_size=16, window=window)
+    kc.num_pages = 9
+    kc.page_table.copy_(ints([[0, 1, 2, 3, 4, 5], [6, -1, 7, 8, 0, 1], [2, 3, 9, 4, 5, 6]]))
+    seq = [s for s in range(3) for _ in range(97)]
+    pos = [p for _ in range(3) for p in range(97)]
+    first, last = ints([1, 1, 1]), ints([96, 96, 96])
+    got = st.readable(kc, ints(seq + [-1, 3]), ints(pos + [0, 0]), first, last, 96).tolist()
+    for s, p, g in zip(seq, pos, got):
+        keys = range(max(1, p - window + 1) if window else 1, p + 1)
+        ok = all(0 <= int(kc.page_table[s, (k - 1) // 16]) < 9 for k in keys)
+        assert g == (p if ok else 0), (s, p)
+    assert got[-2:] == [0, 0]
+    # a range longer than the copy is not read at all: sequence 0's tokens attend to nothing
+    got = st.readable(kc, ints([0, 0, 1]), ints([1, 96, 9]), ints([1, 1, 1]), ints([96, 9, 0]), 90).tolist()
+    assert got == [0, 0, 9]
