@@ -42,6 +42,10 @@ class BeamStack:
     # contiguous copy writes and reads them in BF16 once more, whatever the tokens' number.
     PAGED_MAX_Q = 4
 
+    # A context copy larger than this is worth a wait for the exact number of its sequences: the
+    # read and the attention of so many keys take milliseconds.
+    COPY_BYTES = 1 << 30
+
     def __init__(self, shape, weights, caches, first_layer=0, n_layers=None, device="cuda"):
         """weights[i] / caches[i] belong to global layer first_layer + i of an n_layers-deep
         stack (n_layers defaults to shape.n_layers); the layer index fixes the attention
@@ -75,46 +79,91 @@ class BeamStack:
             self._stage = {T: s}
         return s
 
-    def context(self, kc, seq_id, pos, max_pos, max_q):
+    def context(self, kc, seq_id, pos, max_pos, max_q, n_seqs=None):
         """What a paged layer's prefill reads: (contiguous cache, its sequences, first, last,
-        longest), one row per sequence of the page table. Sequences without tokens in the call
-        read nothing. Layers of one window share the cache."""
-        n, W = kc.page_table.shape[0], kc.window
+        longest), one row for each of the n_seqs sequences at most that have tokens in the call, in
+        their order, or for every sequence of the page table where that is no more. Rows without a
+        sequence read nothing. Layers of one window share the cache."""
+        n, W, dev = kc.page_table.shape[0], kc.window, pos.device
+        rows = n if n_seqs is None else max(1, min(n, n_seqs))
         max_pos = min(max_pos, kc.positions)
         longest = max_pos if W == 0 else min(max_pos, W - 1 + max_q)
         # a ring's capacity is a multiple of the attention's key tiles
         cap = longest if W == 0 else (W - 1 + max_q + 127) // 128 * 128
-        copy = self._copies.get((n, W))
-        if copy is None or copy.k.shape[2] != cap:
-            self._copies.pop((n, W), None)
-            dims = (n, self.shape.n_kv, cap, self.shape.head_dim)
+        held = [key for key in self._copies if key[1] == W]   # one copy for a window
+        copy = self._copies[held[0]] if held else None
+        if copy is None or copy.k.shape[0] < rows or copy.k.shape[2] < cap:
+            for key in held:
+                del self._copies[key]
+            if copy is not None and W == 0 and copy.k.shape[2] < cap:
+                cap = min(cap + cap // 4, kc.positions)   # a context that grew will grow with the next chunk
+            dims = (rows, self.shape.n_kv, cap, self.shape.head_dim)
             k, v = (torch.empty(dims, dtype=torch.bfloat16, device=self.device) for _ in "kv")
-            copy = self._copies[(n, W)] = B.KVCache(k, v, window=W)
+            copy = self._copies[(rows, W)] = B.KVCache(k, v, window=W)
         # other tokens are flagged by the library, and reach into no sequence's range
         known = (seq_id >= 0) & (seq_id < n) & (pos >= 1) & (pos <= max_pos)
         s = torch.where(known, seq_id, 0).long()
-        last = torch.zeros(n, dtype=torch.int32, device=pos.device)
+        last = torch.zeros(n, dtype=torch.int32, device=dev)
         last.scatter_reduce_(0, s, torch.where(known, pos, 0), "amax")
         first = torch.full_like(last, 2 ** 31 - 1)
         first.scatter_reduce_(0, s, torch.where(known, pos, 2 ** 31 - 1), "amin")
+        every = torch.arange(n, dtype=torch.int32, device=dev)
+        if rows < n:
+            # row r: the r-th sequence with tokens, or nothing where there are fewer
+            at = (last > 0).cumsum(0) - 1
+            at = torch.where((last > 0) & (at < rows), at, rows)
+            every = torch.full((rows + 1,), -1, dtype=torch.int32, device=dev).scatter_(0, at, every)[:rows]
+            s = every.clamp_min(0).long()
+            first, last = first[s], torch.where(every < 0, 0, last[s])
+            every = every.clamp_min(0)
         first = (first - W + 1).clamp_min(1) if W else torch.ones_like(last)
         first = torch.where(last > 0, first, 1)
-        return copy, torch.arange(n, dtype=torch.int32, device=pos.device), first, last, longest
+        return copy, every, first, last, longest
 
-    def readable(self, kc, seq_id, pos, first, last, longest):
-        """pos, with 0 (attends to nothing) for tokens some of whose keys beam_paged_kv_read does
-        not bring: one lies in a page that is none, or the sequence's tokens lie further apart
-        than the copy reaches. Either is flagged by the read; the copy holds something else there."""
+    def rows(self, kc, seq_id, pos, every, first, last):
+        """Each token's row of the copy (sequences `every`): its sequence's, any for a token at position
+        0 of a sequence without one, else an id that is none."""
+        n = kc.page_table.shape[0]
+        if every.shape[0] == n:
+            return seq_id
+        at = torch.full((n + 1,), -1, dtype=torch.int32, device=pos.device)
+        order = torch.arange(every.shape[0], dtype=torch.int32, device=pos.device)
+        at.scatter_(0, torch.where(last > 0, every, n).long(), order)
+        known = (seq_id >= 0) & (seq_id < n)
+        row = torch.where(known, at[torch.where(known, seq_id, 0).long()], -1)
+        return torch.where(known & (pos == 0) & (row < 0), 0, row)
+
+    def readable(self, kc, row, pos, first, last, longest, every=None):
+        """pos of tokens that read the ranges `row` (of sequences `every`; None: the table's), with 0
+        (attends to nothing) for tokens some of whose keys beam_paged_kv_read does not bring: one
+        lies in a page that is none, or the sequence's tokens lie further apart than the copy
+        reaches. Either is flagged by the read; the copy holds something else there."""
         table, size = kc.page_table, kc.page_size
-        s = seq_id.clamp(0, table.shape[0] - 1).long()
-        none = ((table < 0) | (table >= kc.num_pages)).cumsum(1)       # up to each page
+        if every is not None and every.shape[0] < table.shape[0]:
+            table = table[every.long()]
+        s = row.clamp(0, table.shape[0] - 1).long()
+        none = ((table < 0) | (table >= kc.num_pages)).cumsum(1, dtype=torch.int32)   # up to each page
         lo = (pos - kc.window).clamp_min(0) if kc.window else torch.zeros_like(pos)
         a, b = lo // size, (pos - 1).clamp_min(0) // size              # pages of a token's keys
         before = torch.where(a > 0, none[s, (a - 1).clamp_min(0).long()], 0)
         whole = (none[s, b.long()] == before) & ((last - first)[s] < longest)
         return torch.where(whole, pos, 0)
 
-    def attention(self, i, b, seq_id, pos, max_pos, ws, stream, max_q_per_seq):
+    def count(self, seq_id, max_pos, stream):
+        """The number of sequences in a call that does not say it, where every sequence that there
+        could be would make a large copy: one wait for the GPU. None where it would not, and under
+        a capture, which cannot wait."""
+        row = 4 * self.shape.n_kv * self.shape.head_dim
+        most = max((min(c.page_table.shape[0], seq_id.shape[0]) * min(max_pos, c.positions) * row
+                    for c in self.caches if isinstance(c, B.PagedKVCache) and c.window == 0), default=0)
+        if most <= self.COPY_BYTES:
+            return None
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            if torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
+                return None
+            return seq_id.unique().numel()
+
+    def attention(self, i, b, seq_id, pos, max_pos, ws, stream, max_q_per_seq, n_seqs=None):
         """Projection, cache write and attention of the i-th layer held, from b["u"] to b["a"]."""
         W, cfg, kc = self.W[i], self.cfgs[i], self.caches[i]
         if not isinstance(kc, B.PagedKVCache):
@@ -140,10 +189,12 @@ class BeamStack:
             # sequence's tokens, and must not take it for the sequence's end
             max_pos = min(max_pos, kc.positions)
             pos = pos.masked_fill(pos > max_pos, 0)
-            copy, every, first, last, longest = self.context(kc, seq_id, pos, max_pos, max_q)
-            pos = self.readable(kc, seq_id, pos, first, last, longest)
+            most = T if n_seqs is None else min(T, n_seqs)
+            copy, every, first, last, longest = self.context(kc, seq_id, pos, max_pos, max_q, most)
+            row = self.rows(kc, seq_id, pos, every, first, last)
+            pos = self.readable(kc, row, pos, first, last, longest, every)
         B.beam_paged_kv_read(kc, every, first, last, longest, copy, stream)
-        B.beam_attn(cfg, b["q"], b["g"], W["gate_bias"], copy, seq_id, pos, max_pos, W["w_o"],
+        B.beam_attn(cfg, b["q"], b["g"], W["gate_bias"], copy, row, pos, max_pos, W["w_o"],
                     b["a"], ws, stream, max_q_per_seq)
 
     def buffers(self, T):
@@ -165,7 +216,8 @@ class BeamStack:
             self._bufs = {T: b}
         return b
 
-    def layer(self, i, b, seq_id, pos, max_pos, ws, stream=None, trace=None, max_q_per_seq=None):
+    def layer(self, i, b, seq_id, pos, max_pos, ws, stream=None, trace=None, max_q_per_seq=None,
+              n_seqs=None):
         """The i-th layer held (global index l): from (h, u = its attention pre-norm) to
         (h, u of the next layer). With a trace list, appends the layer's intermediate tensors:
         u_attn, q, g, attn, h_mid (h after the attention residual), mlp_in, mlp, route
@@ -174,7 +226,7 @@ class BeamStack:
         l = self.ids[i]
         if trace is not None:
             trace.append({"u_attn": b["u"].clone()})
-        self.attention(i, b, seq_id, pos, max_pos, ws, stream, max_q_per_seq)
+        self.attention(i, b, seq_id, pos, max_pos, ws, stream, max_q_per_seq, n_seqs)
         B.beam_boundary_norm(b["a"], b["h"], b["u"], W["attn_post"], W["mlp_pre"], 2 * l + 2,
                              cfg.eps, stream)
         if trace is not None:
@@ -202,12 +254,19 @@ class BeamStack:
         if trace is not None:
             trace[-1]["h"] = b["h"].clone()
 
-    def forward(self, e, seq_id, pos, max_pos, stream=None, trace=None, max_q_per_seq=None):
+    def forward(self, e, seq_id, pos, max_pos, stream=None, trace=None, max_q_per_seq=None,
+                n_seqs=None):
         """Runs the held layers for the tokens (seq_id, pos). e [T][H] (bf16) is the residual
         stream entering the first held layer (the embedding when first_layer is 0); it gets
         its pre-norm first. max_q_per_seq: most tokens of one sequence (1 for a decode batch;
-        None = T). Returns h after the last residual addition (an internal buffer)."""
+        None = T). n_seqs: upper bound of the number of sequences with tokens in the call, which
+        sizes the context copies of a prefill over paged caches (tokens of sequences past it are
+        flagged as of a bad sequence). None: at most T, counted, with one wait for the GPU, where
+        that many would take more than COPY_BYTES (not in a captured call: say it there).
+        Returns h after the last residual addition (an internal buffer)."""
         T = e.shape[0]
+        if self.paged and n_seqs is None and (T if max_q_per_seq is None else max_q_per_seq) > self.PAGED_MAX_Q:
+            n_seqs = self.count(seq_id, max_pos, stream)
         b = self.buffers(T)
         need = B.workspace_bytes(self.cfgs[0], T, max_pos)
         if self.paged:
@@ -217,5 +276,5 @@ class BeamStack:
         B.beam_boundary_norm(None, b["h"], b["u"], None, self.W[0]["attn_pre"], 1,
                              self.cfgs[0].eps, stream)
         for i in range(self.L):
-            self.layer(i, b, seq_id, pos, max_pos, ws, stream, trace, max_q_per_seq)
+            self.layer(i, b, seq_id, pos, max_pos, ws, stream, trace, max_q_per_seq, n_seqs)
         return b["h"]

@@ -7,7 +7,7 @@ from synth import TINY
 from hybrid_attention_moe_gb300 import beam as B
 from hybrid_attention_moe_gb300.stack import BeamStack
 from test_gpu_paged import status
-from test_gpu_paged_stack import PAGE, PAGES, SEQS, paged_caches, prefill, tokens, weights
+from test_gpu_paged_stack import CHUNKS, PAGE, PAGES, SEQS, paged_caches, prefill, tokens, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +74,64 @@ def test_tokens_of_a_sequence_too_far_apart_attend_to_nothing():
     layer = next(i for i, c in enumerate(caches) if c.window)
     assert not runs[1][layer]["attn"][:5].any()
     assert torch.equal(runs[0][layer]["attn"][5:], runs[1][layer]["attn"][5:])
+
+
+ROWS = {0: 35, 1: 2, 2: 17}      # where the small table's sequences lie in the large one
+
+
+def large(caches, rows=40):
+    """The same caches under a table of many sequences, the others' entries naming no page."""
+    table = torch.full((rows, PAGES), -1, dtype=torch.int32, device="cuda")
+    for small, s in ROWS.items():
+        table[s] = caches[0].page_table[small]
+    return [B.PagedKVCache(c.k, c.v, table, c.row_scale, c.block_scale, c.window) for c in caches]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("n_seqs", [None, 2, 7])
+def test_prefill_out_of_a_large_table(fmt, n_seqs):
+    """Chunks of two sequences out of a table of 40 give the bits of a table of three, then a decode
+    step over what they wrote does; the copies have rows for the call's sequences only."""
+    W = weights()
+    a, b = BeamStack(TINY, W, paged_caches(fmt)), BeamStack(TINY, W, large(paged_caches(fmt)))
+    for n, (seq, pos, most) in enumerate(CHUNKS + [([0, 1, 2], [50, 34, 18], 1)]):
+        e, s, p = tokens(seq, pos, n)
+        x = a.forward(e, s, p, max(pos), max_q_per_seq=most)
+        y = b.forward(e, torch.tensor([ROWS[i] for i in seq], dtype=torch.int32, device="cuda"), p, max(pos),
+                      max_q_per_seq=most, n_seqs=n_seqs)
+        assert torch.equal(x, y)
+    assert status() == 0
+    assert {k[0] for k in b._copies} == {40 if n_seqs is None else n_seqs}
+
+
+def test_more_sequences_than_were_said_are_flagged():
+    """n_seqs = 1 with two sequences: the first is served, the other's tokens attend to nothing."""
+    W = weights()
+    seq, pos, most = CHUNKS[0]
+    e, s, p = tokens(seq, pos, 0)
+    runs = []
+    for n_seqs in (2, 1):
+        trace = []
+        BeamStack(TINY, W, paged_caches("fp8")).forward(e, s, p, max(pos), trace=trace, max_q_per_seq=most, n_seqs=n_seqs)
+        assert status() == (0 if n_seqs == 2 else B.DEV_BAD_SEQ)
+        runs.append(trace[0]["attn"])
+    assert torch.equal(runs[0][:40], runs[1][:40]) and not runs[1][40:].any()
+
+
+def test_prefill_of_one_sequence_takes_the_memory_of_one():
+    """One sequence out of a table of 512 that reaches 102,400 positions, and a bound as high."""
+    W = weights()
+    table = torch.full((512, 3200), -1, dtype=torch.int32, device="cuda")
+    table[300, :PAGES] = torch.arange(PAGES)
+    st = BeamStack(TINY, W, [B.PagedKVCache.empty(PAGES, PAGE, TINY.n_kv, TINY.head_dim, table, B.BEAM_PAGED_FP8, c.window)
+                             for c in paged_caches("fp8")])
+    e, s, p = tokens([300] * 100, list(range(1, 101)), 3)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    got = st.forward(e, s, p, 102400)
+    assert status() == 0
+    # one row of keys and values of both kinds of layer, and less than 256 MiB for all else
+    assert torch.cuda.max_memory_allocated() - before < 102400 * TINY.n_kv * TINY.head_dim * 4 + (256 << 20)
+    ref = BeamStack(TINY, W, paged_caches("fp8"))
+    assert torch.equal(got, ref.forward(e, torch.zeros_like(s), p, 100))

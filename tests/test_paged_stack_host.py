@@ -57,3 +57,69 @@ def test_tokens_with_keys_that_are_not_read_attend_to_nothing(window):
     # a range longer than the copy is not read at all: sequence 0's tokens attend to nothing
     got = st.readable(kc, ints([0, 0, 1]), ints([1, 96, 9]), ints([1, 1, 1]), ints([96, 9, 0]), 90).tolist()
     assert got == [0, 0, 9]
+
+
+@pytest.mark.parametrize("window", [0, TINY.window])
+@pytest.mark.parametrize("n_seqs", [None, 2, 3, 50])
+def test_context_has_rows_for_the_call_only(window, n_seqs):
+    """A table of 50 sequences, two of which have tokens in the call: the copy holds n_seqs rows, whose
+    ranges are those of the full table's, and every token finds its sequence's row."""
+    kc = paged(rows=50, pages=8, window=window)
+    seq, pos = [47] * 9 + [-1, 50, 3] + [11] * 6, list(range(30, 39)) + [5, 6, 0] + list(range(1, 7))
+    full = stack().context(kc, ints(seq), ints(pos), 60, 9)
+    copy, every, first, last, longest = got = stack().context(kc, ints(seq), ints(pos), 60, 9, n_seqs)
+    assert copy.k.shape[0] == copy.v.shape[0] == every.numel() == (n_seqs or 50) and longest == full[4]
+    assert copy.k.shape[2:] == full[0].k.shape[2:]
+    row = stack().rows(kc, ints(seq), ints(pos), every, first, last)
+    for t, s in enumerate(seq):
+        r = int(row[t])
+        if s in (47, 11):
+            assert int(every[r]) == s and int(first[r]) == int(full[2][s]) and int(last[r]) == int(full[3][s])
+        elif 0 <= s < 50:
+            assert 0 <= r < every.numel()            # position 0: any row, flagged for the position
+        else:
+            assert not 0 <= r < every.numel()        # flagged for the sequence
+    reads = [int(every[r]) for r in range(every.numel()) if int(last[r]) >= int(first[r])]
+    assert sorted(reads) == [11, 47]
+    p = stack().readable(kc, row, ints(pos), first, last, longest, every)
+    assert p.tolist() == pos
+    assert got[0].k.dtype == torch.bfloat16
+
+
+def test_context_of_more_sequences_than_were_said():
+    """The first n_seqs sequences are served, the others' tokens name no row."""
+    kc = paged(rows=9, pages=8)
+    seq, pos = ints([7, 7, 2, 4, 4]), ints([1, 2, 9, 5, 6])
+    copy, every, first, last, _ = stack().context(kc, seq, pos, 60, 5, 2)
+    row = stack().rows(kc, seq, pos, every, first, last)
+    assert every.tolist() == [2, 4] and last.tolist() == [9, 6] and row.tolist() == [-1, -1, 0, 1, 1]
+
+
+def test_the_copy_grows_and_is_kept():
+    """One copy for a window: kept for calls that fit in it, a quarter larger than asked where a
+    context has outgrown it, never longer than the page table."""
+    st, kc = stack(), paged(rows=50, pages=100)
+    seq, pos = ints([3] * 6), ints(list(range(1, 7)))
+
+    def cap(max_pos, n=1):
+        c = st.context(kc, seq, pos, max_pos, 6, n)[0]
+        assert len(st._copies) == 1 and next(iter(st._copies.values())) is c
+        return tuple(c.k.shape[::2])
+    assert cap(200) == (1, 200) and cap(100) == (1, 200)
+    assert cap(400) == (1, 500) and cap(500) == (1, 500)
+    assert cap(1590) == (1, 1600) and cap(5000) == (1, 1600)
+    assert cap(100, 2) == (2, 100) and cap(100, 1) == (2, 100)
+    st.context(paged(rows=50, pages=100, window=16), seq, pos, 300, 6, 1)
+    assert len(st._copies) == 2
+
+
+def test_the_sequences_of_a_large_call_are_counted():
+    """A call that does not say how many sequences it has: counted where T rows would take more
+    than COPY_BYTES, else not."""
+    seq = ints([3, 3, 90, 3] * 30)
+    st = stack([paged(rows=128, pages=6400), paged(rows=128, pages=6400, window=16)])
+    assert st.count(seq, 102400, None) == 2
+    assert st.count(seq, 1024, None) is None
+    assert stack([paged(rows=128, pages=6400, window=16)]).count(seq, 102400, None) is None
+    copy = st.context(st.caches[0], seq, ints([1] * 120), 102400, 5, 2)[0]
+    assert copy.k.nbytes + copy.v.nbytes == 2 * 102400 * TINY.n_kv * TINY.head_dim * 4
