@@ -282,16 +282,25 @@ class PagedKVCache:
                    torch.zeros(dims, dtype=kind, device=dev), page_table, row, block, window)
 
 
+def capturing():
+    """Whether the current stream's work goes into a CUDA graph, which keeps its addresses."""
+    return torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
+
+
 class Workspace:
-    """Device scratch for the library calls, grown on demand (256-byte aligned)."""
+    """Device scratch for the library calls, grown on demand (256-byte aligned). A buffer that a
+    captured call got stays allocated for its replays when a larger one takes its place."""
 
     def __init__(self, device="cuda"):
         self.device = device
         self.buf = None
+        self.held = []
 
     def get(self, nbytes):
         if self.buf is None or self.buf.numel() < nbytes:
             self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+        if capturing() and all(self.buf is not x for x in self.held):
+            self.held.append(self.buf)
         return self.buf
 
 

@@ -36,6 +36,11 @@ class BeamStack:
              into a contiguous BF16 cache (beam_paged_kv_read) that beam_attn's prefill takes.
              There a token with a key in a bad page attends to nothing (beam_paged_attn leaves
              that key out); both set BEAM_DEV_BAD_PAGE.
+
+    Buffers between calls: those of the last number of tokens, one workspace, and one context copy
+    for each window. What a captured call uses stays allocated as long as the stack, whatever
+    calls come between its replays. All calls and replays of a stack share these buffers, so they
+    run one after the other.
     """
 
     # A call's tokens of one sequence each read their keys in beam_paged_attn; the way through a
@@ -66,7 +71,18 @@ class BeamStack:
         self._bufs = {}
         self._stage = {}
         self._copies = {}
+        self._held = []
         self.paged = any(isinstance(c, B.PagedKVCache) for c in caches)
+
+    def hold(self, x):
+        """x, which a replay of the call being captured, if there is one, will use again."""
+        if B.capturing() and all(x is not y for y in self._held):
+            self._held.append(x)
+        return x
+
+    def held(self, buffers):
+        """The entries of a dict of buffers that captured calls use."""
+        return {k: x for k, x in buffers.items() if any(x is y for y in self._held)}
 
     def stage(self, T):
         """A row per token for the projection's K and V: a ring of one slot per "sequence"."""
@@ -76,8 +92,8 @@ class BeamStack:
             k, v = (torch.empty(dims, dtype=torch.bfloat16, device=self.device) for _ in "kv")
             rows = torch.arange(T, dtype=torch.int32, device=self.device)
             s = (B.KVCache(k, v, window=1), rows, k.view(T, *dims[1::2]), v.view(T, *dims[1::2]))
-            self._stage = {T: s}
-        return s
+            self._stage = {**self.held(self._stage), T: s}
+        return self.hold(s)
 
     def context(self, kc, seq_id, pos, max_pos, max_q, n_seqs=None):
         """What a paged layer's prefill reads: (contiguous cache, its sequences, first, last,
@@ -118,7 +134,7 @@ class BeamStack:
             every = every.clamp_min(0)
         first = (first - W + 1).clamp_min(1) if W else torch.ones_like(last)
         first = torch.where(last > 0, first, 1)
-        return copy, every, first, last, longest
+        return self.hold(copy), every, first, last, longest
 
     def rows(self, kc, seq_id, pos, every, first, last):
         """Each token's row of the copy (sequences `every`): its sequence's, any for a token at position
@@ -159,7 +175,7 @@ class BeamStack:
         if most <= self.COPY_BYTES:
             return None
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
-            if torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
+            if B.capturing():
                 return None
             return seq_id.unique().numel()
 
@@ -213,8 +229,8 @@ class BeamStack:
                 "idx": torch.empty((T, s.topk), dtype=torch.int32, device=dev),
                 "w": torch.empty((T, s.topk), dtype=torch.float32, device=dev),
             }
-            self._bufs = {T: b}
-        return b
+            self._bufs = {**self.held(self._bufs), T: b}
+        return self.hold(b)
 
     def layer(self, i, b, seq_id, pos, max_pos, ws, stream=None, trace=None, max_q_per_seq=None,
               n_seqs=None):

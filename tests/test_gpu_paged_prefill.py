@@ -135,3 +135,72 @@ def test_prefill_of_one_sequence_takes_the_memory_of_one():
     assert torch.cuda.max_memory_allocated() - before < 102400 * TINY.n_kv * TINY.head_dim * 4 + (256 << 20)
     ref = BeamStack(TINY, W, paged_caches("fp8"))
     assert torch.equal(got, ref.forward(e, torch.zeros_like(s), p, 100))
+
+
+def test_replays_after_prefills_of_other_sizes():
+    """A server's order: a decode step captured, a longer prefill chunk (other buffers, a larger
+    workspace, a larger copy) between its replays, memory handed out again in between. The replays
+    give the eager steps' bits and write no one else's memory."""
+    W = weights()
+    outs = []
+    for captured in (False, True):
+        st = BeamStack(TINY, W, paged_caches("nvfp4"))
+        prefill(st)
+        e, s, p = tokens([0, 1, 2], [50, 34, 18], 10)
+        args = dict(max_q_per_seq=1)
+        if captured:
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                h = st.forward(e, s, p, 64, **args)
+        out, junk = [], []
+        for n in range(3):
+            ce, cs, cp = tokens([0] * (40 + 7 * n), [60 + 35 * n + i for i in range(40 + 7 * n)], 30 + n)
+            st.forward(ce, cs, cp, PAGE * PAGES, max_q_per_seq=40 + 7 * n, n_seqs=1)
+            junk += [torch.full((2 ** i,), 77, dtype=torch.uint8, device="cuda") for i in range(9, 23)]
+            e2, s2, p2 = tokens([0, 1, 2], [51 + n, 34 + n, 18 + n], 20 + n)
+            for x, y in ((e, e2), (s, s2), (p, p2)):
+                x.copy_(y)
+            if captured:
+                graph.replay()
+            else:
+                h = st.forward(e, s, p, 64, **args)
+            out.append(h.clone())
+        torch.cuda.synchronize()
+        assert all(bool((x == 77).all()) for x in junk)
+        outs.append(out)
+    assert status() == 0
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
+
+
+def test_captured_prefill_chunk_equals_the_eager_one():
+    """A chunk captured once (n_seqs said) and replayed for other sequences and positions, with eager
+    calls of other sizes between the replays."""
+    W = weights()
+    caches = [paged_caches("fp8"), paged_caches("fp8")]
+    a, b = (BeamStack(TINY, W, large(c)) for c in caches)
+    T = 12
+
+    def chunk(n):
+        seq = [ROWS[n % 3]] * 7 + [ROWS[(n + 1) % 3]] * 5
+        return tokens(seq, list(range(1, 8)) + list(range(1, 6)), 50 + n)
+
+    e, s, p = chunk(0)
+    for st in (a, b):
+        st.forward(e, s, p, 96, max_q_per_seq=7, n_seqs=2)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h = b.forward(e, s, p, 96, max_q_per_seq=7, n_seqs=2)
+    assert h.shape[0] == T
+    for n in range(1, 5):
+        for x, y in zip((e, s, p), chunk(n)):
+            x.copy_(y)
+        ref = a.forward(e, s, p, 96, max_q_per_seq=7, n_seqs=2).clone()
+        graph.replay()
+        assert torch.equal(h, ref)
+        ce, cs, cp = tokens([ROWS[n % 3]] * 30, list(range(20, 50)), 70 + n)
+        for st in (a, b):
+            st.forward(ce, cs, cp, 150, max_q_per_seq=30, n_seqs=n % 3 + 1)
+    assert status() == 0

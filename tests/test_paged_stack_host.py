@@ -1,4 +1,6 @@
 """What BeamStack works out on the host and in torch for a prefill over paged caches, on the CPU."""
+import weakref
+
 import pytest
 import torch
 
@@ -123,3 +125,29 @@ def test_the_sequences_of_a_large_call_are_counted():
     assert stack([paged(rows=128, pages=6400, window=16)]).count(seq, 102400, None) is None
     copy = st.context(st.caches[0], seq, ints([1] * 120), 102400, 5, 2)[0]
     assert copy.k.nbytes + copy.v.nbytes == 2 * 102400 * TINY.n_kv * TINY.head_dim * 4
+
+
+def test_captured_calls_keep_their_buffers(monkeypatch):
+    """Buffers that a captured call got outlive calls of other sizes (a replay writes them), are
+    used again by calls of their size, and what no capture used is dropped."""
+    st, kc = stack(), paged(rows=8, pages=100)
+    seq, pos = ints([3] * 6), ints(list(range(1, 7)))
+
+    def use(T, max_pos, nbytes):
+        st.ws.device = "cpu"
+        got = [st.buffers(T)["h"], st.stage(T)[0].k, st.stage(T)[1],
+               st.context(kc, seq, pos, max_pos, 6, 1)[0].k, st.ws.get(nbytes)]
+        return [weakref.ref(x) for x in got]
+
+    early = use(3, 100, 1000)
+    monkeypatch.setattr(B, "capturing", lambda: True, raising=False)
+    first = use(4, 200, 2000)
+    monkeypatch.setattr(B, "capturing", lambda: False, raising=False)
+    between = use(70, 900, 50000)
+    again = use(4, 100, 100)
+    assert all(x() is not None for x in first)
+    assert [a() is b() for a, b in zip(first[:3], again[:3])] == [True] * 3
+    assert early[0]() is None and early[1]() is None and early[4]() is None
+    assert between[3]() is again[3]() and between[4]() is again[4]()
+    use(5, 100, 100)
+    assert between[0]() is None and between[1]() is None and all(x() is not None for x in first)
