@@ -162,6 +162,9 @@ class LayerCfg:
         self.__dict__.pop("_kept", None)
         self.__dict__[name] = value
 
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_kept"}   # an address of this process
+
     def _ref(self):
         """Reference to a C struct of the present values, built again after a change."""
         kept = self.__dict__.get("_kept")
