@@ -223,9 +223,23 @@ class PagedKVCache:
     block_scale [num_pages][n_kv][2][page_size][D/16] uint8; NVFP4 only
     window      0 for full attention, else the sliding window
     The tensors are checked once, here, and must not be replaced afterwards (their contents may
-    change, the page table's among them)."""
+    change, the page table's among them); the window may be set again."""
 
     page_size, num_pages = 256, 2 ** 31 - 1   # the largest; a cache holds its own
+
+    @property
+    def window(self):
+        return self._window
+
+    @window.setter
+    def window(self, value):
+        self._window = int(value)
+        if "_c" in self.__dict__:   # what the kernels read
+            self._c.window = self._window
+
+    def __reduce__(self):
+        """Copies and pickles by the tensors: the C struct holds addresses of this cache."""
+        return (type(self), (self.k, self.v, self.page_table, self.row_scale, self.block_scale, self.window))
 
     @property
     def positions(self):
@@ -256,7 +270,7 @@ class PagedKVCache:
         if dev < 0:
             raise BeamError("PagedKVCache: the tensors must be on a CUDA device")
         self.k, self.v, self.page_table = k, v, page_table
-        self.row_scale, self.block_scale, self.window = row_scale, block_scale, int(window)
+        self.row_scale, self.block_scale, self.window = row_scale, block_scale, window
         self.num_pages, self.n_kv, self.page_size, self.head_dim = pages, n_kv, size, width
         self.device = dev
         self._c = PagedKVC(k.data_ptr(), v.data_ptr(),

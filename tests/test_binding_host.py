@@ -19,3 +19,13 @@ def test_a_used_layer_cfg_copies_and_pickles():
         made.n_q = 24
         assert made._ref()._obj.n_q == 24 and cfg._ref()._obj.n_q == cfg.n_q == 48
     assert ctypes.addressof(cfg._ref()._obj) == before
+
+
+def test_the_window_of_a_paged_cache_is_the_kernels_window():
+    """Set again on a cache, it reaches the struct that the calls hand over."""
+    c = object.__new__(B.PagedKVCache)
+    c._c = B.PagedKVC(window=512)
+    c.window = 16
+    assert c.window == 16 and c._c.window == 16
+    c.window = 0
+    assert c.window == 0 and c._c.window == 0
