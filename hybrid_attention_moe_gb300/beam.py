@@ -192,12 +192,13 @@ class KVCache:
                         self.v_scale, self.k.shape[0], self.k.shape[2], self.window)
 
 
-def _want(device, name, t, dtype, n):
+def _want(device, name, t, dtype, *shapes):
     """Refuses a tensor that the library would read as something else: another type or device,
-    gaps between its elements, or not the n elements of the documented shape."""
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != device:
-        raise BeamError(f"{name}: {n} contiguous {dtype} elements on cuda:{device} are wanted, got "
-                        f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    gaps between its elements, or none of the shapes (a number: any shape of so many elements)."""
+    if (t.dtype != dtype or not t.is_contiguous() or t.get_device() != device or
+            not any(t.numel() == s if isinstance(s, int) else t.shape == s for s in shapes)):
+        raise BeamError(f"{name}: contiguous {dtype} {' or '.join(map(str, shapes))} on cuda:{device} is wanted, "
+                        f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
 def _on_device(cache):
@@ -254,18 +255,17 @@ class PagedKVCache:
         code = torch.bfloat16 if row_scale is None else torch.uint8
         dev = k.get_device()
         _want(dev, "k", k, code, k.numel())
-        _want(dev, "v", v, code, k.numel())
+        _want(dev, "v", v, code, tuple(k.shape))
         _want(dev, "page_table", page_table, torch.int32, page_table.numel())
         self.dtype = BEAM_PAGED_BF16
         if row_scale is not None:
-            _want(dev, "row_scale", row_scale, torch.uint8, pages * n_kv * 2 * size)
+            _want(dev, "row_scale", row_scale, torch.uint8, (pages, n_kv, 2, size))
             self.dtype = BEAM_PAGED_FP8
         if block_scale is not None:
             if row_scale is None:
                 raise BeamError("PagedKVCache: block_scale without row_scale")
             width *= 2
-            _want(dev, "block_scale", block_scale, torch.uint8,
-                  pages * n_kv * 2 * size * width // 16)
+            _want(dev, "block_scale", block_scale, torch.uint8, (pages, n_kv, 2, size, width // 16))
             self.dtype = BEAM_PAGED_NVFP4
         if dev < 0:
             raise BeamError("PagedKVCache: the tensors must be on a CUDA device")
@@ -384,17 +384,19 @@ def paged_kv_bytes(num_pages, n_kv, page_size, head_dim, dtype=BEAM_PAGED_BF16) 
 
 def beam_paged_kv_write(k, v, seq_id, pos, cache: PagedKVCache, stream=None):
     """k, v [T][n_kv][D] bf16 (rows of a token contiguous, any stride between tokens that is a
-    multiple of 8) into the cache's pages."""
+    multiple of 8; or [T][n_kv*D], contiguous) into the cache's pages."""
     dev, bf, i32 = _on_device(cache), torch.bfloat16, torch.int32
     n_kv, D = cache.n_kv, cache.head_dim
     T, step = k.size(0), n_kv * D
-    n = T * step
     # one test of everything for rows that lie side by side; others, and what is wrong, below
-    if not (k.dtype is bf and k.numel() == n and k.is_contiguous() and k.get_device() == dev and
-            v.dtype is bf and v.numel() == n and v.is_contiguous() and v.get_device() == dev and
+    if not (k.dtype is bf and (k.shape == (T, n_kv, D) or k.shape == (T, step)) and
+            k.is_contiguous() and k.get_device() == dev and
+            v.dtype is bf and v.shape == k.shape and v.is_contiguous() and v.get_device() == dev and
             seq_id.dtype is i32 and seq_id.numel() == T and seq_id.is_contiguous() and
             seq_id.get_device() == dev and pos.dtype is i32 and pos.numel() == T and
             pos.is_contiguous() and pos.get_device() == dev):
+        _want(dev, "seq_id", seq_id, i32, T)
+        _want(dev, "pos", pos, i32, T)
         for name, x in (("k", k), ("v", v)):
             if x.dtype != bf or x.shape != (T, n_kv, D) or x.get_device() != dev:
                 raise BeamError(f"beam_paged_kv_write: {name} must be bfloat16 ({T}, {n_kv}, {D}) "
@@ -406,8 +408,6 @@ def beam_paged_kv_write(k, v, seq_id, pos, cache: PagedKVCache, stream=None):
             step = k.stride(0)
             if v.stride(0) != step:
                 raise BeamError("beam_paged_kv_write: k and v have different strides between tokens")
-        _want(dev, "seq_id", seq_id, i32, T)
-        _want(dev, "pos", pos, i32, T)
     st = lib().beam_paged_kv_write(k.data_ptr(), v.data_ptr(), step, seq_id.data_ptr(),
                                    pos.data_ptr(), T, cache._ref, _raw_stream(stream, dev))
     if st:
@@ -421,19 +421,18 @@ def beam_paged_kv_read(cache: PagedKVCache, seq_id, first, last, max_len, dst: K
     dev, i32, k, v = _on_device(cache), torch.int32, dst.k, dst.v
     N = seq_id.numel()
     rows, _, cap, _ = k.shape
-    n = rows * cache.n_kv * cap * cache.head_dim
+    dims = (rows, cache.n_kv, cap, cache.head_dim)
     if not (seq_id.dtype is i32 and seq_id.is_contiguous() and seq_id.get_device() == dev and
             first.dtype is i32 and first.numel() == N and first.is_contiguous() and
             first.get_device() == dev and last.dtype is i32 and last.numel() == N and
             last.is_contiguous() and last.get_device() == dev and k.dtype is torch.bfloat16 and
-            k.numel() == n and k.is_contiguous() and k.get_device() == dev and
-            v.dtype is torch.bfloat16 and v.shape == k.shape and v.is_contiguous() and
+            k.shape == dims and k.is_contiguous() and k.get_device() == dev and
+            v.dtype is torch.bfloat16 and v.shape == dims and v.is_contiguous() and
             v.get_device() == dev):
         for name, x in (("seq_id", seq_id), ("first", first), ("last", last)):
             _want(dev, name, x, i32, N)
         for name, x in (("dst.k", k), ("dst.v", v)):
-            _want(dev, name, x, torch.bfloat16, n)
-        raise BeamError(f"beam_paged_kv_read: dst.k {tuple(k.shape)} and dst.v {tuple(v.shape)} differ")
+            _want(dev, name, x, torch.bfloat16, dims)
     kc = KVCacheC(k.data_ptr(), v.data_ptr(), BEAM_KV_BF16, 1.0, 1.0, rows, cap, dst.window)
     st = lib().beam_paged_kv_read(cache._ref, seq_id.data_ptr(), first.data_ptr(),
                                   last.data_ptr(), N, int(max_len), ctypes.byref(kc),
@@ -444,32 +443,35 @@ def beam_paged_kv_read(cache: PagedKVCache, seq_id, first, last, max_len, dst: K
 
 def beam_paged_attn(cfg: LayerCfg, q, g, gate_bias, cache: PagedKVCache, seq_id, pos, max_pos,
                     w_o, out, ws: torch.Tensor, stream=None):
-    """Decode attention over the pages; g, gate_bias None: no gate; w_o None: out is [T][n_q*D]."""
+    """Decode attention over the pages. q, g [T][n_q][D] or [T][n_q*D]; g, gate_bias None: no gate;
+    out [T][hidden], or of q's shapes where w_o is None."""
     dev, bf, i32 = _on_device(cache), torch.bfloat16, torch.int32
     T, n_q = q.size(0), cfg.n_q
     row = n_q * cfg.head_dim
-    n, width = T * row, row if w_o is None else cfg.hidden
+    width = row if w_o is None else cfg.hidden
+    heads, flat = (T, n_q, cfg.head_dim), (T, row)
     if (g is None) != (gate_bias is None):
         raise BeamError("beam_paged_attn: g and gate_bias go together")
     # one test of everything; what is wrong is looked for where it fails
-    if not (q.dtype is bf and q.numel() == n and q.is_contiguous() and q.get_device() == dev and
-            out.dtype is bf and out.numel() == T * width and out.is_contiguous() and
-            out.get_device() == dev and seq_id.dtype is i32 and seq_id.numel() == T and
+    if not (q.dtype is bf and (q.shape == heads or q.shape == flat) and q.is_contiguous() and
+            q.get_device() == dev and out.dtype is bf and
+            (out.shape == (T, width) or (w_o is None and out.shape == heads)) and
+            out.is_contiguous() and out.get_device() == dev and seq_id.dtype is i32 and seq_id.numel() == T and
             seq_id.is_contiguous() and seq_id.get_device() == dev and pos.dtype is i32 and
             pos.numel() == T and pos.is_contiguous() and pos.get_device() == dev and
             ws.is_contiguous() and ws.get_device() == dev):
-        _want(dev, "q", q, bf, n)
-        _want(dev, "out", out, bf, T * width)
+        _want(dev, "q", q, bf, heads, flat)
+        _want(dev, "out", out, bf, (T, width), *([heads] if w_o is None else []))
         _want(dev, "seq_id", seq_id, i32, T)
         _want(dev, "pos", pos, i32, T)
         _want(dev, "ws", ws, ws.dtype, ws.numel())
     pg = pb = pw = None
     if g is not None:
-        _want(dev, "g", g, bf, n)
+        _want(dev, "g", g, bf, flat, heads)
         _want(dev, "gate_bias", gate_bias, bf, n_q)
         pg, pb = g.data_ptr(), gate_bias.data_ptr()
     if w_o is not None:
-        _want(dev, "w_o", w_o, bf, width * row)
+        _want(dev, "w_o", w_o, bf, (width, row))
         pw = w_o.data_ptr()
     st = lib().beam_paged_attn(cfg._ref(), q.data_ptr(), pg, pb, cache._ref, seq_id.data_ptr(),
                                pos.data_ptr(), T, int(max_pos), pw, out.data_ptr(), ws.data_ptr(),
