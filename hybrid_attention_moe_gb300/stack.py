@@ -35,7 +35,8 @@ class BeamStack:
              PAGED_MAX_Q tokens per sequence; with more it reads the sequences' context back
              into a contiguous BF16 cache (beam_paged_kv_read) that beam_attn's prefill takes.
              There a token with a key in a bad page attends to nothing (beam_paged_attn leaves
-             that key out); both set BEAM_DEV_BAD_PAGE.
+             that key out); both set BEAM_DEV_BAD_PAGE. Position 0 pads a decode batch over paged
+             layers; with more tokens per sequence, and over contiguous caches, it is flagged.
 
     Buffers between calls: those of the last number of tokens, one workspace, and one context copy
     for each window. What a captured call uses stays allocated as long as the stack, whatever
@@ -94,6 +95,12 @@ class BeamStack:
             s = (B.KVCache(k, v, window=1), rows, k.view(T, *dims[1::2]), v.view(T, *dims[1::2]))
             self._stage = {**self.held(self._stage), T: s}
         return self.hold(s)
+
+    @staticmethod
+    def staged_pos(pos):
+        """Positions for the projection of paged layers, which knows no padding: it computes a padding
+        row for nothing, and beam_paged_kv_write flags what is below 0."""
+        return pos.clamp_min(1)
 
     def context(self, kc, seq_id, pos, max_pos, max_q, n_seqs=None):
         """What a paged layer's prefill reads: (contiguous cache, its sequences, first, last,
@@ -179,8 +186,9 @@ class BeamStack:
                 return None
             return seq_id.unique().numel()
 
-    def attention(self, i, b, seq_id, pos, max_pos, ws, stream, max_q_per_seq, n_seqs=None):
-        """Projection, cache write and attention of the i-th layer held, from b["u"] to b["a"]."""
+    def attention(self, i, b, seq_id, pos, max_pos, ws, stream, max_q_per_seq, n_seqs=None, staged=None):
+        """Projection, cache write and attention of the i-th layer held, from b["u"] to b["a"].
+        staged: staged_pos(pos), where the caller has it."""
         W, cfg, kc = self.W[i], self.cfgs[i], self.caches[i]
         if not isinstance(kc, B.PagedKVCache):
             B.beam_qkv_gate(cfg, b["u"], W["w_qkvg"], W["q_norm"], W["k_norm"], seq_id, pos, b["q"],
@@ -193,7 +201,8 @@ class BeamStack:
         # buffers that a later call may drop belong to the stream that uses them
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
             stage, rows, k, v = self.stage(T)
-        B.beam_qkv_gate(cfg, b["u"], W["w_qkvg"], W["q_norm"], W["k_norm"], rows, pos, b["q"],
+            staged = self.staged_pos(pos) if staged is None else staged
+        B.beam_qkv_gate(cfg, b["u"], W["w_qkvg"], W["q_norm"], W["k_norm"], rows, staged, b["q"],
                         b["g"], stage, ws, stream)
         B.beam_paged_kv_write(k, v, seq_id, pos, kc, stream)
         if max_q <= self.PAGED_MAX_Q:
@@ -233,7 +242,7 @@ class BeamStack:
         return self.hold(b)
 
     def layer(self, i, b, seq_id, pos, max_pos, ws, stream=None, trace=None, max_q_per_seq=None,
-              n_seqs=None):
+              n_seqs=None, staged=None):
         """The i-th layer held (global index l): from (h, u = its attention pre-norm) to
         (h, u of the next layer). With a trace list, appends the layer's intermediate tensors:
         u_attn, q, g, attn, h_mid (h after the attention residual), mlp_in, mlp, route
@@ -242,7 +251,7 @@ class BeamStack:
         l = self.ids[i]
         if trace is not None:
             trace.append({"u_attn": b["u"].clone()})
-        self.attention(i, b, seq_id, pos, max_pos, ws, stream, max_q_per_seq, n_seqs)
+        self.attention(i, b, seq_id, pos, max_pos, ws, stream, max_q_per_seq, n_seqs, staged)
         B.beam_boundary_norm(b["a"], b["h"], b["u"], W["attn_post"], W["mlp_pre"], 2 * l + 2,
                              cfg.eps, stream)
         if trace is not None:
@@ -288,9 +297,13 @@ class BeamStack:
         if self.paged:
             need = max(need, B.paged_workspace_bytes(self.cfgs[0], T, max_pos))
         ws = self.ws.get(need)
+        staged = None
+        if self.paged:
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                staged = self.staged_pos(pos)
         b["h"].copy_(e)
         B.beam_boundary_norm(None, b["h"], b["u"], None, self.W[0]["attn_pre"], 1,
                              self.cfgs[0].eps, stream)
         for i in range(self.L):
-            self.layer(i, b, seq_id, pos, max_pos, ws, stream, trace, max_q_per_seq, n_seqs)
+            self.layer(i, b, seq_id, pos, max_pos, ws, stream, trace, max_q_per_seq, n_seqs, staged)
         return b["h"]

@@ -204,3 +204,35 @@ def test_captured_prefill_chunk_equals_the_eager_one():
         for st in (a, b):
             st.forward(ce, cs, cp, 150, max_q_per_seq=30, n_seqs=n % 3 + 1)
     assert status() == 0
+
+
+def test_a_padded_decode_batch_sets_no_bit():
+    """A captured decode batch of four rows, some of them padding (position 0, any sequence): no
+    device status, nothing written for them, zeros from their attention, and the other rows' bits
+    are those beside real tokens. A negative position is flagged still."""
+    W = weights()
+    caches = paged_caches("fp8")
+    st = BeamStack(TINY, W, caches)
+    prefill(st)
+    e, s, p = tokens([0, 1, 2, 0], [50, 34, 18, 0], 10)
+    st.forward(e, s, p, 64, max_q_per_seq=1)
+    torch.cuda.synchronize()
+    graph, trace = torch.cuda.CUDAGraph(), []
+    with torch.cuda.graph(graph):
+        h = st.forward(e, s, p, 64, trace=trace, max_q_per_seq=1)
+    rows = []
+    for seq, pos in (([0, 1, 2, 0], [50, 34, 18, 0]), ([0, 99, 2, -4], [50, 0, 18, 0]), ([0, 1, 2, 0], [50, 34, 18, 51])):
+        s.copy_(torch.tensor(seq)), p.copy_(torch.tensor(pos))
+        before = [c.k.clone() for c in caches]
+        graph.replay()
+        assert status() == 0
+        for t in trace:
+            for i, x in enumerate(pos):
+                assert bool(t["attn"][i].any()) == (x > 0)
+        if pos[3] == 0 and rows:       # the same rows again, and nothing else
+            assert all(torch.equal(a, c.k) for a, c in zip(before, caches))
+        rows.append(h[[0, 2]].clone())
+    assert torch.equal(rows[0], rows[1]) and torch.equal(rows[0], rows[2])
+    p.copy_(torch.tensor([50, -1, 18, 0]))
+    graph.replay()
+    assert status() == B.DEV_BAD_POSITION

@@ -151,3 +151,23 @@ def test_captured_calls_keep_their_buffers(monkeypatch):
     assert between[3]() is again[3]() and between[4]() is again[4]()
     use(5, 100, 100)
     assert between[0]() is None and between[1]() is None and all(x() is not None for x in first)
+
+
+def test_padding_rows_are_projected_at_a_position_that_there_is(monkeypatch):
+    """Position 0 reaches the write and the attention, which take it for padding, and not the
+    projection, which flags it; one tensor serves all layers."""
+    import synth
+    caches = [paged(window=TINY.window), paged(window=TINY.window)]
+    st = S.BeamStack(TINY, [synth.layer_weights(TINY, layer, 0) for layer in range(2)], caches, device="cpu")
+    seen = {}
+    for name in ("beam_qkv_gate", "beam_attn", "beam_boundary_norm", "beam_dense_mlp", "beam_route", "beam_moe",
+                 "beam_paged_kv_write", "beam_paged_kv_read", "beam_paged_attn"):
+        monkeypatch.setattr(B, name, lambda *a, _n=name, **k: seen.setdefault(_n, []).append(a))
+    monkeypatch.setattr(B, "workspace_bytes", lambda *a: 100)
+    monkeypatch.setattr(B, "paged_workspace_bytes", lambda *a: 100)
+    e = torch.zeros((4, TINY.hidden), dtype=torch.bfloat16)
+    st.forward(e, ints([0, 1, 2, 0]), ints([7, 0, -3, 1]), 7, max_q_per_seq=1)
+    assert [a[6].tolist() for a in seen["beam_qkv_gate"]] == [[7, 1, 1, 1]] * 2
+    assert seen["beam_qkv_gate"][0][6] is seen["beam_qkv_gate"][1][6]
+    assert [a[3].tolist() for a in seen["beam_paged_kv_write"]] == [[7, 0, -3, 1]] * 2
+    assert [a[6].tolist() for a in seen["beam_paged_attn"]] == [[7, 0, -3, 1]] * 2
