@@ -75,3 +75,49 @@ def test_value_rows_of_large_magnitude_and_small_weight(fmt, D, G, n, window, bi
     out = attend(cfg, c, q, ints([0]), ints([n]), n)
     assert status() == 0
     check(cfg, host(c), np64(q), n, np64(out))
+
+
+@pytest.mark.parametrize("D,G,n", [(128, 5, 700), (64, 12, 3000), (128, 16, 90)])
+def test_infinities_over_bf16_pages(D, G, n):
+    """Keys with an infinity: logits of -inf weigh nothing, +inf makes NaN, all of -inf give zero. A
+    value with one makes its element of what reads it infinite or NaN, and no other output."""
+    cfg = cfg_for(2 * G, 2, D)
+    page, inf = 32, float("inf")
+    per = -(-n // page)
+    lens = [n, n, n, 3]
+    c = B.PagedKVCache.empty(4 * per, page, 2, D, torch.arange(4 * per, dtype=torch.int32, device=DEV).view(4, per))
+    seq = [s for s, m in enumerate(lens) for _ in range(m)]
+    pos = [p for m in lens for p in range(1, m + 1)]
+    k, v = randn(311, len(seq), 2, D), randn(312, len(seq), 2, D)
+    q = randn(313, 4, 2 * G, D).abs()
+    k[[n // 2, n - 1], 0, 5] = -inf         # sequence 0, KV head 0: two keys of -inf for every query
+    k[n + n // 3, 1, 7] = inf               # sequence 1, KV head 1: +inf
+    v[2 * n + n // 4, 0, 9] = inf           # sequence 2, KV head 0: an infinite value
+    k[3 * n:, 1, 0] = -inf                  # sequence 3, KV head 1: nothing but -inf
+    B.beam_paged_kv_write(k, v, ints(seq), ints(pos), c)
+    out = np64(attend(cfg, c, q, ints([0, 1, 2, 3]), ints(lens), n)).reshape(4, 2, G, D)
+    assert status() == 0
+    # the same without those keys and values
+    k2, v2 = k.clone(), v.clone()
+    k2[torch.isinf(k2)] = 0
+    v2[torch.isinf(v2)] = 0
+    B.beam_paged_kv_write(k2, v2, ints(seq), ints(pos), c)
+    ref = np64(attend(cfg, c, q, ints([0, 1, 2, 3]), ints(lens), n)).reshape(4, 2, G, D)
+    assert np.array_equal(out[0, 1], ref[0, 1]) and np.array_equal(out[1, 0], ref[1, 0])
+    assert np.all(np.isnan(out[1, 1]))
+    hit = ~np.isfinite(out[2, 0])
+    assert np.all(hit[:, 9]) and not np.any(np.delete(hit, 9, axis=1))
+    assert np.array_equal(np.delete(out[2, 0], 9, axis=1), np.delete(ref[2, 0], 9, axis=1))
+    assert np.array_equal(out[2, 1], ref[2, 1]) and np.array_equal(out[3, 0], ref[3, 0])
+    assert not np.any(out[3, 1])
+    # sequence 0, KV head 0: the other keys' softmax
+    keep = np.array([i for i in range(n) if i not in (n // 2, n - 1)])
+    K, V = np64(k[:n, 0])[keep], np64(v[:n, 0])[keep]
+    for g in range(G):
+        qh = np64(q[0, g])
+        x = K @ qh / np.sqrt(D)
+        p = np.exp(x - x.max())
+        p /= p.sum()
+        want, mag = p @ V, p @ np.abs(V)
+        d = D * 2.0 ** -23 * np.max(np.abs(K) @ np.abs(qh)) / np.sqrt(D)
+        assert np.all(np.abs(out[0, 0, g] - want) <= 2.0 ** -8 * np.abs(want) + mag * (2 * d + 2.0 ** -15))
