@@ -102,11 +102,12 @@ class BeamStack:
         row for nothing, and beam_paged_kv_write flags what is below 0."""
         return pos.clamp_min(1)
 
-    def context(self, kc, seq_id, pos, max_pos, max_q, n_seqs=None):
+    def context(self, kc, seq_id, pos, max_pos, max_q, n_seqs=None, ranges=None):
         """What a paged layer's prefill reads: (contiguous cache, its sequences, first, last,
         longest), one row for each of the n_seqs sequences at most that have tokens in the call, in
         their order, or for every sequence of the page table where that is no more. Rows without a
-        sequence read nothing. Layers of one window share the cache."""
+        sequence read nothing. Layers of one window share the cache. ranges: (its sequences, first,
+        last), where a layer before has found them."""
         n, W, dev = kc.page_table.shape[0], kc.window, pos.device
         rows = n if n_seqs is None else max(1, min(n, n_seqs))
         max_pos = min(max_pos, kc.positions)
@@ -123,6 +124,9 @@ class BeamStack:
             dims = (rows, self.shape.n_kv, cap, self.shape.head_dim)
             k, v = (torch.empty(dims, dtype=torch.bfloat16, device=self.device) for _ in "kv")
             copy = self._copies[(rows, W)] = B.KVCache(k, v, window=W)
+        self.hold(copy)
+        if ranges is not None:
+            return copy, *ranges, longest
         # other tokens are flagged by the library, and reach into no sequence's range
         known = (seq_id >= 0) & (seq_id < n) & (pos >= 1) & (pos <= max_pos)
         s = torch.where(known, seq_id, 0).long()
@@ -141,7 +145,7 @@ class BeamStack:
             every = every.clamp_min(0)
         first = (first - W + 1).clamp_min(1) if W else torch.ones_like(last)
         first = torch.where(last > 0, first, 1)
-        return self.hold(copy), every, first, last, longest
+        return copy, every, first, last, longest
 
     def rows(self, kc, seq_id, pos, every, first, last):
         """Each token's row of the copy (sequences `every`): its sequence's, any for a token at position
@@ -186,9 +190,9 @@ class BeamStack:
                 return None
             return seq_id.unique().numel()
 
-    def attention(self, i, b, seq_id, pos, max_pos, ws, stream, max_q_per_seq, n_seqs=None, staged=None):
+    def attention(self, i, b, seq_id, pos, max_pos, ws, stream, max_q_per_seq, n_seqs=None, call=None):
         """Projection, cache write and attention of the i-th layer held, from b["u"] to b["a"].
-        staged: staged_pos(pos), where the caller has it."""
+        call: a dict for what the layers of one call share."""
         W, cfg, kc = self.W[i], self.cfgs[i], self.caches[i]
         if not isinstance(kc, B.PagedKVCache):
             B.beam_qkv_gate(cfg, b["u"], W["w_qkvg"], W["q_norm"], W["k_norm"], seq_id, pos, b["q"],
@@ -198,12 +202,14 @@ class BeamStack:
             return
         T = seq_id.shape[0]
         max_q = T if max_q_per_seq is None else max_q_per_seq
+        call = {} if call is None else call
         # buffers that a later call may drop belong to the stream that uses them
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
             stage, rows, k, v = self.stage(T)
-            staged = self.staged_pos(pos) if staged is None else staged
-        B.beam_qkv_gate(cfg, b["u"], W["w_qkvg"], W["q_norm"], W["k_norm"], rows, staged, b["q"],
-                        b["g"], stage, ws, stream)
+            if "staged" not in call:
+                call["staged"] = self.staged_pos(pos)
+        B.beam_qkv_gate(cfg, b["u"], W["w_qkvg"], W["q_norm"], W["k_norm"], rows, call["staged"],
+                        b["q"], b["g"], stage, ws, stream)
         B.beam_paged_kv_write(k, v, seq_id, pos, kc, stream)
         if max_q <= self.PAGED_MAX_Q:
             B.beam_paged_attn(cfg, b["q"], b["g"], W["gate_bias"], kc, seq_id, pos, max_pos,
@@ -213,13 +219,22 @@ class BeamStack:
             # a token past the table was flagged by the write; beam_attn shares key tiles between a
             # sequence's tokens, and must not take it for the sequence's end
             max_pos = min(max_pos, kc.positions)
-            pos = pos.masked_fill(pos > max_pos, 0)
             most = T if n_seqs is None else min(T, n_seqs)
-            copy, every, first, last, longest = self.context(kc, seq_id, pos, max_pos, max_q, most)
-            row = self.rows(kc, seq_id, pos, every, first, last)
-            pos = self.readable(kc, row, pos, first, last, longest, every)
+            # layers over one table and window read the same ranges: worked out by the first of them
+            # (a chunk of 512 tokens, six layers, from projection to attention: 0.83 -> 0.23 ms a layer
+            # from the host, 290 -> 187 us in a graph)
+            over = (kc.page_table, kc.window, kc.page_size, kc.num_pages)
+            ranges, row, reach = next((x for o, x in call.get("ranges", []) if o[0] is over[0] and o[1:] == over[1:]),
+                                      (None, None, None))
+            if ranges is None:
+                pos = pos.masked_fill(pos > max_pos, 0)
+            copy, every, first, last, longest = self.context(kc, seq_id, pos, max_pos, max_q, most, ranges)
+            if ranges is None:
+                row = self.rows(kc, seq_id, pos, every, first, last)
+                reach = self.readable(kc, row, pos, first, last, longest, every)
+                call.setdefault("ranges", []).append((over, ((every, first, last), row, reach)))
         B.beam_paged_kv_read(kc, every, first, last, longest, copy, stream)
-        B.beam_attn(cfg, b["q"], b["g"], W["gate_bias"], copy, row, pos, max_pos, W["w_o"],
+        B.beam_attn(cfg, b["q"], b["g"], W["gate_bias"], copy, row, reach, max_pos, W["w_o"],
                     b["a"], ws, stream, max_q_per_seq)
 
     def buffers(self, T):
@@ -242,7 +257,7 @@ class BeamStack:
         return self.hold(b)
 
     def layer(self, i, b, seq_id, pos, max_pos, ws, stream=None, trace=None, max_q_per_seq=None,
-              n_seqs=None, staged=None):
+              n_seqs=None, call=None):
         """The i-th layer held (global index l): from (h, u = its attention pre-norm) to
         (h, u of the next layer). With a trace list, appends the layer's intermediate tensors:
         u_attn, q, g, attn, h_mid (h after the attention residual), mlp_in, mlp, route
@@ -251,7 +266,7 @@ class BeamStack:
         l = self.ids[i]
         if trace is not None:
             trace.append({"u_attn": b["u"].clone()})
-        self.attention(i, b, seq_id, pos, max_pos, ws, stream, max_q_per_seq, n_seqs, staged)
+        self.attention(i, b, seq_id, pos, max_pos, ws, stream, max_q_per_seq, n_seqs, call)
         B.beam_boundary_norm(b["a"], b["h"], b["u"], W["attn_post"], W["mlp_pre"], 2 * l + 2,
                              cfg.eps, stream)
         if trace is not None:
@@ -297,13 +312,10 @@ class BeamStack:
         if self.paged:
             need = max(need, B.paged_workspace_bytes(self.cfgs[0], T, max_pos))
         ws = self.ws.get(need)
-        staged = None
-        if self.paged:
-            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
-                staged = self.staged_pos(pos)
         b["h"].copy_(e)
         B.beam_boundary_norm(None, b["h"], b["u"], None, self.W[0]["attn_pre"], 1,
                              self.cfgs[0].eps, stream)
+        call = {}
         for i in range(self.L):
-            self.layer(i, b, seq_id, pos, max_pos, ws, stream, trace, max_q_per_seq, n_seqs, staged)
+            self.layer(i, b, seq_id, pos, max_pos, ws, stream, trace, max_q_per_seq, n_seqs, call)
         return b["h"]

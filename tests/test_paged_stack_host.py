@@ -171,3 +171,34 @@ def test_padding_rows_are_projected_at_a_position_that_there_is(monkeypatch):
     assert seen["beam_qkv_gate"][0][6] is seen["beam_qkv_gate"][1][6]
     assert [a[3].tolist() for a in seen["beam_paged_kv_write"]] == [[7, 0, -3, 1]] * 2
     assert [a[6].tolist() for a in seen["beam_paged_attn"]] == [[7, 0, -3, 1]] * 2
+
+
+def test_layers_share_what_they_read_over_one_table_only(monkeypatch):
+    """Layers over one table and window use the ranges that the first of them found; another table
+    or window has its own, and so has the next call."""
+    import synth
+    one, other = ints([[0, 1, 2, 3, 4]] * 4), ints([[0, 1, -1, 3, 4]] * 4)
+    caches = [paged(window=w) for w in (TINY.window, 0, TINY.window, TINY.window, 0)]
+    for c, t in zip(caches, (one, one, one, other, other)):
+        c.page_table, c.num_pages = t, 9
+    st = S.BeamStack(TINY, [synth.layer_weights(TINY, 0, 0) for _ in caches], caches, device="cpu")
+    st.dense = [True] * 5
+    seen = {}
+    for name in ("beam_qkv_gate", "beam_attn", "beam_boundary_norm", "beam_dense_mlp", "beam_paged_kv_write",
+                 "beam_paged_kv_read"):
+        monkeypatch.setattr(B, name, lambda *a, _n=name, **k: seen.setdefault(_n, []).append(a))
+    monkeypatch.setattr(B, "workspace_bytes", lambda *a: 100)
+    monkeypatch.setattr(B, "paged_workspace_bytes", lambda *a: 100)
+    for start in (30, 33):
+        seen.clear()
+        e, pos = torch.zeros((9, TINY.hidden), dtype=torch.bfloat16), list(range(start, start + 9))
+        st.forward(e, ints([2] * 9), ints(pos), max(pos), max_q_per_seq=9)
+        reads, attns = seen["beam_paged_kv_read"], seen["beam_attn"]
+        assert reads[0][2] is reads[2][2] and reads[0][1] is reads[2][1] and attns[0][6] is attns[2][6]
+        for read, attn, c in zip(reads, attns, caches):
+            lo = max(1, start - c.window + 1) if c.window else 1
+            assert read[2].tolist() == [1, 1, lo, 1] and read[3].tolist() == [0, 0, start + 8, 0]
+            assert attn[4] is read[5] and attn[5].tolist() == [2] * 9
+            # page 2, positions 33 .. 48, is none in the other table
+            sees = [c.page_table is other and p >= 33 and (c.window == 0 or p - c.window + 1 <= 48) for p in pos]
+            assert attn[6].tolist() == [0 if bad else p for p, bad in zip(pos, sees)]
