@@ -196,7 +196,7 @@ def _want(device, name, t, dtype, *shapes):
     """Refuses a tensor that the library would read as something else: another type or device,
     gaps between its elements, or none of the shapes (a number: any shape of so many elements)."""
     if (t.dtype != dtype or not t.is_contiguous() or t.get_device() != device or
-            not any(t.numel() == s if isinstance(s, int) else t.shape == s for s in shapes)):
+            not (t.shape in shapes or t.numel() in shapes)):
         raise BeamError(f"{name}: contiguous {dtype} {' or '.join(map(str, shapes))} on cuda:{device} is wanted, "
                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
@@ -467,8 +467,11 @@ def beam_paged_attn(cfg: LayerCfg, q, g, gate_bias, cache: PagedKVCache, seq_id,
         _want(dev, "ws", ws, ws.dtype, ws.numel())
     pg = pb = pw = None
     if g is not None:
-        _want(dev, "g", g, bf, flat, heads)
-        _want(dev, "gate_bias", gate_bias, bf, n_q)
+        if not (g.dtype is bf and (g.shape == flat or g.shape == heads) and g.is_contiguous() and
+                g.get_device() == dev and gate_bias.dtype is bf and gate_bias.numel() == n_q and
+                gate_bias.is_contiguous() and gate_bias.get_device() == dev):
+            _want(dev, "g", g, bf, flat, heads)
+            _want(dev, "gate_bias", gate_bias, bf, n_q)
         pg, pb = g.data_ptr(), gate_bias.data_ptr()
     if w_o is not None:
         _want(dev, "w_o", w_o, bf, (width, row))
