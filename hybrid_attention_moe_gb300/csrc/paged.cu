@@ -2,9 +2,10 @@
 // BF16 cache. The formats are those of include/beam.h (beam_paged_kv).
 //
 // Both kernels move bytes once and do little with them. Reading back is bounded by HBM (192,000
-// tokens of 8 heads from FP8: 176.5 us, 99% of the copy rate). Writing 16,384 tokens of 8 heads:
-// BF16 20.3 us, FP8 15.9, NVFP4 15.0 with the input in L2 and 21.8 from HBM (59% of the copy rate),
-// where the quantisation's ~180 warp instructions for 512 elements keep the issue slots 55% busy.
+// tokens of 8 heads from FP8: 176.6 us, 99% of the copy rate; 16,384 from BF16 20.0, 99%). Writing
+// 16,384 tokens of 8 heads: BF16 20.4 us, FP8 16.5, NVFP4 15.5 with the input in L2 and 21.5 from HBM
+// (59% of the copy rate), where the quantisation's ~180 warp instructions for 512 elements keep the
+// issue slots 54% busy.
 // A decode step's rows (32 tokens) take 2.3 us, most of it the launch and three dependent loads.
 #include "mma.cuh"
 #include "paged.cuh"

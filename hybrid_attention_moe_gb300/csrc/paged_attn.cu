@@ -7,12 +7,12 @@
 // partial results of disjoint key ranges join by.
 //
 // What bounds it (device time in a graph; HBM 6784.5 GB/s as a copy): the bytes of the keys and
-// values over long contexts: 128 sequences of 17 to 16,385 tokens in FP8 323 us, 99% of the copy
-// rate; one of 100,001 in BF16 66.7 us, 91%, the rest being the start (1.6 us of plan, 0.9 us of page
+// values over long contexts: 128 sequences of 17 to 16,385 tokens in FP8 321 us, 99% of the copy
+// rate; one of 100,001 in BF16 66.2 us, 91%, the rest being the start (1.6 us of plan, 0.9 us of page
 // lookups) and the join (3 us). Over an NVFP4 cache the arithmetic: 4 sequences of 60,000 to
-// 100,001 tokens 80.4 us, 69%: about 345 warp instructions for 16 keys of one KV head, 128 of them
-// the conversions and the scaling of the codes, which keep the issue slots 64% and the integer
-// pipe 59% busy.
+// 100,001 tokens 82.3 us, 67%: about 360 warp instructions for 16 keys of one KV head, 128 of them
+// the conversions and the scaling of the codes, which keep the issue slots 66% and the integer
+// pipe 58% busy.
 //
 // Split. A (row, KV head) pair's keys are cut into blocks of BK; the blocks of all pairs, laid
 // end to end, are cut into equal ranges, two or three per CTA (one CTA per SM). The ranges are
@@ -49,7 +49,10 @@
 // V's (2^e) goes into P = 2^(x + e - Z + 7), where Z is a second running max, that of x + e. So P's
 // largest values lie near the top of f16 whatever the scales are, a row of large values that
 // weighs nothing takes no bits from the others, and what P loses below f16's smallest step is at
-// most 2^-32 of the largest weighted scale for each key. q is scaled by a power of two per head in
+// most 2^-32 of the largest weighted scale for each key. (Z costs NVFP4 2 to 5%, 4 sequences of
+// 60,000 to 100,001 tokens 80.4 -> 82.3 us; over FP8 the stream hides it, but for 16 heads, 39 of
+// 20,236 276 -> 282.) Against 64 bits the outputs over quantised caches are 0.6% further off than
+// with FP32 weights, the rest being their rounding to bf16. q is scaled by a power of two per head in
 // the same manner. The d axis is permuted the same way in q
 // and K, and undone on the output for V, so that a thread's codes are contiguous bytes.
 //
@@ -91,7 +94,7 @@ struct Cfg {
   static constexpr int GROUPS = FMT == kFmtNVFP4 && (D == 128 || NT == 1) ? 3 : 2;
   // over quantised caches q's fragments lie in shared memory, not in 8 to 32 registers: 39 sequences
   // of 20,236 tokens, 8 KV heads of 16 heads: FP8 313 -> 276 us, NVFP4 346 (with two groups) -> 292;
-  // of 8 heads, NVFP4 184 -> 180, 64-wide 136 -> 132
+  // of 8 heads, NVFP4 184 -> 180, 64-wide 136 -> 132 (before the second running max: now 282, 309, 185, 134)
   static constexpr bool QSM = FMT != kFmtBF16;
   static constexpr int WPG = 4, SPW = HEAVY ? 1 : 2;
   // log2 units by which a reference may lag: P <= 2^(kRescale + kBias) in f16, below 65504

@@ -45,7 +45,11 @@ class BeamStack:
     """
 
     # A call's tokens of one sequence each read their keys in beam_paged_attn; the way through a
-    # contiguous copy writes and reads them in BF16 once more, whatever the tokens' number.
+    # contiguous copy writes and reads them in BF16 once more, whatever the tokens' number. A NoPE
+    # layer from projection to o_proj, pages against copy, for 4 / 5 / 8 tokens of each sequence (us):
+    #   1 x 100,000 keys  BF16 270:313 323:322 488:347   FP8 151:289 171:298 265:323   NVFP4 140:287 162:297 227:322
+    #   32 x 4000         BF16 391:415 461:440 678:479   FP8 251:382 284:407 404:443   NVFP4 226:374 257:400 345:436
+    # So 4 suits BF16; over FP8 and NVFP4 the pages stay ahead up to about 12, and one bound serves all.
     PAGED_MAX_Q = 4
 
     # A context copy larger than this is worth a wait for the exact number of its sequences: the
