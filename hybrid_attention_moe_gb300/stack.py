@@ -112,7 +112,8 @@ class BeamStack:
         their order, or for every sequence of the page table where that is no more. Rows without a
         sequence read nothing. Layers of one window share the cache. ranges: (its sequences, first,
         last), where a layer before has found them."""
-        n, W, dev = kc.page_table.shape[0], kc.window, pos.device
+        # a window past the table's reach is the table's reach
+        n, W, dev = kc.page_table.shape[0], min(kc.window, kc.positions), pos.device
         rows = n if n_seqs is None else max(1, min(n, n_seqs))
         max_pos = min(max_pos, kc.positions)
         longest = max_pos if W == 0 else min(max_pos, W - 1 + max_q)
@@ -174,8 +175,9 @@ class BeamStack:
             table = table[every.long()]
         s = row.clamp(0, table.shape[0] - 1).long()
         none = ((table < 0) | (table >= kc.num_pages)).cumsum(1, dtype=torch.int32)   # up to each page
-        lo = (pos - kc.window).clamp_min(0) if kc.window else torch.zeros_like(pos)
-        a, b = lo // size, (pos - 1).clamp_min(0) // size              # pages of a token's keys
+        p = pos.clamp(0, kc.positions)
+        lo = (p - kc.window).clamp_min(0) if kc.window else torch.zeros_like(p)
+        a, b = lo // size, (p - 1).clamp_min(0) // size              # pages of a token's keys
         before = torch.where(a > 0, none[s, (a - 1).clamp_min(0).long()], 0)
         whole = (none[s, b.long()] == before) & ((last - first)[s] < longest)
         return torch.where(whole, pos, 0)

@@ -202,3 +202,19 @@ def test_layers_share_what_they_read_over_one_table_only(monkeypatch):
             # page 2, positions 33 .. 48, is none in the other table
             sees = [c.page_table is other and p >= 33 and (c.window == 0 or p - c.window + 1 <= 48) for p in pos]
             assert attn[6].tolist() == [0 if bad else p for p, bad in zip(pos, sees)]
+
+
+@pytest.mark.parametrize("window", [0, 512, 2 ** 31 - 1])
+def test_any_position_stays_inside_the_page_table(window):
+    """Positions that the library flags, as far out as there are, index nothing outside the table."""
+    st, kc = stack(), paged(rows=3, pages=6, page_size=16, window=window)
+    far = [-2 ** 31, -2 ** 31 + 5, -600, -1, 0, 2 ** 31 - 1, 97]
+    first, last = ints([1] * 3), ints([96] * 3)
+    got = st.readable(kc, ints([0, 1, 2, -2 ** 31, 2 ** 31 - 1, 1, 0]), ints(far), first, last, 96)
+    assert got.tolist() == far       # left to the library to flag
+    seq, pos = ints([0, -2 ** 31, 2 ** 31 - 1, 1, 2, 2]), ints([-2 ** 31, 5, 5, 2 ** 31 - 1, 3, 4])
+    for n_seqs in (None, 1):
+        copy, every, first, last, longest = st.context(kc, seq, pos, 90, 6, n_seqs)
+        row = st.rows(kc, seq, pos, every, first, last)
+        st.readable(kc, row, pos, first, last, longest, every)
+        assert [int(x) for x in every[last >= first]] == [2] and int(last.max()) == 4
