@@ -106,19 +106,25 @@ class BeamStack:
         row for nothing, and beam_paged_kv_write flags what is below 0."""
         return pos.clamp_min(1)
 
+    @staticmethod
+    def reach(kc, max_pos, max_q):
+        """(Window, longest range, capacity) of a context copy; a window past the page table's
+        reach is that reach, and a ring's capacity a multiple of the attention's key tiles."""
+        W, max_pos = min(kc.window, kc.positions), min(max_pos, kc.positions)
+        if W == 0:
+            return W, max_pos, max_pos
+        return W, min(max_pos, W - 1 + max_q), (W - 1 + max_q + 127) // 128 * 128
+
     def context(self, kc, seq_id, pos, max_pos, max_q, n_seqs=None, ranges=None):
         """What a paged layer's prefill reads: (contiguous cache, its sequences, first, last,
         longest), one row for each of the n_seqs sequences at most that have tokens in the call, in
         their order, or for every sequence of the page table where that is no more. Rows without a
         sequence read nothing. Layers of one window share the cache. ranges: (its sequences, first,
         last), where a layer before has found them."""
-        # a window past the table's reach is the table's reach
-        n, W, dev = kc.page_table.shape[0], min(kc.window, kc.positions), pos.device
+        n, dev = kc.page_table.shape[0], pos.device
         rows = n if n_seqs is None else max(1, min(n, n_seqs))
         max_pos = min(max_pos, kc.positions)
-        longest = max_pos if W == 0 else min(max_pos, W - 1 + max_q)
-        # a ring's capacity is a multiple of the attention's key tiles
-        cap = longest if W == 0 else (W - 1 + max_q + 127) // 128 * 128
+        W, longest, cap = self.reach(kc, max_pos, max_q)
         held = [key for key in self._copies if key[1] == W]   # one copy for a window
         copy = self._copies[held[0]] if held else None
         if copy is None or copy.k.shape[0] < rows or copy.k.shape[2] < cap:
@@ -182,13 +188,13 @@ class BeamStack:
         whole = (none[s, b.long()] == before) & ((last - first)[s] < longest)
         return torch.where(whole, pos, 0)
 
-    def count(self, seq_id, max_pos, stream):
+    def count(self, seq_id, max_pos, stream, max_q=1):
         """The number of sequences in a call that does not say it, where every sequence that there
         could be would make a large copy: one wait for the GPU. None where it would not, and under
         a capture, which cannot wait."""
         row = 4 * self.shape.n_kv * self.shape.head_dim
-        most = max((min(c.page_table.shape[0], seq_id.shape[0]) * min(max_pos, c.positions) * row
-                    for c in self.caches if isinstance(c, B.PagedKVCache) and c.window == 0), default=0)
+        most = max((min(c.page_table.shape[0], seq_id.shape[0]) * self.reach(c, max_pos, max_q)[2] * row
+                    for c in self.caches if isinstance(c, B.PagedKVCache)), default=0)
         if most <= self.COPY_BYTES:
             return None
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
@@ -311,8 +317,9 @@ class BeamStack:
         that many would take more than COPY_BYTES (not in a captured call: say it there).
         Returns h after the last residual addition (an internal buffer)."""
         T = e.shape[0]
-        if self.paged and n_seqs is None and (T if max_q_per_seq is None else max_q_per_seq) > self.PAGED_MAX_Q:
-            n_seqs = self.count(seq_id, max_pos, stream)
+        max_q = T if max_q_per_seq is None else max_q_per_seq
+        if self.paged and n_seqs is None and max_q > self.PAGED_MAX_Q:
+            n_seqs = self.count(seq_id, max_pos, stream, max_q)
         b = self.buffers(T)
         need = B.workspace_bytes(self.cfgs[0], T, max_pos)
         if self.paged:

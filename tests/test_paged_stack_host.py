@@ -218,3 +218,11 @@ def test_any_position_stays_inside_the_page_table(window):
         row = st.rows(kc, seq, pos, every, first, last)
         st.readable(kc, row, pos, first, last, longest, every)
         assert [int(x) for x in every[last >= first]] == [2] and int(last.max()) == 4
+
+
+def test_the_sequences_of_a_windowed_call_are_counted_too():
+    """A window's rings for 2048 rows of window + chunk slots pass COPY_BYTES as a context does."""
+    seq = ints([5] * 2048)
+    st = stack([paged(rows=4096, pages=200, window=16)])
+    assert st.count(seq, 3000, None, 2048) == 1            # 2048 rings of 2176 slots, 512 bytes each
+    assert st.count(seq, 3000, None, 100) is None          # of 128
