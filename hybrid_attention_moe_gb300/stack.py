@@ -20,6 +20,11 @@ def is_nope_layer(layer: int, n_layers: int) -> bool:
     return (layer + 1) % 6 == 0 or layer == n_layers - 1
 
 
+def on(stream):
+    """Context in which torch's work, and the memory it takes, belongs to `stream` (None: the current)."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 class BeamStack:
     """A truncated Beam stack on one GPU.
 
@@ -197,7 +202,7 @@ class BeamStack:
                     for c in self.caches if isinstance(c, B.PagedKVCache)), default=0)
         if most <= self.COPY_BYTES:
             return None
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        with on(stream):
             if B.capturing():
                 return None
             return seq_id.unique().numel()
@@ -216,7 +221,7 @@ class BeamStack:
         max_q = T if max_q_per_seq is None else max_q_per_seq
         call = {} if call is None else call
         # buffers that a later call may drop belong to the stream that uses them
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        with on(stream):
             stage, rows, k, v = self.stage(T)
             if "staged" not in call:
                 call["staged"] = self.staged_pos(pos)
@@ -227,7 +232,7 @@ class BeamStack:
             B.beam_paged_attn(cfg, b["q"], b["g"], W["gate_bias"], kc, seq_id, pos, max_pos,
                               W["w_o"], b["a"], ws, stream)
             return
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        with on(stream):
             # a token past the table was flagged by the write; beam_attn shares key tiles between a
             # sequence's tokens, and must not take it for the sequence's end
             max_pos = min(max_pos, kc.positions)
@@ -274,6 +279,10 @@ class BeamStack:
         (h, u of the next layer). With a trace list, appends the layer's intermediate tensors:
         u_attn, q, g, attn, h_mid (h after the attention residual), mlp_in, mlp, route
         (logits, idx, w) on MoE layers, and the output h."""
+        with on(stream):
+            self._layer(i, b, seq_id, pos, max_pos, ws, stream, trace, max_q_per_seq, n_seqs, call)
+
+    def _layer(self, i, b, seq_id, pos, max_pos, ws, stream, trace, max_q_per_seq, n_seqs, call):
         W, cfg = self.W[i], self.cfgs[i]
         l = self.ids[i]
         if trace is not None:
@@ -315,7 +324,12 @@ class BeamStack:
         sizes the context copies of a prefill over paged caches (tokens of sequences past it are
         flagged as of a bad sequence). None: at most T, counted, with one wait for the GPU, where
         that many would take more than COPY_BYTES (not in a captured call: say it there).
+        stream: where all of the call runs (None: the current one); the inputs are ready there.
         Returns h after the last residual addition (an internal buffer)."""
+        with on(stream):   # torch's copies and allocations too
+            return self._forward(e, seq_id, pos, max_pos, stream, trace, max_q_per_seq, n_seqs)
+
+    def _forward(self, e, seq_id, pos, max_pos, stream, trace, max_q_per_seq, n_seqs):
         T = e.shape[0]
         max_q = T if max_q_per_seq is None else max_q_per_seq
         if self.paged and n_seqs is None and max_q > self.PAGED_MAX_Q:

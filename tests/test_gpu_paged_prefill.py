@@ -7,7 +7,7 @@ from synth import TINY
 from hybrid_attention_moe_gb300 import beam as B
 from hybrid_attention_moe_gb300.stack import BeamStack
 from test_gpu_paged import status
-from test_gpu_paged_stack import CHUNKS, PAGE, PAGES, SEQS, paged_caches, prefill, tokens, weights
+from test_gpu_paged_stack import CHUNKS, PAGE, PAGES, SEQS, contiguous_caches, paged_caches, prefill, tokens, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -236,3 +236,32 @@ def test_a_padded_decode_batch_sets_no_bit():
     p.copy_(torch.tensor([50, -1, 18, 0]))
     graph.replay()
     assert status() == B.DEV_BAD_POSITION
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_a_call_on_another_stream_waits_for_no_other(paged):
+    """forward(stream=...) while the current stream is busy: the input's copy, the buffers and the
+    trace belong to the call's stream, so its results are those of a call by itself."""
+    W = weights()
+    runs = []
+    busy = torch.randn(4096, 4096, device="cuda")
+    for side in (None, torch.cuda.Stream()):
+        st = BeamStack(TINY, W, paged_caches("bf16") if paged else contiguous_caches(40))
+        got = []
+        for n, (seq, pos, most) in enumerate(CHUNKS + [([0, 1, 2], [50, 34, 18], 1)]):
+            e, s, p = tokens(seq, pos, n)
+            torch.cuda.synchronize()
+            trace = []
+            if side is not None:
+                x = busy
+                for _ in range(40):      # tens of milliseconds
+                    x = x @ busy
+            h = st.forward(e, s, p, max(pos), stream=side, trace=trace, max_q_per_seq=most)
+            (side or torch.cuda.current_stream()).synchronize()
+            with torch.cuda.stream(side):
+                got += [h.clone()] + [t[k].clone() for t in trace for k in ("u_attn", "attn", "h")]
+            torch.cuda.synchronize()
+        runs.append(got)
+    assert status() == 0
+    for x, y in zip(*runs):
+        assert torch.equal(x, y)
