@@ -7,9 +7,9 @@
 // partial results of disjoint key ranges join by.
 //
 // What bounds it (device time in a graph; HBM 6784.5 GB/s as a copy): the bytes of the keys and
-// values over long contexts: 128 sequences of 17 to 16,385 tokens in FP8 321 us, 99% of the copy
-// rate; one of 100,001 in BF16 66.2 us, 91%, the rest being the start (1.6 us of plan, 0.9 us of page
-// lookups) and the join (3 us). Over an NVFP4 cache the arithmetic: 4 sequences of 60,000 to
+// values over long contexts: 128 sequences of 17 to 16,385 tokens in FP8 321 to 326 us, 98% of the
+// copy rate; one of 100,001 in BF16 66.2 us, 91%, the rest being the start (1.6 us of plan, 0.9 us
+// of page lookups) and the join (3 us). Over an NVFP4 cache the arithmetic: 4 sequences of 60,000 to
 // 100,001 tokens 82.3 us, 67%: about 360 warp instructions for 16 keys of one KV head, 128 of them
 // the conversions and the scaling of the codes, which keep the issue slots 66% and the integer
 // pipe 58% busy.
