@@ -52,8 +52,9 @@
 // most 2^-32 of the largest weighted scale for each key. (Z costs NVFP4 2 to 5%, 4 sequences of
 // 60,000 to 100,001 tokens 80.4 -> 82.3 us; over FP8 the stream hides it, but for 16 heads, 39 of
 // 20,236 276 -> 282.) Against 64 bits the outputs over quantised caches are 0.6% further off than
-// with FP32 weights, the rest being their rounding to bf16. q is scaled by a power of two per head in
-// the same manner. The d axis is permuted the same way in q
+// with FP32 weights, the rest being their rounding to bf16. q is scaled by a power of two per head
+// to the top of f16: its bf16 values stay exact down to 2^-31 of the head's largest magnitude, and
+// smaller ones are off by at most 2^-39 of it. The d axis is permuted the same way in q
 // and K, and undone on the output for V, so that a thread's codes are contiguous bytes.
 //
 // Every mbarrier wait is bounded: on expiry the CTA records BEAM_DEV_TIMEOUT, stops issuing, lets

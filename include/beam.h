@@ -384,6 +384,8 @@ beam_status beam_paged_kv_read(const beam_paged_kv* cache, const int32_t* seq_id
  *  pos       0: a padding row that attends to nothing; its output row is zero. A row whose
  *            position or sequence is out of range (pos < 0, > max_pos or past the page table)
  *            sets a bit and is zero too. Keys in a bad page are left out and a bit is set.
+ * Over FP8 and NVFP4 pages elements of q below 2^-31 of their head's largest magnitude are rounded,
+ * by at most 2^-39 of it; all others, and every stored value, enter the products exactly.
  * Infinities and NaN: a NaN in q, or in a key or value that a row reads, makes the outputs that it
  * enters NaN. A logit of -inf weighs nothing (a row whose logits all are gives zero), one of
  * +inf makes its head's outputs NaN. An infinite value (BF16 pages; the other formats hold its

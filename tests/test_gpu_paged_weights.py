@@ -121,3 +121,41 @@ def test_infinities_over_bf16_pages(D, G, n):
         want, mag = p @ V, p @ np.abs(V)
         d = D * 2.0 ** -23 * np.max(np.abs(K) @ np.abs(qh)) / np.sqrt(D)
         assert np.all(np.abs(out[0, 0, g] - want) <= 2.0 ** -8 * np.abs(want) + mag * (2 * d + 2.0 ** -15))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("D,G,big", [(128, 5, 30), (64, 12, 30), (128, 5, 33), (64, 12, 34)])
+def test_query_elements_of_very_different_magnitude(fmt, D, G, big):
+    """One element of q 2^big times the others, where the keys hold nothing or little: over quantised
+    caches the others are f16 relative to it, off by at most 2^-39 of it each (2^14 of f16's 2^-25):
+    a logit by 2^-39 max|q| sum|k| / sqrt(D), which joins the bound's d. Up to 2^31 nothing is lost."""
+    n = 1500
+    cfg = cfg_for(G, 1, D)
+    per = -(-n // 64)
+    c = B.PagedKVCache.empty(per, 64, 1, D, torch.arange(per, dtype=torch.int32, device=DEV)[None], FMT[fmt])
+    k, v = randn(321, n, 1, D), randn(322, n, 1, D)
+    k[:, 0, 3] = 0
+    if big > 31:
+        k[::2, 0, 3] = 2.0 ** -40      # of the BF16 cache only: 0 in a code
+    B.beam_paged_kv_write(k, v, ints([0] * n), ints(list(range(1, n + 1))), c)
+    q = randn(323, 1, G, D)
+    q[0, :, 3] = 2.0 ** big
+    out = np64(attend(cfg, c, q, ints([0]), ints([n]), n))
+    assert status() == 0
+    hc, qn = host(c), np64(q)
+    ref, mag = OP.paged_attention(G, qn, hc, [0], [n])
+    K, V = (x[0] for x in hc.load(0, np.arange(1, n + 1)))
+    for h in range(G):
+        sl = slice(h * D, (h + 1) * D)
+        d = D * 2.0 ** -23 * np.max(np.abs(K) @ np.abs(qn[0, h])) / np.sqrt(D)
+        r, floor = 2.0 ** -15, 0.0
+        if fmt != "bf16":
+            x = K @ qn[0, h] / np.sqrt(D)
+            p = np.exp(x - x.max())
+            p /= p.sum()
+            r, floor = r + 2.0 ** -11, n * 2.0 ** -31 * np.max(p * np.abs(V).max(1))
+            if big > 31:
+                d += 2.0 ** -39 * 2.0 ** big * np.max(np.abs(K).sum(1)) / np.sqrt(D)
+        # weights e^x: a logit's error d moves a normalised weight by a factor of e^(2d) at most
+        tol = 2.0 ** -8 * np.abs(ref[0, sl]) + mag[0, sl] * (np.expm1(2 * d) * (1 + r) + r) + floor
+        assert np.all(np.abs(out[0, sl] - ref[0, sl]) <= tol), h
