@@ -433,6 +433,11 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
       asm("{.reg .b16 b; cvt.u16.u32 b, %1; cvt.rn.bf16x2.ue8m0x2 %0, b;}" : "=r"(f2) : "r"(k2));
       fk[i][0] = bf_lo(f2);
       fk[i][1] = bf_hi(f2);
+      // q's factor here, the key's below: their product alone may leave FP32's range
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sx[i][n][e] *= qs[n][e & 1];
     }
   }
   if (!full) {   // keys that are not the row's weigh nothing, whatever their slots hold
@@ -447,9 +452,7 @@ __device__ __forceinline__ void warp_block(uint32_t kb, const Lane<FMT, C> (&ln)
         for (int n = 0; n < NT; ++n) sx[i][n][2 * h] = sx[i][n][2 * h + 1] = kNegInf;
       }
   }
-  auto factor = [&](int i, int n, int e) {   // of a product, to x
-    return FMT == kFmtBF16 ? qs[n][e & 1] : qs[n][e & 1] * fk[i][e >> 1];
-  };
+  auto factor = [&](int i, int n, int e) { return FMT == kFmtBF16 ? qs[n][e & 1] : fk[i][e >> 1]; };   // from sx to x
   auto weigh = [&] {
 #pragma unroll
     for (int i = 0; i < SPW; ++i)

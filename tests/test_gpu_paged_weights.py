@@ -159,3 +159,21 @@ def test_query_elements_of_very_different_magnitude(fmt, D, G, big):
         # weights e^x: a logit's error d moves a normalised weight by a factor of e^(2d) at most
         tol = 2.0 ** -8 * np.abs(ref[0, sl]) + mag[0, sl] * (np.expm1(2 * d) * (1 + r) + r) + floor
         assert np.all(np.abs(out[0, sl] - ref[0, sl]) <= tol), h
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("qe,ke", [(120, 100), (60, 115), (-120, -100), (-130, 120), (120, -130)])
+def test_logits_of_zero_from_large_and_small_factors(fmt, qe, ke):
+    """Queries and keys of 2^qe and 2^ke in different elements: every product is 0 whatever their powers
+    of two come to together, and the weights are equal."""
+    D, G, n = 128, 5, 300
+    cfg = cfg_for(G, 1, D)
+    c = B.PagedKVCache.empty(10, 32, 1, D, torch.arange(10, dtype=torch.int32, device=DEV)[None], FMT[fmt])
+    k, v = torch.zeros((n, 1, D), dtype=torch.bfloat16, device=DEV), randn(332, n, 1, D)
+    k[:, 0, 5::2] = 2.0 ** ke
+    B.beam_paged_kv_write(k, v, ints([0] * n), ints(list(range(1, n + 1))), c)
+    q = torch.zeros((1, G, D), dtype=torch.bfloat16, device=DEV)
+    q[0, :, 4::2] = 2.0 ** qe
+    out = np64(attend(cfg, c, q, ints([0]), ints([n]), n))
+    assert status() == 0
+    check(cfg, host(c), np64(q), n, out)
