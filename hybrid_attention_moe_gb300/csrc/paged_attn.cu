@@ -51,7 +51,7 @@
 // weighs nothing takes no bits from the others, and what P loses below f16's smallest step is at
 // most 2^-32 of the largest weighted scale for each key. (Z costs NVFP4 2 to 5%, 4 sequences of
 // 60,000 to 100,001 tokens 80.4 -> 82.3 us; over FP8 the stream hides it, but for 16 heads, 39 of
-// 20,236 276 -> 282.) Against 64 bits the outputs over quantised caches are 0.6% further off than
+// 20,236 276 -> 290.) Against 64 bits the outputs over quantised caches are 0.6% further off than
 // with FP32 weights, the rest being their rounding to bf16. q is scaled by a power of two per head
 // to the top of f16: its bf16 values stay exact down to 2^-31 of the head's largest magnitude, and
 // smaller ones are off by at most 2^-39 of it. The d axis is permuted the same way in q
@@ -95,7 +95,7 @@ struct Cfg {
   static constexpr int GROUPS = FMT == kFmtNVFP4 && (D == 128 || NT == 1) ? 3 : 2;
   // over quantised caches q's fragments lie in shared memory, not in 8 to 32 registers: 39 sequences
   // of 20,236 tokens, 8 KV heads of 16 heads: FP8 313 -> 276 us, NVFP4 346 (with two groups) -> 292;
-  // of 8 heads, NVFP4 184 -> 180, 64-wide 136 -> 132 (before the second running max: now 282, 309, 185, 134)
+  // of 8 heads, NVFP4 184 -> 180, 64-wide 136 -> 132 (before the second running max: now 290, 294, 185, 135)
   static constexpr bool QSM = FMT != kFmtBF16;
   static constexpr int WPG = 4, SPW = HEAVY ? 1 : 2;
   // log2 units by which a reference may lag: P <= 2^(kRescale + kBias) in f16, below 65504
