@@ -416,7 +416,7 @@ def run(state):
         return {"append": _plain_append, "tree": _plain_tree, "sample": _plain_sample, "step": _plain_step}[c["op"]](s)
     if c["op"] == "sample":
         from hybrid_attention_moe_gb300 import beam as B
-        B.beam_sample(s["logits"], s["u"], s["token"], s["logprob"], s["temperature"], s["top_k"], s["top_p"], s["min_p"], ws=s["scratch"])
+        B.beam_sample(s["logits"], s["u"], s["token"], s["logprob"], s["temperature"], s["top_k"], s["top_p"], s["min_p"])
         return {"token": s["token"], "logprob": s["logprob"]}
     B, caches, cfg, to = _handle(s)
     if c["op"] == "append":
@@ -458,7 +458,6 @@ def _prepare_sample(c, s, gen, dev):
     s["u"] = torch.rand(rows, generator=gen, device=dev)
     s["token"] = torch.empty(rows, dtype=torch.int32, device=dev)
     s["logprob"] = torch.empty(rows, dtype=torch.float32, device=dev)
-    s["scratch"] = torch.empty(8 << 20, dtype=torch.uint8, device=dev)
     return s
 
 
