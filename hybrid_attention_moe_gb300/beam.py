@@ -20,7 +20,7 @@ BEAM_KV_BF16, BEAM_KV_FP8_E4M3 = 0, 1
 BEAM_ATTN_SWA_ROPE, BEAM_ATTN_NOPE_SSMAX = 0, 1
 BEAM_PAGED_BF16, BEAM_PAGED_FP8, BEAM_PAGED_NVFP4 = 0, 1, 2
 DEV_BAD_POSITION, DEV_BAD_SEQ, DEV_BAD_EXPERT, DEV_TIMEOUT = 0x1, 0x2, 0x4, 0x8
-DEV_BAD_PAGE = 0x10
+DEV_BAD_PAGE, DEV_BAD_LOGITS = 0x10, 0x20
 
 
 class BeamError(RuntimeError):
@@ -82,9 +82,18 @@ _SIGS = {
     "beam_paged_attn": [_P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _Z, _P],
     "beam_paged_workspace_bytes": [_P, _I, _I],
     "beam_paged_kv_bytes": [_I, _I, _I, _I, _I],
+    "beam_paged_append": [_P, _P, _I, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P],
+    "beam_paged_qkv_gate": [_P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _Z, _P],
+    "beam_paged_tree_attn": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _Z, _P],
+    "beam_paged_tree_workspace_bytes": [_P, _I],
+    "beam_tree_plan": [_P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P],
+    "beam_tree_accept": [_P, _P, _P, _P, _I, _I, _P, _P, _I, _P, _P],
+    "beam_paged_kv_keep": [_P, _P, _P, _P, _P, _I, _I, _P],
+    "beam_sample": [_P, ctypes.c_int64, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P],
 }
 _RES = {"beam_workspace_bytes": _Z, "beam_kv_cache_bytes": _Z,
         "beam_paged_workspace_bytes": _Z, "beam_paged_kv_bytes": _Z,
+        "beam_paged_tree_workspace_bytes": _Z,
         "beam_status_string": ctypes.c_char_p, "beam_launch_count": ctypes.c_uint64,
         "beam_last_cuda_error": ctypes.c_char_p}
 
@@ -481,6 +490,196 @@ def beam_paged_attn(cfg: LayerCfg, q, g, gate_bias, cache: PagedKVCache, seq_id,
                                ws.nbytes, _raw_stream(stream, dev))
     if st:
         _check(st, "beam_paged_attn")
+
+
+def _is(t, dev, dtype, n):
+    """Whether t is a contiguous tensor of n elements of a type on the device."""
+    return t.dtype is dtype and t.numel() == n and t.is_contiguous() and t.get_device() == dev
+
+
+def _want_all(device, dtype, n, **tensors):
+    for name, t in tensors.items():
+        _want(device, name, t, dtype, n)
+
+
+def beam_paged_append(cfg: LayerCfg, qkv, q_norm_w, k_norm_w, seq_id, pos, slot, q_out, g_out,
+                      cache: PagedKVCache, stream=None):
+    """Packed projection rows qkv [T][Q | K | V (| gate)] bf16 (elements of a token contiguous, any stride between
+    tokens that is a multiple of 8): queries normed and rotated into q_out [T][n_q][D], gate rows into g_out
+    [T][n_q*D] (None: qkv has none), K and V into the pages. q_norm_w, k_norm_w None: no norm. slot None: pos."""
+    dev, bf, i32 = _on_device(cache), torch.bfloat16, torch.int32
+    n_q, D, T = cfg.n_q, cfg.head_dim, qkv.size(0)
+    row, flat = (n_q * (1 if g_out is None else 2) + 2 * cfg.n_kv) * D, T * n_q * D
+    if (q_norm_w is None) != (k_norm_w is None):
+        raise BeamError("beam_paged_append: q_norm_w and k_norm_w go together")
+    if (qkv.dtype is not bf or qkv.dim() != 2 or qkv.size(1) < row or qkv.get_device() != dev or
+            (T and qkv.stride(1) != 1)):
+        raise BeamError(f"beam_paged_append: qkv must be bfloat16 ({T}, {row} or more) on cuda:{dev}, a token's elements "
+                        f"contiguous, got {qkv.dtype} {tuple(qkv.shape)} with strides {qkv.stride()} on {qkv.device}")
+    if not (_is(seq_id, dev, i32, T) and _is(pos, dev, i32, T) and (slot is None or _is(slot, dev, i32, T)) and
+            _is(q_out, dev, bf, flat) and (g_out is None or _is(g_out, dev, bf, flat)) and
+            (q_norm_w is None or (_is(q_norm_w, dev, bf, D) and _is(k_norm_w, dev, bf, D)))):
+        _want_all(dev, i32, T, seq_id=seq_id, pos=pos, **({} if slot is None else {"slot": slot}))
+        _want_all(dev, bf, flat, q_out=q_out, **({} if g_out is None else {"g_out": g_out}))
+        if q_norm_w is not None:
+            _want_all(dev, bf, D, q_norm_w=q_norm_w, k_norm_w=k_norm_w)
+    st = lib().beam_paged_append(cfg._ref(), qkv.data_ptr(), qkv.stride(0) if T > 1 else max(row, qkv.size(1) // 8 * 8),
+                                 None if q_norm_w is None else q_norm_w.data_ptr(),
+                                 None if k_norm_w is None else k_norm_w.data_ptr(), seq_id.data_ptr(),
+                                 pos.data_ptr(), None if slot is None else slot.data_ptr(), T, q_out.data_ptr(),
+                                 None if g_out is None else g_out.data_ptr(), cache._ref, _raw_stream(stream, dev))
+    if st:
+        _check(st, "beam_paged_append")
+
+
+def beam_paged_qkv_gate(cfg: LayerCfg, u, w_qkvg, q_norm_w, k_norm_w, seq_id, pos, slot, q_out, g_out,
+                        cache: PagedKVCache, ws: torch.Tensor, stream=None):
+    """beam_qkv_gate over a paged cache; slot None: pos."""
+    dev, bf, i32 = _on_device(cache), torch.bfloat16, torch.int32
+    T, H, n_q, D = u.size(0), cfg.hidden, cfg.n_q, cfg.head_dim
+    _want(dev, "u", u, bf, (T, H))
+    _want(dev, "w_qkvg", w_qkvg, bf, ((2 * n_q + 2 * cfg.n_kv) * D, H))
+    _want_all(dev, bf, D, q_norm_w=q_norm_w, k_norm_w=k_norm_w)
+    _want_all(dev, i32, T, seq_id=seq_id, pos=pos, **({} if slot is None else {"slot": slot}))
+    _want_all(dev, bf, T * n_q * D, q_out=q_out, g_out=g_out)
+    _want(dev, "ws", ws, ws.dtype, ws.numel())
+    st = lib().beam_paged_qkv_gate(cfg._ref(), u.data_ptr(), w_qkvg.data_ptr(), q_norm_w.data_ptr(), k_norm_w.data_ptr(),
+                                   seq_id.data_ptr(), pos.data_ptr(), None if slot is None else slot.data_ptr(), T,
+                                   q_out.data_ptr(), g_out.data_ptr(), cache._ref, ws.data_ptr(), ws.nbytes,
+                                   _raw_stream(stream, dev))
+    if st:
+        _check(st, "beam_paged_qkv_gate")
+
+
+def paged_tree_workspace_bytes(cfg: LayerCfg, T: int) -> int:
+    return lib().beam_paged_tree_workspace_bytes(cfg._ref(), T)
+
+
+def beam_paged_tree_attn(cfg: LayerCfg, q, g, gate_bias, cache: PagedKVCache, seq_id, row_start, base, mask, max_pos,
+                         w_o, out, ws: torch.Tensor, stream=None):
+    """Attention of drafted trees over the pages: rows row_start[i] .. row_start[i+1]-1 (row_start [N+1]) are the nodes
+    of sequence seq_id[i] behind its base[i] tokens; mask [T] int64. q, g [T][n_q][D] or [T][n_q*D]; g, gate_bias
+    None: no gate; out [T][hidden], or of q's shapes where w_o is None."""
+    dev, bf, i32 = _on_device(cache), torch.bfloat16, torch.int32
+    T, N, n_q = q.size(0), seq_id.numel(), cfg.n_q
+    row = n_q * cfg.head_dim
+    width = row if w_o is None else cfg.hidden
+    heads, flat = (T, n_q, cfg.head_dim), (T, row)
+    if (g is None) != (gate_bias is None):
+        raise BeamError("beam_paged_tree_attn: g and gate_bias go together")
+    if not (_is(q, dev, bf, T * row) and (q.shape == heads or q.shape == flat) and out.dtype is bf and
+            (out.shape == (T, width) or (w_o is None and out.shape == heads)) and out.is_contiguous() and
+            out.get_device() == dev and _is(seq_id, dev, i32, N) and _is(base, dev, i32, N) and
+            _is(row_start, dev, i32, N + 1) and _is(mask, dev, torch.int64, T) and ws.is_contiguous() and
+            ws.get_device() == dev):
+        _want(dev, "q", q, bf, heads, flat)
+        _want(dev, "out", out, bf, (T, width), *([heads] if w_o is None else []))
+        _want_all(dev, i32, N, seq_id=seq_id, base=base)
+        _want(dev, "row_start", row_start, i32, N + 1)
+        _want(dev, "mask", mask, torch.int64, T)
+        _want(dev, "ws", ws, ws.dtype, ws.numel())
+    pg = pb = pw = None
+    if g is not None:
+        if not (_is(g, dev, bf, T * row) and (g.shape == flat or g.shape == heads) and _is(gate_bias, dev, bf, n_q)):
+            _want(dev, "g", g, bf, flat, heads)
+            _want(dev, "gate_bias", gate_bias, bf, n_q)
+        pg, pb = g.data_ptr(), gate_bias.data_ptr()
+    if w_o is not None:
+        _want(dev, "w_o", w_o, bf, (width, row))
+        pw = w_o.data_ptr()
+    st = lib().beam_paged_tree_attn(cfg._ref(), q.data_ptr(), pg, pb, cache._ref, seq_id.data_ptr(),
+                                    row_start.data_ptr(), base.data_ptr(), mask.data_ptr(), N, T, int(max_pos), pw,
+                                    out.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream, dev))
+    if st:
+        _check(st, "beam_paged_tree_attn")
+
+
+def _current(t, what):
+    """The device of t, which has to be the current one: the library launches there."""
+    dev = torch._C._cuda_getDevice() if t.is_cuda else -1
+    if t.get_device() != dev or dev < 0:
+        raise BeamError(f"{what}: the tensors must be on the current CUDA device, got {t.device}")
+    return dev
+
+
+def beam_tree_plan(parent, row_start, seq_id, base, mask, pos, slot, row_seq, stream=None):
+    """From each node's parent (its index in its own tree, -1 for a root): mask [T] int64 of its ancestors and
+    itself, pos, slot and row_seq [T], as beam_paged_append and beam_paged_tree_attn take them."""
+    dev, i32 = _current(parent, "beam_tree_plan"), torch.int32
+    T, N = parent.numel(), seq_id.numel()
+    if not (_is(parent, dev, i32, T) and _is(row_start, dev, i32, N + 1) and _is(seq_id, dev, i32, N) and
+            _is(base, dev, i32, N) and _is(mask, dev, torch.int64, T) and _is(pos, dev, i32, T) and
+            _is(slot, dev, i32, T) and _is(row_seq, dev, i32, T)):
+        _want_all(dev, i32, T, parent=parent, pos=pos, slot=slot, row_seq=row_seq)
+        _want_all(dev, i32, N, seq_id=seq_id, base=base)
+        _want(dev, "row_start", row_start, i32, N + 1)
+        _want(dev, "mask", mask, torch.int64, T)
+    st = lib().beam_tree_plan(parent.data_ptr(), row_start.data_ptr(), seq_id.data_ptr(), base.data_ptr(), N, T,
+                              mask.data_ptr(), pos.data_ptr(), slot.data_ptr(), row_seq.data_ptr(),
+                              _raw_stream(stream, dev))
+    if st:
+        _check(st, "beam_tree_plan")
+
+
+def beam_tree_accept(parent, token, sampled, row_start, count, path, next, stream=None):
+    """The path from node 0 of each tree along the sampled tokens: count [N], path [N][any] (indices, then -1), and the
+    token sampled at its end, next [N]."""
+    dev, i32 = _current(parent, "beam_tree_accept"), torch.int32
+    T, N = parent.numel(), count.numel()
+    if path.dim() != 2 or path.size(0) != N:
+        raise BeamError(f"beam_tree_accept: path must be [{N}][most nodes], got {tuple(path.shape)}")
+    if not (_is(parent, dev, i32, T) and _is(token, dev, i32, T) and _is(sampled, dev, i32, T) and
+            _is(row_start, dev, i32, N + 1) and _is(count, dev, i32, N) and _is(next, dev, i32, N) and
+            _is(path, dev, i32, path.numel())):
+        _want_all(dev, i32, T, parent=parent, token=token, sampled=sampled)
+        _want_all(dev, i32, N, count=count, next=next)
+        _want(dev, "row_start", row_start, i32, N + 1)
+        _want(dev, "path", path, i32, path.numel())
+    st = lib().beam_tree_accept(parent.data_ptr(), token.data_ptr(), sampled.data_ptr(), row_start.data_ptr(), N, T,
+                                count.data_ptr(), path.data_ptr(), path.size(1), next.data_ptr(),
+                                _raw_stream(stream, dev))
+    if st:
+        _check(st, "beam_tree_accept")
+
+
+def beam_paged_kv_keep(cache: PagedKVCache, seq_id, base, count, path, stream=None):
+    """Moves the rows of the accepted nodes path[i][:count[i]] to the front of the tree's slots, behind the base[i]
+    tokens of sequence seq_id[i]."""
+    dev, i32 = _on_device(cache), torch.int32
+    N = seq_id.numel()
+    if path.dim() != 2 or path.size(0) != N:
+        raise BeamError(f"beam_paged_kv_keep: path must be [{N}][most nodes], got {tuple(path.shape)}")
+    if not (_is(seq_id, dev, i32, N) and _is(base, dev, i32, N) and _is(count, dev, i32, N) and
+            _is(path, dev, i32, path.numel())):
+        _want_all(dev, i32, N, seq_id=seq_id, base=base, count=count)
+        _want(dev, "path", path, i32, path.numel())
+    st = lib().beam_paged_kv_keep(cache._ref, seq_id.data_ptr(), base.data_ptr(), count.data_ptr(), path.data_ptr(),
+                                  path.size(1), N, _raw_stream(stream, dev))
+    if st:
+        _check(st, "beam_paged_kv_keep")
+
+
+def beam_sample(logits, u, token, logprob=None, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """One token per row of logits [T][V] fp32 (elements of a row contiguous) from u [T] fp32 in [0, 1): token [T] int32
+    and, unless None, logprob [T] fp32. temperature, top_p, min_p [T] fp32 and top_k [T] int32 on the device, or None."""
+    f32, i32 = torch.float32, torch.int32
+    dev, T = _current(logits, "beam_sample"), logits.size(0)
+    if logits.dtype is not f32 or logits.dim() != 2 or (logits.numel() and logits.stride(1) != 1):
+        raise BeamError(f"beam_sample: logits must be float32 (T, V), a row's elements contiguous, got {logits.dtype} "
+                        f"{tuple(logits.shape)} with strides {logits.stride()}")
+    floats = {"u": u, "logprob": logprob, "temperature": temperature, "top_p": top_p, "min_p": min_p}
+    ints = {"token": token, "top_k": top_k}
+    for dtype, group in ((f32, floats), (i32, ints)):
+        for name, x in group.items():
+            if (x is not None or name in ("u", "token")) and not _is(x, dev, dtype, T):
+                _want(dev, name, x, dtype, T)
+    ptr = {name: None if x is None else x.data_ptr() for name, x in (*floats.items(), *ints.items())}
+    V = logits.size(1)
+    st = lib().beam_sample(logits.data_ptr(), logits.stride(0) if T > 1 else V, T, V, ptr["u"], ptr["temperature"],
+                           ptr["top_k"], ptr["top_p"], ptr["min_p"], ptr["token"], ptr["logprob"],
+                           _raw_stream(stream, dev))
+    if st:
+        _check(st, "beam_sample")
 
 
 class NvFp4ExpertsC(ctypes.Structure):

@@ -25,45 +25,9 @@ struct WriteParams {
   int shift;      // log2(page_size)
 };
 
-// Where a token's rows go: the page, or -1 (padding, or out of range: the bit to set in bad).
-__device__ __forceinline__ int page_of(const beam_paged_kv& c, int s, int p, int shift,
-                                       unsigned& bad) {
-  bad = 0;
-  if (p == 0) return -1;
-  if (p < 0 || ((p - 1) >> shift) >= c.table_stride) {
-    bad = BEAM_DEV_BAD_POSITION;
-    return -1;
-  }
-  if (s < 0 || s >= c.num_seqs) {
-    bad = BEAM_DEV_BAD_SEQ;
-    return -1;
-  }
-  const int pg = c.page_table[size_t(s) * c.table_stride + ((p - 1) >> shift)];
-  if (pg < 0 || pg >= c.num_pages) {
-    bad = BEAM_DEV_BAD_PAGE;
-    return -1;
-  }
-  return pg;
-}
-
-// x to 14 significant bits (to nearest, ties away from zero).
-__device__ __forceinline__ float round14(float x) {
-  return __uint_as_float((__float_as_uint(x) + 0x200u) & 0xFFFFFC00u);
-}
-
 // A warp takes up to kHeads KV heads of one token, K and V, and issues all its loads before the
 // page is looked up. A lane holds 16 elements of a row (an NVFP4 block; a BF16 row, which is only
-// moved, is taken 8 a lane). The row's largest magnitude is an integer maximum of the bf16
-// patterns without their signs (they order like the values, and infinities and NaNs come out on
-// top); the row's power of two follows from that pattern's exponent and fraction alone, so
-// nothing is rounded before the codes are.
-//
-// Quotients by s are taken with a reciprocal and rounded to f16. A quotient that is a midpoint of
-// two codes (3 bits) comes back exactly; any other one is 2^-8 of the midpoint or more away from it
-// (the dividend has 8 bits, s 4), which the reciprocal's error (2^-21) and half a step of f16
-// (2^-11) do not reach, so the code is that of the exact quotient. The sixth of the block's largest
-// value is rounded to 14 bits in the same manner: a midpoint of e4m3 has 5 bits, and any other
-// sixth is 2^-8 of it away (the dividend has 8 bits, 6 midpoints 7).
+// moved, is taken 8 a lane).
 constexpr int kHeads = 8;
 template <int FMT, int D>
 __global__ void __launch_bounds__(128, 8) paged_write_kernel(const WriteParams P) {
@@ -100,21 +64,15 @@ __global__ void __launch_bounds__(128, 8) paged_write_kernel(const WriteParams P
     if constexpr (FMT == kFmtBF16) {
       if (store) *reinterpret_cast<uint4*>(dst + sub * 16) = x[u][0];
     } else {
-      // largest magnitudes of even and odd elements, as two bf16 patterns
-      constexpr unsigned kAbs = 0x7FFF7FFFu;
-      unsigned mx = 0;
+      unsigned mx = 0;   // largest patterns of even and odd elements
 #pragma unroll
-      for (int a = 0; a < NV; ++a)
-        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x[u][a].x & kAbs, x[u][a].y & kAbs),
-                                   __vmaxu2(x[u][a].z & kAbs, x[u][a].w & kAbs)));
+      for (int a = 0; a < NV; ++a) mx = __vmaxu2(mx, abs_max(x[u][a]));
       const unsigned bm = max(mx & 0xFFFFu, mx >> 16);   // of the block of 16
       unsigned rm = bm;
 #pragma unroll
       for (int o = 1; o < LPR; o <<= 1) rm = max(rm, __shfl_xor_sync(0xffffffffu, rm, o));
       const bool finite = rm < 0x7F80u;
-      // most = 448 = 1.75 * 2^8 (fraction 96 / 128), or 2688 = 1.3125 * 2^11 (fraction 40 / 128)
-      constexpr int kExp = FMT == kFmtFP8 ? 8 : 11, kFrac = FMT == kFmtFP8 ? 96 : 40;
-      const int b = max(0, int(rm >> 7) - kExp + (int(rm & 127u) > kFrac ? 1 : 0));
+      const int b = row_byte<FMT>(rm);
       float inv = __uint_as_float(unsigned(254 - b) << 23);   // 2^(127 - b)
       float y[EPL];
 #pragma unroll
@@ -123,18 +81,13 @@ __global__ void __launch_bounds__(128, 8) paged_write_kernel(const WriteParams P
         uint32_t w[EPL / 4];
 #pragma unroll
         for (int i = 0; i < EPL / 4; ++i) {
-          const float* z = y + 4 * i;
-          w[i] = uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(z[0] * inv, z[1] * inv), __NV_SATFINITE, __NV_E4M3)) |
-                 uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(z[2] * inv, z[3] * inv), __NV_SATFINITE, __NV_E4M3)) << 16;
+          w[i] = fp8x4(y + 4 * i, inv);
           if (!finite) w[i] = 0u;
         }
         if (store) *reinterpret_cast<uint4*>(dst + sub * EPL) = make_uint4(w[0], w[1], w[2], w[3]);
       } else {
-        const float q6 = round14(__uint_as_float(bm << 16) * inv * (1.f / 6.f));
-        const unsigned s = finite ? __nv_cvt_float_to_fp8(q6, __NV_SATFINITE, __NV_E4M3) : 0u;
-        float sf, rs, unused;
-        unpack_f16(e4m3x2_f16x2(s), sf, unused);
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(sf));
+        float rs;
+        const unsigned s = block_scale_of(bm, inv, finite, rs);
         if (b < 16) {   // 2^(127 - b) / s may pass FP32's range: part of it goes to the elements
           inv *= 0x1p-32f;
 #pragma unroll
@@ -144,15 +97,7 @@ __global__ void __launch_bounds__(128, 8) paged_write_kernel(const WriteParams P
         uint32_t w[EPL / 8];
 #pragma unroll
         for (int i = 0; i < EPL / 8; ++i) {
-          uint32_t q[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) q[e] = pack_f16x2(y[8 * i + 2 * e] * rs, y[8 * i + 2 * e + 1] * rs);
-          asm("{.reg .b8 a, b, c, d;"
-              " cvt.rn.satfinite.e2m1x2.f16x2 a, %1; cvt.rn.satfinite.e2m1x2.f16x2 b, %2;"
-              " cvt.rn.satfinite.e2m1x2.f16x2 c, %3; cvt.rn.satfinite.e2m1x2.f16x2 d, %4;"
-              " mov.b32 %0, {a, b, c, d};}"
-              : "=r"(w[i])
-              : "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3]));
+          w[i] = fp4x8(y + 8 * i, rs);
           if (s == 0) w[i] = 0u;   // the block is zeros, or the row holds no numbers
         }
         if (store) {

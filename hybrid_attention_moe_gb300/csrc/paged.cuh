@@ -90,5 +90,81 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// Where a token's rows go: the page of its 1-based slot p, or -1 (padding, or out of range: the bit to
+// set in bad).
+__device__ __forceinline__ int page_of(const beam_paged_kv& c, int s, int p, int shift,
+                                       unsigned& bad) {
+  bad = 0;
+  if (p == 0) return -1;
+  if (p < 0 || ((p - 1) >> shift) >= c.table_stride) {
+    bad = BEAM_DEV_BAD_POSITION;
+    return -1;
+  }
+  if (s < 0 || s >= c.num_seqs) {
+    bad = BEAM_DEV_BAD_SEQ;
+    return -1;
+  }
+  const int pg = c.page_table[size_t(s) * c.table_stride + ((p - 1) >> shift)];
+  if (pg < 0 || pg >= c.num_pages) {
+    bad = BEAM_DEV_BAD_PAGE;
+    return -1;
+  }
+  return pg;
+}
+
+// ---- rows to codes. Magnitudes are compared as bf16 patterns without their signs (they order like
+// the values, and infinities and NaNs come out on top); a row's power of two follows from the largest
+// pattern's exponent and fraction alone, so nothing is rounded before the codes are.
+
+// The larger patterns of even and odd elements of two registers of four words.
+__device__ __forceinline__ unsigned abs_max(const uint4& x) {
+  constexpr unsigned kAbs = 0x7FFF7FFFu;
+  return __vmaxu2(__vmaxu2(x.x & kAbs, x.y & kAbs), __vmaxu2(x.z & kAbs, x.w & kAbs));
+}
+// The byte of a row with the largest pattern rm: most = 448 = 1.75 * 2^8 (fraction 96 / 128), or
+// 2688 = 1.3125 * 2^11 (fraction 40 / 128).
+template <int FMT>
+__device__ __forceinline__ int row_byte(unsigned rm) {
+  constexpr int kExp = FMT == kFmtFP8 ? 8 : 11, kFrac = FMT == kFmtFP8 ? 96 : 40;
+  return max(0, int(rm >> 7) - kExp + (int(rm & 127u) > kFrac ? 1 : 0));
+}
+// Four e4m3 codes of y * inv.
+__device__ __forceinline__ uint32_t fp8x4(const float* y, float inv) {
+  return uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(y[0] * inv, y[1] * inv), __NV_SATFINITE, __NV_E4M3)) |
+         uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(y[2] * inv, y[3] * inv), __NV_SATFINITE, __NV_E4M3)) << 16;
+}
+// x to 14 significant bits (to nearest, ties away from zero).
+__device__ __forceinline__ float round14(float x) {
+  return __uint_as_float((__float_as_uint(x) + 0x200u) & 0xFFFFFC00u);
+}
+// The e4m3 scale s of a block of 16 with the largest pattern bm (inv = 2^(127 - b)), and rs = 1 / s. The
+// sixth of the block's largest value is rounded to 14 bits on its way: a midpoint of e4m3 has 5 bits, and
+// any other sixth is 2^-8 of it away (the dividend has 8 bits, 6 midpoints 7).
+__device__ __forceinline__ unsigned block_scale_of(unsigned bm, float inv, bool finite, float& rs) {
+  const float q6 = round14(__uint_as_float(bm << 16) * inv * (1.f / 6.f));
+  const unsigned s = finite ? __nv_cvt_float_to_fp8(q6, __NV_SATFINITE, __NV_E4M3) : 0u;
+  float sf, unused;
+  unpack_f16(e4m3x2_f16x2(s), sf, unused);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(sf));
+  return s;
+}
+// Eight e2m1 codes of y * rs, rs the reciprocal of the block's scale times the row's power of two.
+// Quotients are rounded to f16 on their way. One that is a midpoint of two codes (3 bits) comes back exactly; any
+// other one is 2^-8 of the midpoint or more away from it (the dividend has 8 bits, s 4), which the
+// reciprocal's error (2^-21) and half a step of f16 (2^-11) do not reach, so the code is that of the
+// exact quotient.
+__device__ __forceinline__ uint32_t fp4x8(const float* y, float rs) {
+  uint32_t q[4], w;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) q[e] = pack_f16x2(y[2 * e] * rs, y[2 * e + 1] * rs);
+  asm("{.reg .b8 a, b, c, d;"
+      " cvt.rn.satfinite.e2m1x2.f16x2 a, %1; cvt.rn.satfinite.e2m1x2.f16x2 b, %2;"
+      " cvt.rn.satfinite.e2m1x2.f16x2 c, %3; cvt.rn.satfinite.e2m1x2.f16x2 d, %4;"
+      " mov.b32 %0, {a, b, c, d};}"
+      : "=r"(w)
+      : "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3]));
+  return w;
+}
+
 }  // namespace paged
 }  // namespace beam

@@ -59,6 +59,7 @@ typedef enum {
 #define BEAM_DEV_BAD_EXPERT 0x4u    /* expert index outside [0, n_experts) */
 #define BEAM_DEV_TIMEOUT 0x8u       /* a bounded on-device wait expired (result invalid) */
 #define BEAM_DEV_BAD_PAGE 0x10u     /* page table entry outside [0, num_pages) where a key is due */
+#define BEAM_DEV_BAD_LOGITS 0x20u   /* a row of logits with a NaN, +inf, or nothing above -inf */
 
 typedef enum { BEAM_KV_BF16 = 0, BEAM_KV_FP8_E4M3 = 1 } beam_kv_dtype;
 
@@ -291,6 +292,26 @@ beam_status beam_gemm_bf16(const beam_bf16* A, int M, int K, int lda, const beam
 beam_status beam_lm_head(const beam_bf16* u, const beam_bf16* w_lm, int T, int H, int V,
                          float softcap, float* logits, beam_stream_t stream);
 
+/* One token per row of logits, from given uniform random numbers. (The Beam page names no sampler.)
+ * With z the row and t its temperature, w_i = e^(z_i / t). Tokens in descending order of z, equal ones by
+ * index: the first top_k are kept; of these the fewest, from the front, whose weights hold top_p of theirs; of these
+ * the ones with w_i >= min_p * max w. The token is the first, by index, at which the running sum of the
+ * kept weights passes u times their sum. Sums are exact over weights of 2^-29 relative error, so the
+ * token hangs on no order of summation and is the same on every run and in every batch.
+ *  logits    (device) [T] rows of V fp32, row_stride elements apart (>= V). -inf weighs nothing.
+ *  u         (device) [T] fp32 in [0, 1); taken as 0 below and as the last kept token from 1 on.
+ *  temperature (device) [T] fp32, finite; below 1e-30 (0) the token is the largest logit's. NULL: 1.
+ *  top_k     (device) [T] int32; <= 0: all. NULL: all.
+ *  top_p     (device) [T] fp32; >= 1: all. NULL: all. At least one token is kept.
+ *  min_p     (device) [T] fp32; <= 0: all. NULL: all. The largest logits are always kept.
+ *  token     (device) [T] int32;  logprob (device) [T] fp32 or NULL: the log of the token's share of the kept
+ *            weights.
+ * A row with a NaN, +inf, or nothing above -inf sets BEAM_DEV_BAD_LOGITS; its token is -1, its logprob NaN.
+ * V up to 851,968. No workspace. */
+beam_status beam_sample(const float* logits, int64_t row_stride, int T, int V, const float* u,
+                        const float* temperature, const int32_t* top_k, const float* top_p,
+                        const float* min_p, int32_t* token, float* logprob, beam_stream_t stream);
+
 /* Workspace bytes that every call above needs for T tokens and positions up to max_pos. */
 size_t beam_workspace_bytes(const beam_layer_cfg* cfg, int T, int max_pos);
 
@@ -360,6 +381,35 @@ beam_status beam_paged_kv_write(const beam_bf16* k, const beam_bf16* v, int toke
                                 const int32_t* seq_id, const int32_t* pos, int T,
                                 const beam_paged_kv* cache, beam_stream_t stream);
 
+/* New tokens of a paged layer from the packed projection's rows: per-head Q/K RMSNorm, RoPE or the
+ * SSMax query scale (cfg->kind), and the K and V rows into the pages, as beam_qkv_gate does for
+ * beam_kv_cache. K is rounded to bf16 before it is quantised, so the pages hold what beam_paged_kv_write
+ * of that row stores.
+ *  qkv       (device) bf16: token t's rows Q | K | V (| gate), head-major, start at t * token_stride
+ *            (elements, a multiple of 8, at least the rows' length); 16-byte aligned.
+ *  q_norm_w, k_norm_w (device) [D] bf16 gains, 16-byte aligned; both NULL: no norm.
+ *  pos       (device) [T] int32: positions, which the rotation or scale goes by.
+ *  slot      (device) [T] int32: the 1-based places in the page table that the rows go to; NULL: pos.
+ *            They differ for the nodes of a drafted tree. slot 0: a padding row, nothing is written.
+ *            Out of range (slot, pos < 0, seq_id, page): nothing is written, a bit is set.
+ *  q_out     (device) [T][n_q][D];  g_out (device) [T][n_q*D]: the gate rows, copied; NULL: qkv has
+ *            none. Both are written for every row, padding among them.
+ * No two tokens of a call may name the same slot of a sequence. No workspace. */
+beam_status beam_paged_append(const beam_layer_cfg* cfg, const beam_bf16* qkv, int token_stride,
+                              const beam_bf16* q_norm_w, const beam_bf16* k_norm_w,
+                              const int32_t* seq_id, const int32_t* pos, const int32_t* slot, int T,
+                              beam_bf16* q_out, beam_bf16* g_out, const beam_paged_kv* cache,
+                              beam_stream_t stream);
+
+/* beam_qkv_gate over a paged cache: the packed projection, rounded to bf16, then beam_paged_append.
+ *  ws        beam_workspace_bytes(cfg, T, max_pos) bytes. */
+beam_status beam_paged_qkv_gate(const beam_layer_cfg* cfg, const beam_bf16* u,
+                                const beam_bf16* w_qkvg, const beam_bf16* q_norm_w,
+                                const beam_bf16* k_norm_w, const int32_t* seq_id,
+                                const int32_t* pos, const int32_t* slot, int T, beam_bf16* q_out,
+                                beam_bf16* g_out, const beam_paged_kv* cache, void* ws,
+                                size_t ws_bytes, beam_stream_t stream);
+
 /* Reads positions first[i] .. last[i] of sequence seq_id[i], i < N, back into a contiguous BF16
  * cache, the form that beam_attn's prefill takes: row i of dst, slot (p-1) % dst->capacity.
  *  seq_id, first, last (device) [N] int32; last < first reads nothing. A range that starts
@@ -402,6 +452,73 @@ beam_status beam_paged_attn(const beam_layer_cfg* cfg, const beam_bf16* q, const
 /* Workspace bytes of beam_paged_attn: at most 8 MiB, and T * n_q * head_dim * 2 more for the
  * input of o_proj. */
 size_t beam_paged_workspace_bytes(const beam_layer_cfg* cfg, int T, int max_pos);
+
+/* ---- a drafted tree over the paged cache --------------------------------------------------
+ * Speculative decoding verifies a tree of drafted tokens in one call. (The Beam page's DFlash2
+ * section verifies drafts; trees, and these calls, are this library's own.) A call holds N sequences; rows
+ * row_start[i] .. row_start[i+1]-1 are the nodes 0, 1, ... of sequence i's tree, at most 64,
+ * parents before their children. Node j lies in slot base[i] + 1 + j of the page table's sequence
+ * seq_id[i], behind the base[i] tokens that are its context; its position is base[i] plus its
+ * depth (a root's is 1). row_start [N+1] must not decrease; rows before row_start[0] and from row_start[N]
+ * on are padding. */
+
+/* Masks, positions and slots of the trees' rows from their parents.
+ *  parent    (device) [T] int32: the parent's index in the row's own tree, -1 for a root.
+ *  mask      (device) [T] 64-bit words, 8-byte aligned: bit j set for node j, an ancestor or the row itself.
+ *  pos, slot, row_seq (device) [T] int32: base + depth, base + 1 + index, and the sequence of each row, as
+ *            beam_paged_append takes them.
+ * Padding rows, and rows of a sequence of more than 64 or out-of-range rows (which sets BEAM_DEV_BAD_SEQ),
+ * get zeros. A node whose parent is not an earlier one sets BEAM_DEV_BAD_POSITION; it and its
+ * descendants get mask, pos and slot 0. */
+beam_status beam_tree_plan(const int32_t* parent, const int32_t* row_start, const int32_t* seq_id,
+                           const int32_t* base, int N, int T, uint64_t* mask, int32_t* pos,
+                           int32_t* slot, int32_t* row_seq, beam_stream_t stream);
+
+/* The path of each tree that verification accepts: from node 0 (the token that the last step sampled) to the
+ * child whose drafted token is the one sampled at its parent (the lowest index of several), and on.
+ *  token, sampled (device) [T] int32: each node's drafted token, and the one sampled from its logits.
+ *  count     (device) [N] int32: nodes of the path, 0 for an empty tree.
+ *  path      (device) [N][path_stride] int32: their indices in order, then -1. A longer path is cut off
+ *            there (count is not).
+ *  next      (device) [N] int32: the token sampled at the path's last node, the next step's node 0; -1 for
+ *            an empty tree. */
+beam_status beam_tree_accept(const int32_t* parent, const int32_t* token, const int32_t* sampled,
+                             const int32_t* row_start, int N, int T, int32_t* count, int32_t* path,
+                             int path_stride, int32_t* next, beam_stream_t stream);
+
+/* Moves the accepted nodes' rows, K and V, to the front: of sequence seq_id[i], the row in slot
+ * base[i] + 1 + path[i][k] to slot base[i] + 1 + k, for k < count[i]; all as if at once. The sequence then
+ * holds base[i] + count[i] tokens. A count that is negative or above 64 or path_stride, a path index outside
+ * 0 .. 63, or a slot that is out of range sets a bit; that row (with a bad count, that sequence) is left. The
+ * sequences of a call must differ. */
+beam_status beam_paged_kv_keep(const beam_paged_kv* cache, const int32_t* seq_id,
+                               const int32_t* base, const int32_t* count, const int32_t* path,
+                               int path_stride, int N, beam_stream_t stream);
+
+/* GQA attention of a tree's rows over the pages, optional sigmoid output gate and o_proj: as beam_paged_attn,
+ * but row t of sequence i, with mask m = mask[t], attends to the context 1 .. base[i] and to the
+ * nodes j whose bit j is set in m (its ancestors and itself). Its position is p = base[i] + popcount(m);
+ * with a window W it attends to context positions above p - W, and to the W highest bits of m.
+ * The keys of all nodes must have been written.
+ *  mask      (device) [T] 64-bit words, 8-byte aligned. Bits from the tree's size on are ignored. 0: a padding
+ *            row; it, and every other padding row, gives zero.
+ *  max_pos   host-side upper bound of base[i] + the tree's size.
+ * A sequence whose rows are more than 64 or out of range, or with a bad seq_id, sets
+ * BEAM_DEV_BAD_SEQ, one with base < 0 or past max_pos or the page table BEAM_DEV_BAD_POSITION; its
+ * rows are zero. Keys in a bad page are left out and BEAM_DEV_BAD_PAGE is set.
+ * Infinities and NaN as in beam_paged_attn; a row takes none from keys that it does not attend to.
+ *  w_o       (device) [H][n_q*D] bf16: out = og W_o^T, [T][H]; NULL: out = og, [T][n_q*D].
+ *  ws        beam_paged_tree_workspace_bytes(cfg, T) bytes. */
+beam_status beam_paged_tree_attn(const beam_layer_cfg* cfg, const beam_bf16* q, const beam_bf16* g,
+                                 const beam_bf16* gate_bias, const beam_paged_kv* cache,
+                                 const int32_t* seq_id, const int32_t* row_start,
+                                 const int32_t* base, const uint64_t* mask, int N, int T,
+                                 int max_pos, const beam_bf16* w_o, beam_bf16* out, void* ws,
+                                 size_t ws_bytes, beam_stream_t stream);
+
+/* Workspace bytes of beam_paged_tree_attn: 60 MiB at head_dim 128, half of it at 64, and T * n_q * head_dim * 2 more
+ * for the input of o_proj. */
+size_t beam_paged_tree_workspace_bytes(const beam_layer_cfg* cfg, int T);
 
 /* Bytes of a paged cache of num_pages pages, scales included (the page table is not). */
 size_t beam_paged_kv_bytes(int num_pages, int n_kv, int page_size, int head_dim, int dtype);
