@@ -592,6 +592,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       const RowView v = view_of(P, it.s, node);
       const size_t at = (size_t(it.s.row0 + (real ? node : 0)) * P.n_q + hq) * D;
       const bool work = __any_sync(0xffffffffu, v.tree != 0);   // any row that sees keys
+      const bool none = __any_sync(0xffffffffu, real && v.tree == 0);   // a row among them that sees nothing
       if (units > 0) {
 #pragma unroll 1
         for (int x = 0; x < D / 64; ++x) {
@@ -612,7 +613,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       for (int k = 0; k < units; ++k, ++un) {
         const int j = it.j0 + (it.w == 2 ? k : 2 * k + s);
         const unsigned slices = slices_of(P, it.s, j);
-        const bool full = slices == 15u && whole_block(P, it.s, j);
+        const bool full = !none && slices == 15u && whole_block(P, it.s, j);
         if (!all(mbar_wait(s_full + 8 * s, un & 1))) { ok = false; break; }
         tc_fence_after();
         if (work) {
@@ -1008,7 +1009,6 @@ extern "C" beam_status beam_paged_tree_attn(const beam_layer_cfg* cfg, const bea
   if (!aligned16(q) || !aligned16_or_null(g) || !aligned16_or_null(w_o) || !aligned16(out) ||
       (reinterpret_cast<uintptr_t>(ws) & 255u) || (reinterpret_cast<uintptr_t>(mask) & 7u))
     return BEAM_ERR_INVALID_ARG;
-  if (!tc::tensor_map_encoder_ready()) return BEAM_ERR_UNSUPPORTED;
   const int D = cfg->head_dim, HD = cfg->n_q * D, G = cfg->n_q / cfg->n_kv;
   // most blocks of a sequence: costs are 32-bit
   const int64_t table = int64_t(cache->table_stride) * cache->page_size;
@@ -1026,6 +1026,7 @@ extern "C" beam_status beam_paged_tree_attn(const beam_layer_cfg* cfg, const bea
   p.flush = cv.take<float>(size_t(kGrid) * 2 * ROWS * D);
   uint16_t* og = w_o ? cv.take<uint16_t>(size_t(T) * HD) : out;
   if (!cv.ok) return BEAM_ERR_INVALID_ARG;
+  if (!tc::tensor_map_encoder_ready()) return BEAM_ERR_UNSUPPORTED;
   p.q = q;
   p.g = g;
   p.gate_bias = gate_bias;

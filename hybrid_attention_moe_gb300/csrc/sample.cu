@@ -273,7 +273,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const Params P) {
     }
     if (run > target && run - v <= target) {
       P.token[r] = i0 + i;
-      if (P.logprob) P.logprob[r] = float(log1p(-double(total - v) / double(total)));
+      // near 1 by what is missing, which FP32 then holds to its last bits
+      if (P.logprob)
+        P.logprob[r] = float(v > total / 2 ? log1p(-double(total - v) / double(total)) : log(double(v) / double(total)));
     }
     if (target < all) break;
     target -= all;

@@ -43,6 +43,9 @@ class BeamStack:
              that key out); both set BEAM_DEV_BAD_PAGE. Position 0 pads a decode batch over paged
              layers; with more tokens per sequence, and over contiguous caches, it is flagged.
 
+    Over paged caches alone, verify() runs the held layers for the drafted trees of speculative decoding and keep()
+    moves the rows of the accepted nodes to the sequences' ends, in every layer's pages.
+
     Buffers between calls: those of the last number of tokens, one workspace, and one context copy
     for each window. What a captured call uses stays allocated as long as the stack, whatever
     calls come between its replays. All calls and replays of a stack share these buffers, so they
@@ -81,6 +84,7 @@ class BeamStack:
         self._bufs = {}
         self._stage = {}
         self._copies = {}
+        self._trees = {}
         self._held = []
         self.paged = any(isinstance(c, B.PagedKVCache) for c in caches)
 
@@ -217,9 +221,16 @@ class BeamStack:
             B.beam_attn(cfg, b["q"], b["g"], W["gate_bias"], kc, seq_id, pos, max_pos, W["w_o"],
                         b["a"], ws, stream, max_q_per_seq)
             return
+        call = {} if call is None else call
+        if "tree" in call:
+            ids, start, base, t = call["tree"]
+            B.beam_paged_qkv_gate(cfg, b["u"], W["w_qkvg"], W["q_norm"], W["k_norm"], t["seq"], t["pos"], t["slot"],
+                                  b["q"], b["g"], kc, ws, stream)
+            B.beam_paged_tree_attn(cfg, b["q"], b["g"], W["gate_bias"], kc, ids, start, base, t["mask"], max_pos,
+                                   W["w_o"], b["a"], ws, stream)
+            return
         T = seq_id.shape[0]
         max_q = T if max_q_per_seq is None else max_q_per_seq
-        call = {} if call is None else call
         # buffers that a later call may drop belong to the stream that uses them
         with on(stream):
             stage, rows, k, v = self.stage(T)
@@ -346,3 +357,40 @@ class BeamStack:
         for i in range(self.L):
             self.layer(i, b, seq_id, pos, max_pos, ws, stream, trace, max_q_per_seq, n_seqs, call)
         return b["h"]
+
+    def tree_buffers(self, T):
+        t = self._trees.get(T)
+        if t is None:
+            t = {k: torch.empty(T, dtype=torch.int64 if k == "mask" else torch.int32, device=self.device)
+                 for k in ("mask", "pos", "slot", "seq")}
+            self._trees = {**self.held(self._trees), T: t}
+        return self.hold(t)
+
+    def verify(self, e, parent, row_start, seq_id, base, max_pos, stream=None, trace=None):
+        """Runs the held layers for drafted trees, over paged caches. Rows row_start[i] .. row_start[i+1]-1 of e [T][H]
+        are the nodes of a tree (at most 64, parents before children) behind the base[i] tokens of sequence
+        seq_id[i]; parent [T] is each node's parent within its tree, -1 for a root. Node j's keys and values go to
+        slot base[i] + 1 + j of every layer's pages. max_pos: upper bound of base[i] plus the tree's size. Rows outside
+        all trees are padding. Returns h after the last residual addition (an internal buffer); with the tokens
+        sampled from it, beam_tree_accept gives the path that keep() takes."""
+        if not all(isinstance(c, B.PagedKVCache) for c in self.caches):
+            raise B.BeamError("BeamStack.verify needs paged caches in every layer")
+        with on(stream):
+            T = e.shape[0]
+            b, t = self.buffers(T), self.tree_buffers(T)
+            ws = self.ws.get(max(B.workspace_bytes(self.cfgs[0], T, max_pos),
+                                 B.paged_tree_workspace_bytes(self.cfgs[0], T)))
+            b["h"].copy_(e)
+            B.beam_tree_plan(parent, row_start, seq_id, base, t["mask"], t["pos"], t["slot"], t["seq"], stream)
+            B.beam_boundary_norm(None, b["h"], b["u"], None, self.W[0]["attn_pre"], 1, self.cfgs[0].eps, stream)
+            call = {"tree": (seq_id, row_start, base, t)}
+            for i in range(self.L):
+                self._layer(i, b, t["seq"], t["pos"], max_pos, ws, stream, trace, None, None, call)
+            return b["h"]
+
+    def keep(self, seq_id, base, count, path, stream=None):
+        """After verify(): the accepted nodes path[i][:count[i]] of each tree become the count[i] tokens behind
+        base[i], in every layer's pages."""
+        with on(stream):
+            for kc in self.caches:
+                B.beam_paged_kv_keep(kc, seq_id, base, count, path, stream)

@@ -296,10 +296,11 @@ beam_status beam_lm_head(const beam_bf16* u, const beam_bf16* w_lm, int T, int H
  * With z the row and t its temperature, w_i = e^(z_i / t). Tokens in descending order of z, equal ones by
  * index: the first top_k are kept; of these the fewest, from the front, whose weights hold top_p of theirs; of these
  * the ones with w_i >= min_p * max w. The token is the first, by index, at which the running sum of the
- * kept weights passes u times their sum. Sums are exact over weights of 2^-29 relative error, so the
- * token hangs on no order of summation and is the same on every run and in every batch.
+ * kept weights passes u times their sum. Weights have a relative error near 2^-29 and are cut to whole steps of
+ * 2^-44 of the largest; their sums are exact, so the token hangs on no order of summation and is the
+ * same on every run and in every batch. A token of less than 2^-44 of the largest weight is never drawn.
  *  logits    (device) [T] rows of V fp32, row_stride elements apart (>= V). -inf weighs nothing.
- *  u         (device) [T] fp32 in [0, 1); taken as 0 below and as the last kept token from 1 on.
+ *  u         (device) [T] fp32 in [0, 1); taken as 0 below; from 1 on the last kept token that weighs anything.
  *  temperature (device) [T] fp32, finite; below 1e-30 (0) the token is the largest logit's. NULL: 1.
  *  top_k     (device) [T] int32; <= 0: all. NULL: all.
  *  top_p     (device) [T] fp32; >= 1: all. NULL: all. At least one token is kept.
