@@ -1,0 +1,69 @@
+// Attention of a drafted tree over the paged cache: what its kernel (paged_tree.cu) and the join of its partials
+// (paged_tree_join.cu) share. The kernel is compiled as a unit of its own, without relocatable device code, since the
+// split of its registers between warps (setmaxnreg) needs that; so it does not reach the device status word, and hands the
+// bits to the join.
+#pragma once
+
+#include <math.h>
+
+#include "mma.cuh"
+#include "paged.cuh"
+
+namespace beam {
+namespace paged {
+namespace tree {
+
+constexpr int BK = 64;            // keys of a block
+constexpr int ROWS = 128;         // rows of a tile
+constexpr int kNodes = 64;        // tree rows of a sequence at most
+constexpr int kMaxSeqs = 512;     // sequences of one launch
+constexpr int kGrid = 152;        // CTAs at most (the workspace is sized for this many)
+constexpr int kFlush = 128;       // blocks of a stream between flushes of O: 1024 MMAs
+constexpr float kNegInf = -INFINITY;
+constexpr int kRescale = 8;       // log2 of what a block's weights may sum to before the running max is taken anew
+
+struct Params {
+  const uint16_t* q;
+  const uint16_t* g;
+  const uint16_t* gate_bias;
+  const int32_t* seq_id;
+  const int32_t* row_start;
+  const int32_t* base;
+  const uint64_t* mask;
+  uint16_t* og;
+  float* part_acc;   // [kGrid][2][2][ROWS][D]: partials of a range's first and last item, by tile
+  float2* part_ml;   // [kGrid][2][2][ROWS]
+  float* flush;      // [kGrid][2][ROWS][D]
+  int4* join;        // [kGrid][2]: item that begins in the range and runs on: (head, item, parts, tiles), (row0, n, status bits of the CTA, -)
+  beam_paged_kv c;
+  int N, T, n_q, n_kv, G, max_pos, shift, least;
+  int head_rows, tail_rows;   // whether rows before the first and behind the last sequence are this launch's
+  float sl2;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Four neighbouring outputs, gated, rounded once.
+__device__ __forceinline__ uint2 finish4(bool gated, float4 o, uint2 g, float bias) {
+  if (gated) {
+    o.x *= rcp(1.f + __expf(-(bf_lo(g.x) + bias)));
+    o.y *= rcp(1.f + __expf(-(bf_hi(g.x) + bias)));
+    o.z *= rcp(1.f + __expf(-(bf_lo(g.y) + bias)));
+    o.w *= rcp(1.f + __expf(-(bf_hi(g.y) + bias)));
+  }
+  return make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+}
+// Joins the partials of a launch of the kernel with `grid` CTAs.
+cudaError_t join(const Params& p, int grid, cudaStream_t st);
+
+}  // namespace tree
+}  // namespace paged
+}  // namespace beam
