@@ -50,6 +50,13 @@ namespace {
 
 using namespace beam::tc;
 
+// What the codes of a block's 64 keys leave to the softmax: K's powers of two relative to the largest, 2^top, and the
+// exponents of V's. Blocks whose factors may be in use at once: those of K's stages and of two steps.
+struct Factors {
+  float k[BK], v[BK], top, pad[3];
+};
+constexpr int kFac = 16;
+
 template <int FMT, int D_>
 struct Cfg {
   static constexpr int D = D_, ROWB = row_bytes(FMT, D);
@@ -57,22 +64,23 @@ struct Cfg {
   static constexpr int THREADS = QUANT ? 640 : 512;
   // registers of a thread: at launch (a fifth or a quarter of the SM's for each four warps), then of the softmax and of
   // the other warps; the shares add up to no more than the launch's
-  static constexpr int REG = QUANT ? 96 : 128, REG_S = QUANT ? 136 : 176, REG_L = QUANT ? 64 : 80, REG_C = QUANT ? 72 : 80;
+  static constexpr int REG = QUANT ? 96 : 128, REG_S = QUANT ? 144 : 200, REG_L = QUANT ? 64 : 56, REG_C = QUANT ? 64 : 56;
   static_assert(2 * REG_S + REG_L + (QUANT ? 2 : 1) * REG_C <= THREADS / 128 * REG, "register split");
   static constexpr int NH = D / 64;                 // 64-wide halves of a row
   static constexpr int TILE = BK * D * 2;           // K or V block in bf16
   static constexpr int NST = QUANT ? 3 : (D == 128 ? 4 : 8);
   static constexpr int RAWB = QUANT ? BK * ROWB : 0;
   static constexpr int RBS = FMT == kFmtNVFP4 ? BK * (D / 16) : 0;
-  static constexpr int RAW = QUANT ? RAWB + RBS + BK : 0;   // a raw stage of K or V: codes, block scales, row scales
+  static constexpr int RAW = QUANT ? RAWB + RBS + 2 * BK : 0;   // a raw stage: codes, block scales, row scales (with K's: both)
   static constexpr int NRAW = QUANT ? 3 : 0;
   static constexpr int Q0 = 0, QB = ROWS * D * 2;           // each stream's query tile
   static constexpr int K0 = 2 * QB, V0 = K0 + NST * TILE;
   static constexpr int R0 = V0 + NST * TILE;                // raw stages of K, then of V
   static constexpr int SEQ = (R0 + 2 * NRAW * RAW + 15) / 16 * 16;   // [kMaxSeqs] (row0, n, sid, base)
   static constexpr int CUM = SEQ + kMaxSeqs * 16;                    // [kMaxSeqs + 1] cost prefix
-  static constexpr int XCH = CUM + (kMaxSeqs + 4) * 4;               // [128] (m, sum) of stream 1
-  static constexpr int MASK = XCH + ROWS * 8;                    // [2][8] slices of a K or V stage that have a page
+  static constexpr int FAC = CUM + (kMaxSeqs + 4) * 4;               // [kFac] factors of a block's keys (Factors)
+  static constexpr int XCH = FAC + (QUANT ? kFac * int(sizeof(Factors)) : 0);   // [128] (m, z, sum) of stream 1
+  static constexpr int MASK = XCH + ROWS * 16;                    // [2][8] slices of a K or V stage that have a page
   static constexpr int BAR = MASK + 16 * 4;
   static constexpr int NBAR = 5 * NST + 4 * NRAW + 18;
   static constexpr int MISC = BAR + NBAR * 8;
@@ -169,13 +177,20 @@ __device__ __forceinline__ int units_of(const Item& it, int s) {
   return it.w == 2 ? n : (n + 1 - s) / 2;
 }
 
-// Page of the e-th 16 keys of block j: -1: none, -2: no key of the item among them.
-__device__ __forceinline__ int page_of_slice(const Params& P, const Seq& s, int j, int e) {
+// Page table entry of the e-th 16 keys of block j, compared with the pages' number where it is used (a load ahead of that
+// waits for nothing); -2: no key of the item among them.
+__device__ __forceinline__ int entry_of_slice(const Params& P, const Seq& s, int j, int e) {
   const int k0 = (s.blk0 + j) * BK + 16 * e;   // 0-based
-  if (k0 + 16 < s.lo || k0 >= s.base + s.n) return -2;   // no key of the item
-  const int pg = P.c.page_table[size_t(s.sid) * P.c.table_stride + (k0 >> P.shift)];
-  return pg >= 0 && pg < P.c.num_pages ? pg : -1;
+  if (k0 + 16 < s.lo || k0 >= s.base + s.n) return -2;
+  return P.c.page_table[size_t(s.sid) * P.c.table_stride + (k0 >> P.shift)];
 }
+// The page, -1: none, -2: no key.
+__device__ __forceinline__ int page_of_entry(const Params& P, const Seq& s, int j, int e, int entry) {
+  const int k0 = (s.blk0 + j) * BK + 16 * e;
+  if (k0 + 16 < s.lo || k0 >= s.base + s.n) return -2;
+  return entry >= 0 && entry < P.c.num_pages ? entry : -1;
+}
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t mbar) {
   asm volatile(
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
@@ -198,6 +213,11 @@ __device__ __forceinline__ void f2_split(uint64_t r, float& a, float& b) {
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
@@ -256,7 +276,7 @@ __device__ __noinline__ void add_no_numbers(const Params& P, const Item& it, con
   for (int j = it.j0; j < it.j1; ++j) {
     unsigned slices = 0;
     for (int e = 0; e < 4; ++e)
-      if (page_of_slice(P, s, j, e) >= 0) slices |= 1u << e;
+      if (page_of_entry(P, s, j, e, entry_of_slice(P, s, j, e)) >= 0) slices |= 1u << e;
     if (it.whole(j) && slices == 15u) continue;
     const int kb = (s.blk0 + j) * BK + 1;
     uint64_t bits = seen(v, s, kb, slices);
@@ -286,7 +306,9 @@ __global__ void __launch_bounds__(FMT == kFmtBF16 ? 512 : 640, 1)
 paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const Params P) {
   using C = Cfg<FMT, D>;
   constexpr int NST = C::NST, NRAW = C::NRAW;
-  constexpr uint32_t IDESC_QK = idesc_bf16(ROWS, BK, false), IDESC_PV = idesc_bf16(ROWS, D, true);
+  // bf16, or f16 over quantised pages: there the two format fields are zero
+  constexpr uint32_t KIND = C::QUANT ? ~((1u << 7) | (1u << 10)) : ~0u;
+  constexpr uint32_t IDESC_QK = idesc_bf16(ROWS, BK, false) & KIND, IDESC_PV = idesc_bf16(ROWS, D, true) & KIND;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(sm);
@@ -307,8 +329,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       mbar_init(k_full + 8 * i, C::QUANT ? 4 : 1);
       mbar_init(k_empty + 8 * i, 2);   // both streams
       mbar_init(v_full + 8 * i, C::QUANT ? 4 : 1);
-      mbar_init(v_empty + 8 * i, C::QUANT ? 2 : 6);   // and four warps that look at every block
-      mbar_init(v_clean + 8 * i, 4);
+      mbar_init(v_empty + 8 * i, 2);
+      mbar_init(v_clean + 8 * i, 4);   // of BF16 values, in place of v_full: looked through, and cleaned if need be
     }
     for (int i = 0; i < 2 * NRAW; ++i) {
       mbar_init(r_full + 8 * i, 1);
@@ -383,8 +405,9 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     bool ok = true;
     Item it;
     for (int c = c0; ok && next_item(P, plan, c, c1, it);) {
-      int pg = lane < 4 ? page_of_slice(P, it.s, it.j0, lane) : -2;
+      int entry = lane < 4 ? entry_of_slice(P, it.s, it.j0, lane) : -2;
       for (int j = it.j0; j < it.j1; ++j, ++nb) {
+        const int pg = lane < 4 ? page_of_entry(P, it.s, j, lane, entry) : -2;
         if (pg == -1 && kv == 0 && it.h == 0 && it.m == 0) atomicOr(status, BEAM_DEV_BAD_PAGE);
         const unsigned live = __ballot_sync(0xffffffffu, pg >= 0) & 15u;
         const int k0 = (it.s.blk0 + j) * BK;
@@ -395,13 +418,13 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         const int copies = __popc(__ballot_sync(0xffffffffu, mine));
         const int off = (k0 + 16 * e0) & (P.c.page_size - 1);
         const size_t head = size_t(mine ? page : 0) * P.c.n_kv + it.h;
-        pg = lane < 4 && j + 1 < it.j1 ? page_of_slice(P, it.s, j + 1, lane) : -2;   // the next block's, meanwhile
+        entry = lane < 4 && j + 1 < it.j1 ? entry_of_slice(P, it.s, j + 1, lane) : -2;   // the next block's, meanwhile
         const int st = int(nb % DEPTH);
         if (!__all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ((nb / DEPTH) & 1) ^ 1))) { ok = false; break; }
         const uint32_t keys = uint32_t(run * 16), bar = full + 8 * st;
         if (lane == 0) {
           masks[8 * kv + st] = live;
-          mbar_expect_tx(bar, uint32_t(copies) * keys * (C::QUANT ? C::ROWB + 1 + (FMT == kFmtNVFP4 ? D / 16 : 0) : 2 * D));
+          mbar_expect_tx(bar, uint32_t(copies) * keys * (C::QUANT ? C::ROWB + 2 - kv + (FMT == kFmtNVFP4 ? D / 16 : 0) : 2 * D));
         }
         __syncwarp();
         if (!mine) continue;
@@ -417,6 +440,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
           if constexpr (FMT == kFmtNVFP4)
             bulk_load(at + C::RAWB + e0 * 16 * (D / 16), P.c.block_scale + sc * (D / 16), keys * (D / 16), bar);
           bulk_load(at + C::RAWB + C::RBS + e0 * 16, P.c.row_scale + sc, keys, bar);
+          if (kv == 0) bulk_load(at + C::RAWB + C::RBS + BK + e0 * 16, P.c.row_scale + sc + P.c.page_size, keys, bar);   // V's
         }
       }
     }
@@ -431,7 +455,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     // behind P.V of step x, whose buffer it takes (operations of one thread run in order). Both streams wait for all
     // blocks and release all, so that neither is ever a lap of the ring ahead.
     const int s = warp >> 1;
-    uint32_t nb = 0, cleaned = 0;           // blocks of earlier items; parity of each stage's cleaned blocks
+    const uint32_t v_ready = C::QUANT ? v_full : v_clean;
+    uint32_t nb = 0;                            // blocks of earlier items
     uint32_t sn = 0, un = 0, ost = 0, qn = 0;   // S issued, P.V issued, fresh O, Q
     bool ok = true;
     auto all = [&](bool v) { return __all_sync(0xffffffffu, v); };
@@ -453,8 +478,12 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
 #pragma unroll
       for (int kk = 0; kk < BK / 16; ++kk) {
         const uint32_t b = lo + uint32_t((kk * 16 * 128) >> 4), a = ts + 32 * (kk >> 1) + 8 * (kk & 1);
-        umma_ts_e(to, a, b, dv_hi, IDESC_PV, first && kk == 0 ? 0u : 1u);
-        umma_ts_e(to, a + 16, b, dv_hi, IDESC_PV, 1u);
+        if constexpr (C::QUANT) {
+          umma_ts_e(to, ts + 8 * kk, b, dv_hi, IDESC_PV, first && kk == 0 ? 0u : 1u);
+        } else {
+          umma_ts_e(to, a, b, dv_hi, IDESC_PV, first && kk == 0 ? 0u : 1u);
+          umma_ts_e(to, a + 16, b, dv_hi, IDESC_PV, 1u);
+        }
       }
       umma_commit_e(pv_done + 8 * s);
       ++un;
@@ -466,62 +495,54 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       ++qn;
       if (!ok) break;
       tc_fence_after();
-      // blocks of step x: b and, of items of one tile, b + 1 if there is one; the stream's own is b + own
-      auto make_s = [&](int x) {
+      // Blocks of step x: b and, of items of one tile, b + 1 if there is one; the stream's own is b + s there.
+      auto two_of = [&](int x) { return per == 2 && 2 * x + 1 < cnt; };
+      auto ready = [&](uint32_t bars, uint32_t b) { return mbar_test(bars + 8 * (b % NST), (b / NST) & 1); };
+      auto await = [&](bool r, uint32_t bars, uint32_t b) { return r || mbar_wait(bars + 8 * (b % NST), (b / NST) & 1); };
+      auto make_s = [&](int x) {   // S of step x, whose keys are there
         const uint32_t b = nb + uint32_t(per * x);
-        const bool two = per == 2 && 2 * x + 1 < cnt;
-        const int st = int(b % NST), st1 = int((b + 1) % NST);
-        const bool r0 = mbar_test(k_full + 8 * st, (b / NST) & 1);
-        const bool r1 = !two || mbar_test(k_full + 8 * st1, ((b + 1) / NST) & 1);
-        if (!all((r0 || mbar_wait(k_full + 8 * st, (b / NST) & 1)) && (r1 || mbar_wait(k_full + 8 * st1, ((b + 1) / NST) & 1)))) return false;
-        tc_fence_after();
-        const bool own = per == 1 || s == 0 || two;
-        const int mine = per == 2 && s == 1 ? st1 : st;
+        const bool two = two_of(x), own = per == 1 || s == 0 || two;
+        const int mine = int((per == 2 && s == 1 ? b + 1 : b) % NST), others = int((s == 1 ? b : b + 1) % NST);
         if (own) {
           qk(mine);
           umma_commit_e(k_empty + 8 * mine);
         }
-        if (lane == 0 && per == 2 && (s == 1 || two)) mbar_arrive(k_empty + 8 * (s == 1 ? st : st1));
-        return true;
+        if (lane == 0 && per == 2 && (s == 1 || two)) mbar_arrive(k_empty + 8 * others);
       };
-      for (int x = 0; x < 2 && x < steps && ok; ++x) ok = make_s(x);
-      for (int x = 0; x < steps && ok; ++x) {
+      for (int x = 0; x < 2 && x < steps && ok; ++x) {
         const uint32_t b = nb + uint32_t(per * x);
-        const bool two = per == 2 && 2 * x + 1 < cnt, own = per == 1 || s == 0 || two;
-        const int st = int(b % NST), st1 = int((b + 1) % NST), mine = per == 2 && s == 1 ? st1 : st;
+        ok = all(await(false, k_full, b) && await(!two_of(x), k_full, b + 1));
+        tc_fence_after();
+        if (ok) make_s(x);
+      }
+      for (int x = 0; x < steps && ok; ++x) {
+        const uint32_t b = nb + uint32_t(per * x), bk = b + uint32_t(2 * per);
+        const bool two = two_of(x), own = per == 1 || s == 0 || two, more = x + 2 < steps;
         const bool fresh = own && x % kFlush == 0;
         const uint32_t pb = p_full + 16 * s + 8 * (un & 1);
         // polled together, so that their latencies overlap, then waited for one by one
-        const bool r0 = mbar_test(v_full + 8 * st, (b / NST) & 1);
-        const bool r1 = !two || mbar_test(v_full + 8 * st1, ((b + 1) / NST) & 1);
+        const bool r0 = ready(v_ready, b), r1 = !two || ready(v_ready, b + 1);
         const bool r2 = !own || mbar_test(pb, (un >> 1) & 1);
         const bool r3 = !fresh || mbar_test(o_empty + 8 * s, (ost & 1) ^ 1);
-        if (!all((r0 || mbar_wait(v_full + 8 * st, (b / NST) & 1)) && (r1 || mbar_wait(v_full + 8 * st1, ((b + 1) / NST) & 1)) &&
-                 (r3 || mbar_wait(o_empty + 8 * s, (ost & 1) ^ 1)) && (r2 || mbar_wait(pb, (un >> 1) & 1)))) {
+        const bool k0 = !more || ready(k_full, bk), k1 = !two_of(x + 2) || ready(k_full, bk + 1);
+        if (!all(await(r0, v_ready, b) && await(r1, v_ready, b + 1) && (r3 || mbar_wait(o_empty + 8 * s, (ost & 1) ^ 1)) &&
+                 (r2 || mbar_wait(pb, (un >> 1) & 1)))) {
           ok = false;
           break;
         }
-        if constexpr (!C::QUANT) {
-          const unsigned live = masks[8 + st] & (two ? masks[8 + st1] : 15u);
-          const int j = it.j0 + per * x;
-          if (live != 15u || !it.whole(j) || (two && !it.whole(j + 1))) {
-            for (int e = 0; e <= int(two) && ok; ++e) {
-              const int se = e ? st1 : st;
-              if (masks[8 + se] == 15u && it.whole(j + e)) continue;
-              ok = all(mbar_wait(v_clean + 8 * se, (cleaned >> se) & 1));
-              cleaned ^= 1u << se;
-            }
-            if (!ok) break;
-          }
-        }
+        tc_fence_after();
         if (own) {
-          tc_fence_after();
+          const int mine = int((per == 2 && s == 1 ? b + 1 : b) % NST);
           if (fresh) ++ost;
           pv(mine, fresh);
           umma_commit_e(v_empty + 8 * mine);
         }
-        if (lane == 0 && per == 2 && (s == 1 || two)) mbar_arrive(v_empty + 8 * (s == 1 ? st : st1));
-        if (x + 2 < steps) ok = make_s(x + 2);
+        if (lane == 0 && per == 2 && (s == 1 || two)) mbar_arrive(v_empty + 8 * ((s == 1 ? b : b + 1) % NST));
+        if (more) {
+          ok = all(await(k0, k_full, bk) && await(k1, k_full, bk + 1));
+          tc_fence_after();
+          if (ok) make_s(x + 2);
+        }
       }
       if (!ok) break;
       nb += uint32_t(cnt);
@@ -535,25 +556,25 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     // ------------------------------------------------------------------ softmax
     const int s = (warp - 4) >> 2, q4 = warp & 3, lr = q4 * 32 + lane;
     const uint32_t t0 = tmem + 256 * s + (uint32_t(q4 * 32) << 16), to = t0 + 128;
-    float2* xch = reinterpret_cast<float2*>(sm + C::XCH);
     float* fl = P.flush + (size_t(blockIdx.x) * 2 * ROWS + lr) * D;   // stream 0's; 1's ROWS * D on
-    uint32_t un = 0, items = 0, turns = 0;
+    uint32_t un = 0, items = 0, turns = 0, nb = 0;   // units, items, exchanges; blocks of earlier items
     bool ok = true;
     auto all = [&](bool v) { return __all_sync(0xffffffffu, v); };
-    int4 join = make_int4(0, 0, 0, 0);
-    int2 rows = make_int2(0, 0);
+    if (threadIdx.x == 4 * 32) P.join[2 * r] = make_int4(0, 0, 0, 0);   // no item begins here and runs on
     // The thread's row of an item, and its queries on their way to the products: for every item, so that these are never
     // more than one ahead.
     struct Row {
       RowView v;
       size_t at;
       int hq;
+      float qe;   // log2 of the factor of q's f16 values
       bool real;
     };
     auto row_of = [&](const Item& i) {
       const int row = (2 * i.m + (i.w == 2 ? s : 0)) * ROWS + lr, node = row / P.G;
       Row x;
       x.real = node < i.s.n;
+      x.qe = 0.f;
       x.hq = i.h * P.G + (row - node * P.G);
       x.v = view_of(P, i.s, node);
       x.at = (size_t(i.s.row0 + (x.real ? node : 0)) * P.n_q + x.hq) * D;
@@ -563,10 +584,32 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       }
       if (units_of(i, s) > 0) {
         uint8_t* qt = sm + C::Q0 + s * C::QB + lr * 128;
-#pragma unroll
-        for (int e = 0; e < D / 8; ++e) {
-          const uint4 y = x.real ? ld_stream(P.q + x.at + 8 * e) : make_uint4(0, 0, 0, 0);
+        auto put = [&](int e, const uint4& y) {
           *reinterpret_cast<uint4*>(qt + (e >> 3) * ROWS * 128 + (((e & 7) ^ (lr & 7)) << 4)) = y;
+        };
+        const uint16_t* src = P.q + x.at;
+        if constexpr (!C::QUANT) {
+#pragma unroll
+          for (int e = 0; e < D / 8; ++e) put(e, x.real ? ld_stream(src + 8 * e) : make_uint4(0, 0, 0, 0));
+        } else {
+          // to f16 by a power of two that takes the largest magnitude to 2^15 .. 2^16
+          auto get = [&](int e) { return x.real ? __ldg(reinterpret_cast<const uint4*>(src) + e) : make_uint4(0, 0, 0, 0); };
+          unsigned mx = 0;
+#pragma unroll 8
+          for (int e = 0; e < D / 8; ++e) mx = __vmaxu2(mx, abs_max(get(e)));
+          const unsigned top = max(mx & 0xFFFFu, mx >> 16);
+          // by 2^up in two steps; rows with an infinity or a NaN as they are
+          const int ex = top >= 0x7F80u ? 142 : max(1, int(top >> 7)), up = 142 - ex;
+          const float u0 = __uint_as_float(unsigned(127 + up / 2) << 23), u1 = __uint_as_float(unsigned(127 + up - up / 2) << 23);
+          x.qe = float(-up);
+#pragma unroll 4
+          for (int e = 0; e < D / 8; ++e) {
+            float f[8];
+            unpack8(get(e), f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = f[i] * u0 * u1;
+            put(e, make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]), pack_f16x2(f[6], f[7])));
+          }
         }
         fence_proxy_async_smem();
       }
@@ -585,106 +628,176 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       const bool real = cur.real;
       const bool work = __any_sync(0xffffffffu, v.tree != 0);   // any row that sees keys
       const bool none = __any_sync(0xffffffffu, real && v.tree == 0);   // a row among them that sees nothing
-      float m = kNegInf, l = 0.f;   // reference (log2 units; lags by up to kRescale) and sum
+      // Reference and sum of the weights (log2 units; it lags by up to kRescale); z: that of O, which over quantised pages
+      // follows the weights times their value rows' powers of two
+      float m = kNegInf, l = 0.f, z = kNegInf;
       bool flushed = false;
       const int stride = it.w == 2 ? 1 : 2, j_first = it.j0 + (it.w == 2 ? 0 : s);
-      int pg = units > 0 && lane < 4 ? page_of_slice(P, it.s, j_first, lane) : -2;
+      int entry = units > 0 && lane < 4 ? entry_of_slice(P, it.s, j_first, lane) : -2;
       for (int k = 0; k < units; ++k, ++un) {
         const int j = j_first + k * stride;
-        const unsigned slices = __ballot_sync(0xffffffffu, pg >= 0) & 15u;
-        if (k + 1 < units) pg = lane < 4 ? page_of_slice(P, it.s, j + stride, lane) : -2;   // the next one's, meanwhile
+        const unsigned slices = __ballot_sync(0xffffffffu, lane < 4 && page_of_entry(P, it.s, j, lane, entry) >= 0);
+        if (k + 1 < units) entry = lane < 4 ? entry_of_slice(P, it.s, j + stride, lane) : -2;   // the next one's, meanwhile
         const bool full = !none && slices == 15u && it.whole(j);
         const uint32_t ts = t0 + 64 * (un & 1), bar = 16 * s + 8 * (un & 1);
         if (!all(mbar_wait(s_full + bar, (un >> 1) & 1))) { ok = false; break; }
         tc_fence_after();
         if (work) {
           const uint64_t bits = full ? ~uint64_t(0) : seen(v, it.s, (it.s.blk0 + j) * BK + 1, slices);
-          auto load = [&](uint32_t* sv) {
-            tmem_ld32_nowait(ts, sv);
-            tmem_ld32_nowait(ts + 32, sv + 32);
-            tmem_wait_ld();
-            if (!full) {
-#pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (!((uint32_t(bits >> (e & 32)) >> (e & 31)) & 1u)) sv[e] = __float_as_uint(kNegInf);
-            }
+          // half x of S, keys that the row does not see at -inf
+          auto load = [&](uint32_t (&sv)[32], int x) {
+            tmem_ld32_nowait(ts + 32 * x, sv);
           };
-          // P = 2^(s c - m) in halves over S, in place; the sum of P
-          auto weigh = [&](uint32_t* sv, float m) {
-            const float nm = m == kNegInf ? 0.f : -m;
-            const uint64_t c2 = f2(P.sl2, P.sl2), nm2 = f2(nm, nm);
-            uint64_t ls[4] = {0, 0, 0, 0};
+          auto hide = [&](uint32_t (&sv)[32], int x) {
+            const uint32_t b32 = uint32_t(bits >> (32 * x));
+            if (!full)
 #pragma unroll
-            for (int x = 0; x < 64; x += 32) {
-              uint32_t lo[16];
+              for (int e = 0; e < 32; ++e)
+                if (!((b32 >> e) & 1u)) sv[e] = __float_as_uint(kNegInf);
+          };
+          [[maybe_unused]] const Factors* fa = reinterpret_cast<const Factors*>(sm + C::FAC) + ((nb + uint32_t(j - it.j0)) % kFac);
+          [[maybe_unused]] float rf = 0.f;   // factor of S times its key's, in log2 units of the weight
+          if constexpr (C::QUANT) rf = ex2(fmaxf(fminf(fa->top + cur.qe, 120.f), -120.f)) * P.sl2;
+          unsigned most = 0;   // the largest of P in f16
+          // P of a half; returns the sum of the weights. BF16: 2^(S c - m), its high parts and low parts. Quantised:
+          // 2^(S c k - m + e - (z - m)) in f16, with the keys' factors k and e.
+          auto weigh = [&](const uint32_t (&sv)[32], int x, uint32_t* pk) {
+            const float nm = m == kNegInf ? 0.f : -m;
+            const uint64_t nm2 = f2(nm, nm);
+            uint64_t ls[4] = {0, 0, 0, 0};
+            if constexpr (!C::QUANT) {
+              const uint64_t c2 = f2(P.sl2, P.sl2);
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 float x0, x1;
-                f2_split(fma2(f2(__uint_as_float(sv[x + 2 * e]), __uint_as_float(sv[x + 2 * e + 1])), c2, nm2), x0, x1);
+                f2_split(fma2(f2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), c2, nm2), x0, x1);
                 const float p0 = ex2(x0), p1 = ex2(x1);
                 const uint64_t pp = f2(p0, p1);
                 ls[e & 3] = add2(ls[e & 3], pp);
                 const uint32_t hi = pack_bf16x2(p0, p1);
                 float d0, d1;
                 f2_split(sub2(pp, f2(bf_lo(hi), bf_hi(hi))), d0, d1);
-                sv[x + e] = hi;
-                lo[e] = pack_bf16x2(d0, d1);
+                pk[e] = hi;
+                pk[16 + e] = pack_bf16x2(d0, d1);
               }
+            } else {
+              const uint64_t c2 = f2(rf, rf);
+              const float nz = z == kNegInf ? 0.f : -z;
+              const uint64_t nz2 = f2(nz, nz);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) sv[x + 16 + e] = lo[e];
+              for (int e = 0; e < 8; ++e) {
+                const float4 kf = reinterpret_cast<const float4*>(fa->k + 32 * x)[e], ve = reinterpret_cast<const float4*>(fa->v + 32 * x)[e];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const uint64_t sk = mul2(f2(__uint_as_float(sv[4 * e + 2 * i]), __uint_as_float(sv[4 * e + 2 * i + 1])),
+                                           i ? f2(kf.z, kf.w) : f2(kf.x, kf.y));
+                  float y0, y1, z0, z1;
+                  f2_split(fma2(sk, c2, nm2), y0, y1);
+                  f2_split(fma2(sk, c2, add2(i ? f2(ve.z, ve.w) : f2(ve.x, ve.y), nz2)), z0, z1);
+                  ls[2 * (e & 1) + i] = add2(ls[2 * (e & 1) + i], f2(ex2(y0), ex2(y1)));
+                  const uint32_t w = pack_f16x2(ex2(z0), ex2(z1));
+                  pk[2 * e + i] = w;
+                  most = __vmaxu2(most, w);
+                }
+              }
             }
             float a0, a1, b0, b1;
             f2_split(add2(ls[0], ls[1]), a0, a1);
             f2_split(add2(ls[2], ls[3]), b0, b1);
             return (a0 + b0) + (a1 + b1);
           };
-          uint32_t sv[64];
-          load(sv);
-          // The reference m stays while the block's weights sum to no more than 2^kRescale; a row's first block, and one
-          // that exceeds it, are gone through for their maximum, and O and the sum are rescaled.
+          // The references stay while the block's weights sum to no more than 2^kRescale (quantised pages: while FP32 holds
+          // them, and P is no more than 2^(kRescale + kBias)); a row's first block, and one that exceeds that, are gone
+          // through for their maxima, and O and the sum are rescaled.
+          constexpr int HALF = C::QUANT ? 16 : 32;   // words of P of a half
+          uint32_t pk[2 * HALF];
+          auto weights = [&]() {
+            float sum;
+            if constexpr (C::QUANT) {   // half by half: registers
+              uint32_t sv[32];
+              load(sv, 0);
+              tmem_wait_ld();
+              hide(sv, 0);
+              sum = weigh(sv, 0, pk);
+              load(sv, 1);
+              tmem_wait_ld();
+              hide(sv, 1);
+              sum += weigh(sv, 1, pk + HALF);
+            } else {
+              uint32_t s0[32], s1[32];
+              load(s0, 0);
+              load(s1, 1);
+              tmem_wait_ld();
+              hide(s0, 0);
+              hide(s1, 1);
+              sum = weigh(s0, 0, pk);
+              sum += weigh(s1, 1, pk + HALF);
+            }
+            return sum;
+          };
           float sum = 0.f;
           bool lag = m == kNegInf;
           if (!__any_sync(0xffffffffu, lag)) {
-            sum = weigh(sv, m);
-            lag = !(sum <= float(1 << kRescale));
+            sum = weights();
+            lag = C::QUANT ? !(sum <= 0x1p60f) || max(most & 0xFFFFu, most >> 16) > 0x7800u : !(sum <= float(1 << kRescale));
           }
           if (__any_sync(0xffffffffu, lag)) {
-            load(sv);
-            float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+            float mt = kNegInf, zt = kNegInf;
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+              uint32_t sv[32];
+              load(sv, x);
+              tmem_wait_ld();
+              hide(sv, x);
 #pragma unroll
-            for (int e = 0; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sv[e]));
-            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.sl2;
-            const bool need = m != kNegInf && mt > m;
+              for (int e = 0; e < 32; ++e) {
+                if constexpr (C::QUANT) {
+                  const float y = __uint_as_float(sv[e]) * fa->k[32 * x + e] * rf;
+                  mt = fmaxf(mt, y);
+                  zt = fmaxf(zt, y + fa->v[32 * x + e]);
+                } else {
+                  mt = fmaxf(mt, __uint_as_float(sv[e]));
+                }
+              }
+            }
+            if constexpr (C::QUANT) zt -= float(kBias);
+            else zt = mt = mt * P.sl2;
+            // a row that another's first block brought here is held to the same bound
+            const float by = lag ? 0.f : float(kRescale);
+            const bool need = m != kNegInf && (mt > m + by || zt > z + by);
             if (__any_sync(0xffffffffu, need)) {
               // O holds the stream's earlier products: the last one has to be done
               if (!all(mbar_wait(pv_done + 8 * s, (un - 1) & 1))) { ok = false; break; }
               tc_fence_after();
-              const float f = need ? ex2(m - mt) : 1.f;
+              const float m1 = need ? fmaxf(m, mt) : m, z1 = need ? fmaxf(z, zt) : z;
+              const float f = z1 == z ? 1.f : ex2(z - z1);
               if (k % kFlush != 0) {   // after a flush O is not read again
 #pragma unroll 1
-                for (int x = 0; x < D / 32; ++x) {
-                  uint32_t o[32];
-                  tmem_ld32_nowait(to + 32 * x, o);
-                  tmem_wait_ld();
+                for (int x = 0; x < D / 16; ++x) {
+                  uint32_t o[16];
+                  tmem_ld16(to + 16 * x, o);
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                  tmem_st32(to + 32 * x, o);
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st16(to + 16 * x, o);
                 }
                 tmem_wait_st();
               }
-              if (flushed && need)
+              if (flushed && f != 1.f)
                 for (int x = 0; x < D; ++x) fl[s * ROWS * D + x] *= f;
-              if (need) {
-                l *= f;
-                m = mt;
-              }
+              if (m1 != m) l *= ex2(m - m1);
+              m = m1;
+              z = z1;
             }
-            if (m == kNegInf) m = mt;   // the row's first keys
-            sum = weigh(sv, m);
+            if (m == kNegInf) {   // the row's first keys
+              m = mt;
+              z = zt;
+            }
+            most = 0;
+            sum = weights();
           }
           l += sum;
-          tmem_st32(ts, sv);
-          tmem_st32(ts + 32, sv + 32);
+          tmem_st32(ts, pk);
+          if (!C::QUANT) tmem_st32(ts + 32, pk + 32);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -721,32 +834,38 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       if (ahead) w = row_of(nx);
       if (!all(mbar_wait(o_full + 8 * s, items & 1))) { ok = false; break; }
       tc_fence_after();
-      float f0 = 1.f, f1 = 0.f;
+      // O's factors h^2 (in two steps, which alone may leave FP32's range) to the reference m of what is written
+      float h0 = 1.f, h1 = 0.f;
       bool other = false;   // stream 1's share is added here
+      auto half = [](float zs, float top) { return zs == kNegInf ? 0.f : ex2(0.5f * (zs - top)); };
       if (it.w == 1) {
+        float4* xch = reinterpret_cast<float4*>(sm + C::XCH);
         if (s == 1) {
           // stream 0 writes for both
           if (!all(mbar_wait(x_empty, (turns & 1) ^ 1))) { ok = false; break; }
-          xch[lr] = make_float2(m, l);
+          xch[lr] = make_float4(m, z, l, 0.f);
           mbar_arrive(x_full);
           ++turns;
           if (more && !ahead) w = row_of(nx);
+          nb += uint32_t(it.j1 - it.j0);
           it = nx;
           continue;
         }
         if (!all(mbar_wait(x_full, turns & 1))) { ok = false; break; }
-        const float2 y = xch[lr];
+        const float4 y = xch[lr];
         mbar_arrive(x_empty);
         ++turns;
         other = units_of(it, 1) > 0;
         const float top = fmaxf(m, y.x);
         if (top != kNegInf) {
-          f0 = m == kNegInf ? 0.f : ex2(m - top);
-          f1 = y.x == kNegInf ? 0.f : ex2(y.x - top);
+          h0 = half(z, top);
+          h1 = half(y.y, top);
+          l = (m == kNegInf ? 0.f : ex2(m - top) * l) + (y.x == kNegInf ? 0.f : ex2(y.x - top) * y.z);
+          if (top == INFINITY) l = h0 = h1 = __uint_as_float(0x7FFFFFFFu);   // a logit of +inf
         }
-        if (top != top) f0 = f1 = top;
-        l = f0 * l + f1 * y.y;
         m = top;
+      } else if (C::QUANT && m != kNegInf) {
+        h0 = half(z, m);
       }
       const bool other_flushed = other && units_of(it, 1) > kFlush;
       const bool odd = misc[2] != 0;
@@ -767,19 +886,19 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         tmem_wait_ld();
         float a[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) a[e] = f0 == 0.f ? 0.f : __uint_as_float(o[e]) * f0;
+        for (int e = 0; e < 32; ++e) a[e] = h0 == 0.f ? 0.f : __uint_as_float(o[e]) * h0 * h0;
         if (flushed)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) a[e] += fl[s * ROWS * D + 32 * x + e] * f0;
+          for (int e = 0; e < 32; ++e) a[e] += fl[s * ROWS * D + 32 * x + e] * h0 * h0;
         if (other) {
           tmem_ld32_nowait(to + 256 + 32 * x, o);
           tmem_wait_ld();
-          if (f1 != 0.f)
+          if (h1 != 0.f)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) a[e] += __uint_as_float(o[e]) * f1;
-          if (other_flushed && f1 != 0.f)
+            for (int e = 0; e < 32; ++e) a[e] += __uint_as_float(o[e]) * h1 * h1;
+          if (other_flushed && h1 != 0.f)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) a[e] += fl[ROWS * D + 32 * x + e] * f1;
+            for (int e = 0; e < 32; ++e) a[e] += fl[ROWS * D + 32 * x + e] * h1 * h1;
         }
         if (real) {
           if (l == 0.f)
@@ -814,18 +933,15 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       tc_fence_before();
       if (units > 0) mbar_arrive(o_empty + 8 * s);
       if (other) mbar_arrive(o_empty + 8);
-      if (it.split && it.j0 == 0) {   // the item begins here and runs on
-        join = make_int4(it.h, it.m, range_of(it.f + it.w * (it.s.nb - 1), total, R) - r + 1, it.w);
-        rows = make_int2(it.s.row0, it.s.n);
+      if (it.split && it.j0 == 0 && threadIdx.x == 4 * 32) {   // one does
+        P.join[2 * r] = make_int4(it.h, it.m, range_of(it.f + it.w * (it.s.nb - 1), total, R) - r + 1, it.w);
+        *reinterpret_cast<int2*>(P.join + 2 * r + 1) = make_int2(it.s.row0, it.s.n);
       }
       if (more && !ahead) w = row_of(nx);
+      nb += uint32_t(it.j1 - it.j0);
       it = nx;
     }
     if (!ok) misc[1] = 1;
-    if (threadIdx.x == 4 * 32) {
-      P.join[2 * r] = join;
-      *reinterpret_cast<int2*>(P.join + 2 * r + 1) = rows;
-    }
   } else {
     set_regs<C::REG_C, false>();
     // ------------------------------------------------------------------ rows that attend to nothing
@@ -859,53 +975,61 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
           const int kb = (it.s.blk0 + j) * BK + 1;
           const uint8_t* raw = sm + C::R0 + (kv * NRAW + rs) * C::RAW;
           uint8_t* tile = sm + (kv ? C::V0 : C::K0) + st * C::TILE;
+          const uint8_t* rows = raw + C::RAWB + C::RBS;
+          auto inside = [&](int row) {   // one of the item's keys, in a page
+            return kb + row >= it.s.lo && kb + row <= it.s.base + it.s.n && ((live >> (row >> 4)) & 1u);
+          };
+          if (kv == 0) {
+            // the keys' factors: their powers of two relative to the largest, and those of their values
+            unsigned top = 0;
 #pragma unroll
-            for (int x = tid; x < BK * (D / 16); x += 128) {
-              const int row = x / (D / 16), gr = x % (D / 16), key = kb + row;
-              const unsigned b = raw[C::RAWB + C::RBS + row];
-              const float f = pow2_of(b);
-              uint32_t w[8];
-              if constexpr (FMT == kFmtFP8) {
-                const uint4 y = *reinterpret_cast<const uint4*>(raw + row * C::ROWB + gr * 16);
-                const uint32_t code[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  uint32_t h[2];
-                  e4m3x4_f16(code[e], h[0], h[1]);
-#pragma unroll
-                  for (int z = 0; z < 2; ++z) {
-                    float a0, a1;
-                    unpack_f16(h[z], a0, a1);
-                    w[2 * e + z] = pack_bf16x2(a0 * f, a1 * f);
-                  }
-                }
-              } else {
-                const uint2 y = *reinterpret_cast<const uint2*>(raw + row * C::ROWB + gr * 8);
-                float sf, unused;
-                unpack_f16(e4m3x2_f16x2(raw[C::RAWB + x]), sf, unused);
-                const float unit = sf * f;
-                uint32_t h[8];
-                e2m1x8_f16(y.x, h);
-                e2m1x8_f16(y.y, h + 4);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  float a0, a1;
-                  unpack_f16(h[e], a0, a1);
-                  w[e] = pack_bf16x2(a0 * unit, a1 * unit);
-                }
-              }
-              if (kv == 1 && !whole) {   // rows outside the item's keys, and rows that are no numbers
-                const bool in = key >= it.s.lo && key <= it.s.base + it.s.n && ((live >> (row >> 4)) & 1u);
-                if (in && b == 255) odd = true;
-                if (!in || b == 255)
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) w[e] = 0;
-              }
-              uint8_t* to = tile + (gr >> 2) * BK * 128 + row * 128;
-              const int ch = (2 * gr) & 7;
-              *reinterpret_cast<uint4*>(to + ((ch ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-              *reinterpret_cast<uint4*>(to + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+            for (int e = 0; e < 2; ++e) {
+              const unsigned b = rows[lane + 32 * e];
+              if (inside(lane + 32 * e) && b != 255) top = max(top, b);
             }
+            top = __reduce_max_sync(0xffffffffu, top);
+            Factors* fa = reinterpret_cast<Factors*>(sm + C::FAC) + nb % kFac;
+            const int row = 16 * (warp - 12) + (lane & 15);
+            const unsigned b = rows[row], bv = rows[BK + row];
+            if (lane < 16) {
+              // never zero: hidden keys' logits are -inf (a row that is no numbers brings its NaN in its codes)
+              fa->k[row] = __uint_as_float(unsigned(min(127, max(1, int(b) - int(top) + 127))) << 23);
+            } else {
+              fa->v[row] = bv == 255 ? 0.f : float(int(bv) - 127);
+            }
+            if (row == 0 && lane == 0) fa->top = float(int(top) - 127);
+          }
+#pragma unroll
+          for (int x = tid; x < BK * (D / 16); x += 128) {
+            const int row = x / (D / 16), gr = x % (D / 16);
+            uint32_t w[8];
+            if constexpr (FMT == kFmtFP8) {
+              const uint4 y = *reinterpret_cast<const uint4*>(raw + row * C::ROWB + gr * 16);
+              e4m3x4_f16(y.x, w[0], w[1]);
+              e4m3x4_f16(y.y, w[2], w[3]);
+              e4m3x4_f16(y.z, w[4], w[5]);
+              e4m3x4_f16(y.w, w[6], w[7]);
+            } else {
+              const uint2 y = *reinterpret_cast<const uint2*>(raw + row * C::ROWB + gr * 8);
+              const uint32_t unit = e4m3x2_f16x2(raw[C::RAWB + x] * 0x101u);
+              e2m1x8_f16(y.x, w);
+              e2m1x8_f16(y.y, w + 4);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = mul_f16x2(w[e], unit);
+            }
+            // no numbers: NaN, but for values of blocks that not all rows see: zero, as for keys that are not the item's
+            const bool none = rows[row] == 255, out = kv == 1 && !whole && !inside(row);
+            if (none || out) {
+              const bool zero = kv == 1 && !whole;
+              if (zero && !out) odd = true;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = zero ? 0u : 0x7FFF7FFFu;
+            }
+            uint8_t* to = tile + (gr >> 2) * BK * 128 + row * 128;
+            const int ch = (2 * gr) & 7;
+            *reinterpret_cast<uint4*>(to + ((ch ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(to + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
           if (odd) misc[2] = 1;
           fence_proxy_async_smem();
           __syncwarp();
@@ -929,7 +1053,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
           const unsigned live = masks[8 + st];
           if (live == 15u && it.whole(j)) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(v_empty + 8 * st);
+            if (lane == 0) mbar_arrive(v_clean + 8 * st);
             continue;
           }
           bool odd = false;
@@ -955,10 +1079,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
           if (odd) misc[2] = 1;
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(v_clean + 8 * st);
-            mbar_arrive(v_empty + 8 * st);
-          }
+          if (lane == 0) mbar_arrive(v_clean + 8 * st);
         }
       }
       if (!ok) misc[1] = 1;

@@ -16,11 +16,12 @@ namespace tree {
 constexpr int BK = 64;            // keys of a block
 constexpr int ROWS = 128;         // rows of a tile
 constexpr int kNodes = 64;        // tree rows of a sequence at most
-constexpr int kMaxSeqs = 512;     // sequences of one launch
+constexpr int kMaxSeqs = 256;     // sequences of one launch
 constexpr int kGrid = 152;        // CTAs at most (the workspace is sized for this many)
 constexpr int kFlush = 128;       // blocks of a stream between flushes of O: 1024 MMAs
 constexpr float kNegInf = -INFINITY;
-constexpr int kRescale = 8;       // log2 of what a block's weights may sum to before the running max is taken anew
+constexpr int kRescale = 8;       // log2 of what a block's weights may come to before the running max is taken anew
+constexpr int kBias = 7;          // over quantised pages P <= 2^(kRescale + kBias), below 65504
 
 struct Params {
   const uint16_t* q;

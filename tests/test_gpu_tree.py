@@ -6,8 +6,11 @@ W (2 d + r), W = sum p|v| (64 bits, gated). d bounds the logit error: D products
 each sum off by at most 2^-23 of the sum of magnitudes: d = D 2^-23 max_i sum|q k_i| / sqrt(D). r
 bounds the relative error of a weight and of the sum of O: 2^-15 for P in two bf16 halves (2^-17), exp2
 (2^-21), the joins and the row sums, and 2^-24 of the running sum for each accumulating MMA, two per 16 keys,
-at most 1024 of them before a flush; flushed parts add up in FP32. Stored values of every format are exact
-in bf16. A weight below FP32's smallest normal 2^-126 (relative to the running max, which is the largest logit's or
+at most 1024 of them before a flush; flushed parts add up in FP32. Over quantised pages the codes are exact in f16 and P,
+the weight times its value row's power of two, is rounded to f16 once: half a step, 2^-11, more to r, and the f16 floor: a
+P below f16's smallest step 2^-24 is off by half of it where the largest of the row is 2^7 or more, so by 2^-32 of the
+largest weighted value max|v| for each of the row's keys. q's f16 values are exact down to 2^-31 of the row's largest
+magnitude, and below off by 2^-39 of it: far below d. A weight below FP32's smallest normal 2^-126 (relative to the running max, which is the largest logit's or
 less) is lost, and so is a low half below it: 2^-125 max|v| for each of the row's keys; a result below bf16's normal
 range is off by half its step there, 2^-134. The gate's sigmoid is within 2^-20 and scales what it gates.
 
@@ -53,11 +56,11 @@ def attend(cfg, c, q, seq, start, base, mask, most, g=None, bias=None, w_o=None,
     return out
 
 
-def bound(cfg, ref, mag, counts, logit, most):
+def bound(cfg, fmt, ref, mag, counts, logit, most):
     D = cfg.head_dim
-    r = 2.0 ** -15 + np.minimum(counts / 8 + 2, 1024) * 2.0 ** -24
+    r = 2.0 ** -15 + (0.0 if fmt == "bf16" else 2.0 ** -11) + np.minimum(counts / 8 + 2, 1024) * 2.0 ** -24
     d = D * 2.0 ** -23 * logit
-    floor = counts[:, None] * 2.0 ** -125 * most + 2.0 ** -133
+    floor = counts[:, None] * (2.0 ** -125 if fmt == "bf16" else 2.0 ** -32) * most + 2.0 ** -133
     return 2.0 ** -8 * np.abs(ref) + mag * np.repeat(2 * d + r[:, None], D, axis=1) + np.repeat(floor, D, axis=1)
 
 
@@ -74,7 +77,7 @@ def check(cfg, c, q, seq, start, base, nodes, out, g=None, bias=None, only=None)
             continue
         ref, *sizes = OT.tree_attention(cfg.n_q, qq[a:b], hc, seq[i], base[i], nodes[a:b],
                                                     None if gg is None else gg[a:b], bb)
-        err, tol = np.abs(o[a:b] - ref), bound(cfg, ref, *sizes)
+        err, tol = np.abs(o[a:b] - ref), bound(cfg, hc.fmt, ref, *sizes)
         assert np.array_equal(np.isfinite(o[a:b]), np.isfinite(ref))
         fin = np.isfinite(ref)
         if fin.any():
@@ -650,7 +653,7 @@ def check_layer(W, cache, t, start, held, nodes, what):
     for s in range(3):
         a, b = start[s], start[s + 1]
         og, *sizes = OT.tree_attention(TINY.n_q, q[a:b], hc, s, held[s], nodes[a:b], g[a:b], np64(W["gate_bias"]))
-        tol = bound(cfg_for(TINY.n_q, TINY.n_kv, TINY.head_dim), og, *sizes)
+        tol = bound(cfg_for(TINY.n_q, TINY.n_kv, TINY.head_dim), hc.fmt, og, *sizes)
         ref = og @ w.T
         lim = tol @ np.abs(w).T + og.shape[1] * 2.0 ** -23 * (np.abs(og) @ np.abs(w).T) + 2.0 ** -8 * np.abs(ref)
         worst = float(np.max(np.abs(np64(t["attn"])[a:b] - ref) / lim))
