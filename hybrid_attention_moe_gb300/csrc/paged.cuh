@@ -90,6 +90,12 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Where a token's rows go: the page of its 1-based slot p, or -1 (padding, or out of range: the bit to
 // set in bad).
 __device__ __forceinline__ int page_of(const beam_paged_kv& c, int s, int p, int shift,

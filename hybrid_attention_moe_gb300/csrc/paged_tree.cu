@@ -69,6 +69,7 @@ struct Cfg {
   static constexpr int NH = D / 64;                 // 64-wide halves of a row
   static constexpr int TILE = BK * D * 2;           // K or V block in bf16
   static constexpr int NST = QUANT ? 3 : (D == 128 ? 4 : 8);
+  static_assert(QUANT || NST % 2 == 0, "stages that keys' copies fill in any order: of items of one tile each is one stream's");
   static constexpr int RAWB = QUANT ? BK * ROWB : 0;
   static constexpr int RBS = FMT == kFmtNVFP4 ? BK * (D / 16) : 0;
   static constexpr int RAW = QUANT ? RAWB + RBS + 2 * BK : 0;   // a raw stage: codes, block scales, row scales (with K's: both)
@@ -82,7 +83,7 @@ struct Cfg {
   static constexpr int XCH = FAC + (QUANT ? kFac * int(sizeof(Factors)) : 0);   // [128] (m, z, sum) of stream 1
   static constexpr int MASK = XCH + ROWS * 16;                    // [2][8] slices of a K or V stage that have a page
   static constexpr int BAR = MASK + 16 * 4;
-  static constexpr int NBAR = 5 * NST + 4 * NRAW + 18;
+  static constexpr int NBAR = 5 * NST + 4 * NRAW + 22;
   static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int BYTES = MISC + 32 + 1024;
   static_assert(BYTES <= 227 * 1024, "shared memory");
@@ -196,6 +197,25 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
           "r"(dst), "l"(src), "r"(bytes), "r"(mbar)
       : "memory");
+}
+// mbar_wait whose polls may suspend the thread for some microseconds: the many waiting warps of a CTA would otherwise poll
+// away a quarter of its issue slots. False after about two seconds.
+__device__ __forceinline__ bool wait(uint32_t a, uint32_t parity) {
+  for (uint32_t i = 0; i < 1u << 18; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(a), "r"(parity), "r"(8000u)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+// Arrival of a whole warp, once.
+__device__ __forceinline__ void arrive(uint32_t a) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(a);
 }
 template <int N, bool MORE>
 __device__ __forceinline__ void set_regs() {
@@ -323,7 +343,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
   const uint32_t k_full = sb + C::BAR, k_empty = k_full + 8 * NST, v_full = k_empty + 8 * NST,
                  v_empty = v_full + 8 * NST, r_full = v_empty + 8 * NST, r_empty = r_full + 16 * NRAW;
   const uint32_t q_full = r_empty + 16 * NRAW, s_full = q_full + 16, p_full = s_full + 32, pv_done = p_full + 32,
-                 o_full = pv_done + 16, o_empty = o_full + 16, x_full = o_empty + 16, x_empty = x_full + 8, v_clean = x_empty + 8;
+                 o_full = pv_done + 16, o_empty = o_full + 16, x_full = o_empty + 16, x_empty = x_full + 8, v_clean = x_empty + 8,
+                 meet = v_clean + 8 * NST;   // [item's parity][stream]
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(k_full + 8 * i, C::QUANT ? 4 : 1);
@@ -337,17 +358,19 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       mbar_init(r_empty + 8 * i, 4);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(q_full + 8 * s, ROWS);
+      mbar_init(q_full + 8 * s, 4);
+      mbar_init(meet + 8 * s, 1);
+      mbar_init(meet + 16 + 8 * s, 1);
       for (int i = 0; i < 2; ++i) {
         mbar_init(s_full + 16 * s + 8 * i, 1);
-        mbar_init(p_full + 16 * s + 8 * i, ROWS);
+        mbar_init(p_full + 16 * s + 8 * i, 4);
       }
       mbar_init(pv_done + 8 * s, 1);
       mbar_init(o_full + 8 * s, 2);
-      mbar_init(o_empty + 8 * s, ROWS);
+      mbar_init(o_empty + 8 * s, 4);
     }
-    mbar_init(x_full, ROWS);
-    mbar_init(x_empty, ROWS);
+    mbar_init(x_full, 4);
+    mbar_init(x_empty, 4);
     misc[1] = 0;
     misc[2] = 0;
     *status = 0;
@@ -420,7 +443,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         const size_t head = size_t(mine ? page : 0) * P.c.n_kv + it.h;
         entry = lane < 4 && j + 1 < it.j1 ? entry_of_slice(P, it.s, j + 1, lane) : -2;   // the next block's, meanwhile
         const int st = int(nb % DEPTH);
-        if (!__all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ((nb / DEPTH) & 1) ^ 1))) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, wait(empty + 8 * st, ((nb / DEPTH) & 1) ^ 1))) { ok = false; break; }
         const uint32_t keys = uint32_t(run * 16), bar = full + 8 * st;
         if (lane == 0) {
           masks[8 * kv + st] = live;
@@ -447,13 +470,15 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     if (!ok) {
       misc[1] = 1;
       // copies in flight land before the CTA's shared memory goes away
-      for (uint32_t b = nb > DEPTH ? nb - DEPTH : 0; b < nb; ++b) mbar_wait(full + 8 * (b % DEPTH), (b / DEPTH) & 1);
+      for (uint32_t b = nb > DEPTH ? nb - DEPTH : 0; b < nb; ++b) wait(full + 8 * (b % DEPTH), (b / DEPTH) & 1);
     }
   } else {
     // ------------------------------------------------------------------ matrix products of stream s
-    // A step is one block that both streams take (items of two tiles), or a block for each. S of step x + 2 is issued
-    // behind P.V of step x, whose buffer it takes (operations of one thread run in order). Both streams wait for all
-    // blocks and release all, so that neither is ever a lap of the ring ahead.
+    // A step is one block that both streams take (items of two tiles) or every other block, which the stream alone takes
+    // and releases. S of step x + 2 is issued behind P.V of step x, whose buffer it takes (operations of one thread run
+    // in order). A stream may wait for a stage's phase only where the one before is known to be over: the stage's block
+    // before was its own, or was filled before one that it has seen (the quantised pages' three stages are filled in
+    // order), or is of an earlier item, all of which are over for both where the streams meet.
     const int s = warp >> 1;
     const uint32_t v_ready = C::QUANT ? v_full : v_clean;
     uint32_t nb = 0;                            // blocks of earlier items
@@ -490,58 +515,46 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     };
     Item it;
     for (int c = c0; ok && next_item(P, plan, c, c1, it);) {
-      const int cnt = it.j1 - it.j0, per = it.w == 2 ? 1 : 2, steps = (cnt + per - 1) / per;
-      ok = all(mbar_wait(q_full + 8 * s, qn & 1));
-      ++qn;
+      const int cnt = it.j1 - it.j0, per = it.w == 2 ? 1 : 2, off = it.w == 2 ? 0 : s, steps = units_of(it, s);
+      ok = all(wait(q_full + 8 * s, qn & 1));
       if (!ok) break;
       tc_fence_after();
-      // Blocks of step x: b and, of items of one tile, b + 1 if there is one; the stream's own is b + s there.
-      auto two_of = [&](int x) { return per == 2 && 2 * x + 1 < cnt; };
-      auto ready = [&](uint32_t bars, uint32_t b) { return mbar_test(bars + 8 * (b % NST), (b / NST) & 1); };
-      auto await = [&](bool r, uint32_t bars, uint32_t b) { return r || mbar_wait(bars + 8 * (b % NST), (b / NST) & 1); };
-      auto make_s = [&](int x) {   // S of step x, whose keys are there
-        const uint32_t b = nb + uint32_t(per * x);
-        const bool two = two_of(x), own = per == 1 || s == 0 || two;
-        const int mine = int((per == 2 && s == 1 ? b + 1 : b) % NST), others = int((s == 1 ? b : b + 1) % NST);
-        if (own) {
-          qk(mine);
-          umma_commit_e(k_empty + 8 * mine);
-        }
-        if (lane == 0 && per == 2 && (s == 1 || two)) mbar_arrive(k_empty + 8 * others);
-      };
-      for (int x = 0; x < 2 && x < steps && ok; ++x) {
-        const uint32_t b = nb + uint32_t(per * x);
-        ok = all(await(false, k_full, b) && await(!two_of(x), k_full, b + 1));
-        tc_fence_after();
-        if (ok) make_s(x);
-      }
-      for (int x = 0; x < steps && ok; ++x) {
-        const uint32_t b = nb + uint32_t(per * x), bk = b + uint32_t(2 * per);
-        const bool two = two_of(x), own = per == 1 || s == 0 || two, more = x + 2 < steps;
-        const bool fresh = own && x % kFlush == 0;
+      if (lane == 0) mbar_arrive(meet + 16 * (qn & 1) + 8 * (s ^ 1));
+      ok = all(wait(meet + 16 * (qn & 1) + 8 * s, (qn >> 1) & 1));
+      ++qn;
+      if (!ok) break;
+#pragma unroll 1
+      for (int x = -2; x < steps; ++x) {
+        const uint32_t b = nb + uint32_t(per * x + off), bk = b + uint32_t(2 * per);   // blocks of V and of K that are due
+        const int st = int(b % NST), sk = int(bk % NST);
+        const bool values = x >= 0, more = x + 2 < steps, fresh = values && x % kFlush == 0;
         const uint32_t pb = p_full + 16 * s + 8 * (un & 1);
         // polled together, so that their latencies overlap, then waited for one by one
-        const bool r0 = ready(v_ready, b), r1 = !two || ready(v_ready, b + 1);
-        const bool r2 = !own || mbar_test(pb, (un >> 1) & 1);
-        const bool r3 = !fresh || mbar_test(o_empty + 8 * s, (ost & 1) ^ 1);
-        const bool k0 = !more || ready(k_full, bk), k1 = !two_of(x + 2) || ready(k_full, bk + 1);
-        if (!all(await(r0, v_ready, b) && await(r1, v_ready, b + 1) && (r3 || mbar_wait(o_empty + 8 * s, (ost & 1) ^ 1)) &&
-                 (r2 || mbar_wait(pb, (un >> 1) & 1)))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (own) {
-          const int mine = int((per == 2 && s == 1 ? b + 1 : b) % NST);
-          if (fresh) ++ost;
-          pv(mine, fresh);
-          umma_commit_e(v_empty + 8 * mine);
-        }
-        if (lane == 0 && per == 2 && (s == 1 || two)) mbar_arrive(v_empty + 8 * ((s == 1 ? b : b + 1) % NST));
-        if (more) {
-          ok = all(await(k0, k_full, bk) && await(k1, k_full, bk + 1));
+        const bool r0 = !values || mbar_test(v_ready + 8 * st, (b / NST) & 1);
+        const bool r1 = !values || mbar_test(pb, (un >> 1) & 1);
+        const bool r2 = !more || mbar_test(k_full + 8 * sk, (bk / NST) & 1);
+        if (values) {
+          if (!all(r0 && r1 && !fresh) &&
+              !all((r0 || wait(v_ready + 8 * st, (b / NST) & 1)) && (!fresh || wait(o_empty + 8 * s, (ost & 1) ^ 1)) &&
+                   (r1 || wait(pb, (un >> 1) & 1)))) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
-          if (ok) make_s(x + 2);
+          if (fresh) ++ost;
+          pv(st, fresh);
+          umma_commit_e(v_empty + 8 * st);
+          if (per == 2) umma_commit_e(v_empty + 8 * st);
+        }
+        if (more) {
+          if (!all(r2) && !all(wait(k_full + 8 * sk, (bk / NST) & 1))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          qk(sk);
+          umma_commit_e(k_empty + 8 * sk);
+          if (per == 2) umma_commit_e(k_empty + 8 * sk);
         }
       }
       if (!ok) break;
@@ -613,7 +626,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         }
         fence_proxy_async_smem();
       }
-      mbar_arrive(q_full + 8 * s);
+      arrive(q_full + 8 * s);
       return x;
     };
     Item it, nx;
@@ -640,170 +653,154 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         if (k + 1 < units) entry = lane < 4 ? entry_of_slice(P, it.s, j + stride, lane) : -2;   // the next one's, meanwhile
         const bool full = !none && slices == 15u && it.whole(j);
         const uint32_t ts = t0 + 64 * (un & 1), bar = 16 * s + 8 * (un & 1);
-        if (!all(mbar_wait(s_full + bar, (un >> 1) & 1))) { ok = false; break; }
+        if (!all(wait(s_full + bar, (un >> 1) & 1))) { ok = false; break; }
         tc_fence_after();
         if (work) {
           const uint64_t bits = full ? ~uint64_t(0) : seen(v, it.s, (it.s.blk0 + j) * BK + 1, slices);
-          // half x of S, keys that the row does not see at -inf
-          auto load = [&](uint32_t (&sv)[32], int x) {
-            tmem_ld32_nowait(ts + 32 * x, sv);
-          };
-          auto hide = [&](uint32_t (&sv)[32], int x) {
-            const uint32_t b32 = uint32_t(bits >> (32 * x));
-            if (!full)
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((b32 >> e) & 1u)) sv[e] = __float_as_uint(kNegInf);
-          };
           [[maybe_unused]] const Factors* fa = reinterpret_cast<const Factors*>(sm + C::FAC) + ((nb + uint32_t(j - it.j0)) % kFac);
-          [[maybe_unused]] float rf = 0.f;   // factor of S times its key's, in log2 units of the weight
-          if constexpr (C::QUANT) rf = ex2(fmaxf(fminf(fa->top + cur.qe, 120.f), -120.f)) * P.sl2;
-          unsigned most = 0;   // the largest of P in f16
-          // P of a half; returns the sum of the weights. BF16: 2^(S c - m), its high parts and low parts. Quantised:
-          // 2^(S c k - m + e - (z - m)) in f16, with the keys' factors k and e.
-          auto weigh = [&](const uint32_t (&sv)[32], int x, uint32_t* pk) {
-            const float nm = m == kNegInf ? 0.f : -m;
-            const uint64_t nm2 = f2(nm, nm);
-            uint64_t ls[4] = {0, 0, 0, 0};
-            if constexpr (!C::QUANT) {
-              const uint64_t c2 = f2(P.sl2, P.sl2);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float x0, x1;
-                f2_split(fma2(f2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), c2, nm2), x0, x1);
-                const float p0 = ex2(x0), p1 = ex2(x1);
-                const uint64_t pp = f2(p0, p1);
-                ls[e & 3] = add2(ls[e & 3], pp);
-                const uint32_t hi = pack_bf16x2(p0, p1);
-                float d0, d1;
-                f2_split(sub2(pp, f2(bf_lo(hi), bf_hi(hi))), d0, d1);
-                pk[e] = hi;
-                pk[16 + e] = pack_bf16x2(d0, d1);
-              }
-            } else {
-              const uint64_t c2 = f2(rf, rf);
-              const float nz = z == kNegInf ? 0.f : -z;
-              const uint64_t nz2 = f2(nz, nz);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 kf = reinterpret_cast<const float4*>(fa->k + 32 * x)[e], ve = reinterpret_cast<const float4*>(fa->v + 32 * x)[e];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const uint64_t sk = mul2(f2(__uint_as_float(sv[4 * e + 2 * i]), __uint_as_float(sv[4 * e + 2 * i + 1])),
-                                           i ? f2(kf.z, kf.w) : f2(kf.x, kf.y));
-                  float y0, y1, z0, z1;
-                  f2_split(fma2(sk, c2, nm2), y0, y1);
-                  f2_split(fma2(sk, c2, add2(i ? f2(ve.z, ve.w) : f2(ve.x, ve.y), nz2)), z0, z1);
-                  ls[2 * (e & 1) + i] = add2(ls[2 * (e & 1) + i], f2(ex2(y0), ex2(y1)));
-                  const uint32_t w = pack_f16x2(ex2(z0), ex2(z1));
-                  pk[2 * e + i] = w;
-                  most = __vmaxu2(most, w);
-                }
-              }
-            }
-            float a0, a1, b0, b1;
-            f2_split(add2(ls[0], ls[1]), a0, a1);
-            f2_split(add2(ls[2], ls[3]), b0, b1);
-            return (a0 + b0) + (a1 + b1);
-          };
-          // The references stay while the block's weights sum to no more than 2^kRescale (quantised pages: while FP32 holds
-          // them, and P is no more than 2^(kRescale + kBias)); a row's first block, and one that exceeds that, are gone
-          // through for their maxima, and O and the sum are rescaled.
-          constexpr int HALF = C::QUANT ? 16 : 32;   // words of P of a half
-          uint32_t pk[2 * HALF];
-          auto weights = [&]() {
-            float sum;
-            if constexpr (C::QUANT) {   // half by half: registers
-              uint32_t sv[32];
-              load(sv, 0);
-              tmem_wait_ld();
-              hide(sv, 0);
-              sum = weigh(sv, 0, pk);
-              load(sv, 1);
-              tmem_wait_ld();
-              hide(sv, 1);
-              sum += weigh(sv, 1, pk + HALF);
-            } else {
-              uint32_t s0[32], s1[32];
-              load(s0, 0);
-              load(s1, 1);
-              tmem_wait_ld();
-              hide(s0, 0);
-              hide(s1, 1);
-              sum = weigh(s0, 0, pk);
-              sum += weigh(s1, 1, pk + HALF);
-            }
-            return sum;
-          };
-          float sum = 0.f;
-          bool lag = m == kNegInf;
-          if (!__any_sync(0xffffffffu, lag)) {
-            sum = weights();
-            lag = C::QUANT ? !(sum <= 0x1p60f) || max(most & 0xFFFFu, most >> 16) > 0x7800u : !(sum <= float(1 << kRescale));
-          }
-          if (__any_sync(0xffffffffu, lag)) {
-            float mt = kNegInf, zt = kNegInf;
+          float rf = P.sl2;   // factor of S (over quantised pages, of S times its key's) in log2 units of the weight
+          if constexpr (C::QUANT) rf *= ex2(fmaxf(fminf(fa->top + cur.qe, 120.f), -120.f));
+          constexpr int HALF = C::QUANT ? 16 : 32;   // words of P of 32 keys
+          // 32 keys at a time, in a loop: the code of all roles has to stay in the instruction cache
 #pragma unroll 1
-            for (int x = 0; x < 2; ++x) {
-              uint32_t sv[32];
-              load(sv, x);
-              tmem_wait_ld();
-              hide(sv, x);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                if constexpr (C::QUANT) {
-                  const float y = __uint_as_float(sv[e]) * fa->k[32 * x + e] * rf;
-                  mt = fmaxf(mt, y);
-                  zt = fmaxf(zt, y + fa->v[32 * x + e]);
-                } else {
-                  mt = fmaxf(mt, __uint_as_float(sv[e]));
-                }
-              }
-            }
-            if constexpr (C::QUANT) zt -= float(kBias);
-            else zt = mt = mt * P.sl2;
-            // a row that another's first block brought here is held to the same bound
-            const float by = lag ? 0.f : float(kRescale);
-            const bool need = m != kNegInf && (mt > m + by || zt > z + by);
-            if (__any_sync(0xffffffffu, need)) {
-              // O holds the stream's earlier products: the last one has to be done
-              if (!all(mbar_wait(pv_done + 8 * s, (un - 1) & 1))) { ok = false; break; }
-              tc_fence_after();
-              const float m1 = need ? fmaxf(m, mt) : m, z1 = need ? fmaxf(z, zt) : z;
-              const float f = z1 == z ? 1.f : ex2(z - z1);
-              if (k % kFlush != 0) {   // after a flush O is not read again
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t b32 = uint32_t(bits >> (32 * x));
+            uint32_t sv[32], pk[HALF];
+            tmem_ld32_nowait(ts + 32 * x, sv);
+            tmem_wait_ld();
+            float sum = 0.f;
+            bool lag = m == kNegInf;
 #pragma unroll 1
-                for (int x = 0; x < D / 16; ++x) {
-                  uint32_t o[16];
-                  tmem_ld16(to + 16 * x, o);
+            for (int turn = 0; turn < 2; ++turn) {
+              if (!full) {   // keys that the row does not see
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                  tmem_st16(to + 16 * x, o);
-                }
-                tmem_wait_st();
+                for (int e = 0; e < 32; ++e)
+                  if (!((b32 >> e) & 1u)) sv[e] = __float_as_uint(kNegInf);
               }
-              if (flushed && f != 1.f)
-                for (int x = 0; x < D; ++x) fl[s * ROWS * D + x] *= f;
-              if (m1 != m) l *= ex2(m - m1);
-              m = m1;
-              z = z1;
+              if (turn == 1 || __any_sync(0xffffffffu, lag)) {
+                // The references are taken anew: O, the sum and the P of this block's first half are brought to them by whole
+                // powers of two.
+                float mt = kNegInf, zt = kNegInf;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  if constexpr (C::QUANT) {
+                    const float y = __uint_as_float(sv[e]) * fa->k[32 * x + e] * rf;
+                    mt = fmaxf(mt, y);
+                    zt = fmaxf(zt, y + fa->v[32 * x + e]);
+                  } else {
+                    mt = fmaxf(mt, __uint_as_float(sv[e]));
+                  }
+                }
+                if constexpr (C::QUANT) zt -= float(kBias);
+                else zt = mt = mt * rf;
+                // a row that another's first keys brought here is held to the same bound
+                const float by = lag ? 0.f : float(kRescale);
+                const bool need = m != kNegInf && (mt > m + by || zt > z + by);
+                if (__any_sync(0xffffffffu, need)) {
+                  // O holds the stream's earlier products: the last one has to be done
+                  if (!all(k == 0 || wait(pv_done + 8 * s, (un - 1) & 1))) { ok = false; break; }
+                  tc_fence_after();
+                  const float dm = need ? fmaxf(0.f, ceilf(mt - m)) : 0.f, dz = need ? fmaxf(0.f, ceilf(zt - z)) : 0.f;
+                  const float f = ex2(-dz);
+                  if (k % kFlush != 0) {   // else O is not read again
+#pragma unroll 1
+                    for (int y = 0; y < D / 16; ++y) {
+                      uint32_t o[16];
+                      tmem_ld16(to + 16 * y, o);
+#pragma unroll
+                      for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                      tmem_st16(to + 16 * y, o);
+                    }
+                  }
+                  if (x == 1) {
+                    const uint32_t f16 = C::QUANT ? pack_f16x2(f, f) : pack_bf16x2(f, f);
+#pragma unroll 1
+                    for (int y = 0; y < HALF / 16; ++y) {
+                      uint32_t o[16];
+                      tmem_ld16(ts + 16 * y, o);
+#pragma unroll
+                      for (int e = 0; e < 16; ++e) o[e] = C::QUANT ? mul_f16x2(o[e], f16) : mul_bf16x2(o[e], f16);
+                      tmem_st16(ts + 16 * y, o);
+                    }
+                  }
+                  tmem_wait_st();
+                  if (flushed && dz > 0.f)
+                    for (int y = 0; y < D; ++y) fl[s * ROWS * D + y] *= f;
+                  l *= ex2(-dm);
+                  m += dm;
+                  z += dz;
+                }
+                if (m == kNegInf) {   // the row's first keys
+                  m = mt;
+                  z = zt;
+                }
+                turn = 1;
+              }
+              // P, and the sum of the weights. BF16: 2^(S c - m), its high parts and low parts. Quantised:
+              // 2^(S c k - m + e - (z - m)) in f16, with the keys' factors k and e.
+              const float nm = m == kNegInf ? 0.f : -m;
+              const uint64_t c2 = f2(rf, rf), nm2 = f2(nm, nm);
+              uint64_t ls[4] = {0, 0, 0, 0};
+              unsigned most = 0;   // the largest of P in f16
+              if constexpr (!C::QUANT) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  float x0, x1;
+                  f2_split(fma2(f2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), c2, nm2), x0, x1);
+                  const float p0 = ex2(x0), p1 = ex2(x1);
+                  const uint64_t pp = f2(p0, p1);
+                  ls[e & 3] = add2(ls[e & 3], pp);
+                  const uint32_t hi = pack_bf16x2(p0, p1);
+                  float d0, d1;
+                  f2_split(sub2(pp, f2(bf_lo(hi), bf_hi(hi))), d0, d1);
+                  pk[e] = hi;
+                  pk[16 + e] = pack_bf16x2(d0, d1);
+                }
+              } else {
+                const float nz = z == kNegInf ? 0.f : -z;
+                const uint64_t nz2 = f2(nz, nz);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float4 kf = reinterpret_cast<const float4*>(fa->k + 32 * x)[e], ve = reinterpret_cast<const float4*>(fa->v + 32 * x)[e];
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    const uint64_t sk = mul2(f2(__uint_as_float(sv[4 * e + 2 * i]), __uint_as_float(sv[4 * e + 2 * i + 1])),
+                                             i ? f2(kf.z, kf.w) : f2(kf.x, kf.y));
+                    float y0, y1, z0, z1;
+                    f2_split(fma2(sk, c2, nm2), y0, y1);
+                    f2_split(fma2(sk, c2, add2(i ? f2(ve.z, ve.w) : f2(ve.x, ve.y), nz2)), z0, z1);
+                    ls[2 * (e & 1) + i] = add2(ls[2 * (e & 1) + i], f2(ex2(y0), ex2(y1)));
+                    const uint32_t w = pack_f16x2(ex2(z0), ex2(z1));
+                    pk[2 * e + i] = w;
+                    most = __vmaxu2(most, w);
+                  }
+                }
+              }
+              float a0, a1, b0, b1;
+              f2_split(add2(ls[0], ls[1]), a0, a1);
+              f2_split(add2(ls[2], ls[3]), b0, b1);
+              sum = (a0 + b0) + (a1 + b1);
+              // The references stay while the weights sum to no more than 2^kRescale (quantised pages: while FP32 holds them
+              // and P is no more than 2^(kRescale + kBias)).
+              lag = C::QUANT ? !(sum <= 0x1p60f) || max(most & 0xFFFFu, most >> 16) > 0x7800u : !(sum <= float(1 << kRescale));
+              if (turn == 0) {
+                if (!__any_sync(0xffffffffu, lag)) break;
+                tmem_ld32_nowait(ts + 32 * x, sv);   // P may have taken its registers
+                tmem_wait_ld();
+              }
             }
-            if (m == kNegInf) {   // the row's first keys
-              m = mt;
-              z = zt;
-            }
-            most = 0;
-            sum = weights();
+            if (!ok) break;
+            l += sum;
+            if constexpr (C::QUANT) tmem_st16(ts + 16 * x, pk);
+            else tmem_st32(ts + 32 * x, pk);
           }
-          l += sum;
-          tmem_st32(ts, pk);
-          if (!C::QUANT) tmem_st32(ts + 32, pk + 32);
+          if (!ok) break;
           tmem_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(p_full + bar);
+        arrive(p_full + bar);
         if ((k + 1) % kFlush == 0 && k + 1 < units) {
-          if (!all(mbar_wait(pv_done + 8 * s, un & 1))) { ok = false; ++un; break; }
+          if (!all(wait(pv_done + 8 * s, un & 1))) { ok = false; ++un; break; }
           tc_fence_after();
 #pragma unroll 1
           for (int x = 0; x < D / 32; ++x) {
@@ -823,7 +820,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
           }
           flushed = true;
           tc_fence_before();
-          mbar_arrive(o_empty + 8 * s);
+          arrive(o_empty + 8 * s);
         }
       }
       if (!ok) break;
@@ -832,7 +829,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       more = next_item(P, plan, c, c1, nx);
       const bool ahead = more && units > 0 && units_of(nx, s) > 0;
       if (ahead) w = row_of(nx);
-      if (!all(mbar_wait(o_full + 8 * s, items & 1))) { ok = false; break; }
+      if (!all(wait(o_full + 8 * s, items & 1))) { ok = false; break; }
       tc_fence_after();
       // O's factors h^2 (in two steps, which alone may leave FP32's range) to the reference m of what is written
       float h0 = 1.f, h1 = 0.f;
@@ -842,18 +839,18 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         float4* xch = reinterpret_cast<float4*>(sm + C::XCH);
         if (s == 1) {
           // stream 0 writes for both
-          if (!all(mbar_wait(x_empty, (turns & 1) ^ 1))) { ok = false; break; }
+          if (!all(wait(x_empty, (turns & 1) ^ 1))) { ok = false; break; }
           xch[lr] = make_float4(m, z, l, 0.f);
-          mbar_arrive(x_full);
+          arrive(x_full);
           ++turns;
           if (more && !ahead) w = row_of(nx);
           nb += uint32_t(it.j1 - it.j0);
           it = nx;
           continue;
         }
-        if (!all(mbar_wait(x_full, turns & 1))) { ok = false; break; }
+        if (!all(wait(x_full, turns & 1))) { ok = false; break; }
         const float4 y = xch[lr];
-        mbar_arrive(x_empty);
+        arrive(x_empty);
         ++turns;
         other = units_of(it, 1) > 0;
         const float top = fmaxf(m, y.x);
@@ -931,8 +928,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       }
       if (it.split && real) P.part_ml[part] = make_float2(m, l);
       tc_fence_before();
-      if (units > 0) mbar_arrive(o_empty + 8 * s);
-      if (other) mbar_arrive(o_empty + 8);
+      if (units > 0) arrive(o_empty + 8 * s);
+      if (other) arrive(o_empty + 8);
       if (it.split && it.j0 == 0 && threadIdx.x == 4 * 32) {   // one does
         P.join[2 * r] = make_int4(it.h, it.m, range_of(it.f + it.w * (it.s.nb - 1), total, R) - r + 1, it.w);
         *reinterpret_cast<int2*>(P.join + 2 * r + 1) = make_int2(it.s.row0, it.s.n);
@@ -965,8 +962,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       for (int c = c0; ok && next_item(P, plan, c, c1, it);) {
         for (int j = it.j0; j < it.j1; ++j, ++nb) {
           const int rs = int(nb % (NRAW ? NRAW : 1)), st = int(nb % NST);
-          if (!all(mbar_wait(r_full + 8 * (kv * NRAW + rs), (nb / (NRAW ? NRAW : 1)) & 1) &&
-                   mbar_wait(empty + 8 * st, ((nb / NST) & 1) ^ 1))) {
+          if (!all(wait(r_full + 8 * (kv * NRAW + rs), (nb / (NRAW ? NRAW : 1)) & 1) &&
+                   wait(empty + 8 * st, ((nb / NST) & 1) ^ 1))) {
             ok = false;
             break;
           }
@@ -1049,7 +1046,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       for (int c = c0; ok && next_item(P, plan, c, c1, it);) {
         for (int j = it.j0; j < it.j1; ++j, ++nb) {
           const int st = int(nb % NST), kb = (it.s.blk0 + j) * BK + 1;
-          if (!__all_sync(0xffffffffu, mbar_wait(v_full + 8 * st, (nb / NST) & 1))) { ok = false; break; }
+          if (!__all_sync(0xffffffffu, wait(v_full + 8 * st, (nb / NST) & 1))) { ok = false; break; }
           const unsigned live = masks[8 + st];
           if (live == 15u && it.whole(j)) {
             __syncwarp();
