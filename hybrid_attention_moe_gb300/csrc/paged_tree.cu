@@ -118,6 +118,10 @@ __device__ __forceinline__ Seq seq_of(const Params& P, const int4& w) {
   return s;
 }
 
+// Cost of a sequence's items of one head: their blocks by their tiles, and P.item for each, before its blocks: what an
+// item costs beside them.
+__device__ __forceinline__ int cost_of(const Params& P, const Seq& s) { return s.nb * s.tiles + P.item * ((s.tiles + 1) / 2); }
+
 // A CTA's share [j0, j1) of the blocks of item m (tiles 2m, 2m + 1) of one (sequence, KV head).
 struct Item {
   Seq s;
@@ -148,15 +152,15 @@ __device__ __forceinline__ Item item_at(const Params& P, const Plan& L, int c, i
   }
   Item it;
   it.s = seq_of(P, L.seq[a]);
-  const int per = it.s.nb * it.s.tiles, off = c - cum[a];
+  const int per = cost_of(P, it.s), pair = 2 * it.s.nb + P.item, off = c - cum[a];
   it.h = off / per;
   const int rest = off - it.h * per;
-  it.m = rest / (2 * it.s.nb);
+  it.m = rest / pair;
   it.w = 2 * it.m + 1 < it.s.tiles ? 2 : 1;
-  it.f = c - rest + it.m * 2 * it.s.nb;
-  it.j0 = (c - it.f + it.w - 1) / it.w;
+  it.f = c - rest + it.m * pair + P.item;
+  it.j0 = max(0, c - it.f + it.w - 1) / it.w;
   it.next = it.f + it.w * it.s.nb;
-  it.j1 = it.next <= c1 ? it.s.nb : (c1 - it.f + it.w - 1) / it.w;
+  it.j1 = it.next <= c1 ? it.s.nb : max(0, c1 - it.f + it.w - 1) / it.w;
   it.split = it.j0 > 0 || it.j1 < it.s.nb;
   const int hi = P.c.window > 0 ? max(0, it.s.base + it.s.n - P.c.window) : 0;   // before the deepest row's first key
   it.wa = (hi + BK - 1) / BK - it.s.blk0;
@@ -392,7 +396,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         const int4 w = read_seq(P, i0 + lane, bad);
         seqs[i0 + lane] = w;
         const Seq s = seq_of(P, w);
-        c = s.nb * s.tiles * P.n_kv;
+        c = s.n == 0 ? 0 : cost_of(P, s) * P.n_kv;
         if (bad && blockIdx.x == 0) atomicOr(status, bad);
       }
 #pragma unroll
@@ -1171,7 +1175,7 @@ extern "C" beam_status beam_paged_tree_attn(const beam_layer_cfg* cfg, const bea
   if (cache->window > 0 && int64_t(cache->window) + kNodes < keys) keys = int64_t(cache->window) + kNodes;
   const int64_t nb = keys / BK + 2;
   const int slice = N < kMaxSeqs ? N : kMaxSeqs;
-  if (nb * ((kNodes * G + ROWS - 1) / ROWS) * slice * cfg->n_kv > 1 << 30 || cfg->n_kv > 65535) return BEAM_ERR_UNSUPPORTED;
+  if ((nb + kItemBF16) * ((kNodes * G + ROWS - 1) / ROWS) * slice * cfg->n_kv > 1 << 30 || cfg->n_kv > 65535) return BEAM_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   Carver cv{static_cast<char*>(ws), ws_bytes};
   Params p{};
@@ -1194,7 +1198,8 @@ extern "C" beam_status beam_paged_tree_attn(const beam_layer_cfg* cfg, const bea
   p.G = G;
   p.max_pos = max_pos;
   p.shift = log2i(cache->page_size);
-  p.least = 4;
+  p.item = cache->dtype == kFmtBF16 ? kItemBF16 : kItemQuant;
+  p.least = p.item + 4;
   p.sl2 = float(1.4426950408889634 / sqrt(double(D)));
   for (int i0 = 0; i0 < N; i0 += kMaxSeqs) {   // slices in stream order share the workspace
     p.N = N - i0 < kMaxSeqs ? N - i0 : kMaxSeqs;

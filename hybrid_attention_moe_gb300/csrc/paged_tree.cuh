@@ -17,6 +17,12 @@ constexpr int BK = 64;            // keys of a block
 constexpr int ROWS = 128;         // rows of a tile
 constexpr int kNodes = 64;        // tree rows of a sequence at most
 constexpr int kMaxSeqs = 256;     // sequences of one launch
+// What an item costs beside its blocks (filling and draining the streams, queries, references, output), in blocks of one
+// tile; a range costs four blocks more at least. 32 sequences of 1 to 16 nodes over up to 16K keys, in us:
+//   cost     0    4    8   12   20
+//   BF16   443  358  298  252  219
+//   FP8    523  403  326  285  290   (the last ranges, of short sequences, took twice as long as the others)
+constexpr int kItemBF16 = 20, kItemQuant = 14;
 constexpr int kGrid = 152;        // CTAs at most (the workspace is sized for this many)
 constexpr int kFlush = 128;       // blocks of a stream between flushes of O: 1024 MMAs
 constexpr float kNegInf = -INFINITY;
@@ -37,7 +43,8 @@ struct Params {
   float* flush;      // [kGrid][2][ROWS][D]
   int4* join;        // [kGrid][2]: item that begins in the range and runs on: (head, item, parts, tiles), (row0, n, status bits of the CTA, -)
   beam_paged_kv c;
-  int N, T, n_q, n_kv, G, max_pos, shift, least;
+  int N, T, n_q, n_kv, G, max_pos, shift;
+  int least, item;   // least cost of a range; cost of an item beside its blocks, in blocks of one tile
   int head_rows, tail_rows;   // whether rows before the first and behind the last sequence are this launch's
   float sl2;
 };
