@@ -4,10 +4,15 @@
 //   hold p of their weight; of these the ones with w_i >= min_p;  the first token, by index, at which the kept
 //   weights' running sum passes u times their sum
 //
-// The kept tokens are those in front of a cut (key, index) in that order, so a row needs its maximum, the cut
+// The kept tokens are those in front of a cut (key, index) in that order, so a row needs its maximum, its cuts
 // and a running sum. A cluster of CTAs holds a row in shared memory: HBM is read once. Which token a sum
 // that meets a border chooses hangs on its last bits, so weights are fixed-point numbers of 64 bits (w = 1 is
 // 2^44; relative error near 2^-29): their sums are exact, and the same in every order.
+//
+// A cut is found from counts: the logits are counted into kBins bins of equal width, and a bin's count bounds its weight
+// (that of its two edges times the count). The bins in which the bounds pass the target bracket the cut (top-k: one bin; top-p: about
+// 1 % of the weight). One pass adds the exact weights in front of the bracket and lists the logits in it; up to kList are
+// ordered by comparing all with all. Brackets of more are counted again, over their keys; equal logits are counted by index.
 #include <math.h>
 
 #include "common.cuh"
@@ -18,7 +23,11 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxChunk = 53248;   // logits of a CTA at most: 208 KB
+constexpr int kBins = 2048;        // four of a thread
+constexpr int kList = 256;
+constexpr int kRounds = 3;         // of counting; what is left then is halved key by key
 constexpr float kLeastT = 1e-30f;  // a temperature below it counts as 0
+static_assert(kBins == 4 * kThreads && 2 * kList * 8 <= kBins * 4, "shared memory");
 
 struct Params {
   const float* logits;
@@ -33,18 +42,39 @@ struct Params {
   int V, chunk, seg;   // chunk: logits of a CTA; seg: of a warp, a multiple of 32
 };
 
+using u64 = unsigned long long;
+
 __device__ __forceinline__ uint32_t key_of(float z) {
   const uint32_t b = __float_as_uint(z);
   return b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
-struct Shared {
-  unsigned long long sums[2][kMaxCluster];     // a reduction's partials, by CTA; two in turn
-  unsigned long long warp[kWarps];
-  unsigned long long seg[kWarps];              // kept weight of each warp's logits
-  unsigned long long result;
-  uint32_t table[16];                          // 2^(j/16) in 2^-30
+// What is joined over a row: a sum, a count, the smallest and the largest key.
+struct Red {
+  u64 a;
+  uint32_t n, lo, hi, pad;
 };
+struct Given {
+  float t;
+  int k;
+  float p, mp, u;
+};
+struct Shared {
+  Red red[2][kMaxCluster];   // by CTA; two in turn
+  Red warp[kWarps];
+  u64 seg[kWarps];           // kept weight of each warp's logits
+  u64 scan[2][kWarps];
+  uint32_t table[16];        // 2^(j/16) in 2^-30
+  Given given;
+  int bracket[2], count, tie;
+  uint32_t cut_key;
+  int cut_index;
+};
+// 2^(j/16) * 2^30, rounded
+__constant__ uint32_t kTable[16] = {1073741824u, 1121280436u, 1170923762u, 1222764986u, 1276901417u, 1333434672u,
+                                    1392470869u, 1454120821u, 1518500250u, 1585730000u, 1655936265u, 1729250827u,
+                                    1805811301u, 1885761398u, 1969251188u, 2056437387u};
 
 __device__ __forceinline__ uint32_t ctarank() {
   uint32_t r;
@@ -54,41 +84,65 @@ __device__ __forceinline__ uint32_t ctarank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void remote_store(const void* p, uint32_t rank, unsigned long long v) {
+__device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
   uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(r), "l"(v) : "memory");
+  return r;
+}
+__device__ __forceinline__ void remote_store(const void* p, uint32_t rank, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote(p, rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ void remote_store(const void* p, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ u64 remote_load(const u64* p, uint32_t rank) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 remote_load(const uint4* p, uint32_t rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(remote(p, rank))
+               : "memory");
+  return v;
 }
 
-struct Add {
-  __device__ unsigned long long operator()(unsigned long long a, unsigned long long b) const { return a + b; }
-};
-struct Max {
-  __device__ unsigned long long operator()(unsigned long long a, unsigned long long b) const { return a > b ? a : b; }
-};
-struct Min {
-  __device__ unsigned long long operator()(unsigned long long a, unsigned long long b) const { return a < b ? a : b; }
-};
-
-// One number of each thread joined over the CTA and, by turns in two buffers, over the cluster. Every remote
-// store is in front of a barrier of the cluster, so a CTA may leave after any of them.
-template <class Op>
-__device__ unsigned long long reduce(Shared* sh, int ctas, int& turn, unsigned long long v, Op op) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+// The Reds of a warp's lanes joined; every lane has it.
+__device__ __forceinline__ Red join(Red v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = 16; o > 0; o >>= 1) v.a += __shfl_xor_sync(0xffffffffu, v.a, o);
+  v.n = __reduce_add_sync(0xffffffffu, v.n);
+  v.lo = __reduce_min_sync(0xffffffffu, v.lo);
+  v.hi = __reduce_max_sync(0xffffffffu, v.hi);
+  return v;
+}
+__device__ __forceinline__ Red nothing() { return Red{0, 0, 0xFFFFFFFFu, 0, 0}; }
+
+// One Red of each thread joined over the CTA and, by turns in two buffers, over the cluster (whose CTAs' own stay
+// there). Every remote access is in front of a barrier of the cluster, so a CTA may leave after any of them.
+__device__ Red reduce(Shared* sh, int ctas, int& turn, Red v) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  v = join(v);
   __syncthreads();
   if (lane == 0) sh->warp[w] = v;
   __syncthreads();
-  v = sh->warp[lane % kWarps];
-#pragma unroll
-  for (int o = kWarps / 2; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  v = join(lane < kWarps ? sh->warp[lane] : nothing());
+  turn ^= 1;
   if (ctas > 1) {
-    if (int(threadIdx.x) < ctas) remote_store(&sh->sums[turn][ctarank()], threadIdx.x, v);
+    if (int(threadIdx.x) < ctas) {
+      const Red* to = &sh->red[turn][ctarank()];
+      remote_store(&to->a, threadIdx.x, v.a);
+      remote_store(&to->n, threadIdx.x, v.n);
+      remote_store(&to->lo, threadIdx.x, v.lo);
+      remote_store(&to->hi, threadIdx.x, v.hi);
+    }
     cluster_sync();
-    v = sh->sums[turn][0];
-    for (int c = 1; c < ctas; ++c) v = op(v, sh->sums[turn][c]);
-    turn ^= 1;
+    v = join(lane < ctas ? sh->red[turn][lane] : nothing());
+  } else {
+    if (threadIdx.x == 0) sh->red[turn][0] = v;
+    __syncthreads();
   }
   return v;
 }
@@ -97,7 +151,7 @@ struct Weights {
   float top, ch, cl;   // the largest logit; log2(e) / t in two parts
   const uint32_t* table;
   // 2^44 e^((z - top) / t)
-  __device__ __forceinline__ unsigned long long operator()(float z) const {
+  __device__ __forceinline__ u64 operator()(float z) const {
     const float dh = z - top, b = dh - z, dl = (z - (dh - b)) - (top + b);   // dh + dl = z - top
     const float y = dh * ch;
     if (!(y > -64.f)) return 0;
@@ -112,7 +166,7 @@ struct Weights {
     const float p = r * fmaf(r, fmaf(r, fmaf(r, 0.00961812910762848f, 0.0555041086648216f), 0.240226506959101f), 0.693147180559945f);
     const uint32_t e = table[k & 15];
     const uint32_t m = e + uint32_t(__float2int_rn(p * float(e)));
-    return (static_cast<unsigned long long>(m) << 14) >> (-(k >> 4));
+    return (static_cast<u64>(m) << 14) >> (-(k >> 4));
   }
 };
 
@@ -123,34 +177,58 @@ struct Cut {
   __device__ __forceinline__ bool keeps(uint32_t k, int i) const { return k > key || (k == key && i <= index); }
 };
 
-__global__ void __launch_bounds__(kThreads) sample_kernel(const Params P) {
-  pdl_trigger();
-  pdl_wait();
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
   extern __shared__ __align__(16) float row[];
   __shared__ Shared sh;
+  __shared__ __align__(16) uint32_t hist[kBins];   // later the list of all CTAs, and its weights
+  __shared__ __align__(16) u64 list[kList];        // (key, ~index): larger ones are in front
+  pdl_trigger();
   const int ctas = gridDim.x, rank = blockIdx.x, r = blockIdx.y;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int i0 = rank * P.chunk, n = max(0, min(P.chunk, P.V - i0));
   int turn = 0;
-  if (threadIdx.x < 16) {
-    const double x = exp2(double(threadIdx.x) / 16.0);
-    sh.table[threadIdx.x] = uint32_t(x * 1073741824.0 + 0.5);
-  }
+  if (threadIdx.x < 16) sh.table[threadIdx.x] = kTable[threadIdx.x];
   if (ctas > 1) cluster_sync();   // the others run
-  // ---- the row, its maximum, and whether it has a distribution
+  pdl_wait();
+  // ---- the row, its largest logit, and whether it has a distribution; what is given for the row, read once
+  if (rank == 0 && w == 0) {
+    Given g;
+    g.t = P.temperature ? P.temperature[r] : 1.f;
+    g.k = P.top_k ? P.top_k[r] : 0;
+    g.p = P.top_p ? P.top_p[r] : 1.f;
+    g.mp = P.min_p ? P.min_p[r] : 0.f;
+    g.u = P.u[r];
+    // one lane's, so that all CTAs have the same
+    g.t = __shfl_sync(0xffffffffu, g.t, 0);
+    g.k = __shfl_sync(0xffffffffu, g.k, 0);
+    g.p = __shfl_sync(0xffffffffu, g.p, 0);
+    g.mp = __shfl_sync(0xffffffffu, g.mp, 0);
+    g.u = __shfl_sync(0xffffffffu, g.u, 0);
+    if (ctas == 1) {
+      if (lane == 0) sh.given = g;
+    } else if (lane < ctas) {
+      remote_store(&sh.given.t, lane, __float_as_uint(g.t));
+      remote_store(&sh.given.k, lane, uint32_t(g.k));
+      remote_store(&sh.given.p, lane, __float_as_uint(g.p));
+      remote_store(&sh.given.mp, lane, __float_as_uint(g.mp));
+      remote_store(&sh.given.u, lane, __float_as_uint(g.u));
+    }
+  }
   const float* src = P.logits + int64_t(r) * P.stride + i0;
-  unsigned long long top = 0;
+  Red all = nothing();
+#pragma unroll 16
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const float z = src[i] + 0.f;   // -0 is 0
     row[i] = z;
-    const unsigned long long k = z != z ? 0xFFFFFFFFu : key_of(z);
-    top = max(top, k);
+    all.hi = max(all.hi, z != z ? 0xFFFFFFFFu : key_of(z));
+    if (z > -INFINITY) {
+      ++all.n;
+      all.lo = min(all.lo, key_of(z));
+    }
   }
-  top = reduce(&sh, ctas, turn, top, Max());
-  const float t = P.temperature ? P.temperature[r] : 1.f;
-  const int k = P.top_k ? P.top_k[r] : 0;
-  const uint32_t ktop = uint32_t(top);
-  const float ztop = __uint_as_float(ktop & 0x80000000u ? ktop ^ 0x80000000u : ~ktop);
+  all = reduce(&sh, ctas, turn, all);   // of the logits above -inf
+  const uint32_t ktop = all.hi;
+  const float ztop = of_key(ktop);
   if (!(ztop > -INFINITY && ztop < INFINITY)) {
     if (rank == 0 && threadIdx.x == 0) {
       flag(BEAM_DEV_BAD_LOGITS);
@@ -159,94 +237,262 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const Params P) {
     }
     return;
   }
+  const Given given = sh.given;
   // segments: warp w holds logits [w seg, (w + 1) seg) of the CTA
   const int a = min(n, w * P.seg), b = min(n, a + P.seg);
-  auto sum = [&](auto f) {   // over the row, of f(logit, index)
-    unsigned long long s = 0;
-    for (int i = a + lane; i < b; i += 32) s += f(row[i], i0 + i);
-    return reduce(&sh, ctas, turn, s, Add());
+  auto each = [&](auto f) {   // f(logit, index in the CTA) for the warp's, -inf behind them: by whole warps
+#pragma unroll 4
+    for (int i = a + lane; i - lane < b; i += 32) f(i < b ? row[i] : -INFINITY, i);
   };
-  if (!(t >= kLeastT) || k == 1) {
-    unsigned long long best = ~0ull;
-    for (int i = a + lane; i < b; i += 32)
-      if (row[i] == ztop) best = min(best, static_cast<unsigned long long>(i0 + i));
-    best = reduce(&sh, ctas, turn, best, Min());
+  if (!(given.t >= kLeastT) || given.k == 1) {
+    Red best = nothing();
+    each([&](float z, int i) {
+      if (z == ztop) best.lo = min(best.lo, uint32_t(i0 + i));
+    });
+    best = reduce(&sh, ctas, turn, best);
     if (rank == 0 && threadIdx.x == 0) {
-      P.token[r] = int(best);
+      P.token[r] = int(best.lo);
       if (P.logprob) P.logprob[r] = 0.f;
     }
     return;
   }
-  const double c = 1.4426950408889634 / double(t);
+  const double c = 1.4426950408889634 / double(given.t);
   const Weights weight{ztop, float(c), float(c - double(float(c))), sh.table};
 
-  // The cut behind which the sum of f over the tokens in front of it, one by one, first reaches `target`; f
-  // is a function of the logit, and only tokens in front of `in` count.
-  auto cut_at = [&](auto f, const Cut& in, unsigned long long target) {
-    uint32_t lo = in.key, hi = ktop + 1;   // the sum of keys >= lo reaches it, that of keys >= hi does not
-    while (hi - lo > 1) {
-      const uint32_t mid = lo + (hi - lo) / 2;
-      const unsigned long long s = sum([&](float z, int i) {
-        const uint32_t key = key_of(z);
-        return key >= mid && in.keeps(key, i) ? f(z) : 0ull;
-      });
-      if (s >= target) lo = mid;
-      else hi = mid;
-    }
-    const unsigned long long above = sum([&](float z, int i) {
-      const uint32_t key = key_of(z);
-      return key > lo && in.keeps(key, i) ? f(z) : 0ull;
+  // Logits counted by bin: f(logit, index) is the bin, or kBins: none.
+  auto count = [&](auto f) {
+    reinterpret_cast<uint4*>(hist)[threadIdx.x] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    each([&](float z, int i) {
+      const int x = f(z, i);
+      if (x < kBins) atomicAdd(hist + x, 1u);
     });
-    const float z = __uint_as_float(lo & 0x80000000u ? lo ^ 0x80000000u : ~lo);
-    const unsigned long long each = f(z), need = above >= target || each == 0 ? 0 : (target - above + each - 1) / each;
-    int first = -1, last = in.key == lo ? in.index : P.V - 1;   // as many of the equal ones as are needed
-    while (last - first > 1) {
-      const int mid = first + (last - first) / 2;
-      const unsigned long long s = sum([&](float z, int i) { return key_of(z) == lo && i <= mid ? 1ull : 0ull; });
-      if (s >= need) last = mid;
-      else first = mid;
+  };
+  // The first and the last bin in which the cut may lie, `target` beyond what is in front of bin 0; edges(bin, most, least): bounds of a
+  // logit's weight there.
+  auto bracket = [&](auto edges, u64 target) {
+    if (threadIdx.x < 2) sh.bracket[threadIdx.x] = kBins - 1;
+    uint4 h = make_uint4(0, 0, 0, 0);
+    if (ctas > 1) {
+      cluster_sync();
+#pragma unroll 4
+      for (int x = 0; x < ctas; ++x) {
+        const uint4 y = remote_load(reinterpret_cast<const uint4*>(hist) + threadIdx.x, x);
+        h.x += y.x; h.y += y.y; h.z += y.z; h.w += y.w;
+      }
+    } else {
+      __syncthreads();
+      h = reinterpret_cast<const uint4*>(hist)[threadIdx.x];
     }
-    return Cut{lo, last};
+    const uint32_t cnt[4] = {h.x, h.y, h.z, h.w};
+    u64 v[2][4], run[2] = {0, 0};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      u64 most = 0, least = 0;
+      if (cnt[x] != 0) edges(int(4 * threadIdx.x) + x, most, least);
+      v[0][x] = run[0] += cnt[x] * most;
+      v[1][x] = run[1] += cnt[x] * least;
+    }
+    u64 before[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      u64 s = run[y];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const u64 z = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += z;
+      }
+      if (lane == 31) sh.scan[y][w] = s;
+      before[y] = s - run[y];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      for (int x = 0; x < w; ++x) before[y] += sh.scan[y][x];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (before[y] + (x > 0 ? v[y][x - 1] : 0) < target && before[y] + v[y][x] >= target) sh.bracket[y] = 4 * threadIdx.x + x;
+    }
+    __syncthreads();
+    return make_int2(sh.bracket[0], sh.bracket[1]);
+  };
+  // Joined over the row: the sum of f in front of a bracket, and the number and keys of what lies in it, the first kList of
+  // which the CTA lists. where(logit, key): -1 in front, 0 inside, 1 behind.
+  auto gather = [&](auto f, const Cut& in, auto where) {
+    if (threadIdx.x == 0) sh.count = 0;
+    __syncthreads();
+    Red v = nothing();
+    each([&](float z, int i) {
+      const uint32_t key = key_of(z);
+      const bool valid = z > -INFINITY && in.keeps(key, i0 + i);
+      const int x = valid ? where(z, key) : 1;
+      if (x < 0) v.a += f(z);
+      const unsigned vote = __ballot_sync(0xffffffffu, x == 0);
+      if (vote != 0) {
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&sh.count, __popc(vote));
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(vote & ((1u << lane) - 1u));
+        if (x == 0) {
+          ++v.n;
+          v.lo = min(v.lo, key);
+          v.hi = max(v.hi, key);
+          if (at < kList) list[at] = u64(key) << 32 | uint32_t(~(i0 + i));
+        }
+      }
+    });
+    return reduce(&sh, ctas, turn, v);
+  };
+  // What `reduce` left of the CTAs before this one: their counts.
+  auto counted_before = [&] {
+    const uint32_t x = lane < rank ? sh.red[turn][lane].n : 0u;
+    return __reduce_add_sync(0xffffffffu, x);
+  };
+
+  // Bins of equal width from a logit down; the last has no end.
+  auto bin_of = [&](float from, float z, float scale) { return int(fminf((from - z) * scale, float(kBins - 1))); };
+  auto scale_of = [](float width) { return fminf(float(kBins - 1) / width, 1e30f); };
+  // The cut behind which the sum of f over the tokens in front of it, one by one, first reaches `target`, which the sum
+  // over all does. f is a function of the logit; only tokens in front of `in` count, and none that is `far` (a NaN: any) or farther
+  // below the largest. hist holds them by their distance from it, in bins by `scale`. edges(d0, d1, most, least): bounds of f from
+  // distance d0 to d1.
+  auto cut_at = [&](auto f, const Cut& in, u64 target, float scale, float far, auto edges) {
+    auto bins = [&](float off, u64 rest) {
+      return bracket(
+          [&](int x, u64& most, u64& least) {
+            edges(off + float(x) / scale, x == kBins - 1 ? INFINITY : off + float(x + 1) / scale, most, least);
+          },
+          rest);
+    };
+    int2 br = bins(0.f, target);
+    Red g = gather(f, in, [&](float z, uint32_t) {
+      const int x = bin_of(ztop, z, scale);
+      return x < br.x ? -1 : int(x > br.y || ztop - z >= far);
+    });
+    for (int round = 0; round < kRounds && g.n > uint32_t(kList) && g.lo < g.hi; ++round) {
+      const uint32_t lo = g.lo, hi = g.hi;
+      const float from = of_key(hi);
+      scale = scale_of(from - of_key(lo));
+      auto inside = [&](uint32_t key, int i) { return key >= lo && key <= hi && in.keeps(key, i0 + i); };
+      count([&](float z, int i) { return inside(key_of(z), i) ? bin_of(from, z, scale) : kBins; });
+      br = bins(ztop - from, target - g.a);
+      g = gather(f, in, [&](float z, uint32_t key) {
+        const int x = key > hi ? -1 : bin_of(from, z, scale);
+        return x < br.x ? -1 : int(x > br.y || key < lo);
+      });
+    }
+    if (g.n <= uint32_t(kList)) {
+      u64* q = reinterpret_cast<u64*>(hist);
+      u64* wt = q + kList;
+      const int m = int(g.n);
+      if (int(threadIdx.x) < m) {   // the CTAs' lists, end to end
+        int at = threadIdx.x, x = 0;
+        while (at >= int(sh.red[turn][x].n)) at -= int(sh.red[turn][x++].n);
+        const u64 v = ctas > 1 ? remote_load(list + at, x) : list[at];
+        q[threadIdx.x] = v;
+        wt[threadIdx.x] = f(of_key(uint32_t(v >> 32)));
+      }
+      __syncthreads();
+      if (int(threadIdx.x) < m) {
+        const u64 mine = q[threadIdx.x];
+        u64 before = g.a;
+#pragma unroll 4
+        for (int x = 0; x < m; ++x)
+          if (q[x] > mine) before += wt[x];
+        if (before < target && before + wt[threadIdx.x] >= target) {   // one
+          sh.cut_key = uint32_t(mine >> 32);
+          sh.cut_index = int(~uint32_t(mine));
+        }
+      }
+      __syncthreads();
+      return Cut{sh.cut_key, sh.cut_index};
+    }
+    // the key, by halves of what is left
+    uint32_t lo = g.lo, hi = g.hi + 1;   // the sum of keys >= lo reaches it, that of keys >= hi does not
+    u64 above = g.a;
+    while (hi - lo > 1) {
+      const uint32_t half = lo + (hi - lo) / 2;
+      Red s = nothing();
+      each([&](float z, int i) {
+        const uint32_t key = key_of(z);
+        if (i < b && key >= half && in.keeps(key, i0 + i)) s.a += f(z);
+      });
+      s = reduce(&sh, ctas, turn, s);
+      if (s.a >= target) {
+        lo = half;
+      } else {
+        hi = half;
+        above = s.a;
+      }
+    }
+    // as many of the equal ones as are needed, by index
+    const u64 one = f(of_key(lo)), need = one == 0 ? ~0ull : (target - above + one - 1) / one;
+    auto equal = [&](float z, int i) { return i < b && key_of(z) == lo && in.keeps(lo, i0 + i); };
+    Red s = nothing();
+    each([&](float z, int i) { s.n += equal(z, i); });
+    const uint32_t warps = __reduce_add_sync(0xffffffffu, s.n);
+    s = reduce(&sh, ctas, turn, s);
+    if (lane == 0) sh.seg[w] = warps;
+    u64 before = counted_before();
+    __syncthreads();
+    for (int x = 0; x < w; ++x) before += sh.seg[x];
+    Red at = nothing();
+    if (before < need && before + warps >= need)
+      each([&](float z, int i) {
+        const unsigned vote = __ballot_sync(0xffffffffu, equal(z, i));
+        if (equal(z, i) && before + __popc(vote & ((2u << lane) - 1u)) == need) at.hi = uint32_t(i0 + i) + 1;
+        before += __popc(vote);
+      });
+    at = reduce(&sh, ctas, turn, at);
+    return Cut{lo, at.hi == 0 ? P.V : int(at.hi) - 1};
   };
 
   Cut cut{0, P.V};   // all
-  if (k > 0 && k < P.V) cut = cut_at([](float) { return 1ull; }, cut, k);
-  const float p = P.top_p ? P.top_p[r] : 1.f;
-  if (!(p >= 1.f)) {
-    const unsigned long long all = sum([&](float z, int i) { return cut.keeps(key_of(z), i) ? weight(z) : 0ull; });
-    const double want = ceil(double(all) * double(fmaxf(p, 0.f)));
-    cut = cut_at(weight, cut, max(1ull, static_cast<unsigned long long>(want)));
+  const float zlow = of_key(all.lo);
+  if (given.k > 0 && uint32_t(given.k) < all.n) {   // logits of -inf weigh nothing
+    const float scale = scale_of(ztop - zlow);
+    count([&](float z, int) { return z > -INFINITY ? bin_of(ztop, z, scale) : kBins; });
+    cut = cut_at([](float) { return u64(1); }, cut, u64(given.k), scale, NAN,
+                 [](float, float, u64& most, u64& least) { most = least = 1; });
   }
-  const float mp = P.min_p ? P.min_p[r] : 0.f;
-  if (mp > 0.f) {
-    const double least = fmin(double(ztop), double(ztop) + double(t) * log(double(mp)));
+  if (!(given.p >= 1.f)) {
+    // below the largest by 32 t a weight is less than 2^-46 and so nothing
+    const float far = 32.f * given.t, cf = float(c);
+    const float scale = scale_of(fminf(ztop - (cut.key == 0 ? zlow : of_key(cut.key)), far));
+    Red v = nothing();
+    count([&](float z, int i) {
+      const u64 x = cut.keeps(key_of(z), i0 + i) ? weight(z) : 0;
+      v.a += x;
+      return x != 0 ? bin_of(ztop, z, scale) : kBins;
+    });
+    v = reduce(&sh, ctas, turn, v);
+    const u64 want = u64(ceil(double(v.a) * double(fmaxf(given.p, 0.f))));
+    cut = cut_at(weight, cut, max(u64(1), want), scale, far, [&](float d0, float d1, u64& most, u64& least) {
+      // the errors of y and of the function are below 2^-14 of the weight, that of its fixed point is one step
+      most = u64(fminf(exp2f(-d0 * cf) * (1.f + 0x1p-13f), 1.f) * 0x1p44f) + 1;
+      least = u64(fmaxf(exp2f(-d1 * cf) * (1.f - 0x1p-13f) * 0x1p44f - 1.f, 0.f));
+    });
+  }
+  if (given.mp > 0.f) {
+    const double least = fmin(double(ztop), double(ztop) + double(given.t) * log(double(given.mp)));
     float f = float(least);   // the smallest logit that is not below it
     if (double(f) < least) f = nextafterf(f, INFINITY);
     const uint32_t key = key_of(f + 0.f) - 1;
     if (key >= cut.key) cut = Cut{key, -1};
   }
   // ---- the kept weights' sums, and the token at which they pass u times their total
-  unsigned long long mine = 0;
-  for (int i = a + lane; i < b; i += 32)
-    if (cut.keeps(key_of(row[i]), i0 + i)) mine += weight(row[i]);
+  Red mine = nothing();
+  each([&](float z, int i) {
+    if (i < b && cut.keeps(key_of(z), i0 + i)) mine.a += weight(z);
+  });
+  u64 warps = mine.a;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sh.seg[w] = mine;
-  __syncthreads();
-  unsigned long long cta = 0;
-  for (int x = 0; x < kWarps; ++x) cta += sh.seg[x];
-  unsigned long long before = 0, total = cta;
-  if (ctas > 1) {
-    if (int(threadIdx.x) < ctas) remote_store(&sh.sums[turn][rank], threadIdx.x, cta);
-    cluster_sync();
-    total = 0;
-    for (int x = 0; x < ctas; ++x) {
-      if (x < rank) before += sh.sums[turn][x];
-      total += sh.sums[turn][x];
-    }
-  }
-  const float uu = P.u[r];
-  unsigned long long target = uu > 0.f ? static_cast<unsigned long long>(double(uu) * double(total)) : 0;
+  for (int o = 16; o > 0; o >>= 1) warps += __shfl_xor_sync(0xffffffffu, warps, o);
+  if (lane == 0) sh.seg[w] = warps;
+  mine = reduce(&sh, ctas, turn, mine);
+  const u64 total = mine.a, cta = sh.red[turn][rank].a;
+  u64 before = 0;
+  for (int x = 0; x < rank; ++x) before += sh.red[turn][x].a;
+  u64 target = given.u > 0.f ? u64(double(given.u) * double(total)) : 0;
   target = min(target, total - 1);
   if (target < before || target >= before + cta) return;
   target -= before;
@@ -256,20 +502,20 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const Params P) {
   const int s0 = min(n, x * P.seg), s1 = min(n, s0 + P.seg);
   for (int base = s0; base < s1; base += kThreads) {
     const int i = base + threadIdx.x;
-    const unsigned long long v = i < s1 && cut.keeps(key_of(row[i]), i0 + i) ? weight(row[i]) : 0;
-    unsigned long long run = v;
+    const u64 v = i < s1 && cut.keeps(key_of(row[i]), i0 + i) ? weight(row[i]) : 0;
+    u64 run = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long y = __shfl_up_sync(0xffffffffu, run, o);
+      const u64 y = __shfl_up_sync(0xffffffffu, run, o);
       if (lane >= o) run += y;
     }
     __syncthreads();
-    if (lane == 31) sh.warp[w] = run;
+    if (lane == 31) sh.scan[0][w] = run;
     __syncthreads();
-    unsigned long long all = 0;
+    u64 sums = 0;
     for (int y = 0; y < kWarps; ++y) {
-      if (y < w) run += sh.warp[y];
-      all += sh.warp[y];
+      if (y < w) run += sh.scan[0][y];
+      sums += sh.scan[0][y];
     }
     if (run > target && run - v <= target) {
       P.token[r] = i0 + i;
@@ -277,8 +523,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const Params P) {
       if (P.logprob)
         P.logprob[r] = float(v > total / 2 ? log1p(-double(total - v) / double(total)) : log(double(v) / double(total)));
     }
-    if (target < all) break;
-    target -= all;
+    if (target < sums) break;
+    target -= sums;
   }
 }
 
