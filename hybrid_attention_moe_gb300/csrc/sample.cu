@@ -27,7 +27,7 @@ constexpr int kBins = 2048;        // four of a thread
 constexpr int kList = 256;
 constexpr int kRounds = 3;         // of counting; what is left then is halved key by key
 constexpr float kLeastT = 1e-30f;  // a temperature below it counts as 0
-static_assert(kBins == 4 * kThreads && 2 * kList * 8 <= kBins * 4, "shared memory");
+static_assert(kWarps == kMaxCluster && kBins == 4 * kThreads && 2 * kList * 8 <= kBins * 4, "shared memory");
 
 struct Params {
   const float* logits;
@@ -39,7 +39,7 @@ struct Params {
   int32_t* token;
   float* logprob;
   int64_t stride;
-  int V, chunk, seg;   // chunk: logits of a CTA; seg: of a warp, a multiple of 32
+  int V, chunk, seg;   // chunk: logits of a CTA; seg: of a warp, a multiple of 128
 };
 
 using u64 = unsigned long long;
@@ -63,7 +63,9 @@ struct Given {
 struct Shared {
   Red red[2][kMaxCluster];   // by CTA; two in turn
   Red warp[kWarps];
-  u64 seg[kWarps];           // kept weight of each warp's logits
+  u64 seg[kWarps];           // equal logits of each warp's
+  u64 more[2][kMaxCluster];  // weights to add to those that reduce left: by CTA, and by the CTA's warps
+  u64 total;
   u64 scan[2][kWarps];
   uint32_t table[16];        // 2^(j/16) in 2^-30
   Given given;
@@ -121,7 +123,7 @@ __device__ __forceinline__ Red join(Red v) {
 __device__ __forceinline__ Red nothing() { return Red{0, 0, 0xFFFFFFFFu, 0, 0}; }
 
 // One Red of each thread joined over the CTA and, by turns in two buffers, over the cluster (whose CTAs' own stay
-// there). Every remote access is in front of a barrier of the cluster, so a CTA may leave after any of them.
+// there, and the CTA's warps' in sh->warp). Every remote access is in front of a barrier of the cluster, so a CTA may leave after any of them.
 __device__ Red reduce(Shared* sh, int ctas, int& turn, Red v) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   v = join(v);
@@ -215,6 +217,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
     }
   }
   const float* src = P.logits + int64_t(r) * P.stride + i0;
+  const int n4 = (n + 3) & ~3;
+  if (n + int(threadIdx.x) < n4) row[n + threadIdx.x] = -INFINITY;
   Red all = nothing();
 #pragma unroll 16
   for (int i = threadIdx.x; i < n; i += kThreads) {
@@ -226,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
       all.lo = min(all.lo, key_of(z));
     }
   }
+  const uint32_t best_of_mine = all.hi;
   all = reduce(&sh, ctas, turn, all);   // of the logits above -inf
   const uint32_t ktop = all.hi;
   const float ztop = of_key(ktop);
@@ -239,10 +244,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
   }
   const Given given = sh.given;
   // segments: warp w holds logits [w seg, (w + 1) seg) of the CTA
-  const int a = min(n, w * P.seg), b = min(n, a + P.seg);
-  auto each = [&](auto f) {   // f(logit, index in the CTA) for the warp's, -inf behind them: by whole warps
-#pragma unroll 4
-    for (int i = a + lane; i - lane < b; i += 32) f(i < b ? row[i] : -INFINITY, i);
+  const int a = min(n4, w * P.seg), b = min(n4, a + P.seg);
+  auto each = [&](auto f) {   // f(logit, index in the CTA) for the warp's, and -inf behind them: by whole warps
+#pragma unroll 2
+    for (int i = a + 4 * lane; i - 4 * lane < b; i += 128) {
+      float4 z = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (i < b) z = *reinterpret_cast<const float4*>(row + i);
+      f(z.x, i);
+      f(z.y, i + 1);
+      f(z.z, i + 2);
+      f(z.w, i + 3);
+    }
   };
   if (!(given.t >= kLeastT) || given.k == 1) {
     Red best = nothing();
@@ -351,46 +363,46 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
   // Bins of equal width from a logit down; the last has no end.
   auto bin_of = [&](float from, float z, float scale) { return int(fminf((from - z) * scale, float(kBins - 1))); };
   auto scale_of = [](float width) { return fminf(float(kBins - 1) / width, 1e30f); };
+  // What `gather` found of the row, in q, with f of it in wt.
+  u64* q = reinterpret_cast<u64*>(hist);
+  u64* wt = q + kList;
+  auto fetch = [&](auto f, int m) {
+    if (int(threadIdx.x) < m) {   // the CTAs' lists, end to end
+      int at = threadIdx.x, x = 0;
+      while (at >= int(sh.red[turn][x].n)) at -= int(sh.red[turn][x++].n);
+      const u64 v = ctas > 1 ? remote_load(list + at, x) : list[at];
+      q[threadIdx.x] = v;
+      wt[threadIdx.x] = f(of_key(uint32_t(v >> 32)));
+    }
+  };
   // The cut behind which the sum of f over the tokens in front of it, one by one, first reaches `target`, which the sum
-  // over all does. f is a function of the logit; only tokens in front of `in` count, and none that is `far` (a NaN: any) or farther
-  // below the largest. hist holds them by their distance from it, in bins by `scale`. edges(d0, d1, most, least): bounds of f from
-  // distance d0 to d1.
-  auto cut_at = [&](auto f, const Cut& in, u64 target, float scale, float far, auto edges) {
-    auto bins = [&](float off, u64 rest) {
-      return bracket(
-          [&](int x, u64& most, u64& least) {
-            edges(off + float(x) / scale, x == kBins - 1 ? INFINITY : off + float(x + 1) / scale, most, least);
-          },
-          rest);
-    };
-    int2 br = bins(0.f, target);
-    Red g = gather(f, in, [&](float z, uint32_t) {
-      const int x = bin_of(ztop, z, scale);
-      return x < br.x ? -1 : int(x > br.y || ztop - z >= far);
-    });
+  // over all does. f is a function of the logit; only tokens in front of `in` count. g: what `gather` found of a
+  // bracket. edges(d0, d1, most, least): bounds of f from distance d0 below the largest to d1. `known`: whether the sums
+  // of f that `reduce` left, with sh.more, are those of the tokens in front of the cut, each CTA's and each warp's.
+  bool known = false;
+  auto bins = [&](auto edges, float off, float scale, u64 target) {
+    return bracket(
+        [&](int x, u64& most, u64& least) {
+          edges(off + float(x) / scale, x == kBins - 1 ? INFINITY : off + float(x + 1) / scale, most, least);
+        },
+        target);
+  };
+  auto cut_at = [&](auto f, const Cut& in, u64 target, Red g, auto edges) {
     for (int round = 0; round < kRounds && g.n > uint32_t(kList) && g.lo < g.hi; ++round) {
       const uint32_t lo = g.lo, hi = g.hi;
-      const float from = of_key(hi);
-      scale = scale_of(from - of_key(lo));
+      const float from = of_key(hi), scale = scale_of(from - of_key(lo));
       auto inside = [&](uint32_t key, int i) { return key >= lo && key <= hi && in.keeps(key, i0 + i); };
       count([&](float z, int i) { return inside(key_of(z), i) ? bin_of(from, z, scale) : kBins; });
-      br = bins(ztop - from, target - g.a);
+      const int2 br = bins(edges, ztop - from, scale, target - g.a);
       g = gather(f, in, [&](float z, uint32_t key) {
         const int x = key > hi ? -1 : bin_of(from, z, scale);
         return x < br.x ? -1 : int(x > br.y || key < lo);
       });
     }
     if (g.n <= uint32_t(kList)) {
-      u64* q = reinterpret_cast<u64*>(hist);
-      u64* wt = q + kList;
       const int m = int(g.n);
-      if (int(threadIdx.x) < m) {   // the CTAs' lists, end to end
-        int at = threadIdx.x, x = 0;
-        while (at >= int(sh.red[turn][x].n)) at -= int(sh.red[turn][x++].n);
-        const u64 v = ctas > 1 ? remote_load(list + at, x) : list[at];
-        q[threadIdx.x] = v;
-        wt[threadIdx.x] = f(of_key(uint32_t(v >> 32)));
-      }
+      fetch(f, m);
+      if (threadIdx.x < 2 * kMaxCluster) sh.more[threadIdx.x / kMaxCluster][threadIdx.x % kMaxCluster] = 0;
       __syncthreads();
       if (int(threadIdx.x) < m) {
         const u64 mine = q[threadIdx.x];
@@ -398,12 +410,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
 #pragma unroll 4
         for (int x = 0; x < m; ++x)
           if (q[x] > mine) before += wt[x];
-        if (before < target && before + wt[threadIdx.x] >= target) {   // one
-          sh.cut_key = uint32_t(mine >> 32);
-          sh.cut_index = int(~uint32_t(mine));
+        if (before < target) {
+          const int i = int(~uint32_t(mine)), x = i / P.chunk;
+          atomicAdd(&sh.more[0][x], wt[threadIdx.x]);
+          if (x == rank) atomicAdd(&sh.more[1][(i - i0) / P.seg], wt[threadIdx.x]);
+          if (before + wt[threadIdx.x] >= target) {   // one
+            sh.cut_key = uint32_t(mine >> 32);
+            sh.cut_index = i;
+          }
         }
       }
       __syncthreads();
+      known = true;
       return Cut{sh.cut_key, sh.cut_index};
     }
     // the key, by halves of what is left
@@ -414,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
       Red s = nothing();
       each([&](float z, int i) {
         const uint32_t key = key_of(z);
-        if (i < b && key >= half && in.keeps(key, i0 + i)) s.a += f(z);
+        if (key >= half && in.keeps(key, i0 + i)) s.a += f(z);
       });
       s = reduce(&sh, ctas, turn, s);
       if (s.a >= target) {
@@ -426,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
     }
     // as many of the equal ones as are needed, by index
     const u64 one = f(of_key(lo)), need = one == 0 ? ~0ull : (target - above + one - 1) / one;
-    auto equal = [&](float z, int i) { return i < b && key_of(z) == lo && in.keeps(lo, i0 + i); };
+    auto equal = [&](float z, int i) { return key_of(z) == lo && in.keeps(lo, i0 + i); };
     Red s = nothing();
     each([&](float z, int i) { s.n += equal(z, i); });
     const uint32_t warps = __reduce_add_sync(0xffffffffu, s.n);
@@ -437,22 +455,83 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
     for (int x = 0; x < w; ++x) before += sh.seg[x];
     Red at = nothing();
     if (before < need && before + warps >= need)
-      each([&](float z, int i) {
-        const unsigned vote = __ballot_sync(0xffffffffu, equal(z, i));
-        if (equal(z, i) && before + __popc(vote & ((2u << lane) - 1u)) == need) at.hi = uint32_t(i0 + i) + 1;
+      for (int i = a + lane; i - lane < b; i += 32) {
+        const bool hit = i < b && equal(row[i], i);
+        const unsigned vote = __ballot_sync(0xffffffffu, hit);
+        if (hit && before + __popc(vote & ((2u << lane) - 1u)) == need) at.hi = uint32_t(i0 + i) + 1;
         before += __popc(vote);
-      });
+      }
     at = reduce(&sh, ctas, turn, at);
     return Cut{lo, at.hi == 0 ? P.V : int(at.hi) - 1};
   };
 
+  // Key that min-p's kept ones are above.
+  auto least_key = [&] {
+    const double least = fmin(double(ztop), double(ztop) + double(given.t) * log(double(given.mp)));
+    float f = float(least);   // the smallest logit that is not below it
+    if (double(f) < least) f = nextafterf(f, INFINITY);
+    return key_of(f + 0.f) - 1;
+  };
+  auto wanted = [&](u64 sum) { return max(u64(1), u64(ceil(double(sum) * double(fmaxf(given.p, 0.f))))); };
+  auto target_of = [&](u64 total) { return min(given.u > 0.f ? u64(double(given.u) * double(total)) : 0, total - 1); };
+  auto put = [&](int i, u64 v, u64 total) {
+    P.token[r] = i;
+    // near 1 by what is missing, which FP32 then holds to its last bits
+    if (P.logprob)
+      P.logprob[r] = float(v > total / 2 ? log1p(-double(total - v) / double(total)) : log(double(v) / double(total)));
+  };
   Cut cut{0, P.V};   // all
   const float zlow = of_key(all.lo);
   if (given.k > 0 && uint32_t(given.k) < all.n) {   // logits of -inf weigh nothing
-    const float scale = scale_of(ztop - zlow);
-    count([&](float z, int) { return z > -INFINITY ? bin_of(ztop, z, scale) : kBins; });
-    cut = cut_at([](float) { return u64(1); }, cut, u64(given.k), scale, NAN,
-                 [](float, float, u64& most, u64& least) { most = least = 1; });
+    // The k-th of the threads' largest logits is not above the row's k-th: those that are not below its bin hold the
+    // kept ones, and are few more
+    const float scale = scale_of(ztop - zlow), best = of_key(best_of_mine);
+    reinterpret_cast<uint4*>(hist)[threadIdx.x] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    if (best_of_mine != 0 && best > -INFINITY) atomicAdd(hist + bin_of(ztop, best, scale), 1u);
+    auto one = [](float) { return u64(1); };
+    auto ones = [](float, float, u64& most, u64& least) { most = least = 1; };
+    const int last = bins(ones, 0.f, scale, u64(given.k)).y;
+    const Red g = gather(one, cut, [&](float z, uint32_t) { return int(bin_of(ztop, z, scale) > last); });
+    if (g.n <= uint32_t(kList)) {
+      // All that can be kept is in the list: the row's first CTA does the rest there.
+      const int m = int(g.n), at = threadIdx.x;
+      if (rank == 0) fetch(weight, m);
+      if (ctas > 1) cluster_sync();   // the others' lists were read
+      if (rank != 0) return;
+      __syncthreads();
+      const u64 mine = at < m ? q[at] : 0, v = at < m ? wt[at] : 0;
+      u64 before = 0;
+      int place = 0;
+      if (at < m) {
+#pragma unroll 4
+        for (int x = 0; x < m; ++x)
+          if (q[x] > mine) {
+            before += wt[x];
+            ++place;
+          }
+        if (place == given.k - 1) sh.total = before + v;
+      }
+      __syncthreads();
+      bool keep = at < m && place < given.k;
+      if (!(given.p >= 1.f)) keep = keep && before < wanted(sh.total);
+      if (given.mp > 0.f) keep = keep && uint32_t(mine >> 32) > least_key();
+      if (at < m) wt[at] = keep ? v : 0;
+      __syncthreads();
+      if (keep) {
+        u64 total = 0, run = 0;   // of all, and of those of lower indices: the list holds their complements
+#pragma unroll 4
+        for (int x = 0; x < m; ++x) {
+          total += wt[x];
+          if (uint32_t(q[x]) > uint32_t(mine)) run += wt[x];
+        }
+        const u64 target = target_of(total);
+        if (run <= target && target < run + v) put(int(~uint32_t(mine)), v, total);
+      }
+      return;
+    }
+    cut = cut_at(one, cut, u64(given.k), g, ones);
+    known = false;
   }
   if (!(given.p >= 1.f)) {
     // below the largest by 32 t a weight is less than 2^-46 and so nothing
@@ -464,40 +543,49 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
       v.a += x;
       return x != 0 ? bin_of(ztop, z, scale) : kBins;
     });
-    v = reduce(&sh, ctas, turn, v);
-    const u64 want = u64(ceil(double(v.a) * double(fmaxf(given.p, 0.f))));
-    cut = cut_at(weight, cut, max(u64(1), want), scale, far, [&](float d0, float d1, u64& most, u64& least) {
+    const u64 want = wanted(reduce(&sh, ctas, turn, v).a);
+    auto edges = [&](float d0, float d1, u64& most, u64& least) {
       // the errors of y and of the function are below 2^-14 of the weight, that of its fixed point is one step
       most = u64(fminf(exp2f(-d0 * cf) * (1.f + 0x1p-13f), 1.f) * 0x1p44f) + 1;
       least = u64(fmaxf(exp2f(-d1 * cf) * (1.f - 0x1p-13f) * 0x1p44f - 1.f, 0.f));
+    };
+    const int2 br = bins(edges, 0.f, scale, want);
+    const Red g = gather(weight, cut, [&](float z, uint32_t) {
+      const int x = bin_of(ztop, z, scale);
+      return x < br.x ? -1 : int(x > br.y || ztop - z >= far);
     });
+    cut = cut_at(weight, cut, want, g, edges);
   }
   if (given.mp > 0.f) {
-    const double least = fmin(double(ztop), double(ztop) + double(given.t) * log(double(given.mp)));
-    float f = float(least);   // the smallest logit that is not below it
-    if (double(f) < least) f = nextafterf(f, INFINITY);
-    const uint32_t key = key_of(f + 0.f) - 1;
-    if (key >= cut.key) cut = Cut{key, -1};
+    const uint32_t key = least_key();
+    if (key >= cut.key) {
+      cut = Cut{key, -1};
+      known = false;
+    }
   }
   // ---- the kept weights' sums, and the token at which they pass u times their total
-  Red mine = nothing();
-  each([&](float z, int i) {
-    if (i < b && cut.keeps(key_of(z), i0 + i)) mine.a += weight(z);
-  });
-  u64 warps = mine.a;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) warps += __shfl_xor_sync(0xffffffffu, warps, o);
-  if (lane == 0) sh.seg[w] = warps;
-  mine = reduce(&sh, ctas, turn, mine);
-  const u64 total = mine.a, cta = sh.red[turn][rank].a;
-  u64 before = 0;
-  for (int x = 0; x < rank; ++x) before += sh.red[turn][x].a;
-  u64 target = given.u > 0.f ? u64(double(given.u) * double(total)) : 0;
-  target = min(target, total - 1);
+  if (!known) {
+    if (threadIdx.x < 2 * kMaxCluster) sh.more[threadIdx.x / kMaxCluster][threadIdx.x % kMaxCluster] = 0;
+    Red mine = nothing();
+    each([&](float z, int i) {
+      if (cut.keeps(key_of(z), i0 + i)) mine.a += weight(z);
+    });
+    reduce(&sh, ctas, turn, mine);
+  } else if (ctas > 1) {
+    cluster_sync();   // the others have read this CTA's list
+  }
+  u64 before = 0, total = 0;
+  for (int x = 0; x < ctas; ++x) {
+    if (x == rank) before = total;
+    total += sh.red[turn][x].a + sh.more[0][x];
+  }
+  const u64 cta = sh.red[turn][rank].a + sh.more[0][rank];
+  u64 target = target_of(total);
   if (target < before || target >= before + cta) return;
   target -= before;
+  auto seg = [&](int x) { return sh.warp[x].a + sh.more[1][x]; };
   int x = 0;
-  while (target >= sh.seg[x]) target -= sh.seg[x++];
+  while (target >= seg(x)) target -= seg(x++);
   // the CTA's warps share the segment
   const int s0 = min(n, x * P.seg), s1 = min(n, s0 + P.seg);
   for (int base = s0; base < s1; base += kThreads) {
@@ -517,12 +605,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
       if (y < w) run += sh.scan[0][y];
       sums += sh.scan[0][y];
     }
-    if (run > target && run - v <= target) {
-      P.token[r] = i0 + i;
-      // near 1 by what is missing, which FP32 then holds to its last bits
-      if (P.logprob)
-        P.logprob[r] = float(v > total / 2 ? log1p(-double(total - v) / double(total)) : log(double(v) / double(total)));
-    }
+    if (run > target && run - v <= target) put(i0 + i, v, total);
     if (target < sums) break;
     target -= sums;
   }
@@ -544,7 +627,7 @@ extern "C" beam_status beam_sample(const float* logits, int64_t row_stride, int 
   while (ctas < kMaxCluster && int64_t(T) * ctas * 2 <= num_sms_cached() && V / ctas > 4096) ctas *= 2;
   Params p{logits, u, temperature, top_k, top_p, min_p, token, logprob, row_stride, V, 0, 0};
   p.chunk = ((V + ctas - 1) / ctas + 3) / 4 * 4;
-  p.seg = ((p.chunk + kWarps - 1) / kWarps + 31) / 32 * 32;
+  p.seg = ((p.chunk + kWarps - 1) / kWarps + 127) / 128 * 128;
   const size_t smem = size_t(p.chunk) * 4;
   cudaError_t e = cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxChunk * 4);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
