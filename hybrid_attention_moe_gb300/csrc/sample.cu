@@ -23,11 +23,11 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxChunk = 53248;   // logits of a CTA at most: 208 KB
-constexpr int kBins = 2048;        // four of a thread
+constexpr int kBins = 512;         // one of a thread
 constexpr int kList = 256;
 constexpr int kRounds = 3;         // of counting; what is left then is halved key by key
 constexpr float kLeastT = 1e-30f;  // a temperature below it counts as 0
-static_assert(kWarps == kMaxCluster && kBins == 4 * kThreads && 2 * kList * 8 <= kBins * 4, "shared memory");
+static_assert(kWarps == kMaxCluster && kBins == kThreads, "by thread");
 
 struct Params {
   const float* logits;
@@ -102,12 +102,9 @@ __device__ __forceinline__ u64 remote_load(const u64* p, uint32_t rank) {
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote(p, rank)) : "memory");
   return v;
 }
-__device__ __forceinline__ uint4 remote_load(const uint4* p, uint32_t rank) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(remote(p, rank))
-               : "memory");
+__device__ __forceinline__ uint32_t remote_load(const uint32_t* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote(p, rank)) : "memory");
   return v;
 }
 
@@ -155,11 +152,11 @@ struct Weights {
   // 2^44 e^((z - top) / t)
   __device__ __forceinline__ u64 operator()(float z) const {
     const float dh = z - top, b = dh - z, dl = (z - (dh - b)) - (top + b);   // dh + dl = z - top
-    const float y = dh * ch;
-    if (!(y > -64.f)) return 0;
+    float y = dh * ch;
     float lo = fmaf(dh, ch, -y);   // y + lo = (z - top) log2(e) / t
     lo = fmaf(dh, cl, lo);
     lo = fmaf(dl, ch, lo);
+    y = fmaxf(y, -60.f);   // what is below shifts out, whatever lo is; no branch, so that several are under way
     // y = k / 16 + r, 2^r = 1 + r ln 2 + ... (|r| <= 1/32: the fifth term is below 2^-34)
     constexpr float kRound = 12582912.f;
     const float t = fmaf(y, 16.f, kRound);
@@ -172,6 +169,27 @@ struct Weights {
   }
 };
 
+// s f of f < 1, rounded up or down; 0 of f <= 0 and of NaN.
+__device__ __forceinline__ u64 times(u64 s, float f, bool up) {
+  if (!(f > 0.f)) return 0;
+  const uint32_t b = __float_as_uint(f), e = b >> 23;
+  const u64 m = (b & 0x7FFFFFu) | (e != 0 ? 0x800000u : 0u);
+  const int shift = 150 - int(max(e, 1u));   // f = m 2^-shift, shift >= 24
+  const u64 lo = s * m, hi = __umul64hi(s, m);   // of 88 bits
+  u64 x, rest;
+  if (shift >= 88) {
+    x = 0;
+    rest = lo | hi;
+  } else if (shift >= 64) {
+    x = hi >> (shift - 64);
+    rest = lo | (hi & ((u64(1) << (shift - 64)) - 1));
+  } else {
+    x = hi << (64 - shift) | lo >> shift;
+    rest = lo & ((u64(1) << shift) - 1);
+  }
+  return x + (up && rest != 0);
+}
+
 // Tokens in front of a cut: larger keys, and equal ones up to an index.
 struct Cut {
   uint32_t key;
@@ -182,8 +200,9 @@ struct Cut {
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
   extern __shared__ __align__(16) float row[];
   __shared__ Shared sh;
-  __shared__ __align__(16) uint32_t hist[kBins];   // later the list of all CTAs, and its weights
-  __shared__ __align__(16) u64 list[kList];        // (key, ~index): larger ones are in front
+  __shared__ uint32_t hist[kBins];
+  __shared__ u64 list[kList];             // the CTA's (key, ~index): larger ones are in front
+  __shared__ u64 q[kList], wt[kList];     // the row's, and f of them
   pdl_trigger();
   const int ctas = gridDim.x, rank = blockIdx.x, r = blockIdx.y;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -220,16 +239,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
   const int n4 = (n + 3) & ~3;
   if (n + int(threadIdx.x) < n4) row[n + threadIdx.x] = -INFINITY;
   Red all = nothing();
-#pragma unroll 16
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const float z = src[i] + 0.f;   // -0 is 0
-    row[i] = z;
+  auto take = [&](float x) {
+    const float z = x + 0.f;   // -0 is 0
     all.hi = max(all.hi, z != z ? 0xFFFFFFFFu : key_of(z));
-    if (z > -INFINITY) {
-      ++all.n;
-      all.lo = min(all.lo, key_of(z));
-    }
+    all.n += z > -INFINITY;
+    all.lo = min(all.lo, z > -INFINITY ? key_of(z) : 0xFFFFFFFFu);
+    return z;
+  };
+  const bool wide = (reinterpret_cast<uintptr_t>(src) & 15) == 0;   // rows of an odd stride begin anywhere
+  const int n16 = wide ? n & ~3 : 0;
+#pragma unroll 8
+  for (int i = 4 * threadIdx.x; i < n16; i += 4 * kThreads) {
+    const float4 z = __ldcs(reinterpret_cast<const float4*>(src + i));
+    *reinterpret_cast<float4*>(row + i) = make_float4(take(z.x), take(z.y), take(z.z), take(z.w));
   }
+#pragma unroll 16
+  for (int i = n16 + threadIdx.x; i < n; i += kThreads) row[i] = take(__ldcs(src + i));
   const uint32_t best_of_mine = all.hi;
   all = reduce(&sh, ctas, turn, all);   // of the logits above -inf
   const uint32_t ktop = all.hi;
@@ -245,16 +270,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
   const Given given = sh.given;
   // segments: warp w holds logits [w seg, (w + 1) seg) of the CTA
   const int a = min(n4, w * P.seg), b = min(n4, a + P.seg);
-  auto each = [&](auto f) {   // f(logit, index in the CTA) for the warp's, and -inf behind them: by whole warps
+  auto fours = [&](auto f) {   // f(four logits, first index in the CTA) for the warp's, and -inf behind them: by whole warps
 #pragma unroll 2
     for (int i = a + 4 * lane; i - 4 * lane < b; i += 128) {
       float4 z = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
       if (i < b) z = *reinterpret_cast<const float4*>(row + i);
-      f(z.x, i);
-      f(z.y, i + 1);
-      f(z.z, i + 2);
-      f(z.w, i + 3);
+      const float y[4] = {z.x, z.y, z.z, z.w};
+      f(y, i);
     }
+  };
+  auto each = [&](auto f) {   // f(logit, index in the CTA)
+    fours([&](const float (&z)[4], int i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f(z[e], i + e);
+    });
   };
   if (!(given.t >= kLeastT) || given.k == 1) {
     Red best = nothing();
@@ -268,12 +297,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
     }
     return;
   }
-  const double c = 1.4426950408889634 / double(given.t);
-  const Weights weight{ztop, float(c), float(c - double(float(c))), sh.table};
+  // log2(e) / t as a sum of two: the quotient's remainder is exact (FP64 divisions of all threads took 3 us)
+  constexpr float kL = 1.44269502162933349609375f, kLrest = 1.92596299112661746887e-8f;
+  const float ch = kL / given.t;
+  const Weights weight{ztop, ch, (fmaf(-ch, given.t, kL) + kLrest) / given.t, sh.table};
 
   // Logits counted by bin: f(logit, index) is the bin, or kBins: none.
   auto count = [&](auto f) {
-    reinterpret_cast<uint4*>(hist)[threadIdx.x] = make_uint4(0, 0, 0, 0);
+    hist[threadIdx.x] = 0;
     __syncthreads();
     each([&](float z, int i) {
       const int x = f(z, i);
@@ -284,26 +315,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
   // logit's weight there.
   auto bracket = [&](auto edges, u64 target) {
     if (threadIdx.x < 2) sh.bracket[threadIdx.x] = kBins - 1;
-    uint4 h = make_uint4(0, 0, 0, 0);
+    uint32_t h = 0;
     if (ctas > 1) {
       cluster_sync();
-#pragma unroll 4
-      for (int x = 0; x < ctas; ++x) {
-        const uint4 y = remote_load(reinterpret_cast<const uint4*>(hist) + threadIdx.x, x);
-        h.x += y.x; h.y += y.y; h.z += y.z; h.w += y.w;
-      }
+#pragma unroll 8
+      for (int x = 0; x < ctas; ++x) h += remote_load(hist + threadIdx.x, x);
     } else {
       __syncthreads();
-      h = reinterpret_cast<const uint4*>(hist)[threadIdx.x];
+      h = hist[threadIdx.x];
     }
-    const uint32_t cnt[4] = {h.x, h.y, h.z, h.w};
-    u64 v[2][4], run[2] = {0, 0};
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      u64 most = 0, least = 0;
-      if (cnt[x] != 0) edges(int(4 * threadIdx.x) + x, most, least);
-      v[0][x] = run[0] += cnt[x] * most;
-      v[1][x] = run[1] += cnt[x] * least;
+    u64 run[2] = {0, 0};
+    if (h != 0) {
+      edges(int(threadIdx.x), run[0], run[1]);
+      run[0] *= h;
+      run[1] *= h;
     }
     u64 before[2];
 #pragma unroll
@@ -321,9 +346,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
       for (int x = 0; x < w; ++x) before[y] += sh.scan[y][x];
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (before[y] + (x > 0 ? v[y][x - 1] : 0) < target && before[y] + v[y][x] >= target) sh.bracket[y] = 4 * threadIdx.x + x;
+      if (before[y] < target && before[y] + run[y] >= target) sh.bracket[y] = threadIdx.x;
     }
     __syncthreads();
     return make_int2(sh.bracket[0], sh.bracket[1]);
@@ -334,21 +357,40 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
     if (threadIdx.x == 0) sh.count = 0;
     __syncthreads();
     Red v = nothing();
-    each([&](float z, int i) {
-      const uint32_t key = key_of(z);
-      const bool valid = z > -INFINITY && in.keeps(key, i0 + i);
-      const int x = valid ? where(z, key) : 1;
-      if (x < 0) v.a += f(z);
-      const unsigned vote = __ballot_sync(0xffffffffu, x == 0);
-      if (vote != 0) {
-        int at = 0;
-        if (lane == 0) at = atomicAdd(&sh.count, __popc(vote));
-        at = __shfl_sync(0xffffffffu, at, 0) + __popc(vote & ((1u << lane) - 1u));
-        if (x == 0) {
-          ++v.n;
-          v.lo = min(v.lo, key);
-          v.hi = max(v.hi, key);
-          if (at < kList) list[at] = u64(key) << 32 | uint32_t(~(i0 + i));
+    fours([&](const float (&z)[4], int i) {
+      bool front[4], any_front = false, in_any = false, inside[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t key = key_of(z[e]);
+        const bool valid = z[e] > -INFINITY && in.keeps(key, i0 + i + e);
+        const int x = where(z[e], key);
+        front[e] = valid && x < 0;
+        inside[e] = valid && x == 0;
+        any_front |= front[e];
+        in_any |= inside[e];
+      }
+      if (__any_sync(0xffffffffu, any_front)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const u64 y = f(z[e]);
+          v.a += front[e] ? y : 0;
+        }
+      }
+      if (__any_sync(0xffffffffu, in_any)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t key = key_of(z[e]);
+          const unsigned vote = __ballot_sync(0xffffffffu, inside[e]);
+          if (vote == 0) continue;
+          int at = 0;
+          if (lane == 0) at = atomicAdd(&sh.count, __popc(vote));
+          at = __shfl_sync(0xffffffffu, at, 0) + __popc(vote & ((1u << lane) - 1u));
+          if (inside[e]) {
+            ++v.n;
+            v.lo = min(v.lo, key);
+            v.hi = max(v.hi, key);
+            if (at < kList) list[at] = u64(key) << 32 | uint32_t(~(i0 + i + e));
+          }
         }
       }
     });
@@ -362,10 +404,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
 
   // Bins of equal width from a logit down; the last has no end.
   auto bin_of = [&](float from, float z, float scale) { return int(fminf((from - z) * scale, float(kBins - 1))); };
+  // -1, 0 or 1: in front of bins x.x..x.y, in them, behind them; without the bin
+  auto against = [&](float from, float z, float scale, int2 x) {
+    const float y = (from - z) * scale;   // a NaN (0 times infinity) is of the last bin, as in bin_of
+    return y < float(x.x) ? -1 : int(x.y < kBins - 1 && !(y < float(x.y + 1)));
+  };
   auto scale_of = [](float width) { return fminf(float(kBins - 1) / width, 1e30f); };
   // What `gather` found of the row, in q, with f of it in wt.
-  u64* q = reinterpret_cast<u64*>(hist);
-  u64* wt = q + kList;
   auto fetch = [&](auto f, int m) {
     if (int(threadIdx.x) < m) {   // the CTAs' lists, end to end
       int at = threadIdx.x, x = 0;
@@ -395,8 +440,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
       count([&](float z, int i) { return inside(key_of(z), i) ? bin_of(from, z, scale) : kBins; });
       const int2 br = bins(edges, ztop - from, scale, target - g.a);
       g = gather(f, in, [&](float z, uint32_t key) {
-        const int x = key > hi ? -1 : bin_of(from, z, scale);
-        return x < br.x ? -1 : int(x > br.y || key < lo);
+        return key > hi ? -1 : key < lo ? 1 : against(from, z, scale, br);
       });
     }
     if (g.n <= uint32_t(kList)) {
@@ -472,8 +516,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
     if (double(f) < least) f = nextafterf(f, INFINITY);
     return key_of(f + 0.f) - 1;
   };
-  auto wanted = [&](u64 sum) { return max(u64(1), u64(ceil(double(sum) * double(fmaxf(given.p, 0.f))))); };
-  auto target_of = [&](u64 total) { return min(given.u > 0.f ? u64(double(given.u) * double(total)) : 0, total - 1); };
+  auto wanted = [&](u64 sum) { return max(u64(1), times(sum, given.p, true)); };
+  auto target_of = [&](u64 total) { return given.u >= 1.f ? total - 1 : times(total, given.u, false); };
   auto put = [&](int i, u64 v, u64 total) {
     P.token[r] = i;
     // near 1 by what is missing, which FP32 then holds to its last bits
@@ -486,13 +530,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
     // The k-th of the threads' largest logits is not above the row's k-th: those that are not below its bin hold the
     // kept ones, and are few more
     const float scale = scale_of(ztop - zlow), best = of_key(best_of_mine);
-    reinterpret_cast<uint4*>(hist)[threadIdx.x] = make_uint4(0, 0, 0, 0);
+    hist[threadIdx.x] = 0;
     __syncthreads();
     if (best_of_mine != 0 && best > -INFINITY) atomicAdd(hist + bin_of(ztop, best, scale), 1u);
     auto one = [](float) { return u64(1); };
     auto ones = [](float, float, u64& most, u64& least) { most = least = 1; };
     const int last = bins(ones, 0.f, scale, u64(given.k)).y;
-    const Red g = gather(one, cut, [&](float z, uint32_t) { return int(bin_of(ztop, z, scale) > last); });
+    const Red g = gather(one, cut, [&](float z, uint32_t) { return against(ztop, z, scale, make_int2(0, last)); });
     if (g.n <= uint32_t(kList)) {
       // All that can be kept is in the list: the row's first CTA does the rest there.
       const int m = int(g.n), at = threadIdx.x;
@@ -535,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
   }
   if (!(given.p >= 1.f)) {
     // below the largest by 32 t a weight is less than 2^-46 and so nothing
-    const float far = 32.f * given.t, cf = float(c);
+    const float far = 32.f * given.t;
     const float scale = scale_of(fminf(ztop - (cut.key == 0 ? zlow : of_key(cut.key)), far));
     Red v = nothing();
     count([&](float z, int i) {
@@ -546,13 +590,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
     const u64 want = wanted(reduce(&sh, ctas, turn, v).a);
     auto edges = [&](float d0, float d1, u64& most, u64& least) {
       // the errors of y and of the function are below 2^-14 of the weight, that of its fixed point is one step
-      most = u64(fminf(exp2f(-d0 * cf) * (1.f + 0x1p-13f), 1.f) * 0x1p44f) + 1;
-      least = u64(fmaxf(exp2f(-d1 * cf) * (1.f - 0x1p-13f) * 0x1p44f - 1.f, 0.f));
+      most = u64(fminf(exp2f(-d0 * ch) * (1.f + 0x1p-13f), 1.f) * 0x1p44f) + 1;
+      least = u64(fmaxf(exp2f(-d1 * ch) * (1.f - 0x1p-13f) * 0x1p44f - 1.f, 0.f));
     };
     const int2 br = bins(edges, 0.f, scale, want);
     const Red g = gather(weight, cut, [&](float z, uint32_t) {
-      const int x = bin_of(ztop, z, scale);
-      return x < br.x ? -1 : int(x > br.y || ztop - z >= far);
+      const int x = against(ztop, z, scale, br);
+      return x == 0 && ztop - z >= far ? 1 : x;
     });
     cut = cut_at(weight, cut, want, g, edges);
   }
