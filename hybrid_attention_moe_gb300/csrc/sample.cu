@@ -24,10 +24,10 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxChunk = 53248;   // logits of a CTA at most: 208 KB
 constexpr int kBins = 512;         // one of a thread
-constexpr int kList = 256;
+constexpr int kList = 512;         // one of a thread
 constexpr int kRounds = 3;         // of counting; what is left then is halved key by key
 constexpr float kLeastT = 1e-30f;  // a temperature below it counts as 0
-static_assert(kWarps == kMaxCluster && kBins == kThreads, "by thread");
+static_assert(kWarps == kMaxCluster && kBins == kThreads && kList == kThreads, "by thread");
 
 struct Params {
   const float* logits;
@@ -65,7 +65,7 @@ struct Shared {
   Red warp[kWarps];
   u64 seg[kWarps];           // equal logits of each warp's
   u64 more[2][kMaxCluster];  // weights to add to those that reduce left: by CTA, and by the CTA's warps
-  u64 total;
+  u64 total, before;
   u64 scan[2][kWarps];
   uint32_t table[16];        // 2^(j/16) in 2^-30
   Given given;
@@ -200,9 +200,8 @@ struct Cut {
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
   extern __shared__ __align__(16) float row[];
   __shared__ Shared sh;
-  __shared__ uint32_t hist[kBins];
-  __shared__ u64 list[kList];             // the CTA's (key, ~index): larger ones are in front
-  __shared__ u64 q[kList], wt[kList];     // the row's, and f of them
+  __shared__ __align__(8) uint32_t hists[2][kBins];   // by turns; later the list's sums in kBins / 2 bins
+  __shared__ u64 list[kList], q[kList];           // (key, ~index), of which larger ones are in front: the CTA's, the row's
   pdl_trigger();
   const int ctas = gridDim.x, rank = blockIdx.x, r = blockIdx.y;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -270,8 +269,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
   const Given given = sh.given;
   // segments: warp w holds logits [w seg, (w + 1) seg) of the CTA
   const int a = min(n4, w * P.seg), b = min(n4, a + P.seg);
-  auto fours = [&](auto f) {   // f(four logits, first index in the CTA) for the warp's, and -inf behind them: by whole warps
-#pragma unroll 2
+  // f(four logits, the first's index in the CTA) for the warp's, and -inf behind them: by whole warps. Not unrolled: of few
+  // logits a cold instruction cache takes most of a pass.
+  auto fours = [&](auto f) {
+#pragma unroll 1
     for (int i = a + 4 * lane; i - 4 * lane < b; i += 128) {
       float4 z = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
       if (i < b) z = *reinterpret_cast<const float4*>(row + i);
@@ -279,16 +280,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
       f(y, i);
     }
   };
-  auto each = [&](auto f) {   // f(logit, index in the CTA)
-    fours([&](const float (&z)[4], int i) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f(z[e], i + e);
-    });
-  };
   if (!(given.t >= kLeastT) || given.k == 1) {
     Red best = nothing();
-    each([&](float z, int i) {
-      if (z == ztop) best.lo = min(best.lo, uint32_t(i0 + i));
+    fours([&](const float (&z)[4], int i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (z[e] == ztop) best.lo = min(best.lo, uint32_t(i0 + i + e));
     });
     best = reduce(&sh, ctas, turn, best);
     if (rank == 0 && threadIdx.x == 0) {
@@ -302,211 +299,46 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
   const float ch = kL / given.t;
   const Weights weight{ztop, ch, (fmaf(-ch, given.t, kL) + kLrest) / given.t, sh.table};
 
-  // Logits counted by bin: f(logit, index) is the bin, or kBins: none.
-  auto count = [&](auto f) {
-    hist[threadIdx.x] = 0;
-    __syncthreads();
-    each([&](float z, int i) {
-      const int x = f(z, i);
-      if (x < kBins) atomicAdd(hist + x, 1u);
-    });
-  };
-  // The first and the last bin in which the cut may lie, `target` beyond what is in front of bin 0; edges(bin, most, least): bounds of a
-  // logit's weight there.
-  auto bracket = [&](auto edges, u64 target) {
-    if (threadIdx.x < 2) sh.bracket[threadIdx.x] = kBins - 1;
-    uint32_t h = 0;
-    if (ctas > 1) {
-      cluster_sync();
-#pragma unroll 8
-      for (int x = 0; x < ctas; ++x) h += remote_load(hist + threadIdx.x, x);
-    } else {
-      __syncthreads();
-      h = hist[threadIdx.x];
-    }
-    u64 run[2] = {0, 0};
-    if (h != 0) {
-      edges(int(threadIdx.x), run[0], run[1]);
-      run[0] *= h;
-      run[1] *= h;
-    }
+  auto scale_of = [](float width, int bins) { return fminf(float(bins - 1) / width, 1e30f); };
+  // The bins, one of each thread, in which the running sums of `most` and of `least` first reach the target (the last if they
+  // do not); sh.before: what is in front of the first.
+  auto find = [&](u64 most, u64 least, u64 target) {
+    const u64 own[2] = {most, least};
     u64 before[2];
+    if (threadIdx.x < 2) sh.bracket[threadIdx.x] = kBins - 1;
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-      u64 s = run[y];
+      u64 s = own[y];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const u64 z = __shfl_up_sync(0xffffffffu, s, o);
         if (lane >= o) s += z;
       }
       if (lane == 31) sh.scan[y][w] = s;
-      before[y] = s - run[y];
+      before[y] = s - own[y];
     }
     __syncthreads();
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-      for (int x = 0; x < w; ++x) before[y] += sh.scan[y][x];
-      if (before[y] < target && before[y] + run[y] >= target) sh.bracket[y] = threadIdx.x;
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) before[y] += x < w ? sh.scan[y][x] : 0;
+      if (before[y] < target && before[y] + own[y] >= target) {
+        sh.bracket[y] = threadIdx.x;
+        if (y == 0) sh.before = before[0];
+      }
     }
     __syncthreads();
     return make_int2(sh.bracket[0], sh.bracket[1]);
   };
-  // Joined over the row: the sum of f in front of a bracket, and the number and keys of what lies in it, the first kList of
-  // which the CTA lists. where(logit, key): -1 in front, 0 inside, 1 behind.
-  auto gather = [&](auto f, const Cut& in, auto where) {
-    if (threadIdx.x == 0) sh.count = 0;
-    __syncthreads();
-    Red v = nothing();
-    fours([&](const float (&z)[4], int i) {
-      bool front[4], any_front = false, in_any = false, inside[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t key = key_of(z[e]);
-        const bool valid = z[e] > -INFINITY && in.keeps(key, i0 + i + e);
-        const int x = where(z[e], key);
-        front[e] = valid && x < 0;
-        inside[e] = valid && x == 0;
-        any_front |= front[e];
-        in_any |= inside[e];
-      }
-      if (__any_sync(0xffffffffu, any_front)) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const u64 y = f(z[e]);
-          v.a += front[e] ? y : 0;
-        }
-      }
-      if (__any_sync(0xffffffffu, in_any)) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t key = key_of(z[e]);
-          const unsigned vote = __ballot_sync(0xffffffffu, inside[e]);
-          if (vote == 0) continue;
-          int at = 0;
-          if (lane == 0) at = atomicAdd(&sh.count, __popc(vote));
-          at = __shfl_sync(0xffffffffu, at, 0) + __popc(vote & ((1u << lane) - 1u));
-          if (inside[e]) {
-            ++v.n;
-            v.lo = min(v.lo, key);
-            v.hi = max(v.hi, key);
-            if (at < kList) list[at] = u64(key) << 32 | uint32_t(~(i0 + i + e));
-          }
-        }
-      }
-    });
-    return reduce(&sh, ctas, turn, v);
-  };
-  // What `reduce` left of the CTAs before this one: their counts.
-  auto counted_before = [&] {
-    const uint32_t x = lane < rank ? sh.red[turn][lane].n : 0u;
-    return __reduce_add_sync(0xffffffffu, x);
-  };
-
-  // Bins of equal width from a logit down; the last has no end.
-  auto bin_of = [&](float from, float z, float scale) { return int(fminf((from - z) * scale, float(kBins - 1))); };
-  // -1, 0 or 1: in front of bins x.x..x.y, in them, behind them; without the bin
-  auto against = [&](float from, float z, float scale, int2 x) {
-    const float y = (from - z) * scale;   // a NaN (0 times infinity) is of the last bin, as in bin_of
-    return y < float(x.x) ? -1 : int(x.y < kBins - 1 && !(y < float(x.y + 1)));
-  };
-  auto scale_of = [](float width) { return fminf(float(kBins - 1) / width, 1e30f); };
-  // What `gather` found of the row, in q, with f of it in wt.
-  auto fetch = [&](auto f, int m) {
+  // What `gather` found of the row, one each of the first threads.
+  auto fetch = [&](int m) {
+    u64 v = 0;
     if (int(threadIdx.x) < m) {   // the CTAs' lists, end to end
       int at = threadIdx.x, x = 0;
       while (at >= int(sh.red[turn][x].n)) at -= int(sh.red[turn][x++].n);
-      const u64 v = ctas > 1 ? remote_load(list + at, x) : list[at];
-      q[threadIdx.x] = v;
-      wt[threadIdx.x] = f(of_key(uint32_t(v >> 32)));
+      v = ctas > 1 ? remote_load(list + at, x) : list[at];
     }
-  };
-  // The cut behind which the sum of f over the tokens in front of it, one by one, first reaches `target`, which the sum
-  // over all does. f is a function of the logit; only tokens in front of `in` count. g: what `gather` found of a
-  // bracket. edges(d0, d1, most, least): bounds of f from distance d0 below the largest to d1. `known`: whether the sums
-  // of f that `reduce` left, with sh.more, are those of the tokens in front of the cut, each CTA's and each warp's.
-  bool known = false;
-  auto bins = [&](auto edges, float off, float scale, u64 target) {
-    return bracket(
-        [&](int x, u64& most, u64& least) {
-          edges(off + float(x) / scale, x == kBins - 1 ? INFINITY : off + float(x + 1) / scale, most, least);
-        },
-        target);
-  };
-  auto cut_at = [&](auto f, const Cut& in, u64 target, Red g, auto edges) {
-    for (int round = 0; round < kRounds && g.n > uint32_t(kList) && g.lo < g.hi; ++round) {
-      const uint32_t lo = g.lo, hi = g.hi;
-      const float from = of_key(hi), scale = scale_of(from - of_key(lo));
-      auto inside = [&](uint32_t key, int i) { return key >= lo && key <= hi && in.keeps(key, i0 + i); };
-      count([&](float z, int i) { return inside(key_of(z), i) ? bin_of(from, z, scale) : kBins; });
-      const int2 br = bins(edges, ztop - from, scale, target - g.a);
-      g = gather(f, in, [&](float z, uint32_t key) {
-        return key > hi ? -1 : key < lo ? 1 : against(from, z, scale, br);
-      });
-    }
-    if (g.n <= uint32_t(kList)) {
-      const int m = int(g.n);
-      fetch(f, m);
-      if (threadIdx.x < 2 * kMaxCluster) sh.more[threadIdx.x / kMaxCluster][threadIdx.x % kMaxCluster] = 0;
-      __syncthreads();
-      if (int(threadIdx.x) < m) {
-        const u64 mine = q[threadIdx.x];
-        u64 before = g.a;
-#pragma unroll 4
-        for (int x = 0; x < m; ++x)
-          if (q[x] > mine) before += wt[x];
-        if (before < target) {
-          const int i = int(~uint32_t(mine)), x = i / P.chunk;
-          atomicAdd(&sh.more[0][x], wt[threadIdx.x]);
-          if (x == rank) atomicAdd(&sh.more[1][(i - i0) / P.seg], wt[threadIdx.x]);
-          if (before + wt[threadIdx.x] >= target) {   // one
-            sh.cut_key = uint32_t(mine >> 32);
-            sh.cut_index = i;
-          }
-        }
-      }
-      __syncthreads();
-      known = true;
-      return Cut{sh.cut_key, sh.cut_index};
-    }
-    // the key, by halves of what is left
-    uint32_t lo = g.lo, hi = g.hi + 1;   // the sum of keys >= lo reaches it, that of keys >= hi does not
-    u64 above = g.a;
-    while (hi - lo > 1) {
-      const uint32_t half = lo + (hi - lo) / 2;
-      Red s = nothing();
-      each([&](float z, int i) {
-        const uint32_t key = key_of(z);
-        if (key >= half && in.keeps(key, i0 + i)) s.a += f(z);
-      });
-      s = reduce(&sh, ctas, turn, s);
-      if (s.a >= target) {
-        lo = half;
-      } else {
-        hi = half;
-        above = s.a;
-      }
-    }
-    // as many of the equal ones as are needed, by index
-    const u64 one = f(of_key(lo)), need = one == 0 ? ~0ull : (target - above + one - 1) / one;
-    auto equal = [&](float z, int i) { return key_of(z) == lo && in.keeps(lo, i0 + i); };
-    Red s = nothing();
-    each([&](float z, int i) { s.n += equal(z, i); });
-    const uint32_t warps = __reduce_add_sync(0xffffffffu, s.n);
-    s = reduce(&sh, ctas, turn, s);
-    if (lane == 0) sh.seg[w] = warps;
-    u64 before = counted_before();
-    __syncthreads();
-    for (int x = 0; x < w; ++x) before += sh.seg[x];
-    Red at = nothing();
-    if (before < need && before + warps >= need)
-      for (int i = a + lane; i - lane < b; i += 32) {
-        const bool hit = i < b && equal(row[i], i);
-        const unsigned vote = __ballot_sync(0xffffffffu, hit);
-        if (hit && before + __popc(vote & ((2u << lane) - 1u)) == need) at.hi = uint32_t(i0 + i) + 1;
-        before += __popc(vote);
-      }
-    at = reduce(&sh, ctas, turn, at);
-    return Cut{lo, at.hi == 0 ? P.V : int(at.hi) - 1};
+    return v;
   };
 
   // Key that min-p's kept ones are above.
@@ -525,26 +357,145 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
       P.logprob[r] = float(v > total / 2 ? log1p(-double(total - v) / double(total)) : log(double(v) / double(total)));
   };
   Cut cut{0, P.V};   // all
-  const float zlow = of_key(all.lo);
-  if (given.k > 0 && uint32_t(given.k) < all.n) {   // logits of -inf weigh nothing
-    // The k-th of the threads' largest logits is not above the row's k-th: those that are not below its bin hold the
-    // kept ones, and are few more
-    const float scale = scale_of(ztop - zlow), best = of_key(best_of_mine);
+  // Whether the sums that `reduce` left, with sh.more, are the weights in front of the cut, each CTA's and each warp's.
+  bool known = false;
+  // Two cuts: top-k's, by counting, and top-p's, by weight. A cut is the place behind which the sum of f (1, or the weight) over the
+  // tokens in front of it, one by one, first reaches a target, which the sum over all does.
+#pragma unroll 1
+  for (int by_weight = 0; by_weight < 2; ++by_weight) {
+    if (by_weight ? given.p >= 1.f : !(given.k > 0 && uint32_t(given.k) < all.n)) continue;   // (-inf weighs nothing)
+    const Cut in = cut;
+    auto f = [&](float z) { return by_weight ? weight(z) : u64(1); };
+    u64 target = u64(given.k);
+    // below the largest by 32 t a weight is less than 2^-46 and so nothing
+    const float far = by_weight ? 32.f * given.t : NAN;
+    // The bracket: keys lo..hi, counted in bins, as wide as `width`, of y = (ztop - z) scale from y0 on. The last bin has no end: a NaN (0 times
+    // infinity) is of it.
+    const float scale = scale_of(fminf(ztop - of_key(in.key == 0 ? all.lo : in.key), far), kBins);
+    uint32_t lo = 0, hi = ktop;
+    float y0 = 0.f, width = 1.f, fine = 1.f;   // fine = 1 / width
+    const float by = ch / scale;               // log2 of a weight by y
+    auto place = [&](float z, float from, float bins) { return ((ztop - z) * scale - from) * bins; };
+    auto bin = [&](float y) { return int(fmaxf(fminf(y, float(kBins - 1)), 0.f)); };
+    auto counts = [&](float z, uint32_t key, int i) {
+      return z > -INFINITY && key >= lo && key <= hi && !(ztop - z >= far) && in.keeps(key, i0 + i);
+    };
+    uint32_t* hist = hists[0];
     hist[threadIdx.x] = 0;
     __syncthreads();
-    if (best_of_mine != 0 && best > -INFINITY) atomicAdd(hist + bin_of(ztop, best, scale), 1u);
-    auto one = [](float) { return u64(1); };
-    auto ones = [](float, float, u64& most, u64& least) { most = least = 1; };
-    const int last = bins(ones, 0.f, scale, u64(given.k)).y;
-    const Red g = gather(one, cut, [&](float z, uint32_t) { return against(ztop, z, scale, make_int2(0, last)); });
-    if (g.n <= uint32_t(kList)) {
+    if (!by_weight) {
+      // The k-th of the threads' largest logits is not above the row's k-th: the logits that are not below its bin hold
+      // the kept ones, and are few more
+      const float best = of_key(best_of_mine);
+      if (best_of_mine != 0 && best > -INFINITY) atomicAdd(hist + bin(place(best, 0.f, 1.f)), 1u);
+    } else {
+      Red v = nothing();
+      fours([&](const float (&z)[4], int i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool in_row = counts(z[e], key_of(z[e]), i + e);
+          if (in_row) atomicAdd(hist + bin(place(z[e], 0.f, 1.f)), 1u);
+          const u64 x = weight(z[e]);
+          v.a += in_row ? x : 0;
+        }
+      });
+      target = wanted(reduce(&sh, ctas, turn, v).a);
+    }
+    Red own = nothing(), g = own;   // own.a: the thread's in front of the bracket
+#pragma unroll 1
+    for (int round = 0;; ++round) {
+      // ---- the bins in which the cut may lie
+      uint32_t h = 0;
+      if (ctas > 1) {
+        cluster_sync();
+#pragma unroll 8
+        for (int x = 0; x < ctas; ++x) h += remote_load(hist + threadIdx.x, x);
+      } else {
+        __syncthreads();
+        h = hist[threadIdx.x];
+      }
+      hist = hists[(round + 1) & 1];
+      hist[threadIdx.x] = 0;
+      u64 most = h, least = h;
+      if (by_weight && h != 0) {
+        // 2^-y at the bin's edges; the errors of y and of the function are below 2^-14 of it, that of a weight is one step
+        const float d0 = fmaf(float(threadIdx.x), width, y0) * by,
+                    d1 = threadIdx.x == kBins - 1 ? INFINITY : fmaf(float(threadIdx.x + 1), width, y0) * by;
+        most = (u64(fminf(exp2f(-d0) * (1.f + 0x1p-13f), 1.f) * 0x1p44f) + 1) * h;
+        least = u64(fmaxf(exp2f(-d1) * (1.f - 0x1p-13f) * 0x1p44f - 1.f, 0.f)) * h;
+      }
+      if (threadIdx.x == 0) sh.count = 0;
+      int2 br = find(most, least, target - g.a);
+      if (!by_weight && round == 0) br.x = 0;
+      // ---- the sum in front of them; the number, the keys and the list of what lies in them, and its counts in finer bins
+      const bool open = br.y == kBins - 1;
+      const float first = br.x == 0 ? -INFINITY : float(br.x), end = float(br.y + 1);
+      const float y1 = fmaf(float(br.x), width, y0), w1 = float(br.y + 1 - br.x) * width * (1.f / kBins), finer = 1.f / w1;
+      own.n = 0;
+      own.lo = 0xFFFFFFFFu;
+      own.hi = 0;
+      fours([&](const float (&z)[4], int i) {
+        bool front[4], any_front = false, any_inside = false, inside[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool valid = counts(z[e], key_of(z[e]), i + e);
+          const float y = place(z[e], y0, fine);
+          front[e] = valid && y < first;
+          inside[e] = valid && !(y < first) && (open || y < end);
+          any_front |= front[e];
+          any_inside |= inside[e];
+        }
+        if (__any_sync(0xffffffffu, any_front)) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const u64 x = f(z[e]);
+            own.a += front[e] ? x : 0;
+          }
+        }
+        if (__any_sync(0xffffffffu, any_inside)) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (!inside[e]) continue;
+            const uint32_t key = key_of(z[e]);
+            ++own.n;
+            own.lo = min(own.lo, key);
+            own.hi = max(own.hi, key);
+            atomicAdd(hist + bin(place(z[e], y1, finer)), 1u);
+          }
+          if (*static_cast<volatile int*>(&sh.count) <= kList) {   // a list that is full already is of no use
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const unsigned vote = __ballot_sync(0xffffffffu, inside[e]);
+              if (vote == 0) continue;
+              int at = 0;
+              if (lane == 0) at = atomicAdd(&sh.count, __popc(vote));
+              at = __shfl_sync(0xffffffffu, at, 0) + __popc(vote & ((1u << lane) - 1u));
+              if (inside[e] && at < kList) list[at] = u64(key_of(z[e])) << 32 | uint32_t(~(i0 + i + e));
+            }
+          }
+        }
+      });
+      g = reduce(&sh, ctas, turn, own);
+      if (g.n <= uint32_t(kList) || g.lo >= g.hi || round == kRounds) break;
+      lo = g.lo;
+      hi = g.hi;
+      y0 = y1;
+      width = w1;
+      fine = finer;
+    }
+    const int m = int(min(g.n, uint32_t(kList) + 1)), at = threadIdx.x;
+    if (!by_weight && m <= kList && uint32_t(given.k) <= g.n && g.a == 0) {
       // All that can be kept is in the list: the row's first CTA does the rest there.
-      const int m = int(g.n), at = threadIdx.x;
-      if (rank == 0) fetch(weight, m);
+      u64 mine = 0;
+      if (rank == 0) mine = fetch(m);
       if (ctas > 1) cluster_sync();   // the others' lists were read
       if (rank != 0) return;
+      u64* wt = list;
       __syncthreads();
-      const u64 mine = at < m ? q[at] : 0, v = at < m ? wt[at] : 0;
+      const u64 v = at < m ? weight(of_key(uint32_t(mine >> 32))) : 0;
+      q[at] = mine;
+      wt[at] = v;
+      __syncthreads();
       u64 before = 0;
       int place = 0;
       if (at < m) {
@@ -560,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
       bool keep = at < m && place < given.k;
       if (!(given.p >= 1.f)) keep = keep && before < wanted(sh.total);
       if (given.mp > 0.f) keep = keep && uint32_t(mine >> 32) > least_key();
-      if (at < m) wt[at] = keep ? v : 0;
+      wt[at] = keep ? v : 0;
       __syncthreads();
       if (keep) {
         u64 total = 0, run = 0;   // of all, and of those of lower indices: the list holds their complements
@@ -569,36 +520,89 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
           total += wt[x];
           if (uint32_t(q[x]) > uint32_t(mine)) run += wt[x];
         }
-        const u64 target = target_of(total);
-        if (run <= target && target < run + v) put(int(~uint32_t(mine)), v, total);
+        const u64 goal = target_of(total);
+        if (run <= goal && goal < run + v) put(int(~uint32_t(mine)), v, total);
       }
       return;
     }
-    cut = cut_at(one, cut, u64(given.k), g, ones);
+    if (m <= kList) {
+      // The list's sums in finer bins name one; those in it are ordered by comparing all with all.
+      const u64 mine = fetch(m);
+      const float z = of_key(uint32_t(mine >> 32)), zhi = of_key(g.hi), by_list = scale_of(zhi - of_key(g.lo), kBins / 2);
+      const u64 v = at < m ? f(z) : 0;
+      const int its = at < m ? int(fminf((zhi - z) * by_list, float(kBins / 2 - 1))) : kBins;
+      u64* sums = reinterpret_cast<u64*>(hists[0]);   // the CTAs have read their counts
+      hists[0][at] = 0;
+      if (at < 2 * kMaxCluster) sh.more[at / kMaxCluster][at % kMaxCluster] = 0;
+      if (at == 0) sh.count = 0;
+      __syncthreads();
+      if (at < m) atomicAdd(sums + its, v);
+      __syncthreads();
+      const u64 s = at < kBins / 2 ? sums[at] : 0;
+      const int it = find(s, s, target - g.a).x;
+      if (its == it) q[atomicAdd(&sh.count, 1)] = mine;
+      __syncthreads();
+      bool keep = its < it;
+      if (its == it) {
+        const int n2 = sh.count;
+        u64 before = g.a + sh.before;
+        for (int x = 0; x < n2; ++x)
+          if (q[x] > mine) before += (q[x] ^ mine) >> 32 ? f(of_key(uint32_t(q[x] >> 32))) : v;
+        keep = before < target;
+        if (keep && before + v >= target) {   // one
+          sh.cut_key = uint32_t(mine >> 32);
+          sh.cut_index = int(~uint32_t(mine));
+        }
+      }
+      if (keep) {
+        const int i = int(~uint32_t(mine)), x = i / P.chunk;
+        atomicAdd(&sh.more[0][x], v);
+        if (x == rank) atomicAdd(&sh.more[1][(i - i0) / P.seg], v);
+      }
+      __syncthreads();
+      cut = Cut{sh.cut_key, sh.cut_index};
+      known = by_weight;
+      continue;
+    }
+    // the key, by halves of what is left: the sum of keys >= klo reaches the target, that of keys >= khi does not
+    uint32_t klo = g.lo, khi = g.hi + 1;
+    u64 above = g.a;
+    while (khi - klo > 1) {
+      const uint32_t half = klo + (khi - klo) / 2;
+      Red s = nothing();
+      for (int i = a + lane; i < b; i += 32) {
+        const uint32_t key = key_of(row[i]);
+        if (key >= half && in.keeps(key, i0 + i)) s.a += f(row[i]);
+      }
+      s = reduce(&sh, ctas, turn, s);
+      if (s.a >= target) {
+        klo = half;
+      } else {
+        khi = half;
+        above = s.a;
+      }
+    }
+    // as many of the equal ones as are needed, by index
+    const u64 one = f(of_key(klo)), need = one == 0 ? ~0ull : (target - above + one - 1) / one;
+    auto equal = [&](int i) { return i < b && key_of(row[i]) == klo && in.keeps(klo, i0 + i); };
+    Red s = nothing();
+    for (int i = a + lane; i < b; i += 32) s.n += equal(i);
+    const uint32_t warps = __reduce_add_sync(0xffffffffu, s.n);
+    reduce(&sh, ctas, turn, s);
+    if (lane == 0) sh.seg[w] = warps;
+    u64 before = __reduce_add_sync(0xffffffffu, lane < rank ? sh.red[turn][lane].n : 0u);   // in CTAs before this one
+    __syncthreads();
+    for (int x = 0; x < w; ++x) before += sh.seg[x];
+    Red last = nothing();
+    if (before < need && before + warps >= need)
+      for (int i = a + lane; i - lane < b; i += 32) {
+        const unsigned vote = __ballot_sync(0xffffffffu, equal(i));
+        if (equal(i) && before + __popc(vote & ((2u << lane) - 1u)) == need) last.hi = uint32_t(i0 + i) + 1;
+        before += __popc(vote);
+      }
+    last = reduce(&sh, ctas, turn, last);
+    cut = Cut{klo, last.hi == 0 ? P.V : int(last.hi) - 1};
     known = false;
-  }
-  if (!(given.p >= 1.f)) {
-    // below the largest by 32 t a weight is less than 2^-46 and so nothing
-    const float far = 32.f * given.t;
-    const float scale = scale_of(fminf(ztop - (cut.key == 0 ? zlow : of_key(cut.key)), far));
-    Red v = nothing();
-    count([&](float z, int i) {
-      const u64 x = cut.keeps(key_of(z), i0 + i) ? weight(z) : 0;
-      v.a += x;
-      return x != 0 ? bin_of(ztop, z, scale) : kBins;
-    });
-    const u64 want = wanted(reduce(&sh, ctas, turn, v).a);
-    auto edges = [&](float d0, float d1, u64& most, u64& least) {
-      // the errors of y and of the function are below 2^-14 of the weight, that of its fixed point is one step
-      most = u64(fminf(exp2f(-d0 * ch) * (1.f + 0x1p-13f), 1.f) * 0x1p44f) + 1;
-      least = u64(fmaxf(exp2f(-d1 * ch) * (1.f - 0x1p-13f) * 0x1p44f - 1.f, 0.f));
-    };
-    const int2 br = bins(edges, 0.f, scale, want);
-    const Red g = gather(weight, cut, [&](float z, uint32_t) {
-      const int x = against(ztop, z, scale, br);
-      return x == 0 && ztop - z >= far ? 1 : x;
-    });
-    cut = cut_at(weight, cut, want, g, edges);
   }
   if (given.mp > 0.f) {
     const uint32_t key = least_key();
@@ -611,8 +615,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
   if (!known) {
     if (threadIdx.x < 2 * kMaxCluster) sh.more[threadIdx.x / kMaxCluster][threadIdx.x % kMaxCluster] = 0;
     Red mine = nothing();
-    each([&](float z, int i) {
-      if (cut.keeps(key_of(z), i0 + i)) mine.a += weight(z);
+    fours([&](const float (&z)[4], int i) {
+      bool keep[4], any = false;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) any |= keep[e] = cut.keeps(key_of(z[e]), i0 + i + e);
+      if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const u64 x = weight(z[e]);
+          mine.a += keep[e] ? x : 0;
+        }
+      }
     });
     reduce(&sh, ctas, turn, mine);
   } else if (ctas > 1) {
