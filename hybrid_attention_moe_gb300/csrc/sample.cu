@@ -59,6 +59,7 @@ struct Given {
   float t;
   int k;
   float p, mp, u;
+  u64 least;   // t log(min_p) in FP64: one lane's work (11K cycles of all threads), while the row is on its way
 };
 struct Shared {
   Red red[2][kMaxCluster];   // by CTA; two in turn
@@ -224,6 +225,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
     g.p = __shfl_sync(0xffffffffu, g.p, 0);
     g.mp = __shfl_sync(0xffffffffu, g.mp, 0);
     g.u = __shfl_sync(0xffffffffu, g.u, 0);
+    g.least = 0;
+    if (g.mp > 0.f) g.least = u64(__double_as_longlong(lane == 0 ? double(g.t) * log(double(g.mp)) : 0.0));
+    g.least = __shfl_sync(0xffffffffu, g.least, 0);
     if (ctas == 1) {
       if (lane == 0) sh.given = g;
     } else if (lane < ctas) {
@@ -232,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
       remote_store(&sh.given.p, lane, __float_as_uint(g.p));
       remote_store(&sh.given.mp, lane, __float_as_uint(g.mp));
       remote_store(&sh.given.u, lane, __float_as_uint(g.u));
+      remote_store(&sh.given.least, lane, g.least);
     }
   }
   const float* src = P.logits + int64_t(r) * P.stride + i0;
@@ -343,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
 
   // Key that min-p's kept ones are above.
   auto least_key = [&] {
-    const double least = fmin(double(ztop), double(ztop) + double(given.t) * log(double(given.mp)));
+    const double least = fmin(double(ztop), double(ztop) + __longlong_as_double(static_cast<long long>(given.least)));
     float f = float(least);   // the smallest logit that is not below it
     if (double(f) < least) f = nextafterf(f, INFINITY);
     return key_of(f + 0.f) - 1;
@@ -357,29 +362,30 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
       P.logprob[r] = float(v > total / 2 ? log1p(-double(total - v) / double(total)) : log(double(v) / double(total)));
   };
   Cut cut{0, P.V};   // all
+  float zlow = of_key(all.lo);
   // Whether the sums that `reduce` left, with sh.more, are the weights in front of the cut, each CTA's and each warp's.
   bool known = false;
+  auto keep_only = [&] {   // the row, from here on
+    for (int i = a + lane; i < b; i += 32)
+      if (!cut.keeps(key_of(row[i]), i0 + i)) row[i] = -INFINITY;
+    zlow = of_key(cut.key);
+    cut = Cut{0, P.V};
+    __syncthreads();
+  };
   // Two cuts: top-k's, by counting, and top-p's, by weight. A cut is the place behind which the sum of f (1, or the weight) over the
   // tokens in front of it, one by one, first reaches a target, which the sum over all does.
 #pragma unroll 1
   for (int by_weight = 0; by_weight < 2; ++by_weight) {
     if (by_weight ? given.p >= 1.f : !(given.k > 0 && uint32_t(given.k) < all.n)) continue;   // (-inf weighs nothing)
-    const Cut in = cut;
     auto f = [&](float z) { return by_weight ? weight(z) : u64(1); };
     u64 target = u64(given.k);
-    // below the largest by 32 t a weight is less than 2^-46 and so nothing
-    const float far = by_weight ? 32.f * given.t : NAN;
-    // The bracket: keys lo..hi, counted in bins, as wide as `width`, of y = (ztop - z) scale from y0 on. The last bin has no end: a NaN (0 times
-    // infinity) is of it.
-    const float scale = scale_of(fminf(ztop - of_key(in.key == 0 ? all.lo : in.key), far), kBins);
-    uint32_t lo = 0, hi = ktop;
-    float y0 = 0.f, width = 1.f, fine = 1.f;   // fine = 1 / width
-    const float by = ch / scale;               // log2 of a weight by y
-    auto place = [&](float z, float from, float bins) { return ((ztop - z) * scale - from) * bins; };
+    // The bracket: logits zl..zh, counted in bins of y = d s + o, d the distance from the largest; the last has no end. (In one
+    // rounding, so that y is monotone and the same in every place.) Below the largest by 32 t a weight is less than
+    // 2^-46 and so nothing.
+    float zl = by_weight ? fmaxf(zlow, ztop - 32.f * given.t) : zlow, zh = ztop;
+    float s = fmaxf(scale_of(ztop - zl, kBins), 1e-37f), o = 0.f;
+    auto place = [&](float z, float s, float o) { return fmaf(__fsub_rn(ztop, z), s, o); };
     auto bin = [&](float y) { return int(fmaxf(fminf(y, float(kBins - 1)), 0.f)); };
-    auto counts = [&](float z, uint32_t key, int i) {
-      return z > -INFINITY && key >= lo && key <= hi && !(ztop - z >= far) && in.keeps(key, i0 + i);
-    };
     uint32_t* hist = hists[0];
     hist[threadIdx.x] = 0;
     __syncthreads();
@@ -387,16 +393,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
       // The k-th of the threads' largest logits is not above the row's k-th: the logits that are not below its bin hold
       // the kept ones, and are few more
       const float best = of_key(best_of_mine);
-      if (best_of_mine != 0 && best > -INFINITY) atomicAdd(hist + bin(place(best, 0.f, 1.f)), 1u);
+      if (best_of_mine != 0 && best > -INFINITY) atomicAdd(hist + bin(place(best, s, o)), 1u);
     } else {
       Red v = nothing();
-      fours([&](const float (&z)[4], int i) {
+      fours([&](const float (&z)[4], int) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const bool in_row = counts(z[e], key_of(z[e]), i + e);
-          if (in_row) atomicAdd(hist + bin(place(z[e], 0.f, 1.f)), 1u);
-          const u64 x = weight(z[e]);
-          v.a += in_row ? x : 0;
+          if (z[e] >= zl) atomicAdd(hist + bin(place(z[e], s, o)), 1u);
+          v.a += weight(z[e]);
         }
       });
       target = wanted(reduce(&sh, ctas, turn, v).a);
@@ -419,8 +423,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
       u64 most = h, least = h;
       if (by_weight && h != 0) {
         // 2^-y at the bin's edges; the errors of y and of the function are below 2^-14 of it, that of a weight is one step
-        const float d0 = fmaf(float(threadIdx.x), width, y0) * by,
-                    d1 = threadIdx.x == kBins - 1 ? INFINITY : fmaf(float(threadIdx.x + 1), width, y0) * by;
+        const float by = ch / s, d0 = (float(threadIdx.x) - o) * by, d1 = threadIdx.x == kBins - 1 ? INFINITY : (float(threadIdx.x + 1) - o) * by;
         most = (u64(fminf(exp2f(-d0) * (1.f + 0x1p-13f), 1.f) * 0x1p44f) + 1) * h;
         least = u64(fmaxf(exp2f(-d1) * (1.f - 0x1p-13f) * 0x1p44f - 1.f, 0.f)) * h;
       }
@@ -428,9 +431,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
       int2 br = find(most, least, target - g.a);
       if (!by_weight && round == 0) br.x = 0;
       // ---- the sum in front of them; the number, the keys and the list of what lies in them, and its counts in finer bins
-      const bool open = br.y == kBins - 1;
-      const float first = br.x == 0 ? -INFINITY : float(br.x), end = float(br.y + 1);
-      const float y1 = fmaf(float(br.x), width, y0), w1 = float(br.y + 1 - br.x) * width * (1.f / kBins), finer = 1.f / w1;
+      const float first = br.x == 0 ? -INFINITY : float(br.x), end = br.y == kBins - 1 ? NAN : float(br.y + 1);
+      const float finer = float(kBins) / float(br.y + 1 - br.x), s1 = s * finer, o1 = (o - float(br.x)) * finer;
       own.n = 0;
       own.lo = 0xFFFFFFFFu;
       own.hi = 0;
@@ -438,10 +440,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
         bool front[4], any_front = false, any_inside = false, inside[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const bool valid = counts(z[e], key_of(z[e]), i + e);
-          const float y = place(z[e], y0, fine);
-          front[e] = valid && y < first;
-          inside[e] = valid && !(y < first) && (open || y < end);
+          const bool in = z[e] >= zl && z[e] <= zh;
+          const float y = place(z[e], s, o);
+          front[e] = in && y < first;
+          inside[e] = in && !(y < first) && !(y >= end);
           any_front |= front[e];
           any_inside |= inside[e];
         }
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
             ++own.n;
             own.lo = min(own.lo, key);
             own.hi = max(own.hi, key);
-            atomicAdd(hist + bin(place(z[e], y1, finer)), 1u);
+            atomicAdd(hist + bin(place(z[e], s1, o1)), 1u);
           }
           if (*static_cast<volatile int*>(&sh.count) <= kList) {   // a list that is full already is of no use
 #pragma unroll
@@ -477,11 +479,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
       });
       g = reduce(&sh, ctas, turn, own);
       if (g.n <= uint32_t(kList) || g.lo >= g.hi || round == kRounds) break;
-      lo = g.lo;
-      hi = g.hi;
-      y0 = y1;
-      width = w1;
-      fine = finer;
+      zl = of_key(g.lo);
+      zh = of_key(g.hi);
+      s = s1;
+      o = o1;
     }
     const int m = int(min(g.n, uint32_t(kList) + 1)), at = threadIdx.x;
     if (!by_weight && m <= kList && uint32_t(given.k) <= g.n && g.a == 0) {
@@ -538,8 +539,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
       __syncthreads();
       if (at < m) atomicAdd(sums + its, v);
       __syncthreads();
-      const u64 s = at < kBins / 2 ? sums[at] : 0;
-      const int it = find(s, s, target - g.a).x;
+      const u64 sum = at < kBins / 2 ? sums[at] : 0;
+      const int it = find(sum, sum, target - g.a).x;
       if (its == it) q[atomicAdd(&sh.count, 1)] = mine;
       __syncthreads();
       bool keep = its < it;
@@ -562,6 +563,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
       __syncthreads();
       cut = Cut{sh.cut_key, sh.cut_index};
       known = by_weight;
+      if (!by_weight) keep_only();
       continue;
     }
     // the key, by halves of what is left: the sum of keys >= klo reaches the target, that of keys >= khi does not
@@ -569,26 +571,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
     u64 above = g.a;
     while (khi - klo > 1) {
       const uint32_t half = klo + (khi - klo) / 2;
-      Red s = nothing();
+      Red v = nothing();
       for (int i = a + lane; i < b; i += 32) {
         const uint32_t key = key_of(row[i]);
-        if (key >= half && in.keeps(key, i0 + i)) s.a += f(row[i]);
+        if (key >= half) v.a += f(row[i]);
       }
-      s = reduce(&sh, ctas, turn, s);
-      if (s.a >= target) {
+      v = reduce(&sh, ctas, turn, v);
+      if (v.a >= target) {
         klo = half;
       } else {
         khi = half;
-        above = s.a;
+        above = v.a;
       }
     }
     // as many of the equal ones as are needed, by index
     const u64 one = f(of_key(klo)), need = one == 0 ? ~0ull : (target - above + one - 1) / one;
-    auto equal = [&](int i) { return i < b && key_of(row[i]) == klo && in.keeps(klo, i0 + i); };
-    Red s = nothing();
-    for (int i = a + lane; i < b; i += 32) s.n += equal(i);
-    const uint32_t warps = __reduce_add_sync(0xffffffffu, s.n);
-    reduce(&sh, ctas, turn, s);
+    auto equal = [&](int i) { return i < b && key_of(row[i]) == klo; };
+    Red count = nothing();
+    for (int i = a + lane; i < b; i += 32) count.n += equal(i);
+    const uint32_t warps = __reduce_add_sync(0xffffffffu, count.n);
+    reduce(&sh, ctas, turn, count);
     if (lane == 0) sh.seg[w] = warps;
     u64 before = __reduce_add_sync(0xffffffffu, lane < rank ? sh.red[turn][lane].n : 0u);   // in CTAs before this one
     __syncthreads();
@@ -603,6 +605,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
     last = reduce(&sh, ctas, turn, last);
     cut = Cut{klo, last.hi == 0 ? P.V : int(last.hi) - 1};
     known = false;
+    if (!by_weight) keep_only();
   }
   if (given.mp > 0.f) {
     const uint32_t key = least_key();
