@@ -5,8 +5,9 @@
 //   (p - 1) theta^(-2i/D);  SSMax: q <- q (1 + p / base)^e
 //
 // A CTA takes one token. A lane holds eight elements of a row's lower half and the eight that they pair
-// with, so the rotation stays in the lane, and the lane's gains, sines and cosines are the same for every
-// row: they stay in registers. Rows are loaded before the angles are worked out.
+// with, so the rotation stays in the lane. Rows are loaded before the angles are worked out. What bounds it is
+// memory: two batches of rows are in flight in each warp, and registers decide how many warps there are (64 each: 1024
+// threads an SM; at 120, with the lane's sines and cosines kept over the rows, half as many took 203 us for 149).
 #include <math.h>
 
 #include "gemm_tc.cuh"
@@ -40,13 +41,13 @@ struct AppendParams {
 };
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ AppendParams P) {
+__global__ void __launch_bounds__(512, 2) paged_append_kernel(const __grid_constant__ AppendParams P) {
   pdl_trigger();
   pdl_wait();
   constexpr int LPR = D / 16, RPW = 32 / LPR, HALF = D / 2;   // lanes of a row, rows of a warp
-  constexpr int U = 4;                                        // row groups in flight
-  __shared__ float2 turn[HALF];
-  const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR;
+  constexpr int U = 2;                                        // row groups in flight of a warp
+  __shared__ __align__(16) float2 turn[HALF];   // read where they are used: registers are what limits the loads in flight
+  const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, sub = lane % LPR;
   const int n_q = P.n_q, n_kv = P.c.n_kv;
   const uint16_t* z = P.z + t * P.stride + sub * 8;
   const int groups = (P.rows + RPW - 1) / RPW;
@@ -54,7 +55,7 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
   auto load = [&](int g0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {   // rows past the last repeat it and store nothing
-      const uint16_t* src = z + min((g0 + 8 * u) * RPW + lane / LPR, P.rows - 1) * D;
+      const uint16_t* src = z + min((g0 + warps * u) * RPW + lane / LPR, P.rows - 1) * D;
       lo[u] = ld_stream(src);
       hi[u] = ld_stream(src + HALF);
     }
@@ -75,19 +76,11 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
   const bool keep = pg >= 0 && bad == 0;
   const int off = (sl - 1) & (P.c.page_size - 1);
   __syncthreads();
-  float cs[8], sn[8];
-  if (!P.nope)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float2 x = turn[sub * 8 + e];
-      cs[e] = x.x;
-      sn[e] = x.y;
-    }
-  for (int g0 = warp; g0 < groups; g0 += 8 * U) {
+  for (int g0 = warp; g0 < groups; g0 += warps * U) {
     if (g0 != warp) load(g0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int r0 = (g0 + 8 * u) * RPW, row = r0 + lane / LPR;
+      const int r0 = (g0 + warps * u) * RPW, row = r0 + lane / LPR;
       if (r0 >= P.rows) break;
       uint4 a = lo[u], b = hi[u];
       if (r0 < n_q + n_kv) {   // a group with Q or K rows
@@ -114,10 +107,13 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
         }
         if (!P.nope) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float c = x[e], d = y[e];
-            x[e] = c * cs[e] - d * sn[e];
-            y[e] = d * cs[e] + c * sn[e];
+          for (int e = 0; e < 8; e += 2) {
+            const float4 w = *reinterpret_cast<const float4*>(turn + sub * 8 + e);   // cosine, sine of two
+            const float c0 = x[e], d0 = y[e], c1 = x[e + 1], d1 = y[e + 1];
+            x[e] = c0 * w.x - d0 * w.y;
+            y[e] = d0 * w.x + c0 * w.y;
+            x[e + 1] = c1 * w.z - d1 * w.w;
+            y[e + 1] = d1 * w.z + c1 * w.w;
           }
         } else if (row < n_q) {
 #pragma unroll
@@ -206,7 +202,18 @@ beam_status append(const beam_layer_cfg* cfg, const uint16_t* z, int64_t stride,
                  cfg->kind == BEAM_ATTN_NOPE_SSMAX, cfg->eps, cfg->ssmax_base, cfg->ssmax_exp, {}};
   for (int i = 0; i < D / 2; ++i) p.rope.inv[i] = pow(double(cfg->rope_theta), -2.0 * double(i) / double(D));
   const bool wide = D == 128;
-  auto go = [&](auto kern) { return launch_pdl(kern, dim3(T), dim3(256), 0, st, p); };
+  // The widest block of which all tokens are in flight at once (1024 threads of an SM): a token alone is latency, its rows
+  // in one batch of loads; past that the narrowest, whose barrier holds up the fewest loads. us of BF16 rows, 48 + 8 + 8 + 48 heads of
+  // 128, by threads of a block:
+  //   tokens    64     128     256     512
+  //        1   8.7     6.1     4.7     4.1
+  //      304  11.3     7.8     5.9     5.2
+  //      512  11.9     9.3     7.3     8.3
+  //     1024  14.7    11.7    12.4    13.9
+  //     2048  20.3    21.0    22.4    25.2
+  //    16384   149     156     165     195   (943 MB: 6.3 TB/s)
+  const int sms = num_sms_cached(), threads = T <= 2 * sms ? 512 : T <= 4 * sms ? 256 : T <= 8 * sms ? 128 : 64;
+  auto go = [&](auto kern) { return launch_pdl(kern, dim3(T), dim3(threads), 0, st, p); };
   cudaError_t e;
   if (cache->dtype == kFmtBF16) e = wide ? go(paged_append_kernel<kFmtBF16, 128>) : go(paged_append_kernel<kFmtBF16, 64>);
   else if (cache->dtype == kFmtFP8) e = wide ? go(paged_append_kernel<kFmtFP8, 128>) : go(paged_append_kernel<kFmtFP8, 64>);
