@@ -1002,7 +1002,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
           }
 #pragma unroll
           for (int x = tid; x < BK * (D / 16); x += 128) {
-            const int row = x / (D / 16), gr = x % (D / 16);
+            // the upper half's rows in pairs the other way round: eight lanes then store to all banks
+            const int gr = x % (D / 16), row = (x / (D / 16)) ^ (gr >> 2);
             uint32_t w[8];
             if constexpr (FMT == kFmtFP8) {
               const uint4 y = *reinterpret_cast<const uint4*>(raw + row * C::ROWB + gr * 16);
@@ -1012,7 +1013,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
               e4m3x4_f16(y.w, w[6], w[7]);
             } else {
               const uint2 y = *reinterpret_cast<const uint2*>(raw + row * C::ROWB + gr * 8);
-              const uint32_t unit = e4m3x2_f16x2(raw[C::RAWB + x] * 0x101u);
+              const uint32_t unit = e4m3x2_f16x2(raw[C::RAWB + row * (D / 16) + gr] * 0x101u);
               e2m1x8_f16(y.x, w);
               e2m1x8_f16(y.y, w + 4);
 #pragma unroll
