@@ -53,7 +53,8 @@ using namespace beam::tc;
 // What the codes of a block's 64 keys leave to the softmax: K's powers of two relative to the largest, 2^top, and the
 // exponents of V's. Blocks whose factors may be in use at once: those of K's stages and of two steps.
 struct Factors {
-  float k[BK], v[BK], top, pad[3];
+  float k[BK], v[BK], top;
+  unsigned slices, pad[2];   // of keys that have a page
 };
 constexpr int kFac = 16;
 
@@ -650,18 +651,23 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       float m = kNegInf, l = 0.f, z = kNegInf;
       bool flushed = false;
       const int stride = it.w == 2 ? 1 : 2, j_first = it.j0 + (it.w == 2 ? 0 : s);
-      int entry = units > 0 && lane < 4 ? entry_of_slice(P, it.s, j_first, lane) : -2;
+      [[maybe_unused]] int entry = -2;
+      if constexpr (!C::QUANT) entry = units > 0 && lane < 4 ? entry_of_slice(P, it.s, j_first, lane) : -2;
       for (int k = 0; k < units; ++k, ++un) {
         const int j = j_first + k * stride;
-        const unsigned slices = __ballot_sync(0xffffffffu, lane < 4 && page_of_entry(P, it.s, j, lane, entry) >= 0);
-        if (k + 1 < units) entry = lane < 4 ? entry_of_slice(P, it.s, j + stride, lane) : -2;   // the next one's, meanwhile
-        const bool full = !none && slices == 15u && it.whole(j);
+        unsigned slices = 0;   // of keys that have a page
+        if constexpr (!C::QUANT) {
+          slices = __ballot_sync(0xffffffffu, lane < 4 && page_of_entry(P, it.s, j, lane, entry) >= 0);
+          if (k + 1 < units) entry = lane < 4 ? entry_of_slice(P, it.s, j + stride, lane) : -2;   // the next one's, meanwhile
+        }
         const uint32_t ts = t0 + 64 * (un & 1), bar = 16 * s + 8 * (un & 1);
         if (!all(wait(s_full + bar, (un >> 1) & 1))) { ok = false; break; }
         tc_fence_after();
         if (work) {
-          const uint64_t bits = full ? ~uint64_t(0) : seen(v, it.s, (it.s.blk0 + j) * BK + 1, slices);
           [[maybe_unused]] const Factors* fa = reinterpret_cast<const Factors*>(sm + C::FAC) + ((nb + uint32_t(j - it.j0)) % kFac);
+          if constexpr (C::QUANT) slices = fa->slices;
+          const bool full = !none && slices == 15u && it.whole(j);
+          const uint64_t bits = full ? ~uint64_t(0) : seen(v, it.s, (it.s.blk0 + j) * BK + 1, slices);
           float rf = P.sl2;   // factor of S (over quantised pages, of S times its key's) in log2 units of the weight
           if constexpr (C::QUANT) rf *= ex2(fmaxf(fminf(fa->top + cur.qe, 120.f), -120.f));
           constexpr int HALF = C::QUANT ? 16 : 32;   // words of P of 32 keys
@@ -980,57 +986,64 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
           auto inside = [&](int row) {   // one of the item's keys, in a page
             return kb + row >= it.s.lo && kb + row <= it.s.base + it.s.n && ((live >> (row >> 4)) & 1u);
           };
+          const unsigned b0 = rows[lane], b1 = rows[lane + 32];
           if (kv == 0) {
             // the keys' factors: their powers of two relative to the largest, and those of their values
-            unsigned top = 0;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const unsigned b = rows[lane + 32 * e];
-              if (inside(lane + 32 * e) && b != 255) top = max(top, b);
-            }
+            unsigned top = b0 != 255 && (whole || inside(lane)) ? b0 : 0;
+            if (b1 != 255 && (whole || inside(lane + 32))) top = max(top, b1);
             top = __reduce_max_sync(0xffffffffu, top);
             Factors* fa = reinterpret_cast<Factors*>(sm + C::FAC) + nb % kFac;
             const int row = 16 * (warp - 12) + (lane & 15);
-            const unsigned b = rows[row], bv = rows[BK + row];
             if (lane < 16) {
               // never zero: hidden keys' logits are -inf (a row that is no numbers brings its NaN in its codes)
-              fa->k[row] = __uint_as_float(unsigned(min(127, max(1, int(b) - int(top) + 127))) << 23);
+              fa->k[row] = __uint_as_float(unsigned(min(127, max(1, int(rows[row]) - int(top) + 127))) << 23);
             } else {
+              const unsigned bv = rows[BK + row];
               fa->v[row] = bv == 255 ? 0.f : float(int(bv) - 127);
             }
-            if (row == 0 && lane == 0) fa->top = float(int(top) - 127);
+            if (row == 0 && lane == 0) {
+              fa->top = float(int(top) - 127);
+              fa->slices = live;
+            }
           }
+          // no row that needs a look: no NaN, and of values none that is not the item's
+          const bool plain = (kv == 0 || whole) && !__any_sync(0xffffffffu, b0 == 255 || b1 == 255);
+          // sixteen elements at a time; of the upper half's rows in pairs the other way round: eight lanes then store to all banks
+          constexpr int STEP = 128 / (D / 16);   // rows of a turn, a multiple of 8
+          const int gr = tid % (D / 16), row0 = (tid / (D / 16)) ^ (gr >> 2), ch = (2 * gr) & 7;
+          const uint8_t* from = raw + row0 * C::ROWB + gr * (C::ROWB / (D / 16));
+          uint8_t* to = tile + (gr >> 2) * BK * 128 + row0 * 128;
+          uint8_t *to0 = to + ((ch ^ (row0 & 7)) << 4), *to1 = to + (((ch + 1) ^ (row0 & 7)) << 4);
 #pragma unroll
-          for (int x = tid; x < BK * (D / 16); x += 128) {
-            // the upper half's rows in pairs the other way round: eight lanes then store to all banks
-            const int gr = x % (D / 16), row = (x / (D / 16)) ^ (gr >> 2);
+          for (int i = 0; i < BK / STEP; ++i) {
+            const int row = row0 + i * STEP;
             uint32_t w[8];
             if constexpr (FMT == kFmtFP8) {
-              const uint4 y = *reinterpret_cast<const uint4*>(raw + row * C::ROWB + gr * 16);
+              const uint4 y = *reinterpret_cast<const uint4*>(from + i * STEP * C::ROWB);
               e4m3x4_f16(y.x, w[0], w[1]);
               e4m3x4_f16(y.y, w[2], w[3]);
               e4m3x4_f16(y.z, w[4], w[5]);
               e4m3x4_f16(y.w, w[6], w[7]);
             } else {
-              const uint2 y = *reinterpret_cast<const uint2*>(raw + row * C::ROWB + gr * 8);
+              const uint2 y = *reinterpret_cast<const uint2*>(from + i * STEP * C::ROWB);
               const uint32_t unit = e4m3x2_f16x2(raw[C::RAWB + row * (D / 16) + gr] * 0x101u);
               e2m1x8_f16(y.x, w);
               e2m1x8_f16(y.y, w + 4);
 #pragma unroll
               for (int e = 0; e < 8; ++e) w[e] = mul_f16x2(w[e], unit);
             }
-            // no numbers: NaN, but for values of blocks that not all rows see: zero, as for keys that are not the item's
-            const bool none = rows[row] == 255, out = kv == 1 && !whole && !inside(row);
-            if (none || out) {
-              const bool zero = kv == 1 && !whole;
-              if (zero && !out) odd = true;
+            if (!plain) {
+              // no numbers: NaN, but for values of blocks that not all rows see: zero, as for keys that are not the item's
+              const bool none = rows[row] == 255, out = kv == 1 && !whole && !inside(row);
+              if (none || out) {
+                const bool zero = kv == 1 && !whole;
+                if (zero && !out) odd = true;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) w[e] = zero ? 0u : 0x7FFF7FFFu;
+                for (int e = 0; e < 8; ++e) w[e] = zero ? 0u : 0x7FFF7FFFu;
+              }
             }
-            uint8_t* to = tile + (gr >> 2) * BK * 128 + row * 128;
-            const int ch = (2 * gr) & 7;
-            *reinterpret_cast<uint4*>(to + ((ch ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(to + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+            *reinterpret_cast<uint4*>(to0 + i * STEP * 128) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(to1 + i * STEP * 128) = make_uint4(w[4], w[5], w[6], w[7]);
           }
           if (odd) misc[2] = 1;
           fence_proxy_async_smem();
