@@ -84,6 +84,26 @@ def test_flat_and_peaked_rows():
             assert check(z, floats([x] * 8), **kw)[2] == 0
 
 
+def test_cuts_among_many():
+    """Cuts that lie among more logits than a list holds: flat rows, logits on a coarse grid, masks of the lowest value and of
+    -1e9, two far clusters; top-k around a list's size and beyond it, alone and in front of the other rules."""
+    V = 20000
+    z = torch.stack([logits(31, 1, V, 0.05)[0], logits(32, 1, V, 0.7)[0], logits(33, 1, V, 0.3, True)[0], logits(34, 1, V, 3.0)[0],
+                     logits(35, 1, V, 1.0)[0], logits(36, 1, V, 0.2)[0]])
+    z[3, 1::2] = -3.4028234663852886e38
+    z[4, ::3] = -1e9
+    z[5, 5000:] -= 25.0
+    z[5, 19000:] = -float("inf")
+    T = len(z)
+    for n, p in enumerate((0.05, 0.6, 0.97, 0.9999)):
+        assert check(z, uniform(40 + n, T), p=floats([p] * T))[2] == 0
+        assert check(z, uniform(50 + n, T), t=floats([0.3, 30.0, 1e30, 0.1, 2.0, 0.01]), p=floats([p] * T))[2] == 0
+    for n, k in enumerate((511, 512, 513, 700, 6000, V - 1)):
+        assert check(z, uniform(60 + n, T), k=ints([k] * T))[2] == 0
+        assert check(z, uniform(70 + n, T), k=ints([k] * T), p=floats([0.8] * T))[2] == 0
+        assert check(z, uniform(80 + n, T), t=floats([0.5] * T), k=ints([k] * T), p=floats([0.99] * T), m=floats([0.02] * T))[2] == 0
+
+
 def test_edges_of_the_arguments():
     z, T = logits(9, 12, 500, 3.0), 12
     z[3, 7] = z[3, 9] = 50.0

@@ -280,6 +280,15 @@ def test_many_sequences_and_a_long_row_list():
     verify(k, only=list(range(0, 1030, 37)) + [1023, 1024, 1025, 1029])
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("window", [0, 70])
+def test_attention_of_many_short_items(fmt, window):
+    """Several items of one, two and three tiles of rows and of one to six blocks to each range, whole and cut."""
+    sizes, bases = [(i * 29) % 65 for i in range(300)], [(i * 53) % 310 for i in range(300)]
+    k = case(fmt, 12, 2, 64, 32, bases, sizes, 2150, window=window)
+    verify(k, only=list(range(0, 300, 7)) + [298, 299])
+
+
 def test_offsets_past_32_bits():
     """Pages past 4 GiB of keys give the bits of a small cache."""
     n_kv, D, page = 8, 128, 256
