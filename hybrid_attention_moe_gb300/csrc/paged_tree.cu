@@ -51,11 +51,12 @@ namespace {
 using namespace beam::tc;
 
 // What the codes of a block's 64 keys leave to the softmax: K's powers of two relative to the largest, 2^top, and the
-// exponents of V's. Blocks whose factors may be in use at once: those of K's stages and of two steps.
+// exponents of V's.
 struct Factors {
-  float k[BK], v[BK], top;
-  unsigned slices, pad[2];   // of keys that have a page
+  float k[BK], v[BK], top, pad[3];
 };
+// Blocks that may be in use at once, from the loads of keys to the softmax: a stream at block c has S of c + 2 at most
+// (items of one tile), c + 4 holds a stage, and up to eight stages (three, and three of codes) go on from there.
 constexpr int kFac = 16;
 
 template <int FMT, int D_>
@@ -83,7 +84,8 @@ struct Cfg {
   static constexpr int FAC = CUM + (kMaxSeqs + 4) * 4;               // [kFac] factors of a block's keys (Factors)
   static constexpr int XCH = FAC + (QUANT ? kFac * int(sizeof(Factors)) : 0);   // [128] (m, z, sum) of stream 1
   static constexpr int MASK = XCH + ROWS * 16;                    // [2][8] slices of a K or V stage that have a page
-  static constexpr int BAR = MASK + 16 * 4;
+  static constexpr int LIVE = MASK + 16 * 4;                      // [kFac] the same of the blocks that may be in use at once
+  static constexpr int BAR = LIVE + kFac * 4;
   static constexpr int NBAR = 5 * NST + 4 * NRAW + 22;
   static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int BYTES = MISC + 32 + 1024;
@@ -340,6 +342,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* cum = reinterpret_cast<int*>(sm + C::CUM);
   uint32_t* masks = reinterpret_cast<uint32_t*>(sm + C::MASK);
+  uint32_t* lives = reinterpret_cast<uint32_t*>(sm + C::LIVE);
   volatile int* misc = reinterpret_cast<volatile int*>(sm + C::MISC);   // TMEM address, abort, no numbers, status
   unsigned* status = reinterpret_cast<unsigned*>(sm + C::MISC) + 3;
   int4* seqs = reinterpret_cast<int4*>(sm + C::SEQ);
@@ -452,6 +455,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         const uint32_t keys = uint32_t(run * 16), bar = full + 8 * st;
         if (lane == 0) {
           masks[8 * kv + st] = live;
+          if (kv == 0) lives[nb % kFac] = live;
           mbar_expect_tx(bar, uint32_t(copies) * keys * (C::QUANT ? C::ROWB + 2 - kv + (FMT == kFmtNVFP4 ? D / 16 : 0) : 2 * D));
         }
         __syncwarp();
@@ -651,21 +655,15 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       float m = kNegInf, l = 0.f, z = kNegInf;
       bool flushed = false;
       const int stride = it.w == 2 ? 1 : 2, j_first = it.j0 + (it.w == 2 ? 0 : s);
-      [[maybe_unused]] int entry = -2;
-      if constexpr (!C::QUANT) entry = units > 0 && lane < 4 ? entry_of_slice(P, it.s, j_first, lane) : -2;
       for (int k = 0; k < units; ++k, ++un) {
         const int j = j_first + k * stride;
-        unsigned slices = 0;   // of keys that have a page
-        if constexpr (!C::QUANT) {
-          slices = __ballot_sync(0xffffffffu, lane < 4 && page_of_entry(P, it.s, j, lane, entry) >= 0);
-          if (k + 1 < units) entry = lane < 4 ? entry_of_slice(P, it.s, j + stride, lane) : -2;   // the next one's, meanwhile
-        }
         const uint32_t ts = t0 + 64 * (un & 1), bar = 16 * s + 8 * (un & 1);
         if (!all(wait(s_full + bar, (un >> 1) & 1))) { ok = false; break; }
         tc_fence_after();
         if (work) {
-          [[maybe_unused]] const Factors* fa = reinterpret_cast<const Factors*>(sm + C::FAC) + ((nb + uint32_t(j - it.j0)) % kFac);
-          if constexpr (C::QUANT) slices = fa->slices;
+          const uint32_t ring = (nb + uint32_t(j - it.j0)) % kFac;
+          [[maybe_unused]] const Factors* fa = reinterpret_cast<const Factors*>(sm + C::FAC) + ring;
+          const unsigned slices = lives[ring];   // of keys that have a page
           const bool full = !none && slices == 15u && it.whole(j);
           const uint64_t bits = full ? ~uint64_t(0) : seen(v, it.s, (it.s.blk0 + j) * BK + 1, slices);
           float rf = P.sl2;   // factor of S (over quantised pages, of S times its key's) in log2 units of the weight
@@ -1001,10 +999,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
               const unsigned bv = rows[BK + row];
               fa->v[row] = bv == 255 ? 0.f : float(int(bv) - 127);
             }
-            if (row == 0 && lane == 0) {
-              fa->top = float(int(top) - 127);
-              fa->slices = live;
-            }
+            if (row == 0 && lane == 0) fa->top = float(int(top) - 127);
           }
           // no row that needs a look: no NaN, and of values none that is not the item's
           const bool plain = (kv == 0 || whole) && !__any_sync(0xffffffffu, b0 == 255 || b1 == 255);
