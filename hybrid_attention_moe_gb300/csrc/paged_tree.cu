@@ -14,16 +14,19 @@
 // TMEM columns of stream s, from 256 s: two buffers of S, then P over it, [0, 64) and [64, 128); O [128, 128 + D).
 //   S = Q . K^T      A = Q, B = K block (shared memory, both K-major)
 //   O += P . V       A = P (TMEM), B = V block (MN-major)
-// P is split into a high and a low bf16 half, so that the products keep FP32's accuracy. A stream's next S
-// is made while its softmax works on this one.
+// A stream's next S is made while its softmax works on this one. BF16 pages: P is split into a high and a low bf16 half, so
+// that the products keep FP32's accuracy. FP8 and NVFP4 pages: codes become f16 exactly, q becomes f16 by a power of two
+// for each row (what FP32 does not hold of it beside the row's largest is rounded), the rows' own powers of two go to the
+// logits (K) and to P (V), and P is rounded to f16 once (2^-11); its reference z follows the weights times their value
+// rows' powers, so that a large value row of small weight keeps its bits, and what it takes from others is below 2^-32 of it.
 //
-// The blocks of all items, laid end to end and weighed by their tiles, are cut into equal ranges, one for
-// each CTA; partials of an item that several ranges share go to the workspace and a second kernel joins
-// them. Ranges are planned on the device from the sequences' own lengths.
+// The blocks of all items, laid end to end and weighed by their tiles, with a cost for each item besides, are cut into
+// equal ranges, one for each CTA; partials of an item that several ranges share go to the workspace and a second kernel
+// joins them. Ranges are planned on the device from the sequences' own lengths.
 //
 // Warps: 0 loads keys and 2 values (page table and TMA); 1 and 3 issue the streams' matrix products (the tensor pipe
 // queues only a few, so what one spends on waits the other's products cover); 4-7 and 8-11 are the streams' softmax (a
-// thread per row); over FP8 and NVFP4 pages 12-15 turn keys' codes and 16-19 values' codes into bf16 tiles, exactly; over
+// thread per row); over FP8 and NVFP4 pages 12-15 turn keys' codes and 16-19 values' codes into f16 tiles; over
 // BF16 pages 12-15 clean blocks (below). From 12 on they first write the rows that attend to nothing.
 //
 // A key that only some rows see may hold infinities or NaN, which 0 . V would carry into the others. Blocks
@@ -35,6 +38,19 @@
 //
 // Every mbarrier wait is bounded: on expiry the CTA records BEAM_DEV_TIMEOUT, lets its issued copies land,
 // frees TMEM and returns.
+//
+// Measured with the join, 48 query and 8 KV heads of 128, pages of 64 (us; in brackets the floor of bytes or products):
+//   1 sequence, 100K keys, BF16:   16 nodes 85 (60.5: keys at 4.8 TB/s)   64 nodes 185 (81; three tiles, the third read apart)
+//                          FP8:    16 nodes 108 (30.5)                    64 nodes 282 (81)
+//   32 sequences of 1 to 16 nodes over up to 16K keys:   BF16 217 (157)   FP8 274 (80)
+//   1 sequence, 200 keys, 5 nodes: 16.8 (launch, plan 1, queries 3, four blocks 3, output 6, join)
+// BF16 of one tile is bound by the key stream and the 10 us around it, of more by the streams' softmax beside the tensor pipe (a unit
+// of 64 keys by 128 rows takes a stream 2.8K cycles, 1.5K of them arithmetic; the products 0.9K). Quantised pages are bound by
+// issue slots: 1100 of them each block and SM sub-partition, of 2200 cycles, a third in the conversion, 40 % in the softmax.
+// What paid, at 32 sequences over FP8 (us): first kernel 568; f16 and P by z 543; ranges that count an item's own cost 286 (the
+// last CTA had 24 short items); conversions by turns of whole rows 276. Not kept: 32-wide output columns shared by the streams and queries
+// and output out of line (registers of the loop over blocks: 16 nodes over FP8 119 -> 131 and 138), halves of an item of one tile
+// for each stream (the keys of 64 nodes read once: 193 -> 197, not what bounds it).
 #define BEAM_NO_STATUS_WORD
 #include <cuda.h>
 

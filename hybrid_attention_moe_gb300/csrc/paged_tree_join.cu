@@ -1,5 +1,5 @@
 // Joins the partials of the tree attention over pages (paged_tree.cu): o = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s
-// over an item's parts, m = max m_s, gated and rounded once. It also hands the kernel's status bits on.
+// over an item's parts, m = max m_s, gated and rounded once. It also hands the kernel's status bits on. A few us behind the main kernel: partials are in L2.
 #include "paged_tree.cuh"
 
 namespace beam {

@@ -17,7 +17,9 @@ attn_swa_prefill (the same over a 512-key sliding window, 8 sequences), attn_nop
 (--tokens new tokens of one sequence after --ctx cached keys, NoPE, BF16 KV, bound = tokens:
 the grouped decode form of a verification batch), paged_decode, paged_write, paged_read (the
 paged cache in the format --kv: attention of one new token for each of --tokens sequences of
---ctx tokens; writing --ctx tokens of one; reading all back).
+--ctx tokens; writing --ctx tokens of one; reading all back), paged_tree (a drafted tree of --nodes nodes behind each of
+--tokens sequences of --ctx tokens), paged_append (--ctx packed projection rows of one sequence into the pages), sample
+(--tokens rows of 201,088 logits, top-p 0.9).
 """
 from __future__ import annotations
 
@@ -44,6 +46,7 @@ def main():
     ap.add_argument("--warmup", type=int, default=2)
     ap.add_argument("--ctx", type=int, default=16384)
     ap.add_argument("--tokens", type=int, default=1)
+    ap.add_argument("--nodes", type=int, default=16)
     ap.add_argument("--kv", choices=("bf16", "fp8", "nvfp4"), default="fp8")
     args = ap.parse_args()
     _build.build()
@@ -159,10 +162,15 @@ def main():
         ws = torch.empty(B.workspace_bytes(cf, T, ctx + T), dtype=torch.uint8, device=dev)
         fn = lambda: B.beam_attn(cf, q, gg, W["gate_bias"], kc, seq, pos, ctx + T, W["w_o"], out,  # noqa: E731
                                  ws, max_q_per_seq=T)
-    elif c in ("paged_decode", "paged_write", "paged_read"):
+    elif c == "sample":
+        z = synth.normal((args.tokens, 201088), 2.5, 0.0, 0, ("z",), dev).float()
+        half = torch.full((args.tokens,), 0.5, device=dev)
+        token, top_p = torch.empty(args.tokens, dtype=torch.int32, device=dev), torch.full_like(half, 0.9)
+        fn = lambda: B.beam_sample(z, half, token, None, None, None, top_p)  # noqa: E731
+    elif c in ("paged_decode", "paged_write", "paged_read", "paged_tree", "paged_append"):
         S, ctx, page = args.tokens, args.ctx, 64
         cf = B.LayerCfg.from_shape(shape, B.BEAM_ATTN_NOPE_SSMAX)
-        per = -(-ctx // page)
+        per = -(-(ctx + (args.nodes if c == "paged_tree" else 0)) // page)
         table = torch.randperm(S * per, generator=torch.Generator().manual_seed(0))
         kind = {"bf16": B.BEAM_PAGED_BF16, "fp8": B.BEAM_PAGED_FP8, "nvfp4": B.BEAM_PAGED_NVFP4}
         cache = B.PagedKVCache.empty(S * per, page, shape.n_kv, shape.head_dim,
@@ -172,7 +180,26 @@ def main():
         pos = torch.arange(1, ctx + 1, dtype=torch.int32, device=dev)
         for i in range(S):
             B.beam_paged_kv_write(k, v, torch.full_like(pos, i), pos, cache)
-        if c == "paged_write":
+        if c == "paged_append":
+            qkvg = synth.normal((ctx, shape.qkvg_rows), 1.0, 0.0, 0, ("qkvg",), dev)
+            gain = synth.normal((shape.head_dim,), 0.1, 1.0, 0, ("gain",), dev)
+            qo = torch.empty((ctx, shape.n_q, shape.head_dim), dtype=torch.bfloat16, device=dev)
+            go, row = torch.empty((ctx, shape.q_rows), dtype=torch.bfloat16, device=dev), torch.zeros_like(pos)
+            fn = lambda: B.beam_paged_append(cf, qkvg, gain, gain, row, pos, None, qo, go, cache)  # noqa: E731
+        elif c == "paged_tree":
+            n = args.nodes
+            T = S * n
+            parent = torch.arange(-1, n - 1, dtype=torch.int32, device=dev).repeat(S)
+            start = torch.arange(0, T + 1, n, dtype=torch.int32, device=dev)
+            base, mask = torch.full_like(seqs, ctx), torch.empty(T, dtype=torch.int64, device=dev)
+            B.beam_tree_plan(parent, start, seqs, base, mask, *(torch.empty(T, dtype=torch.int32, device=dev) for _ in range(3)))
+            q = synth.normal((T, shape.n_q, shape.head_dim), 1.0, 0.0, 0, ("q",), dev)
+            gg = synth.activations(T, shape.q_rows, 0, "g", dev)
+            gb = synth.normal((shape.n_q,), 1.0, 0.0, 0, ("gate_bias",), dev)
+            out = torch.empty((T, shape.q_rows), dtype=torch.bfloat16, device=dev)
+            ws = torch.empty(B.paged_tree_workspace_bytes(cf, T), dtype=torch.uint8, device=dev)
+            fn = lambda: B.beam_paged_tree_attn(cf, q, gg, gb, cache, seqs, start, base, mask, ctx + n, None, out, ws)  # noqa: E731
+        elif c == "paged_write":
             row = torch.zeros_like(pos)
             fn = lambda: B.beam_paged_kv_write(k, v, row, pos, cache)  # noqa: E731
         elif c == "paged_read":

@@ -508,6 +508,9 @@ beam_status beam_paged_kv_keep(const beam_paged_kv* cache, const int32_t* seq_id
  * BEAM_DEV_BAD_SEQ, one with base < 0 or past max_pos or the page table BEAM_DEV_BAD_POSITION; its
  * rows are zero. Keys in a bad page are left out and BEAM_DEV_BAD_PAGE is set.
  * Infinities and NaN as in beam_paged_attn; a row takes none from keys that it does not attend to.
+ * Over FP8 and NVFP4 pages q is rounded as in beam_paged_attn, and a weight times its value row's power of two
+ * to f16: by at most 2^-11 of it, or 2^-32 of the row's largest such product where that is more.
+ * Concurrent calls need a workspace each; a call leaves nothing in it that a later one relies on.
  *  w_o       (device) [H][n_q*D] bf16: out = og W_o^T, [T][H]; NULL: out = og, [T][n_q*D].
  *  ws        beam_paged_tree_workspace_bytes(cfg, T) bytes. */
 beam_status beam_paged_tree_attn(const beam_layer_cfg* cfg, const beam_bf16* q, const beam_bf16* g,
