@@ -129,30 +129,41 @@ __device__ __forceinline__ Red join(Red v) {
 __device__ __forceinline__ Red nothing() { return Red{0, 0, 0xFFFFFFFFu, 0, 0}; }
 
 // One Red of each thread joined over the CTA and, by turns in two buffers, over the cluster (whose CTAs' own stay
-// there, and the CTA's warps' in sh->warp). Every remote access is in front of a barrier of the cluster, so a CTA may leave after any of them.
-__device__ Red reduce(Shared* sh, int ctas, int& turn, Red v) {
+// there, and the CTA's warps' in sh->warp): `publish`, a barrier of the cluster (of the CTA, if it is alone), `collect`.
+// Every remote access is in front of a barrier of the cluster, so a CTA may leave after any of them.
+__device__ __forceinline__ void publish(Shared* sh, int ctas, int& turn, Red v) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   v = join(v);
   __syncthreads();
   if (lane == 0) sh->warp[w] = v;
   __syncthreads();
-  v = join(lane < kWarps ? sh->warp[lane] : nothing());
   turn ^= 1;
+  if (w != 0) return;
+  v = join(lane < kWarps ? sh->warp[lane] : nothing());
   if (ctas > 1) {
-    if (int(threadIdx.x) < ctas) {
+    if (lane < ctas) {
       const Red* to = &sh->red[turn][ctarank()];
-      remote_store(&to->a, threadIdx.x, v.a);
-      remote_store(&to->n, threadIdx.x, v.n);
-      remote_store(&to->lo, threadIdx.x, v.lo);
-      remote_store(&to->hi, threadIdx.x, v.hi);
+      remote_store(&to->a, lane, v.a);
+      remote_store(&to->n, lane, v.n);
+      remote_store(&to->lo, lane, v.lo);
+      remote_store(&to->hi, lane, v.hi);
     }
-    cluster_sync();
-    v = join(lane < ctas ? sh->red[turn][lane] : nothing());
-  } else {
-    if (threadIdx.x == 0) sh->red[turn][0] = v;
-    __syncthreads();
+  } else if (lane == 0) {
+    sh->red[turn][0] = v;
   }
-  return v;
+}
+__device__ __forceinline__ void barrier(int ctas) {
+  if (ctas > 1) cluster_sync();
+  else __syncthreads();
+}
+__device__ __forceinline__ Red collect(const Shared* sh, int ctas, int turn) {
+  const int lane = threadIdx.x & 31;
+  return join(lane < ctas ? sh->red[turn][lane] : nothing());
+}
+__device__ Red reduce(Shared* sh, int ctas, int& turn, Red v) {
+  publish(sh, ctas, turn, v);
+  barrier(ctas);
+  return collect(sh, ctas, turn);
 }
 
 struct Weights {
@@ -411,21 +422,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
           v.a += weight(z[e]);
         }
       });
-      target = wanted(reduce(&sh, ctas, turn, v).a);
+      publish(&sh, ctas, turn, v);   // collected behind the barrier of the counts
     }
     Red own = nothing(), g = own;   // own.a: the thread's in front of the bracket
 #pragma unroll 1
     for (int round = 0;; ++round) {
       // ---- the bins in which the cut may lie
       uint32_t h = 0;
+      barrier(ctas);
       if (ctas > 1) {
-        cluster_sync();
 #pragma unroll 8
         for (int x = 0; x < ctas; ++x) h += remote_load(hist + threadIdx.x, x);
       } else {
-        __syncthreads();
         h = hist[threadIdx.x];
       }
+      if (by_weight && round == 0) target = wanted(collect(&sh, ctas, turn).a);
       hist = hists[(round + 1) & 1];
       hist[threadIdx.x] = 0;
       u64 most = h, least = h;

@@ -198,6 +198,24 @@ def test_tokens_do_not_hang_on_the_batch_and_replay():
     assert torch.equal(token, ref[0]) and torch.equal(logprob, ref[1]) and status() == 0
 
 
+def test_two_calls_at_once():
+    """Calls on two streams, of one row and of many, side by side."""
+    z, u, t = logits(23, 64, 90000, 2.0), uniform(24, 64), uniform(25, 64, 0.6, 1.3)
+    p, k = uniform(26, 64, 0.5, 0.99), ints([(i % 3) * 400 for i in range(64)])
+    refs = [draw(z[:1], u[:1], t[:1], None, p[:1]), draw(z, u, t, k, p)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = [[torch.full_like(x, 9) for x in r] for r in refs for _ in range(4)]
+    torch.cuda.synchronize()
+    for n in range(4):
+        B.beam_sample(z[:1], u[:1], *outs[n], t[:1], None, p[:1], None, streams[0])
+        B.beam_sample(z, u, *outs[4 + n], t, k, p, None, streams[1])
+    torch.cuda.synchronize()
+    for n, o in enumerate(outs):
+        assert torch.equal(o[0], refs[n // 4][0]) and torch.equal(o[1], refs[n // 4][1])
+    assert status() == 0
+
+
 def test_shares_of_many_draws():
     """One row, evenly spaced u: each token is drawn as often as its weight says, to one draw at either end."""
     V, T = 50, 20000

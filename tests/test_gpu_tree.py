@@ -379,6 +379,31 @@ def test_attention_repeats_streams_and_replays():
     assert status() == B.DEV_BAD_PAGE      # the last step's second sequence ends past its pages
 
 
+def test_captured_calls_share_a_workspace():
+    """Two graphs over one workspace, replayed in turn, of calls that split their items (partials, flushed parts and the
+    list of what to join lie there) and of one that does not; garbage in it between the replays."""
+    ks = [case("bf16", 12, 2, 128, 64, [20000], [33], 2600), case("nvfp4", 12, 2, 128, 64, [3000, 50], [64, 3], 2610),
+          case("fp8", 2, 1, 128, 64, [40], [4], 2620)]
+    refs = [run(k) for k in ks]
+    ws = torch.empty(max(B.paged_tree_workspace_bytes(k["cfg"], k["q"].shape[0]) for k in ks), dtype=torch.uint8, device=DEV)
+    held = [[ints(k["seq"]), ints(k["start"]), ints(k["base"]), words(k["nodes"]), torch.zeros_like(r)] for k, r in zip(ks, refs)]
+    torch.cuda.synchronize()
+    graphs = []
+    for k, h in zip(ks, held):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            attend(k["cfg"], k["c"], k["q"], *h[:4], k["most"], k["g"], k["bias"], ws=ws, out=h[4])
+        graphs.append(g)
+    for i in (0, 1, 2, 1, 0, 2, 2, 0):
+        ws.fill_(255 if i else 1)
+        held[i][4].zero_()
+        graphs[i].replay()
+        assert torch.equal(held[i][4], refs[i])
+    for i in (0, 1, 2):          # and without a change between them
+        graphs[i].replay()
+    assert all(torch.equal(h[4], r) for h, r in zip(held, refs)) and status() == 0
+
+
 def test_bindings_refuse_wrong_tensors():
     k = case("bf16", 4, 2, 64, 16, [20], [4], 2600)
     m = words(k["nodes"])
