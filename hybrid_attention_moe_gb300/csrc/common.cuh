@@ -10,12 +10,10 @@
 
 namespace beam {
 
-#ifndef BEAM_NO_STATUS_WORD   // defined by units that are compiled without relocatable device code
 // Status word of the device (BEAM_DEV_* bits). Defined once in misc.cu.
 extern __device__ unsigned int g_dev_status;
 
 __device__ __forceinline__ void flag(unsigned int bit) { atomicOr(&g_dev_status, bit); }
-#endif
 
 // ---- bf16 <-> fp32 ------------------------------------------------------------------
 __device__ __forceinline__ float bf2f(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }

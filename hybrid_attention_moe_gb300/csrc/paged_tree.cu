@@ -16,7 +16,7 @@
 //   O += P . V       A = P (TMEM), B = V block (MN-major)
 // A stream's next S is made while its softmax works on this one. BF16 pages: P is split into a high and a low bf16 half, so
 // that the products keep FP32's accuracy. FP8 and NVFP4 pages: codes become f16 exactly, q becomes f16 by a power of two
-// for each row (what FP32 does not hold of it beside the row's largest is rounded), the rows' own powers of two go to the
+// for each row (exact down to 2^-31 of the row's largest magnitude), the rows' own powers of two go to the
 // logits (K) and to P (V), and P is rounded to f16 once (2^-11); its reference z follows the weights times their value
 // rows' powers, so that a large value row of small weight keeps its bits, and what it takes from others is below 2^-32 of it.
 //
@@ -51,7 +51,9 @@
 // last CTA had 24 short items); conversions by turns of whole rows 276. Not kept: 32-wide output columns shared by the streams and queries
 // and output out of line (registers of the loop over blocks: 16 nodes over FP8 119 -> 131 and 138), halves of an item of one tile
 // for each stream (the keys of 64 nodes read once: 193 -> 197, not what bounds it).
-#define BEAM_NO_STATUS_WORD
+// Without relocatable device code the status word's declaration is a variable of this unit's own, which nothing here
+// uses: the kernel's bits go through the join.
+#pragma nv_diag_suppress 20044
 #include <cuda.h>
 
 #include <atomic>
