@@ -508,12 +508,14 @@ def beam_paged_append(cfg: LayerCfg, qkv, q_norm_w, k_norm_w, seq_id, pos, slot,
     tokens that is a multiple of 8): queries normed and rotated into q_out [T][n_q][D], gate rows into g_out
     [T][n_q*D] (None: qkv has none), K and V into the pages. q_norm_w, k_norm_w None: no norm. slot None: pos."""
     dev, bf, i32 = _on_device(cache), torch.bfloat16, torch.int32
-    n_q, D, T = cfg.n_q, cfg.head_dim, qkv.size(0)
+    if qkv.dim() != 2:
+        raise BeamError(f"beam_paged_append: qkv must be (T, a token's rows), got {tuple(qkv.shape)}")
+    (T, width), (step, unit) = qkv.shape, qkv.stride()
+    n_q, D = cfg.n_q, cfg.head_dim
     row, flat = (n_q * (1 if g_out is None else 2) + 2 * cfg.n_kv) * D, T * n_q * D
     if (q_norm_w is None) != (k_norm_w is None):
         raise BeamError("beam_paged_append: q_norm_w and k_norm_w go together")
-    if (qkv.dtype is not bf or qkv.dim() != 2 or qkv.size(1) < row or qkv.get_device() != dev or
-            (T and qkv.stride(1) != 1)):
+    if qkv.dtype is not bf or width < row or qkv.get_device() != dev or (T and unit != 1):
         raise BeamError(f"beam_paged_append: qkv must be bfloat16 ({T}, {row} or more) on cuda:{dev}, a token's elements "
                         f"contiguous, got {qkv.dtype} {tuple(qkv.shape)} with strides {qkv.stride()} on {qkv.device}")
     if not (_is(seq_id, dev, i32, T) and _is(pos, dev, i32, T) and (slot is None or _is(slot, dev, i32, T)) and
@@ -523,7 +525,7 @@ def beam_paged_append(cfg: LayerCfg, qkv, q_norm_w, k_norm_w, seq_id, pos, slot,
         _want_all(dev, bf, flat, q_out=q_out, **({} if g_out is None else {"g_out": g_out}))
         if q_norm_w is not None:
             _want_all(dev, bf, D, q_norm_w=q_norm_w, k_norm_w=k_norm_w)
-    st = lib().beam_paged_append(cfg._ref(), qkv.data_ptr(), qkv.stride(0) if T > 1 else max(row, qkv.size(1) // 8 * 8),
+    st = lib().beam_paged_append(cfg._ref(), qkv.data_ptr(), step if T > 1 else max(row, width // 8 * 8),
                                  None if q_norm_w is None else q_norm_w.data_ptr(),
                                  None if k_norm_w is None else k_norm_w.data_ptr(), seq_id.data_ptr(),
                                  pos.data_ptr(), None if slot is None else slot.data_ptr(), T, q_out.data_ptr(),
@@ -626,7 +628,7 @@ def beam_tree_accept(parent, token, sampled, row_start, count, path, next, strea
     token sampled at its end, next [N]."""
     dev, i32 = _current(parent, "beam_tree_accept"), torch.int32
     T, N = parent.numel(), count.numel()
-    if path.dim() != 2 or path.size(0) != N:
+    if path.dim() != 2 or path.shape[0] != N:
         raise BeamError(f"beam_tree_accept: path must be [{N}][most nodes], got {tuple(path.shape)}")
     if not (_is(parent, dev, i32, T) and _is(token, dev, i32, T) and _is(sampled, dev, i32, T) and
             _is(row_start, dev, i32, N + 1) and _is(count, dev, i32, N) and _is(next, dev, i32, N) and
@@ -647,7 +649,7 @@ def beam_paged_kv_keep(cache: PagedKVCache, seq_id, base, count, path, stream=No
     tokens of sequence seq_id[i]."""
     dev, i32 = _on_device(cache), torch.int32
     N = seq_id.numel()
-    if path.dim() != 2 or path.size(0) != N:
+    if path.dim() != 2 or path.shape[0] != N:
         raise BeamError(f"beam_paged_kv_keep: path must be [{N}][most nodes], got {tuple(path.shape)}")
     if not (_is(seq_id, dev, i32, N) and _is(base, dev, i32, N) and _is(count, dev, i32, N) and
             _is(path, dev, i32, path.numel())):
@@ -663,21 +665,22 @@ def beam_sample(logits, u, token, logprob=None, temperature=None, top_k=None, to
     """One token per row of logits [T][V] fp32 (elements of a row contiguous) from u [T] fp32 in [0, 1): token [T] int32
     and, unless None, logprob [T] fp32. temperature, top_p, min_p [T] fp32 and top_k [T] int32 on the device, or None."""
     f32, i32 = torch.float32, torch.int32
-    dev, T = _current(logits, "beam_sample"), logits.size(0)
-    if logits.dtype is not f32 or logits.dim() != 2 or (logits.numel() and logits.stride(1) != 1):
+    dev = _current(logits, "beam_sample")
+    if logits.dtype is not f32 or logits.dim() != 2 or (logits.numel() and logits.stride()[1] != 1):
         raise BeamError(f"beam_sample: logits must be float32 (T, V), a row's elements contiguous, got {logits.dtype} "
                         f"{tuple(logits.shape)} with strides {logits.stride()}")
-    floats = {"u": u, "logprob": logprob, "temperature": temperature, "top_p": top_p, "min_p": min_p}
-    ints = {"token": token, "top_k": top_k}
-    for dtype, group in ((f32, floats), (i32, ints)):
-        for name, x in group.items():
-            if (x is not None or name in ("u", "token")) and not _is(x, dev, dtype, T):
-                _want(dev, name, x, dtype, T)
-    ptr = {name: None if x is None else x.data_ptr() for name, x in (*floats.items(), *ints.items())}
-    V = logits.size(1)
-    st = lib().beam_sample(logits.data_ptr(), logits.stride(0) if T > 1 else V, T, V, ptr["u"], ptr["temperature"],
-                           ptr["top_k"], ptr["top_p"], ptr["min_p"], ptr["token"], ptr["logprob"],
-                           _raw_stream(stream, dev))
+    T, V = logits.shape
+    if not (_is(u, dev, f32, T) and _is(token, dev, i32, T) and (logprob is None or _is(logprob, dev, f32, T)) and
+            (temperature is None or _is(temperature, dev, f32, T)) and (top_k is None or _is(top_k, dev, i32, T)) and
+            (top_p is None or _is(top_p, dev, f32, T)) and (min_p is None or _is(min_p, dev, f32, T))):
+        floats = {"u": u, "logprob": logprob, "temperature": temperature, "top_p": top_p, "min_p": min_p}
+        _want_all(dev, f32, T, **{k: x for k, x in floats.items() if x is not None or k == "u"})
+        _want_all(dev, i32, T, **({"token": token} if top_k is None else {"token": token, "top_k": top_k}))
+    st = lib().beam_sample(logits.data_ptr(), logits.stride()[0] if T > 1 else V, T, V, u.data_ptr(),
+                           None if temperature is None else temperature.data_ptr(),
+                           None if top_k is None else top_k.data_ptr(), None if top_p is None else top_p.data_ptr(),
+                           None if min_p is None else min_p.data_ptr(), token.data_ptr(),
+                           None if logprob is None else logprob.data_ptr(), _raw_stream(stream, dev))
     if st:
         _check(st, "beam_sample")
 
