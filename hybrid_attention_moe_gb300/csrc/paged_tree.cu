@@ -41,14 +41,14 @@
 //
 // Measured with the join, 48 query and 8 KV heads of 128, pages of 64 (us; in brackets the floor of bytes or products):
 //   1 sequence, 100K keys, BF16:   16 nodes 85 (60.5: keys at 4.8 TB/s)   64 nodes 185 (81; three tiles, the third read apart)
-//                          FP8:    16 nodes 108 (30.5)                    64 nodes 282 (81)
-//   32 sequences of 1 to 16 nodes over up to 16K keys:   BF16 217 (157)   FP8 274 (80)
+//                          FP8:    16 nodes 108 (30.5)                    64 nodes 275 (81)
+//   32 sequences of 1 to 16 nodes over up to 16K keys:   BF16 217 (157)   FP8 261 (80)
 //   1 sequence, 200 keys, 5 nodes: 16.8 (launch, plan 1, queries 3, four blocks 3, output 6, join)
 // BF16 of one tile is bound by the key stream and the 10 us around it, of more by the streams' softmax beside the tensor pipe (a unit
 // of 64 keys by 128 rows takes a stream 2.8K cycles, 1.5K of them arithmetic; the products 0.9K). Quantised pages are bound by
 // issue slots: 1100 of them each block and SM sub-partition, of 2200 cycles, a third in the conversion, 40 % in the softmax.
 // What paid, at 32 sequences over FP8 (us): first kernel 568; f16 and P by z 543; ranges that count an item's own cost 286 (the
-// last CTA had 24 short items); conversions by turns of whole rows 276. Not kept: 32-wide output columns shared by the streams and queries
+// last CTA had 24 short items); conversions by turns of whole rows 276; output by sectors 261. Not kept: 32-wide output columns shared by the streams and queries
 // and output out of line (registers of the loop over blocks: 16 nodes over FP8 119 -> 131 and 138), halves of an item of one tile
 // for each stream (the keys of 64 nodes read once: 193 -> 197, not what bounds it).
 // Without relocatable device code the status word's declaration is a variable of this unit's own, which nothing here
@@ -940,14 +940,38 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = make_float4(a[4 * e], a[4 * e + 1], a[4 * e + 2], a[4 * e + 3]);
           } else {
-            uint4* y = reinterpret_cast<uint4*>(P.og + cur.at + 32 * x);
+            [[maybe_unused]] uint4* y = reinterpret_cast<uint4*>(P.og + cur.at + 32 * x);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float* z = a + 8 * e;
               const uint2 u0 = finish4(gated, make_float4(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv), make_uint2(g[e].x, g[e].y), bias);
               const uint2 u1 = finish4(gated, make_float4(z[4] * inv, z[5] * inv, z[6] * inv, z[7] * inv), make_uint2(g[e].z, g[e].w), bias);
-              y[e] = make_uint4(u0.x, u0.y, u1.x, u1.y);
+              g[e] = make_uint4(u0.x, u0.y, u1.x, u1.y);
+              if constexpr (!C::QUANT) y[e] = g[e];
             }
+          }
+        }
+        if (C::QUANT && !it.split) {
+          // Two lanes write one row's 32 bytes at a time, then the other's: whole sectors, half the lines of a store (32
+          // sequences over FP8 274 -> 261 us; over BF16, whose warps wait for keys at the end, 217 -> 219)
+          const bool odd_lane = lane & 1;
+          auto swap = [](const uint4& v) {
+            return make_uint4(__shfl_xor_sync(0xffffffffu, v.x, 1), __shfl_xor_sync(0xffffffffu, v.y, 1),
+                              __shfl_xor_sync(0xffffffffu, v.z, 1), __shfl_xor_sync(0xffffffffu, v.w, 1));
+          };
+          const uint4 s0 = swap(odd_lane ? g[0] : g[1]), s1 = swap(odd_lane ? g[2] : g[3]);
+          const size_t mate = __shfl_xor_sync(0xffffffffu, static_cast<unsigned long long>(cur.at), 1);
+          const bool mate_real = __shfl_xor_sync(0xffffffffu, int(real), 1) != 0;
+          uint4* own = reinterpret_cast<uint4*>(P.og + cur.at + 32 * x) + (odd_lane ? 1 : 0);
+          uint4* its = reinterpret_cast<uint4*>(P.og + mate + 32 * x) + (odd_lane ? 1 : 0);
+          uint4 *even = odd_lane ? its : own, *odd_row = odd_lane ? own : its;
+          if (odd_lane ? mate_real : real) {
+            even[0] = odd_lane ? s0 : g[0];
+            even[2] = odd_lane ? s1 : g[2];
+          }
+          if (odd_lane ? real : mate_real) {
+            odd_row[0] = odd_lane ? g[1] : s0;
+            odd_row[2] = odd_lane ? g[3] : s1;
           }
         }
         __syncwarp();
