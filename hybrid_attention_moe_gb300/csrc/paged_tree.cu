@@ -860,6 +860,10 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       // O's factors h^2 (in two steps, which alone may leave FP32's range) to the reference m of what is written
       float h0 = 1.f, h1 = 0.f;
       bool other = false;   // stream 1's share is added here
+      // Whether the row has keys in this stream, and in stream 1. A factor of zero is no sign of none: the share of a stream that
+      // the other outweighs may hold a NaN or an infinity, which reaches the row all the same.
+      const bool own = l != 0.f;
+      bool theirs = false;
       auto half = [](float zs, float top) { return zs == kNegInf ? 0.f : ex2(0.5f * (zs - top)); };
       if (it.w == 1) {
         float4* xch = reinterpret_cast<float4*>(sm + C::XCH);
@@ -879,12 +883,14 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         arrive(x_empty);
         ++turns;
         other = units_of(it, 1) > 0;
+        theirs = y.z != 0.f;
         const float top = fmaxf(m, y.x);
-        if (top != kNegInf) {
+        if (l != l || y.z != y.z || top == INFINITY) {   // a logit that is NaN (its stream's m may be -inf) or +inf
+          l = h0 = h1 = __uint_as_float(0x7FFFFFFFu);
+        } else if (top != kNegInf) {
           h0 = half(z, top);
           h1 = half(y.y, top);
-          l = (m == kNegInf ? 0.f : ex2(m - top) * l) + (y.x == kNegInf ? 0.f : ex2(y.x - top) * y.z);
-          if (top == INFINITY) l = h0 = h1 = __uint_as_float(0x7FFFFFFFu);   // a logit of +inf
+          l = (own ? ex2(m - top) * l : 0.f) + (theirs ? ex2(y.x - top) * y.z : 0.f);
         }
         m = top;
       } else if (C::QUANT && m != kNegInf) {
@@ -909,17 +915,17 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         tmem_wait_ld();
         float a[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) a[e] = h0 == 0.f ? 0.f : __uint_as_float(o[e]) * h0 * h0;
-        if (flushed)
+        for (int e = 0; e < 32; ++e) a[e] = own ? __uint_as_float(o[e]) * h0 * h0 : 0.f;
+        if (flushed && own)
 #pragma unroll
           for (int e = 0; e < 32; ++e) a[e] += fl[s * ROWS * D + 32 * x + e] * h0 * h0;
         if (other) {
           tmem_ld32_nowait(to + 256 + 32 * x, o);
           tmem_wait_ld();
-          if (h1 != 0.f)
+          if (theirs)
 #pragma unroll
             for (int e = 0; e < 32; ++e) a[e] += __uint_as_float(o[e]) * h1 * h1;
-          if (other_flushed && h1 != 0.f)
+          if (other_flushed && theirs)
 #pragma unroll
             for (int e = 0; e < 32; ++e) a[e] += fl[ROWS * D + 32 * x + e] * h1 * h1;
         }
