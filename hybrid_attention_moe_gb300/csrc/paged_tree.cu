@@ -726,7 +726,9 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                   // O holds the stream's earlier products: the last one has to be done
                   if (!all(k == 0 || wait(pv_done + 8 * s, (un - 1) & 1))) { ok = false; break; }
                   tc_fence_after();
-                  const float dm = need ? fmaxf(0.f, ceilf(mt - m)) : 0.f, dz = need ? fmaxf(0.f, ceilf(zt - z)) : 0.f;
+                  // (z down to a whole power: the largest product is at least 2^kBias then, as at a row's first keys)
+                  const float dm = need ? fmaxf(0.f, ceilf(mt - m)) : 0.f;
+                  const float dz = need ? fmaxf(0.f, C::QUANT ? floorf(zt - z) : ceilf(zt - z)) : 0.f;
                   const float f = ex2(-dz);
                   if (k % kFlush != 0) {   // else O is not read again
 #pragma unroll 1
@@ -739,13 +741,22 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                     }
                   }
                   if (x == 1) {
-                    const uint32_t f16 = C::QUANT ? pack_f16x2(f, f) : pack_bf16x2(f, f);
+                    // in FP32 for f16, which has no 2^-25, while a P of up to 2^16 times it is still a number there
+                    const uint32_t fb = pack_bf16x2(f, f);
 #pragma unroll 1
                     for (int y = 0; y < HALF / 16; ++y) {
                       uint32_t o[16];
                       tmem_ld16(ts + 16 * y, o);
 #pragma unroll
-                      for (int e = 0; e < 16; ++e) o[e] = C::QUANT ? mul_f16x2(o[e], f16) : mul_bf16x2(o[e], f16);
+                      for (int e = 0; e < 16; ++e) {
+                        if constexpr (C::QUANT) {
+                          float p0, p1;
+                          unpack_f16(o[e], p0, p1);
+                          o[e] = pack_f16x2(p0 * f, p1 * f);
+                        } else {
+                          o[e] = mul_bf16x2(o[e], fb);
+                        }
+                      }
                       tmem_st16(ts + 16 * y, o);
                     }
                   }
@@ -807,8 +818,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
               f2_split(add2(ls[2], ls[3]), b0, b1);
               sum = (a0 + b0) + (a1 + b1);
               // The references stay while the weights sum to no more than 2^kRescale (quantised pages: while FP32 holds them
-              // and P is no more than 2^(kRescale + kBias)).
-              lag = C::QUANT ? !(sum <= 0x1p60f) || max(most & 0xFFFFu, most >> 16) > 0x7800u : !(sum <= float(1 << kRescale));
+              // and P is no more than kMostP).
+              lag = C::QUANT ? !(sum <= 0x1p60f) || max(most & 0xFFFFu, most >> 16) > kMostP : !(sum <= float(1 << kRescale));
               if (turn == 0) {
                 if (!__any_sync(0xffffffffu, lag)) break;
                 tmem_ld32_nowait(ts + 32 * x, sv);   // P may have taken its registers

@@ -27,7 +27,11 @@ constexpr int kGrid = 152;        // CTAs at most (the workspace is sized for th
 constexpr int kFlush = 128;       // blocks of a stream between flushes of O: 1024 MMAs
 constexpr float kNegInf = -INFINITY;
 constexpr int kRescale = 8;       // log2 of what a block's weights may come to before the running max is taken anew
-constexpr int kBias = 7;          // over quantised pages P <= 2^(kRescale + kBias), below 65504
+// Over quantised pages: log2 of the largest P when the references are taken (it may be just below twice that when they are
+// taken anew). f16 rounds a P below its normal range by up to 2^-25, and once more where a block's first half is brought
+// to new references: 1.5 x 2^-25 in all, less than 2^-32 of the largest.
+constexpr int kBias = 8;
+constexpr unsigned kMostP = 0x7BFFu;   // f16's largest number: past it (an infinity) the references are taken anew
 
 struct Params {
   const uint16_t* q;
