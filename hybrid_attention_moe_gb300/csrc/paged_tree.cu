@@ -913,13 +913,14 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       const int slot = it.j0 > 0 ? 0 : 1;
       const size_t part = ((size_t(r) * 2 + slot) * 2 + (tile & 1)) * ROWS + lr;
       const bool gated = P.g != nullptr && !it.split;
-      const float bias = gated && real ? bf2f(P.gate_bias[cur.hq]) : 0.f;
+      const bool gates = gated && real && l != 0.f;   // a row that sees nothing is zero, whatever its gate holds
+      const float bias = gates ? bf2f(P.gate_bias[cur.hq]) : 0.f;
 #pragma unroll 1
       for (int x = 0; x < D / 32; ++x) {
         uint4 g[4];
-        if (gated && real)
+        if (gated)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) g[e] = reinterpret_cast<const uint4*>(P.g + cur.at + 32 * x)[e];
+          for (int e = 0; e < 4; ++e) g[e] = gates ? reinterpret_cast<const uint4*>(P.g + cur.at + 32 * x)[e] : make_uint4(0, 0, 0, 0);
         __syncwarp();
         uint32_t o[32];
         tmem_ld32_nowait(to + 32 * x, o);

@@ -47,10 +47,11 @@ __global__ void __launch_bounds__(8 * kJoinRows) paged_tree_join_kernel(const Pa
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
+  const bool gated = P.g != nullptr && L != 0.f;   // a row that sees nothing is zero, whatever its gate holds
 #pragma unroll
   for (int e = 0; e < D / 32; ++e)
     *reinterpret_cast<uint2*>(P.og + o + 32 * e) =
-        finish4(P.g != nullptr, make_float4(O[e].x * inv, O[e].y * inv, O[e].z * inv, O[e].w * inv), gv[e], bias);
+        finish4(gated, make_float4(O[e].x * inv, O[e].y * inv, O[e].z * inv, O[e].w * inv), gv[e], bias);
 }
 
 }  // namespace

@@ -502,7 +502,7 @@ beam_status beam_paged_kv_keep(const beam_paged_kv* cache, const int32_t* seq_id
  * with a window W it attends to context positions above p - W, and to the W highest bits of m.
  * The keys of all nodes must have been written.
  *  mask      (device) [T] 64-bit words, 8-byte aligned. Bits from the tree's size on are ignored. 0: a padding
- *            row; it, and every other padding row, gives zero.
+ *            row; it, and every other row that sees no key, gives zero, whatever its gate holds.
  *  max_pos   host-side upper bound of base[i] + the tree's size.
  * A sequence whose rows are more than 64 or out of range, or with a bad seq_id, sets
  * BEAM_DEV_BAD_SEQ, one with base < 0 or past max_pos or the page table BEAM_DEV_BAD_POSITION; its

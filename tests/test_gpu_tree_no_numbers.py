@@ -1,5 +1,5 @@
 """Tree attention over pages: NaN and infinities that reach a row from one of the two streams, which take an item's blocks of 64
-keys in turn, alone."""
+keys in turn, alone; and rows that see nothing beside gates that hold no numbers."""
 import numpy as np
 import pytest
 import torch
@@ -8,7 +8,7 @@ from oracle import tree as OT
 from hybrid_attention_moe_gb300 import beam as B
 from parity import np64
 from test_gpu_paged import FMT, cfg_for, host, ints, randn, status
-from test_gpu_tree import attend, words
+from test_gpu_tree import attend, case, check, run, words
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -91,3 +91,29 @@ def test_values_of_a_stream_that_the_other_outweighs(fmt, bad, base, spot, lead)
     # where the leading value is 0 the others' are due, e^-512 of values below 2^3: FP32 loses weights below 2^-126, so that up to
     # 130 keys come to less than 2^-115 in all
     assert np.all(np.abs(out - ref) <= (2.0 ** -8 + 2.0 ** -11) * np.abs(ref) + 2.0 ** -115)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("base", [100, 20000])
+def test_gates_of_rows_that_see_nothing(fmt, base):
+    """Rows of a tree with mask 0, rows outside all trees and rows without a page give zero, whatever their gates hold; at 20,000
+    keys the item is cut into ranges, whose parts are joined."""
+    k = case(fmt, 6, 2, 128, 32, [base, 40], [9, 5], 3700, pad=(1, 2), spread=0)
+    nodes = [set() if i in (3, 6) else x for i, x in enumerate(k["nodes"])]
+    clean = run(k, nodes)
+    check(k["cfg"], k["c"], k["q"], k["seq"], k["start"], k["base"], nodes, clean, k["g"], k["bias"], only=[0, 1] if base == 100 else [1])
+    idle = [0, 3, 6, 15, 16]
+    for x in (NAN, INF, -INF):
+        g = k["g"].clone()
+        g[idle] = x
+        out = run(k, nodes, g=g)
+        assert status() == 0 and torch.equal(out, clean) and not out[idle].any()
+    bias = k["bias"].clone()
+    bias[1] = NAN
+    out = run(k, nodes, bias=bias).view(-1, 6, 128)
+    assert status() == 0 and not out[idle].any() and torch.isnan(out[[1, 2, 10], 1]).all()
+    k["c"].page_table[1] = -1          # the second sequence has no page at all
+    g = k["g"].clone()
+    g[10:15] = NAN
+    out = run(k, nodes, g=g)
+    assert status() == B.DEV_BAD_PAGE and not out[10:15].any() and torch.equal(out[:10], clean[:10])
