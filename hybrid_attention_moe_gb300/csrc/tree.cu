@@ -123,7 +123,8 @@ struct AcceptParams {
 };
 
 // Each node that its parent's sampled token names offers itself as that parent's successor (the lowest
-// index wins); the path follows the successors from the root.
+// index wins); the path follows the successors from the root. -1, the token of a row that could not be sampled, names none,
+// and a node 0 with a parent is none that the plan has given a place.
 __global__ void __launch_bounds__(32 * kPlanWarps) tree_accept_kernel(const AcceptParams P) {
   pdl_trigger();
   pdl_wait();
@@ -147,11 +148,12 @@ __global__ void __launch_bounds__(32 * kPlanWarps) tree_accept_kernel(const Acce
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int j = lane + 32 * e;
-    if (up[e] >= 0 && up[e] < j && tok[e] == sam[w][up[e]]) atomicMin(&to[w][up[e]], j);
+    if (up[e] >= 0 && up[e] < j && tok[e] >= 0 && tok[e] == sam[w][up[e]]) atomicMin(&to[w][up[e]], j);
   }
   __syncwarp();
   int n = 0, last = 0;
-  for (int j = x.n > 0 ? 0 : kNodes; j < kNodes; j = to[w][j]) {   // successors come later: at most 64 steps
+  const bool root = x.n > 0 && __shfl_sync(0xffffffffu, up[0], 0) == -1;
+  for (int j = root ? 0 : kNodes; j < kNodes; j = to[w][j]) {   // successors come later: at most 64 steps
     if (lane == 0) way[w][n] = j;
     last = j;
     ++n;

@@ -477,12 +477,13 @@ beam_status beam_tree_plan(const int32_t* parent, const int32_t* row_start, cons
 
 /* The path of each tree that verification accepts: from node 0 (the token that the last step sampled) to the
  * child whose drafted token is the one sampled at its parent (the lowest index of several), and on.
- *  token, sampled (device) [T] int32: each node's drafted token, and the one sampled from its logits.
- *  count     (device) [N] int32: nodes of the path, 0 for an empty tree.
+ *  token, sampled (device) [T] int32: each node's drafted token, and the one sampled from its logits. Below 0
+ *            (beam_sample's -1, a filler) they match nothing.
+ *  count     (device) [N] int32: nodes of the path, 0 for an empty tree and where node 0 has a parent.
  *  path      (device) [N][path_stride] int32: their indices in order, then -1. A longer path is cut off
  *            there (count is not).
- *  next      (device) [N] int32: the token sampled at the path's last node, the next step's node 0; -1 for
- *            an empty tree. */
+ *  next      (device) [N] int32: the token sampled at the path's last node, the next step's node 0; -1
+ *            where there is no path. */
 beam_status beam_tree_accept(const int32_t* parent, const int32_t* token, const int32_t* sampled,
                              const int32_t* row_start, int N, int T, int32_t* count, int32_t* path,
                              int path_stride, int32_t* next, beam_stream_t stream);

@@ -40,13 +40,13 @@ def bits(nodes):
 
 
 def accept(parent, token, sampled):
-    """(path, next token) of one tree."""
-    if len(parent) == 0:
+    """(path, next token) of one tree. Tokens below 0 match nothing; without a root there is no path."""
+    if len(parent) == 0 or parent[0] != -1:
         return [], -1
     path = [0]
     while True:
         at = path[-1]
-        child = [j for j in range(at + 1, len(parent)) if parent[j] == at and token[j] == sampled[at]]
+        child = [j for j in range(at + 1, len(parent)) if parent[j] == at and token[j] == sampled[at] >= 0]
         if not child:
             return path, sampled[at]
         path.append(child[0])

@@ -1,0 +1,42 @@
+"""A drafted tree's bookkeeping where a sample failed or node 0 is no root."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import tree as OT
+from hybrid_attention_moe_gb300 import beam as B
+from test_gpu_paged import ints, status
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def accept(parent, token, sampled, start=None):
+    start = [0, len(parent)] if start is None else start
+    N = len(start) - 1
+    count, path, nxt = ints([77] * N), torch.full((N, 8), 77, dtype=torch.int32, device=DEV), ints([77] * N)
+    B.beam_tree_accept(ints(parent), ints(token), ints(sampled), ints(start), count, path, nxt)
+    return count.tolist(), path.tolist(), nxt.tolist()
+
+
+def same_as_the_oracle(trees):
+    start = np.cumsum([0] + [len(t[0]) for t in trees]).tolist()
+    got = accept(*(sum((t[i] for t in trees), []) for i in range(3)), start)
+    assert status() == 0
+    for i, t in enumerate(trees):
+        path, after = OT.accept(*t)
+        assert (got[0][i], got[1][i], got[2][i]) == (len(path), path + [-1] * (8 - len(path)), after), i
+
+
+def test_a_failed_sample_names_no_child():
+    """-1, which sampling gives where a row has no distribution, ends the path, whatever a drafter filled its tokens with."""
+    same_as_the_oracle([([-1, 0, 1], [5, -1, 6], [-1, 6, 7]), ([-1, 0, 1], [5, 4, -1], [4, -1, 7]), ([-1], [-1], [-1]),
+                        ([-1, 0, 0, 2], [5, -1, 4, 9], [4, 3, 9, 1]), ([-1, 0], [5, -7], [-7, 1])])
+    assert OT.accept([-1, 0, 1], [5, -1, 6], [-1, 6, 7]) == ([0], -1)
+
+
+def test_a_node_0_that_is_no_root():
+    """What the plan leaves out is not accepted."""
+    for up in (0, 3, -2, 7):
+        same_as_the_oracle([([-1, 0], [1, 2], [2, 3]), ([up, 0, 1, 1], [1, 2, 3, 4], [2, 3, 4, 5]), ([-1, 0], [1, 2], [2, 3])])
+        assert OT.accept([up, 0, 1, 1], [1, 2, 3, 4], [2, 3, 4, 5]) == ([], -1)

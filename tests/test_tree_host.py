@@ -210,3 +210,9 @@ def test_verify_needs_pages_in_every_layer():
     st = S.BeamStack(synth.TINY, [], [object()], device="cpu")
     with pytest.raises(B.BeamError):
         st.verify(torch.zeros(1, 8), None, None, None, None, 1)
+
+
+def test_accept_takes_no_failed_sample_and_no_lost_root():
+    assert OT.accept([-1, 0, 1], [5, -1, 6], [-1, 6, 7]) == ([0], -1)
+    assert OT.accept([-1, 0], [5, -7], [-7, 1]) == ([0], -7)
+    assert OT.accept([0, 0], [1, 2], [2, 3]) == OT.accept([-2, 0], [1, 2], [2, 3]) == ([], -1)
