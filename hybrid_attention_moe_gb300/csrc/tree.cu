@@ -65,12 +65,15 @@ __global__ void __launch_bounds__(32 * kPlanWarps) tree_plan_kernel(const PlanPa
     pad(P.row_start[i], P.row_start[i + 1]);
     return;
   }
-  bool lost = false;
+  const int base = P.base[i], s = P.seq_id[i];
+  // behind no length, later nodes would take the slots of real tokens: all of them are lost
+  bool lost = x.n > 0 && (base < 0 || base > INT32_MAX - kNodes);
+  const bool none = lost;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int j = lane + 32 * e;
     int up = j < x.n ? P.parent[x.r0 + j] : -1;
-    if (up < -1 || up >= j) {
+    if (none || up < -1 || up >= j) {
       up = -2;
       lost = true;
     }
@@ -97,7 +100,6 @@ __global__ void __launch_bounds__(32 * kPlanWarps) tree_plan_kernel(const PlanPa
     }
     __syncwarp();
   }
-  const int base = P.base[i], s = P.seq_id[i];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int j = lane + 32 * e;

@@ -470,7 +470,7 @@ size_t beam_paged_workspace_bytes(const beam_layer_cfg* cfg, int T, int max_pos)
  *            beam_paged_append takes them.
  * Padding rows, and rows of a sequence of more than 64 or out-of-range rows (which sets BEAM_DEV_BAD_SEQ),
  * get zeros. A node whose parent is not an earlier one sets BEAM_DEV_BAD_POSITION; it and its
- * descendants get mask, pos and slot 0. */
+ * descendants get mask, pos and slot 0, as do all nodes of a tree whose base is negative or above INT32_MAX - 64. */
 beam_status beam_tree_plan(const int32_t* parent, const int32_t* row_start, const int32_t* seq_id,
                            const int32_t* base, int N, int T, uint64_t* mask, int32_t* pos,
                            int32_t* slot, int32_t* row_seq, beam_stream_t stream);

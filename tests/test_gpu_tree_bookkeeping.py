@@ -1,4 +1,4 @@
-"""A drafted tree's bookkeeping where a sample failed or node 0 is no root."""
+"""A drafted tree's bookkeeping where a sample failed, node 0 is no root or a context's length is none."""
 import numpy as np
 import pytest
 import torch
@@ -40,3 +40,21 @@ def test_a_node_0_that_is_no_root():
     for up in (0, 3, -2, 7):
         same_as_the_oracle([([-1, 0], [1, 2], [2, 3]), ([up, 0, 1, 1], [1, 2, 3, 4], [2, 3, 4, 5]), ([-1, 0], [1, 2], [2, 3])])
         assert OT.accept([up, 0, 1, 1], [1, 2, 3, 4], [2, 3, 4, 5]) == ([], -1)
+
+
+@pytest.mark.parametrize("base", [-1, -5, -64, -2 ** 31, 2 ** 31 - 1, 2 ** 31 - 64])
+def test_a_plan_behind_a_length_that_is_none(base):
+    """A negative length (or one whose slots pass 32 bits) would put the tree's later nodes into the slots of real tokens."""
+    parent, start = [-1, 0, 1, 2, 3, 4, 5] + [-1, 0] + [-1], [0, 7, 9, 10]
+    out = [torch.full((10,), 77, dtype=torch.int64 if x == 0 else torch.int32, device=DEV) for x in range(4)]
+    B.beam_tree_plan(ints(parent), ints(start), ints([0, 1, 2]), ints([base, 10, 0]), *out)
+    assert status() == B.DEV_BAD_POSITION
+    assert out[0].tolist() == [0] * 7 + [1, 3, 1]
+    assert out[1].tolist() == [0] * 7 + [11, 12, 1] and out[2].tolist() == [0] * 7 + [11, 12, 1]
+
+
+def test_a_plan_at_the_last_length():
+    out = [torch.full((64,), 77, dtype=torch.int64 if x == 0 else torch.int32, device=DEV) for x in range(4)]
+    base = 2 ** 31 - 1 - 64
+    B.beam_tree_plan(ints(list(range(-1, 63))), ints([0, 64]), ints([0]), ints([base]), *out)
+    assert status() == 0 and out[1].tolist() == out[2].tolist() == list(range(base + 1, 2 ** 31))
