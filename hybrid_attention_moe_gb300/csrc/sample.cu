@@ -169,8 +169,8 @@ __device__ Red reduce(Shared* sh, int ctas, int& turn, Red v) {
 struct Weights {
   float top, ch, cl;   // the largest logit; log2(e) / t in two parts
   const uint32_t* table;
-  // 2^44 e^((z - top) / t)
-  __device__ __forceinline__ u64 operator()(float z) const {
+  // e^((z - top) / t) = m 2^-(30 + shift), before what is below 2^-44 is cut off
+  __device__ __forceinline__ uint32_t parts(float z, int& shift) const {
     const float dh = z - top, b = dh - z, dl = (z - (dh - b)) - (top + b);   // dh + dl = z - top
     float y = dh * ch;
     float lo = fmaf(dh, ch, -y);   // y + lo = (z - top) log2(e) / t
@@ -184,8 +184,14 @@ struct Weights {
     const float r = fmaf(t - kRound, -0.0625f, y) + lo;
     const float p = r * fmaf(r, fmaf(r, fmaf(r, 0.00961812910762848f, 0.0555041086648216f), 0.240226506959101f), 0.693147180559945f);
     const uint32_t e = table[k & 15];
-    const uint32_t m = e + uint32_t(__float2int_rn(p * float(e)));
-    return (static_cast<u64>(m) << 14) >> (-(k >> 4));
+    shift = -(k >> 4);
+    return e + uint32_t(__float2int_rn(p * float(e)));
+  }
+  // 2^44 e^((z - top) / t)
+  __device__ __forceinline__ u64 operator()(float z) const {
+    int shift;
+    const uint32_t m = parts(z, shift);
+    return (static_cast<u64>(m) << 14) >> shift;
   }
 };
 
@@ -374,11 +380,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
   };
   auto wanted = [&](u64 sum) { return max(u64(1), times(sum, given.p, true)); };
   auto target_of = [&](u64 total) { return given.u >= 1.f ? total - 1 : times(total, given.u, false); };
-  auto put = [&](int i, u64 v, u64 total) {
+  auto put = [&](int i, float z, u64 v, u64 total) {
     P.token[r] = i;
-    // near 1 by what is missing, which FP32 then holds to its last bits
-    if (P.logprob)
-      P.logprob[r] = float(v > total / 2 ? log1p(-double(total - v) / double(total)) : log(double(v) / double(total)));
+    if (!P.logprob) return;
+    // near 1 by what is missing, which FP32 then holds to its last bits; else by the weight before it was cut to steps, of which a
+    // small one has few
+    int shift;
+    const double whole = double(weight.parts(z, shift)) * __longlong_as_double((1023ll + 14 - shift) << 52);
+    P.logprob[r] = float(v > total / 2 ? log1p(-double(total - v) / double(total)) : log(whole / double(total)));
   };
   Cut cut{0, P.V};   // all
   float zlow = of_key(all.lo);
@@ -541,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
           if (uint32_t(q[x]) > uint32_t(mine)) run += wt[x];
         }
         const u64 goal = target_of(total);
-        if (run <= goal && goal < run + v) put(int(~uint32_t(mine)), v, total);
+        if (run <= goal && goal < run + v) put(int(~uint32_t(mine)), of_key(uint32_t(mine >> 32)), v, total);
       }
       return;
     }
@@ -684,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
       if (y < w) run += sh.scan[0][y];
       sums += sh.scan[0][y];
     }
-    if (run > target && run - v <= target) put(i0 + i, v, total);
+    if (run > target && run - v <= target) put(i0 + i, row[i], v, total);
     if (target < sums) break;
     target -= sums;
   }

@@ -306,7 +306,8 @@ beam_status beam_lm_head(const beam_bf16* u, const beam_bf16* w_lm, int T, int H
  *  top_p     (device) [T] fp32; >= 1: all. NULL: all. At least one token is kept.
  *  min_p     (device) [T] fp32; <= 0: all. NULL: all. The largest logits are always kept.
  *  token     (device) [T] int32;  logprob (device) [T] fp32 or NULL: the log of the token's share of the kept
- *            weights.
+ *            weights, from its logit and their sum: off by V 2^-44 + 2^-28 and one rounding to FP32 at most. (Of a
+ *            token that is all but certain it is that far off what is missing from 1, which may be less.)
  * A row with a NaN, +inf, or nothing above -inf sets BEAM_DEV_BAD_LOGITS; its token is -1, its logprob NaN.
  * V up to 851,968. No workspace. */
 beam_status beam_sample(const float* logits, int64_t row_stride, int T, int V, const float* u,

@@ -106,15 +106,15 @@ def kept(z, t, k, p, m):
 
 
 def sample(z, u, t=1.0, k=0, p=1.0, m=0.0):
-    """(token, log of its share of the kept weights). Weights count in steps of 2^-44 of the largest."""
+    """(token, log of its share of the kept weights). For the token weights count in steps of 2^-44 of the largest."""
     z = np.asarray(z, np.float64)
     if np.any(np.isnan(z)) or np.any(z == np.inf) or not np.any(np.isfinite(z)):
         return -1, np.nan
     at = kept(z, t, k, p, m)
     w = np.exp((z[at] - z[at].max()) / (t if t >= 1e-30 else 1.0))
-    w = np.floor(w * 2.0 ** 44)
-    run = np.cumsum(w)
+    steps = np.floor(w * 2.0 ** 44)
+    run = np.cumsum(steps)
     over = np.nonzero(run > u * run[-1])[0]
-    j = over[0] if len(over) else np.nonzero(w)[0][-1]
-    return int(at[j]), float(np.log(w[j] / run[-1]))
+    j = over[0] if len(over) else np.nonzero(steps)[0][-1]
+    return int(at[j]), float(np.log(w[j] / w.sum()))
 

@@ -216,3 +216,10 @@ def test_accept_takes_no_failed_sample_and_no_lost_root():
     assert OT.accept([-1, 0, 1], [5, -1, 6], [-1, 6, 7]) == ([0], -1)
     assert OT.accept([-1, 0], [5, -7], [-7, 1]) == ([0], -7)
     assert OT.accept([0, 0], [1, 2], [2, 3]) == OT.accept([-2, 0], [1, 2], [2, 3]) == ([], -1)
+
+
+def test_logprobs_are_those_of_the_logits():
+    """Of a weight of one step of 2^-44 too: 30 nats below the largest, log(1 / 2^44) would be 0.5 off."""
+    for d in (1.0, 20.0, 30.0):
+        tok, lp = OT.sample([-d, 0.0, -1.0], 0.0)
+        assert tok == 0 and abs(lp - (-d - np.log(1 + np.exp(-1) + np.exp(-d)))) < 1e-12
