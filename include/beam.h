@@ -299,7 +299,8 @@ beam_status beam_lm_head(const beam_bf16* u, const beam_bf16* w_lm, int T, int H
  * kept weights passes u times their sum. Weights have a relative error near 2^-29 and are cut to whole steps of
  * 2^-44 of the largest; their sums are exact, so the token hangs on no order of summation and is the
  * same on every run and in every batch. A token of less than 2^-44 of the largest weight is never drawn.
- *  logits    (device) [T] rows of V fp32, row_stride elements apart (>= V). -inf weighs nothing.
+ *  logits    (device) [T] rows of V fp32, row_stride elements apart (>= V). -inf weighs nothing, nor does a logit whose distance
+ *            from the largest leaves FP32's range.
  *  u         (device) [T] fp32 in [0, 1); taken as 0 below; from 1 on the last kept token that weighs anything.
  *  temperature (device) [T] fp32, finite; below 1e-30 (0) the token is the largest logit's. NULL: 1.
  *  top_k     (device) [T] int32; <= 0: all. NULL: all.
@@ -309,7 +310,7 @@ beam_status beam_lm_head(const beam_bf16* u, const beam_bf16* w_lm, int T, int H
  *            weights, from its logit and their sum: off by V 2^-44 + 2^-28 and one rounding to FP32 at most. (Of a
  *            token that is all but certain it is that far off what is missing from 1, which may be less.)
  * A row with a NaN, +inf, or nothing above -inf sets BEAM_DEV_BAD_LOGITS; its token is -1, its logprob NaN.
- * V up to 851,968. No workspace. */
+ * V up to 851,968 and T up to 65,535, else BEAM_ERR_UNSUPPORTED. No workspace. */
 beam_status beam_sample(const float* logits, int64_t row_stride, int T, int V, const float* u,
                         const float* temperature, const int32_t* top_k, const float* top_p,
                         const float* min_p, int32_t* token, float* logprob, beam_stream_t stream);
@@ -512,7 +513,9 @@ beam_status beam_paged_kv_keep(const beam_paged_kv* cache, const int32_t* seq_id
  * Infinities and NaN as in beam_paged_attn; a row takes none from keys that it does not attend to.
  * Over FP8 and NVFP4 pages q is rounded as in beam_paged_attn, and a weight times its value row's power of two
  * to f16: by at most 2^-11 of it, or 2^-32 of the row's largest such product where that is more.
- * Concurrent calls need a workspace each; a call leaves nothing in it that a later one relies on.
+ * Concurrent calls need a workspace each; a call leaves nothing in it that a later one relies on. Work is counted in 32 bits:
+ * BEAM_ERR_UNSUPPORTED where (keys / 64 + 22) ceil(n_q / (2 n_kv)) n_kv min(N, 256) is above 2^30, keys being what max_pos, the
+ * page table and the window (plus 64) allow.
  *  w_o       (device) [H][n_q*D] bf16: out = og W_o^T, [T][H]; NULL: out = og, [T][n_q*D].
  *  ws        beam_paged_tree_workspace_bytes(cfg, T) bytes. */
 beam_status beam_paged_tree_attn(const beam_layer_cfg* cfg, const beam_bf16* q, const beam_bf16* g,

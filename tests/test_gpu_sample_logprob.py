@@ -62,3 +62,12 @@ def test_logprobs_of_all_tokens_add_up():
             assert abs(lp - np.log(w[i] / w.sum())) <= 2.0 ** -28 + 2.0 ** -24 * abs(lp)
         else:
             near(lp, np.log(w[i] / w.sum()), 61)
+
+
+def test_differences_past_the_range_of_fp32():
+    z = torch.full((2, 100), 3e38, device=DEV)
+    z[:, ::2] = -3e38
+    for t in (1.0, 1e30, 3e38):
+        for u in (0.0, 0.5, 1.0):
+            token, lp = draw(z, floats([u] * 2), floats([t] * 2), p=floats([1.0, 0.9]))
+            assert status() == 0 and int(token[0]) % 2 == int(token[1]) % 2 == 1 and abs(float(lp[0]) + np.log(50)) < 1e-5
