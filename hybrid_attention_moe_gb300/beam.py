@@ -515,9 +515,9 @@ def beam_paged_append(cfg: LayerCfg, qkv, q_norm_w, k_norm_w, seq_id, pos, slot,
     row, flat = (n_q * (1 if g_out is None else 2) + 2 * cfg.n_kv) * D, T * n_q * D
     if (q_norm_w is None) != (k_norm_w is None):
         raise BeamError("beam_paged_append: q_norm_w and k_norm_w go together")
-    if qkv.dtype is not bf or width < row or qkv.get_device() != dev or (T and unit != 1):
+    if qkv.dtype is not bf or width < row or qkv.get_device() != dev or (T and unit != 1) or (T > 1 and step >= 1 << 31):
         raise BeamError(f"beam_paged_append: qkv must be bfloat16 ({T}, {row} or more) on cuda:{dev}, a token's elements "
-                        f"contiguous, got {qkv.dtype} {tuple(qkv.shape)} with strides {qkv.stride()} on {qkv.device}")
+                        f"contiguous and tokens less than 2^31 elements apart, got {qkv.dtype} {tuple(qkv.shape)} with strides {qkv.stride()} on {qkv.device}")
     if not (_is(seq_id, dev, i32, T) and _is(pos, dev, i32, T) and (slot is None or _is(slot, dev, i32, T)) and
             _is(q_out, dev, bf, flat) and (g_out is None or _is(g_out, dev, bf, flat)) and
             (q_norm_w is None or (_is(q_norm_w, dev, bf, D) and _is(k_norm_w, dev, bf, D)))):
