@@ -505,24 +505,27 @@ def _want_all(device, dtype, n, **tensors):
 def beam_paged_append(cfg: LayerCfg, qkv, q_norm_w, k_norm_w, seq_id, pos, slot, q_out, g_out,
                       cache: PagedKVCache, stream=None):
     """Packed projection rows qkv [T][Q | K | V (| gate)] bf16 (elements of a token contiguous, any stride between
-    tokens that is a multiple of 8): queries normed and rotated into q_out [T][n_q][D], gate rows into g_out
-    [T][n_q*D] (None: qkv has none), K and V into the pages. q_norm_w, k_norm_w None: no norm. slot None: pos."""
+    tokens that is a multiple of 8): queries normed and rotated into q_out, gate rows into g_out (None: qkv has
+    none), both [T][n_q][D] or [T][n_q*D], K and V into the pages. q_norm_w, k_norm_w None: no norm. slot None: pos."""
     dev, bf, i32 = _on_device(cache), torch.bfloat16, torch.int32
     if qkv.dim() != 2:
         raise BeamError(f"beam_paged_append: qkv must be (T, a token's rows), got {tuple(qkv.shape)}")
     (T, width), (step, unit) = qkv.shape, qkv.stride()
     n_q, D = cfg.n_q, cfg.head_dim
     row, flat = (n_q * (1 if g_out is None else 2) + 2 * cfg.n_kv) * D, T * n_q * D
+    shapes = (T, n_q, D), (T, n_q * D)
     if (q_norm_w is None) != (k_norm_w is None):
         raise BeamError("beam_paged_append: q_norm_w and k_norm_w go together")
     if qkv.dtype is not bf or width < row or qkv.get_device() != dev or (T and unit != 1) or (T > 1 and step >= 1 << 31):
         raise BeamError(f"beam_paged_append: qkv must be bfloat16 ({T}, {row} or more) on cuda:{dev}, a token's elements "
                         f"contiguous and tokens less than 2^31 elements apart, got {qkv.dtype} {tuple(qkv.shape)} with strides {qkv.stride()} on {qkv.device}")
     if not (_is(seq_id, dev, i32, T) and _is(pos, dev, i32, T) and (slot is None or _is(slot, dev, i32, T)) and
-            _is(q_out, dev, bf, flat) and (g_out is None or _is(g_out, dev, bf, flat)) and
+            _is(q_out, dev, bf, flat) and q_out.shape in shapes and
+            (g_out is None or (_is(g_out, dev, bf, flat) and g_out.shape in shapes)) and
             (q_norm_w is None or (_is(q_norm_w, dev, bf, D) and _is(k_norm_w, dev, bf, D)))):
         _want_all(dev, i32, T, seq_id=seq_id, pos=pos, **({} if slot is None else {"slot": slot}))
-        _want_all(dev, bf, flat, q_out=q_out, **({} if g_out is None else {"g_out": g_out}))
+        for name, t in (("q_out", q_out),) + (() if g_out is None else (("g_out", g_out),)):
+            _want(dev, name, t, bf, *shapes)
         if q_norm_w is not None:
             _want_all(dev, bf, D, q_norm_w=q_norm_w, k_norm_w=k_norm_w)
     st = lib().beam_paged_append(cfg._ref(), qkv.data_ptr(), step if T > 1 else max(row, width // 8 * 8),
@@ -543,7 +546,8 @@ def beam_paged_qkv_gate(cfg: LayerCfg, u, w_qkvg, q_norm_w, k_norm_w, seq_id, po
     _want(dev, "w_qkvg", w_qkvg, bf, ((2 * n_q + 2 * cfg.n_kv) * D, H))
     _want_all(dev, bf, D, q_norm_w=q_norm_w, k_norm_w=k_norm_w)
     _want_all(dev, i32, T, seq_id=seq_id, pos=pos, **({} if slot is None else {"slot": slot}))
-    _want_all(dev, bf, T * n_q * D, q_out=q_out, g_out=g_out)
+    _want(dev, "q_out", q_out, bf, (T, n_q, D), (T, n_q * D))
+    _want(dev, "g_out", g_out, bf, (T, n_q, D), (T, n_q * D))
     _want(dev, "ws", ws, ws.dtype, ws.numel())
     st = lib().beam_paged_qkv_gate(cfg._ref(), u.data_ptr(), w_qkvg.data_ptr(), q_norm_w.data_ptr(), k_norm_w.data_ptr(),
                                    seq_id.data_ptr(), pos.data_ptr(), None if slot is None else slot.data_ptr(), T,

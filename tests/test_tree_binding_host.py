@@ -33,3 +33,22 @@ def test_append_refuses_tokens_further_apart_than_an_int_says(calls):  # noqa: F
     assert not calls
     append(rows((1 << 31) - 8))
     assert calls == ["beam_paged_append"]
+
+
+def project(q=None, g=None):
+    B.beam_paged_qkv_gate(cfg(), z(T, 96), z(WIDTH, 96), z(D), z(D), index(), index(), None, z(T, N_Q, D) if q is None else q,
+                          z(T, N_Q * D) if g is None else g, cache(), z(256, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("call", [append, project])
+def test_rows_are_written_into_the_documented_shapes_only(calls, call):  # noqa: F811
+    """A tensor of as many elements in another order is refused, not written as something else."""
+    good = [dict(), dict(q=z(T, N_Q * D)), dict(g=z(T, N_Q, D))]
+    for kw in good:
+        call(**kw)
+    assert len(calls) == len(good)
+    for kw in (dict(q=z(T, D, N_Q)), dict(q=z(N_Q, T, D)), dict(q=z(T * N_Q * D)), dict(g=z(T, D, N_Q)), dict(g=z(N_Q * D, T)),
+               dict(q=z(T, N_Q, D).float()), dict(g=z(T, N_Q - 1, D))):
+        with pytest.raises(B.BeamError):
+            call(**kw)
+    assert len(calls) == len(good)
