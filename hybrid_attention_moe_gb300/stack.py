@@ -391,6 +391,8 @@ class BeamStack:
     def keep(self, seq_id, base, count, path, stream=None):
         """After verify(): the accepted nodes path[i][:count[i]] of each tree become the count[i] tokens behind
         base[i], in every layer's pages."""
+        if not all(isinstance(c, B.PagedKVCache) for c in self.caches):
+            raise B.BeamError("BeamStack.keep needs paged caches in every layer")
         with on(stream):
             for kc in self.caches:
                 B.beam_paged_kv_keep(kc, seq_id, base, count, path, stream)

@@ -223,3 +223,10 @@ def test_logprobs_are_those_of_the_logits():
     for d in (1.0, 20.0, 30.0):
         tok, lp = OT.sample([-d, 0.0, -1.0], 0.0)
         assert tok == 0 and abs(lp - (-d - np.log(1 + np.exp(-1) + np.exp(-d)))) < 1e-12
+
+
+def test_keep_needs_pages_in_every_layer():
+    """Before the first layer's rows are moved."""
+    st = S.BeamStack(synth.TINY, [], [object()], device="cpu")
+    with pytest.raises(B.BeamError):
+        st.keep(None, None, None, None)
