@@ -38,7 +38,7 @@ def _stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(ROOT, "include", "beam.h"))
+    deps += [os.path.join(ROOT, "include", "beam.h"), os.path.abspath(__file__)]   # the rules of this file too
     return any(os.path.getmtime(d) > t for d in deps)
 
 
