@@ -1,11 +1,12 @@
-"""A drafted tree's bookkeeping where a sample failed, node 0 is no root or a context's length is none."""
+"""A drafted tree's bookkeeping where a sample failed, node 0 is no root, a context's length is none, or sequences share
+pages."""
 import numpy as np
 import pytest
 import torch
 
 from oracle import tree as OT
 from hybrid_attention_moe_gb300 import beam as B
-from test_gpu_paged import ints, status
+from test_gpu_paged import host, ints, make_cache, status
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -58,3 +59,26 @@ def test_a_plan_at_the_last_length():
     base = 2 ** 31 - 1 - 64
     B.beam_tree_plan(ints(list(range(-1, 63))), ints([0, 64]), ints([0]), ints([base]), *out)
     assert status() == 0 and out[1].tolist() == out[2].tolist() == list(range(base + 1, 2 ** 31))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+def test_keep_of_sequences_that_share_their_prefix(fmt):
+    """Two sequences whose tables name the same pages for their common context: each moves rows of its own pages."""
+    c, *_ = make_cache(fmt, 2, 64, 32, [96, 96], 4400)
+    c.page_table[1, :2] = c.page_table[0, :2]
+    ref, before = host(c), host(c)
+    paths = [[0, 3, 4, 9], [1, 2, 7, 20]]
+    for s, p in enumerate(paths):
+        for i, x in enumerate(p):
+            (pa, oa), (pb, ob) = before.place(s, 64 + 1 + x), before.place(s, 64 + 1 + i)
+            for name in ("k", "v"):
+                getattr(ref, name)[pb, :, ob] = getattr(before, name)[pa, :, oa]
+            for name in ("row", "block"):
+                if getattr(ref, name) is not None:
+                    getattr(ref, name)[pb, :, :, ob] = getattr(before, name)[pa, :, :, oa]
+    B.beam_paged_kv_keep(c, ints([0, 1]), ints([64, 64]), ints([4, 4]), ints(paths))
+    assert status() == 0
+    after = host(c)
+    for name in ("k", "v", "row", "block"):
+        a, b = getattr(ref, name), getattr(after, name)
+        assert a is None or np.array_equal(a, b, equal_nan=a.dtype.kind == "f"), name
