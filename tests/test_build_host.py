@@ -15,9 +15,8 @@ def test_a_library_older_than_what_makes_it_is_stale(dep, tmp_path, monkeypatch)
     monkeypatch.setattr(b, "LIB", str(lib))
     assert b._stale()
     lib.write_bytes(b"")
-    real, newest = os.path.getmtime, os.path.abspath(dep)
+    newest = os.path.abspath(dep)
     monkeypatch.setattr(b.os.path, "getmtime", lambda p: 100.0 if os.path.abspath(p) == newest else 50.0 if p == str(lib) else 10.0)
     assert b._stale()
     monkeypatch.setattr(b.os.path, "getmtime", lambda p: 50.0 if p == str(lib) else 10.0)
     assert not b._stale()
-    monkeypatch.setattr(b.os.path, "getmtime", real)
