@@ -82,10 +82,6 @@ struct Shared {
   uint32_t cut_key;
   int cut_index;
 };
-// 2^(j/16) * 2^30, rounded
-__constant__ uint32_t kTable[16] = {1073741824u, 1121280436u, 1170923762u, 1222764986u, 1276901417u, 1333434672u,
-                                    1392470869u, 1454120821u, 1518500250u, 1585730000u, 1655936265u, 1729250827u,
-                                    1805811301u, 1885761398u, 1969251188u, 2056437387u};
 
 __device__ __forceinline__ uint32_t ctarank() {
   uint32_t r;
@@ -233,7 +229,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int i0 = rank * P.chunk, n = max(0, min(P.chunk, P.V - i0));
   int turn = 0;
-  if (threadIdx.x < 16) sh.table[threadIdx.x] = kTable[threadIdx.x];
+  // 2^(j/16) * 2^30, rounded. (No __constant__ memory: it is the whole library's, and cost every kernel of it 0.1 to 0.2 us a launch:
+  // paged writes of 32 tokens 2.00 us without, 2.21 with.)
+  constexpr uint32_t kTable[16] = {1073741824u, 1121280436u, 1170923762u, 1222764986u, 1276901417u, 1333434672u,
+                                   1392470869u, 1454120821u, 1518500250u, 1585730000u, 1655936265u, 1729250827u,
+                                   1805811301u, 1885761398u, 1969251188u, 2056437387u};
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (threadIdx.x == j) sh.table[j] = kTable[j];
   if (ctas > 1) cluster_sync();   // the others run
   pdl_wait();
   // ---- the row, its largest logit, and whether it has a distribution; what is given for the row, read once

@@ -20,3 +20,11 @@ def test_a_library_older_than_what_makes_it_is_stale(dep, tmp_path, monkeypatch)
     assert b._stale()
     monkeypatch.setattr(b.os.path, "getmtime", lambda p: 50.0 if p == str(lib) else 10.0)
     assert not b._stale()
+
+
+def test_no_kernel_uses_constant_memory():
+    """All units link into one module, whose constant memory every kernel's launch pays for."""
+    for name in os.listdir(b.CSRC):
+        with open(os.path.join(b.CSRC, name)) as f:
+            code = [line.split("//")[0] for line in f]
+        assert not any("__constant__" in line for line in code), name
