@@ -48,6 +48,10 @@ struct Params {
   float* logprob;
   int64_t stride;
   int V, chunk, seg;   // chunk: logits of a CTA; seg: of a warp, a multiple of 128
+  // 2^(j/16) * 2^30, rounded. (A parameter: __constant__ memory is the whole library's, and cost every kernel of it 0.1 to 0.2 us a
+  // launch; paged writes of 32 tokens took 2.21 us for 2.00.)
+  uint32_t table[16] = {1073741824u, 1121280436u, 1170923762u, 1222764986u, 1276901417u, 1333434672u, 1392470869u, 1454120821u,
+                        1518500250u, 1585730000u, 1655936265u, 1729250827u, 1805811301u, 1885761398u, 1969251188u, 2056437387u};
 };
 
 using u64 = unsigned long long;
@@ -219,7 +223,7 @@ struct Cut {
   __device__ __forceinline__ bool keeps(uint32_t k, int i) const { return k > key || (k == key && i <= index); }
 };
 
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ Params P) {
   extern __shared__ __align__(16) float row[];
   __shared__ Shared sh;
   __shared__ __align__(8) uint32_t hists[2][kBins];   // by turns; later the list's sums in kBins / 2 bins
@@ -229,14 +233,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int i0 = rank * P.chunk, n = max(0, min(P.chunk, P.V - i0));
   int turn = 0;
-  // 2^(j/16) * 2^30, rounded. (No __constant__ memory: it is the whole library's, and cost every kernel of it 0.1 to 0.2 us a launch:
-  // paged writes of 32 tokens 2.00 us without, 2.21 with.)
-  constexpr uint32_t kTable[16] = {1073741824u, 1121280436u, 1170923762u, 1222764986u, 1276901417u, 1333434672u,
-                                   1392470869u, 1454120821u, 1518500250u, 1585730000u, 1655936265u, 1729250827u,
-                                   1805811301u, 1885761398u, 1969251188u, 2056437387u};
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (threadIdx.x == j) sh.table[j] = kTable[j];
+  if (threadIdx.x < 16) sh.table[threadIdx.x] = P.table[threadIdx.x];
   if (ctas > 1) cluster_sync();   // the others run
   pdl_wait();
   // ---- the row, its largest logit, and whether it has a distribution; what is given for the row, read once
