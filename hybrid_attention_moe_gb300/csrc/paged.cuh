@@ -1,5 +1,6 @@
-// The paged key-value cache: geometry, argument checks and the formats' small conversions,
-// shared by the write and read kernels (paged.cu) and the decode attention (paged_attn.cu).
+// The paged key-value cache: geometry, argument checks, a slot's page, and the formats' small conversions both ways,
+// shared by the write and read kernels (paged.cu), the append (paged_append.cu), the attentions (paged_attn.cu,
+// paged_tree.cu) and the trees' bookkeeping (tree.cu).
 #pragma once
 
 #include "common.cuh"

@@ -18,7 +18,8 @@
 // that the products keep FP32's accuracy. FP8 and NVFP4 pages: codes become f16 exactly, q becomes f16 by a power of two
 // for each row (exact down to 2^-31 of the row's largest magnitude), the rows' own powers of two go to the
 // logits (K) and to P (V), and P is rounded to f16 once (2^-11); its reference z follows the weights times their value
-// rows' powers, so that a large value row of small weight keeps its bits, and what it takes from others is below 2^-32 of it.
+// rows' powers, so that a large value row of small weight keeps its bits, and what it takes from others is below 2^-32 of it (a
+// block's first half goes to a new reference through FP32).
 //
 // The blocks of all items, laid end to end and weighed by their tiles, with a cost for each item besides, are cut into
 // equal ranges, one for each CTA; partials of an item that several ranges share go to the workspace and a second kernel
@@ -40,15 +41,16 @@
 // frees TMEM and returns.
 //
 // Measured with the join, 48 query and 8 KV heads of 128, pages of 64 (us; in brackets the floor of bytes or products):
-//   1 sequence, 100K keys, BF16:   16 nodes 85 (60.5: keys at 4.8 TB/s)   64 nodes 185 (81; three tiles, the third read apart)
-//                          FP8:    16 nodes 108 (30.5)                    64 nodes 275 (81)
-//   32 sequences of 1 to 16 nodes over up to 16K keys:   BF16 217 (157)   FP8 261 (80)
-//   1 sequence, 200 keys, 5 nodes: 16.8 (launch, plan 1, queries 3, four blocks 3, output 6, join)
+//   1 sequence, 100K keys, BF16:   16 nodes 86 (60.5: keys at 4.8 TB/s)   64 nodes 186 (81; three tiles, the third read apart)
+//                          FP8:    16 nodes 114 (30.5)                    64 nodes 289 (81)
+//   32 sequences of 1 to 16 nodes over up to 16K keys:   BF16 219 (157)   FP8 259 (80)   NVFP4 270 (45)
+//   1 sequence, 200 keys, 5 nodes: 17.3 (launch, plan 1, queries 3, four blocks 3, output 6, join)
 // BF16 of one tile is bound by the key stream and the 10 us around it, of more by the streams' softmax beside the tensor pipe (a unit
 // of 64 keys by 128 rows takes a stream 2.8K cycles, 1.5K of them arithmetic; the products 0.9K). Quantised pages are bound by
 // issue slots: 1100 of them each block and SM sub-partition, of 2200 cycles, a third in the conversion, 40 % in the softmax.
 // What paid, at 32 sequences over FP8 (us): first kernel 568; f16 and P by z 543; ranges that count an item's own cost 286 (the
-// last CTA had 24 short items); conversions by turns of whole rows 276; output by sectors 261. Not kept: 32-wide output columns shared by the streams and queries
+// last CTA had 24 short items); conversions by turns of whole rows 276; output by sectors 263; P up to all of f16's range before its
+// reference moves 259. Not kept: 32-wide output columns shared by the streams and queries
 // and output out of line (registers of the loop over blocks: 16 nodes over FP8 119 -> 131 and 138), halves of an item of one tile
 // for each stream (the keys of 64 nodes read once: 193 -> 197, not what bounds it).
 // Without relocatable device code the status word's declaration is a variable of this unit's own, which nothing here
@@ -1020,7 +1022,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     for (int i = 0; i < P.N; ++i)
       if (cum[i + 1] == cum[i]) zero(P.row_start[i], P.row_start[i + 1]);
     if constexpr (C::QUANT) {
-      // ---------------------------------------------------------------- codes to bf16 tiles
+      // ---------------------------------------------------------------- codes to f16 tiles
       const int kv = (warp - 12) >> 2, tid = threadIdx.x - (12 + 4 * kv) * 32;   // four warps for K, four for V
       const uint32_t full = kv ? v_full : k_full, empty = kv ? v_empty : k_empty;
       uint32_t nb = 0;

@@ -18,10 +18,15 @@ constexpr int ROWS = 128;         // rows of a tile
 constexpr int kNodes = 64;        // tree rows of a sequence at most
 constexpr int kMaxSeqs = 256;     // sequences of one launch
 // What an item costs beside its blocks (filling and draining the streams, queries, references, output), in blocks of one
-// tile; a range costs four blocks more at least. 32 sequences of 1 to 16 nodes over up to 16K keys, in us:
-//   cost     0    4    8   12   20
-//   BF16   443  358  298  252  219
-//   FP8    523  403  326  285  290   (the last ranges, of short sequences, took twice as long as the others)
+// tile; a range costs four blocks more at least. In us, 32 sequences of 1 to 16 nodes over up to 16K keys / 8 over up to 2K:
+//   cost             8         12         14         16         20         24         36
+//   D 128  BF16   295/30    251/30     234/29     234/30     219/33     215/33     202/39
+//          FP8    326/34    271/35     259/36     259/39     266/45     269/46     278/54
+//          NVFP4  335/34    280/35     272/36     270/39     270/45     272/46     280/54
+//   D 64   BF16   174/21    147/22     146/22     146/24     147/26     149/27     154/31
+//          FP8    240/26    241/29     244/31     247/34     245/37     250/39     253/45
+// A full batch gains from a high cost up to the item's own, above all at D 128 (below it the last ranges, of short sequences,
+// take twice as long as the others); a small one loses by it, as it then has fewer ranges than there are SMs.
 constexpr int kItemBF16 = 20, kItemQuant = 14;
 constexpr int kGrid = 152;        // CTAs at most (the workspace is sized for this many)
 constexpr int kFlush = 128;       // blocks of a stream between flushes of O: 1024 MMAs

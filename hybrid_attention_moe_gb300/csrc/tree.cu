@@ -2,8 +2,8 @@
 // and the move of the accepted rows to the front of the tree's slots.
 //
 // All are bound by a launch and a few dependent loads. A warp takes a sequence's up to 64 nodes, two a lane.
-// Measured in a graph: plan, accept and keep of one tree of 16 nodes 5.2 us together; plan, accept and six layers' keep of
-// 64 trees of up to 64 nodes over FP8 pages 19.7 us (from the host 71: eight calls of 9 us).
+// Measured in a graph: plan, accept and keep of one tree of 16 nodes 5.4 us together; plan, accept and six layers' keep of
+// 64 trees of up to 64 nodes over FP8 pages 20.2 us (from the host 72: eight calls of 9 us, as keep takes one layer's cache).
 #include "paged.cuh"
 
 namespace beam {

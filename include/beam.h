@@ -386,8 +386,8 @@ beam_status beam_paged_kv_write(const beam_bf16* k, const beam_bf16* v, int toke
 
 /* New tokens of a paged layer from the packed projection's rows: per-head Q/K RMSNorm, RoPE or the
  * SSMax query scale (cfg->kind), and the K and V rows into the pages, as beam_qkv_gate does for
- * beam_kv_cache. K is rounded to bf16 before it is quantised, so the pages hold what beam_paged_kv_write
- * of that row stores.
+ * beam_kv_cache. Norm and rotation are FP32 work, off by at most 2^-19 (|x| + |y|) of a rotated pair x, y before the rounding
+ * to bf16. K is rounded to bf16 before it is quantised, so the pages hold what beam_paged_kv_write of that row stores.
  *  qkv       (device) bf16: token t's rows Q | K | V (| gate), head-major, start at t * token_stride
  *            (elements, a multiple of 8, at least the rows' length); 16-byte aligned.
  *  q_norm_w, k_norm_w (device) [D] bf16 gains, 16-byte aligned; both NULL: no norm.
