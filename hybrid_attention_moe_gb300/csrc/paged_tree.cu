@@ -873,10 +873,10 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       // O's factors h^2 (in two steps, which alone may leave FP32's range) to the reference m of what is written
       float h0 = 1.f, h1 = 0.f;
       bool other = false;   // stream 1's share is added here
-      // Whether the row has keys in this stream, and in stream 1. A factor of zero is no sign of none: the share of a stream that
-      // the other outweighs may hold a NaN or an infinity, which reaches the row all the same.
-      const bool own = l != 0.f;
-      bool theirs = false;
+      // O is the row's if it sees anything: a row that sees nothing has the others' P . V, or no P at all. Neither a factor nor a sum
+      // of zero says that: a stream that the other outweighs, or whose logits all are -inf, may hold a NaN or an infinity of a
+      // value that the row reads, which reaches it all the same.
+      const bool sees = v.tree != 0;
       auto half = [](float zs, float top) { return zs == kNegInf ? 0.f : ex2(0.5f * (zs - top)); };
       if (it.w == 1) {
         float4* xch = reinterpret_cast<float4*>(sm + C::XCH);
@@ -896,14 +896,13 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         arrive(x_empty);
         ++turns;
         other = units_of(it, 1) > 0;
-        theirs = y.z != 0.f;
         const float top = fmaxf(m, y.x);
         if (l != l || y.z != y.z || top == INFINITY) {   // a logit that is NaN (its stream's m may be -inf) or +inf
           l = h0 = h1 = __uint_as_float(0x7FFFFFFFu);
         } else if (top != kNegInf) {
           h0 = half(z, top);
           h1 = half(y.y, top);
-          l = (own ? ex2(m - top) * l : 0.f) + (theirs ? ex2(y.x - top) * y.z : 0.f);
+          l = (l == 0.f ? 0.f : ex2(m - top) * l) + (y.z == 0.f ? 0.f : ex2(y.x - top) * y.z);
         }
         m = top;
       } else if (C::QUANT && m != kNegInf) {
@@ -929,24 +928,21 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         tmem_wait_ld();
         float a[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) a[e] = own ? __uint_as_float(o[e]) * h0 * h0 : 0.f;
-        if (flushed && own)
+        for (int e = 0; e < 32; ++e) a[e] = sees ? __uint_as_float(o[e]) * h0 * h0 : 0.f;
+        if (flushed && sees)
 #pragma unroll
           for (int e = 0; e < 32; ++e) a[e] += fl[s * ROWS * D + 32 * x + e] * h0 * h0;
         if (other) {
           tmem_ld32_nowait(to + 256 + 32 * x, o);
           tmem_wait_ld();
-          if (theirs)
+          if (sees)
 #pragma unroll
             for (int e = 0; e < 32; ++e) a[e] += __uint_as_float(o[e]) * h1 * h1;
-          if (other_flushed && theirs)
+          if (other_flushed && sees)
 #pragma unroll
             for (int e = 0; e < 32; ++e) a[e] += fl[ROWS * D + 32 * x + e] * h1 * h1;
         }
         if (real) {
-          if (l == 0.f)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) a[e] = 0.f;
           if (odd) {   // in an array of its own: the call takes its address
             float y[32];
 #pragma unroll

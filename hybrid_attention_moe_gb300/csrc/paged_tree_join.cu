@@ -39,7 +39,6 @@ __global__ void __launch_bounds__(8 * kJoinRows) paged_tree_join_kernel(const Pa
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) {
       const float4 v = __ldcg(reinterpret_cast<const float4*>(P.part_acc + at(s) * D + d + 32 * e));
-      if (ml.y == 0.f) continue;   // no key of this part
       O[e].x += f * v.x;
       O[e].y += f * v.y;
       O[e].z += f * v.z;

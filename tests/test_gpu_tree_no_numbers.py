@@ -117,3 +117,45 @@ def test_gates_of_rows_that_see_nothing(fmt, base):
     g[10:15] = NAN
     out = run(k, nodes, g=g)
     assert status() == B.DEV_BAD_PAGE and not out[10:15].any() and torch.equal(out[:10], clean[:10])
+
+
+@pytest.mark.parametrize("base", [64, 65, 127, 128, 2560, 2561])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_a_value_beside_a_logit_of_minus_infinity(base, bad):
+    """It is the row's like any other that it reads, wherever the item is cut: the key of -inf is the last block's only one at 64, 128
+    and 2,560 keys. The other columns are as if the key were not there."""
+    k, v = rows(base + 1, 40)
+    q = randn(42, 1, 1, D).float()
+    q[0, 0, 0] = -1.0
+    k[base, 0] = INF
+    clean, _ = finite_as_the_oracle("bf16", k, v, q, base)
+    v[base, 3] = bad
+    out, ref = finite_as_the_oracle("bf16", k, v, q, base)
+    assert not np.isfinite(out[0, 3]) and np.array_equal(np.delete(out, 3, 1), np.delete(clean, 3, 1))
+
+
+def test_a_row_of_logits_of_minus_infinity_alone():
+    """Zero, but for a value that is no number."""
+    k, v = rows(65, 50)
+    q = randn(52, 2, 1, D).to(torch.bfloat16)
+    q[1, 0, 0] = -1.0
+    k[64, 0] = INF
+    v[64, 7] = NAN
+    out = attend(cfg_for(1, 1, D), filled("bf16", k, v, 1), q, ints([0]), ints([0, 2]), ints([63]), words([{0}, {0, 1}]), 65)
+    out = np64(out)
+    assert status() == 0 and np.isfinite(out[0]).all() and np.isnan(out[1, 7]) and not np.delete(out[1], 7).any()
+
+
+@pytest.mark.parametrize("base,first,last,spot", [(128, 64, 128, 70), (128, 0, 64, 5), (2560, 0, 1280, 100), (2560, 1280, 2560, 1300)])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_whole_blocks_of_logits_of_minus_infinity(base, first, last, spot, bad):
+    """All keys of a stream's blocks, or of a range's, weigh nothing, and one's value is no number."""
+    k, v = rows(base + 1, 60)
+    q = randn(62, 1, 1, D).float()
+    q[0, 0, 0] = -1.0
+    k[first:last, 0] = INF
+    clean, _ = finite_as_the_oracle("bf16", k, v, q, base)
+    assert np.isfinite(clean).all()
+    v[spot, 3] = bad
+    out, ref = finite_as_the_oracle("bf16", k, v, q, base)
+    assert not np.isfinite(out[0, 3]) and np.array_equal(np.delete(out, 3, 1), np.delete(clean, 3, 1))
