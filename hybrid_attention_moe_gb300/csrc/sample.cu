@@ -18,9 +18,11 @@
 // Measured, us: one row of 201,088 logits 14 (top-k 50), 22 to 69 (top-p, by how flat the row is and where the cut falls), 33 rows
 // of 32,003 with top-k 18; 128 rows of 201,088: 45 (greedy: the row's load finds the largest, a pass over shared memory its
 // index), 69 (min-p), 93 (top-k), 106 (no rule), 159 to 420 (top-p); 103 MB are 15.2 us of HBM. What bounds it is arithmetic (issue
-// 55 %; a greedy row, by reading, its two passes of latency): a weight is 40 instructions, a comparison pass 10 a logit, and a row alone has 16 SMs (a cluster) and six exchanges of 2K cycles. The first kernel halved a range of keys 32 times, a pass each: one
-// row with top-p took 147 us, 33 with top-k 193, 128 of mixed rules 811 (139 to 150 now). Clusters: 128 rows over 4 / 8 / 16 CTAs 347 / 314 / 436 us, one row 49 / 31 / 25,
-// 33 rows of 32,003 over 1 / 2 / 4 / 8 / 16: 24 / 20 / 18 / 19 / 33. Bins: 2048 cost the exchange 10K cycles, 512 2K.
+// 55 %; a greedy row, by reading, its two passes of latency): a weight is 40 instructions, a comparison pass 10 a logit, and a
+// row alone has 16 SMs (a cluster) and six exchanges of 2K cycles. The first kernel halved a range of keys 32 times, a pass each:
+// one row with top-p took 147 us, 33 with top-k 193, 128 of mixed rules 811 (139 to 150 now). Clusters: 128 rows over 4 / 8 / 16
+// CTAs 347 / 314 / 436 us, one row 49 / 31 / 25, 33 rows of 32,003 over 1 / 2 / 4 / 8 / 16: 24 / 20 / 18 / 19 / 33. Bins: 2048 cost
+// the exchange 10K cycles, 512 2K.
 #include <math.h>
 
 #include "common.cuh"
