@@ -722,8 +722,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                 if constexpr (C::QUANT) zt -= float(kBias);
                 else zt = mt = mt * rf;
                 // a row that another's first keys brought here is held to the same bound
-                const float by = lag ? 0.f : float(kRescale);
-                const bool need = m != kNegInf && (mt > m + by || zt > z + by);
+                const float by = lag ? 0.f : float(kRescale), byz = lag ? 0.f : float(C::QUANT ? kRise : kRescale);
+                const bool need = m != kNegInf && (mt > m + by || zt > z + byz);
                 if (__any_sync(0xffffffffu, need)) {
                   // O holds the stream's earlier products: the last one has to be done
                   if (!all(k == 0 || wait(pv_done + 8 * s, (un - 1) & 1))) { ok = false; break; }

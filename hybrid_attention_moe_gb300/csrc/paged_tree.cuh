@@ -37,6 +37,7 @@ constexpr int kRescale = 8;       // log2 of what a block's weights may come to 
 // to new references: 1.5 x 2^-25 in all, less than 2^-32 of the largest.
 constexpr int kBias = 8;
 constexpr unsigned kMostP = 0x7BFFu;   // f16's largest number: past it (an infinity) the references are taken anew
+constexpr int kRise = 15 - kBias;      // where another row has them looked at, P may rise by this power: to 2^15, a number of f16
 
 struct Params {
   const uint16_t* q;

@@ -64,3 +64,24 @@ def test_small_weights_beside_large_ones(fmt, n, at, lead, x):
     o, ref, tol = upper_half(fmt, n, at, 3.0, lead, x, 1.0)
     assert np.all(np.abs(o - ref) <= tol), (float(np.max(np.abs(o - ref) / np.abs(ref))), float(np.max(tol / np.abs(ref))))
     assert np.all(o > 0)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("n,lead", [(63, 40), (63, 20), (300, 40), (300, 130), (300, 200)])
+@pytest.mark.parametrize("e", range(4, 20))
+def test_products_that_rise_beside_a_row_that_sees_nothing(fmt, n, lead, e):
+    """Rows without keys have the references looked at in every block, and a row beside them moves its own only where its products
+    have risen enough: up to there P has to be a number of f16. Keys of equal logits, one value row 2^e times the others."""
+    k, v = torch.zeros(n + 2, D, device=DEV), torch.ones(n + 2, D, device=DEV)
+    v[lead, :D // 2] = 2.0 ** e
+    v[lead, D // 2:] = -(2.0 ** e)
+    c = filled(fmt, k, v)
+    q = torch.zeros((3, 1, D), device=DEV, dtype=torch.bfloat16)
+    out = attend(cfg_for(1, 1, D), c, q, ints([0]), ints([0, 3]), ints([n - 1]), words([{0}, set(), {0, 2}]), n + 2)
+    assert status() == 0
+    V = host(c).load(0, np.arange(1, n + 1))[1][0]
+    o, ref = np64(out), V.mean(0)
+    assert np.all(np.abs(o[0] - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -15) * np.abs(V).mean(0))
+    V = np.concatenate([V, host(c).load(0, np.array([n + 2]))[1][0]])
+    ref = V.mean(0)
+    assert not o[1].any() and np.all(np.abs(o[2] - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -15) * np.abs(V).mean(0))
